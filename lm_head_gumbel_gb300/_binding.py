@@ -1,4 +1,5 @@
-"""ctypes binding of ``libfs.so`` (declared in ``include/fs_sample.h``).
+"""ctypes binding of ``libfs.so`` (declared in ``include/fs_sample.h`` and
+``include/fs_vocab.h``).
 
 Argument marshalling only: tensors become device pointers, sizes and strides;
 every step of the sampling path runs in the library's CUDA kernels.  PyTorch
@@ -9,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from typing import NamedTuple, Optional
 
 import torch
 
@@ -24,6 +26,8 @@ FS_ERR_WORKSPACE = 5
 FS_TOPK_MAX = 16
 FS_SYNC_NONE, FS_SYNC_STREAM, FS_SYNC_IDS = 0, 1, 2
 FS_FLAG_OVERLAP_PREVIOUS = 1
+FS_LOGPROBS_TOPK_MAX = 20
+FS_BF16, FS_F32 = 0, 1
 FS_MERGE_EXACT = 0
 FS_MERGE_GROUP_GUMBEL = 1
 
@@ -50,6 +54,32 @@ class FsSampleArgs(ctypes.Structure):
         ("out_tile_lse", _c_ptr), ("workspace", _c_ptr), ("workspace_bytes", ctypes.c_size_t),
         ("vocab_offset", _c_i64), ("out_max", _c_ptr), ("out_lse", _c_ptr),
         ("flags", ctypes.c_uint32),
+    ]
+
+
+class FsLogprobsArgs(ctypes.Structure):
+    """Mirror of ``fs_logprobs_args``."""
+    _fields_ = [
+        ("H", _c_ptr), ("W", _c_ptr), ("temperature", _c_ptr),
+        ("vocab_mask", _c_ptr), ("mask_ld", _c_i64), ("tokens", _c_ptr),
+        ("B", _c_i64), ("d", _c_i64), ("V", _c_i64), ("ldh", _c_i64), ("ldw", _c_i64),
+        ("vocab_offset", _c_i64), ("K", _c_i64),
+        ("out_logp", _c_ptr), ("out_entropy", _c_ptr), ("out_lse", _c_ptr),
+        ("out_topk_idx", _c_ptr), ("out_topk_logp", _c_ptr),
+        ("workspace", _c_ptr), ("workspace_bytes", ctypes.c_size_t), ("flags", ctypes.c_uint32),
+    ]
+
+
+class FsLogprobsGradArgs(ctypes.Structure):
+    """Mirror of ``fs_logprobs_grad_args``."""
+    _fields_ = [
+        ("H", _c_ptr), ("W", _c_ptr), ("temperature", _c_ptr),
+        ("vocab_mask", _c_ptr), ("mask_ld", _c_i64), ("tokens", _c_ptr),
+        ("lse", _c_ptr), ("entropy", _c_ptr), ("grad_logp", _c_ptr), ("grad_entropy", _c_ptr),
+        ("B", _c_i64), ("d", _c_i64), ("V", _c_i64), ("ldh", _c_i64), ("ldw", _c_i64),
+        ("vocab_offset", _c_i64), ("out_dH", _c_ptr), ("out_dW", _c_ptr),
+        ("lddh", _c_i64), ("lddw", _c_i64),
+        ("workspace", _c_ptr), ("workspace_bytes", ctypes.c_size_t),
     ]
 
 
@@ -95,6 +125,23 @@ def load_library(path: str = LIB_PATH):
     lib.fs_wait_timeout_selftest.restype = ctypes.c_int
     lib.fs_last_device_error.argtypes = [_c_ptr, ctypes.POINTER(ctypes.c_int)]
     lib.fs_last_device_error.restype = ctypes.c_int
+    lib.fs_logprobs_workspace_size.argtypes = [_c_i64, _c_i64, _c_i64]
+    lib.fs_logprobs_workspace_size.restype = ctypes.c_size_t
+    lib.fs_logprobs.argtypes = [ctypes.POINTER(FsLogprobsArgs), _c_ptr]
+    lib.fs_logprobs.restype = ctypes.c_int
+    lib.fs_logprobs_grad_workspace_size.argtypes = [_c_i64, _c_i64, _c_i64]
+    lib.fs_logprobs_grad_workspace_size.restype = ctypes.c_size_t
+    lib.fs_logprobs_grad.argtypes = [ctypes.POINTER(FsLogprobsGradArgs), _c_ptr]
+    lib.fs_logprobs_grad.restype = ctypes.c_int
+    lib.fs_embed.argtypes = [_c_ptr, _c_i64, _c_ptr, _c_i64, _c_i64, _c_i64, ctypes.c_int,
+                             ctypes.c_float, _c_i64, _c_ptr, _c_i64, _c_ptr]
+    lib.fs_embed.restype = ctypes.c_int
+    lib.fs_embed_grad_workspace_size.argtypes = [_c_i64, _c_i64]
+    lib.fs_embed_grad_workspace_size.restype = ctypes.c_size_t
+    lib.fs_embed_grad.argtypes = [_c_ptr, _c_i64, _c_ptr, _c_i64, _c_i64, _c_i64, ctypes.c_int,
+                                  ctypes.c_float, _c_i64, _c_ptr, _c_i64, ctypes.c_int,
+                                  ctypes.c_int, _c_ptr, ctypes.c_size_t, _c_ptr]
+    lib.fs_embed_grad.restype = ctypes.c_int
     lib.fs_status_string.argtypes = [ctypes.c_int]
     lib.fs_status_string.restype = ctypes.c_char_p
     _lib = lib
@@ -348,4 +395,270 @@ def fs_gumbel_noise(b0, nb, v0, nv, *, seed=0, offset=0, seeds=None, out=None, d
                                  _stream_handle(stream, device))
     if st != FS_OK:
         raise FsError(st, "fs_gumbel_noise")
+    return out
+
+
+# ---- the operators of fs_vocab.h ------------------------------------------
+def _check_on(dev, **tensors):
+    """Every given tensor lies on `dev` (the kernels read raw pointers)."""
+    for name, t in tensors.items():
+        if t is not None and t.device != dev:
+            raise FsError(FS_ERR_INVALID_ARG, f"{name} must be on {dev}")
+
+
+def _check_rows(name, t, dtype, n):
+    if t is not None and (t.dtype != dtype or t.dim() != 1 or t.shape[0] != n
+                          or not t.is_contiguous()):
+        raise FsError(FS_ERR_INVALID_ARG, f"{name} must be a contiguous {dtype} vector of {n}")
+
+
+def _check_mask(vocab_mask, B, V):
+    if vocab_mask is not None and (
+            vocab_mask.dtype != torch.int32 or vocab_mask.dim() != 2 or vocab_mask.shape[0] != B
+            or vocab_mask.shape[1] < (V + 31) // 32 or vocab_mask.stride(1) != 1):
+        raise FsError(FS_ERR_INVALID_ARG, "vocab_mask must be an int32 matrix [B, >= ceil(V/32)]")
+
+
+def _ld(t):
+    """Row stride of a matrix; of a single row, one that any check accepts."""
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), (t.shape[1] + 7) // 8 * 8)
+
+
+def _check_workspace(workspace, dev):
+    if workspace is not None and (workspace.device != dev or not workspace.is_contiguous()):
+        raise FsError(FS_ERR_WORKSPACE, f"workspace must be a contiguous tensor on {dev}")
+
+
+def _run(name, dev, call):
+    """Call the library with `dev` current and its status checked."""
+    if torch.cuda.current_device() == dev.index:
+        st = call()
+    else:
+        with torch.cuda.device(dev):
+            st = call()
+    if st != FS_OK:
+        raise FsError(st, name)
+
+
+class FsLogprobs(NamedTuple):
+    """What fs_logprobs returns; None where it was not asked for."""
+    logp: Optional[torch.Tensor]       # fp32 [B]
+    entropy: torch.Tensor              # fp32 [B]
+    lse: torch.Tensor                  # fp32 [B]
+    topk_idx: Optional[torch.Tensor]   # int64 [B, K]
+    topk_logp: Optional[torch.Tensor]  # fp32 [B, K]
+
+
+def fs_logprobs_workspace_size(B: int, V: int, K: int = 0) -> int:
+    return int(load_library().fs_logprobs_workspace_size(int(B), int(V), int(K)))
+
+
+def fs_logprobs(H, W, tokens=None, K=0, *, temperature=None, vocab_mask=None, vocab_offset=0,
+                out_logp=None, out_entropy=None, out_lse=None, out_topk_idx=None,
+                out_topk_logp=None, workspace=None, stream=None, overlap_previous=False):
+    """Log-probabilities of `tokens` under softmax(H W^T / T) (masked), the
+    entropy and log-sum-exp of every row, and the row's K <= 20 most probable
+    tokens, without writing the logits.
+
+    H: bf16 [B, d]; W: bf16 [V, d]; tokens: int64 [B] or None (no logp; a
+    token below 0 gives 0, one that is masked or not among W's ids -inf);
+    temperature, vocab_mask, vocab_offset, stream, overlap_previous: as in
+    fs_sample (rows it samples greedily are scored at T = 1).  out_*: result
+    tensors to fill, made when None.  workspace: a uint8 tensor of
+    fs_logprobs_workspace_size(B, V, K) bytes, or None.  Returns FsLogprobs."""
+    lib = load_library()
+    _check_2d("H", H, torch.bfloat16)
+    _check_2d("W", W, torch.bfloat16)
+    B, d = H.shape
+    V = W.shape[0]
+    dev = H.device
+    K = int(K)
+    if W.shape[1] != d:
+        raise FsError(FS_ERR_INVALID_ARG, "H and W must have the same number of columns")
+    if not 0 <= K <= FS_LOGPROBS_TOPK_MAX:
+        raise FsError(FS_ERR_INVALID_ARG, f"K must be 0 to {FS_LOGPROBS_TOPK_MAX}")
+    _check_rows("tokens", tokens, torch.int64, B)
+    _check_rows("temperature", temperature, torch.float32, B)
+    _check_mask(vocab_mask, B, V)
+    if tokens is None:
+        out_logp = None
+    elif out_logp is None:
+        out_logp = torch.empty(B, dtype=torch.float32, device=dev)
+    if out_entropy is None:
+        out_entropy = torch.empty(B, dtype=torch.float32, device=dev)
+    if out_lse is None:
+        out_lse = torch.empty(B, dtype=torch.float32, device=dev)
+    if K == 0:
+        out_topk_idx = out_topk_logp = None
+    else:
+        if out_topk_idx is None:
+            out_topk_idx = torch.empty((B, K), dtype=torch.int64, device=dev)
+        if out_topk_logp is None:
+            out_topk_logp = torch.empty((B, K), dtype=torch.float32, device=dev)
+        for name, t, dtype in (("out_topk_idx", out_topk_idx, torch.int64),
+                               ("out_topk_logp", out_topk_logp, torch.float32)):
+            if t.dtype != dtype or tuple(t.shape) != (B, K) or not t.is_contiguous():
+                raise FsError(FS_ERR_INVALID_ARG, f"{name} must be a contiguous {dtype} [B, K]")
+    for name, t in (("out_logp", out_logp), ("out_entropy", out_entropy), ("out_lse", out_lse)):
+        _check_rows(name, t, torch.float32, B)
+    if workspace is None:
+        workspace = torch.empty(max(1, lib.fs_logprobs_workspace_size(B, V, K)),
+                                dtype=torch.uint8, device=dev)
+    _check_on(dev, W=W, tokens=tokens, temperature=temperature, vocab_mask=vocab_mask,
+              out_logp=out_logp, out_entropy=out_entropy, out_lse=out_lse,
+              out_topk_idx=out_topk_idx, out_topk_logp=out_topk_logp)
+    _check_workspace(workspace, dev)
+    args = FsLogprobsArgs(
+        H=_ptr(H), W=_ptr(W), temperature=_ptr(temperature), vocab_mask=_ptr(vocab_mask),
+        mask_ld=0 if vocab_mask is None else max(vocab_mask.stride(0), vocab_mask.shape[1]),
+        tokens=_ptr(tokens), B=B, d=d, V=V, ldh=_ld(H), ldw=_ld(W),
+        vocab_offset=int(vocab_offset), K=K, out_logp=_ptr(out_logp),
+        out_entropy=_ptr(out_entropy), out_lse=_ptr(out_lse), out_topk_idx=_ptr(out_topk_idx),
+        out_topk_logp=_ptr(out_topk_logp), workspace=_ptr(workspace),
+        workspace_bytes=workspace.numel() * workspace.element_size(),
+        flags=FS_FLAG_OVERLAP_PREVIOUS if overlap_previous else 0)
+    _run("fs_logprobs", dev,
+         lambda: lib.fs_logprobs(ctypes.byref(args), _stream_handle(stream, dev)))
+    return FsLogprobs(out_logp, out_entropy, out_lse, out_topk_idx, out_topk_logp)
+
+
+def fs_logprobs_grad_workspace_size(B: int, d: int, V: int) -> int:
+    return int(load_library().fs_logprobs_grad_workspace_size(int(B), int(d), int(V)))
+
+
+def _grad_like(name, out, n, d, dev):
+    """bf16 [n, d] result whose rows start on 16-byte boundaries."""
+    if out is None:
+        return torch.empty((n, (d + 7) // 8 * 8), dtype=torch.bfloat16, device=dev)[:, :d]
+    _check_2d(name, out, torch.bfloat16)
+    if tuple(out.shape) != (n, d):
+        raise FsError(FS_ERR_INVALID_ARG, f"{name} must be [{n}, {d}]")
+    return out
+
+
+def fs_logprobs_grad(H, W, tokens, lse, grad_logp, *, entropy=None, grad_entropy=None,
+                     temperature=None, vocab_mask=None, vocab_offset=0, out_dH=None, out_dW=None,
+                     need_dH=True, need_dW=True, workspace=None, stream=None):
+    """Gradient of sum(grad_logp * logp + grad_entropy * entropy) to H and W,
+    with logp and entropy as fs_logprobs computes them for the same arguments.
+
+    lse (and, with grad_entropy, entropy): its results, fp32 [B]; grad_logp,
+    grad_entropy: fp32 [B].  Returns (dH, dW) in bf16 ([B, d], [V, d]; out_dH /
+    out_dW when given), None where need_dH / need_dW is false.  workspace: a
+    uint8 tensor of fs_logprobs_grad_workspace_size(B, d, V) bytes, or None."""
+    lib = load_library()
+    _check_2d("H", H, torch.bfloat16)
+    _check_2d("W", W, torch.bfloat16)
+    B, d = H.shape
+    V = W.shape[0]
+    dev = H.device
+    if W.shape[1] != d:
+        raise FsError(FS_ERR_INVALID_ARG, "H and W must have the same number of columns")
+    if not (need_dH or need_dW):
+        raise FsError(FS_ERR_INVALID_ARG, "neither dH nor dW is asked for")
+    for name, t, dtype in (("tokens", tokens, torch.int64), ("lse", lse, torch.float32),
+                           ("grad_logp", grad_logp, torch.float32)):
+        if t is None:
+            raise FsError(FS_ERR_INVALID_ARG, f"{name} is required")
+        _check_rows(name, t, dtype, B)
+    for name, t in (("entropy", entropy), ("grad_entropy", grad_entropy),
+                    ("temperature", temperature)):
+        _check_rows(name, t, torch.float32, B)
+    if grad_entropy is None:
+        entropy = None
+    _check_mask(vocab_mask, B, V)
+    dH = _grad_like("out_dH", out_dH, B, d, dev) if need_dH else None
+    dW = _grad_like("out_dW", out_dW, V, d, dev) if need_dW else None
+    if workspace is None:
+        workspace = torch.empty(max(1, lib.fs_logprobs_grad_workspace_size(B, d, V)),
+                                dtype=torch.uint8, device=dev)
+    _check_on(dev, W=W, tokens=tokens, lse=lse, grad_logp=grad_logp, entropy=entropy,
+              grad_entropy=grad_entropy, temperature=temperature, vocab_mask=vocab_mask,
+              out_dH=dH, out_dW=dW)
+    _check_workspace(workspace, dev)
+    args = FsLogprobsGradArgs(
+        H=_ptr(H), W=_ptr(W), temperature=_ptr(temperature), vocab_mask=_ptr(vocab_mask),
+        mask_ld=0 if vocab_mask is None else max(vocab_mask.stride(0), vocab_mask.shape[1]),
+        tokens=_ptr(tokens), lse=_ptr(lse), entropy=_ptr(entropy), grad_logp=_ptr(grad_logp),
+        grad_entropy=_ptr(grad_entropy), B=B, d=d, V=V, ldh=_ld(H), ldw=_ld(W),
+        vocab_offset=int(vocab_offset), out_dH=_ptr(dH), out_dW=_ptr(dW),
+        lddh=_ld(dH) if need_dH else 0, lddw=_ld(dW) if need_dW else 0,
+        workspace=_ptr(workspace),
+        workspace_bytes=workspace.numel() * workspace.element_size())
+    _run("fs_logprobs_grad", dev,
+         lambda: lib.fs_logprobs_grad(ctypes.byref(args), _stream_handle(stream, dev)))
+    return dH, dW
+
+
+_ELEMENT = {torch.bfloat16: FS_BF16, torch.float32: FS_F32}
+
+
+def _check_table(name, t):
+    if t.dtype not in _ELEMENT or t.dim() != 2 or t.shape[1] < 1 or t.stride(1) != 1 \
+            or not t.is_cuda:
+        raise FsError(FS_ERR_INVALID_ARG,
+                      f"{name} must be a CUDA bfloat16 or float32 matrix with unit column stride")
+
+
+def fs_embed(ids, E, *, scale=1.0, vocab_offset=0, out=None, stream=None):
+    """Embedding lookup: scale * E[ids - vocab_offset], 0 where the id is not
+    one of E's rows (padding, another shard).  ids: int64 [N]; E: bf16 or fp32
+    [V, d].  Returns out ([N, d] of E's type)."""
+    lib = load_library()
+    _check_table("E", E)
+    dev = E.device
+    V, d = E.shape
+    if ids.dim() != 1:
+        raise FsError(FS_ERR_INVALID_ARG, "ids must be a vector")
+    N = ids.shape[0]
+    _check_rows("ids", ids, torch.int64, N)
+    if out is None:
+        out = torch.empty((N, d), dtype=E.dtype, device=dev)
+    elif out.dtype != E.dtype or tuple(out.shape) != (N, d) or out.stride(1) != 1:
+        raise FsError(FS_ERR_INVALID_ARG, "out must be [N, d] of E's type")
+    _check_on(dev, ids=ids, out=out)
+    _run("fs_embed", dev, lambda: lib.fs_embed(
+        ids.data_ptr(), N, E.data_ptr(), V, d, max(E.stride(0), d), _ELEMENT[E.dtype],
+        float(scale), int(vocab_offset), out.data_ptr(), max(out.stride(0), d),
+        _stream_handle(stream, dev)))
+    return out
+
+
+def fs_embed_grad_workspace_size(N: int, d: int) -> int:
+    return int(load_library().fs_embed_grad_workspace_size(int(N), int(d)))
+
+
+def fs_embed_grad(ids, dY, V, *, scale=1.0, vocab_offset=0, out=None, out_dtype=None,
+                  accumulate=False, workspace=None, stream=None):
+    """Gradient of fs_embed to its table: out[v] = scale * sum of dY[n] over the
+    n with ids[n] = vocab_offset + v, added to `out` with accumulate (which
+    needs out), else 0 for rows no id names.  ids: int64 [N]; dY: bf16 or fp32
+    [N, d]; out: [V, d], bf16 or fp32 (fp32 for fp32 dY); out_dtype: the type of
+    a result made here (dY's when None).  The same inputs always give the same
+    bits.  workspace: a uint8 tensor of fs_embed_grad_workspace_size(N, d)
+    bytes, or None."""
+    lib = load_library()
+    _check_table("dY", dY)
+    dev = dY.device
+    N, d = dY.shape
+    V = int(V)
+    _check_rows("ids", ids, torch.int64, N)
+    if out is None:
+        if accumulate:
+            raise FsError(FS_ERR_INVALID_ARG, "accumulate needs out")
+        out = torch.empty((V, d), dtype=out_dtype or dY.dtype, device=dev)
+    _check_table("out", out)
+    if tuple(out.shape) != (V, d):
+        raise FsError(FS_ERR_INVALID_ARG, f"out must be [{V}, {d}]")
+    if workspace is None and N > 0:
+        workspace = torch.empty(max(1, lib.fs_embed_grad_workspace_size(N, d)),
+                                dtype=torch.uint8, device=dev)
+    _check_on(dev, ids=ids, out=out)
+    _check_workspace(workspace, dev)
+    _run("fs_embed_grad", dev, lambda: lib.fs_embed_grad(
+        ids.data_ptr(), N, dY.data_ptr(), V, d, max(dY.stride(0), d), _ELEMENT[dY.dtype],
+        float(scale), int(vocab_offset), out.data_ptr(), max(out.stride(0), d),
+        _ELEMENT[out.dtype], 1 if accumulate else 0, _ptr(workspace),
+        0 if workspace is None else workspace.numel() * workspace.element_size(),
+        _stream_handle(stream, dev)))
     return out

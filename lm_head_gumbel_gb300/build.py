@@ -10,10 +10,11 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIBRARY = os.path.join(PKG, "libfs.so")
-SOURCES = [os.path.join(CSRC, "fs_sample.cu"), os.path.join(CSRC, "fs_merge.cu")]
+SOURCES = [os.path.join(CSRC, f) for f in ("fs_sample.cu", "fs_merge.cu", "fs_logprobs.cu",
+                                          "fs_embed.cu")]
 DEPENDS = SOURCES + [os.path.join(CSRC, f) for f in ("fs_kernels.cuh", "fs_ptx.cuh",
-                                                    "fs_noise.cuh")] + [
-    os.path.join(INCLUDE, "fs_sample.h")]
+                                                    "fs_noise.cuh", "fs_contract.cuh")] + [
+    os.path.join(INCLUDE, f) for f in ("fs_sample.h", "fs_vocab.h")]
 
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
@@ -26,7 +27,7 @@ def nvcc_path() -> str:
 
 
 def command(output: str = LIBRARY, extra=()) -> list:
-    return [nvcc_path(), *ARCH_FLAGS, "-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
+    return [nvcc_path(), *ARCH_FLAGS, "--threads", "0", "-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
             "-shared", f"-I{INCLUDE}", *extra, "-o", output, *SOURCES]
 
 

@@ -1,0 +1,586 @@
+// fs_contract.cuh -- one persistent tcgen05 contraction kernel, D[m,n] =
+// sum_k A[m,k] B[n,k] in fp32, with the operand layouts and the epilogue as
+// template parameters.  The log-probability operators are four uses of it:
+//   scores     A = H (k contiguous), B = W (k contiguous)  -> row statistics
+//   gradient G A = H,                B = W                 -> bf16 [B, V]
+//   dH = G W   A = G (k contiguous), B = W (n contiguous)  -> bf16 / partial sums
+//   dW = G^T H A = G (m contiguous), B = H (n contiguous)  -> bf16 [V, d]
+// so no operand is ever transposed in memory: TMA brings 64 x 64 boxes of the
+// contiguous dimension with the 128-byte swizzle either way, and the matrix
+// descriptors say which dimension that is.
+//
+// Warp roles as in the sampler's stage 1: warp 0 issues TMA copies into a ring
+// of 64-wide k slices, warp 1 issues the MMAs (M = 128 per CTA and N = 256; for
+// CTA pairs cta_group::2, M = 256 over both), warps 2-9 read finished
+// accumulators (two of them, so an epilogue overlaps the next unit's MMAs).
+// Every wait is bounded: past the limit the roles wind down and the device
+// error word records it.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+
+#include "fs_ptx.cuh"
+
+namespace fs {
+namespace ptx {
+
+// 2-D tiled store of one box from shared memory (bulk async group).
+__device__ __forceinline__ void tma_store_2d(const void* tmap, const void* smem_src, int32_t x,
+                                             int32_t y) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::
+                   "l"(reinterpret_cast<uint64_t>(tmap)),
+               "r"(x), "r"(y), "r"(smem_u32(smem_src))
+               : "memory");
+}
+__device__ __forceinline__ void bulk_commit() {
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+// All of this thread's bulk stores have read their shared memory.
+__device__ __forceinline__ void bulk_wait_read() {
+  asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+}
+__device__ __forceinline__ void bulk_wait() {
+  asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+}
+// Order this thread's shared-memory writes before later async-proxy reads.
+__device__ __forceinline__ void fence_async_smem() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
+// Shared-memory matrix descriptor of an operand whose M (or N) dimension is
+// contiguous, stored with the 128-byte swizzle: atoms of 64 bf16 along it by 8
+// along K (1024 bytes), K-neighbouring atoms 1024 bytes apart, neighbours along
+// M (N) `lead` bytes apart.
+__device__ __forceinline__ uint64_t smem_desc_sw128_mn(uint32_t saddr, uint32_t lead) {
+  uint64_t desc = 0;
+  desc |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
+  desc |= static_cast<uint64_t>(lead >> 4) << 16;
+  desc |= static_cast<uint64_t>(1024u >> 4) << 32;
+  desc |= static_cast<uint64_t>(1u) << 46;
+  desc |= static_cast<uint64_t>(2u) << 61;
+  return desc;
+}
+
+// max that returns NaN if either input is NaN.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float ex2(float a) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(a));
+  return r;
+}
+
+}  // namespace ptx
+
+namespace vocab {
+
+constexpr int kBM = 128;  // M rows per CTA = tensor-memory lanes
+constexpr int kBN = 256;  // N columns per unit = accumulator columns
+constexpr int kBK = 64;   // k slice: 64 bf16 = one 128-byte swizzle row
+constexpr int kUK = 16;   // k of one MMA
+constexpr int kEpiWarps = 8;
+constexpr int kThreads = 32 * (2 + kEpiWarps);
+constexpr int kMaxStages = 8;
+constexpr uint32_t kChunkBytes = 64 * kBK * 2;  // one 64 x 64 box, 8 KB
+constexpr uint32_t kTmemCols = 2 * kBN;
+constexpr uint32_t kStagingBytes = kEpiWarps * 4096;  // one 32 x 64 bf16 box per epilogue warp
+constexpr int kErrWaitTimeout = 1;  // the library's device error word, bit 0
+
+template <class Epi>
+__host__ __device__ constexpr uint32_t ring_bytes() {
+  return Epi::kStaged ? 192u * 1024u : 224u * 1024u;
+}
+template <class Epi>
+__host__ __device__ constexpr size_t smem_bytes() {
+  return 1024 /* alignment slack */ + ring_bytes<Epi>() + (Epi::kStaged ? kStagingBytes : 0) + 256;
+}
+
+enum : uint32_t { kPolicyNormal = 0, kPolicyFirst = 1, kPolicyLast = 2 };
+
+struct Shape {
+  int32_t n_mt, n_nt;      // tiles along M (128 rows, 256 for CTA pairs) and N (256)
+  int32_t n_units;         // n_mt * n_nt * number of k splits
+  int32_t n_kb;            // 64-wide k slices in all
+  int32_t kb_per_split;    // k slices of one unit (the last split may have fewer)
+  int32_t m_rows, n_cols;  // extents of M and N
+  uint32_t m_fastest;      // unit order: M tiles (else N tiles) innermost, k splits outermost
+  uint32_t a_box_rows;     // rows of A's box when k is contiguous (a multiple of 8)
+  uint32_t a_bytes, stage_bytes, n_stages;
+  uint32_t policy_a, policy_b;  // L2 eviction hints
+  // The launch overlaps the kernel before it on the stream, which writes A and
+  // the epilogue's inputs: B streams at once, the rest waits for that kernel.
+  uint32_t pdl;
+  uint64_t wait_limit_ns;
+  int* error_word;
+};
+
+struct Unit {
+  int mt, nt, split, kb0, n_kb;
+};
+
+__device__ __forceinline__ Unit unit_of(const Shape& s, int u) {
+  const int n_tiles = s.n_mt * s.n_nt;
+  Unit r;
+  r.split = u / n_tiles;
+  const int t = u - r.split * n_tiles;
+  if (s.m_fastest) {
+    r.nt = t / s.n_mt;
+    r.mt = t - r.nt * s.n_mt;
+  } else {
+    r.mt = t / s.n_nt;
+    r.nt = t - r.mt * s.n_nt;
+  }
+  r.kb0 = r.split * s.kb_per_split;
+  r.n_kb = min(s.kb_per_split, s.n_kb - r.kb0);
+  return r;
+}
+
+// Bounded mbarrier waits, with the sampler's semantics: past the limit the
+// CTA raises its abort flag and the device error word, and every role winds
+// down instead of spinning.
+struct BoundedWait {
+  volatile uint32_t* abort_flag;
+  uint64_t limit_ns;
+  int* error_word;
+
+  __device__ bool wait(uint64_t* bar, uint32_t parity) const {
+    if (ptx::mbar_try_wait(bar, parity)) return true;
+    const uint64_t t0 = ptx::global_timer_ns();
+    while (true) {
+      if (ptx::mbar_try_wait(bar, parity)) return true;
+      if (*abort_flag) return false;
+      if (ptx::global_timer_ns() - t0 > limit_ns) {
+        *abort_flag = 1u;
+        atomicOr(error_word, kErrWaitTimeout);
+        return false;
+      }
+    }
+  }
+  __device__ bool wait_warp(uint64_t* bar, uint32_t parity) const {
+    return __all_sync(0xFFFFFFFFu, wait(bar, parity));
+  }
+  // While winding down: ignores the abort flag, still bounded.
+  __device__ bool drain(uint64_t* bar, uint32_t parity) const {
+    const uint64_t t0 = ptx::global_timer_ns();
+    while (!ptx::mbar_try_wait(bar, parity)) {
+      if (ptx::global_timer_ns() - t0 > limit_ns) {
+        atomicOr(error_word, kErrWaitTimeout);
+        return false;
+      }
+    }
+    return true;
+  }
+};
+
+__device__ __forceinline__ uint64_t policy_of(uint32_t code) {
+  return code == kPolicyFirst  ? ptx::policy_evict_first()
+         : code == kPolicyLast ? ptx::policy_evict_last()
+                               : ptx::policy_evict_normal();
+}
+
+// What an epilogue call knows about its 32 rows x 128 columns.
+struct TileAt {
+  Unit unit;
+  int row0;         // first M row of the warp's 32 lanes
+  int col0;         // first N column of the warp's 128 columns
+  int rank;         // CTA of the pair
+  int quad, half;   // rows quad*32.. and columns half*128.. of the CTA's tile
+  uint32_t taddr;   // tensor-memory address of (row0, col0)
+};
+
+// kAmn / kBmn: A's M (B's N) dimension is the contiguous one in memory.
+// finish() gets the thread's M row in its worker's first unit.
+// Epi: struct with Params, State, kStaged (uses a bf16 box per warp in shared
+// memory and tmap_d), and static device functions start / tile / finish.
+template <class Epi, bool kPair, bool kAmn, bool kBmn>
+__global__ void __launch_bounds__(kThreads, 1)
+    contract_kernel(const __grid_constant__ CUtensorMap tmap_a,
+                    const __grid_constant__ CUtensorMap tmap_b,
+                    const __grid_constant__ CUtensorMap tmap_d, const Shape s,
+                    const __grid_constant__ typename Epi::Params ep) {
+  constexpr int kCtas = kPair ? 2 : 1;
+  constexpr int kBRows = kBN / kCtas;  // B rows in this CTA's shared memory
+  constexpr uint32_t kBBytes = kBRows * kBK * 2;
+  constexpr uint32_t kIdesc = ptx::idesc_bf16_f32(kBM * kCtas, kBN) | (kAmn ? 1u << 15 : 0u) |
+                              (kBmn ? 1u << 16 : 0u);
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* staging = smem + ring_bytes<Epi>();
+  uint64_t* full_bar = reinterpret_cast<uint64_t*>(staging + (Epi::kStaged ? kStagingBytes : 0));
+  uint64_t* empty_bar = full_bar + kMaxStages;
+  uint64_t* tfull_bar = empty_bar + kMaxStages;
+  uint64_t* tempty_bar = tfull_bar + 2;
+  uint64_t* drain_bar = tempty_bar + 2;
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drain_bar + 1);
+  volatile uint32_t* abort_flag = tmem_holder + 1;
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const int rank = kPair ? int(ptx::cluster_ctarank()) : 0;
+  const bool leader = rank == 0;
+  const int worker = int(blockIdx.x) / kCtas;
+  const int n_workers = int(gridDim.x) / kCtas;
+
+  if (threadIdx.x == 0) {
+    for (uint32_t i = 0; i < s.n_stages; ++i) {
+      ptx::mbar_init(&full_bar[i], 1);
+      ptx::mbar_init(&empty_bar[i], 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      ptx::mbar_init(&tfull_bar[a], 1);
+      ptx::mbar_init(&tempty_bar[a], kCtas * kEpiWarps);
+    }
+    ptx::mbar_init(drain_bar, 1);
+    *abort_flag = 0u;
+    ptx::fence_barrier_init();
+  }
+  if (warp == 0 && lane == 0) {
+    ptx::prefetch_tmap(&tmap_a);
+    ptx::prefetch_tmap(&tmap_b);
+    if (Epi::kStaged) ptx::prefetch_tmap(&tmap_d);
+  }
+  if (warp == 1) {
+    if constexpr (kPair) {
+      ptx::tmem_alloc_pair(tmem_holder, kTmemCols);
+      ptx::tmem_relinquish_pair();
+    } else {
+      ptx::tmem_alloc(tmem_holder, kTmemCols);
+      ptx::tmem_relinquish();
+    }
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  if constexpr (kPair) ptx::cluster_sync();
+  ptx::tc_fence_after();
+  const uint32_t tmem_base = *tmem_holder;
+  const BoundedWait waiter{abort_flag, s.wait_limit_ns, s.error_word};
+
+  if (warp == 0) {
+    // ---------------- TMA producer ----------------
+    const bool issuer = ptx::elect_one();
+    const uint64_t pol_a = policy_of(s.policy_a), pol_b = policy_of(s.policy_b);
+    auto load = [&](uint8_t* dst, const CUtensorMap* map, uint32_t stage, int x, int y,
+                    uint64_t pol) {
+      if constexpr (kPair)
+        ptx::tma_load_2d_pair(dst, map, ptx::cluster_addr(&full_bar[stage], 0), x, y, pol);
+      else
+        ptx::tma_load_2d(dst, map, &full_bar[stage], x, y, pol);
+    };
+    // Rows (k contiguous) or 64-wide chunks (M or N contiguous) past the end
+    // are read from the last valid ones instead: they only feed accumulator
+    // rows or columns that no epilogue reads.
+    auto load_a = [&](uint32_t stage, int kb, int mt) {
+      uint8_t* dst = smem + size_t(stage) * s.stage_bytes;
+      const int m0 = (mt * kCtas + rank) * kBM;
+      if constexpr (kAmn) {
+#pragma unroll
+        for (int i = 0; i < kBM / 64; ++i)
+          load(dst + i * kChunkBytes, &tmap_a, stage, min(m0 + 64 * i, (s.m_rows - 1) & ~63),
+               kb * kBK, pol_a);
+      } else {
+        load(dst, &tmap_a, stage, kb * kBK, min(m0, s.m_rows - 1), pol_a);
+      }
+    };
+    auto load_b = [&](uint32_t stage, int kb, int nt) {
+      uint8_t* dst = smem + size_t(stage) * s.stage_bytes + s.a_bytes;
+      const int n0 = nt * kBN + rank * kBRows;
+      if constexpr (kBmn) {
+#pragma unroll
+        for (int i = 0; i < kBRows / 64; ++i)
+          load(dst + i * kChunkBytes, &tmap_b, stage, min(n0 + 64 * i, (s.n_cols - 1) & ~63),
+               kb * kBK, pol_b);
+      } else {
+        load(dst, &tmap_b, stage, kb * kBK, min(n0, s.n_cols - 1), pol_b);
+      }
+    };
+    uint32_t stage = 0, phase = 0, issued = 0;
+    bool ok = true;
+    // The first ring fill's A copies, held back until the kernel before is done.
+    bool deferring = s.pdl != 0;
+    int n_held = 0, held_kb[kMaxStages], held_mt[kMaxStages];
+    auto release = [&]() {
+      ptx::grid_dependency_wait();
+      if (issuer)
+        for (int i = 0; i < n_held; ++i) load_a(uint32_t(i), held_kb[i], held_mt[i]);
+      deferring = false;
+    };
+    for (int u = worker; ok && u < s.n_units; u += n_workers) {
+      const Unit t = unit_of(s, u);
+      for (int kb = t.kb0; kb < t.kb0 + t.n_kb; ++kb) {
+        if (!waiter.wait_warp(&empty_bar[stage], phase ^ 1u)) {
+          ok = false;
+          break;
+        }
+        if (issuer) {
+          if (leader)
+            ptx::mbar_arrive_expect_tx(&full_bar[stage], kCtas * (s.a_bytes + kBBytes));
+          load_b(stage, kb, t.nt);
+          if (!deferring) load_a(stage, kb, t.mt);
+        }
+        if (deferring) {  // the first fill: stage n_held
+          held_kb[n_held] = kb;
+          held_mt[n_held++] = t.mt;
+        }
+        ++issued;
+        if (++stage == s.n_stages) {
+          stage = 0;
+          phase ^= 1u;
+        }
+        if (deferring && n_held == int(s.n_stages)) release();
+      }
+    }
+    if (deferring) release();
+    // Every issued copy lands before the CTA's shared memory goes away (the
+    // leader's barriers see both CTAs' copies).
+    if (leader) {
+      for (uint32_t i = 0; i < s.n_stages; ++i) {
+        const uint32_t fills = issued / s.n_stages + (i < issued % s.n_stages ? 1u : 0u);
+        if (fills) waiter.drain(&full_bar[i], (fills - 1u) & 1u);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ---------------- MMA issuer (the leader CTA's) ----------------
+    if (leader) {
+      const bool issuer = ptx::elect_one();
+      uint32_t stage = 0, phase = 0, acc = 0, acc_phase = 0;
+      bool ok = true;
+      const uint32_t s0 = ptx::smem_u32(smem);
+      // Descriptors of stage 0; stages and k steps only add to the start
+      // address (addresses stay below 256 KB, so the 14-bit field never carries).
+      const uint64_t desc_a0 =
+          kAmn ? ptx::smem_desc_sw128_mn(s0, kChunkBytes) : ptx::smem_desc_sw128(s0);
+      const uint64_t desc_b0 = kBmn ? ptx::smem_desc_sw128_mn(s0 + s.a_bytes, kChunkBytes)
+                                    : ptx::smem_desc_sw128(s0 + s.a_bytes);
+      constexpr uint64_t kStepA = kAmn ? 2048 >> 4 : (kUK * 2) >> 4;
+      constexpr uint64_t kStepB = kBmn ? 2048 >> 4 : (kUK * 2) >> 4;
+      auto commit = [&](uint64_t* bar) {
+        if constexpr (kPair)
+          ptx::mma_commit_pair_multicast(bar, 0x3);
+        else
+          ptx::mma_commit(bar);
+      };
+      for (int u = worker; ok && u < s.n_units; u += n_workers) {
+        const Unit t = unit_of(s, u);
+        if (!waiter.wait_warp(&tempty_bar[acc], acc_phase ^ 1u)) break;
+        ptx::tc_fence_after();
+        const uint32_t d_tmem = tmem_base + acc * kBN;
+        for (int kb = 0; kb < t.n_kb; ++kb) {
+          if (!waiter.wait_warp(&full_bar[stage], phase)) {
+            ok = false;
+            break;
+          }
+          ptx::tc_fence_after();
+          const uint64_t off = uint64_t(stage * (s.stage_bytes >> 4));
+          if (issuer) {
+#pragma unroll
+            for (int k = 0; k < kBK / kUK; ++k) {
+              const uint64_t da = desc_a0 + off + kStepA * k, db = desc_b0 + off + kStepB * k;
+              const uint32_t more = (kb | k) != 0 ? 1u : 0u;
+              if constexpr (kPair)
+                ptx::mma_bf16_pair(d_tmem, da, db, kIdesc, more);
+              else
+                ptx::mma_bf16(d_tmem, da, db, kIdesc, more);
+            }
+            commit(&empty_bar[stage]);
+          }
+          __syncwarp();
+          if (++stage == s.n_stages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+        if (!ok) break;
+        if (issuer) commit(&tfull_bar[acc]);
+        __syncwarp();
+        acc ^= 1u;
+        if (acc == 0) acc_phase ^= 1u;
+      }
+      // All MMAs complete before tensor memory is released.
+      if (issuer) {
+        if constexpr (kPair)
+          ptx::mma_commit_pair(drain_bar);
+        else
+          ptx::mma_commit(drain_bar);
+      }
+      __syncwarp();
+      waiter.drain(drain_bar, 0);
+    }
+    __syncwarp();
+  } else {
+    // ---------------- epilogue ----------------
+    if (s.pdl) ptx::grid_dependency_wait();  // its inputs may still be in flight
+    const int e = warp - 2;
+    const int quad = warp & 3;  // the tensor-memory lane quadrant this warp may read
+    const int half = e >> 2;
+    uint8_t* box = staging + e * 4096;
+    uint32_t acc = 0, acc_phase = 0;
+    typename Epi::State st;
+    Epi::start(ep, st);
+    for (int u = worker; u < s.n_units; u += n_workers) {
+      TileAt at;
+      at.unit = unit_of(s, u);
+      at.rank = rank;
+      at.quad = quad;
+      at.half = half;
+      at.row0 = (at.unit.mt * kCtas + rank) * kBM + quad * 32;
+      at.col0 = at.unit.nt * kBN + half * 128;
+      at.taddr = tmem_base + (uint32_t(quad * 32) << 16) + acc * kBN + uint32_t(half * 128);
+      int ok = 0;
+      if (lane == 0) ok = waiter.wait(&tfull_bar[acc], acc_phase) ? 1 : 0;
+      ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
+      if (!ok) break;
+      ptx::tc_fence_after();
+      if (at.row0 < s.m_rows && at.col0 < s.n_cols)
+        Epi::tile(ep, st, at, lane, box, &tmap_d, s);
+      ptx::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if constexpr (kPair)
+          ptx::mbar_arrive_cluster(ptx::cluster_addr(&tempty_bar[acc], 0));
+        else
+          ptx::mbar_arrive(&tempty_bar[acc]);
+      }
+      acc ^= 1u;
+      if (acc == 0) acc_phase ^= 1u;
+    }
+    Epi::finish(ep, st, worker, (unit_of(s, worker).mt * kCtas + rank) * kBM + quad * 32 + lane,
+                half, s);
+    if (Epi::kStaged && lane == 0) ptx::bulk_wait();
+  }
+
+  ptx::tc_fence_before();
+  __syncthreads();
+  // Both CTAs are done with each other's barriers and the MMAs have drained
+  // before the pair's tensor memory is released.
+  if constexpr (kPair) ptx::cluster_sync();
+  if (warp == 1) {
+    ptx::tc_fence_after();
+    if constexpr (kPair)
+      ptx::tmem_dealloc_pair(tmem_base, kTmemCols);
+    else
+      ptx::tmem_dealloc(tmem_base, kTmemCols);
+  }
+  if constexpr (kPair) ptx::cluster_sync();
+  // A kernel launched as this one's programmatic dependent may be scheduled as
+  // blocks finish; it waits for the whole grid before it reads anything.
+  ptx::grid_launch_dependents();
+}
+
+// ---------------------------------------------------------------------------
+// A bf16 tile through shared memory: the warp's 32 rows x 64 columns are
+// written in the store box's 128-byte swizzle (16-byte chunk c of row r at
+// chunk c ^ (r & 7), so a warp's writes touch every bank once) and one TMA
+// store takes them out, clipped at the tensor's edges.
+__device__ __forceinline__ void box_begin(int lane) {
+  if (lane == 0) ptx::bulk_wait_read();  // the box's last store has been read
+  __syncwarp();
+}
+// Columns [8c, 8c+8) of the lane's row.
+__device__ __forceinline__ void box_put(uint8_t* box, int lane, int c, const float (&v)[8]) {
+  __nv_bfloat162 h[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) h[i] = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+  *reinterpret_cast<uint4*>(box + lane * 128 + ((c ^ (lane & 7)) << 4)) =
+      *reinterpret_cast<const uint4*>(h);
+}
+__device__ __forceinline__ void box_end(uint8_t* box, const void* tmap, int lane, int x, int y) {
+  ptx::fence_async_smem();
+  __syncwarp();
+  if (lane == 0) {
+    ptx::tma_store_2d(tmap, box, x, y);
+    ptx::bulk_commit();
+  }
+}
+
+// The accumulator rounded to bf16 (once, to nearest even) and stored.  A TMA
+// store writes whole 16-byte pieces, so tmap_d covers the columns below whole_n
+// (a multiple of 8); the up to 7 columns behind are stored one by one, and
+// nothing past a row's end is touched.
+struct StoreEpi {
+  static constexpr bool kStaged = true;
+  struct Params {
+    __nv_bfloat16* out;
+    int64_t ld;
+    int32_t whole_n;
+  };
+  struct State {};
+  static __device__ __forceinline__ void start(const Params&, State&) {}
+  static __device__ __forceinline__ void tile(const Params& p, State&, const TileAt& at, int lane,
+                                              uint8_t* box, const void* tmap, const Shape& s) {
+#pragma unroll 1
+    for (int c = 0; c < 2; ++c) {
+      const int x0 = at.col0 + c * 64;
+      if (x0 >= s.n_cols) break;
+      uint32_t r[32];
+      box_begin(lane);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        ptx::tmem_ld_32x32b_x32(at.taddr + uint32_t(c * 64 + h * 32), r);
+        ptx::tmem_wait_ld();
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          float v[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[q * 8 + i]);
+          box_put(box, lane, h * 4 + q, v);
+          const int x = x0 + h * 32 + q * 8;
+          if (x == p.whole_n && at.row0 + lane < s.m_rows) {
+            __nv_bfloat16* out = p.out + int64_t(at.row0 + lane) * p.ld;
+#pragma unroll
+            for (int i = 0; i < 7; ++i)
+              if (x + i < s.n_cols) out[x + i] = __float2bfloat16_rn(v[i]);
+          }
+        }
+      }
+      if (x0 < p.whole_n) box_end(box, tmap, lane, x0, at.row0);
+    }
+  }
+  static __device__ __forceinline__ void finish(const Params&, State&, int, int, int,
+                                                const Shape&) {}
+};
+
+// One k split's fp32 accumulator, for a later sum in split order.  A CTA tile
+// (128 x 256) is stored as [64 column quads][128 rows] float4, so a warp's
+// 16-byte stores are contiguous.
+struct PartialEpi {
+  static constexpr bool kStaged = false;
+  struct Params {
+    float4* partial;
+    int32_t ctas;  // CTAs per tile
+  };
+  struct State {};
+  static __device__ __forceinline__ void start(const Params&, State&) {}
+  static __device__ __forceinline__ void tile(const Params& p, State&, const TileAt& at, int lane,
+                                              uint8_t*, const void*, const Shape& s) {
+    const int64_t slot =
+        (int64_t(at.unit.split) * s.n_mt * s.n_nt + int64_t(at.unit.mt) * s.n_nt + at.unit.nt) *
+            p.ctas + at.rank;
+    float4* out = p.partial + slot * (kBM * kBN / 4) + at.quad * 32 + lane;
+#pragma unroll 1
+    for (int c = 0; c < 4; ++c) {
+      uint32_t r[32];
+      ptx::tmem_ld_32x32b_x32(at.taddr + uint32_t(c * 32), r);
+      ptx::tmem_wait_ld();
+#pragma unroll
+      for (int q = 0; q < 8; ++q)
+        out[int64_t(at.half * 32 + c * 8 + q) * kBM] =
+            make_float4(__uint_as_float(r[4 * q]), __uint_as_float(r[4 * q + 1]),
+                        __uint_as_float(r[4 * q + 2]), __uint_as_float(r[4 * q + 3]));
+    }
+  }
+  static __device__ __forceinline__ void finish(const Params&, State&, int, int, int,
+                                                const Shape&) {}
+};
+
+}  // namespace vocab
+}  // namespace fs

@@ -652,6 +652,17 @@ namespace fs {
 // g_error_taken, ordered on the stream of the caller that asks for it.
 __device__ int g_error_taken = 0;
 __global__ void take_error_word_kernel() { g_error_taken = atomicExch(&g_error_word, 0); }
+
+// Device address of the error word on the current device, for the kernels of
+// other source files; null if it cannot be had.
+int* device_error_word() {
+  void* p = nullptr;
+  if (cudaGetSymbolAddress(&p, g_error_word) != cudaSuccess) {
+    cudaGetLastError();
+    return nullptr;
+  }
+  return static_cast<int*>(p);
+}
 }  // namespace fs
 
 extern "C" fs_status fs_last_device_error(void* stream_ptr, int* code) {

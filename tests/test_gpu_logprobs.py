@@ -1,0 +1,414 @@
+"""Token log-probabilities, entropy, alternatives and their gradient on the GPU
+against 64-bit forms, within the bounds derived in vocab_ref.py; alternatives'
+ids are compared exactly."""
+import math
+
+import pytest
+import torch
+
+import lm_head_gumbel_gb300 as fs
+from lm_head_gumbel_gb300 import workloads as wl
+import vocab_ref as ref
+from gpu_cases import assert_no_device_error
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    fs.load_library()
+    yield
+    assert_no_device_error()
+
+
+def padded(t):
+    """The same matrix with rows at a stride of 8 elements more than needed."""
+    n, d = t.shape
+    out = torch.full((n, (d + 7) // 8 * 8 + 8), 7.0, dtype=t.dtype, device=t.device)
+    out[:, :d] = t
+    return out[:, :d]
+
+
+def problem(B, d, V, *, T=None, mask_frac=0.0, seed=0):
+    H = padded(wl.make_hidden(B, d, seed=10 + seed, device="cuda"))
+    W = padded(wl.make_weights(d, V, seed=20 + seed, device="cuda"))
+    gen = torch.Generator().manual_seed(30 + seed)
+    tokens = torch.randint(0, V, (B,), generator=gen)
+    temp = None
+    if T == "rows":
+        temp = torch.rand(B, generator=gen) + 0.5
+        temp[::3] = 0.0  # greedy rows are scored at T = 1
+        temp = temp.cuda()
+    elif T is not None:
+        temp = torch.full((B,), float(T), device="cuda")
+    mask = wl.make_mask(B, V, mask_frac, seed=40 + seed, device="cuda") if mask_frac else None
+    return dict(H=H, W=W, tokens=tokens.cuda(), temperature=temp, vocab_mask=mask)
+
+
+def near(got, want, bound, what):
+    got, want = got.detach().cpu().double(), want.double()
+    inf = torch.isinf(want)
+    assert torch.equal(got[inf], want[inf]), what
+    off = (got - want).abs()[~inf]
+    assert not torch.isnan(off).any(), what
+    bound = bound if not torch.is_tensor(bound) else bound[~inf]
+    assert bool((off <= bound).all()), (what, float(off.max()), float((off / bound).max()))
+
+
+def check_forward(p, K, **kw):
+    r = fs.fs_logprobs(p["H"], p["W"], p["tokens"], K, temperature=p["temperature"],
+                       vocab_mask=p["vocab_mask"], **kw)
+    w = ref.forward(p["H"], p["W"], p["tokens"], K, p["temperature"], p["vocab_mask"],
+                    kw.get("vocab_offset", 0))
+    near(r.lse, w["lse"], w["e_lse"], "lse")
+    near(r.entropy, w["entropy"], w["e_entropy"], "entropy")
+    near(r.logp, w["logp"], w["e_lse"] + 2 * ref.U * w["logp"].abs(), "logp")
+    if K:
+        assert torch.equal(r.topk_idx.cpu(), w["topk_idx"])
+        near(r.topk_logp, w["topk_logp"], w["e_lse"] + 2 * ref.U * w["topk_logp"].abs(),
+             "topk_logp")
+    return r, w
+
+
+# One row to several launches; one vocabulary block to several per worker; k
+# slices, tiles, 16-byte vectors and mask words that end early.
+SHAPES = [(1, 8, 1), (1, 64, 100), (2, 3, 33), (3, 100, 257), (5, 320, 1000), (64, 256, 4096),
+          (128, 72, 513), (129, 64, 300), (257, 129, 511), (300, 264, 1003), (700, 72, 2001),
+          (1300, 64, 600), (4, 128, 40001), (140, 64, 20011)]
+
+
+@pytest.mark.parametrize("B,d,V", SHAPES)
+@pytest.mark.parametrize("K", [0, 3, 20])
+def test_forward(B, d, V, K):
+    check_forward(problem(B, d, V, T="rows", seed=B + V + K), K)
+
+
+@pytest.mark.parametrize("B,d,V", [(5, 64, 1000), (130, 64, 700)])
+@pytest.mark.parametrize("K", [1, 2, 4, 5, 16, 19])
+def test_every_list_capacity(B, d, V, K):
+    check_forward(problem(B, d, V, T=0.7, seed=K), K)
+
+
+@pytest.mark.parametrize("B,d,V", [(3, 100, 257), (128, 72, 513), (300, 264, 1003)])
+@pytest.mark.parametrize("frac", [0.05, 0.97])
+def test_masks(B, d, V, frac):
+    p = problem(B, d, V, T="rows", mask_frac=frac, seed=V)
+    p["vocab_mask"][0] = 0                      # a row that allows nothing
+    p["vocab_mask"][1] = 0
+    p["vocab_mask"][1, 2] = 1 << 5              # a row that allows one id
+    p["tokens"][1] = 69
+    r, w = check_forward(p, 20)
+    assert r.lse[0].item() == -math.inf and r.entropy[0].item() == 0.0
+    assert r.logp[0].item() == -math.inf and bool((r.topk_idx[0] == -1).all())
+    assert r.entropy[1].item() == 0.0 and r.topk_idx[1, 0].item() == 69
+    assert abs(r.logp[1].item()) <= w["e_lse"]
+
+
+@pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf, 3e38])
+def test_values_behind_the_mask_change_nothing(bad):
+    p = problem(6, 96, 700, mask_frac=0.1, seed=5)
+    gone = torch.tensor([0, 31, 32, 255, 256, 699], device="cuda")
+    for v in gone.tolist():
+        word = ~torch.tensor(1 << (v % 32), dtype=torch.int64).to(torch.int32)
+        p["vocab_mask"][:, v // 32] &= word.cuda()
+    want = fs.fs_logprobs(p["H"], p["W"], p["tokens"], 20, vocab_mask=p["vocab_mask"])
+    p["W"][gone] = bad
+    got = fs.fs_logprobs(p["H"], p["W"], p["tokens"], 20, vocab_mask=p["vocab_mask"])
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+
+
+def test_non_finite_logits_of_allowed_ids():
+    p = problem(4, 64, 500, seed=6)
+    p["H"][1, 3] = math.nan
+    p["W"][77] = -math.inf
+    p["H"][:, :] = p["H"].abs()      # every logit of id 77 is -inf, but row 1's (NaN)
+    p["tokens"][:] = torch.tensor([77, 5, 6, 7], device="cuda")
+    r = fs.fs_logprobs(p["H"], p["W"], p["tokens"], 5)
+    assert bool(torch.isnan(r.lse[1])) and bool(torch.isnan(r.entropy[1]))
+    assert bool(torch.isnan(r.logp[1]))
+    ok = [0, 2, 3]
+    assert bool(torch.isfinite(r.lse[ok]).all()) and bool(torch.isfinite(r.entropy[ok]).all())
+    assert r.logp[0].item() == -math.inf
+    assert not bool((r.topk_idx[ok] == 77).any())
+    p["W"][78] = math.inf            # and one of +inf
+    r = fs.fs_logprobs(p["H"], p["W"], p["tokens"], 5)
+    assert bool(torch.isnan(r.lse).all()) and bool(torch.isnan(r.topk_logp[ok]).all())
+    assert bool((r.topk_idx[ok, 0] == 78).all())
+
+
+def test_special_tokens_and_shards():
+    """-1: no token.  A vocabulary in three shards: lse and alternatives join to
+    the whole call's, and a token's log-probability is its shard's."""
+    p = problem(9, 128, 1500, T=0.8, seed=8)
+    p["tokens"][2] = -1
+    p["tokens"][3] = -100
+    whole, _ = check_forward(p, 8)
+    assert whole.logp[2].item() == 0.0 and whole.logp[3].item() == 0.0
+    parts, lo = [], 0
+    for hi in (512, 611, 1500):
+        q = dict(p, W=p["W"][lo:hi])
+        parts.append(check_forward(q, 8, vocab_offset=lo)[0])
+        lo = hi
+    lse = torch.logsumexp(torch.stack([r.lse.double() for r in parts]), 0)
+    assert bool(((lse - whole.lse).abs() < 1e-5).all())
+    logp = torch.stack([r.logp.double() + r.lse - lse for r in parts]).max(0).values
+    named = p["tokens"] >= 0
+    assert bool(((logp - whole.logp).abs()[named] < 1e-5).all())
+    ids = torch.cat([r.topk_idx for r in parts], 1)
+    val = torch.cat([r.topk_logp.double() + (r.lse - lse).unsqueeze(1) for r in parts], 1)
+    at = val.sort(dim=1, descending=True, stable=True).indices[:, :8]
+    assert torch.equal(ids.gather(1, at), whole.topk_idx)
+    r = fs.fs_logprobs(p["H"], p["W"], torch.full_like(p["tokens"], 1500))
+    assert bool((r.logp == -math.inf).all())
+
+
+def test_ties_go_to_the_lower_id():
+    """Equal logits everywhere, and copies of the best row in other tiles."""
+    p = problem(130, 64, 5000, seed=9)
+    zero = torch.zeros_like(p["H"])
+    r = fs.fs_logprobs(zero, p["W"], p["tokens"], 20)
+    assert torch.equal(r.topk_idx.cpu(), torch.arange(20).expand(130, 20))
+    near(r.entropy, torch.full((130,), math.log(5000.0), dtype=torch.float64), 1e-4, "entropy")
+    W = p["W"]
+    W[:] = W * 0.25
+    best = 2 * p["H"][7].clone()
+    at = torch.arange(130, 4990, 37)          # 132 equal rows, best for row 7
+    W[at.cuda()] = best
+    r = fs.fs_logprobs(p["H"], W, p["tokens"], 20)
+    assert torch.equal(r.topk_idx[7].cpu(), at[:20])
+    one = fs.fs_logprobs(p["H"][7:8], W, p["tokens"][7:8], 20)  # the single-CTA kernel
+    assert torch.equal(one.topk_idx[0].cpu(), at[:20])
+
+
+def test_near_ties_rank_by_exact_logit():
+    """24 ids whose logits differ by less than fp32 resolves at their size: in
+    64 bits the order is known by construction."""
+    d, V = 512, 3000
+    gen = torch.Generator().manual_seed(3)
+    h = torch.ones(1, d)
+    W = (torch.randn((V, d), generator=gen) * 0.01).bfloat16()
+    ids = torch.randperm(V, generator=gen)[:24]
+    for j, v in enumerate(ids.tolist()):
+        W[v] = 8.0                            # the logit is 4096 but for
+        W[v, 100] = 8.0 + 0.0625 * (j % 2)    # coarse steps
+        W[v, 7] = 2.0 ** -16 * (24 - j)       # and steps of 2^-16, an ulp of 4088 being 2^-12
+    H = h.bfloat16().cuda()
+    tokens = torch.zeros(1, dtype=torch.int64, device="cuda")
+    r = fs.fs_logprobs(H, W.cuda(), tokens, 20)
+    l = W.double().sum(1)
+    want = sorted(range(V), key=lambda v: (-l[v].item(), v))[:20]
+    assert r.topk_idx[0].tolist() == want
+    assert len(set(l[ids].float().tolist())) < 24
+
+
+def test_same_results_on_other_streams_in_graphs_and_overlapped():
+    p = problem(200, 128, 3000, T="rows", mask_frac=0.05, seed=11)
+    args = dict(temperature=p["temperature"], vocab_mask=p["vocab_mask"])
+    want = fs.fs_logprobs(p["H"], p["W"], p["tokens"], 10, **args)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        got = fs.fs_logprobs(p["H"], p["W"], p["tokens"], 10, **args)
+    again = fs.fs_logprobs(p["H"], p["W"], p["tokens"], 10, stream=side, **args)
+    side.synchronize()
+    for r in (got, again):
+        assert all(torch.equal(a, b) for a, b in zip(r, want))
+    # H written by the kernel before, on the same stream
+    for rows in (200, 64):
+        w2 = fs.fs_logprobs(p["H"][:rows], p["W"], p["tokens"][:rows], 10,
+                            temperature=p["temperature"][:rows], vocab_mask=p["vocab_mask"][:rows])
+        for _ in range(5):
+            H2 = torch.empty_like(p["H"][:rows])
+            H2.copy_(p["H"][:rows])
+            r = fs.fs_logprobs(H2, p["W"], p["tokens"][:rows], 10, overlap_previous=True,
+                               temperature=p["temperature"][:rows],
+                               vocab_mask=p["vocab_mask"][:rows])
+            assert all(torch.equal(a, b) for a, b in zip(r, w2))
+    ws = torch.empty(fs.fs_logprobs_workspace_size(200, 3000, 10), dtype=torch.uint8,
+                     device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        r = fs.fs_logprobs(p["H"], p["W"], p["tokens"], 10, workspace=ws, **args)
+    for _ in range(3):
+        ws.fill_(255)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(r, want))
+
+
+def test_rows_do_not_depend_on_the_batch():
+    """Alternatives of a row are the same alone, in a batch and in a large one."""
+    p = problem(600, 256, 9000, seed=12)
+    big = fs.fs_logprobs(p["H"], p["W"], p["tokens"], 20)
+    for rows in (1, 100, 300):
+        r = fs.fs_logprobs(p["H"][:rows], p["W"], p["tokens"][:rows], 20)
+        assert torch.equal(r.topk_idx, big.topk_idx[:rows])
+
+
+def test_logp_agrees_with_the_sampler():
+    """The token that greedy sampling picks is the first alternative."""
+    p = problem(33, 256, 5000, seed=13)
+    ids = fs.fs_sample(p["H"], p["W"], temperature=torch.zeros(33, device="cuda"))
+    r = fs.fs_logprobs(p["H"], p["W"], ids, 2)
+    gap = (r.topk_logp[:, 0] - r.topk_logp[:, 1]) > 1e-2
+    assert int(gap.sum()) > 20
+    assert torch.equal(r.topk_idx[gap, 0], ids[gap])
+    assert torch.equal(r.logp[gap], r.topk_logp[gap, 0])
+
+
+# --------------------------------------------------------------------------- gradient
+def upstream(B, entropy, seed):
+    gen = torch.Generator().manual_seed(50 + seed)
+    a = torch.randn(B, generator=gen).cuda()
+    e = torch.randn(B, generator=gen).cuda() if entropy else None
+    return a, e
+
+
+def check_gradient(p, a, e, **kw):
+    f = fs.fs_logprobs(p["H"], p["W"], p["tokens"], temperature=p["temperature"],
+                       vocab_mask=p["vocab_mask"])
+    dH, dW = fs.fs_logprobs_grad(p["H"], p["W"], p["tokens"], f.lse, a,
+                                 entropy=f.entropy if e is not None else None, grad_entropy=e,
+                                 temperature=p["temperature"], vocab_mask=p["vocab_mask"], **kw)
+    wH, bH, wW, bW, G = ref.gradient(p["H"], p["W"], p["tokens"], a, e, p["temperature"],
+                                     p["vocab_mask"])
+    if dH is not None:
+        near(dH, wH, bH, "dH")
+    if dW is not None:
+        near(dW, wW, bW, "dW")
+    return dH, dW, wH, bH, wW, bW
+
+
+@pytest.mark.parametrize("B,d,V", SHAPES)
+@pytest.mark.parametrize("entropy", [False, True])
+def test_gradient(B, d, V, entropy):
+    p = problem(B, d, V, T="rows", seed=B + V)
+    check_gradient(p, *upstream(B, entropy, V))
+
+
+@pytest.mark.parametrize("B,d,V", [(3, 100, 257), (128, 72, 513), (300, 264, 1003)])
+def test_gradient_with_masks(B, d, V):
+    p = problem(B, d, V, T="rows", mask_frac=0.3, seed=V)
+    p["vocab_mask"][0] = 0
+    p["vocab_mask"][1] = 0
+    p["vocab_mask"][1, 2] = 1 << 5
+    p["tokens"][1] = 69
+    p["tokens"][2] = -1
+    dH, dW, *_ = check_gradient(p, *upstream(B, True, V))
+    assert bool((dH[0] == 0).all())
+
+
+def test_gradient_against_differences():
+    """Along a random direction, the 64-bit loss's central difference."""
+    p = problem(7, 40, 300, T=0.9, mask_frac=0.1, seed=14)
+    a, e = upstream(7, True, 14)
+    dH, dW, wH, bH, wW, bW = check_gradient(p, a, e)
+    gen = torch.Generator().manual_seed(15)
+    H, W = p["H"].cpu().double(), p["W"].cpu().double()
+    held = ref.forward(H, W, p["tokens"], 0, p["temperature"], p["vocab_mask"])["held"]
+
+    def loss(Hx, Wx):
+        f = ref.forward(Hx, Wx, p["tokens"], 0, p["temperature"], p["vocab_mask"])
+        lp = torch.where(held, f["logp"], 0.0)
+        return float((a.cpu().double() * lp).sum() + (e.cpu().double() * f["entropy"]).sum())
+
+    h = 1e-5
+    for which, (g, bound) in enumerate(((dH, bH), (dW, bW))):
+        D = torch.randn(g.shape, generator=gen, dtype=torch.float64)
+        step = [(D * h, 0.0), (0.0, D * h)][which]
+        diff = (loss(H + step[0], W + step[1]) - loss(H - step[0], W - step[1])) / (2 * h)
+        got = float((g.cpu().double() * D).sum())
+        # the elementwise bounds, and the difference's own error (h^2, 1e-16/h)
+        assert abs(got - diff) <= float((bound * D.abs()).sum()) + 1e-6 * abs(diff) + 1e-8
+
+
+def test_gradient_of_shards_adds_up():
+    p = problem(6, 72, 900, T=0.8, seed=16)
+    a, e = upstream(6, True, 16)
+    f = fs.fs_logprobs(p["H"], p["W"], p["tokens"], temperature=p["temperature"])
+    wH, bH, wW, bW, _ = ref.gradient(p["H"], p["W"], p["tokens"], a, e, p["temperature"])
+    total = torch.zeros(6, 72, dtype=torch.float64)
+    rounding = torch.zeros(6, 72, dtype=torch.float64)
+    lo = 0
+    for hi in (128, 131, 900):
+        dH, dW = fs.fs_logprobs_grad(p["H"], p["W"][lo:hi], p["tokens"], f.lse, a,
+                                     entropy=f.entropy, grad_entropy=e,
+                                     temperature=p["temperature"], vocab_offset=lo)
+        near(dW, wW[lo:hi], bW[lo:hi], "dW")
+        total += dH.cpu().double()
+        rounding += dH.cpu().double().abs() * ref.BF16 * 2  # each shard's own result
+        lo = hi
+    assert bool(((total - wH).abs() <= bH + rounding).all())
+
+
+def test_gradient_parts_and_given_outputs():
+    """dH or dW alone, into given strided outputs, leave everything else alone."""
+    p = problem(70, 100, 1000, seed=17)
+    a, _ = upstream(70, False, 17)
+    dH, dW, *_ = check_gradient(p, a, None)
+    bufH = torch.full((72, 112), 3.0, dtype=torch.bfloat16, device="cuda")
+    bufW = torch.full((1002, 112), 3.0, dtype=torch.bfloat16, device="cuda")
+    f = fs.fs_logprobs(p["H"], p["W"], p["tokens"])
+    r = fs.fs_logprobs_grad(p["H"], p["W"], p["tokens"], f.lse, a, out_dH=bufH[:70, :100],
+                            need_dW=False)
+    assert r[1] is None and torch.equal(bufH[:70, :100], dH)
+    r = fs.fs_logprobs_grad(p["H"], p["W"], p["tokens"], f.lse, a, out_dW=bufW[:1000, :100],
+                            need_dH=False)
+    assert r[0] is None and torch.equal(bufW[:1000, :100], dW)
+    for buf, n in ((bufH, 70), (bufW, 1000)):
+        assert bool((buf[n:] == 3.0).all()) and bool((buf[:, 100:] == 3.0).all())
+
+
+def test_gradient_in_a_graph_and_on_a_stream():
+    p = problem(300, 136, 2000, T="rows", seed=18)
+    a, e = upstream(300, True, 18)
+    f = fs.fs_logprobs(p["H"], p["W"], p["tokens"], temperature=p["temperature"])
+    call = dict(entropy=f.entropy, grad_entropy=e, temperature=p["temperature"])
+    want = fs.fs_logprobs_grad(p["H"], p["W"], p["tokens"], f.lse, a, **call)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    got = fs.fs_logprobs_grad(p["H"], p["W"], p["tokens"], f.lse, a, stream=side, **call)
+    side.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip(got, want))
+    ws = torch.empty(fs.fs_logprobs_grad_workspace_size(300, 136, 2000), dtype=torch.uint8,
+                     device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = fs.fs_logprobs_grad(p["H"], p["W"], p["tokens"], f.lse, a, workspace=ws, **call)
+    for _ in range(3):
+        ws.fill_(255)  # NaN in bf16: nothing unwritten is read
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(got, want))
+
+
+def test_binding_refusals():
+    p = problem(4, 64, 500, seed=19)
+    f = fs.fs_logprobs(p["H"], p["W"], p["tokens"])
+    bad = [
+        lambda: fs.fs_logprobs(p["H"].float(), p["W"], p["tokens"]),
+        lambda: fs.fs_logprobs(p["H"], p["W"][:, :32], p["tokens"]),
+        lambda: fs.fs_logprobs(p["H"], p["W"], p["tokens"][:3]),
+        lambda: fs.fs_logprobs(p["H"], p["W"], p["tokens"].int()),
+        lambda: fs.fs_logprobs(p["H"], p["W"], p["tokens"].cpu()),
+        lambda: fs.fs_logprobs(p["H"], p["W"], p["tokens"], 21),
+        lambda: fs.fs_logprobs(p["H"], p["W"], p["tokens"], temperature=torch.ones(4).cuda().double()),
+        lambda: fs.fs_logprobs(p["H"], p["W"], p["tokens"],
+                               vocab_mask=torch.zeros((4, 15), dtype=torch.int32, device="cuda")),
+        lambda: fs.fs_logprobs(p["H"], p["W"], p["tokens"], 4,
+                               out_topk_idx=torch.zeros((4, 5), dtype=torch.int64, device="cuda")),
+        lambda: fs.fs_logprobs(p["H"], p["W"], p["tokens"],
+                               workspace=torch.empty(16, dtype=torch.uint8, device="cuda")),
+        lambda: fs.fs_logprobs_grad(p["H"], p["W"], p["tokens"], f.lse, f.lse, grad_entropy=f.lse),
+        lambda: fs.fs_logprobs_grad(p["H"], p["W"], p["tokens"], f.lse, f.lse, need_dH=False,
+                                    need_dW=False),
+        lambda: fs.fs_logprobs_grad(p["H"], p["W"], p["tokens"], f.lse.double(), f.lse),
+        lambda: fs.fs_logprobs_grad(p["H"], p["W"], p["tokens"], f.lse, f.lse,
+                                    out_dH=torch.empty((4, 65), dtype=torch.bfloat16, device="cuda")),
+    ]
+    for call in bad:
+        with pytest.raises(fs.FsError):
+            call()
