@@ -29,106 +29,132 @@ namespace fs {
 namespace embed {
 namespace {
 
-constexpr int kCols = 8;  // columns a lane works on
-
 __device__ __forceinline__ float to_float(float v) { return v; }
 __device__ __forceinline__ float to_float(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ void put(float* p, float v) { *p = v; }
+__device__ __forceinline__ void put(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 
-// Eight columns from `col` of a row of d, in fp32; `vec`: the row starts on a
-// 16-byte boundary (col is a multiple of 8).  Columns past d read as 0.
-__device__ __forceinline__ void load8(const __nv_bfloat16* row, int col, int d, bool vec,
-                                      float (&v)[kCols]) {
-  if (vec && col + kCols <= d) {
-    const uint4 a = __ldg(reinterpret_cast<const uint4*>(row + col));
-    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+// C columns of a row from p, as loaded (C = 8: 16-byte loads, p on a 16-byte
+// boundary; C = 1: one element).  Loading and converting are apart so that a
+// warp's loads of several rows are all in flight before the first is used.
+template <typename T, int C>
+struct Piece;
+template <typename T>
+struct Piece<T, 1> {
+  T v;
+  __device__ __forceinline__ void load(const T* p) { v = *p; }
+  __device__ __forceinline__ void get(float (&f)[1]) const { f[0] = to_float(v); }
+};
+template <>
+struct Piece<__nv_bfloat16, 8> {
+  uint4 v;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) {
+    v = *reinterpret_cast<const uint4*>(p);
+  }
+  __device__ __forceinline__ void get(float (&f)[8]) const {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      v[2 * i] = __uint_as_float(w[i] << 16);
-      v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+      f[2 * i] = __uint_as_float(w[i] << 16);
+      f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
     }
-  } else {
-#pragma unroll
-    for (int i = 0; i < kCols; ++i) v[i] = col + i < d ? to_float(row[col + i]) : 0.0f;
   }
+};
+template <>
+struct Piece<float, 8> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float* p) {
+    a = reinterpret_cast<const float4*>(p)[0];
+    b = reinterpret_cast<const float4*>(p)[1];
+  }
+  __device__ __forceinline__ void get(float (&f)[8]) const {
+    f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w;
+    f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+  }
+};
+template <typename T>
+__device__ __forceinline__ void store(T* p, const float (&f)[1]) {
+  put(p, f[0]);
 }
-__device__ __forceinline__ void load8(const float* row, int col, int d, bool vec,
-                                      float (&v)[kCols]) {
-  if (vec && col + kCols <= d) {
-    const float4 a = __ldg(reinterpret_cast<const float4*>(row + col));
-    const float4 b = __ldg(reinterpret_cast<const float4*>(row + col) + 1);
-    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
-    v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-  } else {
+__device__ __forceinline__ void store(__nv_bfloat16* p, const float (&f)[8]) {
+  __nv_bfloat162 h[4];
 #pragma unroll
-    for (int i = 0; i < kCols; ++i) v[i] = col + i < d ? row[col + i] : 0.0f;
-  }
+  for (int i = 0; i < 4; ++i) h[i] = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+  *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(h);
 }
-__device__ __forceinline__ void store8(__nv_bfloat16* row, int col, int d, bool vec,
-                                       const float (&v)[kCols]) {
-  if (vec && col + kCols <= d) {
-    __nv_bfloat162 h[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) h[i] = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-    *reinterpret_cast<uint4*>(row + col) = *reinterpret_cast<const uint4*>(h);
-  } else {
-#pragma unroll
-    for (int i = 0; i < kCols; ++i)
-      if (col + i < d) row[col + i] = __float2bfloat16_rn(v[i]);
-  }
+__device__ __forceinline__ void store(float* p, const float (&f)[8]) {
+  reinterpret_cast<float4*>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
+  reinterpret_cast<float4*>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
 }
-__device__ __forceinline__ void store8(float* row, int col, int d, bool vec,
-                                       const float (&v)[kCols]) {
-  if (vec && col + kCols <= d) {
-    reinterpret_cast<float4*>(row + col)[0] = make_float4(v[0], v[1], v[2], v[3]);
-    reinterpret_cast<float4*>(row + col)[1] = make_float4(v[4], v[5], v[6], v[7]);
-  } else {
-#pragma unroll
-    for (int i = 0; i < kCols; ++i)
-      if (col + i < d) row[col + i] = v[i];
-  }
+
+// How a row's columns are divided among warps: columns below `vec` (a multiple
+// of 8; 0 where rows do not start on 16-byte boundaries) in segments of 8
+// columns a lane and G groups of lanes, the rest in segments of one column a
+// lane.  A warp works on one segment, so its path is uniform.
+struct Columns {
+  int32_t d, vec, vec_segments, segments;
+};
+__host__ Columns columns_of(int64_t d, bool vec, int groups) {
+  Columns c;
+  c.d = int32_t(d);
+  c.vec = vec ? int32_t(d & ~int64_t(7)) : 0;
+  c.vec_segments = (c.vec + 256 * groups - 1) / (256 * groups);
+  c.segments = c.vec_segments + (c.d - c.vec + 32 * groups - 1) / (32 * groups);
+  return c;
 }
 
 // ---------------------------------------------------------------------------
 // Lookup
 // ---------------------------------------------------------------------------
 constexpr int kLookupThreads = 128;
-constexpr int kLookupGroups = 4;  // 8-column groups per lane
+constexpr int kLookupGroups = 4;
+
+// G pieces of C columns from col0, 32 C apart, of one row.
+template <typename T, int C>
+__device__ __forceinline__ void lookup_piece(const T* src, T* dst, int col0, int end, bool held,
+                                             float scale) {
+  Piece<T, C> piece[kLookupGroups];
+  if (held) {
+#pragma unroll
+    for (int g = 0; g < kLookupGroups; ++g) {
+      const int col = col0 + g * 32 * C;
+      piece[g].load(src + (col < end ? col : 0));  // always a column of the row
+    }
+  }
+#pragma unroll
+  for (int g = 0; g < kLookupGroups; ++g) {
+    const int col = col0 + g * 32 * C;
+    if (col >= end) break;
+    float v[C] = {};
+    if (held) {
+      piece[g].get(v);
+#pragma unroll
+      for (int i = 0; i < C; ++i) v[i] *= scale;
+    }
+    store(dst + col, v);
+  }
+}
 
 template <typename T>
 __global__ void __launch_bounds__(kLookupThreads)
     lookup_kernel(const int64_t* __restrict__ ids, int64_t N, const T* __restrict__ E, int32_t V,
-                  int32_t d, int64_t lde, float scale, int64_t vocab_offset, T* __restrict__ out,
-                  int64_t ldo, int32_t segments, int vec_in, int vec_out) {
+                  int64_t lde, float scale, int64_t vocab_offset, T* __restrict__ out,
+                  int64_t ldo, const Columns cols) {
   const int lane = threadIdx.x & 31;
   const int64_t item = (int64_t(blockIdx.x) * kLookupThreads + threadIdx.x) >> 5;
-  const int64_t n = item / segments;
+  const int64_t n = item / cols.segments;
   if (n >= N) return;
-  const int col0 = int(item - n * segments) * (32 * kLookupGroups * kCols) + lane * kCols;
+  const int seg = int(item - n * cols.segments);
   const int64_t id = ids[n] - vocab_offset;
   const bool held = id >= 0 && id < V;
   const T* src = E + (held ? id : 0) * lde;
   T* dst = out + n * ldo;
-  float v[kLookupGroups][kCols];
-#pragma unroll
-  for (int g = 0; g < kLookupGroups; ++g) {
-    const int col = col0 + g * 32 * kCols;
-    if (held && col < d) {
-      load8(src, col, d, vec_in != 0, v[g]);
-    } else {
-#pragma unroll
-      for (int i = 0; i < kCols; ++i) v[g][i] = 0.0f;
-    }
-  }
-#pragma unroll
-  for (int g = 0; g < kLookupGroups; ++g) {
-    const int col = col0 + g * 32 * kCols;
-    if (col >= d) break;
-    if (held) {
-#pragma unroll
-      for (int i = 0; i < kCols; ++i) v[g][i] *= scale;
-    }
-    store8(dst, col, d, vec_out != 0, v[g]);
-  }
+  if (seg < cols.vec_segments)
+    lookup_piece<T, 8>(src, dst, seg * (256 * kLookupGroups) + lane * 8, cols.vec, held, scale);
+  else
+    lookup_piece<T, 1>(src, dst,
+                       cols.vec + (seg - cols.vec_segments) * (32 * kLookupGroups) + lane, cols.d,
+                       held, scale);
 }
 
 // ---------------------------------------------------------------------------
@@ -139,7 +165,7 @@ constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kCluster = 8;
 constexpr int kMaxBits = 9;  // of a radix digit
 constexpr int kBins = 1 << kMaxBits;
-constexpr int kFillRows = 1 << 16;  // rows whose marks a fill CTA holds at once
+constexpr int kFillRows = 1 << 16;  // rows whose marks a CTA holds at once
 
 struct SortParams {
   const int64_t* ids;
@@ -148,9 +174,10 @@ struct SortParams {
   int32_t bits, passes;  // digit width, number of passes
   uint32_t* key[2];      // [N] ping-pong; the result is in [passes & 1]
   uint32_t* pos[2];
-  uint8_t* fill;  // rows to zero (null: none), strides and lengths in bytes
-  int64_t fill_ld;
-  int64_t fill_row;
+  // When the whole table is written (else null):
+  uint8_t* table;
+  int64_t table_ld, row_bytes;
+  int64_t fill_rows;  // zero the unnamed ones of the first rows here
 };
 
 // An id as a row of the table, V where the table has no such row.
@@ -257,37 +284,40 @@ __device__ void sort_cluster(const SortParams& p, uint32_t rank) {
   }
 }
 
-// CTA `part` of `parts` zeroes its share of the rows that no id names: it marks
-// the named ones of its range in shared memory (one pass over the ids), then
-// writes the others, a warp per row.
+// A row's zeros by one warp: two bytes at a time up to a 16-byte boundary, 16 at
+// a time from there.
+__device__ __forceinline__ void zero_row(uint8_t* row, int64_t bytes, int lane) {
+  const int64_t head =
+      min(int64_t((16u - uint32_t(reinterpret_cast<uintptr_t>(row) & 15u)) & 15u), bytes);
+  const int64_t n16 = (bytes - head) / 16, tail = head + n16 * 16;
+  for (int64_t i = lane * 2; i < head; i += 64) *reinterpret_cast<uint16_t*>(row + i) = 0;
+  for (int64_t i = lane; i < n16; i += 32)
+    reinterpret_cast<uint4*>(row + head)[i] = make_uint4(0u, 0u, 0u, 0u);
+  for (int64_t i = tail + lane * 2; i < bytes; i += 64) *reinterpret_cast<uint16_t*>(row + i) = 0;
+}
+
+// CTA `part` of `parts` zeroes its share of the first fill_rows rows, but those
+// that some id names: it marks them in shared memory (one pass over the ids),
+// then a warp zeroes a row.
 __device__ void fill_rows(const SortParams& p, int part, int parts) {
   __shared__ uint32_t marks[kFillRows / 32];
-  const int64_t per = (int64_t(p.V) + parts - 1) / parts;
-  const int64_t r0 = int64_t(part) * per, r1 = min(r0 + per, int64_t(p.V));
+  const int64_t per = (p.fill_rows + parts - 1) / parts;
+  const int64_t r0 = int64_t(part) * per, r1 = min(r0 + per, p.fill_rows);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   for (int64_t b0 = r0; b0 < r1; b0 += kFillRows) {
     const int rows = int(min(int64_t(kFillRows), r1 - b0));
     __syncthreads();
     for (int i = threadIdx.x; i < (rows + 31) / 32; i += kSortThreads) marks[i] = 0u;
     __syncthreads();
+#pragma unroll 8
     for (int i = threadIdx.x; i < p.N; i += kSortThreads) {
       const int64_t r = int64_t(row_of(p, p.ids[i])) - b0;
       if (r >= 0 && r < rows) atomicOr(&marks[r >> 5], 1u << (r & 31));
     }
     __syncthreads();
-    for (int r = warp; r < rows; r += kSortWarps) {
-      if ((marks[r >> 5] >> (r & 31)) & 1u) continue;
-      // Two bytes at a time up to a 16-byte boundary, 16 at a time from there.
-      uint8_t* row = p.fill + (b0 + r) * p.fill_ld;
-      const int64_t head =
-          min(int64_t((16u - uint32_t(reinterpret_cast<uintptr_t>(row) & 15u)) & 15u), p.fill_row);
-      const int64_t n16 = (p.fill_row - head) / 16, tail = head + n16 * 16;
-      for (int64_t i = lane * 2; i < head; i += 64) *reinterpret_cast<uint16_t*>(row + i) = 0;
-      for (int64_t i = lane; i < n16; i += 32)
-        reinterpret_cast<uint4*>(row + head)[i] = make_uint4(0u, 0u, 0u, 0u);
-      for (int64_t i = tail + lane * 2; i < p.fill_row; i += 64)
-        *reinterpret_cast<uint16_t*>(row + i) = 0;
-    }
+    for (int r = warp; r < rows; r += kSortWarps)
+      if (!((marks[r >> 5] >> (r & 31)) & 1u))
+        zero_row(p.table + (b0 + r) * p.table_ld, p.row_bytes, lane);
   }
 }
 
@@ -303,147 +333,186 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kSortThreads)
 // ---------------------------------------------------------------------------
 // Gradient: sums over the sorted positions
 // ---------------------------------------------------------------------------
-constexpr int kRun = 32;        // sorted positions of a run
 constexpr int kRunThreads = 128;
-constexpr int kAhead = 8;       // rows in flight per warp
+constexpr int kRunWarps = kRunThreads / 32;
+constexpr int kAhead = 8;  // rows in flight per warp
 
 struct RunParams {
   const uint32_t* key;  // sorted rows of the table, V at the end for dropped ids
   const uint32_t* pos;
-  int32_t N, V, d, n_runs, segments;
+  int32_t N, V, run, n_runs;  // sorted positions of a run (a multiple of 32), runs
+  Columns cols;
   const void* dY;
   int64_t ldy;
   void* dE;
   int64_t lde;
   float scale;
-  float* partial;  // [n_runs][2][d]: sums of the ids crossing a run's start, end
-  int vec_in, vec_out, accumulate;
+  float* partial;  // [n_runs][2][ldp]: sums of the ids crossing a run's start, end
+  int64_t ldp;
+  int64_t zero_from;  // zero the unnamed rows from here on (V: none)
 };
 
+__device__ __forceinline__ float* partial_at(const RunParams& p, int run, int end, int col) {
+  return p.partial + (int64_t(run) * 2 + end) * p.ldp + col;
+}
+
 template <typename TO>
-__device__ __forceinline__ void write_row(const RunParams& p, uint32_t row, int col,
-                                          float (&sum)[kCols]) {
-  TO* dst = static_cast<TO*>(p.dE) + int64_t(row) * p.lde;
+__device__ __forceinline__ TO* table_at(const RunParams& p, uint32_t row, int col) {
+  return static_cast<TO*>(p.dE) + int64_t(row) * p.lde + col;
+}
+
+// A row's finished sum, scaled and (kAdd) added to what the row held.
+template <bool kAdd, typename TO, int C>
+__device__ __forceinline__ void write_sum(const RunParams& p, TO* dst, const Piece<TO, C>& old,
+                                          const float (&sum)[C]) {
+  float v[C];
 #pragma unroll
-  for (int i = 0; i < kCols; ++i) sum[i] *= p.scale;
-  if (p.accumulate) {
-    float old[kCols];
-    if (p.vec_out && col + kCols <= p.d) {  // not __ldg: this launch writes the row
-      if constexpr (sizeof(TO) == 4) {
-        const float4 a = reinterpret_cast<const float4*>(dst + col)[0];
-        const float4 b = reinterpret_cast<const float4*>(dst + col)[1];
-        old[0] = a.x, old[1] = a.y, old[2] = a.z, old[3] = a.w;
-        old[4] = b.x, old[5] = b.y, old[6] = b.z, old[7] = b.w;
-      } else {
-        const uint4 a = *reinterpret_cast<const uint4*>(dst + col);
-        const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+  for (int i = 0; i < C; ++i) v[i] = sum[i] * p.scale;
+  if (kAdd) {
+    float o[C];
+    old.get(o);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          old[2 * i] = __uint_as_float(w[i] << 16);
-          old[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-        }
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < kCols; ++i) old[i] = col + i < p.d ? to_float(dst[col + i]) : 0.0f;
-    }
-#pragma unroll
-    for (int i = 0; i < kCols; ++i) sum[i] += old[i];
+    for (int i = 0; i < C; ++i) v[i] += o[i];
   }
-  store8(dst, col, p.d, p.vec_out != 0, sum);
+  store(dst, v);
 }
 
-// Partial rows start on 16-byte boundaries: d rounded up to 8.
-__host__ __device__ __forceinline__ int64_t partial_ld(int64_t d) { return (d + 7) / 8 * 8; }
-
-__device__ __forceinline__ float4* partial_at(const RunParams& p, int run, int end, int col) {
-  return reinterpret_cast<float4*>(p.partial + (int64_t(run) * 2 + end) * partial_ld(p.d) + col);
+// One warp, one run, C columns a lane from col (inactive lanes, `in` false,
+// follow along on the row's first columns).  The run's ids come in order; the
+// first may continue the previous run's last (then its sum is the run's start
+// partial), the last may go on in the next run (the end partial; a run that is
+// one id crossing both ways has a start partial only).  The rows of dY, and
+// with kAdd the table's rows that are finished here, are loaded kAhead at once.
+template <typename TY, typename TO, int C, bool kAdd>
+__device__ __forceinline__ void sum_run(const RunParams& p, int run, int col, bool in, int lane) {
+  const int i0 = run * p.run, i1 = min(i0 + p.run, p.N);
+  const uint32_t dropped = uint32_t(p.V);
+  const TY* src = static_cast<const TY*>(p.dY) + (in ? col : 0);
+  float sum[C] = {};
+  uint32_t prev = i0 > 0 ? p.key[i0 - 1] : dropped;
+  bool crosses_start = false;  // the sum continues the previous run's
+  bool open = false;           // the sum goes on past the last position seen
+  for (int j0 = i0; j0 < i1; j0 += 32) {
+    // Lane i holds sorted position j0 + i and whether its id ends there.
+    uint32_t key = dropped, pos = 0u, next = dropped;
+    const int j = j0 + lane;
+    if (j < i1) {
+      key = p.key[j];
+      pos = p.pos[j];
+    }
+    if (j + 1 < p.N && j < i1) next = p.key[j + 1];
+    const int live = __popc(__ballot_sync(0xFFFFFFFFu, key != dropped));
+    const uint32_t ends = __ballot_sync(0xFFFFFFFFu, key != dropped && next != key);
+    if (live == 0) break;
+    if (j0 == i0) crosses_start = i0 > 0 && prev == __shfl_sync(0xFFFFFFFFu, key, 0);
+#pragma unroll 1
+    for (int g = 0; g < live; g += kAhead) {
+      Piece<TY, C> piece[kAhead];
+      Piece<TO, C> old[kAdd ? kAhead : 1];
+#pragma unroll
+      for (int a = 0; a < kAhead; ++a) {  // past the end: the last row again, unused
+        const int i = min(g + a, live - 1);
+        piece[a].load(src + int64_t(__shfl_sync(0xFFFFFFFFu, pos, i)) * p.ldy);
+        if (kAdd && ((ends >> i) & 1u))
+          old[a].load(table_at<TO>(p, __shfl_sync(0xFFFFFFFFu, key, i), in ? col : 0));
+      }
+#pragma unroll
+      for (int a = 0; a < kAhead; ++a) {
+        if (g + a >= live) break;
+        float v[C];
+        piece[a].get(v);
+#pragma unroll
+        for (int i = 0; i < C; ++i) sum[i] += v[i];
+        if (!((ends >> (g + a)) & 1u)) continue;  // warp-uniform
+        const uint32_t row = __shfl_sync(0xFFFFFFFFu, key, g + a);
+        if (in) {
+          if (crosses_start)
+            store(partial_at(p, run, 0, col), sum);
+          else
+            write_sum<kAdd>(p, table_at<TO>(p, row, col), old[kAdd ? a : 0], sum);
+        }
+        crosses_start = false;
+#pragma unroll
+        for (int i = 0; i < C; ++i) sum[i] = 0.0f;
+      }
+    }
+    open = !((ends >> (live - 1)) & 1u);
+  }
+  if (open && in) store(partial_at(p, run, crosses_start ? 0 : 1, col), sum);
 }
 
-// One warp: run `run`, columns [seg * 256, ...).  The run's ids come in order;
-// the first may continue the previous run's last (then its sum is the run's
-// start partial), the last may go on in the next run (the end partial; a run
-// that is one id crossing both ways has a start partial only).
-template <typename TY, typename TO>
+// The id that begins in run `run` and goes on up to run `last`: its partial
+// sums in order.
+template <typename TO, int C, bool kAdd>
+__device__ __forceinline__ void join_runs(const RunParams& p, int run, int last, uint32_t id,
+                                          int col) {
+  float sum[C];
+  Piece<TO, C> old;
+  if (kAdd) old.load(table_at<TO>(p, id, col));
+  Piece<float, C> piece;
+  piece.load(partial_at(p, run, 1, col));
+  piece.get(sum);
+#pragma unroll 8
+  for (int r = run + 1; r <= last; ++r) {
+    float v[C];
+    piece.load(partial_at(p, r, 0, col));
+    piece.get(v);
+#pragma unroll
+    for (int i = 0; i < C; ++i) sum[i] += v[i];
+  }
+  write_sum<kAdd>(p, table_at<TO>(p, id, col), old, sum);
+}
+
+template <typename TY, typename TO, bool kAdd>
 __global__ void __launch_bounds__(kRunThreads) run_sum_kernel(const RunParams p) {
   ptx::grid_dependency_wait();
   const int lane = threadIdx.x & 31;
   const int64_t item = (int64_t(blockIdx.x) * kRunThreads + threadIdx.x) >> 5;
-  const int run = int(item / p.segments);
-  if (run >= p.n_runs) return;
-  const int col = int(item - int64_t(run) * p.segments) * (32 * kCols) + lane * kCols;
-  const int i0 = run * kRun, n = min(kRun, p.N - i0);
-  const uint32_t dropped = uint32_t(p.V);
-  // Lane i holds sorted position i0 + i.
-  uint32_t key = dropped, pos = 0u;
-  if (lane < n) {
-    key = p.key[i0 + lane];
-    pos = p.pos[i0 + lane];
-  }
-  const uint32_t before = i0 > 0 ? p.key[i0 - 1] : dropped;
-  const uint32_t after = i0 + n < p.N ? p.key[i0 + n] : dropped;
-  const int live = __popc(__ballot_sync(0xFFFFFFFFu, lane < n && key != dropped));
-  const bool in = col < p.d;
-  const TY* dY = static_cast<const TY*>(p.dY);
-  float sum[kCols] = {};
-  uint32_t cur = __shfl_sync(0xFFFFFFFFu, key, 0);
-  bool crosses_start = live > 0 && i0 > 0 && before == cur;
-  for (int g = 0; g < live; g += kAhead) {
-    float v[kAhead][kCols];
-#pragma unroll
-    for (int a = 0; a < kAhead; ++a) {
-      const uint32_t at = __shfl_sync(0xFFFFFFFFu, pos, (g + a) & 31);
-      if (g + a < live && in) {
-        load8(dY + int64_t(at) * p.ldy, col, p.d, p.vec_in != 0, v[a]);
-      } else {
-#pragma unroll
-        for (int i = 0; i < kCols; ++i) v[a][i] = 0.0f;
-      }
-    }
-#pragma unroll
-    for (int a = 0; a < kAhead; ++a) {
-      const uint32_t k = __shfl_sync(0xFFFFFFFFu, key, (g + a) & 31);
-      if (g + a >= live) break;
-      if (k != cur) {  // warp-uniform: `cur` ends here
-        if (in) {
-          if (crosses_start) {
-            partial_at(p, run, 0, col)[0] = make_float4(sum[0], sum[1], sum[2], sum[3]);
-            partial_at(p, run, 0, col)[1] = make_float4(sum[4], sum[5], sum[6], sum[7]);
-          } else {
-            write_row<TO>(p, cur, col, sum);
-          }
-        }
-        crosses_start = false;
-        cur = k;
-#pragma unroll
-        for (int i = 0; i < kCols; ++i) sum[i] = 0.0f;
-      }
-#pragma unroll
-      for (int i = 0; i < kCols; ++i) sum[i] += v[a][i];
+  const int run = int(item / p.cols.segments);
+  if (run < p.n_runs) {
+    const int seg = int(item - int64_t(run) * p.cols.segments);
+    if (seg < p.cols.vec_segments) {
+      const int col = seg * 256 + lane * 8;
+      sum_run<TY, TO, 8, kAdd>(p, run, col, col < p.cols.vec, lane);
+    } else {
+      const int col = p.cols.vec + (seg - p.cols.vec_segments) * 32 + lane;
+      sum_run<TY, TO, 1, kAdd>(p, run, col, col < p.cols.d, lane);
     }
   }
-  if (live == 0 || !in) return;
-  const bool crosses_end = live == n && after == cur;
-  if (crosses_start || crosses_end) {
-    float4* to = partial_at(p, run, crosses_start ? 0 : 1, col);
-    to[0] = make_float4(sum[0], sum[1], sum[2], sum[3]);
-    to[1] = make_float4(sum[4], sum[5], sum[6], sum[7]);
-  } else {
-    write_row<TO>(p, cur, col, sum);
+  // Then the warp's part of the rows still to zero, 8 neighbouring rows at a
+  // time: lanes 0-7 look theirs up among the sorted rows.
+  const int64_t n_warps = int64_t(gridDim.x) * kRunWarps;
+  for (int64_t r0 = p.zero_from + item * 8; r0 < p.V; r0 += n_warps * 8) {
+    bool unnamed = false;
+    if (lane < 8 && r0 + lane < p.V) {
+      const uint32_t row = uint32_t(r0 + lane);
+      int lo = 0, hi = p.N;  // the first sorted position not below row
+      while (lo < hi) {
+        const int mid = lo + (hi - lo) / 2;
+        if (p.key[mid] < row)
+          lo = mid + 1;
+        else
+          hi = mid;
+      }
+      unnamed = lo == p.N || p.key[lo] != row;
+    }
+    uint32_t todo = __ballot_sync(0xFFFFFFFFu, unnamed);
+    for (; todo != 0u; todo &= todo - 1u)
+      zero_row(reinterpret_cast<uint8_t*>(
+                   table_at<TO>(p, uint32_t(r0 + __ffs(todo) - 1), 0)),
+               int64_t(p.cols.d) * int64_t(sizeof(TO)), lane);
   }
 }
 
-// One warp: the id that begins in run `run` and goes on past its end, if there
-// is one: its partial sums in order.
-template <typename TO>
+template <typename TO, bool kAdd>
 __global__ void __launch_bounds__(kRunThreads) run_join_kernel(const RunParams p) {
   ptx::grid_dependency_wait();
   const int lane = threadIdx.x & 31;
   const int64_t item = (int64_t(blockIdx.x) * kRunThreads + threadIdx.x) >> 5;
-  const int run = int(item / p.segments);
+  const int run = int(item / p.cols.segments);
   if (run >= p.n_runs - 1) return;  // the last run's ids end in it
-  const int col = int(item - int64_t(run) * p.segments) * (32 * kCols) + lane * kCols;
-  const int i0 = run * kRun, i1 = i0 + kRun;  // a run before the last is full
+  const int seg = int(item - int64_t(run) * p.cols.segments);
+  const int i0 = run * p.run, i1 = i0 + p.run;  // a run before the last is full
   const uint32_t id = p.key[i1 - 1];
   if (id == uint32_t(p.V) || p.key[i1] != id) return;
   if (p.key[i0] == id && i0 > 0 && p.key[i0 - 1] == id) return;  // began earlier
@@ -451,23 +520,18 @@ __global__ void __launch_bounds__(kRunThreads) run_join_kernel(const RunParams p
   int last = run;
   while (true) {
     const int r = last + 1 + lane;
-    const bool on = r < p.n_runs && p.key[int64_t(r) * kRun] == id;
+    const bool on = r < p.n_runs && p.key[int64_t(r) * p.run] == id;
     const uint32_t all = __ballot_sync(0xFFFFFFFFu, on);
     last += all == 0xFFFFFFFFu ? 32 : __ffs(~all) - 1;
     if (all != 0xFFFFFFFFu) break;
   }
-  if (col >= p.d) return;
-  const float4* first = partial_at(p, run, 1, col);
-  float4 a = first[0], b = first[1];
-  float sum[kCols] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-#pragma unroll 8
-  for (int r = run + 1; r <= last; ++r) {
-    const float4* q = partial_at(p, r, 0, col);
-    a = q[0], b = q[1];
-    sum[0] += a.x, sum[1] += a.y, sum[2] += a.z, sum[3] += a.w;
-    sum[4] += b.x, sum[5] += b.y, sum[6] += b.z, sum[7] += b.w;
+  if (seg < p.cols.vec_segments) {
+    const int col = seg * 256 + lane * 8;
+    if (col < p.cols.vec) join_runs<TO, 8, kAdd>(p, run, last, id, col);
+  } else {
+    const int col = p.cols.vec + (seg - p.cols.vec_segments) * 32 + lane;
+    if (col < p.cols.d) join_runs<TO, 1, kAdd>(p, run, last, id, col);
   }
-  write_row<TO>(p, id, col, sum);
 }
 
 // ---------------------------------------------------------------------------
@@ -503,6 +567,8 @@ bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 size_t round256(size_t n) { return (n + 255u) & ~size_t(255u); }
 int64_t element(int dtype) { return dtype == FS_F32 ? 4 : 2; }
+// Partial rows start on 16-byte boundaries: d rounded up to 8.
+int64_t partial_ld(int64_t d) { return (d + 7) / 8 * 8; }
 bool rows_vec(const void* p, int64_t ld, int dtype) {
   return aligned(p, 16) && ld * element(dtype) % 16 == 0;
 }
@@ -541,29 +607,57 @@ extern "C" fs_status fs_embed(const int64_t* ids, int64_t N, const void* E, int6
   if (!ids || !E || !out || !aligned(ids, 8) || !aligned(E, element(dtype)) ||
       !aligned(out, element(dtype)))
     return FS_ERR_INVALID_ARG;
-  const int64_t segments = ceil_div(d, 32 * kLookupGroups * kCols);
-  const int64_t blocks = ceil_div(N * segments, kLookupThreads / 32);
+  const Columns cols =
+      columns_of(d, rows_vec(E, lde, dtype) && rows_vec(out, ldo, dtype), kLookupGroups);
+  const int64_t blocks = ceil_div(N * cols.segments, kLookupThreads / 32);
   if (blocks > INT_MAX) return FS_ERR_INVALID_ARG;
   const fs_status st = device_check();
   if (st != FS_OK) return st;
-  const int vi = rows_vec(E, lde, dtype), vo = rows_vec(out, ldo, dtype);
   cudaStream_t stream = static_cast<cudaStream_t>(stream_ptr);
   if (dtype == FS_BF16)
     lookup_kernel<__nv_bfloat16><<<unsigned(blocks), kLookupThreads, 0, stream>>>(
-        ids, N, static_cast<const __nv_bfloat16*>(E), int32_t(V), int32_t(d), lde, scale,
-        vocab_offset, static_cast<__nv_bfloat16*>(out), ldo, int32_t(segments), vi, vo);
+        ids, N, static_cast<const __nv_bfloat16*>(E), int32_t(V), lde, scale, vocab_offset,
+        static_cast<__nv_bfloat16*>(out), ldo, cols);
   else
     lookup_kernel<float><<<unsigned(blocks), kLookupThreads, 0, stream>>>(
-        ids, N, static_cast<const float*>(E), int32_t(V), int32_t(d), lde, scale, vocab_offset,
-        static_cast<float*>(out), ldo, int32_t(segments), vi, vo);
+        ids, N, static_cast<const float*>(E), int32_t(V), lde, scale, vocab_offset,
+        static_cast<float*>(out), ldo, cols);
   return cudaGetLastError() == cudaSuccess ? FS_OK : FS_ERR_CUDA;
 }
 
+namespace fs {
+namespace embed {
+namespace {
+
+// Sorted positions of a run: long ones leave fewer partial sums to join, short
+// ones more warps.
+int64_t run_length(int64_t N) { return N <= 8192 ? 32 : 64; }
+
+constexpr int kFillCtas = 19 * kCluster;  // with the sorting cluster, 160 CTAs
+
+template <bool kAdd>
+const void* sum_kernel(int y_dtype, int e_dtype) {
+  if (y_dtype == FS_F32)
+    return reinterpret_cast<const void*>(&run_sum_kernel<float, float, kAdd>);
+  if (e_dtype == FS_F32)
+    return reinterpret_cast<const void*>(&run_sum_kernel<__nv_bfloat16, float, kAdd>);
+  return reinterpret_cast<const void*>(&run_sum_kernel<__nv_bfloat16, __nv_bfloat16, kAdd>);
+}
+template <bool kAdd>
+const void* join_kernel_of(int e_dtype) {
+  return e_dtype == FS_F32 ? reinterpret_cast<const void*>(&run_join_kernel<float, kAdd>)
+                           : reinterpret_cast<const void*>(&run_join_kernel<__nv_bfloat16, kAdd>);
+}
+
+}  // namespace
+}  // namespace embed
+}  // namespace fs
+
 // Workspace: two buffers of sorted rows, two of positions, the runs' partial sums.
 extern "C" size_t fs_embed_grad_workspace_size(int64_t N, int64_t d) {
-  if (N <= 0 || N > kMaxN || d < 1 || d > INT_MAX - 2048) return 0;
+  if (N < 1 || !sizes_ok(N, 1, d, 0)) return 0;
   return 4 * round256(size_t(N) * 4u) +
-         round256(size_t(ceil_div(N, kRun)) * 2u * size_t(partial_ld(d)) * 4u);
+         round256(size_t(ceil_div(N, run_length(N))) * 2u * size_t(partial_ld(d)) * 4u);
 }
 
 extern "C" fs_status fs_embed_grad(const int64_t* ids, int64_t N, const void* dY, int64_t V,
@@ -576,18 +670,29 @@ extern "C" fs_status fs_embed_grad(const int64_t* ids, int64_t N, const void* dY
       (y_dtype == FS_F32 && e_dtype != FS_F32))
     return FS_ERR_INVALID_ARG;
   if (!dE || !aligned(dE, element(e_dtype))) return FS_ERR_INVALID_ARG;
-  if (N > 0 && (!ids || !dY || !aligned(ids, 8) || !aligned(dY, element(y_dtype))))
-    return FS_ERR_INVALID_ARG;
-  if (N == 0 && accumulate) return FS_OK;
-  const int64_t n_runs = ceil_div(N, kRun), segments = ceil_div(d, 32 * kCols);
-  const int64_t blocks = ceil_div(n_runs * segments, kRunThreads / 32);
+  cudaStream_t stream = static_cast<cudaStream_t>(stream_ptr);
+  if (N == 0) {
+    if (accumulate) return FS_OK;
+    const fs_status st = device_check();
+    if (st != FS_OK) return st;
+    if (cudaMemset2DAsync(dE, size_t(lde * element(e_dtype)), 0, size_t(d * element(e_dtype)),
+                          size_t(V), stream) != cudaSuccess) {
+      cudaGetLastError();
+      return FS_ERR_CUDA;
+    }
+    return FS_OK;
+  }
+  if (!ids || !dY || !aligned(ids, 8) || !aligned(dY, element(y_dtype))) return FS_ERR_INVALID_ARG;
+  const int64_t run = run_length(N), n_runs = ceil_div(N, run);
+  const Columns cols =
+      columns_of(d, rows_vec(dY, ldy, y_dtype) && rows_vec(dE, lde, e_dtype), 1);
+  const int64_t blocks = ceil_div(n_runs * cols.segments, kRunWarps);
   if (blocks > INT_MAX) return FS_ERR_INVALID_ARG;
-  if (N > 0 && (!workspace || !aligned(workspace, 256) ||
-                workspace_bytes < fs_embed_grad_workspace_size(N, d)))
+  if (!workspace || !aligned(workspace, 256) ||
+      workspace_bytes < fs_embed_grad_workspace_size(N, d))
     return FS_ERR_WORKSPACE;
   const fs_status st = device_check();
   if (st != FS_OK) return st;
-  cudaStream_t stream = static_cast<cudaStream_t>(stream_ptr);
 
   SortParams sp = {};
   sp.ids = ids;
@@ -600,51 +705,46 @@ extern "C" fs_status fs_embed_grad(const int64_t* ids, int64_t N, const void* dY
   sp.bits = (bits + sp.passes - 1) / sp.passes;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   const size_t one = round256(size_t(N) * 4u);
-  if (N > 0) {
-    for (int i = 0; i < 2; ++i) {
-      sp.key[i] = reinterpret_cast<uint32_t*>(ws + one * i);
-      sp.pos[i] = reinterpret_cast<uint32_t*>(ws + one * (2 + i));
-    }
-  } else {
-    sp.passes = 0;
+  for (int i = 0; i < 2; ++i) {
+    sp.key[i] = reinterpret_cast<uint32_t*>(ws + one * i);
+    sp.pos[i] = reinterpret_cast<uint32_t*>(ws + one * (2 + i));
   }
-  if (!accumulate) {
-    sp.fill = static_cast<uint8_t*>(dE);
-    sp.fill_ld = lde * element(e_dtype);
-    sp.fill_row = d * element(e_dtype);
-  }
-  // One cluster sorts; 19 more (152 CTAs) zero rows.
-  sort_fill_kernel<<<accumulate ? kCluster : 20 * kCluster, kSortThreads, 0, stream>>>(sp);
-  if (cudaGetLastError() != cudaSuccess) return FS_ERR_CUDA;
-  if (N == 0) return FS_OK;
-
   RunParams rp = {};
+  rp.zero_from = V;
+  if (!accumulate) {
+    sp.table = static_cast<uint8_t*>(dE);
+    sp.table_ld = lde * element(e_dtype);
+    sp.row_bytes = d * element(e_dtype);
+    // As many rows as the other CTAs can zero while the cluster sorts; the rest
+    // are zeroed beside the sums, whose reads they do not slow.
+    const int64_t bytes = (int64_t(8) + N / 1024) * 4000000;
+    sp.fill_rows = std::min(V, ceil_div(bytes, sp.row_bytes));
+    rp.zero_from = sp.fill_rows;
+  }
+  sort_fill_kernel<<<accumulate ? kCluster : kCluster + kFillCtas, kSortThreads, 0, stream>>>(sp);
+  if (cudaGetLastError() != cudaSuccess) return FS_ERR_CUDA;
+
   rp.key = sp.key[sp.passes & 1];
   rp.pos = sp.pos[sp.passes & 1];
   rp.N = int32_t(N);
   rp.V = int32_t(V);
-  rp.d = int32_t(d);
+  rp.run = int32_t(run);
   rp.n_runs = int32_t(n_runs);
-  rp.segments = int32_t(segments);
+  rp.cols = cols;
   rp.dY = dY;
   rp.ldy = ldy;
   rp.dE = dE;
   rp.lde = lde;
   rp.scale = scale;
   rp.partial = reinterpret_cast<float*>(ws + 4 * one);
-  rp.vec_in = rows_vec(dY, ldy, y_dtype);
-  rp.vec_out = rows_vec(dE, lde, e_dtype);
-  rp.accumulate = accumulate ? 1 : 0;
-  const void* sum = y_dtype == FS_F32 ? reinterpret_cast<const void*>(&run_sum_kernel<float, float>)
-                    : e_dtype == FS_F32
-                        ? reinterpret_cast<const void*>(&run_sum_kernel<__nv_bfloat16, float>)
-                        : reinterpret_cast<const void*>(
-                              &run_sum_kernel<__nv_bfloat16, __nv_bfloat16>);
-  const void* join = e_dtype == FS_F32
-                         ? reinterpret_cast<const void*>(&run_join_kernel<float>)
-                         : reinterpret_cast<const void*>(&run_join_kernel<__nv_bfloat16>);
+  rp.ldp = partial_ld(d);
+  const void* sum = accumulate ? sum_kernel<true>(y_dtype, e_dtype)
+                               : sum_kernel<false>(y_dtype, e_dtype);
+  const void* join = accumulate ? join_kernel_of<true>(e_dtype) : join_kernel_of<false>(e_dtype);
   void* args[] = {&rp};
-  cudaError_t err = launch_after(sum, blocks, kRunThreads, args, stream);
+  // With rows to zero, warps for them too: 8 blocks an SM.
+  cudaError_t err = launch_after(sum, accumulate ? blocks : std::max<int64_t>(blocks, 8 * 152),
+                                 kRunThreads, args, stream);
   if (err == cudaSuccess && n_runs > 1)
     err = launch_after(join, blocks, kRunThreads, args, stream);
   if (err != cudaSuccess) {
