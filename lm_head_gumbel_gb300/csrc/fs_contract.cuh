@@ -66,6 +66,11 @@ __device__ __forceinline__ uint64_t smem_desc_sw128_mn(uint32_t saddr, uint32_t 
   return desc;
 }
 
+// Store to an address from cluster_addr, in this or another CTA of the cluster.
+__device__ __forceinline__ void st_cluster(uint32_t addr, uint64_t v) {
+  asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(addr), "l"(v) : "memory");
+}
+
 // max that returns NaN if either input is NaN.
 __device__ __forceinline__ float max_nan(float a, float b) {
   float r;
@@ -118,6 +123,9 @@ struct Shape {
   // The launch overlaps the kernel before it on the stream, which writes A and
   // the epilogue's inputs: B streams at once, the rest waits for that kernel.
   uint32_t pdl;
+  // A dependent kernel may be scheduled from the start (it takes SMs as this
+  // one's CTAs leave them) instead of as the last CTAs end.
+  uint32_t early_trigger;
   uint64_t wait_limit_ns;
   int* error_word;
 };
@@ -261,6 +269,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   if constexpr (kPair) ptx::cluster_sync();
   ptx::tc_fence_after();
+  if (s.early_trigger) ptx::grid_launch_dependents();
   const uint32_t tmem_base = *tmem_holder;
   const BoundedWait waiter{abort_flag, s.wait_limit_ns, s.error_word};
 
@@ -471,9 +480,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       ptx::tmem_dealloc(tmem_base, kTmemCols);
   }
   if constexpr (kPair) ptx::cluster_sync();
-  // A kernel launched as this one's programmatic dependent may be scheduled as
-  // blocks finish; it waits for the whole grid before it reads anything.
-  ptx::grid_launch_dependents();
+  // A dependent kernel waits for the whole grid before it reads anything of it.
+  if (!s.early_trigger) ptx::grid_launch_dependents();
 }
 
 // ---------------------------------------------------------------------------
@@ -521,25 +529,24 @@ struct StoreEpi {
     for (int c = 0; c < 2; ++c) {
       const int x0 = at.col0 + c * 64;
       if (x0 >= s.n_cols) break;
-      uint32_t r[32];
+      // The sums first: the box's last store is being read meanwhile.
+      uint32_t r[2][32];
+      ptx::tmem_ld_32x32b_x32(at.taddr + uint32_t(c * 64), r[0]);
+      ptx::tmem_ld_32x32b_x32(at.taddr + uint32_t(c * 64 + 32), r[1]);
+      ptx::tmem_wait_ld();
       box_begin(lane);
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        ptx::tmem_ld_32x32b_x32(at.taddr + uint32_t(c * 64 + h * 32), r);
-        ptx::tmem_wait_ld();
+      for (int q = 0; q < 8; ++q) {
+        float v[8];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          float v[8];
+        for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[q >> 2][(q & 3) * 8 + i]);
+        box_put(box, lane, q, v);
+        const int x = x0 + q * 8;
+        if (x == p.whole_n && at.row0 + lane < s.m_rows) {
+          __nv_bfloat16* out = p.out + int64_t(at.row0 + lane) * p.ld;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[q * 8 + i]);
-          box_put(box, lane, h * 4 + q, v);
-          const int x = x0 + h * 32 + q * 8;
-          if (x == p.whole_n && at.row0 + lane < s.m_rows) {
-            __nv_bfloat16* out = p.out + int64_t(at.row0 + lane) * p.ld;
-#pragma unroll
-            for (int i = 0; i < 7; ++i)
-              if (x + i < s.n_cols) out[x + i] = __float2bfloat16_rn(v[i]);
-          }
+          for (int i = 0; i < 7; ++i)
+            if (x + i < s.n_cols) out[x + i] = __float2bfloat16_rn(v[i]);
         }
       }
       if (x0 < p.whole_n) box_end(box, tmap, lane, x0, at.row0);

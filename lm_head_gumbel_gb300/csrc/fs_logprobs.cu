@@ -30,8 +30,24 @@ int* device_error_word();  // fs_sample.cu
 namespace vocab {
 namespace {
 
+// Workspaces and k splits are planned for this many SMs (GB300); a device that
+// offers fewer co-resident CTA pairs uses less of them.
+constexpr int kPlanSms = 152;
+
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
+
+// The tensor core adds 16 products to the fp32 accumulator at a time and cuts
+// the sum off towards zero, so a logit comes out short by about half a unit in
+// the accumulator's last place per step: measured over heads of d = 256 to 5120,
+// 1.55e-8 (0.26 2^-24) of the logit per step of 16 -- 4e-6 at d = 4096, a bias
+// that does not average out of the log-sum-exp.  The scale that turns logits
+// into base-2 units carries the correction; what is left is the part that
+// differs from logit to logit.
+constexpr float kCutPerStep = 1.55e-8f;
+__device__ __forceinline__ float scale_to_log2(float T, int n_kb) {
+  return kLog2e / T * (1.0f + kCutPerStep * float(n_kb * (kBK / kUK)));
+}
 
 __device__ __forceinline__ float row_temperature(const float* temperature, int row) {
   const float T = temperature ? temperature[row] : 1.0f;
@@ -156,12 +172,12 @@ struct ScoreEpi {
     st.m = m;
   }
   static __device__ __forceinline__ void tile(const Params& p, State& st, const TileAt& at,
-                                              int lane, uint8_t*, const void*, const Shape&) {
+                                              int lane, uint8_t*, const void*, const Shape& s) {
     const int row = at.row0 + lane;
     const bool valid = row < p.B;
     if (valid && st.row < 0) {  // the thread's row, the same in every unit
       st.row = row;
-      st.scale2 = kLog2e / row_temperature(p.temperature, row);
+      st.scale2 = scale_to_log2(row_temperature(p.temperature, row), s.n_kb);
       if (p.mask) st.mrow = p.mask + int64_t(row) * p.mask_ld;
     }
     const AllowWords allow(st.mrow, at.col0, p.V);
@@ -229,6 +245,7 @@ struct JoinParams {
   const __nv_bfloat16* W;
   int64_t ldh, ldw;
   int32_t d, V, n_slots, K;
+  int32_t ctas;  // blocks (a cluster) per row
   const float* temperature;
   const uint32_t* mask;
   int64_t mask_ld;
@@ -251,37 +268,48 @@ __device__ __forceinline__ float two_sum(float a, float b, float& err) {
 }
 
 // One logit by a warp: bf16 products are exact in fp32, and their sum is kept
-// as an unevaluated pair (hi, lo), so the result is good to about 2^-45 of the
-// terms' magnitude.  Every lane returns it; the order of the terms depends on
-// d alone.
-__device__ __forceinline__ double warp_logit(const __nv_bfloat16* __restrict__ h,
+// as an unevaluated pair hi + lo, good to about 2^-45 of the terms' magnitude.
+// Every lane returns it, normalised (hi is the sum rounded to fp32); the order
+// of the terms depends on d alone.  kDeep 16-byte loads of w are in flight per lane
+// (a warp usually reads its row from DRAM); h is shared by the row's warps and
+// comes from L1.
+template <int kDeep>
+__device__ __forceinline__ float2 warp_logit(const __nv_bfloat16* __restrict__ h,
                                              const __nv_bfloat16* __restrict__ w, int d,
                                              int lane) {
+  const uint4* h4 = reinterpret_cast<const uint4*>(h);
+  const uint4* w4 = reinterpret_cast<const uint4*>(w);
   float hi = 0.0f, lo = 0.0f;
+  auto add = [&](float x) {
+    float err;
+    hi = two_sum(hi, x, err);
+    lo = __fadd_rn(lo, err);
+  };
   const int n8 = d >> 3;
-#pragma unroll 4
-  for (int i = lane; i < n8; i += 32) {
-    const uint4 a = reinterpret_cast<const uint4*>(h)[i];
-    const uint4 b = reinterpret_cast<const uint4*>(w)[i];
-    const uint32_t av[4] = {a.x, a.y, a.z, a.w}, bv[4] = {b.x, b.y, b.z, b.w};
+  for (int i0 = lane; i0 < n8; i0 += 32 * kDeep) {
+    uint4 wv[kDeep];
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      float err;
-      hi = two_sum(hi, __fmul_rn(__uint_as_float(av[q] << 16), __uint_as_float(bv[q] << 16)), err);
-      lo = __fadd_rn(lo, err);
-      hi = two_sum(hi,
-                   __fmul_rn(__uint_as_float(av[q] & 0xFFFF0000u),
-                             __uint_as_float(bv[q] & 0xFFFF0000u)),
-                   err);
-      lo = __fadd_rn(lo, err);
+    for (int u = 0; u < kDeep; ++u) {
+      const int i = i0 + 32 * u;
+      wv[u] = i < n8 ? __ldg(w4 + i) : make_uint4(0u, 0u, 0u, 0u);
+    }
+#pragma unroll
+    for (int u = 0; u < kDeep; ++u) {
+      const int i = i0 + 32 * u;
+      if (i >= n8) break;
+      const uint4 hv = __ldg(h4 + i);
+      const uint32_t av[4] = {hv.x, hv.y, hv.z, hv.w};
+      const uint32_t bv[4] = {wv[u].x, wv[u].y, wv[u].z, wv[u].w};
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        add(__fmul_rn(__uint_as_float(av[q] << 16), __uint_as_float(bv[q] << 16)));
+        add(__fmul_rn(__uint_as_float(av[q] & 0xFFFF0000u),
+                      __uint_as_float(bv[q] & 0xFFFF0000u)));
+      }
     }
   }
   const int tail = n8 * 8 + lane;
-  if (tail < d) {
-    float err;
-    hi = two_sum(hi, __fmul_rn(__bfloat162float(h[tail]), __bfloat162float(w[tail])), err);
-    lo = __fadd_rn(lo, err);
-  }
+  if (tail < d) add(__fmul_rn(__bfloat162float(h[tail]), __bfloat162float(w[tail])));
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) {
     const float ohi = __shfl_xor_sync(0xFFFFFFFFu, hi, off);
@@ -290,134 +318,151 @@ __device__ __forceinline__ double warp_logit(const __nv_bfloat16* __restrict__ h
     hi = two_sum(hi, ohi, err);
     lo = __fadd_rn(__fadd_rn(lo, olo), err);
   }
-  return isfinite(hi) ? double(hi) + double(lo) : double(hi);
+  // Infinite or NaN: hi alone.
+  if (!isfinite(hi)) return make_float2(hi, 0.0f);
+  float err;
+  const float sum = two_sum(hi, lo, err);
+  return make_float2(sum, err);
 }
 
-// An order-preserving map of non-NaN floats to unsigned integers above 0 (-0
-// folded into +0).
-__device__ __forceinline__ uint32_t order_key(float f) {
+// logit / T - lse in fp32 without the quotient's rounding.
+__device__ __forceinline__ float scaled_logp(float2 logit, float T, float lse) {
+  const float q = __fdiv_rn(logit.x, T);
+  if (!isfinite(q)) return q - lse;
+  const float rest = (__fmaf_rn(-q, T, logit.x) + logit.y) / T;
+  return (q - lse) + rest;
+}
+
+// An order-preserving map of floats to unsigned integers; NaN counts as +inf
+// (it ranks first, so that every place is filled; the row's lse is NaN too).
+__device__ __forceinline__ uint32_t order_bits(float f) {
+  if (!(f == f)) f = INFINITY;
   const uint32_t u = __float_as_uint(f + 0.0f);
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
-__device__ __forceinline__ float key_value(uint32_t k) {
-  return __uint_as_float((k & 0x80000000u) ? (k & 0x7FFFFFFFu) : ~k);
+
+// (value, id) as one unsigned integer whose order is: higher value first, then
+// lower id; 0 (no entry) comes last.  -0 counts as +0; values are not NaN.
+__device__ __forceinline__ uint64_t entry_key(float f, int32_t id) {
+  if (id < 0) return 0u;
+  return (uint64_t(order_bits(f)) << 32) | (0xFFFFFFFFu - uint32_t(id));
 }
 
-// The warp's n best entries of up to 32 sorted lists, one per lane, in shared
-// memory: n rounds of the best head, lower id on ties, popped by its lane.
-template <typename Emit>
-__device__ __forceinline__ void warp_best(const float* val, const int32_t* id, int len, bool has,
-                                          int n, Emit emit) {
-  int pos = 0;
-  uint32_t key = 0u;
-  int32_t head = INT_MAX;
-  auto load = [&]() {
-    const bool more = has && pos < len && id[pos] >= 0;
-    key = more ? order_key(val[pos]) : 0u;
-    head = more ? id[pos] : INT_MAX;
-  };
-  load();
-  for (int j = 0; j < n; ++j) {
-    const uint32_t best = __reduce_max_sync(0xFFFFFFFFu, key);
-    const int32_t who = __reduce_min_sync(0xFFFFFFFFu, key == best ? head : INT_MAX);
-    if (best == 0u) {
-      emit(j, -INFINITY, -1);
-      continue;
-    }
-    emit(j, key_value(best), who);
-    if (key == best && head == who) {
-      ++pos;
-      load();
-    }
+// How many of the n keys in shared memory exceed `key`.
+__device__ __forceinline__ int count_above(const uint64_t* keys, int n, uint64_t key) {
+  int above[4] = {};
+  int i = 0;
+  for (; i + 4 <= n; i += 4) {
+    uint64_t k[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) k[q] = keys[i + q];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) above[q] += k[q] > key ? 1 : 0;
   }
+  for (; i < n; ++i) above[0] += keys[i] > key ? 1 : 0;
+  return above[0] + above[1] + above[2] + above[3];
 }
 
-template <int KC>
-constexpr int kJoinThreads = KC > 0 ? 320 : 128;
-// At most one slot per thread of a warp-select: 2 * 152 slots in 10 warps.
-constexpr int kMaxSlots = 320;
-
-// One block per row.  Launched as a programmatic dependent of the contraction.
-template <int KC>
-__global__ void __launch_bounds__(kJoinThreads<KC>) join_kernel(const JoinParams p) {
-  constexpr int kThreadsJ = kJoinThreads<KC>;
-  constexpr int kWarps = kThreadsJ / 32;
-  constexpr int kList = KC > 0 ? KC : 1;
-  extern __shared__ __align__(16) uint8_t dyn[];  // the row's lists
-  __shared__ float s_m[kWarps], s_S[kWarps], s_U[kWarps];
-  __shared__ float s_wv[kWarps * kList];
-  __shared__ int32_t s_wi[kWarps * kList];
-  __shared__ int32_t s_id[kList + 1];
-  __shared__ double s_logit[kList + 1];
-  const int row = blockIdx.x;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  ptx::grid_dependency_wait();
-
-  // ---- the row's lists into shared memory
-  float* lv = reinterpret_cast<float*>(dyn);
-  int32_t* li = reinterpret_cast<int32_t*>(lv + p.n_slots * KC);
-  if constexpr (KC > 0) {
-    const float4* v4 = reinterpret_cast<const float4*>(p.cand_val + int64_t(row) * p.n_slots * KC);
-    const int4* i4 = reinterpret_cast<const int4*>(p.cand_id + int64_t(row) * p.n_slots * KC);
-    for (int i = threadIdx.x; i < p.n_slots * KC / 4; i += kThreadsJ) {
-      reinterpret_cast<float4*>(lv)[i] = v4[i];
-      reinterpret_cast<int4*>(li)[i] = i4[i];
-    }
+// Fold the state (m1, S1, U1) into (m0, S0, U0).
+__device__ __forceinline__ void join_state(float& m0, float& S0, float& U0, float m1, float S1,
+                                           float U1) {
+  if (m1 == -INFINITY) return;
+  if (m0 == -INFINITY) {
+    m0 = m1, S0 = S1, U0 = U1;
+    return;
   }
-
-  // ---- statistics: threads in slot order, then lanes, then warps
-  const RowPart* part = p.part + int64_t(row) * p.n_slots;
-  float m = -INFINITY, S = 0.0f, U = 0.0f;
-  auto join = [](float& m0, float& S0, float& U0, float m1, float S1, float U1) {
-    if (m1 == -INFINITY) return;
-    if (m0 == -INFINITY) {
-      m0 = m1, S0 = S1, U0 = U1;
-      return;
-    }
-    const float mm = ptx::max_nan(m0, m1);
-    const float d0 = ptx::max_nan(m0 - mm, -16384.0f), d1 = ptx::max_nan(m1 - mm, -16384.0f);
-    const float f0 = exp2f(d0), f1 = exp2f(d1);
-    U0 = f0 * fmaf(d0, S0, U0) + f1 * fmaf(d1, S1, U1);
-    S0 = f0 * S0 + f1 * S1;
-    m0 = mm;
-  };
-  for (int i = threadIdx.x; i < p.n_slots; i += kThreadsJ) {
-    const RowPart r = part[i];
-    join(m, S, U, r.m, r.S, r.U);
-  }
+  const float mm = ptx::max_nan(m0, m1);
+  const float d0 = ptx::max_nan(m0 - mm, -16384.0f), d1 = ptx::max_nan(m1 - mm, -16384.0f);
+  const float f0 = exp2f(d0), f1 = exp2f(d1);
+  U0 = f0 * fmaf(d0, S0, U0) + f1 * fmaf(d1, S1, U1);
+  S0 = f0 * S0 + f1 * S1;
+  m0 = mm;
+}
+__device__ __forceinline__ void join_lanes(float& m, float& S, float& U) {
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) {
     const float om = __shfl_xor_sync(0xFFFFFFFFu, m, off);
     const float oS = __shfl_xor_sync(0xFFFFFFFFu, S, off);
     const float oU = __shfl_xor_sync(0xFFFFFFFFu, U, off);
-    join(m, S, U, om, oS, oU);
+    join_state(m, S, U, om, oS, oU);
   }
-  if (lane == 0) s_m[warp] = m, s_S[warp] = S, s_U[warp] = U;
-  __syncthreads();
-  m = s_m[0], S = s_S[0], U = s_U[0];
-  for (int w = 1; w < kWarps; ++w) join(m, S, U, s_m[w], s_S[w], s_U[w]);
-  const bool none = m == -INFINITY;
-  const float log2S = log2f(S);
-  const float lse = none ? -INFINITY : kLn2 * (m + log2S);
+}
 
-  // ---- candidates: the K + 4 best fp32 sums of all lists
+// Blocks of the join kernel: a thread per slot at least.  Up to a block per SM
+// what counts is a row's latency: a warp for every logit of K <= 5, whole rows
+// of W in flight.  Beyond (CTA pairs: half the slots) it is the number of rows
+// in flight: small blocks of fewer registers (1000 rows at d = 4096, K = 5: 29 us,
+// with the large blocks 64).
+struct JoinWide {
+  static constexpr int kThreads = 320, kDeep = 16, kBlocks = 2;
+};
+struct JoinNarrow {
+  static constexpr int kThreads = 160, kDeep = 4, kBlocks = 8;
+};
+constexpr int kMaxSlots = 2 * kPlanSms;
+static_assert(kMaxSlots <= JoinWide::kThreads && kPlanSms <= JoinNarrow::kThreads,
+              "a thread per slot");
+
+// A row's block, or with more logits to sum than a block has warps and few
+// rows, its cluster of `ctas` blocks: every block selects the candidates, the
+// logits are dealt out to all warps, and block 0 ranks and writes them.
+// Launched as a programmatic dependent of the contraction.
+//
+// The n = K + 4 best entries of the row's lists, in three steps:
+//   heads     the largest head of every 8 lists bounds the n-th best head from
+//             below (n of these reach it); the few heads that reach the bound
+//             are ranked by counting;
+//   entries   an entry in place q of the list with the r-th best head has r + q
+//             better ones, so only r + q < n can matter, and only entries that
+//             reach the n-th best head;
+//   ranks     those (rarely more than n + a few) are ranked by counting.
+// Keys are all different, so counting gives each its place whatever order the
+// threads came in.
+//
+// What bounds it is latency: dependent loads, barriers and short loops, hidden
+// behind other rows where there are more rows than SMs.
+template <int KC, class Block>
+__global__ void __launch_bounds__(Block::kThreads, Block::kBlocks)
+    join_kernel(const JoinParams p) {
+  constexpr int kJoinThreads = Block::kThreads;
+  constexpr int kJoinWarps = kJoinThreads / 32;
+  constexpr int kList = KC > 0 ? KC : 1;
+  constexpr int kGroups = kJoinThreads / 8;
+  constexpr int kEntries = kList * (kList + 1) / 2;
+  __shared__ float s_m[kJoinWarps], s_S[kJoinWarps], s_U[kJoinWarps];
+  __shared__ uint32_t s_group[kGroups];
+  __shared__ uint32_t s_bound;
+  __shared__ int32_t s_heads, s_entries;
+  __shared__ uint64_t s_head[KC > 0 ? kJoinThreads : 1];
+  __shared__ int32_t s_slot[KC > 0 ? kJoinThreads : 1];
+  __shared__ uint64_t s_entry[kEntries];
+  __shared__ int32_t s_list[kList];
+  __shared__ uint64_t s_least;
+  __shared__ int32_t s_id[kList], s_rank[kList];
+  __shared__ uint64_t s_key[kList];
+  __shared__ float2 s_logit[kList];
+  const int cta = int(blockIdx.x) % p.ctas;
+  const int row = int(blockIdx.x) / p.ctas;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int n_cand = KC > 0 ? p.K + 4 : 0;  // at most KC
-  if constexpr (KC > 0) {
-    const int slot = threadIdx.x;
-    warp_best(lv + slot * KC, li + slot * KC, KC, slot < p.n_slots, n_cand,
-              [&](int j, float v, int32_t id) {
-                if (lane == 0) s_wv[warp * KC + j] = v, s_wi[warp * KC + j] = id;
-              });
-    __syncthreads();
-    if (warp == 0)
-      warp_best(s_wv + lane * KC, s_wi + lane * KC, n_cand, lane < kWarps, n_cand,
-                [&](int j, float, int32_t id) {
-                  if (lane == 0) s_id[j] = id;
-                });
+  if (tid < kList) s_list[tid] = s_id[tid] = -1, s_rank[tid] = 0, s_key[tid] = 0u;
+  if (tid == 0) s_bound = 0u, s_heads = s_entries = 0, s_least = 0u;
+  if (KC > 0 && p.ctas > 1) ptx::cluster_sync();  // block 0's keys are cleared before any arrives
+  ptx::grid_dependency_wait();
+
+  // ---- what the row needs from memory, at once
+  const int64_t slot0 = int64_t(row) * p.n_slots;
+  float m = -INFINITY, S = 0.0f, U = 0.0f;
+  uint64_t head = 0u;
+  if (tid < p.n_slots) {
+    const RowPart r = p.part[slot0 + tid];
+    if constexpr (KC > 0)
+      head = entry_key(p.cand_val[(slot0 + tid) * KC], p.cand_id[(slot0 + tid) * KC]);
+    m = r.m, S = r.S, U = r.U;
   }
-  // ---- the token
+  const float T = row_temperature(p.temperature, row);
   int64_t token = -1, local = -1;
-  bool scored = false;  // its logit is wanted
+  bool scored = false;  // the token has a logit
   if (p.tokens) {
     token = p.tokens[row];
     local = token - p.vocab_offset;
@@ -425,42 +470,121 @@ __global__ void __launch_bounds__(kJoinThreads<KC>) join_kernel(const JoinParams
     if (scored && p.mask)
       scored = (p.mask[int64_t(row) * p.mask_ld + (local >> 5)] >> (local & 31)) & 1u;
   }
-  if (threadIdx.x == 0) s_id[n_cand] = scored ? int32_t(local) : -1;
-  __syncthreads();
-  // ---- their logits again, compensated
-  for (int j = warp; j <= n_cand; j += kWarps) {
-    const int32_t id = s_id[j];
-    if (id < 0) continue;
-    const double l = warp_logit(p.H + int64_t(row) * p.ldh, p.W + int64_t(id) * p.ldw, p.d, lane);
-    // NaN (the row's lse is NaN too) ranks first, so every place is filled.
-    if (lane == 0) s_logit[j] = l == l ? l : double(INFINITY);
+
+  // ---- statistics: lanes, then (below) warps
+  join_lanes(m, S, U);
+  if (lane == 0) s_m[warp] = m, s_S[warp] = S, s_U[warp] = U;
+
+  // ---- candidates
+  if constexpr (KC > 0) {
+    const uint32_t value = uint32_t(head >> 32);
+    uint32_t top = value;
+#pragma unroll
+    for (int off = 4; off > 0; off >>= 1)
+      top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, off));
+    if ((lane & 7) == 0) s_group[tid >> 3] = top;
+    __syncthreads();
+    if (tid < kGroups) {  // the group whose largest head is the n-th largest
+      const uint32_t mine = s_group[tid];
+      int above = 0, reach = 0;
+#pragma unroll 8
+      for (int i = 0; i < kGroups; ++i) {
+        const uint32_t g = s_group[i];
+        above += g > mine ? 1 : 0;
+        reach += g >= mine ? 1 : 0;
+      }
+      if (above < n_cand && reach >= n_cand) s_bound = mine;
+    }
+    __syncthreads();
+    if (head != 0u && value >= s_bound) {
+      const int i = atomicAdd(&s_heads, 1);
+      s_head[i] = head;
+      s_slot[i] = tid;
+    }
+    __syncthreads();
+    if (tid < s_heads) {
+      const uint64_t key = s_head[tid];
+      const int r = count_above(s_head, s_heads, key);
+      if (r < n_cand) s_list[r] = s_slot[tid];
+      if (r == n_cand - 1) s_least = key;
+    }
+    __syncthreads();
+    for (int r = warp; r < n_cand; r += kJoinWarps) {
+      const int32_t list = s_list[r];
+      if (list < 0 || lane >= n_cand - r) continue;
+      const int64_t at = (slot0 + list) * KC + lane;
+      const uint64_t key = entry_key(p.cand_val[at], p.cand_id[at]);
+      if (key != 0u && key >= s_least) s_entry[atomicAdd(&s_entries, 1)] = key;
+    }
+    __syncthreads();
+    for (int i = tid; i < s_entries; i += kJoinThreads) {
+      const uint64_t key = s_entry[i];
+      const int r = count_above(s_entry, s_entries, key);
+      if (r < n_cand) s_id[r] = int32_t(0xFFFFFFFFu - uint32_t(key));
+    }
   }
   __syncthreads();
-  const double inv_t = 1.0 / double(row_temperature(p.temperature, row));
-  if (threadIdx.x == 0) {
-    if (p.out_lse) p.out_lse[row] = lse;
-    if (p.out_entropy) p.out_entropy[row] = none ? 0.0f : kLn2 * (log2S - U / S);
-    if (p.tokens)
-      p.out_logp[row] = token < 0 ? 0.0f
-                        : !scored ? -INFINITY
-                                  : float(s_logit[n_cand] * inv_t - double(lse));
+
+  // ---- the logits again, a warp each (0: the token, from 1: candidates), dealt
+  // out to the warps of all blocks
+  const __nv_bfloat16* h = p.H + int64_t(row) * p.ldh;
+  for (int j = cta * kJoinWarps + warp; j <= n_cand; j += p.ctas * kJoinWarps) {
+    if (j == 0) {  // and the row's statistics
+      m = lane < kJoinWarps ? s_m[lane] : -INFINITY;
+      S = lane < kJoinWarps ? s_S[lane] : 0.0f;
+      U = lane < kJoinWarps ? s_U[lane] : 0.0f;
+      join_lanes(m, S, U);
+      const bool none = m == -INFINITY;
+      const float log2S = log2f(S);
+      const float lse = none ? -INFINITY : kLn2 * (m + log2S);
+      __syncwarp();
+      if (lane == 0) {
+        s_m[0] = lse;
+        if (p.out_lse) p.out_lse[row] = lse;
+        if (p.out_entropy) p.out_entropy[row] = none ? 0.0f : kLn2 * (log2S - U / S);
+      }
+      if (p.tokens) {
+        float logp = token < 0 ? 0.0f : -INFINITY;
+        if (scored) logp = scaled_logp(warp_logit<Block::kDeep>(h, p.W + local * p.ldw, p.d, lane), T, lse);
+        if (lane == 0) p.out_logp[row] = logp;
+      }
+      continue;
+    }
+    const int32_t id = s_id[j - 1];
+    if (id < 0) continue;
+    const float2 l = warp_logit<Block::kDeep>(h, p.W + int64_t(id) * p.ldw, p.d, lane);
+    if (lane == 0) {
+      const uint64_t key = (uint64_t(order_bits(l.x)) << 32) | order_bits(l.y);
+      if (cta == 0) {
+        s_logit[j - 1] = l;
+        s_key[j - 1] = key;
+      } else {
+        ptx::st_cluster(ptx::cluster_addr(&s_logit[j - 1], 0),
+                        *reinterpret_cast<const uint64_t*>(&l));
+        ptx::st_cluster(ptx::cluster_addr(&s_key[j - 1], 0), key);
+      }
+    }
   }
   if constexpr (KC > 0) {
-    if (int(threadIdx.x) < n_cand) {
-      const int j = threadIdx.x;
-      const int32_t id = s_id[j];
-      const double l = id < 0 ? 0.0 : s_logit[j];
-      int rank = 0;
-      for (int i = 0; i < n_cand; ++i) {
-        const int32_t oi = s_id[i];
-        if (oi < 0 || i == j) continue;
-        rank += (id < 0 || s_logit[i] > l || (s_logit[i] == l && oi < id)) ? 1 : 0;
-      }
-      if (id < 0) rank = j;  // absent entries come last, in place
+    if (p.ctas > 1) {
+      ptx::cluster_sync();
+      if (cta != 0) return;
+    } else {
+      __syncthreads();
+    }
+    for (int pair = tid; pair < n_cand * n_cand; pair += kJoinThreads) {
+      const int j = pair / n_cand, i = pair - j * n_cand;
+      const uint64_t a = s_key[i], b = s_key[j];  // 0: absent
+      if (a != 0u && (a > b || (a == b && s_id[i] < s_id[j]))) atomicAdd(&s_rank[j], 1);
+    }
+    __syncthreads();
+    if (tid < n_cand) {
+      const int32_t id = s_id[tid];
+      const int rank = id < 0 ? tid : s_rank[tid];  // absent ones come last, in place
       if (rank < p.K) {
         const int64_t o = int64_t(row) * p.K + rank;
         p.out_topk_idx[o] = id < 0 ? -1 : p.vocab_offset + id;
-        p.out_topk_logp[o] = id < 0 ? -INFINITY : float(l * inv_t - double(lse));
+        p.out_topk_logp[o] = id < 0 ? -INFINITY : scaled_logp(s_logit[tid], T, s_m[0]);
       }
     }
   }
@@ -492,7 +616,8 @@ struct GradEpi {
     bool live;  // false: the row's G is 0
   };
   static __device__ __forceinline__ void start(const Params&, State&) {}
-  static __device__ __forceinline__ void load_row(const Params& p, State& st, int row) {
+  static __device__ __forceinline__ void load_row(const Params& p, State& st, int row,
+                                                  int n_kb) {
     st.row = row;
     st.mrow = nullptr;
     st.live = false;
@@ -502,7 +627,7 @@ struct GradEpi {
     const float T = row_temperature(p.temperature, row);
     const float lse = p.lse[row];
     if (p.mask) st.mrow = p.mask + int64_t(row) * p.mask_ld;
-    st.scale2 = kLog2e / T;
+    st.scale2 = scale_to_log2(T, n_kb);
     st.lse2 = lse * kLog2e;
     st.live = lse != -INFINITY;
     float a = p.grad_logp[row] / T;
@@ -526,9 +651,9 @@ struct GradEpi {
   }
   static __device__ __forceinline__ void tile(const Params& p, State& st, const TileAt& at,
                                               int lane, uint8_t* box, const void* tmap,
-                                              const Shape&) {
+                                              const Shape& s) {
     const int row = at.row0 + lane;
-    if (row != st.row) load_row(p, st, row);
+    if (row != st.row) load_row(p, st, row, s.n_kb);
     const AllowWords allow(st.mrow, at.col0, p.V);
 #pragma unroll 1
     for (int c = 0; c < 2; ++c) {
@@ -565,39 +690,39 @@ struct GradEpi {
 };
 
 // dH from its k splits, in split order, rounded to bf16 once.  A thread takes
-// 8 columns of one row; neighbouring threads take neighbouring rows, the order
+// 4 columns of one row; neighbouring threads take neighbouring rows, the order
 // the partial tiles are stored in (PartialEpi).
 constexpr int kSumThreads = 256;
+constexpr int kSumBlocksPerTile = kBM * kBN / 4 / kSumThreads;  // of one CTA's tile
 __global__ void __launch_bounds__(kSumThreads)
     sum_splits_kernel(const float4* __restrict__ partial, int32_t n_splits, int32_t n_tiles,
                       int32_t n_nt, int32_t ctas, int32_t B, int32_t d,
                       __nv_bfloat16* __restrict__ dH, int64_t lddh) {
+  ptx::grid_launch_dependents();
   ptx::grid_dependency_wait();
-  constexpr int kTile = kBM * kBN / 4;               // float4 of a CTA's tile
-  const int tile = blockIdx.x / (kBN / 8 * kBM / kSumThreads);  // (tile of the grid, CTA)
-  const int in = blockIdx.x % (kBN / 8 * kBM / kSumThreads) * kSumThreads + threadIdx.x;
-  const int r = in % kBM, c8 = in / kBM;  // row, group of 8 columns
+  constexpr int kTile = kBM * kBN / 4;              // float4 of a CTA's tile
+  const int tile = blockIdx.x / kSumBlocksPerTile;  // (tile of the grid, CTA)
+  const int in = blockIdx.x % kSumBlocksPerTile * kSumThreads + threadIdx.x;
+  const int r = in % kBM, c4 = in / kBM;  // row, group of 4 columns
   const int t = tile / ctas, rank = tile - t * ctas;
   const int row = (t / n_nt * ctas + rank) * kBM + r;
-  const int col = t % n_nt * kBN + c8 * 8;
+  const int col = t % n_nt * kBN + c4 * 4;
   if (row >= B || col >= d) return;
-  float v[8] = {};
+  const float4* src = partial + (int64_t(t) * ctas + rank) * kTile + in;
+  const int64_t step = int64_t(n_tiles) * ctas * kTile;
+  float v[4] = {};
+#pragma unroll 8
   for (int s = 0; s < n_splits; ++s) {
-    const float4* src = partial + ((int64_t(s) * n_tiles + t) * ctas + rank) * kTile +
-                        int64_t(c8 * 2) * kBM + r;
-    const float4 a = src[0], b = src[kBM];
+    const float4 a = src[s * step];
     v[0] += a.x, v[1] += a.y, v[2] += a.z, v[3] += a.w;
-    v[4] += b.x, v[5] += b.y, v[6] += b.z, v[7] += b.w;
   }
   __nv_bfloat16* out = dH + int64_t(row) * lddh + col;
-  if (col + 8 <= d) {
-    __nv_bfloat162 h[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) h[i] = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-    *reinterpret_cast<uint4*>(out) = *reinterpret_cast<const uint4*>(h);
+  if (col + 4 <= d) {
+    __nv_bfloat162 h[2] = {__floats2bfloat162_rn(v[0], v[1]), __floats2bfloat162_rn(v[2], v[3])};
+    *reinterpret_cast<uint2*>(out) = *reinterpret_cast<const uint2*>(h);
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+    for (int i = 0; i < 3; ++i)
       if (col + i < d) out[i] = __float2bfloat16_rn(v[i]);
   }
 }
@@ -613,9 +738,6 @@ using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t
 
 constexpr int kMaxDevices = 64;
 constexpr uint64_t kWaitLimitNs = 2000000000ull;  // 2 s
-// Workspaces and k splits are planned for this many SMs (GB300); a device that
-// offers fewer co-resident CTA pairs uses less of them.
-constexpr int kPlanSms = 152;
 
 struct Device {
   bool initialised = false;
@@ -657,9 +779,32 @@ bool prepare_kernel(int sms, int* pairs) {
 template <int KC>
 bool prepare_scores(int sms, int* pairs) {
   return prepare_kernel<ScoreEpi<KC>, false, false, false>(sms, pairs) &&
-         prepare_kernel<ScoreEpi<KC>, true, false, false>(sms, pairs) &&
-         cudaFuncSetAttribute(join_kernel<KC>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              std::max(1, kMaxSlots * KC * 8)) == cudaSuccess;
+         prepare_kernel<ScoreEpi<KC>, true, false, false>(sms, pairs);
+}
+
+template <int KC>
+cudaError_t launch_join(JoinParams j, int64_t rows, cudaStream_t stream) {
+  const bool wide = rows <= kPlanSms || j.n_slots > JoinNarrow::kThreads;
+  // More logits than a block has warps: as many blocks as leave every SM at
+  // most one.
+  j.ctas = 1;
+  while (wide && j.ctas < 4 && (j.K > 0 ? j.K + 5 : 1) > j.ctas * (JoinWide::kThreads / 32) &&
+         rows * j.ctas * 2 <= kPlanSms)
+    j.ctas *= 2;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = unsigned(j.ctas);
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(rows * j.ctas), 1, 1);
+  cfg.blockDim = dim3(unsigned(wide ? JoinWide::kThreads : JoinNarrow::kThreads), 1, 1);
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = j.ctas > 1 ? 2 : 1;
+  return wide ? cudaLaunchKernelEx(&cfg, join_kernel<KC, JoinWide>, j)
+              : cudaLaunchKernelEx(&cfg, join_kernel<KC, JoinNarrow>, j);
 }
 
 fs_status device_setup(const Device** out) {
@@ -869,17 +1014,7 @@ fs_status run_scores(const fs_logprobs_args* a, const Device& dev, cudaStream_t 
     j.out_lse = a->out_lse ? a->out_lse + b0 : nullptr;
     j.out_topk_idx = KC ? a->out_topk_idx + b0 * a->K : nullptr;
     j.out_topk_logp = KC ? a->out_topk_logp + b0 * a->K : nullptr;
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(unsigned(rows), 1, 1);
-    cfg.blockDim = dim3(kJoinThreads<KC>, 1, 1);
-    cfg.dynamicSmemBytes = size_t(n_slots) * KC * 8u;
-    cfg.stream = stream;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, join_kernel<KC>, j) != cudaSuccess) {
+    if (launch_join<KC>(j, rows, stream) != cudaSuccess) {
       cudaGetLastError();
       return FS_ERR_CUDA;
     }
@@ -906,7 +1041,7 @@ Split plan_split(int64_t B, int64_t d, int64_t V) {
     const int64_t kb = ceil_div(n_kb, want), n = ceil_div(n_kb, kb);
     const int64_t waves = ceil_div(tiles * n, workers);
     const double partial_mb = n > 1 ? double(n * tiles) * (pair ? 2 : 1) * 0.131 : 0.0;
-    const double cost = double(waves * (kb + 8)) + partial_mb * 2.2;
+    const double cost = double(waves * (kb + 8)) + (n > 1 ? 30.0 + partial_mb * 2.2 : 0.0);
     if (cost < best_cost) {
       best_cost = cost;
       best = {n, kb};
@@ -980,7 +1115,7 @@ namespace {
 bool grad_sizes_ok(int64_t B, int64_t d, int64_t V) {
   return sizes_ok(B, d, V) && ceil_div(V, kBM) * ceil_div(d, kBN) <= INT_MAX &&
          ceil_div(V, kBN) * ceil_div(B, kBM) <= INT_MAX &&
-         ceil_div(B, kBM) * ceil_div(d, kBN) * 64 <= INT_MAX;
+         (ceil_div(B, kBM) + 1) * ceil_div(d, kBN) * 64 <= INT_MAX;
 }
 }  // namespace
 
@@ -1039,6 +1174,7 @@ extern "C" fs_status fs_logprobs_grad(const fs_logprobs_grad_args* a, void* stre
     s.a_box_rows = uint32_t(box_rows);
     s.policy_a = kPolicyLast;
     s.policy_b = kPolicyNormal;
+    s.early_trigger = 1;
     GradEpi::Params ep = {};
     ep.B = int32_t(B);
     ep.V = int32_t(V);
@@ -1075,26 +1211,37 @@ extern "C" fs_status fs_logprobs_grad(const fs_logprobs_grad_args* a, void* stre
     s.n_cols = int32_t(d);
     s.m_fastest = 1;
     s.a_box_rows = uint32_t(box_rows);
+    s.pdl = s.early_trigger = 1;  // W streams while the kernel before ends
     const int n = balanced(s.n_units, workers);
     if (sp.n == 1) {
       const StoreEpi::Params ep = {static_cast<__nv_bfloat16*>(a->out_dH), a->lddh,
                                    int32_t(d & ~int64_t(7))};
-      st = pair ? launch<StoreEpi, true, false, true>(dev, mg, mw, mo, s, ep, n, false, stream)
-                : launch<StoreEpi, false, false, true>(dev, mg, mw, mo, s, ep, n, false, stream);
+      st = pair ? launch<StoreEpi, true, false, true>(dev, mg, mw, mo, s, ep, n, true, stream)
+                : launch<StoreEpi, false, false, true>(dev, mg, mw, mo, s, ep, n, true, stream);
       if (st != FS_OK) return st;
     } else {
       PartialEpi::Params ep = {};
       ep.partial = reinterpret_cast<float4*>(static_cast<uint8_t*>(G) + g_bytes(B, V));
       ep.ctas = ctas;
-      st = pair ? launch<PartialEpi, true, false, true>(dev, mg, mw, mo, s, ep, n, false, stream)
-                : launch<PartialEpi, false, false, true>(dev, mg, mw, mo, s, ep, n, false, stream);
+      st = pair ? launch<PartialEpi, true, false, true>(dev, mg, mw, mo, s, ep, n, true, stream)
+                : launch<PartialEpi, false, false, true>(dev, mg, mw, mo, s, ep, n, true, stream);
       if (st != FS_OK) return st;
-      const int64_t blocks = int64_t(s.n_mt) * s.n_nt * ctas * (kBM * kBN / 8 / kSumThreads);
-      if (blocks > INT_MAX) return FS_ERR_INVALID_ARG;
-      sum_splits_kernel<<<unsigned(blocks), kSumThreads, 0, stream>>>(
-          ep.partial, int32_t(sp.n), s.n_mt * s.n_nt, s.n_nt, ctas, int32_t(B), int32_t(d),
-          static_cast<__nv_bfloat16*>(a->out_dH), a->lddh);
-      if (cudaGetLastError() != cudaSuccess) return FS_ERR_CUDA;
+      cudaLaunchAttribute attr;
+      attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+      attr.val.programmaticStreamSerializationAllowed = 1;
+      cudaLaunchConfig_t cfg = {};
+      cfg.gridDim = dim3(unsigned(s.n_mt * s.n_nt * ctas * kSumBlocksPerTile), 1, 1);
+      cfg.blockDim = dim3(kSumThreads, 1, 1);
+      cfg.stream = stream;
+      cfg.attrs = &attr;
+      cfg.numAttrs = 1;
+      if (cudaLaunchKernelEx(&cfg, sum_splits_kernel, static_cast<const float4*>(ep.partial),
+                             int32_t(sp.n), s.n_mt * s.n_nt, s.n_nt, int32_t(ctas), int32_t(B),
+                             int32_t(d), static_cast<__nv_bfloat16*>(a->out_dH),
+                             a->lddh) != cudaSuccess) {
+        cudaGetLastError();
+        return FS_ERR_CUDA;
+      }
     }
   }
 
@@ -1116,11 +1263,12 @@ extern "C" fs_status fs_logprobs_grad(const fs_logprobs_grad_args* a, void* stre
     s.m_fastest = 0;
     s.a_box_rows = 0;
     s.policy_b = kPolicyLast;
+    s.pdl = 1;  // H streams while the kernel before ends
     const StoreEpi::Params ep = {static_cast<__nv_bfloat16*>(a->out_dW), a->lddw,
                                  int32_t(d & ~int64_t(7))};
     const int n = balanced(s.n_units, wpair ? dev.pairs : dev.sms);
-    st = wpair ? launch<StoreEpi, true, true, true>(dev, mg, mh, mo, s, ep, n, false, stream)
-               : launch<StoreEpi, false, true, true>(dev, mg, mh, mo, s, ep, n, false, stream);
+    st = wpair ? launch<StoreEpi, true, true, true>(dev, mg, mh, mo, s, ep, n, true, stream)
+               : launch<StoreEpi, false, true, true>(dev, mg, mh, mo, s, ep, n, true, stream);
     if (st != FS_OK) return st;
   }
   return FS_OK;
