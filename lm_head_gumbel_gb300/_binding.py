@@ -9,6 +9,7 @@ built, every call raises ``FsError`` -- there is no fallback.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import NamedTuple, Optional
 
@@ -399,43 +400,80 @@ def fs_gumbel_noise(b0, nb, v0, nv, *, seed=0, offset=0, seeds=None, out=None, d
 
 
 # ---- the operators of fs_vocab.h ------------------------------------------
-def _check_on(dev, **tensors):
-    """Every given tensor lies on `dev` (the kernels read raw pointers)."""
-    for name, t in tensors.items():
-        if t is not None and t.device != dev:
-            raise FsError(FS_ERR_INVALID_ARG, f"{name} must be on {dev}")
+# These calls take a few microseconds on the GPU at decode sizes, so their host
+# side is kept short: one check per argument, raw pointers instead of ctypes
+# objects.
+def _refuse(what):
+    raise FsError(FS_ERR_INVALID_ARG, what)
 
 
-def _check_rows(name, t, dtype, n):
-    if t is not None and (t.dtype != dtype or t.dim() != 1 or t.shape[0] != n
-                          or not t.is_contiguous()):
-        raise FsError(FS_ERR_INVALID_ARG, f"{name} must be a contiguous {dtype} vector of {n}")
+def _vector(name, t, dtype, n, dev):
+    """Address of a contiguous vector of n elements on `dev`."""
+    if t.dtype is not dtype or t.dim() != 1 or t.shape[0] != n or t.device != dev \
+            or not t.is_contiguous():
+        _refuse(f"{name} must be a contiguous {dtype} vector of {n} on {dev}")
+    return t.data_ptr()
 
 
-def _check_mask(vocab_mask, B, V):
-    if vocab_mask is not None and (
-            vocab_mask.dtype != torch.int32 or vocab_mask.dim() != 2 or vocab_mask.shape[0] != B
-            or vocab_mask.shape[1] < (V + 31) // 32 or vocab_mask.stride(1) != 1):
-        raise FsError(FS_ERR_INVALID_ARG, "vocab_mask must be an int32 matrix [B, >= ceil(V/32)]")
+def _vector_or_none(name, t, dtype, n, dev):
+    return None if t is None else _vector(name, t, dtype, n, dev)
 
 
-def _ld(t):
-    """Row stride of a matrix; of a single row, one that any check accepts."""
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), (t.shape[1] + 7) // 8 * 8)
+def _matrix(name, t, dtype, n, d, dev):
+    """Address and row stride of an [n, d] matrix on `dev` (of a single row: a
+    stride that every check accepts)."""
+    if t.dtype is not dtype or t.dim() != 2 or t.device != dev:
+        _refuse(f"{name} must be a {dtype} matrix on {dev}")
+    rows, cols = t.shape
+    ld, unit = t.stride()
+    if rows != n or cols != d or unit != 1:
+        _refuse(f"{name} must be [{n}, {d}] with unit column stride")
+    return t.data_ptr(), ld if n > 1 else max(ld, (d + 7) // 8 * 8)
 
 
-def _check_workspace(workspace, dev):
-    if workspace is not None and (workspace.device != dev or not workspace.is_contiguous()):
+def _mask(vocab_mask, B, V, dev):
+    if vocab_mask is None:
+        return None, 0
+    if vocab_mask.dtype is not torch.int32 or vocab_mask.dim() != 2 \
+            or vocab_mask.shape[0] != B or vocab_mask.shape[1] < (V + 31) // 32 \
+            or vocab_mask.stride(1) != 1 or vocab_mask.device != dev:
+        _refuse(f"vocab_mask must be an int32 matrix [B, >= ceil(V/32)] on {dev}")
+    return vocab_mask.data_ptr(), max(vocab_mask.stride(0), vocab_mask.shape[1])
+
+
+def _workspace(workspace, size, dev):
+    """Address and bytes of the given workspace, or of a new one.  (A new one
+    may be freed when the call returns: torch reuses it in stream order.)"""
+    if workspace is None:
+        workspace = torch.empty(size, dtype=torch.uint8, device=dev)
+    elif workspace.device != dev or not workspace.is_contiguous():
         raise FsError(FS_ERR_WORKSPACE, f"workspace must be a contiguous tensor on {dev}")
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
-def _run(name, dev, call):
+def _head(H, W):
+    """H's and W's sizes, addresses and strides."""
+    if not H.is_cuda or H.dim() != 2 or W.dim() != 2:
+        _refuse("H and W must be CUDA bfloat16 matrices")
+    (B, d), dev = H.shape, H.device
+    V = W.shape[0]
+    return (B, d, V, dev) + _matrix("H", H, torch.bfloat16, B, d, dev) \
+        + _matrix("W", W, torch.bfloat16, V, d, dev)
+
+
+def _stream(stream, dev):
+    if stream is None:  # without building a Stream object
+        return torch._C._cuda_getCurrentRawStream(dev.index)
+    return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
+
+
+def _run(name, dev, function, *args):
     """Call the library with `dev` current and its status checked."""
     if torch.cuda.current_device() == dev.index:
-        st = call()
+        st = function(*args)
     else:
         with torch.cuda.device(dev):
-            st = call()
+            st = function(*args)
     if st != FS_OK:
         raise FsError(st, name)
 
@@ -449,6 +487,7 @@ class FsLogprobs(NamedTuple):
     topk_logp: Optional[torch.Tensor]  # fp32 [B, K]
 
 
+@functools.lru_cache(maxsize=256)
 def fs_logprobs_workspace_size(B: int, V: int, K: int = 0) -> int:
     return int(load_library().fs_logprobs_workspace_size(int(B), int(V), int(K)))
 
@@ -467,73 +506,47 @@ def fs_logprobs(H, W, tokens=None, K=0, *, temperature=None, vocab_mask=None, vo
     tensors to fill, made when None.  workspace: a uint8 tensor of
     fs_logprobs_workspace_size(B, V, K) bytes, or None.  Returns FsLogprobs."""
     lib = load_library()
-    _check_2d("H", H, torch.bfloat16)
-    _check_2d("W", W, torch.bfloat16)
-    B, d = H.shape
-    V = W.shape[0]
-    dev = H.device
+    B, d, V, dev, h, ldh, w, ldw = _head(H, W)
     K = int(K)
-    if W.shape[1] != d:
-        raise FsError(FS_ERR_INVALID_ARG, "H and W must have the same number of columns")
     if not 0 <= K <= FS_LOGPROBS_TOPK_MAX:
-        raise FsError(FS_ERR_INVALID_ARG, f"K must be 0 to {FS_LOGPROBS_TOPK_MAX}")
-    _check_rows("tokens", tokens, torch.int64, B)
-    _check_rows("temperature", temperature, torch.float32, B)
-    _check_mask(vocab_mask, B, V)
+        _refuse(f"K must be 0 to {FS_LOGPROBS_TOPK_MAX}")
+    f32 = torch.float32
+    mask, mask_ld = _mask(vocab_mask, B, V, dev)
     if tokens is None:
         out_logp = None
     elif out_logp is None:
-        out_logp = torch.empty(B, dtype=torch.float32, device=dev)
+        out_logp = torch.empty(B, dtype=f32, device=dev)
     if out_entropy is None:
-        out_entropy = torch.empty(B, dtype=torch.float32, device=dev)
+        out_entropy = torch.empty(B, dtype=f32, device=dev)
     if out_lse is None:
-        out_lse = torch.empty(B, dtype=torch.float32, device=dev)
+        out_lse = torch.empty(B, dtype=f32, device=dev)
+    idx = top = None
     if K == 0:
         out_topk_idx = out_topk_logp = None
     else:
         if out_topk_idx is None:
             out_topk_idx = torch.empty((B, K), dtype=torch.int64, device=dev)
         if out_topk_logp is None:
-            out_topk_logp = torch.empty((B, K), dtype=torch.float32, device=dev)
-        for name, t, dtype in (("out_topk_idx", out_topk_idx, torch.int64),
-                               ("out_topk_logp", out_topk_logp, torch.float32)):
-            if t.dtype != dtype or tuple(t.shape) != (B, K) or not t.is_contiguous():
-                raise FsError(FS_ERR_INVALID_ARG, f"{name} must be a contiguous {dtype} [B, K]")
-    for name, t in (("out_logp", out_logp), ("out_entropy", out_entropy), ("out_lse", out_lse)):
-        _check_rows(name, t, torch.float32, B)
-    if workspace is None:
-        workspace = torch.empty(max(1, lib.fs_logprobs_workspace_size(B, V, K)),
-                                dtype=torch.uint8, device=dev)
-    _check_on(dev, W=W, tokens=tokens, temperature=temperature, vocab_mask=vocab_mask,
-              out_logp=out_logp, out_entropy=out_entropy, out_lse=out_lse,
-              out_topk_idx=out_topk_idx, out_topk_logp=out_topk_logp)
-    _check_workspace(workspace, dev)
+            out_topk_logp = torch.empty((B, K), dtype=f32, device=dev)
+        if not (out_topk_idx.is_contiguous() and out_topk_logp.is_contiguous()):
+            _refuse("out_topk_idx and out_topk_logp must be contiguous")
+        idx = _matrix("out_topk_idx", out_topk_idx, torch.int64, B, K, dev)[0]
+        top = _matrix("out_topk_logp", out_topk_logp, f32, B, K, dev)[0]
+    workspace, ws, ws_bytes = _workspace(workspace, fs_logprobs_workspace_size(B, V, K), dev)
     args = FsLogprobsArgs(
-        H=_ptr(H), W=_ptr(W), temperature=_ptr(temperature), vocab_mask=_ptr(vocab_mask),
-        mask_ld=0 if vocab_mask is None else max(vocab_mask.stride(0), vocab_mask.shape[1]),
-        tokens=_ptr(tokens), B=B, d=d, V=V, ldh=_ld(H), ldw=_ld(W),
-        vocab_offset=int(vocab_offset), K=K, out_logp=_ptr(out_logp),
-        out_entropy=_ptr(out_entropy), out_lse=_ptr(out_lse), out_topk_idx=_ptr(out_topk_idx),
-        out_topk_logp=_ptr(out_topk_logp), workspace=_ptr(workspace),
-        workspace_bytes=workspace.numel() * workspace.element_size(),
-        flags=FS_FLAG_OVERLAP_PREVIOUS if overlap_previous else 0)
-    _run("fs_logprobs", dev,
-         lambda: lib.fs_logprobs(ctypes.byref(args), _stream_handle(stream, dev)))
+        h, w, _vector_or_none("temperature", temperature, f32, B, dev), mask, mask_ld,
+        _vector_or_none("tokens", tokens, torch.int64, B, dev), B, d, V, ldh, ldw,
+        int(vocab_offset), K, _vector_or_none("out_logp", out_logp, f32, B, dev),
+        _vector("out_entropy", out_entropy, f32, B, dev),
+        _vector("out_lse", out_lse, f32, B, dev), idx, top, ws, ws_bytes,
+        FS_FLAG_OVERLAP_PREVIOUS if overlap_previous else 0)
+    _run("fs_logprobs", dev, lib.fs_logprobs, args, _stream(stream, dev))
     return FsLogprobs(out_logp, out_entropy, out_lse, out_topk_idx, out_topk_logp)
 
 
+@functools.lru_cache(maxsize=256)
 def fs_logprobs_grad_workspace_size(B: int, d: int, V: int) -> int:
     return int(load_library().fs_logprobs_grad_workspace_size(int(B), int(d), int(V)))
-
-
-def _grad_like(name, out, n, d, dev):
-    """bf16 [n, d] result whose rows start on 16-byte boundaries."""
-    if out is None:
-        return torch.empty((n, (d + 7) // 8 * 8), dtype=torch.bfloat16, device=dev)[:, :d]
-    _check_2d(name, out, torch.bfloat16)
-    if tuple(out.shape) != (n, d):
-        raise FsError(FS_ERR_INVALID_ARG, f"{name} must be [{n}, {d}]")
-    return out
 
 
 def fs_logprobs_grad(H, W, tokens, lse, grad_logp, *, entropy=None, grad_entropy=None,
@@ -547,57 +560,51 @@ def fs_logprobs_grad(H, W, tokens, lse, grad_logp, *, entropy=None, grad_entropy
     out_dW when given), None where need_dH / need_dW is false.  workspace: a
     uint8 tensor of fs_logprobs_grad_workspace_size(B, d, V) bytes, or None."""
     lib = load_library()
-    _check_2d("H", H, torch.bfloat16)
-    _check_2d("W", W, torch.bfloat16)
-    B, d = H.shape
-    V = W.shape[0]
-    dev = H.device
-    if W.shape[1] != d:
-        raise FsError(FS_ERR_INVALID_ARG, "H and W must have the same number of columns")
+    B, d, V, dev, h, ldh, w, ldw = _head(H, W)
+    f32, bf16 = torch.float32, torch.bfloat16
     if not (need_dH or need_dW):
-        raise FsError(FS_ERR_INVALID_ARG, "neither dH nor dW is asked for")
-    for name, t, dtype in (("tokens", tokens, torch.int64), ("lse", lse, torch.float32),
-                           ("grad_logp", grad_logp, torch.float32)):
-        if t is None:
-            raise FsError(FS_ERR_INVALID_ARG, f"{name} is required")
-        _check_rows(name, t, dtype, B)
-    for name, t in (("entropy", entropy), ("grad_entropy", grad_entropy),
-                    ("temperature", temperature)):
-        _check_rows(name, t, torch.float32, B)
+        _refuse("neither dH nor dW is asked for")
+    if tokens is None or lse is None or grad_logp is None:
+        _refuse("tokens, lse and grad_logp are required")
     if grad_entropy is None:
         entropy = None
-    _check_mask(vocab_mask, B, V)
-    dH = _grad_like("out_dH", out_dH, B, d, dev) if need_dH else None
-    dW = _grad_like("out_dW", out_dW, V, d, dev) if need_dW else None
-    if workspace is None:
-        workspace = torch.empty(max(1, lib.fs_logprobs_grad_workspace_size(B, d, V)),
-                                dtype=torch.uint8, device=dev)
-    _check_on(dev, W=W, tokens=tokens, lse=lse, grad_logp=grad_logp, entropy=entropy,
-              grad_entropy=grad_entropy, temperature=temperature, vocab_mask=vocab_mask,
-              out_dH=dH, out_dW=dW)
-    _check_workspace(workspace, dev)
+    mask, mask_ld = _mask(vocab_mask, B, V, dev)
+    ld = (d + 7) // 8 * 8  # results made here: rows on 16-byte boundaries
+    dh = dw = None
+    lddh = lddw = 0
+    if not need_dH:
+        out_dH = None
+    else:
+        if out_dH is None:
+            out_dH = torch.empty((B, ld), dtype=bf16, device=dev)[:, :d]
+        dh, lddh = _matrix("out_dH", out_dH, bf16, B, d, dev)
+    if not need_dW:
+        out_dW = None
+    else:
+        if out_dW is None:
+            out_dW = torch.empty((V, ld), dtype=bf16, device=dev)[:, :d]
+        dw, lddw = _matrix("out_dW", out_dW, bf16, V, d, dev)
+    workspace, ws, ws_bytes = _workspace(workspace, fs_logprobs_grad_workspace_size(B, d, V), dev)
     args = FsLogprobsGradArgs(
-        H=_ptr(H), W=_ptr(W), temperature=_ptr(temperature), vocab_mask=_ptr(vocab_mask),
-        mask_ld=0 if vocab_mask is None else max(vocab_mask.stride(0), vocab_mask.shape[1]),
-        tokens=_ptr(tokens), lse=_ptr(lse), entropy=_ptr(entropy), grad_logp=_ptr(grad_logp),
-        grad_entropy=_ptr(grad_entropy), B=B, d=d, V=V, ldh=_ld(H), ldw=_ld(W),
-        vocab_offset=int(vocab_offset), out_dH=_ptr(dH), out_dW=_ptr(dW),
-        lddh=_ld(dH) if need_dH else 0, lddw=_ld(dW) if need_dW else 0,
-        workspace=_ptr(workspace),
-        workspace_bytes=workspace.numel() * workspace.element_size())
-    _run("fs_logprobs_grad", dev,
-         lambda: lib.fs_logprobs_grad(ctypes.byref(args), _stream_handle(stream, dev)))
-    return dH, dW
+        h, w, _vector_or_none("temperature", temperature, f32, B, dev), mask, mask_ld,
+        _vector("tokens", tokens, torch.int64, B, dev), _vector("lse", lse, f32, B, dev),
+        _vector_or_none("entropy", entropy, f32, B, dev),
+        _vector("grad_logp", grad_logp, f32, B, dev),
+        _vector_or_none("grad_entropy", grad_entropy, f32, B, dev), B, d, V, ldh, ldw,
+        int(vocab_offset), dh, dw, lddh, lddw, ws, ws_bytes)
+    _run("fs_logprobs_grad", dev, lib.fs_logprobs_grad, args, _stream(stream, dev))
+    return out_dH, out_dW
 
 
 _ELEMENT = {torch.bfloat16: FS_BF16, torch.float32: FS_F32}
 
 
-def _check_table(name, t):
-    if t.dtype not in _ELEMENT or t.dim() != 2 or t.shape[1] < 1 or t.stride(1) != 1 \
-            or not t.is_cuda:
-        raise FsError(FS_ERR_INVALID_ARG,
-                      f"{name} must be a CUDA bfloat16 or float32 matrix with unit column stride")
+def _table(name, t):
+    """Element code of a bf16 or fp32 CUDA matrix."""
+    code = _ELEMENT.get(t.dtype)
+    if code is None or t.dim() != 2 or not t.is_cuda:
+        _refuse(f"{name} must be a CUDA bfloat16 or float32 matrix")
+    return code
 
 
 def fs_embed(ids, E, *, scale=1.0, vocab_offset=0, out=None, stream=None):
@@ -605,25 +612,19 @@ def fs_embed(ids, E, *, scale=1.0, vocab_offset=0, out=None, stream=None):
     one of E's rows (padding, another shard).  ids: int64 [N]; E: bf16 or fp32
     [V, d].  Returns out ([N, d] of E's type)."""
     lib = load_library()
-    _check_table("E", E)
-    dev = E.device
+    code, dev, dtype = _table("E", E), E.device, E.dtype
     V, d = E.shape
-    if ids.dim() != 1:
-        raise FsError(FS_ERR_INVALID_ARG, "ids must be a vector")
     N = ids.shape[0]
-    _check_rows("ids", ids, torch.int64, N)
     if out is None:
-        out = torch.empty((N, d), dtype=E.dtype, device=dev)
-    elif out.dtype != E.dtype or tuple(out.shape) != (N, d) or out.stride(1) != 1:
-        raise FsError(FS_ERR_INVALID_ARG, "out must be [N, d] of E's type")
-    _check_on(dev, ids=ids, out=out)
-    _run("fs_embed", dev, lambda: lib.fs_embed(
-        ids.data_ptr(), N, E.data_ptr(), V, d, max(E.stride(0), d), _ELEMENT[E.dtype],
-        float(scale), int(vocab_offset), out.data_ptr(), max(out.stride(0), d),
-        _stream_handle(stream, dev)))
+        out = torch.empty((N, d), dtype=dtype, device=dev)
+    e, lde = _matrix("E", E, dtype, V, d, dev)
+    o, ldo = _matrix("out", out, dtype, N, d, dev)
+    _run("fs_embed", dev, lib.fs_embed, _vector("ids", ids, torch.int64, N, dev), N, e, V, d, lde,
+         code, scale, vocab_offset, o, ldo, _stream(stream, dev))
     return out
 
 
+@functools.lru_cache(maxsize=256)
 def fs_embed_grad_workspace_size(N: int, d: int) -> int:
     return int(load_library().fs_embed_grad_workspace_size(int(N), int(d)))
 
@@ -638,27 +639,19 @@ def fs_embed_grad(ids, dY, V, *, scale=1.0, vocab_offset=0, out=None, out_dtype=
     bits.  workspace: a uint8 tensor of fs_embed_grad_workspace_size(N, d)
     bytes, or None."""
     lib = load_library()
-    _check_table("dY", dY)
-    dev = dY.device
+    y_code, dev = _table("dY", dY), dY.device
     N, d = dY.shape
     V = int(V)
-    _check_rows("ids", ids, torch.int64, N)
     if out is None:
         if accumulate:
-            raise FsError(FS_ERR_INVALID_ARG, "accumulate needs out")
+            _refuse("accumulate needs out")
         out = torch.empty((V, d), dtype=out_dtype or dY.dtype, device=dev)
-    _check_table("out", out)
-    if tuple(out.shape) != (V, d):
-        raise FsError(FS_ERR_INVALID_ARG, f"out must be [{V}, {d}]")
-    if workspace is None and N > 0:
-        workspace = torch.empty(max(1, lib.fs_embed_grad_workspace_size(N, d)),
-                                dtype=torch.uint8, device=dev)
-    _check_on(dev, ids=ids, out=out)
-    _check_workspace(workspace, dev)
-    _run("fs_embed_grad", dev, lambda: lib.fs_embed_grad(
-        ids.data_ptr(), N, dY.data_ptr(), V, d, max(dY.stride(0), d), _ELEMENT[dY.dtype],
-        float(scale), int(vocab_offset), out.data_ptr(), max(out.stride(0), d),
-        _ELEMENT[out.dtype], 1 if accumulate else 0, _ptr(workspace),
-        0 if workspace is None else workspace.numel() * workspace.element_size(),
-        _stream_handle(stream, dev)))
+    e_code = _table("out", out)
+    y, ldy = _matrix("dY", dY, dY.dtype, N, d, dev)
+    e, lde = _matrix("out", out, out.dtype, V, d, dev)
+    ids_at = _vector("ids", ids, torch.int64, N, dev)
+    workspace, ws, ws_bytes = _workspace(workspace, fs_embed_grad_workspace_size(N, d), dev)
+    _run("fs_embed_grad", dev, lib.fs_embed_grad, ids_at, N, y, V, d, ldy, y_code, scale,
+         vocab_offset, e, lde, e_code, 1 if accumulate else 0, ws, ws_bytes,
+         _stream(stream, dev))
     return out
