@@ -71,6 +71,16 @@ __device__ __forceinline__ void st_cluster(uint32_t addr, uint64_t v) {
   asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(addr), "l"(v) : "memory");
 }
 
+// Arrive on an mbarrier given by its shared::cluster address, ordering no
+// memory: what it reports is that tensor-memory loads have completed (their
+// wait has returned).  The releasing form first waits for the thread's earlier
+// stores, 2100 cycles beside this kernel's TMA stores.
+__device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t bar_cluster_addr) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(
+                   bar_cluster_addr)
+               : "memory");
+}
+
 // max that returns NaN if either input is NaN.
 __device__ __forceinline__ float max_nan(float a, float b) {
   float r;
@@ -96,12 +106,13 @@ constexpr int kThreads = 32 * (2 + kEpiWarps);
 constexpr int kMaxStages = 8;
 constexpr uint32_t kChunkBytes = 64 * kBK * 2;  // one 64 x 64 box, 8 KB
 constexpr uint32_t kTmemCols = 2 * kBN;
-constexpr uint32_t kStagingBytes = kEpiWarps * 4096;  // one 32 x 64 bf16 box per epilogue warp
+constexpr uint32_t kBoxBytes = 2 * 4096;  // an epilogue warp's two 32 x 64 bf16 boxes
+constexpr uint32_t kStagingBytes = kEpiWarps * kBoxBytes;
 constexpr int kErrWaitTimeout = 1;  // the library's device error word, bit 0
 
 template <class Epi>
 __host__ __device__ constexpr uint32_t ring_bytes() {
-  return Epi::kStaged ? 192u * 1024u : 224u * 1024u;
+  return Epi::kStaged ? 160u * 1024u : 224u * 1024u;
 }
 template <class Epi>
 __host__ __device__ constexpr size_t smem_bytes() {
@@ -134,22 +145,46 @@ struct Unit {
   int mt, nt, split, kb0, n_kb;
 };
 
-__device__ __forceinline__ Unit unit_of(const Shape& s, int u) {
-  const int n_tiles = s.n_mt * s.n_nt;
-  Unit r;
-  r.split = u / n_tiles;
-  const int t = u - r.split * n_tiles;
-  if (s.m_fastest) {
-    r.nt = t / s.n_mt;
-    r.mt = t - r.nt * s.n_mt;
-  } else {
-    r.mt = t / s.n_nt;
-    r.nt = t - r.mt * s.n_nt;
+// A worker's units, every n_workers-th of the list, without a division each.
+struct Units {
+  int u, step;              // unit, stride
+  int inner, outer, split;  // of unit u
+  int inner_step, outer_step;
+  __device__ __forceinline__ Units(const Shape& s, int worker, int n_workers)
+      : u(worker), step(n_workers) {
+    const int n_inner = s.m_fastest ? s.n_mt : s.n_nt, n_outer = s.m_fastest ? s.n_nt : s.n_mt;
+    const int t = worker / n_inner;
+    inner = worker - t * n_inner;
+    split = t / n_outer;
+    outer = t - split * n_outer;
+    outer_step = n_workers / n_inner;
+    inner_step = n_workers - outer_step * n_inner;
   }
-  r.kb0 = r.split * s.kb_per_split;
-  r.n_kb = min(s.kb_per_split, s.n_kb - r.kb0);
-  return r;
-}
+  __device__ __forceinline__ bool more(const Shape& s) const { return u < s.n_units; }
+  __device__ __forceinline__ Unit get(const Shape& s) const {
+    Unit r;
+    r.mt = s.m_fastest ? inner : outer;
+    r.nt = s.m_fastest ? outer : inner;
+    r.split = split;
+    r.kb0 = split * s.kb_per_split;
+    r.n_kb = min(s.kb_per_split, s.n_kb - r.kb0);
+    return r;
+  }
+  __device__ __forceinline__ void next(const Shape& s) {
+    const int n_inner = s.m_fastest ? s.n_mt : s.n_nt, n_outer = s.m_fastest ? s.n_nt : s.n_mt;
+    u += step;
+    inner += inner_step;
+    outer += outer_step;
+    if (inner >= n_inner) {
+      inner -= n_inner;
+      ++outer;
+    }
+    while (outer >= n_outer) {
+      outer -= n_outer;
+      ++split;
+    }
+  }
+};
 
 // Bounded mbarrier waits, with the sampler's semantics: past the limit the
 // CTA raises its abort flag and the device error word, and every role winds
@@ -206,8 +241,8 @@ struct TileAt {
 
 // kAmn / kBmn: A's M (B's N) dimension is the contiguous one in memory.
 // finish() gets the thread's M row in its worker's first unit.
-// Epi: struct with Params, State, kStaged (uses a bf16 box per warp in shared
-// memory and tmap_d), and static device functions start / tile / finish.
+// Epi: struct with Params, State, kStaged (uses bf16 boxes in shared memory and
+// tmap_d), and static device functions start / tile / finish.
 template <class Epi, bool kPair, bool kAmn, bool kBmn>
 __global__ void __launch_bounds__(kThreads, 1)
     contract_kernel(const __grid_constant__ CUtensorMap tmap_a,
@@ -322,8 +357,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < n_held; ++i) load_a(uint32_t(i), held_kb[i], held_mt[i]);
       deferring = false;
     };
-    for (int u = worker; ok && u < s.n_units; u += n_workers) {
-      const Unit t = unit_of(s, u);
+    for (Units it(s, worker, n_workers); ok && it.more(s); it.next(s)) {
+      const Unit t = it.get(s);
       for (int kb = t.kb0; kb < t.kb0 + t.n_kb; ++kb) {
         if (!waiter.wait_warp(&empty_bar[stage], phase ^ 1u)) {
           ok = false;
@@ -378,8 +413,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         else
           ptx::mma_commit(bar);
       };
-      for (int u = worker; ok && u < s.n_units; u += n_workers) {
-        const Unit t = unit_of(s, u);
+      for (Units it(s, worker, n_workers); ok && it.more(s); it.next(s)) {
+        const Unit t = it.get(s);
         if (!waiter.wait_warp(&tempty_bar[acc], acc_phase ^ 1u)) break;
         ptx::tc_fence_after();
         const uint32_t d_tmem = tmem_base + acc * kBN;
@@ -431,13 +466,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int e = warp - 2;
     const int quad = warp & 3;  // the tensor-memory lane quadrant this warp may read
     const int half = e >> 2;
-    uint8_t* box = staging + e * 4096;
+    uint8_t* box = staging + e * kBoxBytes;
     uint32_t acc = 0, acc_phase = 0;
     typename Epi::State st;
     Epi::start(ep, st);
-    for (int u = worker; u < s.n_units; u += n_workers) {
+    Units it(s, worker, n_workers);
+    const int first_row = (it.get(s).mt * kCtas + rank) * kBM + quad * 32 + lane;
+    for (; it.more(s); it.next(s)) {
       TileAt at;
-      at.unit = unit_of(s, u);
+      at.unit = it.get(s);
       at.rank = rank;
       at.quad = quad;
       at.half = half;
@@ -449,21 +486,26 @@ __global__ void __launch_bounds__(kThreads, 1)
       ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
       if (!ok) break;
       ptx::tc_fence_after();
+      // The epilogue calls this once its last tensor-memory load has completed:
+      // the next MMAs into this accumulator need not wait for its stores.
+      auto release = [&]() {
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if constexpr (kPair)
+            ptx::mbar_arrive_cluster_relaxed(ptx::cluster_addr(&tempty_bar[acc], 0));
+          else
+            ptx::mbar_arrive(&tempty_bar[acc]);
+        }
+      };
       if (at.row0 < s.m_rows && at.col0 < s.n_cols)
-        Epi::tile(ep, st, at, lane, box, &tmap_d, s);
-      ptx::tc_fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        if constexpr (kPair)
-          ptx::mbar_arrive_cluster(ptx::cluster_addr(&tempty_bar[acc], 0));
-        else
-          ptx::mbar_arrive(&tempty_bar[acc]);
-      }
+        Epi::tile(ep, st, at, lane, box, &tmap_d, s, release);
+      else
+        release();
       acc ^= 1u;
       if (acc == 0) acc_phase ^= 1u;
     }
-    Epi::finish(ep, st, worker, (unit_of(s, worker).mt * kCtas + rank) * kBM + quad * 32 + lane,
-                half, s);
+    Epi::finish(ep, st, worker, first_row, half, s);
     if (Epi::kStaged && lane == 0) ptx::bulk_wait();
   }
 
@@ -485,27 +527,32 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // ---------------------------------------------------------------------------
-// A bf16 tile through shared memory: the warp's 32 rows x 64 columns are
-// written in the store box's 128-byte swizzle (16-byte chunk c of row r at
-// chunk c ^ (r & 7), so a warp's writes touch every bank once) and one TMA
-// store takes them out, clipped at the tensor's edges.
+// A bf16 tile through shared memory: the warp's 32 rows x 128 columns are
+// written as two boxes of 64 columns in the store's 128-byte swizzle (16-byte
+// chunk c of row r at chunk c ^ (r & 7), so a warp's writes touch every bank
+// equally often) and TMA stores take them out, clipped at the tensor's edges.
 __device__ __forceinline__ void box_begin(int lane) {
-  if (lane == 0) ptx::bulk_wait_read();  // the box's last store has been read
+  if (lane == 0) ptx::bulk_wait_read();  // the boxes' last stores have been read
   __syncwarp();
 }
-// Columns [8c, 8c+8) of the lane's row.
-__device__ __forceinline__ void box_put(uint8_t* box, int lane, int c, const float (&v)[8]) {
-  __nv_bfloat162 h[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) h[i] = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-  *reinterpret_cast<uint4*>(box + lane * 128 + ((c ^ (lane & 7)) << 4)) =
-      *reinterpret_cast<const uint4*>(h);
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
 }
-__device__ __forceinline__ void box_end(uint8_t* box, const void* tmap, int lane, int x, int y) {
+// Columns [8c, 8c + 8) of the lane's row, as bf16 pairs.
+__device__ __forceinline__ void box_put(uint8_t* box, int lane, int c, uint32_t v0, uint32_t v1,
+                                        uint32_t v2, uint32_t v3) {
+  *reinterpret_cast<uint4*>(box + (c >> 3) * 4096 + lane * 128 + (((c & 7) ^ (lane & 7)) << 4)) =
+      make_uint4(v0, v1, v2, v3);
+}
+// Store the boxes whose first column lies below `cols`.
+__device__ __forceinline__ void box_end(uint8_t* box, const void* tmap, int lane, int x, int y,
+                                        int cols) {
   ptx::fence_async_smem();
   __syncwarp();
   if (lane == 0) {
-    ptx::tma_store_2d(tmap, box, x, y);
+    if (x < cols) ptx::tma_store_2d(tmap, box, x, y);
+    if (x + 64 < cols) ptx::tma_store_2d(tmap, box + 4096, x + 64, y);
     ptx::bulk_commit();
   }
 }
@@ -514,6 +561,11 @@ __device__ __forceinline__ void box_end(uint8_t* box, const void* tmap, int lane
 // store writes whole 16-byte pieces, so tmap_d covers the columns below whole_n
 // (a multiple of 8); the up to 7 columns behind are stored one by one, and
 // nothing past a row's end is touched.
+//
+// With few k slices per unit this epilogue is what bounds the kernel (dW of 96
+// rows: 2 slices): its steps -- load, wait for the boxes, write them, fence,
+// store -- depend on one another, so they are taken once per 128 columns, and
+// the accumulator is given back before the boxes are written.
 struct StoreEpi {
   static constexpr bool kStaged = true;
   struct Params {
@@ -523,33 +575,38 @@ struct StoreEpi {
   };
   struct State {};
   static __device__ __forceinline__ void start(const Params&, State&) {}
+  template <class Release>
   static __device__ __forceinline__ void tile(const Params& p, State&, const TileAt& at, int lane,
-                                              uint8_t* box, const void* tmap, const Shape& s) {
-#pragma unroll 1
+                                              uint8_t* box, const void* tmap, const Shape& s,
+                                              Release release) {
+    uint32_t v[64];  // the row's 128 columns as bf16 pairs
+#pragma unroll
     for (int c = 0; c < 2; ++c) {
-      const int x0 = at.col0 + c * 64;
-      if (x0 >= s.n_cols) break;
-      // The sums first: the box's last store is being read meanwhile.
       uint32_t r[2][32];
       ptx::tmem_ld_32x32b_x32(at.taddr + uint32_t(c * 64), r[0]);
       ptx::tmem_ld_32x32b_x32(at.taddr + uint32_t(c * 64 + 32), r[1]);
       ptx::tmem_wait_ld();
-      box_begin(lane);
 #pragma unroll
-      for (int q = 0; q < 8; ++q) {
-        float v[8];
+      for (int i = 0; i < 32; ++i)
+        v[c * 32 + i] = pack_bf16(__uint_as_float(r[i >> 4][(i & 15) * 2]),
+                                  __uint_as_float(r[i >> 4][(i & 15) * 2 + 1]));
+    }
+    release();
+    box_begin(lane);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[q >> 2][(q & 3) * 8 + i]);
-        box_put(box, lane, q, v);
-        const int x = x0 + q * 8;
-        if (x == p.whole_n && at.row0 + lane < s.m_rows) {
-          __nv_bfloat16* out = p.out + int64_t(at.row0 + lane) * p.ld;
+    for (int q = 0; q < 16; ++q)
+      box_put(box, lane, q, v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+    box_end(box, tmap, lane, at.col0, at.row0, p.whole_n);
+    const int tail = p.whole_n - at.col0;  // where the single columns begin
+    if (tail >= 0 && tail < 128 && p.whole_n < s.n_cols && at.row0 + lane < s.m_rows) {
+      uint16_t* out = reinterpret_cast<uint16_t*>(p.out + int64_t(at.row0 + lane) * p.ld);
+#pragma unroll
+      for (int q = 0; q < 16; ++q)
+        if (tail == q * 8)
 #pragma unroll
           for (int i = 0; i < 7; ++i)
-            if (x + i < s.n_cols) out[x + i] = __float2bfloat16_rn(v[i]);
-        }
-      }
-      if (x0 < p.whole_n) box_end(box, tmap, lane, x0, at.row0);
+            if (p.whole_n + i < s.n_cols)
+              out[p.whole_n + i] = uint16_t(v[4 * q + i / 2] >> (16 * (i & 1)));
     }
   }
   static __device__ __forceinline__ void finish(const Params&, State&, int, int, int,
@@ -567,8 +624,10 @@ struct PartialEpi {
   };
   struct State {};
   static __device__ __forceinline__ void start(const Params&, State&) {}
+  template <class Release>
   static __device__ __forceinline__ void tile(const Params& p, State&, const TileAt& at, int lane,
-                                              uint8_t*, const void*, const Shape& s) {
+                                              uint8_t*, const void*, const Shape& s,
+                                              Release release) {
     const int64_t slot =
         (int64_t(at.unit.split) * s.n_mt * s.n_nt + int64_t(at.unit.mt) * s.n_nt + at.unit.nt) *
             p.ctas + at.rank;
@@ -584,6 +643,7 @@ struct PartialEpi {
             make_float4(__uint_as_float(r[4 * q]), __uint_as_float(r[4 * q + 1]),
                         __uint_as_float(r[4 * q + 2]), __uint_as_float(r[4 * q + 3]));
     }
+    release();
   }
   static __device__ __forceinline__ void finish(const Params&, State&, int, int, int,
                                                 const Shape&) {}

@@ -171,8 +171,10 @@ struct ScoreEpi {
     }
     st.m = m;
   }
+  template <class Release>
   static __device__ __forceinline__ void tile(const Params& p, State& st, const TileAt& at,
-                                              int lane, uint8_t*, const void*, const Shape& s) {
+                                              int lane, uint8_t*, const void*, const Shape& s,
+                                              Release release) {
     const int row = at.row0 + lane;
     const bool valid = row < p.B;
     if (valid && st.row < 0) {  // the thread's row, the same in every unit
@@ -215,6 +217,7 @@ struct ScoreEpi {
         }
       }
     }
+    release();
   }
   static __device__ __forceinline__ void finish(const Params& p, State& st, int worker, int row,
                                                 int half, const Shape& s) {
@@ -649,41 +652,40 @@ struct GradEpi {
       st.c1 = -e * kLn2;
     }
   }
+  template <class Release>
   static __device__ __forceinline__ void tile(const Params& p, State& st, const TileAt& at,
                                               int lane, uint8_t* box, const void* tmap,
-                                              const Shape& s) {
+                                              const Shape& s, Release release) {
     const int row = at.row0 + lane;
     if (row != st.row) load_row(p, st, row, s.n_kb);
     const AllowWords allow(st.mrow, at.col0, p.V);
+    box_begin(lane);
 #pragma unroll 1
-    for (int c = 0; c < 2; ++c) {
-      if (at.col0 + c * 64 >= p.V) break;
-      box_begin(lane);
-#pragma unroll 1
-      for (int h = 0; h < 2; ++h) {
-        uint32_t r[32];
-        ptx::tmem_ld_32x32b_x32(at.taddr + uint32_t(c * 64 + h * 32), r);
-        ptx::tmem_wait_ld();
-        const uint32_t w = st.live ? allow.at(2 * c + h) : 0u;
-        const uint32_t tok = uint32_t(st.token - (at.col0 + c * 64 + h * 32));
+    for (int c = 0; c < 4; ++c) {
+      uint32_t r[32];
+      ptx::tmem_ld_32x32b_x32(at.taddr + uint32_t(c * 32), r);
+      ptx::tmem_wait_ld();
+      const uint32_t w = st.live ? allow.at(c) : 0u;  // 0 past V
+      const uint32_t tok = uint32_t(st.token - (at.col0 + c * 32));
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          float g[8];
+      for (int q = 0; q < 4; ++q) {
+        float g[8];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int j = q * 8 + i;
-            // Far below 1, p is 0 in fp32; the bound keeps 0 * -inf out of G.
-            const float x =
-                ptx::max_nan(fmaf(__uint_as_float(r[j]), st.scale2, -st.lse2), -16384.0f);
-            float v = ptx::ex2(x) * fmaf(st.c1, x, st.c0);
-            if (tok == uint32_t(j)) v += st.a;
-            g[i] = ((w >> j) & 1u) ? v : 0.0f;
-          }
-          box_put(box, lane, h * 4 + q, g);
+        for (int i = 0; i < 8; ++i) {
+          const int j = q * 8 + i;
+          // Far below 1, p is 0 in fp32; the bound keeps 0 * -inf out of G.
+          const float x =
+              ptx::max_nan(fmaf(__uint_as_float(r[j]), st.scale2, -st.lse2), -16384.0f);
+          float v = ptx::ex2(x) * fmaf(st.c1, x, st.c0);
+          if (tok == uint32_t(j)) v += st.a;
+          g[i] = ((w >> j) & 1u) ? v : 0.0f;
         }
+        box_put(box, lane, c * 4 + q, pack_bf16(g[0], g[1]), pack_bf16(g[2], g[3]),
+                pack_bf16(g[4], g[5]), pack_bf16(g[6], g[7]));
       }
-      box_end(box, tmap, lane, at.col0 + c * 64, at.row0);
     }
+    release();
+    box_end(box, tmap, lane, at.col0, at.row0, p.V);
   }
   static __device__ __forceinline__ void finish(const Params&, State&, int, int, int,
                                                 const Shape&) {}
