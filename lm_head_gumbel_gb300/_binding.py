@@ -401,79 +401,72 @@ def fs_gumbel_noise(b0, nb, v0, nv, *, seed=0, offset=0, seeds=None, out=None, d
 
 # ---- the operators of fs_vocab.h ------------------------------------------
 # These calls take a few microseconds on the GPU at decode sizes, so their host
-# side is kept short: one check per argument, raw pointers instead of ctypes
-# objects.
+# side is kept short: one check per argument, none for results made here, raw
+# addresses instead of ctypes objects.
+_F32, _I64, _BF16 = torch.float32, torch.int64, torch.bfloat16
+_ELEMENT = {_BF16: FS_BF16, _F32: FS_F32}
+
+
 def _refuse(what):
     raise FsError(FS_ERR_INVALID_ARG, what)
 
 
-def _vector(name, t, dtype, n, dev):
-    """Address of a contiguous vector of n elements on `dev`."""
-    if t.dtype is not dtype or t.dim() != 1 or t.shape[0] != n or t.device != dev \
-            or not t.is_contiguous():
-        _refuse(f"{name} must be a contiguous {dtype} vector of {n} on {dev}")
+def _vector(name, t, dtype, n, gpu):
+    """Address of a contiguous vector of n elements on device `gpu`."""
+    if t.dtype is not dtype or t.get_device() != gpu or t.shape != (n,) or not t.is_contiguous():
+        _refuse(f"{name} must be a contiguous {dtype} vector of {n} on cuda:{gpu}")
     return t.data_ptr()
 
 
-def _vector_or_none(name, t, dtype, n, dev):
-    return None if t is None else _vector(name, t, dtype, n, dev)
-
-
-def _matrix(name, t, dtype, n, d, dev):
-    """Address and row stride of an [n, d] matrix on `dev` (of a single row: a
-    stride that every check accepts)."""
-    if t.dtype is not dtype or t.dim() != 2 or t.device != dev:
-        _refuse(f"{name} must be a {dtype} matrix on {dev}")
-    rows, cols = t.shape
+def _matrix(name, t, dtype, n, d, gpu):
+    """Address and row stride of an [n, d] matrix on device `gpu` (of a single
+    row: a stride that every check accepts)."""
+    if t.dtype is not dtype or t.get_device() != gpu or t.shape != (n, d):
+        _refuse(f"{name} must be a {dtype} matrix [{n}, {d}] on cuda:{gpu}")
     ld, unit = t.stride()
-    if rows != n or cols != d or unit != 1:
-        _refuse(f"{name} must be [{n}, {d}] with unit column stride")
+    if unit != 1 and d > 1:
+        _refuse(f"{name} must have unit column stride")
     return t.data_ptr(), ld if n > 1 else max(ld, (d + 7) // 8 * 8)
 
 
-def _mask(vocab_mask, B, V, dev):
-    if vocab_mask is None:
-        return None, 0
+def _head(H, W):
+    """Sizes, device, addresses and row strides of H [B, d] and W [V, d]."""
+    if H.dim() != 2 or W.dim() != 2 or not H.is_cuda:
+        _refuse("H and W must be CUDA bfloat16 matrices")
+    B, d = H.shape
+    V, gpu = W.shape[0], H.get_device()
+    h, ldh = _matrix("H", H, _BF16, B, d, gpu)
+    w, ldw = _matrix("W", W, _BF16, V, d, gpu)
+    return B, d, V, gpu, h, ldh, w, ldw
+
+
+def _mask(vocab_mask, B, V, gpu):
     if vocab_mask.dtype is not torch.int32 or vocab_mask.dim() != 2 \
             or vocab_mask.shape[0] != B or vocab_mask.shape[1] < (V + 31) // 32 \
-            or vocab_mask.stride(1) != 1 or vocab_mask.device != dev:
-        _refuse(f"vocab_mask must be an int32 matrix [B, >= ceil(V/32)] on {dev}")
+            or vocab_mask.stride(1) != 1 or vocab_mask.get_device() != gpu:
+        _refuse(f"vocab_mask must be an int32 matrix [B, >= ceil(V/32)] on cuda:{gpu}")
     return vocab_mask.data_ptr(), max(vocab_mask.stride(0), vocab_mask.shape[1])
 
 
-def _workspace(workspace, size, dev):
-    """Address and bytes of the given workspace, or of a new one.  (A new one
-    may be freed when the call returns: torch reuses it in stream order.)"""
-    if workspace is None:
-        workspace = torch.empty(size, dtype=torch.uint8, device=dev)
-    elif workspace.device != dev or not workspace.is_contiguous():
-        raise FsError(FS_ERR_WORKSPACE, f"workspace must be a contiguous tensor on {dev}")
-    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+def _workspace(workspace, gpu):
+    """Address and bytes of a given workspace."""
+    if workspace.get_device() != gpu or not workspace.is_contiguous():
+        raise FsError(FS_ERR_WORKSPACE, f"workspace must be a contiguous tensor on cuda:{gpu}")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
-def _head(H, W):
-    """H's and W's sizes, addresses and strides."""
-    if not H.is_cuda or H.dim() != 2 or W.dim() != 2:
-        _refuse("H and W must be CUDA bfloat16 matrices")
-    (B, d), dev = H.shape, H.device
-    V = W.shape[0]
-    return (B, d, V, dev) + _matrix("H", H, torch.bfloat16, B, d, dev) \
-        + _matrix("W", W, torch.bfloat16, V, d, dev)
-
-
-def _stream(stream, dev):
+def _call(name, function, gpu, stream, *args):
+    """Call the library on `stream` (default: the device's current one) with
+    device `gpu` current, and check its status."""
     if stream is None:  # without building a Stream object
-        return torch._C._cuda_getCurrentRawStream(dev.index)
-    return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
-
-
-def _run(name, dev, function, *args):
-    """Call the library with `dev` current and its status checked."""
-    if torch.cuda.current_device() == dev.index:
-        st = function(*args)
+        stream = torch._C._cuda_getCurrentRawStream(gpu)
     else:
-        with torch.cuda.device(dev):
-            st = function(*args)
+        stream = stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
+    if torch._C._cuda_getDevice() == gpu:
+        st = function(*args, stream)
+    else:
+        with torch.cuda.device(gpu):
+            st = function(*args, stream)
     if st != FS_OK:
         raise FsError(st, name)
 
@@ -505,48 +498,77 @@ def fs_logprobs(H, W, tokens=None, K=0, *, temperature=None, vocab_mask=None, vo
     fs_sample (rows it samples greedily are scored at T = 1).  out_*: result
     tensors to fill, made when None.  workspace: a uint8 tensor of
     fs_logprobs_workspace_size(B, V, K) bytes, or None.  Returns FsLogprobs."""
-    lib = load_library()
-    B, d, V, dev, h, ldh, w, ldw = _head(H, W)
-    K = int(K)
+    lib = _lib or load_library()
+    B, d, V, gpu, h, ldh, w, ldw = _head(H, W)
     if not 0 <= K <= FS_LOGPROBS_TOPK_MAX:
         _refuse(f"K must be 0 to {FS_LOGPROBS_TOPK_MAX}")
-    f32 = torch.float32
-    mask, mask_ld = _mask(vocab_mask, B, V, dev)
+    dev, empty = H.device, torch.empty
+    temp = mask = tok = logp = idx = top = None
+    mask_ld = 0
+    if temperature is not None:
+        temp = _vector("temperature", temperature, _F32, B, gpu)
+    if vocab_mask is not None:
+        mask, mask_ld = _mask(vocab_mask, B, V, gpu)
     if tokens is None:
         out_logp = None
-    elif out_logp is None:
-        out_logp = torch.empty(B, dtype=f32, device=dev)
+    else:
+        tok = _vector("tokens", tokens, _I64, B, gpu)
+        if out_logp is None:
+            out_logp = empty(B, dtype=_F32, device=dev)
+            logp = out_logp.data_ptr()
+        else:
+            logp = _vector("out_logp", out_logp, _F32, B, gpu)
     if out_entropy is None:
-        out_entropy = torch.empty(B, dtype=f32, device=dev)
+        out_entropy = empty(B, dtype=_F32, device=dev)
+        entropy = out_entropy.data_ptr()
+    else:
+        entropy = _vector("out_entropy", out_entropy, _F32, B, gpu)
     if out_lse is None:
-        out_lse = torch.empty(B, dtype=f32, device=dev)
-    idx = top = None
+        out_lse = empty(B, dtype=_F32, device=dev)
+        lse = out_lse.data_ptr()
+    else:
+        lse = _vector("out_lse", out_lse, _F32, B, gpu)
     if K == 0:
         out_topk_idx = out_topk_logp = None
     else:
         if out_topk_idx is None:
-            out_topk_idx = torch.empty((B, K), dtype=torch.int64, device=dev)
+            out_topk_idx = empty((B, K), dtype=_I64, device=dev)
+            idx = out_topk_idx.data_ptr()
+        else:
+            idx = _matrix("out_topk_idx", out_topk_idx, _I64, B, K, gpu)[0]
         if out_topk_logp is None:
-            out_topk_logp = torch.empty((B, K), dtype=f32, device=dev)
+            out_topk_logp = empty((B, K), dtype=_F32, device=dev)
+            top = out_topk_logp.data_ptr()
+        else:
+            top = _matrix("out_topk_logp", out_topk_logp, _F32, B, K, gpu)[0]
         if not (out_topk_idx.is_contiguous() and out_topk_logp.is_contiguous()):
             _refuse("out_topk_idx and out_topk_logp must be contiguous")
-        idx = _matrix("out_topk_idx", out_topk_idx, torch.int64, B, K, dev)[0]
-        top = _matrix("out_topk_logp", out_topk_logp, f32, B, K, dev)[0]
-    workspace, ws, ws_bytes = _workspace(workspace, fs_logprobs_workspace_size(B, V, K), dev)
-    args = FsLogprobsArgs(
-        h, w, _vector_or_none("temperature", temperature, f32, B, dev), mask, mask_ld,
-        _vector_or_none("tokens", tokens, torch.int64, B, dev), B, d, V, ldh, ldw,
-        int(vocab_offset), K, _vector_or_none("out_logp", out_logp, f32, B, dev),
-        _vector("out_entropy", out_entropy, f32, B, dev),
-        _vector("out_lse", out_lse, f32, B, dev), idx, top, ws, ws_bytes,
-        FS_FLAG_OVERLAP_PREVIOUS if overlap_previous else 0)
-    _run("fs_logprobs", dev, lib.fs_logprobs, args, _stream(stream, dev))
+    if workspace is None:
+        ws_bytes = fs_logprobs_workspace_size(B, V, K)
+        workspace = empty(ws_bytes, dtype=torch.uint8, device=dev)
+        ws = workspace.data_ptr()
+    else:
+        ws, ws_bytes = _workspace(workspace, gpu)
+    args = FsLogprobsArgs(h, w, temp, mask, mask_ld, tok, B, d, V, ldh, ldw, int(vocab_offset), K,
+                          logp, entropy, lse, idx, top, ws, ws_bytes,
+                          FS_FLAG_OVERLAP_PREVIOUS if overlap_previous else 0)
+    _call("fs_logprobs", lib.fs_logprobs, gpu, stream, args)
     return FsLogprobs(out_logp, out_entropy, out_lse, out_topk_idx, out_topk_logp)
 
 
 @functools.lru_cache(maxsize=256)
 def fs_logprobs_grad_workspace_size(B: int, d: int, V: int) -> int:
     return int(load_library().fs_logprobs_grad_workspace_size(int(B), int(d), int(V)))
+
+
+def _gradient(name, out, n, d, gpu, dev):
+    """A bf16 [n, d] result (made here with rows on 16-byte boundaries when
+    None), its address and row stride."""
+    if out is None:
+        ld = (d + 7) // 8 * 8
+        out = torch.empty((n, ld), dtype=_BF16, device=dev)
+        return (out if ld == d else out[:, :d]), out.data_ptr(), ld
+    return (out,) + _matrix(name, out, _BF16, n, d, gpu)
 
 
 def fs_logprobs_grad(H, W, tokens, lse, grad_logp, *, entropy=None, grad_entropy=None,
@@ -559,68 +581,64 @@ def fs_logprobs_grad(H, W, tokens, lse, grad_logp, *, entropy=None, grad_entropy
     grad_entropy: fp32 [B].  Returns (dH, dW) in bf16 ([B, d], [V, d]; out_dH /
     out_dW when given), None where need_dH / need_dW is false.  workspace: a
     uint8 tensor of fs_logprobs_grad_workspace_size(B, d, V) bytes, or None."""
-    lib = load_library()
-    B, d, V, dev, h, ldh, w, ldw = _head(H, W)
-    f32, bf16 = torch.float32, torch.bfloat16
+    lib = _lib or load_library()
+    B, d, V, gpu, h, ldh, w, ldw = _head(H, W)
     if not (need_dH or need_dW):
         _refuse("neither dH nor dW is asked for")
     if tokens is None or lse is None or grad_logp is None:
         _refuse("tokens, lse and grad_logp are required")
-    if grad_entropy is None:
-        entropy = None
-    mask, mask_ld = _mask(vocab_mask, B, V, dev)
-    ld = (d + 7) // 8 * 8  # results made here: rows on 16-byte boundaries
-    dh = dw = None
-    lddh = lddw = 0
-    if not need_dH:
+    if grad_entropy is not None and entropy is None:
+        _refuse("grad_entropy needs entropy")
+    dev = H.device
+    temp = mask = ent = g_ent = dh = dw = None
+    mask_ld = lddh = lddw = 0
+    if temperature is not None:
+        temp = _vector("temperature", temperature, _F32, B, gpu)
+    if vocab_mask is not None:
+        mask, mask_ld = _mask(vocab_mask, B, V, gpu)
+    if grad_entropy is not None:
+        ent = _vector("entropy", entropy, _F32, B, gpu)
+        g_ent = _vector("grad_entropy", grad_entropy, _F32, B, gpu)
+    if need_dH:
+        out_dH, dh, lddh = _gradient("out_dH", out_dH, B, d, gpu, dev)
+    else:
         out_dH = None
+    if need_dW:
+        out_dW, dw, lddw = _gradient("out_dW", out_dW, V, d, gpu, dev)
     else:
-        if out_dH is None:
-            out_dH = torch.empty((B, ld), dtype=bf16, device=dev)[:, :d]
-        dh, lddh = _matrix("out_dH", out_dH, bf16, B, d, dev)
-    if not need_dW:
         out_dW = None
+    if workspace is None:
+        ws_bytes = fs_logprobs_grad_workspace_size(B, d, V)
+        workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
+        ws = workspace.data_ptr()
     else:
-        if out_dW is None:
-            out_dW = torch.empty((V, ld), dtype=bf16, device=dev)[:, :d]
-        dw, lddw = _matrix("out_dW", out_dW, bf16, V, d, dev)
-    workspace, ws, ws_bytes = _workspace(workspace, fs_logprobs_grad_workspace_size(B, d, V), dev)
+        ws, ws_bytes = _workspace(workspace, gpu)
     args = FsLogprobsGradArgs(
-        h, w, _vector_or_none("temperature", temperature, f32, B, dev), mask, mask_ld,
-        _vector("tokens", tokens, torch.int64, B, dev), _vector("lse", lse, f32, B, dev),
-        _vector_or_none("entropy", entropy, f32, B, dev),
-        _vector("grad_logp", grad_logp, f32, B, dev),
-        _vector_or_none("grad_entropy", grad_entropy, f32, B, dev), B, d, V, ldh, ldw,
-        int(vocab_offset), dh, dw, lddh, lddw, ws, ws_bytes)
-    _run("fs_logprobs_grad", dev, lib.fs_logprobs_grad, args, _stream(stream, dev))
+        h, w, temp, mask, mask_ld, _vector("tokens", tokens, _I64, B, gpu),
+        _vector("lse", lse, _F32, B, gpu), ent, _vector("grad_logp", grad_logp, _F32, B, gpu),
+        g_ent, B, d, V, ldh, ldw, int(vocab_offset), dh, dw, lddh, lddw, ws, ws_bytes)
+    _call("fs_logprobs_grad", lib.fs_logprobs_grad, gpu, stream, args)
     return out_dH, out_dW
-
-
-_ELEMENT = {torch.bfloat16: FS_BF16, torch.float32: FS_F32}
-
-
-def _table(name, t):
-    """Element code of a bf16 or fp32 CUDA matrix."""
-    code = _ELEMENT.get(t.dtype)
-    if code is None or t.dim() != 2 or not t.is_cuda:
-        _refuse(f"{name} must be a CUDA bfloat16 or float32 matrix")
-    return code
 
 
 def fs_embed(ids, E, *, scale=1.0, vocab_offset=0, out=None, stream=None):
     """Embedding lookup: scale * E[ids - vocab_offset], 0 where the id is not
     one of E's rows (padding, another shard).  ids: int64 [N]; E: bf16 or fp32
     [V, d].  Returns out ([N, d] of E's type)."""
-    lib = load_library()
-    code, dev, dtype = _table("E", E), E.device, E.dtype
-    V, d = E.shape
-    N = ids.shape[0]
+    lib = _lib or load_library()
+    dtype = E.dtype
+    code = _ELEMENT.get(dtype)
+    if code is None or E.dim() != 2 or not E.is_cuda:
+        _refuse("E must be a CUDA bfloat16 or float32 matrix")
+    (V, d), (N, *_), gpu = E.shape, ids.shape, E.get_device()
+    e, lde = _matrix("E", E, dtype, V, d, gpu)
     if out is None:
-        out = torch.empty((N, d), dtype=dtype, device=dev)
-    e, lde = _matrix("E", E, dtype, V, d, dev)
-    o, ldo = _matrix("out", out, dtype, N, d, dev)
-    _run("fs_embed", dev, lib.fs_embed, _vector("ids", ids, torch.int64, N, dev), N, e, V, d, lde,
-         code, scale, vocab_offset, o, ldo, _stream(stream, dev))
+        out = torch.empty((N, d), dtype=dtype, device=E.device)
+        o, ldo = out.data_ptr(), d
+    else:
+        o, ldo = _matrix("out", out, dtype, N, d, gpu)
+    _call("fs_embed", lib.fs_embed, gpu, stream, _vector("ids", ids, _I64, N, gpu), N, e, V, d,
+          lde, code, scale, vocab_offset, o, ldo)
     return out
 
 
@@ -638,20 +656,27 @@ def fs_embed_grad(ids, dY, V, *, scale=1.0, vocab_offset=0, out=None, out_dtype=
     a result made here (dY's when None).  The same inputs always give the same
     bits.  workspace: a uint8 tensor of fs_embed_grad_workspace_size(N, d)
     bytes, or None."""
-    lib = load_library()
-    y_code, dev = _table("dY", dY), dY.device
-    N, d = dY.shape
-    V = int(V)
+    lib = _lib or load_library()
+    y_code = _ELEMENT.get(dY.dtype)
+    if y_code is None or dY.dim() != 2 or not dY.is_cuda:
+        _refuse("dY must be a CUDA bfloat16 or float32 matrix")
+    (N, d), gpu, V = dY.shape, dY.get_device(), int(V)
+    y, ldy = _matrix("dY", dY, dY.dtype, N, d, gpu)
     if out is None:
         if accumulate:
             _refuse("accumulate needs out")
-        out = torch.empty((V, d), dtype=out_dtype or dY.dtype, device=dev)
-    e_code = _table("out", out)
-    y, ldy = _matrix("dY", dY, dY.dtype, N, d, dev)
-    e, lde = _matrix("out", out, out.dtype, V, d, dev)
-    ids_at = _vector("ids", ids, torch.int64, N, dev)
-    workspace, ws, ws_bytes = _workspace(workspace, fs_embed_grad_workspace_size(N, d), dev)
-    _run("fs_embed_grad", dev, lib.fs_embed_grad, ids_at, N, y, V, d, ldy, y_code, scale,
-         vocab_offset, e, lde, e_code, 1 if accumulate else 0, ws, ws_bytes,
-         _stream(stream, dev))
+        out = torch.empty((V, d), dtype=out_dtype or dY.dtype, device=dY.device)
+    e_code = _ELEMENT.get(out.dtype)
+    if e_code is None:
+        _refuse("out must be bfloat16 or float32")
+    e, lde = _matrix("out", out, out.dtype, V, d, gpu)
+    if workspace is None:
+        ws_bytes = fs_embed_grad_workspace_size(N, d)
+        workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=dY.device)
+        ws = workspace.data_ptr()
+    else:
+        ws, ws_bytes = _workspace(workspace, gpu)
+    _call("fs_embed_grad", lib.fs_embed_grad, gpu, stream, _vector("ids", ids, _I64, N, gpu), N,
+          y, V, d, ldy, y_code, scale, vocab_offset, e, lde, e_code, 1 if accumulate else 0, ws,
+          ws_bytes)
     return out
