@@ -98,16 +98,17 @@ __device__ __forceinline__ float ex2(float a) {
 namespace vocab {
 
 constexpr int kBM = 128;  // M rows per CTA = tensor-memory lanes
-constexpr int kBN = 256;  // N columns per unit = accumulator columns
+constexpr int kBN = 256;  // N columns per unit = accumulator columns (fewer: Epi::kN)
 constexpr int kBK = 64;   // k slice: 64 bf16 = one 128-byte swizzle row
 constexpr int kUK = 16;   // k of one MMA
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = 32 * (2 + kEpiWarps);
 constexpr int kMaxStages = 8;
 constexpr uint32_t kChunkBytes = 64 * kBK * 2;  // one 64 x 64 box, 8 KB
-constexpr uint32_t kTmemCols = 2 * kBN;
 constexpr uint32_t kBoxBytes = 2 * 4096;  // an epilogue warp's two 32 x 64 bf16 boxes
 constexpr uint32_t kStagingBytes = kEpiWarps * kBoxBytes;
+constexpr uint32_t kBarrierBytes = 256;
+static_assert((2 * kMaxStages + 5) * 8 + 8 <= kBarrierBytes, "barriers, tensor-memory address, flag");
 constexpr int kErrWaitTimeout = 1;  // the library's device error word, bit 0
 
 template <class Epi>
@@ -116,20 +117,29 @@ __host__ __device__ constexpr uint32_t ring_bytes() {
 }
 template <class Epi>
 __host__ __device__ constexpr size_t smem_bytes() {
-  return 1024 /* alignment slack */ + ring_bytes<Epi>() + (Epi::kStaged ? kStagingBytes : 0) + 256;
+  return 1024 /* alignment slack */ + ring_bytes<Epi>() + (Epi::kStaged ? kStagingBytes : 0) +
+         kBarrierBytes;
+}
+
+// k slices per ring stage: narrow units have small slices, and a slice of its
+// own stage costs the producer about 450 cycles (8 rows at d = 2048, V = 4096:
+// 32 slices, 7.6 of 14 us) -- as long as 64 columns of W take to stream.
+template <class Epi>
+__host__ __device__ constexpr int slices() {
+  return kBN / Epi::kN;
 }
 
 enum : uint32_t { kPolicyNormal = 0, kPolicyFirst = 1, kPolicyLast = 2 };
 
 struct Shape {
-  int32_t n_mt, n_nt;      // tiles along M (128 rows, 256 for CTA pairs) and N (256)
+  int32_t n_mt, n_nt;      // tiles along M (128 rows, 256 for CTA pairs) and N (Epi::kN)
   int32_t n_units;         // n_mt * n_nt * number of k splits
   int32_t n_kb;            // 64-wide k slices in all
   int32_t kb_per_split;    // k slices of one unit (the last split may have fewer)
   int32_t m_rows, n_cols;  // extents of M and N
   uint32_t m_fastest;      // unit order: M tiles (else N tiles) innermost, k splits outermost
   uint32_t a_box_rows;     // rows of A's box when k is contiguous (a multiple of 8)
-  uint32_t a_bytes, stage_bytes, n_stages;
+  uint32_t a_bytes, stage_bytes, n_stages;  // A's part of a slice; a stage holds slices<Epi>()
   uint32_t policy_a, policy_b;  // L2 eviction hints
   // The launch overlaps the kernel before it on the stream, which writes A and
   // the epilogue's inputs: B streams at once, the rest waits for that kernel.
@@ -229,20 +239,21 @@ __device__ __forceinline__ uint64_t policy_of(uint32_t code) {
                                : ptx::policy_evict_normal();
 }
 
-// What an epilogue call knows about its 32 rows x 128 columns.
+// What an epilogue call knows about its 32 rows x kN / 2 columns.
 struct TileAt {
   Unit unit;
   int row0;         // first M row of the warp's 32 lanes
-  int col0;         // first N column of the warp's 128 columns
+  int col0;         // first N column of the warp's columns
   int rank;         // CTA of the pair
-  int quad, half;   // rows quad*32.. and columns half*128.. of the CTA's tile
+  int quad, half;   // rows quad*32.. and which half of the CTA's tile's columns
   uint32_t taddr;   // tensor-memory address of (row0, col0)
 };
 
 // kAmn / kBmn: A's M (B's N) dimension is the contiguous one in memory.
 // finish() gets the thread's M row in its worker's first unit.
-// Epi: struct with Params, State, kStaged (uses bf16 boxes in shared memory and
-// tmap_d), and static device functions start / tile / finish.
+// Epi: struct with Params, State, kN (columns of a unit: 256, or 64 / 128 where
+// 256 would leave CTAs without units), kStaged (uses bf16 boxes in shared memory
+// and tmap_d), and static device functions start / tile / finish.
 template <class Epi, bool kPair, bool kAmn, bool kBmn>
 __global__ void __launch_bounds__(kThreads, 1)
     contract_kernel(const __grid_constant__ CUtensorMap tmap_a,
@@ -250,9 +261,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const __grid_constant__ CUtensorMap tmap_d, const Shape s,
                     const __grid_constant__ typename Epi::Params ep) {
   constexpr int kCtas = kPair ? 2 : 1;
-  constexpr int kBRows = kBN / kCtas;  // B rows in this CTA's shared memory
+  constexpr int kN = Epi::kN;
+  constexpr uint32_t kTmemCols = 2 * kN;
+  static_assert(kN == 256 || (!kPair && !kBmn && (kN == 64 || kN == 128)), "unit columns");
+  constexpr int kBRows = kN / kCtas;  // B rows in this CTA's shared memory
   constexpr uint32_t kBBytes = kBRows * kBK * 2;
-  constexpr uint32_t kIdesc = ptx::idesc_bf16_f32(kBM * kCtas, kBN) | (kAmn ? 1u << 15 : 0u) |
+  constexpr int kS = slices<Epi>();
+  constexpr uint32_t kIdesc = ptx::idesc_bf16_f32(kBM * kCtas, kN) | (kAmn ? 1u << 15 : 0u) |
                               (kBmn ? 1u << 16 : 0u);
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
@@ -322,8 +337,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     // Rows (k contiguous) or 64-wide chunks (M or N contiguous) past the end
     // are read from the last valid ones instead: they only feed accumulator
     // rows or columns that no epilogue reads.
-    auto load_a = [&](uint32_t stage, int kb, int mt) {
-      uint8_t* dst = smem + size_t(stage) * s.stage_bytes;
+    auto load_a = [&](uint32_t stage, int i, int kb, int mt) {
+      uint8_t* dst = smem + size_t(stage) * s.stage_bytes + i * (s.a_bytes + kBBytes);
       const int m0 = (mt * kCtas + rank) * kBM;
       if constexpr (kAmn) {
 #pragma unroll
@@ -334,9 +349,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         load(dst, &tmap_a, stage, kb * kBK, min(m0, s.m_rows - 1), pol_a);
       }
     };
-    auto load_b = [&](uint32_t stage, int kb, int nt) {
-      uint8_t* dst = smem + size_t(stage) * s.stage_bytes + s.a_bytes;
-      const int n0 = nt * kBN + rank * kBRows;
+    auto load_b = [&](uint32_t stage, int i, int kb, int nt) {
+      uint8_t* dst = smem + size_t(stage) * s.stage_bytes + i * (s.a_bytes + kBBytes) + s.a_bytes;
+      const int n0 = nt * kN + rank * kBRows;
       if constexpr (kBmn) {
 #pragma unroll
         for (int i = 0; i < kBRows / 64; ++i)
@@ -350,28 +365,36 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     // The first ring fill's A copies, held back until the kernel before is done.
     bool deferring = s.pdl != 0;
-    int n_held = 0, held_kb[kMaxStages], held_mt[kMaxStages];
+    int n_held = 0, held_kb[kMaxStages], held_n[kMaxStages], held_mt[kMaxStages];
     auto release = [&]() {
       ptx::grid_dependency_wait();
       if (issuer)
-        for (int i = 0; i < n_held; ++i) load_a(uint32_t(i), held_kb[i], held_mt[i]);
+        for (int h = 0; h < n_held; ++h)
+          for (int i = 0; i < held_n[h]; ++i) load_a(uint32_t(h), i, held_kb[h] + i, held_mt[h]);
       deferring = false;
     };
     for (Units it(s, worker, n_workers); ok && it.more(s); it.next(s)) {
       const Unit t = it.get(s);
-      for (int kb = t.kb0; kb < t.kb0 + t.n_kb; ++kb) {
+      for (int k = 0; k < t.n_kb; k += kS) {
         if (!waiter.wait_warp(&empty_bar[stage], phase ^ 1u)) {
           ok = false;
           break;
         }
+        const int n = min(kS, t.n_kb - k);
         if (issuer) {
           if (leader)
-            ptx::mbar_arrive_expect_tx(&full_bar[stage], kCtas * (s.a_bytes + kBBytes));
-          load_b(stage, kb, t.nt);
-          if (!deferring) load_a(stage, kb, t.mt);
+            ptx::mbar_arrive_expect_tx(&full_bar[stage],
+                                       uint32_t(n) * kCtas * (s.a_bytes + kBBytes));
+#pragma unroll
+          for (int i = 0; i < kS; ++i) {
+            if (i >= n) break;
+            load_b(stage, i, t.kb0 + k + i, t.nt);
+            if (!deferring) load_a(stage, i, t.kb0 + k + i, t.mt);
+          }
         }
         if (deferring) {  // the first fill: stage n_held
-          held_kb[n_held] = kb;
+          held_kb[n_held] = t.kb0 + k;
+          held_n[n_held] = n;
           held_mt[n_held++] = t.mt;
         }
         ++issued;
@@ -417,23 +440,28 @@ __global__ void __launch_bounds__(kThreads, 1)
         const Unit t = it.get(s);
         if (!waiter.wait_warp(&tempty_bar[acc], acc_phase ^ 1u)) break;
         ptx::tc_fence_after();
-        const uint32_t d_tmem = tmem_base + acc * kBN;
-        for (int kb = 0; kb < t.n_kb; ++kb) {
+        const uint32_t d_tmem = tmem_base + acc * kN;
+        for (int kb = 0; kb < t.n_kb; kb += kS) {
           if (!waiter.wait_warp(&full_bar[stage], phase)) {
             ok = false;
             break;
           }
           ptx::tc_fence_after();
-          const uint64_t off = uint64_t(stage * (s.stage_bytes >> 4));
           if (issuer) {
 #pragma unroll
-            for (int k = 0; k < kBK / kUK; ++k) {
-              const uint64_t da = desc_a0 + off + kStepA * k, db = desc_b0 + off + kStepB * k;
-              const uint32_t more = (kb | k) != 0 ? 1u : 0u;
-              if constexpr (kPair)
-                ptx::mma_bf16_pair(d_tmem, da, db, kIdesc, more);
-              else
-                ptx::mma_bf16(d_tmem, da, db, kIdesc, more);
+            for (int i = 0; i < kS; ++i) {
+              if (i >= t.n_kb - kb) break;
+              const uint64_t off =
+                  uint64_t((stage * s.stage_bytes + i * (s.a_bytes + kBBytes)) >> 4);
+#pragma unroll
+              for (int k = 0; k < kBK / kUK; ++k) {
+                const uint64_t da = desc_a0 + off + kStepA * k, db = desc_b0 + off + kStepB * k;
+                const uint32_t more = (kb | i | k) != 0 ? 1u : 0u;
+                if constexpr (kPair)
+                  ptx::mma_bf16_pair(d_tmem, da, db, kIdesc, more);
+                else
+                  ptx::mma_bf16(d_tmem, da, db, kIdesc, more);
+              }
             }
             commit(&empty_bar[stage]);
           }
@@ -479,8 +507,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       at.quad = quad;
       at.half = half;
       at.row0 = (at.unit.mt * kCtas + rank) * kBM + quad * 32;
-      at.col0 = at.unit.nt * kBN + half * 128;
-      at.taddr = tmem_base + (uint32_t(quad * 32) << 16) + acc * kBN + uint32_t(half * 128);
+      at.col0 = at.unit.nt * kN + half * (kN / 2);
+      at.taddr = tmem_base + (uint32_t(quad * 32) << 16) + acc * kN + uint32_t(half * (kN / 2));
       int ok = 0;
       if (lane == 0) ok = waiter.wait(&tfull_bar[acc], acc_phase) ? 1 : 0;
       ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
@@ -567,6 +595,7 @@ __device__ __forceinline__ void box_end(uint8_t* box, const void* tmap, int lane
 // store -- depend on one another, so they are taken once per 128 columns, and
 // the accumulator is given back before the boxes are written.
 struct StoreEpi {
+  static constexpr int kN = kBN;
   static constexpr bool kStaged = true;
   struct Params {
     __nv_bfloat16* out;
@@ -617,6 +646,7 @@ struct StoreEpi {
 // (128 x 256) is stored as [64 column quads][128 rows] float4, so a warp's
 // 16-byte stores are contiguous.
 struct PartialEpi {
+  static constexpr int kN = kBN;
   static constexpr bool kStaged = false;
   struct Params {
     float4* partial;

@@ -110,24 +110,78 @@ __device__ __forceinline__ float pick32(const uint32_t (&v)[32], uint32_t j) {
   return __uint_as_float((j & 1u) ? a[1] : a[0]);
 }
 
-template <int KC>
+// A logit as a sort key: an order-preserving unsigned integer whose low 7 bits
+// hold 127 - j, so that of equal values the one at the lower column j < 128 is
+// the greater.  The value's own low 7 bits go (it is rounded down to 17 bits):
+// lists only choose candidates, four more than asked for, whose logits are
+// summed again.  0: no candidate (-inf, NaN).
+__device__ __forceinline__ uint32_t sort_key(uint32_t bits, int j) {
+  const float f = __uint_as_float(bits) + 0.0f;  // -0 counts as +0
+  const uint32_t b = __float_as_uint(f);
+  const uint32_t u = b ^ (uint32_t(int32_t(b) >> 31) | 0x80000000u);
+  return f > -INFINITY ? (u & ~127u) | uint32_t(127 - j) : 0u;
+}
+__device__ __forceinline__ float key_value(uint32_t key) {
+  const uint32_t u = key & ~127u;
+  return __uint_as_float((u & 0x80000000u) ? u ^ 0x80000000u : ~u);
+}
+
+// Bitonic networks on 32 keys in registers, largest first.
+__device__ __forceinline__ void order_pair(uint32_t& a, uint32_t& b) {
+  const uint32_t hi = max(a, b), lo = min(a, b);
+  a = hi;
+  b = lo;
+}
+__device__ __forceinline__ void sort32(uint32_t (&k)[32]) {
+#pragma unroll
+  for (int size = 2; size <= 32; size *= 2) {
+#pragma unroll
+    for (int step = size / 2; step > 0; step /= 2) {
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        if ((i & step) != 0) continue;
+        if ((i & size) == 0)
+          order_pair(k[i], k[i + step]);
+        else
+          order_pair(k[i + step], k[i]);
+      }
+    }
+  }
+}
+// The 32 largest of two sorted lists, sorted, into a.
+__device__ __forceinline__ void merge32(uint32_t (&a)[32], const uint32_t (&b)[32]) {
+#pragma unroll
+  for (int i = 0; i < 32; ++i) a[i] = max(a[i], b[31 - i]);
+#pragma unroll
+  for (int step = 16; step > 0; step /= 2) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+      if ((i & step) == 0) order_pair(a[i], a[i + step]);
+  }
+}
+
+struct ScoreParams {
+  int32_t B, V;  // rows of this launch, ids
+  const float* temperature;
+  const uint32_t* mask;
+  int64_t mask_ld;
+  RowPart* part;     // [B][n_slots]
+  float* cand_val;   // [B][n_slots][KC] raw logits, best first
+  int32_t* cand_id;  // ids from 0, -1 past the end
+  int32_t n_slots;
+};
+
+template <int KC, int kCols>
 struct ScoreEpi {
+  static constexpr int kN = kCols;
   static constexpr bool kStaged = false;
-  struct Params {
-    int32_t B, V;  // rows of this launch, ids
-    const float* temperature;
-    const uint32_t* mask;
-    int64_t mask_ld;
-    RowPart* part;     // [B][n_slots]
-    float* cand_val;   // [B][n_slots][KC] raw logits, best first
-    int32_t* cand_id;  // ids from 0, -1 past the end
-    int32_t n_slots;
-  };
+  using Params = ScoreParams;
   struct State {
     float m = -INFINITY, S = 0.0f, U = 0.0f;  // m: the largest raw logit
     float scale2 = 0.0f;                      // log2(e) / T
     const uint32_t* mrow = nullptr;
     int row = -1;
+    bool first = true;  // no unit seen yet
     float ts[KC > 0 ? KC : 1];
     int32_t ti[KC > 0 ? KC : 1];
   };
@@ -183,20 +237,49 @@ struct ScoreEpi {
       if (p.mask) st.mrow = p.mask + int64_t(row) * p.mask_ld;
     }
     const AllowWords allow(st.mrow, at.col0, p.V);
-#pragma unroll 1
-    for (int c = 0; c < 4; ++c) {
-      if (at.col0 + c * 32 >= p.V) break;
-      uint32_t r[32];
+    auto load = [&](int c, uint32_t (&r)[32]) {
       ptx::tmem_ld_32x32b_x32(at.taddr + uint32_t(c * 32), r);
       ptx::tmem_wait_ld();
       const uint32_t w = allow.at(c);
       const bool full = __all_sync(0xFFFFFFFFu, !valid || w == 0xFFFFFFFFu);
-      if (valid) {
-        if (full)
-          chunk<false>(st, r, w);
-        else
-          chunk<true>(st, r, w);
+      if (!valid) return;
+      if (full)
+        chunk<false>(st, r, w);
+      else
+        chunk<true>(st, r, w);
+    };
+    if (KC > 0 && st.first) {
+      // The first unit fills the list: its logits are sorted, 32 at a time, and
+      // merged (inserting them one by one took 28 us a call at KC = 24 where a
+      // CTA has one unit, this 4).
+      uint32_t best[32];
+#pragma unroll
+      for (int i = 0; i < 32; ++i) best[i] = 0u;
+#pragma unroll 1
+      for (int c = 0; c < kN / 64; ++c) {
+        if (at.col0 + c * 32 >= p.V) break;
+        uint32_t r[32];
+        load(c, r);
+#pragma unroll
+        for (int j = 0; j < 32; ++j) r[j] = sort_key(r[j], c * 32 + j);
+        sort32(r);
+        merge32(best, r);
       }
+      st.first = false;
+#pragma unroll
+      for (int q = 0; q < KC; ++q) {
+        const uint32_t key = best[q];
+        st.ts[q] = key != 0u ? key_value(key) : -INFINITY;
+        st.ti[q] = key != 0u ? at.col0 + 127 - int(key & 127u) : -1;
+      }
+      release();
+      return;
+    }
+#pragma unroll 1
+    for (int c = 0; c < kN / 64; ++c) {
+      if (at.col0 + c * 32 >= p.V) break;
+      uint32_t r[32];
+      load(c, r);
       if constexpr (KC > 0) {
         // Every lane marks the logits that beat its list's last entry; the
         // warp then inserts one per lane and round, lowest id first.  (An
@@ -211,7 +294,7 @@ struct ScoreEpi {
           if (want != 0u) {
             const uint32_t j = uint32_t(__ffs(want) - 1);
             want &= want - 1u;
-            const float v = pick32(r, j);
+            const float v = key_value(sort_key(__float_as_uint(pick32(r, j)), 0));
             if (v > st.ts[KC - 1]) list_insert<KC>(st.ts, st.ti, v, at.col0 + c * 32 + int(j));
           }
         }
@@ -222,7 +305,7 @@ struct ScoreEpi {
   static __device__ __forceinline__ void finish(const Params& p, State& st, int worker, int row,
                                                 int half, const Shape& s) {
     // A slot per (group of workers on the same vocabulary blocks, half); every
-    // one is written, also by a thread whose 128 columns lay past V.
+    // one is written, also by a thread whose columns lay past V.
     if (row >= p.B) return;
     const int64_t slot = int64_t(row) * p.n_slots + (worker / s.n_mt) * 2 + half;
     const float m2 = st.m == -INFINITY ? st.m : st.m * st.scale2;
@@ -597,17 +680,21 @@ __global__ void __launch_bounds__(Block::kThreads, Block::kBlocks)
 // Backward: G = dLoss / dlogits
 // ---------------------------------------------------------------------------
 
+struct GradParams {
+  int32_t B, V;
+  const float* temperature;
+  const uint32_t* mask;
+  int64_t mask_ld;
+  const int64_t* tokens;
+  const float *lse, *entropy, *grad_logp, *grad_entropy;
+  int64_t vocab_offset;
+};
+
+template <int kCols>
 struct GradEpi {
+  static constexpr int kN = kCols;
   static constexpr bool kStaged = true;
-  struct Params {
-    int32_t B, V;
-    const float* temperature;
-    const uint32_t* mask;
-    int64_t mask_ld;
-    const int64_t* tokens;
-    const float *lse, *entropy, *grad_logp, *grad_entropy;
-    int64_t vocab_offset;
-  };
+  using Params = GradParams;
   // With a, e the row's upstream gradients over T, P = 2^x the probability and
   // x = log2 p = l scale2 - lse2:  G = P (c0 + c1 x), + a at the token, where
   // c1 = -e ln2, c0 = -a - e entropy.
@@ -661,7 +748,7 @@ struct GradEpi {
     const AllowWords allow(st.mrow, at.col0, p.V);
     box_begin(lane);
 #pragma unroll 1
-    for (int c = 0; c < 4; ++c) {
+    for (int c = 0; c < kN / 64; ++c) {
       uint32_t r[32];
       ptx::tmem_ld_32x32b_x32(at.taddr + uint32_t(c * 32), r);
       ptx::tmem_wait_ld();
@@ -685,7 +772,7 @@ struct GradEpi {
       }
     }
     release();
-    box_end(box, tmap, lane, at.col0, at.row0, p.V);
+    box_end(box, tmap, lane, at.col0, at.row0, min(p.V, at.col0 + kN / 2));
   }
   static __device__ __forceinline__ void finish(const Params&, State&, int, int, int,
                                                 const Shape&) {}
@@ -780,8 +867,10 @@ bool prepare_kernel(int sms, int* pairs) {
 
 template <int KC>
 bool prepare_scores(int sms, int* pairs) {
-  return prepare_kernel<ScoreEpi<KC>, false, false, false>(sms, pairs) &&
-         prepare_kernel<ScoreEpi<KC>, true, false, false>(sms, pairs);
+  return prepare_kernel<ScoreEpi<KC, 64>, false, false, false>(sms, pairs) &&
+         prepare_kernel<ScoreEpi<KC, 128>, false, false, false>(sms, pairs) &&
+         prepare_kernel<ScoreEpi<KC, 256>, false, false, false>(sms, pairs) &&
+         prepare_kernel<ScoreEpi<KC, 256>, true, false, false>(sms, pairs);
 }
 
 template <int KC>
@@ -834,9 +923,11 @@ fs_status device_setup(const Device** out) {
       d.error_word = device_error_word();
       const bool ok =
           d.error_word != nullptr && prepare_scores<0>(d.sms, &d.pairs) &&
-          prepare_scores<8>(d.sms, &d.pairs) && prepare_scores<24>(d.sms, &d.pairs) &&
-          prepare_kernel<GradEpi, false, false, false>(d.sms, &d.pairs) &&
-          prepare_kernel<GradEpi, true, false, false>(d.sms, &d.pairs) &&
+          prepare_scores<8>(d.sms, &d.pairs) && prepare_scores<16>(d.sms, &d.pairs) &&
+          prepare_scores<24>(d.sms, &d.pairs) &&
+          prepare_kernel<GradEpi<128>, false, false, false>(d.sms, &d.pairs) &&
+          prepare_kernel<GradEpi<256>, false, false, false>(d.sms, &d.pairs) &&
+          prepare_kernel<GradEpi<256>, true, false, false>(d.sms, &d.pairs) &&
           prepare_kernel<StoreEpi, false, false, true>(d.sms, &d.pairs) &&
           prepare_kernel<StoreEpi, true, false, true>(d.sms, &d.pairs) &&
           prepare_kernel<PartialEpi, false, false, true>(d.sms, &d.pairs) &&
@@ -874,9 +965,9 @@ template <class Epi, bool kPair, bool kAmn, bool kBmn>
 fs_status launch(const Device& dev, const CUtensorMap& a, const CUtensorMap& b,
                  const CUtensorMap& d, Shape s, const typename Epi::Params& ep, int workers,
                  bool overlap, cudaStream_t stream) {
-  constexpr uint32_t kBBytes = (kPair ? kBN / 2 : kBN) * kBK * 2;
+  constexpr uint32_t kBBytes = (kPair ? Epi::kN / 2 : Epi::kN) * kBK * 2;
   s.a_bytes = kAmn ? kBM * kBK * 2 : s.a_box_rows * 128u;
-  s.stage_bytes = s.a_bytes + kBBytes;
+  s.stage_bytes = slices<Epi>() * (s.a_bytes + kBBytes);
   s.n_stages = std::min<uint32_t>(kMaxStages, ring_bytes<Epi>() / s.stage_bytes);
   s.wait_limit_ns = kWaitLimitNs;
   s.error_word = dev.error_word;
@@ -924,13 +1015,23 @@ int64_t rows_per_launch(int64_t B) {
   return ceil_div(blocks, ceil_div(blocks, 5)) * 2 * kBM;
 }
 
-int list_cap(int64_t K) { return K <= 0 ? 0 : K <= 4 ? 8 : 24; }
+int list_cap(int64_t K) { return K <= 0 ? 0 : K <= 4 ? 8 : K <= 12 ? 16 : 24; }
+
+// Columns of a single-CTA unit of the logits' kernels: the narrowest that still
+// gives every SM at most one unit, so that a small vocabulary starts as many
+// CTAs as it can (6 rows at d = 1790, V = 11137, K = 5: 256 wide 27.6 us, 128 23.6;
+// 64 would need two units of some CTAs: 37.2), else 256 (at V = 38281 47.7 us,
+// 128 wide 51.0): wide units read H least often and need the fewest barriers.
+int unit_cols(int64_t V, int least) {
+  int n = least;
+  while (n < kBN && ceil_div(V, n) > kPlanSms) n *= 2;
+  return n;
+}
 
 // Upper bound of a row's slots: groups of workers x 2 halves.
 int64_t plan_slots(int64_t rows, int64_t V) {
-  const int64_t workers = rows <= kBM ? kPlanSms : kPlanSms / 2;
-  const int64_t n_mt = rows <= kBM ? 1 : ceil_div(rows, 2 * kBM);
-  return 2 * std::min(ceil_div(V, kBN), workers / n_mt);
+  if (rows <= kBM) return 2 * std::min<int64_t>(ceil_div(V, unit_cols(V, 64)), kPlanSms);
+  return 2 * std::min<int64_t>(ceil_div(V, kBN), kPlanSms / 2 / ceil_div(rows, 2 * kBM));
 }
 
 bool sizes_ok(int64_t B, int64_t d, int64_t V) {
@@ -954,14 +1055,15 @@ fs_status run_scores(const fs_logprobs_args* a, const Device& dev, cudaStream_t 
     const int64_t rows = std::min(chunk, a->B - b0);
     const bool pair = rows > kBM;
     const int n_mt = pair ? int(ceil_div(rows, 2 * kBM)) : 1;
-    const int n_nt = int(ceil_div(a->V, kBN));
+    const int cols = pair ? kBN : unit_cols(a->V, 64);
+    const int n_nt = int(ceil_div(a->V, cols));
     const int groups = balanced(n_nt, (pair ? dev.pairs : dev.sms) / n_mt);
     const int n_slots = 2 * groups;
     const int box_rows = pair ? kBM : int(std::min<int64_t>(kBM, (rows + 7) / 8 * 8));
     const auto* H = static_cast<const __nv_bfloat16*>(a->H) + b0 * a->ldh;
     CUtensorMap mh, mw;
     if (!encode(dev, &mh, H, a->d, rows, a->ldh, box_rows) ||
-        !encode(dev, &mw, a->W, a->d, a->V, a->ldw, pair ? kBN / 2 : kBN))
+        !encode(dev, &mw, a->W, a->d, a->V, a->ldw, pair ? kBN / 2 : cols))
       return FS_ERR_INVALID_ARG;
     Shape s = {};
     s.n_mt = n_mt;
@@ -975,7 +1077,7 @@ fs_status run_scores(const fs_logprobs_args* a, const Device& dev, cudaStream_t 
     s.policy_a = kPolicyLast;
     s.policy_b = n_mt > 1 ? kPolicyNormal : kPolicyFirst;
     s.pdl = (a->flags & FS_FLAG_OVERLAP_PREVIOUS) && b0 == 0;
-    typename ScoreEpi<KC>::Params ep = {};
+    ScoreParams ep = {};
     ep.B = int32_t(rows);
     ep.V = int32_t(a->V);
     ep.temperature = a->temperature ? a->temperature + b0 : nullptr;
@@ -988,11 +1090,21 @@ fs_status run_scores(const fs_logprobs_args* a, const Device& dev, cudaStream_t 
     ep.cand_val = reinterpret_cast<float*>(ws);
     ws += round256(size_t(rows) * n_slots * KC * 4u);
     ep.cand_id = reinterpret_cast<int32_t*>(ws);
-    const fs_status st =
-        pair ? launch<ScoreEpi<KC>, true, false, false>(dev, mh, mw, mh, s, ep, groups * n_mt,
-                                                        s.pdl != 0, stream)
-             : launch<ScoreEpi<KC>, false, false, false>(dev, mh, mw, mh, s, ep, groups,
-                                                         s.pdl != 0, stream);
+    const bool overlap = s.pdl != 0;
+    const int workers = groups * n_mt;
+    fs_status st;
+    if (pair)
+      st = launch<ScoreEpi<KC, 256>, true, false, false>(dev, mh, mw, mh, s, ep, workers, overlap,
+                                                         stream);
+    else if (cols == 256)
+      st = launch<ScoreEpi<KC, 256>, false, false, false>(dev, mh, mw, mh, s, ep, workers, overlap,
+                                                          stream);
+    else if (cols == 128)
+      st = launch<ScoreEpi<KC, 128>, false, false, false>(dev, mh, mw, mh, s, ep, workers, overlap,
+                                                          stream);
+    else
+      st = launch<ScoreEpi<KC, 64>, false, false, false>(dev, mh, mw, mh, s, ep, workers, overlap,
+                                                         stream);
     if (st != FS_OK) return st;
     JoinParams j = {};
     j.H = H;
@@ -1108,6 +1220,7 @@ extern "C" fs_status fs_logprobs(const fs_logprobs_args* a, void* stream_ptr) {
   switch (list_cap(a->K)) {
     case 0: return run_scores<0>(a, *dev, stream);
     case 8: return run_scores<8>(a, *dev, stream);
+    case 16: return run_scores<16>(a, *dev, stream);
     default: return run_scores<24>(a, *dev, stream);
   }
 }
@@ -1160,14 +1273,15 @@ extern "C" fs_status fs_logprobs_grad(const fs_logprobs_grad_args* a, void* stre
   // G: the logits again, as in the forward pass.
   {
     const int box_rows = pair ? kBM : int(std::min<int64_t>(kBM, (B + 7) / 8 * 8));
+    const int cols = pair ? kBN : unit_cols(V, 128);  // a box of 64 columns a half
     CUtensorMap mh, mw, mg;
     if (!encode(dev, &mh, a->H, d, B, a->ldh, box_rows) ||
-        !encode(dev, &mw, a->W, d, V, a->ldw, pair ? kBN / 2 : kBN) ||
+        !encode(dev, &mw, a->W, d, V, a->ldw, pair ? kBN / 2 : cols) ||
         !encode(dev, &mg, G, ldg, B, ldg, 32))  // its padding columns are written (as 0)
       return FS_ERR_INVALID_ARG;
     Shape s = {};
     s.n_mt = int32_t(ceil_div(B, kBM * ctas));
-    s.n_nt = int32_t(ceil_div(V, kBN));
+    s.n_nt = int32_t(ceil_div(V, cols));
     s.n_units = s.n_mt * s.n_nt;
     s.n_kb = s.kb_per_split = int32_t(ceil_div(d, kBK));
     s.m_rows = int32_t(B);
@@ -1177,7 +1291,7 @@ extern "C" fs_status fs_logprobs_grad(const fs_logprobs_grad_args* a, void* stre
     s.policy_a = kPolicyLast;
     s.policy_b = kPolicyNormal;
     s.early_trigger = 1;
-    GradEpi::Params ep = {};
+    GradParams ep = {};
     ep.B = int32_t(B);
     ep.V = int32_t(V);
     ep.temperature = a->temperature;
@@ -1190,8 +1304,12 @@ extern "C" fs_status fs_logprobs_grad(const fs_logprobs_grad_args* a, void* stre
     ep.grad_entropy = a->grad_entropy;
     ep.vocab_offset = a->vocab_offset;
     const int n = balanced(s.n_units, workers);
-    st = pair ? launch<GradEpi, true, false, false>(dev, mh, mw, mg, s, ep, n, false, stream)
-              : launch<GradEpi, false, false, false>(dev, mh, mw, mg, s, ep, n, false, stream);
+    if (pair)
+      st = launch<GradEpi<256>, true, false, false>(dev, mh, mw, mg, s, ep, n, false, stream);
+    else if (cols == 256)
+      st = launch<GradEpi<256>, false, false, false>(dev, mh, mw, mg, s, ep, n, false, stream);
+    else
+      st = launch<GradEpi<128>, false, false, false>(dev, mh, mw, mg, s, ep, n, false, stream);
     if (st != FS_OK) return st;
   }
 

@@ -62,13 +62,13 @@ def test_workspace_sizes(lib):
     for bad in ((0, 100, 0), (65536, 100, 0), (4, 0, 0), (4, 2**31, 0), (4, 100, -1),
                 (4, 100, 21)):
         assert fs.fs_logprobs_workspace_size(*bad) == 0
-    # One vocabulary block: 2 slots a row; a slot is 16 bytes and its two lists.
+    # Small vocabularies: units of 64 ids, 2 slots each; a slot is 16 bytes and its two lists.
     assert fs.fs_logprobs_workspace_size(1, 100, 0) == 256
-    assert fs.fs_logprobs_workspace_size(64, 256, 4) == 64 * 2 * 16 + 2 * 64 * 2 * 8 * 4
+    assert fs.fs_logprobs_workspace_size(64, 256, 4) == 64 * 8 * 16 + 2 * 64 * 8 * 8 * 4
     # 594 vocabulary blocks: a group per SM for up to 128 rows.
     assert fs.fs_logprobs_workspace_size(128, 151936, 20) == 128 * 304 * (16 + 24 * 8)
     # 4 pair blocks of 256 rows: 19 groups of 4 pairs.
-    assert fs.fs_logprobs_workspace_size(1024, 151936, 5) == 1024 * 38 * (16 + 24 * 8)
+    assert fs.fs_logprobs_workspace_size(1024, 151936, 5) == 1024 * 38 * (16 + 16 * 8)
     # Above 5 pair blocks the rows go in several launches, each reusing it.
     assert (fs.fs_logprobs_workspace_size(65535, 151936, 5)
             <= 1280 * 50 * (16 + 24 * 8))
