@@ -4,14 +4,19 @@
 // Lookup: a copy bound by memory; a warp takes 2 KB of one row, 64 bytes a
 // lane in flight.
 //
-// Gradient, three kernels:
-//   sort_fill_kernel  a cluster of 8 CTAs sorts (id, position) stably; when the
-//                     whole table is written, the other CTAs meanwhile zero
-//                     the rows that no id names
-//   run_sum_kernel    the sorted positions in runs of 32: a warp sums one run
-//                     over 256 columns, writes the ids that begin and end in
-//                     the run, and leaves a partial sum for those that cross
-//                     into its neighbours
+// Gradient, up to 1024 ids, one kernel: every CTA sorts the (id, position) pairs
+// in shared memory, a warp sums each run of 32 sorted positions over the CTA's 64
+// columns, and ids that cross runs are joined; other CTAs zero the rows that no
+// id names.
+//
+// Gradient, more ids, three kernels:
+//   sort_fill_kernel  a cluster of 8 CTAs sorts the pairs, stably; when the whole
+//                     table is written, the other CTAs meanwhile zero rows that
+//                     no id names
+//   run_sum_kernel    the sorted positions in runs: a warp sums one run over 256
+//                     columns, writes the ids that begin and end in the run, and
+//                     leaves a partial sum for those that cross into its
+//                     neighbours; then it zeroes its share of the rows left
 //   run_join_kernel   the ids that cross runs, from their partial sums in order
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -35,7 +40,7 @@ __device__ __forceinline__ void put(float* p, float v) { *p = v; }
 __device__ __forceinline__ void put(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 
 // C columns of a row from p, as loaded (C = 8: 16-byte loads, p on a 16-byte
-// boundary; C = 1: one element).  Loading and converting are apart so that a
+// boundary; C = 2: a pair; C = 1: one element).  Loading and converting are apart so that a
 // warp's loads of several rows are all in flight before the first is used.
 template <typename T, int C>
 struct Piece;
@@ -44,6 +49,25 @@ struct Piece<T, 1> {
   T v;
   __device__ __forceinline__ void load(const T* p) { v = *p; }
   __device__ __forceinline__ void get(float (&f)[1]) const { f[0] = to_float(v); }
+};
+template <>
+struct Piece<__nv_bfloat16, 2> {
+  uint32_t v;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) {
+    v = *reinterpret_cast<const uint32_t*>(p);
+  }
+  __device__ __forceinline__ void get(float (&f)[2]) const {
+    f[0] = __uint_as_float(v << 16);
+    f[1] = __uint_as_float(v & 0xFFFF0000u);
+  }
+};
+template <>
+struct Piece<float, 2> {
+  float2 v;
+  __device__ __forceinline__ void load(const float* p) {
+    v = *reinterpret_cast<const float2*>(p);
+  }
+  __device__ __forceinline__ void get(float (&f)[2]) const { f[0] = v.x, f[1] = v.y; }
 };
 template <>
 struct Piece<__nv_bfloat16, 8> {
@@ -76,6 +100,12 @@ template <typename T>
 __device__ __forceinline__ void store(T* p, const float (&f)[1]) {
   put(p, f[0]);
 }
+__device__ __forceinline__ void store(__nv_bfloat16* p, const float (&f)[2]) {
+  *reinterpret_cast<__nv_bfloat162*>(p) = __floats2bfloat162_rn(f[0], f[1]);
+}
+__device__ __forceinline__ void store(float* p, const float (&f)[2]) {
+  *reinterpret_cast<float2*>(p) = make_float2(f[0], f[1]);
+}
 __device__ __forceinline__ void store(__nv_bfloat16* p, const float (&f)[8]) {
   __nv_bfloat162 h[4];
 #pragma unroll
@@ -88,17 +118,17 @@ __device__ __forceinline__ void store(float* p, const float (&f)[8]) {
 }
 
 // How a row's columns are divided among warps: columns below `vec` (a multiple
-// of 8; 0 where rows do not start on 16-byte boundaries) in segments of 8
-// columns a lane and G groups of lanes, the rest in segments of one column a
-// lane.  A warp works on one segment, so its path is uniform.
+// of 8; 0 where rows do not start on 16-byte boundaries) in segments of C columns
+// a lane and G groups of lanes, the rest in segments of one column a lane.  A
+// warp works on one segment, so its path is uniform.
 struct Columns {
   int32_t d, vec, vec_segments, segments;
 };
-__host__ Columns columns_of(int64_t d, bool vec, int groups) {
+__host__ Columns columns_of(int64_t d, bool vec, int C, int groups) {
   Columns c;
   c.d = int32_t(d);
   c.vec = vec ? int32_t(d & ~int64_t(7)) : 0;
-  c.vec_segments = (c.vec + 256 * groups - 1) / (256 * groups);
+  c.vec_segments = (c.vec + 32 * C * groups - 1) / (32 * C * groups);
   c.segments = c.vec_segments + (c.d - c.vec + 32 * groups - 1) / (32 * groups);
   return c;
 }
@@ -166,6 +196,7 @@ constexpr int kCluster = 8;
 constexpr int kMaxBits = 9;  // of a radix digit
 constexpr int kBins = 1 << kMaxBits;
 constexpr int kFillRows = 1 << 16;  // rows whose marks a CTA holds at once
+constexpr int kSmallMax = 1024;      // ids of the one-kernel gradient
 
 struct SortParams {
   const int64_t* ids;
@@ -186,6 +217,21 @@ __device__ __forceinline__ uint32_t row_of(const SortParams& p, int64_t id) {
   return (v >= 0 && v < p.V) ? uint32_t(v) : uint32_t(p.V);
 }
 
+// The lanes of the warp that hold an element with the same digit, for a lane that
+// holds one: a vote per digit bit (bits past the digit's width are 0 everywhere).
+// __match_any_sync takes several times as long where most lanes differ.
+template <int kBits>
+__device__ __forceinline__ uint32_t same_digit(uint32_t digit, bool has) {
+  uint32_t peers = __ballot_sync(0xFFFFFFFFu, has);
+#pragma unroll
+  for (int b = 0; b < kBits; ++b) {
+    const bool one = (digit >> b) & 1u;
+    const uint32_t ones = __ballot_sync(0xFFFFFFFFu, one);
+    peers &= one ? ones : ~ones;
+  }
+  return peers;
+}
+
 __device__ __forceinline__ uint32_t load_cluster(const uint32_t* p, uint32_t rank) {
   uint32_t v;
   asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(ptx::cluster_addr(p, rank))
@@ -197,17 +243,19 @@ __device__ __forceinline__ uint32_t load_cluster(const uint32_t* p, uint32_t ran
 // A pass: digit counts per CTA; every CTA reads all counts and places its own
 // after those of smaller digits and of earlier CTAs; then tiles of 1024
 // elements in order, each element ranked among the equal digits of its warp
-// (match), of the tile's earlier warps (a scan over the warps' counts) and of
+// (by votes), of the tile's earlier warps (a scan over the warps' counts) and of
 // earlier tiles (the running base).
 __device__ void sort_cluster(const SortParams& p, uint32_t rank) {
   __shared__ uint32_t hist[kBins];          // this CTA's digit counts
   __shared__ uint32_t base[kBins];          // next place of each digit
   __shared__ uint32_t scan[kSortWarps];
-  __shared__ uint16_t wc[kSortWarps][kBins];  // a tile's counts per warp, then offsets
+  __shared__ __align__(16) uint16_t wc[kSortWarps][kBins];  // a tile's counts per warp, then
+                                                            // offsets
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = (p.N + kCluster - 1) / kCluster;
   const int e0 = min(int(rank) * per, p.N), e1 = min(e0 + per, p.N);
   const int bins = 1 << p.bits;
+  const int warps = min(kSortWarps, (e1 - e0 + 31) / 32);  // that hold elements of a tile
   for (int pass = 0; pass < p.passes; ++pass) {
     const int shift = pass * p.bits;
     const uint32_t* kin = p.key[pass & 1];
@@ -215,9 +263,17 @@ __device__ void sort_cluster(const SortParams& p, uint32_t rank) {
     uint32_t* kout = p.key[(pass + 1) & 1];
     uint32_t* pout = p.pos[(pass + 1) & 1];
     auto key_at = [&](int i) { return pass == 0 ? row_of(p, p.ids[i]) : __ldcg(kin + i); };
+    // The first tile's elements stay in registers from the count to the move.
+    uint32_t key = 0u, at = 0u;
+    if (e0 + tid < e1) {
+      key = key_at(e0 + tid);
+      at = pass == 0 ? uint32_t(e0 + tid) : __ldcg(pin + e0 + tid);
+    }
     for (int i = tid; i < bins; i += kSortThreads) hist[i] = 0u;
     __syncthreads();
-    for (int i = e0 + tid; i < e1; i += kSortThreads)
+    if (e0 + tid < e1) atomicAdd(&hist[(key >> shift) & (bins - 1)], 1u);
+#pragma unroll 4
+    for (int i = e0 + kSortThreads + tid; i < e1; i += kSortThreads)
       atomicAdd(&hist[(key_at(i) >> shift) & (bins - 1)], 1u);
     ptx::cluster_sync();  // every CTA's counts are complete
     // Thread b: the digit's total, and its count in earlier CTAs.
@@ -239,29 +295,27 @@ __device__ void sort_cluster(const SortParams& p, uint32_t rank) {
     }
     if (lane == 31) scan[warp] = incl;
     __syncthreads();
-    uint32_t prev = 0u;
-    for (int w = 0; w < warp; ++w) prev += scan[w];
+    const uint32_t prev = __reduce_add_sync(0xFFFFFFFFu, lane < warp ? scan[lane] : 0u);
     if (tid < bins) base[tid] = prev + incl - total + before;
     for (int t0 = e0; t0 < e1; t0 += kSortThreads) {
-      for (int i = tid; i < kSortWarps * bins; i += kSortThreads)
-        wc[i / bins][i & (bins - 1)] = 0;
-      __syncthreads();
+      for (int w = warp; w < warps; w += kSortWarps)  // bins is even: 4 bytes at a time
+        for (int i = lane; i < bins / 2; i += 32) reinterpret_cast<uint32_t*>(wc[w])[i] = 0u;
       const int i = t0 + tid;
       const bool has = i < e1;
-      uint32_t key = 0u, digit = 0xFFFFFFFFu, at = 0u;
-      if (has) {
-        key = key_at(i);
-        at = pass == 0 ? uint32_t(i) : __ldcg(pin + i);
-        digit = (key >> shift) & (bins - 1);
+      if (t0 != e0) {
+        key = has ? key_at(i) : 0u;
+        at = !has ? 0u : pass == 0 ? uint32_t(i) : __ldcg(pin + i);
       }
-      const uint32_t peers = __match_any_sync(0xFFFFFFFFu, digit);
+      __syncthreads();
+      const uint32_t digit = (key >> shift) & (bins - 1);
+      const uint32_t peers = same_digit<kMaxBits>(digit, has);
       const uint32_t earlier = __popc(peers & ((1u << lane) - 1u));
       if (has && earlier == 0u) wc[warp][digit] = uint16_t(__popc(peers));
       __syncthreads();
       if (tid < bins) {
         uint32_t run = 0u;
 #pragma unroll 8
-        for (int w = 0; w < kSortWarps; ++w) {
+        for (int w = 0; w < warps; ++w) {
           const uint32_t n = wc[w][tid];
           wc[w][tid] = uint16_t(run);
           run += n;
@@ -281,6 +335,67 @@ __device__ void sort_cluster(const SortParams& p, uint32_t rank) {
     // all have been read.
     __threadfence();
     ptx::cluster_sync();
+  }
+}
+
+// Stable LSD radix sort of up to 1024 pairs by one CTA, a pair a thread, in shared
+// memory.  A pass counts the digits of every warp's pairs, sums the counts in
+// (digit, warp) order -- each count becomes the first place of its digit's pairs
+// -- and moves the pairs there.  Ends with the sorted pairs in key and pos.
+constexpr int kBlockBits = 7;  // of a digit, at most
+struct BlockSort {
+  uint16_t count[(1 << kBlockBits) * kSortWarps];
+  uint32_t key[kSortThreads];
+  uint32_t pos[kSortThreads];
+  uint32_t total[kSortWarps];
+};
+__device__ void sort_block(const SortParams& p, BlockSort& sm) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int bins = 1 << p.bits, n_counts = bins * kSortWarps;
+  const int chunk = max(1, n_counts / kSortThreads);  // counts of a thread's part of the sum
+  const int c0 = tid * chunk;
+  const bool has = tid < p.N;
+  uint32_t key = has ? row_of(p, p.ids[tid]) : 0u;
+  uint32_t pos = uint32_t(tid);
+  for (int pass = 0; pass < p.passes; ++pass) {
+    const uint32_t digit = (key >> (pass * p.bits)) & (bins - 1);
+    for (int i = tid; i < n_counts; i += kSortThreads) sm.count[i] = 0;
+    __syncthreads();
+    const uint32_t peers = same_digit<kBlockBits>(digit, has);
+    const uint32_t earlier = __popc(peers & ((1u << lane) - 1u));
+    if (has && earlier == 0u) sm.count[digit * kSortWarps + warp] = uint16_t(__popc(peers));
+    __syncthreads();
+    // Exclusive sums of the counts.
+    uint32_t mine = 0u;
+    if (c0 < n_counts)
+      for (int c = 0; c < chunk; ++c) mine += sm.count[c0 + c];
+    uint32_t incl = mine;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const uint32_t o = __shfl_up_sync(0xFFFFFFFFu, incl, off);
+      if (lane >= off) incl += o;
+    }
+    if (lane == 31) sm.total[warp] = incl;
+    __syncthreads();
+    const uint32_t before = __reduce_add_sync(0xFFFFFFFFu, lane < warp ? sm.total[lane] : 0u);
+    uint32_t run = before + incl - mine;
+    if (c0 < n_counts)
+      for (int c = 0; c < chunk; ++c) {
+        const uint32_t n = sm.count[c0 + c];
+        sm.count[c0 + c] = uint16_t(run);
+        run += n;
+      }
+    __syncthreads();
+    if (has) {
+      const uint32_t to = sm.count[digit * kSortWarps + warp] + earlier;
+      sm.key[to] = key;
+      sm.pos[to] = pos;
+    }
+    __syncthreads();
+    if (has) {
+      key = sm.key[tid];
+      pos = sm.pos[tid];
+    }
   }
 }
 
@@ -335,7 +450,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kSortThreads)
 // ---------------------------------------------------------------------------
 constexpr int kRunThreads = 128;
 constexpr int kRunWarps = kRunThreads / 32;
-constexpr int kAhead = 8;  // rows in flight per warp
+constexpr int kAhead = 8;  // rows in flight per warp (16 at 2 columns a lane: no gain)
 
 struct RunParams {
   const uint32_t* key;  // sorted rows of the table, V at the end for dropped ids
@@ -504,33 +619,89 @@ __global__ void __launch_bounds__(kRunThreads) run_sum_kernel(const RunParams p)
   }
 }
 
-template <typename TO, bool kAdd>
-__global__ void __launch_bounds__(kRunThreads) run_join_kernel(const RunParams p) {
-  ptx::grid_dependency_wait();
-  const int lane = threadIdx.x & 31;
-  const int64_t item = (int64_t(blockIdx.x) * kRunThreads + threadIdx.x) >> 5;
-  const int run = int(item / p.cols.segments);
-  if (run >= p.n_runs - 1) return;  // the last run's ids end in it
-  const int seg = int(item - int64_t(run) * p.cols.segments);
+// The last run that goes on with the id that run `run` ends in (by a warp; 32 runs
+// looked at at once), or -1 if no id begins in the run and goes on.
+__device__ __forceinline__ int last_run(const RunParams& p, int run, int lane) {
+  if (run >= p.n_runs - 1) return -1;  // the last run's ids end in it
   const int i0 = run * p.run, i1 = i0 + p.run;  // a run before the last is full
   const uint32_t id = p.key[i1 - 1];
-  if (id == uint32_t(p.V) || p.key[i1] != id) return;
-  if (p.key[i0] == id && i0 > 0 && p.key[i0 - 1] == id) return;  // began earlier
-  // The runs that go on with the id (32 looked at at once).
+  if (id == uint32_t(p.V) || p.key[i1] != id) return -1;
+  if (p.key[i0] == id && i0 > 0 && p.key[i0 - 1] == id) return -1;  // began earlier
   int last = run;
   while (true) {
     const int r = last + 1 + lane;
     const bool on = r < p.n_runs && p.key[int64_t(r) * p.run] == id;
     const uint32_t all = __ballot_sync(0xFFFFFFFFu, on);
     last += all == 0xFFFFFFFFu ? 32 : __ffs(~all) - 1;
-    if (all != 0xFFFFFFFFu) break;
+    if (all != 0xFFFFFFFFu) return last;
   }
+}
+
+template <typename TO, bool kAdd>
+__global__ void __launch_bounds__(kRunThreads) run_join_kernel(const RunParams p) {
+  ptx::grid_dependency_wait();
+  const int lane = threadIdx.x & 31;
+  const int64_t item = (int64_t(blockIdx.x) * kRunThreads + threadIdx.x) >> 5;
+  const int run = int(item / p.cols.segments);
+  const int seg = int(item - int64_t(run) * p.cols.segments);
+  const int last = last_run(p, run, lane);
+  if (last < 0) return;
+  const uint32_t id = p.key[(run + 1) * p.run - 1];
   if (seg < p.cols.vec_segments) {
     const int col = seg * 256 + lane * 8;
     if (col < p.cols.vec) join_runs<TO, 8, kAdd>(p, run, last, id, col);
   } else {
     const int col = p.cols.vec + (seg - p.cols.vec_segments) * 32 + lane;
     if (col < p.cols.d) join_runs<TO, 1, kAdd>(p, run, last, id, col);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Gradient of up to kSmallMax ids, one kernel
+// ---------------------------------------------------------------------------
+constexpr int kSmallCols = 64;  // columns of a CTA: two a lane (one where rows are not aligned)
+struct SmallShared {
+  BlockSort sort;
+  float partial[kSmallMax / 32 * 2 * kSmallCols];
+};
+
+template <typename TY, typename TO, int C, bool kAdd>
+__device__ __forceinline__ void small_segment(const RunParams& p, int warp, int lane, int col,
+                                              bool in) {
+  if (warp < p.n_runs) sum_run<TY, TO, C, kAdd>(p, warp, col, in, lane);
+  __syncthreads();
+  const int last = last_run(p, warp, lane);
+  if (last >= 0 && in)
+    join_runs<TO, C, kAdd>(p, warp, last, p.key[(warp + 1) * p.run - 1], col);
+}
+
+// CTAs 0 .. segments - 1: a segment of the columns, a warp for each run of 32
+// sorted positions; the others zero rows.  The sort is done by every CTA for
+// itself (about 1.5 us), so that none waits for another.
+template <typename TY, typename TO, bool kAdd>
+__global__ void __launch_bounds__(kSortThreads)
+    small_grad_kernel(const SortParams sp, const RunParams rp) {
+  __shared__ SmallShared sm;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int seg = blockIdx.x;
+  if (seg >= rp.cols.segments) {
+    fill_rows(sp, seg - rp.cols.segments, int(gridDim.x) - rp.cols.segments);
+    return;
+  }
+  sort_block(sp, sm.sort);
+  __syncthreads();
+  RunParams p = rp;
+  p.key = sm.sort.key;
+  p.pos = sm.sort.pos;
+  p.ldp = kSmallCols;
+  if (seg < p.cols.vec_segments) {
+    const int col0 = seg * 64, col = col0 + lane * 2;
+    p.partial = sm.partial - col0;
+    small_segment<TY, TO, 2, kAdd>(p, warp, lane, col, col < p.cols.vec);
+  } else {
+    const int col0 = p.cols.vec + (seg - p.cols.vec_segments) * 32, col = col0 + lane;
+    p.partial = sm.partial - col0;
+    small_segment<TY, TO, 1, kAdd>(p, warp, lane, col, col < p.cols.d);
   }
 }
 
@@ -578,17 +749,19 @@ bool sizes_ok(int64_t N, int64_t V, int64_t d, int64_t vocab_offset) {
          V <= INT_MAX && vocab_offset + V <= INT_MAX;
 }
 
-cudaError_t launch_after(const void* kernel, int64_t blocks, int threads, void** args,
-                         cudaStream_t stream) {
+// `after`: as a programmatic dependent of the kernel before.
+cudaError_t launch(const void* kernel, int64_t blocks, int threads, size_t smem, bool after,
+                   void** args, cudaStream_t stream) {
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(blocks), 1, 1);
   cfg.blockDim = dim3(unsigned(threads), 1, 1);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cfg.attrs = &attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = after ? 1 : 0;
   return cudaLaunchKernelExC(&cfg, kernel, args);
 }
 
@@ -608,7 +781,7 @@ extern "C" fs_status fs_embed(const int64_t* ids, int64_t N, const void* E, int6
       !aligned(out, element(dtype)))
     return FS_ERR_INVALID_ARG;
   const Columns cols =
-      columns_of(d, rows_vec(E, lde, dtype) && rows_vec(out, ldo, dtype), kLookupGroups);
+      columns_of(d, rows_vec(E, lde, dtype) && rows_vec(out, ldo, dtype), 8, kLookupGroups);
   const int64_t blocks = ceil_div(N * cols.segments, kLookupThreads / 32);
   if (blocks > INT_MAX) return FS_ERR_INVALID_ARG;
   const fs_status st = device_check();
@@ -633,7 +806,14 @@ namespace {
 // ones more warps.
 int64_t run_length(int64_t N) { return N <= 8192 ? 32 : 64; }
 
-constexpr int kFillCtas = 19 * kCluster;  // with the sorting cluster, 160 CTAs
+template <bool kAdd>
+const void* small_kernel(int y_dtype, int e_dtype) {
+  if (y_dtype == FS_F32)
+    return reinterpret_cast<const void*>(&small_grad_kernel<float, float, kAdd>);
+  if (e_dtype == FS_F32)
+    return reinterpret_cast<const void*>(&small_grad_kernel<__nv_bfloat16, float, kAdd>);
+  return reinterpret_cast<const void*>(&small_grad_kernel<__nv_bfloat16, __nv_bfloat16, kAdd>);
+}
 
 template <bool kAdd>
 const void* sum_kernel(int y_dtype, int e_dtype) {
@@ -683,9 +863,10 @@ extern "C" fs_status fs_embed_grad(const int64_t* ids, int64_t N, const void* dY
     return FS_OK;
   }
   if (!ids || !dY || !aligned(ids, 8) || !aligned(dY, element(y_dtype))) return FS_ERR_INVALID_ARG;
+  const bool small = N <= kSmallMax;
   const int64_t run = run_length(N), n_runs = ceil_div(N, run);
-  const Columns cols =
-      columns_of(d, rows_vec(dY, ldy, y_dtype) && rows_vec(dE, lde, e_dtype), 1);
+  const bool vec = rows_vec(dY, ldy, y_dtype) && rows_vec(dE, lde, e_dtype);
+  const Columns cols = columns_of(d, vec, small ? 2 : 8, 1);
   const int64_t blocks = ceil_div(n_runs * cols.segments, kRunWarps);
   if (blocks > INT_MAX) return FS_ERR_INVALID_ARG;
   if (!workspace || !aligned(workspace, 256) ||
@@ -701,31 +882,15 @@ extern "C" fs_status fs_embed_grad(const int64_t* ids, int64_t N, const void* dY
   sp.vocab_offset = vocab_offset;
   int bits = 1;
   while (bits < 31 && (int64_t(1) << bits) <= V) ++bits;  // rows 0 .. V
-  sp.passes = (bits + kMaxBits - 1) / kMaxBits;
+  const int most = small ? kBlockBits : kMaxBits;
+  sp.passes = (bits + most - 1) / most;
   sp.bits = (bits + sp.passes - 1) / sp.passes;
-  uint8_t* ws = static_cast<uint8_t*>(workspace);
-  const size_t one = round256(size_t(N) * 4u);
-  for (int i = 0; i < 2; ++i) {
-    sp.key[i] = reinterpret_cast<uint32_t*>(ws + one * i);
-    sp.pos[i] = reinterpret_cast<uint32_t*>(ws + one * (2 + i));
-  }
-  RunParams rp = {};
-  rp.zero_from = V;
   if (!accumulate) {
     sp.table = static_cast<uint8_t*>(dE);
     sp.table_ld = lde * element(e_dtype);
     sp.row_bytes = d * element(e_dtype);
-    // As many rows as the other CTAs can zero while the cluster sorts; the rest
-    // are zeroed beside the sums, whose reads they do not slow.
-    const int64_t bytes = (int64_t(8) + N / 1024) * 4000000;
-    sp.fill_rows = std::min(V, ceil_div(bytes, sp.row_bytes));
-    rp.zero_from = sp.fill_rows;
   }
-  sort_fill_kernel<<<accumulate ? kCluster : kCluster + kFillCtas, kSortThreads, 0, stream>>>(sp);
-  if (cudaGetLastError() != cudaSuccess) return FS_ERR_CUDA;
-
-  rp.key = sp.key[sp.passes & 1];
-  rp.pos = sp.pos[sp.passes & 1];
+  RunParams rp = {};
   rp.N = int32_t(N);
   rp.V = int32_t(V);
   rp.run = int32_t(run);
@@ -736,17 +901,58 @@ extern "C" fs_status fs_embed_grad(const int64_t* ids, int64_t N, const void* dY
   rp.dE = dE;
   rp.lde = lde;
   rp.scale = scale;
+  rp.zero_from = V;
+  cudaError_t err;
+
+  if (small) {
+    // A CTA to zero every 128 KB, at most two an SM.
+    int64_t fill = 0;
+    if (!accumulate) {
+      sp.fill_rows = V;
+      fill = std::min<int64_t>(2 * 152, ceil_div(V * sp.row_bytes, 131072));
+    }
+    void* args[] = {&sp, &rp};
+    err = launch(accumulate ? small_kernel<true>(y_dtype, e_dtype)
+                            : small_kernel<false>(y_dtype, e_dtype),
+                 cols.segments + fill, kSortThreads, 0, false, args, stream);
+    if (err != cudaSuccess) {
+      cudaGetLastError();
+      return FS_ERR_CUDA;
+    }
+    return FS_OK;
+  }
+
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  const size_t one = round256(size_t(N) * 4u);
+  for (int i = 0; i < 2; ++i) {
+    sp.key[i] = reinterpret_cast<uint32_t*>(ws + one * i);
+    sp.pos[i] = reinterpret_cast<uint32_t*>(ws + one * (2 + i));
+  }
+  if (!accumulate) {
+    // As many rows as the other CTAs can zero while the ids are sorted; the rest
+    // are zeroed beside the sums, whose reads they do not slow.
+    const int64_t us = 8 + N / 1024;
+    sp.fill_rows = std::min(V, ceil_div(us * 4000000, sp.row_bytes));
+    rp.zero_from = sp.fill_rows;
+  }
+  rp.key = sp.key[sp.passes & 1];
+  rp.pos = sp.pos[sp.passes & 1];
   rp.partial = reinterpret_cast<float*>(ws + 4 * one);
   rp.ldp = partial_ld(d);
+  void* sort_args[] = {&sp};
+  // One cluster sorts; 19 more (152 CTAs) zero rows.
+  err = launch(reinterpret_cast<const void*>(&sort_fill_kernel),
+               accumulate ? kCluster : 20 * kCluster, kSortThreads, 0, false, sort_args, stream);
   const void* sum = accumulate ? sum_kernel<true>(y_dtype, e_dtype)
                                : sum_kernel<false>(y_dtype, e_dtype);
   const void* join = accumulate ? join_kernel_of<true>(e_dtype) : join_kernel_of<false>(e_dtype);
   void* args[] = {&rp};
   // With rows to zero, warps for them too: 8 blocks an SM.
-  cudaError_t err = launch_after(sum, accumulate ? blocks : std::max<int64_t>(blocks, 8 * 152),
-                                 kRunThreads, args, stream);
+  if (err == cudaSuccess)
+    err = launch(sum, accumulate ? blocks : std::max<int64_t>(blocks, 8 * 152), kRunThreads, 0,
+                 true, args, stream);
   if (err == cudaSuccess && n_runs > 1)
-    err = launch_after(join, blocks, kRunThreads, args, stream);
+    err = launch(join, blocks, kRunThreads, 0, true, args, stream);
   if (err != cudaSuccess) {
     cudaGetLastError();
     return FS_ERR_CUDA;
