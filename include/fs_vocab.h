@@ -37,11 +37,11 @@ extern "C" {
  *                the lower id, with their log-probabilities
  * The [B,V] logits never reach device memory.
  *
- * The logits of the token and of the K best candidates (K + 4 of them are
- * taken from the fp32 tensor-core sums) are summed again in compensated fp32,
- * about 48 bits, and ranked on that: ids whose logits differ by less than fp32
- * resolves still come in the order of their exact logits, and the alternatives
- * do not depend on B or on how the work was split.
+ * The logits of the token and of K + 4 candidates (the best by their tensor-core
+ * sums, compared in 17 bits) are summed again in compensated fp32, about 45
+ * bits, and ranked on that: ids whose logits differ by less than fp32 resolves
+ * still come in the order of their exact logits, and the alternatives do not
+ * depend on B or on how the work was split.
  *
  * Conventions: T_b <= 0, NaN or +inf (greedy rows of the sampler) means T = 1.
  * A token below 0 means "no token": logp 0.  A token that the mask clears, or

@@ -411,12 +411,14 @@ __device__ __forceinline__ float2 warp_logit(const __nv_bfloat16* __restrict__ h
   return make_float2(sum, err);
 }
 
-// logit / T - lse in fp32 without the quotient's rounding.
+// logit / T - lse in fp32 without the quotient's rounding; at most 0 (lse is off
+// by its own rounding where one token has nearly all the mass).  NaN stays.
 __device__ __forceinline__ float scaled_logp(float2 logit, float T, float lse) {
   const float q = __fdiv_rn(logit.x, T);
   if (!isfinite(q)) return q - lse;
   const float rest = (__fmaf_rn(-q, T, logit.x) + logit.y) / T;
-  return (q - lse) + rest;
+  const float logp = (q - lse) + rest;
+  return logp > 0.0f ? 0.0f : logp;
 }
 
 // An order-preserving map of floats to unsigned integers; NaN counts as +inf
