@@ -2,14 +2,15 @@
 ``include/fs_vocab.h``).
 
 Argument marshalling only: tensors become device pointers, sizes and strides;
-every step of the sampling path runs in the library's CUDA kernels.  PyTorch
-provides device memory and the current stream.  When the library has not been
-built, every call raises ``FsError`` -- there is no fallback.
+every step of the operators runs in the library's CUDA kernels.  PyTorch
+provides device memory and the current stream.  The operators of fs_vocab.h are
+marshalled by ``_marshal.so`` (``csrc/fs_marshal.cpp``), the same in C++.  When
+the libraries have not been built, every call raises ``FsError`` -- there is no
+fallback.
 """
 from __future__ import annotations
 
 import ctypes
-import functools
 import os
 from typing import NamedTuple, Optional
 
@@ -85,6 +86,7 @@ class FsLogprobsGradArgs(ctypes.Structure):
 
 
 _lib = None
+_marshal = None
 
 
 def load_library(path: str = LIB_PATH):
@@ -146,7 +148,22 @@ def load_library(path: str = LIB_PATH):
     lib.fs_status_string.argtypes = [ctypes.c_int]
     lib.fs_status_string.restype = ctypes.c_char_p
     _lib = lib
+    _bind_marshal(lib)
     return lib
+
+
+def _bind_marshal(lib):
+    """Load _marshal.so (once) and hand it the library's entry points."""
+    global _marshal
+    try:
+        from . import _marshal
+    except ImportError as e:
+        raise FsError(FS_ERR_UNSUPPORTED, f"_marshal.so cannot be loaded ({e}); build it with "
+                                          "lm_head_gumbel_gb300.build.build()") from e
+    _marshal.bind(FsError, *(ctypes.cast(f, ctypes.c_void_p).value for f in (
+        lib.fs_logprobs, lib.fs_logprobs_workspace_size, lib.fs_logprobs_grad,
+        lib.fs_logprobs_grad_workspace_size, lib.fs_embed, lib.fs_embed_grad,
+        lib.fs_embed_grad_workspace_size)))
 
 
 def _ptr(t):
@@ -400,75 +417,11 @@ def fs_gumbel_noise(b0, nb, v0, nv, *, seed=0, offset=0, seeds=None, out=None, d
 
 
 # ---- the operators of fs_vocab.h ------------------------------------------
-# These calls take a few microseconds on the GPU at decode sizes, so their host
-# side is kept short: one check per argument, none for results made here, raw
-# addresses instead of ctypes objects.
-_F32, _I64, _BF16 = torch.float32, torch.int64, torch.bfloat16
-_ELEMENT = {_BF16: FS_BF16, _F32: FS_F32}
-
-
-def _refuse(what):
-    raise FsError(FS_ERR_INVALID_ARG, what)
-
-
-def _vector(name, t, dtype, n, gpu):
-    """Address of a contiguous vector of n elements on device `gpu`."""
-    if t.dtype is not dtype or t.get_device() != gpu or t.shape != (n,) or not t.is_contiguous():
-        _refuse(f"{name} must be a contiguous {dtype} vector of {n} on cuda:{gpu}")
-    return t.data_ptr()
-
-
-def _matrix(name, t, dtype, n, d, gpu):
-    """Address and row stride of an [n, d] matrix on device `gpu` (of a single
-    row: a stride that every check accepts)."""
-    if t.dtype is not dtype or t.get_device() != gpu or t.shape != (n, d):
-        _refuse(f"{name} must be a {dtype} matrix [{n}, {d}] on cuda:{gpu}")
-    ld, unit = t.stride()
-    if unit != 1 and d > 1:
-        _refuse(f"{name} must have unit column stride")
-    return t.data_ptr(), ld if n > 1 else max(ld, (d + 7) // 8 * 8)
-
-
-def _head(H, W):
-    """Sizes, device, addresses and row strides of H [B, d] and W [V, d]."""
-    if H.dim() != 2 or W.dim() != 2 or not H.is_cuda:
-        _refuse("H and W must be CUDA bfloat16 matrices")
-    B, d = H.shape
-    V, gpu = W.shape[0], H.get_device()
-    h, ldh = _matrix("H", H, _BF16, B, d, gpu)
-    w, ldw = _matrix("W", W, _BF16, V, d, gpu)
-    return B, d, V, gpu, h, ldh, w, ldw
-
-
-def _mask(vocab_mask, B, V, gpu):
-    if vocab_mask.dtype is not torch.int32 or vocab_mask.dim() != 2 \
-            or vocab_mask.shape[0] != B or vocab_mask.shape[1] < (V + 31) // 32 \
-            or vocab_mask.stride(1) != 1 or vocab_mask.get_device() != gpu:
-        _refuse(f"vocab_mask must be an int32 matrix [B, >= ceil(V/32)] on cuda:{gpu}")
-    return vocab_mask.data_ptr(), max(vocab_mask.stride(0), vocab_mask.shape[1])
-
-
-def _workspace(workspace, gpu):
-    """Address and bytes of a given workspace."""
-    if workspace.get_device() != gpu or not workspace.is_contiguous():
-        raise FsError(FS_ERR_WORKSPACE, f"workspace must be a contiguous tensor on cuda:{gpu}")
-    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
-
-
-def _call(name, function, gpu, stream, *args):
-    """Call the library on `stream` (default: the device's current one) with
-    device `gpu` current, and check its status."""
-    if stream is None:  # without building a Stream object
-        stream = torch._C._cuda_getCurrentRawStream(gpu)
-    else:
-        stream = stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
-    if torch._C._cuda_getDevice() == gpu:
-        st = function(*args, stream)
-    else:
-        with torch.cuda.device(gpu):
-            st = function(*args, stream)
-    if st != FS_OK:
-        raise FsError(st, name)
+# Keyword interfaces; _marshal.so checks the tensors, makes the results that were
+# not given and calls the library.
+def _handle(stream):
+    """A stream as _marshal.so takes it: None (the current one) or its handle."""
+    return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else stream
 
 
 class FsLogprobs(NamedTuple):
@@ -480,7 +433,6 @@ class FsLogprobs(NamedTuple):
     topk_logp: Optional[torch.Tensor]  # fp32 [B, K]
 
 
-@functools.lru_cache(maxsize=256)
 def fs_logprobs_workspace_size(B: int, V: int, K: int = 0) -> int:
     return int(load_library().fs_logprobs_workspace_size(int(B), int(V), int(K)))
 
@@ -498,77 +450,16 @@ def fs_logprobs(H, W, tokens=None, K=0, *, temperature=None, vocab_mask=None, vo
     fs_sample (rows it samples greedily are scored at T = 1).  out_*: result
     tensors to fill, made when None.  workspace: a uint8 tensor of
     fs_logprobs_workspace_size(B, V, K) bytes, or None.  Returns FsLogprobs."""
-    lib = _lib or load_library()
-    B, d, V, gpu, h, ldh, w, ldw = _head(H, W)
-    if not 0 <= K <= FS_LOGPROBS_TOPK_MAX:
-        _refuse(f"K must be 0 to {FS_LOGPROBS_TOPK_MAX}")
-    dev, empty = H.device, torch.empty
-    temp = mask = tok = logp = idx = top = None
-    mask_ld = 0
-    if temperature is not None:
-        temp = _vector("temperature", temperature, _F32, B, gpu)
-    if vocab_mask is not None:
-        mask, mask_ld = _mask(vocab_mask, B, V, gpu)
-    if tokens is None:
-        out_logp = None
-    else:
-        tok = _vector("tokens", tokens, _I64, B, gpu)
-        if out_logp is None:
-            out_logp = empty(B, dtype=_F32, device=dev)
-            logp = out_logp.data_ptr()
-        else:
-            logp = _vector("out_logp", out_logp, _F32, B, gpu)
-    if out_entropy is None:
-        out_entropy = empty(B, dtype=_F32, device=dev)
-        entropy = out_entropy.data_ptr()
-    else:
-        entropy = _vector("out_entropy", out_entropy, _F32, B, gpu)
-    if out_lse is None:
-        out_lse = empty(B, dtype=_F32, device=dev)
-        lse = out_lse.data_ptr()
-    else:
-        lse = _vector("out_lse", out_lse, _F32, B, gpu)
-    if K == 0:
-        out_topk_idx = out_topk_logp = None
-    else:
-        if out_topk_idx is None:
-            out_topk_idx = empty((B, K), dtype=_I64, device=dev)
-            idx = out_topk_idx.data_ptr()
-        else:
-            idx = _matrix("out_topk_idx", out_topk_idx, _I64, B, K, gpu)[0]
-        if out_topk_logp is None:
-            out_topk_logp = empty((B, K), dtype=_F32, device=dev)
-            top = out_topk_logp.data_ptr()
-        else:
-            top = _matrix("out_topk_logp", out_topk_logp, _F32, B, K, gpu)[0]
-        if not (out_topk_idx.is_contiguous() and out_topk_logp.is_contiguous()):
-            _refuse("out_topk_idx and out_topk_logp must be contiguous")
-    if workspace is None:
-        ws_bytes = fs_logprobs_workspace_size(B, V, K)
-        workspace = empty(ws_bytes, dtype=torch.uint8, device=dev)
-        ws = workspace.data_ptr()
-    else:
-        ws, ws_bytes = _workspace(workspace, gpu)
-    args = FsLogprobsArgs(h, w, temp, mask, mask_ld, tok, B, d, V, ldh, ldw, int(vocab_offset), K,
-                          logp, entropy, lse, idx, top, ws, ws_bytes,
-                          FS_FLAG_OVERLAP_PREVIOUS if overlap_previous else 0)
-    _call("fs_logprobs", lib.fs_logprobs, gpu, stream, args)
-    return FsLogprobs(out_logp, out_entropy, out_lse, out_topk_idx, out_topk_logp)
+    if _lib is None:
+        load_library()
+    return FsLogprobs(*_marshal.logprobs(
+        H, W, tokens, K, temperature, vocab_mask, vocab_offset, out_logp, out_entropy, out_lse,
+        out_topk_idx, out_topk_logp, workspace, _handle(stream),
+        FS_FLAG_OVERLAP_PREVIOUS if overlap_previous else 0))
 
 
-@functools.lru_cache(maxsize=256)
 def fs_logprobs_grad_workspace_size(B: int, d: int, V: int) -> int:
     return int(load_library().fs_logprobs_grad_workspace_size(int(B), int(d), int(V)))
-
-
-def _gradient(name, out, n, d, gpu, dev):
-    """A bf16 [n, d] result (made here with rows on 16-byte boundaries when
-    None), its address and row stride."""
-    if out is None:
-        ld = (d + 7) // 8 * 8
-        out = torch.empty((n, ld), dtype=_BF16, device=dev)
-        return (out if ld == d else out[:, :d]), out.data_ptr(), ld
-    return (out,) + _matrix(name, out, _BF16, n, d, gpu)
 
 
 def fs_logprobs_grad(H, W, tokens, lse, grad_logp, *, entropy=None, grad_entropy=None,
@@ -581,68 +472,22 @@ def fs_logprobs_grad(H, W, tokens, lse, grad_logp, *, entropy=None, grad_entropy
     grad_entropy: fp32 [B].  Returns (dH, dW) in bf16 ([B, d], [V, d]; out_dH /
     out_dW when given), None where need_dH / need_dW is false.  workspace: a
     uint8 tensor of fs_logprobs_grad_workspace_size(B, d, V) bytes, or None."""
-    lib = _lib or load_library()
-    B, d, V, gpu, h, ldh, w, ldw = _head(H, W)
-    if not (need_dH or need_dW):
-        _refuse("neither dH nor dW is asked for")
-    if tokens is None or lse is None or grad_logp is None:
-        _refuse("tokens, lse and grad_logp are required")
-    if grad_entropy is not None and entropy is None:
-        _refuse("grad_entropy needs entropy")
-    dev = H.device
-    temp = mask = ent = g_ent = dh = dw = None
-    mask_ld = lddh = lddw = 0
-    if temperature is not None:
-        temp = _vector("temperature", temperature, _F32, B, gpu)
-    if vocab_mask is not None:
-        mask, mask_ld = _mask(vocab_mask, B, V, gpu)
-    if grad_entropy is not None:
-        ent = _vector("entropy", entropy, _F32, B, gpu)
-        g_ent = _vector("grad_entropy", grad_entropy, _F32, B, gpu)
-    if need_dH:
-        out_dH, dh, lddh = _gradient("out_dH", out_dH, B, d, gpu, dev)
-    else:
-        out_dH = None
-    if need_dW:
-        out_dW, dw, lddw = _gradient("out_dW", out_dW, V, d, gpu, dev)
-    else:
-        out_dW = None
-    if workspace is None:
-        ws_bytes = fs_logprobs_grad_workspace_size(B, d, V)
-        workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
-        ws = workspace.data_ptr()
-    else:
-        ws, ws_bytes = _workspace(workspace, gpu)
-    args = FsLogprobsGradArgs(
-        h, w, temp, mask, mask_ld, _vector("tokens", tokens, _I64, B, gpu),
-        _vector("lse", lse, _F32, B, gpu), ent, _vector("grad_logp", grad_logp, _F32, B, gpu),
-        g_ent, B, d, V, ldh, ldw, int(vocab_offset), dh, dw, lddh, lddw, ws, ws_bytes)
-    _call("fs_logprobs_grad", lib.fs_logprobs_grad, gpu, stream, args)
-    return out_dH, out_dW
+    if _lib is None:
+        load_library()
+    return _marshal.logprobs_grad(H, W, tokens, lse, grad_logp, entropy, grad_entropy,
+                                  temperature, vocab_mask, vocab_offset, out_dH, out_dW, need_dH,
+                                  need_dW, workspace, _handle(stream))
 
 
 def fs_embed(ids, E, *, scale=1.0, vocab_offset=0, out=None, stream=None):
     """Embedding lookup: scale * E[ids - vocab_offset], 0 where the id is not
     one of E's rows (padding, another shard).  ids: int64 [N]; E: bf16 or fp32
     [V, d].  Returns out ([N, d] of E's type)."""
-    lib = _lib or load_library()
-    dtype = E.dtype
-    code = _ELEMENT.get(dtype)
-    if code is None or E.dim() != 2 or not E.is_cuda:
-        _refuse("E must be a CUDA bfloat16 or float32 matrix")
-    (V, d), (N, *_), gpu = E.shape, ids.shape, E.get_device()
-    e, lde = _matrix("E", E, dtype, V, d, gpu)
-    if out is None:
-        out = torch.empty((N, d), dtype=dtype, device=E.device)
-        o, ldo = out.data_ptr(), d
-    else:
-        o, ldo = _matrix("out", out, dtype, N, d, gpu)
-    _call("fs_embed", lib.fs_embed, gpu, stream, _vector("ids", ids, _I64, N, gpu), N, e, V, d,
-          lde, code, scale, vocab_offset, o, ldo)
-    return out
+    if _lib is None:
+        load_library()
+    return _marshal.embed(ids, E, scale, vocab_offset, out, _handle(stream))
 
 
-@functools.lru_cache(maxsize=256)
 def fs_embed_grad_workspace_size(N: int, d: int) -> int:
     return int(load_library().fs_embed_grad_workspace_size(int(N), int(d)))
 
@@ -656,27 +501,11 @@ def fs_embed_grad(ids, dY, V, *, scale=1.0, vocab_offset=0, out=None, out_dtype=
     a result made here (dY's when None).  The same inputs always give the same
     bits.  workspace: a uint8 tensor of fs_embed_grad_workspace_size(N, d)
     bytes, or None."""
-    lib = _lib or load_library()
-    y_code = _ELEMENT.get(dY.dtype)
-    if y_code is None or dY.dim() != 2 or not dY.is_cuda:
-        _refuse("dY must be a CUDA bfloat16 or float32 matrix")
-    (N, d), gpu, V = dY.shape, dY.get_device(), int(V)
-    y, ldy = _matrix("dY", dY, dY.dtype, N, d, gpu)
-    if out is None:
-        if accumulate:
-            _refuse("accumulate needs out")
-        out = torch.empty((V, d), dtype=out_dtype or dY.dtype, device=dY.device)
-    e_code = _ELEMENT.get(out.dtype)
-    if e_code is None:
-        _refuse("out must be bfloat16 or float32")
-    e, lde = _matrix("out", out, out.dtype, V, d, gpu)
-    if workspace is None:
-        ws_bytes = fs_embed_grad_workspace_size(N, d)
-        workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=dY.device)
-        ws = workspace.data_ptr()
-    else:
-        ws, ws_bytes = _workspace(workspace, gpu)
-    _call("fs_embed_grad", lib.fs_embed_grad, gpu, stream, _vector("ids", ids, _I64, N, gpu), N,
-          y, V, d, ldy, y_code, scale, vocab_offset, e, lde, e_code, 1 if accumulate else 0, ws,
-          ws_bytes)
-    return out
+    if _lib is None:
+        load_library()
+    if out_dtype is not None and out_dtype not in (torch.bfloat16, torch.float32):
+        raise FsError(FS_ERR_INVALID_ARG, "out_dtype must be bfloat16 or float32")
+    if out is None and out_dtype is torch.bfloat16 and dY.dtype is torch.float32:
+        raise FsError(FS_ERR_INVALID_ARG, "the gradient of float32 dY is float32")
+    return _marshal.embed_grad(ids, dY, V, scale, vocab_offset, out, accumulate,
+                               out_dtype is torch.float32, workspace, _handle(stream))
