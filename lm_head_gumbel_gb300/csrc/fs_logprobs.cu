@@ -1141,8 +1141,11 @@ fs_status run_scores(const fs_logprobs_args* a, const Device& dev, cudaStream_t 
 // ---- gradient ------------------------------------------------------------
 
 // How dH = G W is split along k (the vocabulary).  Unsplit, the tiles of
-// [B, d] leave workers idle or in a thin last wave; each split adds a partial
-// tile written and read in fp32.  Costs are in k slices of a worker's MMAs.
+// [B, d] leave workers idle or in a thin last wave; each split adds partial tiles
+// written and read in fp32 and a kernel to sum them.  Costs in us as measured: a
+// k slice 0.33 (9 rows at d = 2492, V = 2769: 44 slices of one CTA 18 us, in splits
+// 7), 8 slices to fill the pipeline and drain a tile, 4 for the sum kernel and
+// 0.06 for each partial tile.
 struct Split {
   int64_t n, kb;  // splits, k slices of each
 };
@@ -1156,8 +1159,8 @@ Split plan_split(int64_t B, int64_t d, int64_t V) {
   for (int64_t want = 1; want <= 64 && want <= n_kb; ++want) {
     const int64_t kb = ceil_div(n_kb, want), n = ceil_div(n_kb, kb);
     const int64_t waves = ceil_div(tiles * n, workers);
-    const double partial_mb = n > 1 ? double(n * tiles) * (pair ? 2 : 1) * 0.131 : 0.0;
-    const double cost = double(waves * (kb + 8)) + (n > 1 ? 30.0 + partial_mb * 2.2 : 0.0);
+    const double sum = n > 1 ? 4.0 + 0.06 * double(n * tiles * (pair ? 2 : 1)) : 0.0;
+    const double cost = double(waves * (kb + 8)) * 0.33 + sum;
     if (cost < best_cost) {
       best_cost = cost;
       best = {n, kb};
