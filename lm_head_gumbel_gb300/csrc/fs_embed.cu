@@ -9,14 +9,13 @@
 // columns, and ids that cross runs are joined; other CTAs zero the rows that no
 // id names.
 //
-// Gradient, more ids, three kernels:
-//   sort_fill_kernel  a cluster of 8 CTAs sorts the pairs, stably; when the whole
-//                     table is written, the other CTAs meanwhile zero rows that
-//                     no id names
+// Gradient, more ids, three or four kernels:
+//   sort_kernel       a cluster of 8 CTAs sorts the pairs, stably
+//   zero_kernel       beside it, when the whole table is written: zeroes it
 //   run_sum_kernel    the sorted positions in runs: a warp sums one run over 256
 //                     columns, writes the ids that begin and end in the run, and
 //                     leaves a partial sum for those that cross into its
-//                     neighbours; then it zeroes its share of the rows left
+//                     neighbours
 //   run_join_kernel   the ids that cross runs, from their partial sums in order
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -195,7 +194,8 @@ constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kCluster = 8;
 constexpr int kMaxBits = 9;  // of a radix digit
 constexpr int kBins = 1 << kMaxBits;
-constexpr int kFillRows = 1 << 16;  // rows whose marks a CTA holds at once
+constexpr int kFillRows = 1 << 16;   // rows of a zeroing CTA, at most
+constexpr int kFillBytes = 1 << 18;  // and bytes, about
 constexpr int kSmallMax = 1024;      // ids of the one-kernel gradient
 
 struct SortParams {
@@ -208,7 +208,7 @@ struct SortParams {
   // When the whole table is written (else null):
   uint8_t* table;
   int64_t table_ld, row_bytes;
-  int64_t fill_rows;  // zero the unnamed ones of the first rows here
+  int32_t fill_rows;  // rows of a zeroing CTA
 };
 
 // An id as a row of the table, V where the table has no such row.
@@ -399,50 +399,72 @@ __device__ void sort_block(const SortParams& p, BlockSort& sm) {
   }
 }
 
-// A row's zeros by one warp: two bytes at a time up to a 16-byte boundary, 16 at
-// a time from there.
-__device__ __forceinline__ void zero_row(uint8_t* row, int64_t bytes, int lane) {
+// Zeros: two bytes at a time up to a 16-byte boundary, 16 at a time from there,
+// by `n` threads of which this is number i.
+__device__ __forceinline__ void zero_span(uint8_t* to, int64_t bytes, int i, int n) {
   const int64_t head =
-      min(int64_t((16u - uint32_t(reinterpret_cast<uintptr_t>(row) & 15u)) & 15u), bytes);
+      min(int64_t((16u - uint32_t(reinterpret_cast<uintptr_t>(to) & 15u)) & 15u), bytes);
   const int64_t n16 = (bytes - head) / 16, tail = head + n16 * 16;
-  for (int64_t i = lane * 2; i < head; i += 64) *reinterpret_cast<uint16_t*>(row + i) = 0;
-  for (int64_t i = lane; i < n16; i += 32)
-    reinterpret_cast<uint4*>(row + head)[i] = make_uint4(0u, 0u, 0u, 0u);
-  for (int64_t i = tail + lane * 2; i < bytes; i += 64) *reinterpret_cast<uint16_t*>(row + i) = 0;
+  for (int64_t k = i * 2; k < head; k += n * 2) *reinterpret_cast<uint16_t*>(to + k) = 0;
+#pragma unroll 4
+  for (int64_t k = i; k < n16; k += n)
+    reinterpret_cast<uint4*>(to + head)[k] = make_uint4(0u, 0u, 0u, 0u);
+  for (int64_t k = tail + i * 2; k < bytes; k += n * 2)
+    *reinterpret_cast<uint16_t*>(to + k) = 0;
 }
 
-// CTA `part` of `parts` zeroes its share of the first fill_rows rows, but those
-// that some id names: it marks them in shared memory (one pass over the ids),
-// then a warp zeroes a row.
-__device__ void fill_rows(const SortParams& p, int part, int parts) {
-  __shared__ uint32_t marks[kFillRows / 32];
-  const int64_t per = (p.fill_rows + parts - 1) / parts;
-  const int64_t r0 = int64_t(part) * per, r1 = min(r0 + per, p.fill_rows);
+// CTA `part` zeroes its fill_rows rows of the table (about 256 KB, in the order
+// the CTAs start: 7.6 TB/s; as few CTAs as SMs, each on rows far apart, wrote at
+// 4.9).  kMarked: all but those that some id names, found by one pass over the ids.
+template <bool kMarked>
+__device__ void fill_rows(const SortParams& p, int64_t part) {
+  const int64_t r0 = part * p.fill_rows;
+  if (r0 >= p.V) return;
+  const int rows = int(min(int64_t(p.fill_rows), p.V - r0));
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  for (int64_t b0 = r0; b0 < r1; b0 += kFillRows) {
-    const int rows = int(min(int64_t(kFillRows), r1 - b0));
-    __syncthreads();
+  uint8_t* first = p.table + r0 * p.table_ld;
+  __shared__ uint32_t marks[kMarked ? kFillRows / 32 : 1];
+  if (kMarked) {
     for (int i = threadIdx.x; i < (rows + 31) / 32; i += kSortThreads) marks[i] = 0u;
     __syncthreads();
-#pragma unroll 8
+    int any = 0;
     for (int i = threadIdx.x; i < p.N; i += kSortThreads) {
-      const int64_t r = int64_t(row_of(p, p.ids[i])) - b0;
-      if (r >= 0 && r < rows) atomicOr(&marks[r >> 5], 1u << (r & 31));
+      const int64_t r = int64_t(row_of(p, p.ids[i])) - r0;
+      if (r >= 0 && r < rows) {
+        atomicOr(&marks[r >> 5], 1u << (r & 31));
+        any = 1;
+      }
     }
-    __syncthreads();
-    for (int r = warp; r < rows; r += kSortWarps)
-      if (!((marks[r >> 5] >> (r & 31)) & 1u))
-        zero_row(p.table + (b0 + r) * p.table_ld, p.row_bytes, lane);
+    if (__syncthreads_or(any)) {
+      for (int r = warp; r < rows; r += kSortWarps)
+        if (!((marks[r >> 5] >> (r & 31)) & 1u))
+          zero_span(first + r * p.table_ld, p.row_bytes, lane, 32);
+      return;
+    }
   }
+  if (p.table_ld == p.row_bytes)
+    zero_span(first, rows * p.row_bytes, threadIdx.x, kSortThreads);
+  else
+    for (int r = warp; r < rows; r += kSortWarps)
+      zero_span(first + r * p.table_ld, p.row_bytes, lane, 32);
 }
 
+// One cluster.  Its dependent may start at once: the sums wait for its end, and
+// the zeroing needs nothing of it.
 __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kSortThreads)
-    sort_fill_kernel(const SortParams p) {
-  if (blockIdx.x < kCluster)
-    sort_cluster(p, ptx::cluster_ctarank());
-  else
-    fill_rows(p, int(blockIdx.x) - kCluster, int(gridDim.x) - kCluster);
+    sort_kernel(const SortParams p) {
   ptx::grid_launch_dependents();
+  sort_cluster(p, ptx::cluster_ctarank());
+}
+
+// Zeroes the table while the ids are sorted, as a programmatic dependent of the
+// sort: it may start once the sort has (so everything before the sort is done)
+// and reads nothing.  Its last CTA ends after the sort, so what waits for this
+// kernel waits for both.  (In one launch with the sort, as clusters of 8, the
+// zeroing took 242 us instead of 170 at V = 151936, d = 4096.)
+__global__ void __launch_bounds__(kSortThreads, 2) zero_kernel(const SortParams p) {
+  fill_rows<false>(p, int64_t(blockIdx.x));
+  if (blockIdx.x == gridDim.x - 1) ptx::grid_dependency_wait();
 }
 
 // ---------------------------------------------------------------------------
@@ -464,7 +486,6 @@ struct RunParams {
   float scale;
   float* partial;  // [n_runs][2][ldp]: sums of the ids crossing a run's start, end
   int64_t ldp;
-  int64_t zero_from;  // zero the unnamed rows from here on (V: none)
 };
 
 __device__ __forceinline__ float* partial_at(const RunParams& p, int run, int end, int col) {
@@ -584,38 +605,14 @@ __global__ void __launch_bounds__(kRunThreads) run_sum_kernel(const RunParams p)
   const int lane = threadIdx.x & 31;
   const int64_t item = (int64_t(blockIdx.x) * kRunThreads + threadIdx.x) >> 5;
   const int run = int(item / p.cols.segments);
-  if (run < p.n_runs) {
-    const int seg = int(item - int64_t(run) * p.cols.segments);
-    if (seg < p.cols.vec_segments) {
-      const int col = seg * 256 + lane * 8;
-      sum_run<TY, TO, 8, kAdd>(p, run, col, col < p.cols.vec, lane);
-    } else {
-      const int col = p.cols.vec + (seg - p.cols.vec_segments) * 32 + lane;
-      sum_run<TY, TO, 1, kAdd>(p, run, col, col < p.cols.d, lane);
-    }
-  }
-  // Then the warp's part of the rows still to zero, 8 neighbouring rows at a
-  // time: lanes 0-7 look theirs up among the sorted rows.
-  const int64_t n_warps = int64_t(gridDim.x) * kRunWarps;
-  for (int64_t r0 = p.zero_from + item * 8; r0 < p.V; r0 += n_warps * 8) {
-    bool unnamed = false;
-    if (lane < 8 && r0 + lane < p.V) {
-      const uint32_t row = uint32_t(r0 + lane);
-      int lo = 0, hi = p.N;  // the first sorted position not below row
-      while (lo < hi) {
-        const int mid = lo + (hi - lo) / 2;
-        if (p.key[mid] < row)
-          lo = mid + 1;
-        else
-          hi = mid;
-      }
-      unnamed = lo == p.N || p.key[lo] != row;
-    }
-    uint32_t todo = __ballot_sync(0xFFFFFFFFu, unnamed);
-    for (; todo != 0u; todo &= todo - 1u)
-      zero_row(reinterpret_cast<uint8_t*>(
-                   table_at<TO>(p, uint32_t(r0 + __ffs(todo) - 1), 0)),
-               int64_t(p.cols.d) * int64_t(sizeof(TO)), lane);
+  if (run >= p.n_runs) return;
+  const int seg = int(item - int64_t(run) * p.cols.segments);
+  if (seg < p.cols.vec_segments) {
+    const int col = seg * 256 + lane * 8;
+    sum_run<TY, TO, 8, kAdd>(p, run, col, col < p.cols.vec, lane);
+  } else {
+    const int col = p.cols.vec + (seg - p.cols.vec_segments) * 32 + lane;
+    sum_run<TY, TO, 1, kAdd>(p, run, col, col < p.cols.d, lane);
   }
 }
 
@@ -685,7 +682,7 @@ __global__ void __launch_bounds__(kSortThreads)
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int seg = blockIdx.x;
   if (seg >= rp.cols.segments) {
-    fill_rows(sp, seg - rp.cols.segments, int(gridDim.x) - rp.cols.segments);
+    fill_rows<true>(sp, int64_t(seg) - rp.cols.segments);
     return;
   }
   sort_block(sp, sm.sort);
@@ -889,7 +886,11 @@ extern "C" fs_status fs_embed_grad(const int64_t* ids, int64_t N, const void* dY
     sp.table = static_cast<uint8_t*>(dE);
     sp.table_ld = lde * element(e_dtype);
     sp.row_bytes = d * element(e_dtype);
+    sp.fill_rows =
+        int32_t(std::min<int64_t>(kFillRows, std::max<int64_t>(1, kFillBytes / sp.row_bytes)));
   }
+  const int64_t fill = accumulate ? 0 : ceil_div(V, sp.fill_rows);  // CTAs that zero rows
+  if (fill > INT_MAX - cols.segments - 2 * kCluster) return FS_ERR_INVALID_ARG;
   RunParams rp = {};
   rp.N = int32_t(N);
   rp.V = int32_t(V);
@@ -901,16 +902,9 @@ extern "C" fs_status fs_embed_grad(const int64_t* ids, int64_t N, const void* dY
   rp.dE = dE;
   rp.lde = lde;
   rp.scale = scale;
-  rp.zero_from = V;
   cudaError_t err;
 
   if (small) {
-    // A CTA to zero every 128 KB, at most two an SM.
-    int64_t fill = 0;
-    if (!accumulate) {
-      sp.fill_rows = V;
-      fill = std::min<int64_t>(2 * 152, ceil_div(V * sp.row_bytes, 131072));
-    }
     void* args[] = {&sp, &rp};
     err = launch(accumulate ? small_kernel<true>(y_dtype, e_dtype)
                             : small_kernel<false>(y_dtype, e_dtype),
@@ -928,29 +922,23 @@ extern "C" fs_status fs_embed_grad(const int64_t* ids, int64_t N, const void* dY
     sp.key[i] = reinterpret_cast<uint32_t*>(ws + one * i);
     sp.pos[i] = reinterpret_cast<uint32_t*>(ws + one * (2 + i));
   }
-  if (!accumulate) {
-    // As many rows as the other CTAs can zero while the ids are sorted; the rest
-    // are zeroed beside the sums, whose reads they do not slow.
-    const int64_t us = 8 + N / 1024;
-    sp.fill_rows = std::min(V, ceil_div(us * 4000000, sp.row_bytes));
-    rp.zero_from = sp.fill_rows;
-  }
   rp.key = sp.key[sp.passes & 1];
   rp.pos = sp.pos[sp.passes & 1];
   rp.partial = reinterpret_cast<float*>(ws + 4 * one);
   rp.ldp = partial_ld(d);
   void* sort_args[] = {&sp};
-  // One cluster sorts; 19 more (152 CTAs) zero rows.
-  err = launch(reinterpret_cast<const void*>(&sort_fill_kernel),
-               accumulate ? kCluster : 20 * kCluster, kSortThreads, 0, false, sort_args, stream);
+  err = launch(reinterpret_cast<const void*>(&sort_kernel), kCluster, kSortThreads, 0, false,
+               sort_args, stream);
+  // All rows are zeroed: those that ids name are written twice, which is less
+  // than telling them apart costs (every zeroing CTA would read all ids).
+  if (err == cudaSuccess && !accumulate)
+    err = launch(reinterpret_cast<const void*>(&zero_kernel), fill, kSortThreads, 0, true,
+                 sort_args, stream);
   const void* sum = accumulate ? sum_kernel<true>(y_dtype, e_dtype)
                                : sum_kernel<false>(y_dtype, e_dtype);
   const void* join = accumulate ? join_kernel_of<true>(e_dtype) : join_kernel_of<false>(e_dtype);
   void* args[] = {&rp};
-  // With rows to zero, warps for them too: 8 blocks an SM.
-  if (err == cudaSuccess)
-    err = launch(sum, accumulate ? blocks : std::max<int64_t>(blocks, 8 * 152), kRunThreads, 0,
-                 true, args, stream);
+  if (err == cudaSuccess) err = launch(sum, blocks, kRunThreads, 0, true, args, stream);
   if (err == cudaSuccess && n_runs > 1)
     err = launch(join, blocks, kRunThreads, 0, true, args, stream);
   if (err != cudaSuccess) {
