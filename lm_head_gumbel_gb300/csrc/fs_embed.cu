@@ -245,12 +245,16 @@ __device__ __forceinline__ uint32_t load_cluster(const uint32_t* p, uint32_t ran
 // elements in order, each element ranked among the equal digits of its warp
 // (by votes), of the tile's earlier warps (a scan over the warps' counts) and of
 // earlier tiles (the running base).
-__device__ void sort_cluster(const SortParams& p, uint32_t rank) {
-  __shared__ uint32_t hist[kBins];          // this CTA's digit counts
-  __shared__ uint32_t base[kBins];          // next place of each digit
-  __shared__ uint32_t scan[kSortWarps];
-  __shared__ __align__(16) uint16_t wc[kSortWarps][kBins];  // a tile's counts per warp, then
-                                                            // offsets
+struct ClusterSort {
+  uint32_t hist[kBins];          // this CTA's digit counts
+  uint32_t base[kBins];          // next place of each digit
+  uint32_t scan[kSortWarps];
+  uint16_t wc[kSortWarps][kBins];  // a tile's counts per warp, then offsets
+};
+__device__ void sort_cluster(const SortParams& p, uint32_t rank, ClusterSort& sm) {
+  auto &hist = sm.hist, &base = sm.base;
+  auto& scan = sm.scan;
+  auto& wc = sm.wc;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = (p.N + kCluster - 1) / kCluster;
   const int e0 = min(int(rank) * per, p.N), e1 = min(e0 + per, p.N);
@@ -335,6 +339,94 @@ __device__ void sort_cluster(const SortParams& p, uint32_t rank) {
     // all have been read.
     __threadfence();
     ptx::cluster_sync();
+  }
+}
+
+__device__ __forceinline__ void store_cluster(uint32_t* p, uint32_t rank, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(ptx::cluster_addr(p, rank)), "r"(v)
+               : "memory");
+}
+
+// The same for up to 1024 pairs a CTA, which stay in registers and shared memory:
+// a pass ranks the CTA's pairs, sends its digit counts to every CTA, and then each
+// pair to the CTA that holds its place.  (4099 ids: 4 us less than through L2.)
+struct SmallClusterSort {
+  uint32_t hist[kCluster][kBins];  // every CTA's digit counts
+  uint32_t base[kBins];            // first place of this CTA's pairs of a digit
+  uint32_t scan[kSortWarps];
+  uint32_t in_key[kSortThreads], in_pos[kSortThreads];  // this CTA's pairs
+  uint16_t wc[kSortWarps][kBins];  // counts per warp, then offsets
+};
+__device__ void sort_cluster_small(const SortParams& p, uint32_t rank, SmallClusterSort& sm) {
+  auto& hist = sm.hist;
+  auto& base = sm.base;
+  auto& scan = sm.scan;
+  auto &in_key = sm.in_key, &in_pos = sm.in_pos;
+  auto& wc = sm.wc;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int per = (p.N + kCluster - 1) / kCluster;
+  const int e0 = min(int(rank) * per, p.N), n = min(per, p.N - e0);
+  const int bins = 1 << p.bits;
+  const int warps = (n + 31) / 32;
+  const bool has = tid < n;
+  uint32_t key = has ? row_of(p, p.ids[e0 + tid]) : 0u;
+  uint32_t pos = uint32_t(e0 + tid);
+  for (int pass = 0; pass < p.passes; ++pass) {
+    if (warp < warps)
+      for (int i = lane; i < bins / 2; i += 32) reinterpret_cast<uint32_t*>(wc[warp])[i] = 0u;
+    __syncwarp();
+    const uint32_t digit = (key >> (pass * p.bits)) & (bins - 1);
+    const uint32_t peers = same_digit<kMaxBits>(digit, has);
+    const uint32_t earlier = __popc(peers & ((1u << lane) - 1u));
+    if (has && earlier == 0u) wc[warp][digit] = uint16_t(__popc(peers));
+    __syncthreads();
+    if (tid < bins) {
+      uint32_t run = 0u;
+#pragma unroll 8
+      for (int w = 0; w < warps; ++w) {
+        const uint32_t c = wc[w][tid];
+        wc[w][tid] = uint16_t(run);
+        run += c;
+      }
+#pragma unroll
+      for (int c = 0; c < kCluster; ++c) store_cluster(&hist[rank][tid], uint32_t(c), run);
+    }
+    ptx::cluster_sync();  // every CTA's counts have arrived, and its pairs have been read
+    uint32_t total = 0u, before = 0u;
+    if (tid < bins) {
+#pragma unroll
+      for (int c = 0; c < kCluster; ++c) {
+        const uint32_t h = hist[c][tid];
+        total += h;
+        if (c < int(rank)) before += h;
+      }
+    }
+    uint32_t incl = total;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const uint32_t o = __shfl_up_sync(0xFFFFFFFFu, incl, off);
+      if (lane >= off) incl += o;
+    }
+    if (lane == 31) scan[warp] = incl;
+    __syncthreads();
+    const uint32_t prev = __reduce_add_sync(0xFFFFFFFFu, lane < warp ? scan[lane] : 0u);
+    if (tid < bins) base[tid] = prev + incl - total + before;
+    __syncthreads();
+    if (has) {
+      const uint32_t to = base[digit] + wc[warp][digit] + earlier;
+      const uint32_t c = to / uint32_t(per);
+      store_cluster(&in_key[to - c * per], c, key);
+      store_cluster(&in_pos[to - c * per], c, pos);
+    }
+    ptx::cluster_sync();  // every pair has arrived; no counts change before all were read
+    if (has) {
+      key = in_key[tid];
+      pos = in_pos[tid];
+    }
+  }
+  if (has) {
+    p.key[p.passes & 1][e0 + tid] = key;
+    p.pos[p.passes & 1][e0 + tid] = pos;
   }
 }
 
@@ -449,12 +541,18 @@ __device__ void fill_rows(const SortParams& p, int64_t part) {
       zero_span(first + r * p.table_ld, p.row_bytes, lane, 32);
 }
 
+constexpr size_t kSortSmem = std::max(sizeof(ClusterSort), sizeof(SmallClusterSort));
+
 // One cluster.  Its dependent may start at once: the sums wait for its end, and
 // the zeroing needs nothing of it.
 __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kSortThreads)
     sort_kernel(const SortParams p) {
+  extern __shared__ __align__(16) uint8_t dyn[];
   ptx::grid_launch_dependents();
-  sort_cluster(p, ptx::cluster_ctarank());
+  if (p.N <= kCluster * kSortThreads)
+    sort_cluster_small(p, ptx::cluster_ctarank(), *reinterpret_cast<SmallClusterSort*>(dyn));
+  else
+    sort_cluster(p, ptx::cluster_ctarank(), *reinterpret_cast<ClusterSort*>(dyn));
 }
 
 // Zeroes the table while the ids are sorted, as a programmatic dependent of the
@@ -477,7 +575,7 @@ constexpr int kAhead = 8;  // rows in flight per warp (16 at 2 columns a lane: n
 struct RunParams {
   const uint32_t* key;  // sorted rows of the table, V at the end for dropped ids
   const uint32_t* pos;
-  int32_t N, V, run, n_runs;  // sorted positions of a run (a multiple of 32), runs
+  int32_t N, V, run, n_runs;  // sorted positions of a run (16 or a multiple of 32), runs
   Columns cols;
   const void* dY;
   int64_t ldy;
@@ -726,6 +824,12 @@ fs_status device_check() {
       return FS_ERR_CUDA;
     }
     g_status[dev] = major == 10 && minor == 3 ? FS_OK : FS_ERR_UNSUPPORTED;
+    if (g_status[dev] == FS_OK &&
+        cudaFuncSetAttribute(sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             int(kSortSmem)) != cudaSuccess) {
+      cudaGetLastError();
+      g_status[dev] = FS_ERR_CUDA;
+    }
     g_known[dev] = true;
   }
   return g_status[dev];
@@ -799,9 +903,9 @@ namespace fs {
 namespace embed {
 namespace {
 
-// Sorted positions of a run: long ones leave fewer partial sums to join, short
-// ones more warps.
-int64_t run_length(int64_t N) { return N <= 8192 ? 32 : 64; }
+// Sorted positions of a run (32 in the one-kernel gradient): long ones leave fewer
+// partial sums to join, short ones more warps.
+int64_t run_length(int64_t N) { return N <= kSmallMax ? 32 : N <= 8192 ? 16 : 64; }
 
 template <bool kAdd>
 const void* small_kernel(int y_dtype, int e_dtype) {
@@ -927,8 +1031,8 @@ extern "C" fs_status fs_embed_grad(const int64_t* ids, int64_t N, const void* dY
   rp.partial = reinterpret_cast<float*>(ws + 4 * one);
   rp.ldp = partial_ld(d);
   void* sort_args[] = {&sp};
-  err = launch(reinterpret_cast<const void*>(&sort_kernel), kCluster, kSortThreads, 0, false,
-               sort_args, stream);
+  err = launch(reinterpret_cast<const void*>(&sort_kernel), kCluster, kSortThreads, kSortSmem,
+               false, sort_args, stream);
   // All rows are zeroed: those that ids name are written twice, which is less
   // than telling them apart costs (every zeroing CTA would read all ids).
   if (err == cudaSuccess && !accumulate)
