@@ -250,3 +250,48 @@ def test_binding_refusals():
     for call in bad:
         with pytest.raises(fs.FsError):
             call()
+
+
+# --------------------------------------------------------------------------- sizes at which the work is cut differently
+@pytest.mark.parametrize("ty,to", COMBOS)
+@pytest.mark.parametrize("N,V,d", [(1023, 3000, 100), (1024, 3000, 65), (1025, 3000, 100),
+                                   (4099, 70000, 40), (8192, 300, 136), (8193, 300, 136),
+                                   (33000, 40000, 24)])
+def test_gradient_of_every_path(ty, to, N, V, d):
+    """One kernel, the cluster's shared memory, the cluster through L2; all rows
+    written or some added to; hot ids over several runs."""
+    dY, _ = matrix(N, d, ty, ld=(d + 7) // 8 * 8, seed=N)
+    for kind in ("ragged", "few"):
+        ids = some_ids(kind, N, V, seed=N)
+        check_gradient(ids, dY, V, scale=0.5, out_dtype=to)
+        old, _ = matrix(V, d, to, ld=(d + 7) // 8 * 8, seed=3)
+        check_gradient(ids, dY, V, scale=0.5, out=old, accumulate=True)
+
+
+def test_dense_gradient_in_a_graph_on_a_side_stream():
+    """The zeroing runs beside the sort; what follows on the stream sees both done."""
+    for N in (700, 5000, 20000):
+        ids = some_ids("ragged", N, 30000, seed=N)
+        dY, _ = matrix(N, 64, torch.bfloat16, seed=N)
+        want = fs.fs_embed_grad(ids, dY, 30000)
+        ws = torch.empty(fs.fs_embed_grad_workspace_size(N, 64), dtype=torch.uint8, device="cuda")
+        out = torch.empty_like(want)
+        copy = torch.empty_like(want)
+        torch.cuda.synchronize()
+        side = torch.cuda.Stream()
+        with torch.cuda.stream(side):
+            for _ in range(20):
+                out.fill_(7.0)
+                fs.fs_embed_grad(ids, dY, 30000, out=out, workspace=ws)
+                copy.copy_(out)
+                assert torch.equal(copy, want)
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph, stream=side):
+                out.fill_(7.0)
+                fs.fs_embed_grad(ids, dY, 30000, out=out, workspace=ws)
+                copy.copy_(out)
+        for _ in range(20):
+            copy.zero_()
+            graph.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(copy, want)

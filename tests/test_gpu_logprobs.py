@@ -412,3 +412,54 @@ def test_binding_refusals():
     for call in bad:
         with pytest.raises(fs.FsError):
             call()
+
+
+# --------------------------------------------------------------------------- sizes at which the work is cut differently
+@pytest.mark.parametrize("B,V", [(3, 9728), (3, 9729), (70, 19456), (70, 19457), (128, 38912),
+                                 (5, 39000), (129, 40000)])
+@pytest.mark.parametrize("K", [0, 5])
+def test_unit_widths(B, V, K):
+    """Units of 64, 128 and 256 ids, one per CTA and more; ragged k slices in a stage."""
+    check_forward(problem(B, 200, V, T="rows", mask_frac=0.02, seed=V + B), K)
+
+
+@pytest.mark.parametrize("K", [8, 12, 13, 20])
+def test_more_list_capacities(K):
+    check_forward(problem(6, 128, 45000, T=0.9, seed=60 + K), K)
+    check_forward(problem(150, 64, 5000, T=0.9, seed=61 + K), K)
+
+
+@pytest.mark.parametrize("B", [127, 128, 129, 256, 257, 1280, 1281, 1537])
+def test_rows_per_launch(B):
+    check_forward(problem(B, 32, 300, T="rows", seed=B), 3)
+
+
+@pytest.mark.parametrize("B,d,V", [(9, 2492, 300), (2, 8, 5000), (260, 40, 3000), (130, 520, 129),
+                                   (16, 72, 19457)])
+def test_gradient_splits(B, d, V):
+    """dH with and without splits, singles and pairs, narrow and wide units."""
+    p = problem(B, d, V, T="rows", mask_frac=0.02, seed=B + d)
+    check_gradient(p, *upstream(B, True, V))
+
+
+def test_log_probabilities_are_at_most_zero():
+    """Rows whose mass is on one token, by 20 to 200 units of logit."""
+    p = problem(64, 64, 3000, seed=70)
+    p["W"][:64] = (p["H"] * torch.linspace(0.3, 3.0, 64, device="cuda").unsqueeze(1)).bfloat16()
+    p["tokens"][:] = torch.arange(64, device="cuda")
+    r, _ = check_forward(p, 4)
+    assert bool((r.logp <= 0).all()) and bool((r.topk_logp <= 0).all())
+    assert bool((r.logp[-1] > -1e-6).all())
+
+
+def test_few_rows_at_low_temperature():
+    """What the accumulator's truncation would show in: one row, a long k, T = 0.5.
+    The bound is fp32's own for sums of this length, not vocab_ref's (16 products
+    cut off at a time): 4 u sqrt(d/16) of the logits' size, and 4 u of lse's."""
+    p = problem(3, 4096, 20000, T=0.5, seed=71)
+    r = fs.fs_logprobs(p["H"], p["W"], p["tokens"], 20, temperature=p["temperature"])
+    w = ref.forward(p["H"], p["W"], p["tokens"], 20, p["temperature"])
+    size = float((w["topk_logp"] + w["lse"].unsqueeze(1)).abs().max())
+    bound = 4 * ref.U * math.sqrt(4096 / 16) * size + 4 * ref.U * float(w["lse"].abs().max())
+    near(r.lse, w["lse"], bound, "lse")
+    near(r.topk_logp, w["topk_logp"], bound + 2 * ref.U * w["topk_logp"].abs(), "topk_logp")
