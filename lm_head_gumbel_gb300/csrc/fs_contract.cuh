@@ -135,7 +135,8 @@ struct Shape {
   int32_t n_mt, n_nt;      // tiles along M (128 rows, 256 for CTA pairs) and N (Epi::kN)
   int32_t n_units;         // n_mt * n_nt * number of k splits
   int32_t n_kb;            // 64-wide k slices in all
-  int32_t kb_per_split;    // k slices of one unit (the last split may have fewer)
+  int32_t n_splits;        // split i takes slices i, i + n_splits, ... of them
+  uint32_t k_descending;   // counted from the last slice: what the kernel before read last is in L2
   int32_t m_rows, n_cols;  // extents of M and N
   uint32_t m_fastest;      // unit order: M tiles (else N tiles) innermost, k splits outermost
   uint32_t a_box_rows;     // rows of A's box when k is contiguous (a multiple of 8)
@@ -152,7 +153,8 @@ struct Shape {
 };
 
 struct Unit {
-  int mt, nt, split, kb0, n_kb;
+  int mt, nt, split;
+  int kb0, n_kb;  // first k slice, number of them
 };
 
 // A worker's units, every n_workers-th of the list, without a division each.
@@ -176,8 +178,8 @@ struct Units {
     r.mt = s.m_fastest ? inner : outer;
     r.nt = s.m_fastest ? outer : inner;
     r.split = split;
-    r.kb0 = split * s.kb_per_split;
-    r.n_kb = min(s.kb_per_split, s.n_kb - r.kb0);
+    r.kb0 = s.k_descending ? s.n_kb - 1 - split : split;
+    r.n_kb = (s.n_kb - split + s.n_splits - 1) / s.n_splits;
     return r;
   }
   __device__ __forceinline__ void next(const Shape& s) {
@@ -366,11 +368,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     // The first ring fill's A copies, held back until the kernel before is done.
     bool deferring = s.pdl != 0;
     int n_held = 0, held_kb[kMaxStages], held_n[kMaxStages], held_mt[kMaxStages];
+    const int kb_step = s.k_descending ? -s.n_splits : s.n_splits;
     auto release = [&]() {
       ptx::grid_dependency_wait();
       if (issuer)
         for (int h = 0; h < n_held; ++h)
-          for (int i = 0; i < held_n[h]; ++i) load_a(uint32_t(h), i, held_kb[h] + i, held_mt[h]);
+          for (int i = 0; i < held_n[h]; ++i) load_a(uint32_t(h), i, held_kb[h] + i * kb_step, held_mt[h]);
       deferring = false;
     };
     for (Units it(s, worker, n_workers); ok && it.more(s); it.next(s)) {
@@ -388,12 +391,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int i = 0; i < kS; ++i) {
             if (i >= n) break;
-            load_b(stage, i, t.kb0 + k + i, t.nt);
-            if (!deferring) load_a(stage, i, t.kb0 + k + i, t.mt);
+            const int kb = t.kb0 + (k + i) * kb_step;
+            load_b(stage, i, kb, t.nt);
+            if (!deferring) load_a(stage, i, kb, t.mt);
           }
         }
         if (deferring) {  // the first fill: stage n_held
-          held_kb[n_held] = t.kb0 + k;
+          held_kb[n_held] = t.kb0 + k * kb_step;
           held_n[n_held] = n;
           held_mt[n_held++] = t.mt;
         }

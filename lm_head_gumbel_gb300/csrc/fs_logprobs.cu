@@ -1071,7 +1071,8 @@ fs_status run_scores(const fs_logprobs_args* a, const Device& dev, cudaStream_t 
     s.n_mt = n_mt;
     s.n_nt = n_nt;
     s.n_units = n_mt * n_nt;
-    s.n_kb = s.kb_per_split = int32_t(ceil_div(a->d, kBK));
+    s.n_kb = int32_t(ceil_div(a->d, kBK));
+    s.n_splits = 1;
     s.m_rows = int32_t(rows);
     s.n_cols = int32_t(a->V);
     s.m_fastest = 1;
@@ -1146,15 +1147,12 @@ fs_status run_scores(const fs_logprobs_args* a, const Device& dev, cudaStream_t 
 // k slice 0.33 (9 rows at d = 2492, V = 2769: 44 slices of one CTA 18 us, in splits
 // 7), 8 slices to fill the pipeline and drain a tile, 4 for the sum kernel and
 // 0.06 for each partial tile.
-struct Split {
-  int64_t n, kb;  // splits, k slices of each
-};
-Split plan_split(int64_t B, int64_t d, int64_t V) {
+int64_t plan_split(int64_t B, int64_t d, int64_t V) {
   const bool pair = B > kBM;
   const int64_t workers = pair ? kPlanSms / 2 : kPlanSms;
   const int64_t tiles = ceil_div(B, pair ? 2 * kBM : kBM) * ceil_div(d, kBN);
   const int64_t n_kb = ceil_div(V, kBK);
-  Split best = {1, n_kb};
+  int64_t best = 1;
   double best_cost = 1e300;
   for (int64_t want = 1; want <= 64 && want <= n_kb; ++want) {
     const int64_t kb = ceil_div(n_kb, want), n = ceil_div(n_kb, kb);
@@ -1163,7 +1161,7 @@ Split plan_split(int64_t B, int64_t d, int64_t V) {
     const double cost = double(waves * (kb + 8)) * 0.33 + sum;
     if (cost < best_cost) {
       best_cost = cost;
-      best = {n, kb};
+      best = n;
     }
   }
   return best;
@@ -1174,10 +1172,10 @@ int64_t store_cols(int64_t d) { return d < 8 ? 8 : d & ~int64_t(7); }
 
 size_t g_bytes(int64_t B, int64_t V) { return round256(size_t(B) * size_t((V + 7) / 8 * 8) * 2u); }
 size_t partial_bytes(int64_t B, int64_t d, int64_t V) {
-  const Split sp = plan_split(B, d, V);
-  if (sp.n == 1) return 0;
+  const int64_t n = plan_split(B, d, V);
+  if (n == 1) return 0;
   const int64_t ctas = B > kBM ? 2 : 1;
-  return size_t(sp.n * ceil_div(B, kBM * ctas) * ceil_div(d, kBN) * ctas) * kBM * kBN * 4u;
+  return size_t(n * ceil_div(B, kBM * ctas) * ceil_div(d, kBN) * ctas) * kBM * kBN * 4u;
 }
 
 }  // namespace
@@ -1288,7 +1286,8 @@ extern "C" fs_status fs_logprobs_grad(const fs_logprobs_grad_args* a, void* stre
     s.n_mt = int32_t(ceil_div(B, kBM * ctas));
     s.n_nt = int32_t(ceil_div(V, cols));
     s.n_units = s.n_mt * s.n_nt;
-    s.n_kb = s.kb_per_split = int32_t(ceil_div(d, kBK));
+    s.n_kb = int32_t(ceil_div(d, kBK));
+    s.n_splits = 1;
     s.m_rows = int32_t(B);
     s.n_cols = int32_t(V);
     s.m_fastest = 1;
@@ -1320,7 +1319,7 @@ extern "C" fs_status fs_logprobs_grad(const fs_logprobs_grad_args* a, void* stre
 
   // dH = G W.
   if (a->out_dH) {
-    const Split sp = plan_split(B, d, V);
+    const int64_t n_splits = plan_split(B, d, V);
     const int box_rows = pair ? kBM : int(std::min<int64_t>(kBM, (B + 7) / 8 * 8));
     CUtensorMap mg, mw, mo;
     if (!encode(dev, &mg, G, V, B, ldg, box_rows) || !encode(dev, &mw, a->W, d, V, a->ldw, kBK) ||
@@ -1329,16 +1328,17 @@ extern "C" fs_status fs_logprobs_grad(const fs_logprobs_grad_args* a, void* stre
     Shape s = {};
     s.n_mt = int32_t(ceil_div(B, kBM * ctas));
     s.n_nt = int32_t(ceil_div(d, kBN));
-    s.n_units = int32_t(s.n_mt * s.n_nt * sp.n);
+    s.n_units = int32_t(s.n_mt * s.n_nt * n_splits);
     s.n_kb = int32_t(ceil_div(V, kBK));
-    s.kb_per_split = int32_t(sp.kb);
+    s.n_splits = int32_t(n_splits);
+    s.k_descending = 1;  // from the ids whose rows of W and columns of G came last
     s.m_rows = int32_t(B);
     s.n_cols = int32_t(d);
     s.m_fastest = 1;
     s.a_box_rows = uint32_t(box_rows);
     s.pdl = s.early_trigger = 1;  // W streams while the kernel before ends
     const int n = balanced(s.n_units, workers);
-    if (sp.n == 1) {
+    if (n_splits == 1) {
       const StoreEpi::Params ep = {static_cast<__nv_bfloat16*>(a->out_dH), a->lddh,
                                    int32_t(d & ~int64_t(7))};
       st = pair ? launch<StoreEpi, true, false, true>(dev, mg, mw, mo, s, ep, n, true, stream)
@@ -1361,7 +1361,7 @@ extern "C" fs_status fs_logprobs_grad(const fs_logprobs_grad_args* a, void* stre
       cfg.attrs = &attr;
       cfg.numAttrs = 1;
       if (cudaLaunchKernelEx(&cfg, sum_splits_kernel, static_cast<const float4*>(ep.partial),
-                             int32_t(sp.n), s.n_mt * s.n_nt, s.n_nt, int32_t(ctas), int32_t(B),
+                             int32_t(n_splits), s.n_mt * s.n_nt, s.n_nt, int32_t(ctas), int32_t(B),
                              int32_t(d), static_cast<__nv_bfloat16*>(a->out_dH),
                              a->lddh) != cudaSuccess) {
         cudaGetLastError();
@@ -1382,7 +1382,8 @@ extern "C" fs_status fs_logprobs_grad(const fs_logprobs_grad_args* a, void* stre
     s.n_mt = int32_t(ceil_div(V, wpair ? 2 * kBM : kBM));
     s.n_nt = int32_t(ceil_div(d, kBN));
     s.n_units = s.n_mt * s.n_nt;
-    s.n_kb = s.kb_per_split = int32_t(ceil_div(B, kBK));
+    s.n_kb = int32_t(ceil_div(B, kBK));
+    s.n_splits = 1;
     s.m_rows = int32_t(V);
     s.n_cols = int32_t(d);
     s.m_fastest = 0;
