@@ -87,14 +87,16 @@ fs_status fs_logprobs(const fs_logprobs_args *args, void *stream);
  *                      - grad_entropy[b] p (log p + entropy[b])),  0 if masked
  *   dH[b,:] = sum_v G[b,v] W[v,:]        dW[v,:] = sum_b G[b,v] H[b,:]
  * The logits are computed again; G goes through the workspace in bf16 (each
- * term rounded once, relative error at most 2^-8, sums in fp32) and dH, dW are
- * rounded to bf16 once.  lse and entropy are fs_logprobs' outputs; on a shard of
+ * term rounded once, relative error at most 2^-8, sums in fp32), but for G at the
+ * row's token, most of a row's gradient, what that rounding takes is kept in fp32
+ * and added to the sums; dH, dW are rounded to bf16 once.  lse and entropy are fs_logprobs' outputs; on a shard of
  * the vocabulary they are those of the whole vocabulary, and the shards' dH add
  * up to the whole one.  A token below 0 or cleared by the mask (logp 0 or -inf)
  * gets no gradient from logp; for a token outside [vocab_offset, vocab_offset +
  * V) the one-hot term lies in another shard and only the p term is added here.
  * A fully masked row (lse -inf) gets no gradient.
- * W's rows must be finite where dH is asked for (0 times NaN is NaN).
+ * H and W must be finite, masked ids' rows of W and fully masked rows of H too:
+ * where G is 0 they are multiplied by 0, and 0 times NaN is NaN.
  */
 typedef struct fs_logprobs_grad_args {
   const void *H;

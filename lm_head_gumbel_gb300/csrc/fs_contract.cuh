@@ -252,10 +252,12 @@ struct TileAt {
 };
 
 // kAmn / kBmn: A's M (B's N) dimension is the contiguous one in memory.
-// finish() gets the thread's M row in its worker's first unit.
+// before() runs ahead of the wait for a unit's accumulator and gets the first row of
+// the warp's next unit too; start() and finish() get the thread's M row in its
+// worker's first unit.
 // Epi: struct with Params, State, kN (columns of a unit: 256, or 64 / 128 where
 // 256 would leave CTAs without units), kStaged (uses bf16 boxes in shared memory
-// and tmap_d), and static device functions start / tile / finish.
+// and tmap_d), and static device functions start / before / tile / finish.
 template <class Epi, bool kPair, bool kAmn, bool kBmn>
 __global__ void __launch_bounds__(kThreads, 1)
     contract_kernel(const __grid_constant__ CUtensorMap tmap_a,
@@ -501,9 +503,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint8_t* box = staging + e * kBoxBytes;
     uint32_t acc = 0, acc_phase = 0;
     typename Epi::State st;
-    Epi::start(ep, st);
     Units it(s, worker, n_workers);
     const int first_row = (it.get(s).mt * kCtas + rank) * kBM + quad * 32 + lane;
+    Epi::start(ep, st, first_row, lane, s);
     for (; it.more(s); it.next(s)) {
       TileAt at;
       at.unit = it.get(s);
@@ -513,6 +515,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       at.row0 = (at.unit.mt * kCtas + rank) * kBM + quad * 32;
       at.col0 = at.unit.nt * kN + half * (kN / 2);
       at.taddr = tmem_base + (uint32_t(quad * 32) << 16) + acc * kN + uint32_t(half * (kN / 2));
+      Units ahead = it;
+      ahead.next(s);
+      Epi::before(ep, st, at, (ahead.get(s).mt * kCtas + rank) * kBM + quad * 32, lane, s);
       int ok = 0;
       if (lane == 0) ok = waiter.wait(&tfull_bar[acc], acc_phase) ? 1 : 0;
       ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
@@ -598,6 +603,56 @@ __device__ __forceinline__ void box_end(uint8_t* box, const void* tmap, int lane
 // rows: 2 slices): its steps -- load, wait for the boxes, write them, fence,
 // store -- depend on one another, so they are taken once per 128 columns, and
 // the accumulator is given back before the boxes are written.
+//
+// What bf16 rounded away of G at the rows' tokens (Rounding) is added here, in fp32
+// and in the order of H's rows.  kByRow (dH): the lane's row is a row of H, its
+// token names a row of W.  Else (dW): the lane's row is a row of W; the words the
+// logits' pass left for the warp's 32 rows say which rows of H have one of them as
+// their token -- usually none, B 32 / V on average.  They are read a unit ahead, and
+// the first such row of H before the wait for the accumulator.
+struct Rounding {
+  const float* delta;  // [B]: G at the row's token, less what is stored of it
+  // [V / 32][ceil(B / 32)]: for 32 ids and 32 rows of H, a bit for each row whose
+  // token is among the ids, and the first one's token (of the 32) and delta.
+  const uint4* marks;
+  const int64_t* tokens;
+  int64_t vocab_offset;
+  int32_t B, V;
+  const __nv_bfloat16* X;  // W for dH, H for dW
+  int64_t ldx;
+  // The token of H's row b as a row of W, or -1.
+  __device__ __forceinline__ int32_t row_of_w(int b) const {
+    const int64_t local = tokens[b] - vocab_offset;
+    return local >= 0 && local < V ? int32_t(local) : -1;
+  }
+  // The marks of the 32 ids from row0 and the lane's of 32 blocks of H's rows.
+  __device__ __forceinline__ uint4 load_marks(int block0, int row0, int lane) const {
+    const int blocks = (B + 31) / 32;
+    if (block0 + lane >= blocks || row0 >= V) return make_uint4(0u, 0u, 0u, 0u);
+    return marks[int64_t(row0 >> 5) * blocks + block0 + lane];
+  }
+};
+
+// r += f * x for 8 columns from x, of which `n` exist.
+__device__ __forceinline__ void add_scaled8(uint32_t* r, float f, const __nv_bfloat16* x, int n) {
+  if (n >= 8) {
+    const uint4 v = __ldg(reinterpret_cast<const uint4*>(x));
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      r[2 * i] = __float_as_uint(fmaf(f, __uint_as_float(w[i] << 16), __uint_as_float(r[2 * i])));
+      r[2 * i + 1] = __float_as_uint(
+          fmaf(f, __uint_as_float(w[i] & 0xFFFF0000u), __uint_as_float(r[2 * i + 1])));
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 7; ++i)
+      if (i < n)
+        r[i] = __float_as_uint(fmaf(f, __bfloat162float(x[i]), __uint_as_float(r[i])));
+  }
+}
+
+template <bool kByRow>
 struct StoreEpi {
   static constexpr int kN = kBN;
   static constexpr bool kStaged = true;
@@ -605,42 +660,142 @@ struct StoreEpi {
     __nv_bfloat16* out;
     int64_t ld;
     int32_t whole_n;
+    Rounding g;
   };
-  struct State {};
-  static __device__ __forceinline__ void start(const Params&, State&) {}
+  struct State {
+    float delta;             // kByRow: the row's, 0 for no token
+    const __nv_bfloat16* x;  // kByRow: the row of W its token names
+    uint4 marks, next;       // else: the first 32 blocks' marks of this unit, the next
+    uint32_t some;           // else: which blocks have any
+    uint2 quad;              // the first marked row of H: columns 4 lane .. + 3 of 128
+  };
+  // Columns 4 lane .. + 3 of the 128 from col of H's row b.
+  static __device__ __forceinline__ uint2 load_quad(const Params& p, int b, int col, int lane,
+                                                    int n_cols) {
+    const __nv_bfloat16* x = p.g.X + int64_t(b) * p.g.ldx + col + 4 * lane;
+    const int n = n_cols - (col + 4 * lane);
+    if (n >= 4) return __ldg(reinterpret_cast<const uint2*>(x));
+    uint32_t v[3];
+#pragma unroll
+    for (int i = 0; i < 3; ++i) v[i] = i < n ? __bfloat16_as_ushort(x[i]) : 0u;
+    return make_uint2(v[0] | v[1] << 16, v[2]);
+  }
+  static __device__ __forceinline__ void start(const Params& p, State& st, int row, int lane,
+                                               const Shape&) {
+    if constexpr (!kByRow) st.next = p.g.load_marks(0, row - lane, lane);
+  }
+  static __device__ __forceinline__ void before(const Params& p, State& st, const TileAt& at,
+                                                int next_row0, int lane, const Shape& s) {
+    if constexpr (kByRow) {
+      const int b = at.row0 + lane;
+      const int32_t v = b < s.m_rows ? p.g.row_of_w(b) : -1;
+      st.delta = v >= 0 ? p.g.delta[b] : 0.0f;
+      st.x = p.g.X + int64_t(max(v, 0)) * p.g.ldx;
+    } else {
+      st.marks = st.next;
+      st.next = p.g.load_marks(0, next_row0, lane);
+      st.some = __ballot_sync(0xFFFFFFFFu, st.marks.x != 0u);
+      if (st.some != 0u) {
+        const int k = __ffs(st.some) - 1;
+        const int b = k * 32 + __ffs(__shfl_sync(0xFFFFFFFFu, st.marks.x, k)) - 1;
+        st.quad = load_quad(p, b, at.col0, lane, s.n_cols);
+      }
+    }
+  }
+  // The accumulator of lane `row`, 128 columns, += f times H's (quad).  Short loops:
+  // code that few units run comes from far away, and unrolled it took longer to
+  // fetch than to run (2 us a unit).
+  static __device__ __forceinline__ void add_row(uint32_t taddr, bool here, float f, uint2 quad) {
+#pragma unroll 1
+    for (int c = 0; c < 4; ++c) {
+      uint32_t r[32];
+      ptx::tmem_ld_32x32b_x32(taddr + uint32_t(c * 32), r);
+      ptx::tmem_wait_ld();
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        const uint32_t w =
+            __shfl_sync(0xFFFFFFFFu, (j & 1) ? quad.y : quad.x, c * 8 + (j >> 1));
+        const float h0 = __uint_as_float(w << 16), h1 = __uint_as_float(w & 0xFFFF0000u);
+        if (here) {
+          r[2 * j] = __float_as_uint(fmaf(f, h0, __uint_as_float(r[2 * j])));
+          r[2 * j + 1] = __float_as_uint(fmaf(f, h1, __uint_as_float(r[2 * j + 1])));
+        }
+      }
+      ptx::tmem_st_32x32b_x32(taddr + uint32_t(c * 32), r);
+    }
+    ptx::tmem_wait_st();
+  }
+  // G's rounding at the tokens among the warp's rows, into the accumulator.
+  static __device__ __forceinline__ void add_marked(const Params& p, const State& st,
+                                                    const TileAt& at, int lane, int n_cols) {
+    bool first = st.some != 0u;  // quad holds its row
+#pragma unroll 1
+    for (int block0 = 0; block0 < (p.g.B + 31) / 32; block0 += 32) {
+      const uint4 m = block0 == 0 ? st.marks : p.g.load_marks(block0, at.row0, lane);
+#pragma unroll 1
+      for (uint32_t some = __ballot_sync(0xFFFFFFFFu, m.x != 0u); some != 0u; some &= some - 1u) {
+        const int k = __ffs(some) - 1, b0 = (block0 + k) * 32;
+        uint32_t word = __shfl_sync(0xFFFFFFFFu, m.x, k);
+        int32_t row = int32_t(__shfl_sync(0xFFFFFFFFu, m.y, k));
+        float f = __uint_as_float(__shfl_sync(0xFFFFFFFFu, m.z, k));
+#pragma unroll 1
+        while (true) {
+          const uint2 quad =
+              first ? st.quad : load_quad(p, b0 + __ffs(word) - 1, at.col0, lane, n_cols);
+          first = false;
+          add_row(at.taddr, row == lane, f, quad);
+          word &= word - 1u;
+          if (word == 0u) break;
+          row = p.g.row_of_w(b0 + __ffs(word) - 1) - at.row0;
+          f = p.g.delta[b0 + __ffs(word) - 1];
+        }
+      }
+    }
+  }
+  // 8 columns of the lane's row, from col: into the box or, from whole_n on, out.
+  static __device__ __forceinline__ void put8(const Params& p, const TileAt& at, int lane,
+                                              uint8_t* box, const Shape& s, int q, uint32_t v0,
+                                              uint32_t v1, uint32_t v2, uint32_t v3) {
+    box_put(box, lane, q, v0, v1, v2, v3);
+    if (at.col0 + 8 * q == p.whole_n && p.whole_n < s.n_cols && at.row0 + lane < s.m_rows) {
+      uint16_t* out = reinterpret_cast<uint16_t*>(p.out + int64_t(at.row0 + lane) * p.ld);
+      const uint32_t v[4] = {v0, v1, v2, v3};
+#pragma unroll
+      for (int i = 0; i < 7; ++i)
+        if (p.whole_n + i < s.n_cols) out[p.whole_n + i] = uint16_t(v[i / 2] >> (16 * (i & 1)));
+    }
+  }
   template <class Release>
-  static __device__ __forceinline__ void tile(const Params& p, State&, const TileAt& at, int lane,
-                                              uint8_t* box, const void* tmap, const Shape& s,
-                                              Release release) {
+  static __device__ __forceinline__ void tile(const Params& p, State& st, const TileAt& at,
+                                              int lane, uint8_t* box, const void* tmap,
+                                              const Shape& s, Release release) {
+    if constexpr (!kByRow)
+      if (st.some != 0u || p.g.B > 32 * 32) add_marked(p, st, at, lane, s.n_cols);
     uint32_t v[64];  // the row's 128 columns as bf16 pairs
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
-      uint32_t r[2][32];
-      ptx::tmem_ld_32x32b_x32(at.taddr + uint32_t(c * 64), r[0]);
-      ptx::tmem_ld_32x32b_x32(at.taddr + uint32_t(c * 64 + 32), r[1]);
+      uint32_t r[64];
+      ptx::tmem_ld_32x32b_x32(at.taddr + uint32_t(c * 64), reinterpret_cast<uint32_t(&)[32]>(r));
+      ptx::tmem_ld_32x32b_x32(at.taddr + uint32_t(c * 64 + 32),
+                              reinterpret_cast<uint32_t(&)[32]>(r[32]));
       ptx::tmem_wait_ld();
+      if constexpr (kByRow) {
+        const int col = at.col0 + c * 64;
+        if (st.delta != 0.0f)
+#pragma unroll
+          for (int q = 0; q < 8; ++q)
+            add_scaled8(r + 8 * q, st.delta, st.x + col + 8 * q, s.n_cols - (col + 8 * q));
+      }
 #pragma unroll
       for (int i = 0; i < 32; ++i)
-        v[c * 32 + i] = pack_bf16(__uint_as_float(r[i >> 4][(i & 15) * 2]),
-                                  __uint_as_float(r[i >> 4][(i & 15) * 2 + 1]));
+        v[c * 32 + i] = pack_bf16(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
     }
     release();
     box_begin(lane);
 #pragma unroll
     for (int q = 0; q < 16; ++q)
-      box_put(box, lane, q, v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+      put8(p, at, lane, box, s, q, v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
     box_end(box, tmap, lane, at.col0, at.row0, p.whole_n);
-    const int tail = p.whole_n - at.col0;  // where the single columns begin
-    if (tail >= 0 && tail < 128 && p.whole_n < s.n_cols && at.row0 + lane < s.m_rows) {
-      uint16_t* out = reinterpret_cast<uint16_t*>(p.out + int64_t(at.row0 + lane) * p.ld);
-#pragma unroll
-      for (int q = 0; q < 16; ++q)
-        if (tail == q * 8)
-#pragma unroll
-          for (int i = 0; i < 7; ++i)
-            if (p.whole_n + i < s.n_cols)
-              out[p.whole_n + i] = uint16_t(v[4 * q + i / 2] >> (16 * (i & 1)));
-    }
   }
   static __device__ __forceinline__ void finish(const Params&, State&, int, int, int,
                                                 const Shape&) {}
@@ -657,7 +812,9 @@ struct PartialEpi {
     int32_t ctas;  // CTAs per tile
   };
   struct State {};
-  static __device__ __forceinline__ void start(const Params&, State&) {}
+  static __device__ __forceinline__ void start(const Params&, State&, int, int, const Shape&) {}
+  static __device__ __forceinline__ void before(const Params&, State&, const TileAt&, int, int,
+                                                const Shape&) {}
   template <class Release>
   static __device__ __forceinline__ void tile(const Params& p, State&, const TileAt& at, int lane,
                                               uint8_t*, const void*, const Shape& s,

@@ -185,13 +185,16 @@ struct ScoreEpi {
     float ts[KC > 0 ? KC : 1];
     int32_t ti[KC > 0 ? KC : 1];
   };
-  static __device__ __forceinline__ void start(const Params&, State& st) {
+  static __device__ __forceinline__ void start(const Params&, State& st, int, int,
+                                               const Shape&) {
 #pragma unroll
     for (int q = 0; q < KC; ++q) {
       st.ts[q] = -INFINITY;
       st.ti[q] = -1;
     }
   }
+  static __device__ __forceinline__ void before(const Params&, State&, const TileAt&, int, int,
+                                                const Shape&) {}
   // 32 logits.  kMasked: a cleared id's logit counts as -inf, whatever it is.
   template <bool kMasked>
   static __device__ __forceinline__ void chunk(State& st, uint32_t (&r)[32], uint32_t allow) {
@@ -690,6 +693,8 @@ struct GradParams {
   const int64_t* tokens;
   const float *lse, *entropy, *grad_logp, *grad_entropy;
   int64_t vocab_offset;
+  float* delta;  // [B]: what rounding took from G at the row's token, where W has it
+  uint4* marks;  // as Rounding's
 };
 
 template <int kCols>
@@ -699,15 +704,22 @@ struct GradEpi {
   using Params = GradParams;
   // With a, e the row's upstream gradients over T, P = 2^x the probability and
   // x = log2 p = l scale2 - lse2:  G = P (c0 + c1 x), + a at the token, where
-  // c1 = -e ln2, c0 = -a - e entropy.
+  // c1 = -e ln2, c0 = -a - e entropy.  The token's element is the largest of its
+  // row by far and repeats its rounding error in all of dH's row and dW's, where
+  // the others' average out; so what bf16 leaves of it is kept (delta) and added
+  // to those rows in fp32: with it the results are as close as their own bf16
+  // rounding allows (4 to 96 rows: 1.0 times the error of that rounding alone,
+  // without it 1.3 to 1.6).
   struct State {
     int row = -1;
     float scale2, lse2, c0, c1, a;
-    int32_t token;  // id from 0, -1 for none
+    int32_t token;  // id from 0, -1 for none among W's
     const uint32_t* mrow;
     bool live;  // false: the row's G is 0
   };
-  static __device__ __forceinline__ void start(const Params&, State&) {}
+  static __device__ __forceinline__ void start(const Params&, State&, int, int, const Shape&) {}
+  static __device__ __forceinline__ void before(const Params&, State&, const TileAt&, int, int,
+                                                const Shape&) {}
   static __device__ __forceinline__ void load_row(const Params& p, State& st, int row,
                                                   int n_kb) {
     st.row = row;
@@ -728,10 +740,7 @@ struct GradEpi {
       a = 0.0f;
     } else if (local >= 0 && local < p.V) {
       st.token = int32_t(local);
-      if (st.mrow && !((st.mrow[local >> 5] >> (local & 31)) & 1u)) {
-        a = 0.0f;
-        st.token = -1;
-      }
+      if (st.mrow && !((st.mrow[local >> 5] >> (local & 31)) & 1u)) a = 0.0f;
     }
     st.a = a;
     st.c0 = -a;
@@ -741,6 +750,31 @@ struct GradEpi {
       st.c1 = -e * kLn2;
     }
   }
+  // 32 columns of G into the box; returns the token's, if it is among them.
+  template <bool kToken>
+  static __device__ __forceinline__ float put_chunk(const State& st, const uint32_t (&r)[32],
+                                                    uint32_t w, uint32_t tok, uint8_t* box,
+                                                    int lane, int c) {
+    float at_token = 0.0f;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      float g[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int j = q * 8 + i;
+        // Far below 1, p is 0 in fp32; the bound keeps 0 * -inf out of G.
+        const float x =
+            ptx::max_nan(fmaf(__uint_as_float(r[j]), st.scale2, -st.lse2), -16384.0f);
+        float v = ptx::ex2(x) * fmaf(st.c1, x, st.c0);
+        if (kToken && tok == uint32_t(j)) v += st.a;
+        g[i] = ((w >> j) & 1u) ? v : 0.0f;
+        if (kToken && tok == uint32_t(j)) at_token = g[i];
+      }
+      box_put(box, lane, c * 4 + q, pack_bf16(g[0], g[1]), pack_bf16(g[2], g[3]),
+              pack_bf16(g[4], g[5]), pack_bf16(g[6], g[7]));
+    }
+    return at_token;
+  }
   template <class Release>
   static __device__ __forceinline__ void tile(const Params& p, State& st, const TileAt& at,
                                               int lane, uint8_t* box, const void* tmap,
@@ -749,6 +783,7 @@ struct GradEpi {
     if (row != st.row) load_row(p, st, row, s.n_kb);
     const AllowWords allow(st.mrow, at.col0, p.V);
     box_begin(lane);
+    const int blocks = (p.B + 31) / 32;
 #pragma unroll 1
     for (int c = 0; c < kN / 64; ++c) {
       uint32_t r[32];
@@ -756,22 +791,21 @@ struct GradEpi {
       ptx::tmem_wait_ld();
       const uint32_t w = st.live ? allow.at(c) : 0u;  // 0 past V
       const uint32_t tok = uint32_t(st.token - (at.col0 + c * 32));
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        float g[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int j = q * 8 + i;
-          // Far below 1, p is 0 in fp32; the bound keeps 0 * -inf out of G.
-          const float x =
-              ptx::max_nan(fmaf(__uint_as_float(r[j]), st.scale2, -st.lse2), -16384.0f);
-          float v = ptx::ex2(x) * fmaf(st.c1, x, st.c0);
-          if (tok == uint32_t(j)) v += st.a;
-          g[i] = ((w >> j) & 1u) ? v : 0.0f;
-        }
-        box_put(box, lane, c * 4 + q, pack_bf16(g[0], g[1]), pack_bf16(g[2], g[3]),
-                pack_bf16(g[4], g[5]), pack_bf16(g[6], g[7]));
+      // The rows with their token here: dW's epilogue looks for them, and a warp
+      // without one need not.
+      const uint32_t marked = __ballot_sync(0xFFFFFFFFu, tok < 32u);
+      uint4 mark = make_uint4(marked, 0u, 0u, 0u);
+      if (marked == 0u) {
+        put_chunk<false>(st, r, w, tok, box, lane, c);
+      } else {
+        const float at_token = put_chunk<true>(st, r, w, tok, box, lane, c);
+        float delta = at_token - __bfloat162float(__float2bfloat16_rn(at_token));
+        if (!isfinite(delta)) delta = 0.0f;
+        if (tok < 32u) p.delta[row] = delta;  // one thread of the grid for each row
+        mark.y = __shfl_sync(0xFFFFFFFFu, tok, __ffs(marked) - 1);
+        mark.z = __float_as_uint(__shfl_sync(0xFFFFFFFFu, delta, __ffs(marked) - 1));
       }
+      if (lane == 0) p.marks[int64_t((at.col0 >> 5) + c) * blocks + (at.row0 >> 5)] = mark;
     }
     release();
     box_end(box, tmap, lane, at.col0, at.row0, min(p.V, at.col0 + kN / 2));
@@ -787,34 +821,55 @@ constexpr int kSumThreads = 256;
 constexpr int kSumBlocksPerTile = kBM * kBN / 4 / kSumThreads;  // of one CTA's tile
 __global__ void __launch_bounds__(kSumThreads)
     sum_splits_kernel(const float4* __restrict__ partial, int32_t n_splits, int32_t n_tiles,
-                      int32_t n_nt, int32_t ctas, int32_t B, int32_t d,
+                      int32_t n_nt, int32_t ctas, int32_t B, int32_t d, const Rounding g,
                       __nv_bfloat16* __restrict__ dH, int64_t lddh) {
   ptx::grid_launch_dependents();
-  ptx::grid_dependency_wait();
   constexpr int kTile = kBM * kBN / 4;              // float4 of a CTA's tile
   const int tile = blockIdx.x / kSumBlocksPerTile;  // (tile of the grid, CTA)
-  const int in = blockIdx.x % kSumBlocksPerTile * kSumThreads + threadIdx.x;
-  const int r = in % kBM, c4 = in / kBM;  // row, group of 4 columns
+  const int at = blockIdx.x % kSumBlocksPerTile * kSumThreads + threadIdx.x;
+  const int r = at % kBM, c4 = at / kBM;  // row, group of 4 columns
   const int t = tile / ctas, rank = tile - t * ctas;
   const int row = (t / n_nt * ctas + rank) * kBM + r;
   const int col = t % n_nt * kBN + c4 * 4;
-  if (row >= B || col >= d) return;
-  const float4* src = partial + (int64_t(t) * ctas + rank) * kTile + in;
+  const bool in = row < B && col < d;
+  // The row of W that G's rounding at the token belongs to.
+  const int32_t v = in ? g.row_of_w(row) : -1;
+  uint32_t x[4] = {};
+  if (v >= 0) {
+    const __nv_bfloat16* w = g.X + int64_t(v) * g.ldx + col;
+    if (col + 4 <= d) {
+      const uint2 two = __ldg(reinterpret_cast<const uint2*>(w));
+      x[0] = two.x << 16, x[1] = two.x & 0xFFFF0000u;
+      x[2] = two.y << 16, x[3] = two.y & 0xFFFF0000u;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 3; ++i)
+        if (col + i < d) x[i] = __float_as_uint(__bfloat162float(w[i]));
+    }
+  }
+  ptx::grid_dependency_wait();
+  if (!in) return;
+  const float delta = v >= 0 ? g.delta[row] : 0.0f;
+  const float4* src = partial + (int64_t(t) * ctas + rank) * kTile + at;
   const int64_t step = int64_t(n_tiles) * ctas * kTile;
-  float v[4] = {};
+  float sum[4] = {};
 #pragma unroll 8
   for (int s = 0; s < n_splits; ++s) {
     const float4 a = src[s * step];
-    v[0] += a.x, v[1] += a.y, v[2] += a.z, v[3] += a.w;
+    sum[0] += a.x, sum[1] += a.y, sum[2] += a.z, sum[3] += a.w;
   }
+  if (delta != 0.0f)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) sum[i] = fmaf(delta, __uint_as_float(x[i]), sum[i]);
   __nv_bfloat16* out = dH + int64_t(row) * lddh + col;
   if (col + 4 <= d) {
-    __nv_bfloat162 h[2] = {__floats2bfloat162_rn(v[0], v[1]), __floats2bfloat162_rn(v[2], v[3])};
+    __nv_bfloat162 h[2] = {__floats2bfloat162_rn(sum[0], sum[1]),
+                               __floats2bfloat162_rn(sum[2], sum[3])};
     *reinterpret_cast<uint2*>(out) = *reinterpret_cast<const uint2*>(h);
   } else {
 #pragma unroll
     for (int i = 0; i < 3; ++i)
-      if (col + i < d) out[i] = __float2bfloat16_rn(v[i]);
+      if (col + i < d) out[i] = __float2bfloat16_rn(sum[i]);
   }
 }
 
@@ -930,12 +985,12 @@ fs_status device_setup(const Device** out) {
           prepare_kernel<GradEpi<128>, false, false, false>(d.sms, &d.pairs) &&
           prepare_kernel<GradEpi<256>, false, false, false>(d.sms, &d.pairs) &&
           prepare_kernel<GradEpi<256>, true, false, false>(d.sms, &d.pairs) &&
-          prepare_kernel<StoreEpi, false, false, true>(d.sms, &d.pairs) &&
-          prepare_kernel<StoreEpi, true, false, true>(d.sms, &d.pairs) &&
+          prepare_kernel<StoreEpi<true>, false, false, true>(d.sms, &d.pairs) &&
+          prepare_kernel<StoreEpi<true>, true, false, true>(d.sms, &d.pairs) &&
           prepare_kernel<PartialEpi, false, false, true>(d.sms, &d.pairs) &&
           prepare_kernel<PartialEpi, true, false, true>(d.sms, &d.pairs) &&
-          prepare_kernel<StoreEpi, false, true, true>(d.sms, &d.pairs) &&
-          prepare_kernel<StoreEpi, true, true, true>(d.sms, &d.pairs) &&
+          prepare_kernel<StoreEpi<false>, false, true, true>(d.sms, &d.pairs) &&
+          prepare_kernel<StoreEpi<false>, true, true, true>(d.sms, &d.pairs) &&
           cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000,
                                            cudaEnableDefault, &q) == cudaSuccess &&
           q == cudaDriverEntryPointSuccess && fn != nullptr;
@@ -1171,6 +1226,10 @@ int64_t plan_split(int64_t B, int64_t d, int64_t V) {
 int64_t store_cols(int64_t d) { return d < 8 ? 8 : d & ~int64_t(7); }
 
 size_t g_bytes(int64_t B, int64_t V) { return round256(size_t(B) * size_t((V + 7) / 8 * 8) * 2u); }
+size_t delta_bytes(int64_t B) { return round256(size_t(B) * 4u); }
+size_t marks_bytes(int64_t B, int64_t V) {  // whole units of ids
+  return round256(size_t(ceil_div(V, kBN)) * (kBN / 32) * size_t(ceil_div(B, 32)) * sizeof(uint4));
+}
 size_t partial_bytes(int64_t B, int64_t d, int64_t V) {
   const int64_t n = plan_split(B, d, V);
   if (n == 1) return 0;
@@ -1239,7 +1298,7 @@ bool grad_sizes_ok(int64_t B, int64_t d, int64_t V) {
 
 extern "C" size_t fs_logprobs_grad_workspace_size(int64_t B, int64_t d, int64_t V) {
   if (!grad_sizes_ok(B, d, V)) return 0;
-  return g_bytes(B, V) + partial_bytes(B, d, V);
+  return g_bytes(B, V) + delta_bytes(B) + marks_bytes(B, V) + partial_bytes(B, d, V);
 }
 
 extern "C" fs_status fs_logprobs_grad(const fs_logprobs_grad_args* a, void* stream_ptr) {
@@ -1269,6 +1328,9 @@ extern "C" fs_status fs_logprobs_grad(const fs_logprobs_grad_args* a, void* stre
   cudaStream_t stream = static_cast<cudaStream_t>(stream_ptr);
   const int64_t B = a->B, d = a->d, V = a->V, ldg = (V + 7) / 8 * 8;
   void* G = a->workspace;
+  uint8_t* behind_g = static_cast<uint8_t*>(G) + g_bytes(B, V);
+  float* delta = reinterpret_cast<float*>(behind_g);
+  uint4* marks = reinterpret_cast<uint4*>(behind_g + delta_bytes(B));
   const bool pair = B > kBM;
   const int ctas = pair ? 2 : 1;
   const int workers = pair ? dev.pairs : dev.sms;
@@ -1307,6 +1369,8 @@ extern "C" fs_status fs_logprobs_grad(const fs_logprobs_grad_args* a, void* stre
     ep.grad_logp = a->grad_logp;
     ep.grad_entropy = a->grad_entropy;
     ep.vocab_offset = a->vocab_offset;
+    ep.delta = delta;
+    ep.marks = marks;
     const int n = balanced(s.n_units, workers);
     if (pair)
       st = launch<GradEpi<256>, true, false, false>(dev, mh, mw, mg, s, ep, n, false, stream);
@@ -1338,15 +1402,18 @@ extern "C" fs_status fs_logprobs_grad(const fs_logprobs_grad_args* a, void* stre
     s.a_box_rows = uint32_t(box_rows);
     s.pdl = s.early_trigger = 1;  // W streams while the kernel before ends
     const int n = balanced(s.n_units, workers);
+    const Rounding rounding = {delta, marks, a->tokens, a->vocab_offset, int32_t(B), int32_t(V),
+                               static_cast<const __nv_bfloat16*>(a->W), a->ldw};
     if (n_splits == 1) {
-      const StoreEpi::Params ep = {static_cast<__nv_bfloat16*>(a->out_dH), a->lddh,
-                                   int32_t(d & ~int64_t(7))};
-      st = pair ? launch<StoreEpi, true, false, true>(dev, mg, mw, mo, s, ep, n, true, stream)
-                : launch<StoreEpi, false, false, true>(dev, mg, mw, mo, s, ep, n, true, stream);
+      using Epi = StoreEpi<true>;
+      const Epi::Params ep = {static_cast<__nv_bfloat16*>(a->out_dH), a->lddh,
+                              int32_t(d & ~int64_t(7)), rounding};
+      st = pair ? launch<Epi, true, false, true>(dev, mg, mw, mo, s, ep, n, true, stream)
+                : launch<Epi, false, false, true>(dev, mg, mw, mo, s, ep, n, true, stream);
       if (st != FS_OK) return st;
     } else {
       PartialEpi::Params ep = {};
-      ep.partial = reinterpret_cast<float4*>(static_cast<uint8_t*>(G) + g_bytes(B, V));
+      ep.partial = reinterpret_cast<float4*>(behind_g + delta_bytes(B) + marks_bytes(B, V));
       ep.ctas = ctas;
       st = pair ? launch<PartialEpi, true, false, true>(dev, mg, mw, mo, s, ep, n, true, stream)
                 : launch<PartialEpi, false, false, true>(dev, mg, mw, mo, s, ep, n, true, stream);
@@ -1362,8 +1429,8 @@ extern "C" fs_status fs_logprobs_grad(const fs_logprobs_grad_args* a, void* stre
       cfg.numAttrs = 1;
       if (cudaLaunchKernelEx(&cfg, sum_splits_kernel, static_cast<const float4*>(ep.partial),
                              int32_t(n_splits), s.n_mt * s.n_nt, s.n_nt, int32_t(ctas), int32_t(B),
-                             int32_t(d), static_cast<__nv_bfloat16*>(a->out_dH),
-                             a->lddh) != cudaSuccess) {
+                             int32_t(d), rounding,
+                             static_cast<__nv_bfloat16*>(a->out_dH), a->lddh) != cudaSuccess) {
         cudaGetLastError();
         return FS_ERR_CUDA;
       }
@@ -1390,11 +1457,14 @@ extern "C" fs_status fs_logprobs_grad(const fs_logprobs_grad_args* a, void* stre
     s.a_box_rows = 0;
     s.policy_b = kPolicyLast;
     s.pdl = 1;  // H streams while the kernel before ends
-    const StoreEpi::Params ep = {static_cast<__nv_bfloat16*>(a->out_dW), a->lddw,
-                                 int32_t(d & ~int64_t(7))};
+    using Epi = StoreEpi<false>;
+    const Epi::Params ep = {static_cast<__nv_bfloat16*>(a->out_dW), a->lddw,
+                            int32_t(d & ~int64_t(7)),
+                            {delta, marks, a->tokens, a->vocab_offset, int32_t(B), int32_t(V),
+                             static_cast<const __nv_bfloat16*>(a->H), a->ldh}};
     const int n = balanced(s.n_units, wpair ? dev.pairs : dev.sms);
-    st = wpair ? launch<StoreEpi, true, true, true>(dev, mg, mh, mo, s, ep, n, true, stream)
-               : launch<StoreEpi, false, true, true>(dev, mg, mh, mo, s, ep, n, true, stream);
+    st = wpair ? launch<Epi, true, true, true>(dev, mg, mh, mo, s, ep, n, true, stream)
+               : launch<Epi, false, true, true>(dev, mg, mh, mo, s, ep, n, true, stream);
     if (st != FS_OK) return st;
   }
   return FS_OK;

@@ -463,3 +463,32 @@ def test_few_rows_at_low_temperature():
     bound = 4 * ref.U * math.sqrt(4096 / 16) * size + 4 * ref.U * float(w["lse"].abs().max())
     near(r.lse, w["lse"], bound, "lse")
     near(r.topk_logp, w["topk_logp"], bound + 2 * ref.U * w["topk_logp"].abs(), "topk_logp")
+
+
+@pytest.mark.parametrize("B,d,V,tokens", [
+    (2, 520, 2000, "one"), (60, 516, 2000, "one"), (128, 520, 700, "few"), (200, 520, 2000, "few"),
+    (300, 1000, 500, "rows"), (5, 520, 20000, "one"), (700, 520, 3000, "rows"),
+    (150, 520, 40000, "one"), (1500, 264, 700, "few"), (1100, 272, 900, "rows")])
+def test_gradient_has_no_rounding_bias_at_the_token(B, d, V, tokens):
+    """Upstream gradients that bf16 rounds the furthest, all the same way: the
+    rounding of the results (u = 2^-8 at most, either way) averages out along a
+    row, one of the token's factor would not.  Small logits, so that the token's
+    term is nearly all of its rows; "few" and "one": many rows share a token."""
+    p = problem(B, d, V, seed=B + V)
+    p["H"].mul_(1 / 64)
+    n = {"one": 1, "few": 3, "rows": V}[tokens]
+    gen = torch.Generator().manual_seed(B)
+    p["tokens"] = (torch.randint(0, n, (B,), generator=gen) * 37 % V).cuda()
+    p["vocab_mask"] = None
+    f = fs.fs_logprobs(p["H"], p["W"], p["tokens"])
+    # G at the token, a (1 - P), close to 1 + 2^-8: half a step above 1.
+    a = (1 + 2.0 ** -8 - 2.0 ** -14) / (1 - f.logp.exp())
+    dH, dW, wH, _, wW, _ = check_gradient(p, a, None)
+    held = torch.unique(p["tokens"]).cpu()
+    for got, want in ((dH.cpu().double(), wH), (dW.cpu().double()[held], wW[held])):
+        bias = ((got - want) * want).sum(1) / (want * want).sum(1)
+        # 8 deviations of a mean of d roundings (weights want^2: 3 d^-1 for normal
+        # values), and the other ids' elements of G, a/V each: 2^-8 / sqrt(V) a row.
+        limit = 8 * 2.0 ** -8 / math.sqrt(3) * math.sqrt(3 / d) + 2 * 2.0 ** -8 / math.sqrt(V)
+        assert limit < 2.0 ** -8 * 0.6
+        assert float(bias.abs().max()) < limit
