@@ -74,8 +74,9 @@ def test_workspace_sizes(lib):
             <= 1280 * 50 * (16 + 24 * 8))
     for bad in ((0, 64, 100), (65536, 64, 100), (4, 0, 100), (4, 64, 0)):
         assert fs.fs_logprobs_grad_workspace_size(*bad) == 0
-    # G in bf16, its rows padded to 8 ids, and dH's partial tiles.
-    assert fs.fs_logprobs_grad_workspace_size(3, 64, 64) == 512  # one k slice: unsplit
+    # G in bf16, its rows padded to 8 ids, its rounding at the tokens, where they are, and
+    # dH's partial tiles (one k slice: unsplit).
+    assert fs.fs_logprobs_grad_workspace_size(3, 64, 64) == 512 + 256 + 256
     assert fs.fs_logprobs_grad_workspace_size(1024, 4096, 151936) >= 1024 * 151936 * 2
     assert fs.fs_embed_grad_workspace_size(0, 64) == 0
     assert fs.fs_embed_grad_workspace_size(5, 0) == 0
