@@ -15,6 +15,13 @@
 // accumulators (two of them, so an epilogue overlaps the next unit's MMAs).
 // Every wait is bounded: past the limit the roles wind down and the device
 // error word records it.
+//
+// Bound: W's bytes for few rows, the tensor cores for many.  Measured (GB300, copy
+// 6.7 TB/s, bf16 1900 TFLOP/s in bursts, 1730 held at the power limit): scores of 64
+// rows at d = 4096, V = 151936 read W at 6.6 TB/s with what follows them; of 1000
+// rows 1480 TFLOP/s held, 1680 in bursts (a slice of a CTA pair takes 600 cycles, 544
+// at the unit's nominal rate); dH of 96 rows at d = 2048 6.5 TB/s; dW of 96 rows
+// writes 5.4 TB/s: 2 slices a unit, its epilogue and stores bound it.
 #pragma once
 
 #include <cuda.h>
@@ -803,7 +810,8 @@ struct StoreEpi {
 
 // One k split's fp32 accumulator, for a later sum in split order.  A CTA tile
 // (128 x 256) is stored as [64 column quads][128 rows] float4, so a warp's
-// 16-byte stores are contiguous.
+// 16-byte stores are contiguous.  Once a unit of dozens of slices: 94 us at 96 rows,
+// d = 2048, V = 151936, of which W's stream is 93.
 struct PartialEpi {
   static constexpr int kN = kBN;
   static constexpr bool kStaged = false;

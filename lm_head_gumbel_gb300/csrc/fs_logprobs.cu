@@ -76,7 +76,7 @@ struct AllowWords {
 
 // One thread's state of a row, as left in the workspace.
 struct RowPart {
-  float m, S, U, unused;
+  float m, S, U, pad;  // 16 bytes
 };
 
 // Insert (v, id) into a list sorted by decreasing value whose last entry it
@@ -511,7 +511,8 @@ static_assert(kMaxSlots <= JoinWide::kThreads && kPlanSms <= JoinNarrow::kThread
 // threads came in.
 //
 // What bounds it is latency: dependent loads, barriers and short loops, hidden
-// behind other rows where there are more rows than SMs.
+// behind other rows where there are more rows than SMs.  It adds 9 us to 64 rows at
+// d = 4096 with K = 5 (18 us alone, cold), 17 to 1000.
 template <int KC, class Block>
 __global__ void __launch_bounds__(Block::kThreads, Block::kBlocks)
     join_kernel(const JoinParams p) {
@@ -814,9 +815,10 @@ struct GradEpi {
                                                 const Shape&) {}
 };
 
-// dH from its k splits, in split order, rounded to bf16 once.  A thread takes
-// 4 columns of one row; neighbouring threads take neighbouring rows, the order
-// the partial tiles are stored in (PartialEpi).
+// dH from its k splits, in split order, with G's rounding at the row's token, rounded
+// to bf16 once.  A thread takes 4 columns of one row; neighbouring threads take
+// neighbouring rows, the order the partial tiles are stored in (PartialEpi).  The
+// partials come from L2: 9 us alone and cold for 19 splits of 96 rows at d = 2048.
 constexpr int kSumThreads = 256;
 constexpr int kSumBlocksPerTile = kBM * kBN / 4 / kSumThreads;  // of one CTA's tile
 __global__ void __launch_bounds__(kSumThreads)
