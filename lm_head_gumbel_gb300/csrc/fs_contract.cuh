@@ -265,12 +265,12 @@ struct TileAt {
 // Epi: struct with Params, State, kN (columns of a unit: 256, or 64 / 128 where
 // 256 would leave CTAs without units), kStaged (uses bf16 boxes in shared memory
 // and tmap_d), and static device functions start / before / tile / finish.
+// The tensor maps and parameters are the kernel's own; `block` of `n_blocks` CTAs.
 template <class Epi, bool kPair, bool kAmn, bool kBmn>
-__global__ void __launch_bounds__(kThreads, 1)
-    contract_kernel(const __grid_constant__ CUtensorMap tmap_a,
-                    const __grid_constant__ CUtensorMap tmap_b,
-                    const __grid_constant__ CUtensorMap tmap_d, const Shape s,
-                    const __grid_constant__ typename Epi::Params ep) {
+__device__ __forceinline__ void contract(const CUtensorMap& tmap_a, const CUtensorMap& tmap_b,
+                                         const CUtensorMap& tmap_d, const Shape& s,
+                                         const typename Epi::Params& ep, int block,
+                                         int n_blocks) {
   constexpr int kCtas = kPair ? 2 : 1;
   constexpr int kN = Epi::kN;
   constexpr uint32_t kTmemCols = 2 * kN;
@@ -296,8 +296,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int lane = threadIdx.x & 31;
   const int rank = kPair ? int(ptx::cluster_ctarank()) : 0;
   const bool leader = rank == 0;
-  const int worker = int(blockIdx.x) / kCtas;
-  const int n_workers = int(gridDim.x) / kCtas;
+  const int worker = block / kCtas;
+  const int n_workers = n_blocks / kCtas;
 
   if (threadIdx.x == 0) {
     for (uint32_t i = 0; i < s.n_stages; ++i) {
@@ -568,6 +568,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   if constexpr (kPair) ptx::cluster_sync();
   // A dependent kernel waits for the whole grid before it reads anything of it.
   if (!s.early_trigger) ptx::grid_launch_dependents();
+}
+
+template <class Epi, bool kPair, bool kAmn, bool kBmn>
+__global__ void __launch_bounds__(kThreads, 1)
+    contract_kernel(const __grid_constant__ CUtensorMap tmap_a,
+                    const __grid_constant__ CUtensorMap tmap_b,
+                    const __grid_constant__ CUtensorMap tmap_d, const Shape s,
+                    const __grid_constant__ typename Epi::Params ep) {
+  contract<Epi, kPair, kAmn, kBmn>(tmap_a, tmap_b, tmap_d, s, ep, int(blockIdx.x),
+                                   int(gridDim.x));
 }
 
 // ---------------------------------------------------------------------------

@@ -875,6 +875,23 @@ __global__ void __launch_bounds__(kSumThreads)
   }
 }
 
+// dH's partial tiles and dW in one launch, the first `n_h` CTAs the former's, where
+// a CTA has at most one unit of either: then a launch's start is most of its time
+// (4 rows at d = 256, V = 4096: 20.5 us a call in two launches, 16.4 in one).
+constexpr size_t kBothSmem = std::max(smem_bytes<PartialEpi>(), smem_bytes<StoreEpi<false>>());
+__global__ void __launch_bounds__(kThreads, 1)
+    both_kernel(const __grid_constant__ CUtensorMap h_a, const __grid_constant__ CUtensorMap h_b,
+                const __grid_constant__ CUtensorMap w_a, const __grid_constant__ CUtensorMap w_b,
+                const __grid_constant__ CUtensorMap w_d, const __grid_constant__ Shape h,
+                const __grid_constant__ Shape w, const __grid_constant__ PartialEpi::Params hp,
+                const __grid_constant__ StoreEpi<false>::Params wp, int n_h) {
+  if (int(blockIdx.x) < n_h)
+    contract<PartialEpi, false, false, true>(h_a, h_b, w_d, h, hp, int(blockIdx.x), n_h);
+  else
+    contract<StoreEpi<false>, false, true, true>(w_a, w_b, w_d, w, wp, int(blockIdx.x) - n_h,
+                                                 int(gridDim.x) - n_h);
+}
+
 // ---------------------------------------------------------------------------
 // Host side
 // ---------------------------------------------------------------------------
@@ -993,6 +1010,8 @@ fs_status device_setup(const Device** out) {
           prepare_kernel<PartialEpi, true, false, true>(d.sms, &d.pairs) &&
           prepare_kernel<StoreEpi<false>, false, true, true>(d.sms, &d.pairs) &&
           prepare_kernel<StoreEpi<false>, true, true, true>(d.sms, &d.pairs) &&
+          cudaFuncSetAttribute(both_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               int(kBothSmem)) == cudaSuccess &&
           cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000,
                                            cudaEnableDefault, &q) == cudaSuccess &&
           q == cudaDriverEntryPointSuccess && fn != nullptr;
@@ -1020,16 +1039,21 @@ bool encode(const Device& dev, CUtensorMap* m, const void* base, int64_t inner, 
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <class Epi, bool kPair, bool kAmn, bool kBmn>
-fs_status launch(const Device& dev, const CUtensorMap& a, const CUtensorMap& b,
-                 const CUtensorMap& d, Shape s, const typename Epi::Params& ep, int workers,
-                 bool overlap, cudaStream_t stream) {
+template <class Epi, bool kPair, bool kAmn>
+void fill_ring(const Device& dev, Shape& s) {
   constexpr uint32_t kBBytes = (kPair ? Epi::kN / 2 : Epi::kN) * kBK * 2;
   s.a_bytes = kAmn ? kBM * kBK * 2 : s.a_box_rows * 128u;
   s.stage_bytes = slices<Epi>() * (s.a_bytes + kBBytes);
   s.n_stages = std::min<uint32_t>(kMaxStages, ring_bytes<Epi>() / s.stage_bytes);
   s.wait_limit_ns = kWaitLimitNs;
   s.error_word = dev.error_word;
+}
+
+template <class Epi, bool kPair, bool kAmn, bool kBmn>
+fs_status launch(const Device& dev, const CUtensorMap& a, const CUtensorMap& b,
+                 const CUtensorMap& d, Shape s, const typename Epi::Params& ep, int workers,
+                 bool overlap, cudaStream_t stream) {
+  fill_ring<Epi, kPair, kAmn>(dev, s);
   cudaLaunchAttribute attr[2];
   unsigned n = 0;
   if (kPair) {
@@ -1384,89 +1408,108 @@ extern "C" fs_status fs_logprobs_grad(const fs_logprobs_grad_args* a, void* stre
   }
 
   // dH = G W.
+  const int64_t n_splits = a->out_dH ? plan_split(B, d, V) : 1;
+  CUtensorMap hg, hw, ho;
+  Shape h = {};
   if (a->out_dH) {
-    const int64_t n_splits = plan_split(B, d, V);
     const int box_rows = pair ? kBM : int(std::min<int64_t>(kBM, (B + 7) / 8 * 8));
-    CUtensorMap mg, mw, mo;
-    if (!encode(dev, &mg, G, V, B, ldg, box_rows) || !encode(dev, &mw, a->W, d, V, a->ldw, kBK) ||
-        !encode(dev, &mo, a->out_dH, store_cols(d), B, a->lddh, 32))
+    if (!encode(dev, &hg, G, V, B, ldg, box_rows) || !encode(dev, &hw, a->W, d, V, a->ldw, kBK) ||
+        !encode(dev, &ho, a->out_dH, store_cols(d), B, a->lddh, 32))
       return FS_ERR_INVALID_ARG;
-    Shape s = {};
-    s.n_mt = int32_t(ceil_div(B, kBM * ctas));
-    s.n_nt = int32_t(ceil_div(d, kBN));
-    s.n_units = int32_t(s.n_mt * s.n_nt * n_splits);
-    s.n_kb = int32_t(ceil_div(V, kBK));
-    s.n_splits = int32_t(n_splits);
-    s.k_descending = 1;  // from the ids whose rows of W and columns of G came last
-    s.m_rows = int32_t(B);
-    s.n_cols = int32_t(d);
-    s.m_fastest = 1;
-    s.a_box_rows = uint32_t(box_rows);
-    s.pdl = s.early_trigger = 1;  // W streams while the kernel before ends
-    const int n = balanced(s.n_units, workers);
-    const Rounding rounding = {delta, marks, a->tokens, a->vocab_offset, int32_t(B), int32_t(V),
-                               static_cast<const __nv_bfloat16*>(a->W), a->ldw};
-    if (n_splits == 1) {
-      using Epi = StoreEpi<true>;
-      const Epi::Params ep = {static_cast<__nv_bfloat16*>(a->out_dH), a->lddh,
-                              int32_t(d & ~int64_t(7)), rounding};
-      st = pair ? launch<Epi, true, false, true>(dev, mg, mw, mo, s, ep, n, true, stream)
-                : launch<Epi, false, false, true>(dev, mg, mw, mo, s, ep, n, true, stream);
-      if (st != FS_OK) return st;
-    } else {
-      PartialEpi::Params ep = {};
-      ep.partial = reinterpret_cast<float4*>(behind_g + delta_bytes(B) + marks_bytes(B, V));
-      ep.ctas = ctas;
-      st = pair ? launch<PartialEpi, true, false, true>(dev, mg, mw, mo, s, ep, n, true, stream)
-                : launch<PartialEpi, false, false, true>(dev, mg, mw, mo, s, ep, n, true, stream);
-      if (st != FS_OK) return st;
-      cudaLaunchAttribute attr;
-      attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-      attr.val.programmaticStreamSerializationAllowed = 1;
-      cudaLaunchConfig_t cfg = {};
-      cfg.gridDim = dim3(unsigned(s.n_mt * s.n_nt * ctas * kSumBlocksPerTile), 1, 1);
-      cfg.blockDim = dim3(kSumThreads, 1, 1);
-      cfg.stream = stream;
-      cfg.attrs = &attr;
-      cfg.numAttrs = 1;
-      if (cudaLaunchKernelEx(&cfg, sum_splits_kernel, static_cast<const float4*>(ep.partial),
-                             int32_t(n_splits), s.n_mt * s.n_nt, s.n_nt, int32_t(ctas), int32_t(B),
-                             int32_t(d), rounding,
-                             static_cast<__nv_bfloat16*>(a->out_dH), a->lddh) != cudaSuccess) {
-        cudaGetLastError();
-        return FS_ERR_CUDA;
-      }
-    }
+    h.n_mt = int32_t(ceil_div(B, kBM * ctas));
+    h.n_nt = int32_t(ceil_div(d, kBN));
+    h.n_units = int32_t(h.n_mt * h.n_nt * n_splits);
+    h.n_kb = int32_t(ceil_div(V, kBK));
+    h.n_splits = int32_t(n_splits);
+    h.k_descending = 1;  // from the ids whose rows of W and columns of G came last
+    h.m_rows = int32_t(B);
+    h.n_cols = int32_t(d);
+    h.m_fastest = 1;
+    h.a_box_rows = uint32_t(box_rows);
+    h.pdl = h.early_trigger = 1;  // W streams while the kernel before ends
   }
 
   // dW = G^T H: M is the vocabulary, so the units of one vocabulary block
   // (its slice of G) run over the columns of H next to one another.
+  const bool both = a->out_dH && a->out_dW && !pair && n_splits > 1 &&
+                    h.n_units + ceil_div(V, kBM) * ceil_div(d, kBN) <= dev.sms;
+  const bool wpair = !both && V > kBM;
+  CUtensorMap wg, wh, wo;
+  Shape w = {};
   if (a->out_dW) {
-    const bool wpair = V > kBM;
-    CUtensorMap mg, mh, mo;
-    if (!encode(dev, &mg, G, V, B, ldg, kBK) || !encode(dev, &mh, a->H, d, B, a->ldh, kBK) ||
-        !encode(dev, &mo, a->out_dW, store_cols(d), V, a->lddw, 32))
+    if (!encode(dev, &wg, G, V, B, ldg, kBK) || !encode(dev, &wh, a->H, d, B, a->ldh, kBK) ||
+        !encode(dev, &wo, a->out_dW, store_cols(d), V, a->lddw, 32))
       return FS_ERR_INVALID_ARG;
-    Shape s = {};
-    s.n_mt = int32_t(ceil_div(V, wpair ? 2 * kBM : kBM));
-    s.n_nt = int32_t(ceil_div(d, kBN));
-    s.n_units = s.n_mt * s.n_nt;
-    s.n_kb = int32_t(ceil_div(B, kBK));
-    s.n_splits = 1;
-    s.m_rows = int32_t(V);
-    s.n_cols = int32_t(d);
-    s.m_fastest = 0;
-    s.a_box_rows = 0;
-    s.policy_b = kPolicyLast;
-    s.pdl = 1;  // H streams while the kernel before ends
+    w.n_mt = int32_t(ceil_div(V, wpair ? 2 * kBM : kBM));
+    w.n_nt = int32_t(ceil_div(d, kBN));
+    w.n_units = w.n_mt * w.n_nt;
+    w.n_kb = int32_t(ceil_div(B, kBK));
+    w.n_splits = 1;
+    w.m_rows = int32_t(V);
+    w.n_cols = int32_t(d);
+    w.policy_b = kPolicyLast;
+    w.pdl = 1;  // H streams while the kernel before ends
+    w.early_trigger = both;
+  }
+  const int32_t whole_d = int32_t(d & ~int64_t(7));
+  const Rounding h_rounding = {delta, marks, a->tokens, a->vocab_offset, int32_t(B), int32_t(V),
+                               static_cast<const __nv_bfloat16*>(a->W), a->ldw};
+  const PartialEpi::Params hp = {
+      reinterpret_cast<float4*>(behind_g + delta_bytes(B) + marks_bytes(B, V)), ctas};
+  const StoreEpi<false>::Params wp = {static_cast<__nv_bfloat16*>(a->out_dW), a->lddw, whole_d,
+                                      {delta, marks, a->tokens, a->vocab_offset, int32_t(B),
+                                       int32_t(V), static_cast<const __nv_bfloat16*>(a->H),
+                                       a->ldh}};
+
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  if (both) {
+    fill_ring<PartialEpi, false, false>(dev, h);
+    fill_ring<StoreEpi<false>, false, true>(dev, w);
+    cfg.gridDim = dim3(unsigned(h.n_units + w.n_units), 1, 1);
+    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.dynamicSmemBytes = kBothSmem;
+    if (cudaLaunchKernelEx(&cfg, both_kernel, hg, hw, wg, wh, wo, h, w, hp, wp, int(h.n_units)) !=
+        cudaSuccess) {
+      cudaGetLastError();
+      return FS_ERR_CUDA;
+    }
+  } else if (a->out_dH) {
+    const int n = balanced(h.n_units, workers);
+    if (n_splits == 1) {
+      using Epi = StoreEpi<true>;
+      const Epi::Params ep = {static_cast<__nv_bfloat16*>(a->out_dH), a->lddh, whole_d,
+                              h_rounding};
+      st = pair ? launch<Epi, true, false, true>(dev, hg, hw, ho, h, ep, n, true, stream)
+                : launch<Epi, false, false, true>(dev, hg, hw, ho, h, ep, n, true, stream);
+    } else {
+      st = pair ? launch<PartialEpi, true, false, true>(dev, hg, hw, ho, h, hp, n, true, stream)
+                : launch<PartialEpi, false, false, true>(dev, hg, hw, ho, h, hp, n, true, stream);
+    }
+    if (st != FS_OK) return st;
+  }
+  if (n_splits > 1) {
+    cfg.gridDim = dim3(unsigned(h.n_mt * h.n_nt * ctas * kSumBlocksPerTile), 1, 1);
+    cfg.blockDim = dim3(kSumThreads, 1, 1);
+    cfg.dynamicSmemBytes = 0;
+    if (cudaLaunchKernelEx(&cfg, sum_splits_kernel, static_cast<const float4*>(hp.partial),
+                           int32_t(n_splits), h.n_mt * h.n_nt, h.n_nt, int32_t(ctas), int32_t(B),
+                           int32_t(d), h_rounding, static_cast<__nv_bfloat16*>(a->out_dH),
+                           a->lddh) != cudaSuccess) {
+      cudaGetLastError();
+      return FS_ERR_CUDA;
+    }
+  }
+  if (a->out_dW && !both) {
     using Epi = StoreEpi<false>;
-    const Epi::Params ep = {static_cast<__nv_bfloat16*>(a->out_dW), a->lddw,
-                            int32_t(d & ~int64_t(7)),
-                            {delta, marks, a->tokens, a->vocab_offset, int32_t(B), int32_t(V),
-                             static_cast<const __nv_bfloat16*>(a->H), a->ldh}};
-    const int n = balanced(s.n_units, wpair ? dev.pairs : dev.sms);
-    st = wpair ? launch<Epi, true, true, true>(dev, mg, mh, mo, s, ep, n, true, stream)
-               : launch<Epi, false, true, true>(dev, mg, mh, mo, s, ep, n, true, stream);
+    const int n = balanced(w.n_units, wpair ? dev.pairs : dev.sms);
+    st = wpair ? launch<Epi, true, true, true>(dev, wg, wh, wo, w, wp, n, true, stream)
+               : launch<Epi, false, true, true>(dev, wg, wh, wo, w, wp, n, true, stream);
     if (st != FS_OK) return st;
   }
   return FS_OK;
