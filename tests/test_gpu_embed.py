@@ -295,3 +295,37 @@ def test_dense_gradient_in_a_graph_on_a_side_stream():
             graph.replay()
             torch.cuda.synchronize()
             assert torch.equal(copy, want)
+
+
+# --------------------------------------------------------------------------- offsets past 32 bits
+def test_tables_past_32_bits():
+    """Lookup and gradients (of one, a few thousand and more ids) of a table, and of
+    an output, of more than 2^32 elements.  Whole numbers: every sum is exact."""
+    V, d, ld = 70000, 24, 1 << 16
+    table = torch.as_strided(torch.zeros((V - 1) * ld + d, dtype=torch.bfloat16, device="cuda"),
+                             (V, d), (ld, 1))
+    rows = torch.arange(V, device="cuda").unsqueeze(1)
+    table.copy_((rows + torch.arange(d, device="cuda")) % 251 - 125)
+    ids = torch.tensor([V - 1, 0, V - 2, 65536, -1, V], device="cuda")
+    want = torch.zeros(6, d, dtype=torch.bfloat16, device="cuda")
+    want[:4] = table[ids[:4]]
+    assert torch.equal(fs.fs_embed(ids, table), want)
+    out = torch.as_strided(torch.empty(5 * (1 << 30) + d, dtype=torch.bfloat16, device="cuda"),
+                           (6, d), (1 << 30, 1))
+    assert torch.equal(fs.fs_embed(ids, table, out=out), want)
+    del out
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    for N in (1000, 5000, 20000):
+        ids = torch.randint(0, V, (N,), generator=gen, device="cuda")
+        ids[:4] = torch.tensor([V - 1, 0, V - 2, 65536], device="cuda")
+        dY = torch.randint(-8, 9, (N, d), generator=gen, device="cuda").bfloat16()
+        sums = torch.zeros(V, d, device="cuda").index_add_(0, ids, dY.float())
+        assert float(sums.abs().max()) <= 256
+        dE = torch.as_strided(torch.full(((V - 1) * ld + d,), 3.0, dtype=torch.bfloat16,
+                                         device="cuda"), (V, d), (ld, 1))
+        fs.fs_embed_grad(ids, dY, V, out=dE)
+        assert torch.equal(dE.float(), sums)
+        assert float(dE.as_strided((V - 1, 8), (ld, 1), d).min()) == 3.0  # between the rows
+        fs.fs_embed_grad(ids, dY, V, out=dE, accumulate=True)
+        assert torch.equal(dE.float(), 2 * sums)
+        del dE

@@ -492,3 +492,64 @@ def test_gradient_has_no_rounding_bias_at_the_token(B, d, V, tokens):
         limit = 8 * 2.0 ** -8 / math.sqrt(3) * math.sqrt(3 / d) + 2 * 2.0 ** -8 / math.sqrt(V)
         assert limit < 2.0 ** -8 * 0.6
         assert float(bias.abs().max()) < limit
+
+
+# --------------------------------------------------------------------------- offsets past 32 bits
+def far_apart(t, ld):
+    """The same matrix with rows at stride ld (what lies between is never touched)."""
+    out = torch.empty((t.shape[0] - 1) * ld + t.shape[1], dtype=t.dtype, device=t.device)
+    out = torch.as_strided(out, t.shape, (ld, 1))
+    out.copy_(t)
+    return out
+
+
+def test_row_strides_past_32_bits():
+    """H and W, and dH and dW, of more than 2^32 elements from first to last."""
+    for B, V, ldh, ldw in ((4, 40000, 64, 1 << 17), (300, 700, 1 << 24, 64)):
+        p = problem(B, 64, V, seed=80)
+        p["H"], p["W"] = far_apart(p["H"], ldh), far_apart(p["W"], ldw)
+        p["tokens"][-1] = V - 1
+        check_forward(p, 3)
+        out_dH = far_apart(torch.zeros_like(p["H"]), ldh)
+        out_dW = far_apart(torch.zeros_like(p["W"]), ldw)
+        check_gradient(p, *upstream(B, True, V), out_dH=out_dH, out_dW=out_dW)
+        del p, out_dH, out_dW
+        torch.cuda.empty_cache()
+
+
+def test_gradient_whose_logits_pass_32_bits():
+    """B V > 2^32; dH and dW compared at the first, some and the last rows."""
+    B, d, V = 33000, 32, 131200
+    gen = torch.Generator(device="cuda").manual_seed(81)
+    H = torch.randn(B, d, generator=gen, device="cuda").bfloat16()
+    W = (torch.randn(V, d, generator=gen, device="cuda") * 0.3).bfloat16()
+    t = torch.randint(0, V, (B,), generator=gen, device="cuda")
+    t[-1], t[-2] = V - 1, 0
+    a = torch.randn(B, generator=gen, device="cuda")
+    f = fs.fs_logprobs(H, W, t)
+    dH, dW = fs.fs_logprobs_grad(H, W, t, f.lse, a)
+    rows = torch.cat([torch.randint(0, B, (6,), generator=gen, device="cuda"),
+                      torch.tensor([0, B - 2, B - 1], device="cuda")])
+    ids = torch.cat([torch.randint(0, V, (6,), generator=gen, device="cuda"),
+                     torch.tensor([0, V - 2, V - 1], device="cuda"), t[rows]])
+    Hd, Wd = H.double(), W.double()
+    l = Hd[rows] @ Wd.T
+    lse = torch.logsumexp(l, 1)
+    # Bounds as in vocab_ref, from these rows' and ids' own magnitudes.
+    e_l = (d / 16 + 1) * 2.0 ** -23 * float((Hd.abs() @ Wd.abs().max(0).values).max())
+    e_lse = (e_l + 4 * ref.U * float(l.abs().max()) / math.log(2) + 2.0 ** -22
+             + (700 + V / 64) * ref.U + 4 * ref.U * float(lse.abs().max()))
+    near(f.lse[rows], lse.cpu(), e_lse, "lse")
+
+    def compare(got, p, hot, scale, other, terms, what):
+        G, mag = scale * (hot - p), scale.abs() * (hot + p)
+        want = G @ other
+        dG = (ref.BF16 * G.abs() + mag * (4 * e_lse + 8 * ref.U)) * (1 + ref.BF16)
+        bound = dG @ other.abs() + (terms / 16 + 64) * 2.0 ** -23 * (G.abs() @ other.abs())
+        near(got, want.cpu(), (bound * (1 + ref.BF16) + ref.BF16 * want.abs()).cpu(), what)
+
+    hot = torch.zeros_like(l).scatter_(1, t[rows].unsqueeze(1), 1.0)
+    compare(dH[rows], (l - lse.unsqueeze(1)).exp(), hot, a[rows].double().unsqueeze(1), Wd, V, "dH")
+    p = (Wd[ids] @ Hd.T - f.lse.double()).exp()  # lse's own error is in the bound
+    hot = (ids.unsqueeze(1) == t.unsqueeze(0)).double()
+    compare(dW[ids], p, hot, a.double(), Hd, B, "dW")
