@@ -5,10 +5,11 @@
 // lane in flight (16384 ids at d = 5120, bf16: 35 us with what L2 holds, 42 with
 // none of it, 5.8 TB/s).
 //
-// Gradient, up to 1024 ids, one kernel: every CTA sorts the (id, position) pairs
-// in shared memory, a warp sums each run of 32 sorted positions over the CTA's 64
-// columns, and ids that cross runs are joined; other CTAs zero the rows that no
-// id names.
+// Gradient, up to 1024 ids, one kernel (512 ids, d = 256: 11.1 us, 13.1 by the
+// kernels below; 1024 ids, d = 2048: 14.7, 14.3): every CTA sorts the (id, position)
+// pairs in shared memory, a warp sums each run of 32 sorted positions over the
+// CTA's 64 columns, and ids that cross runs are joined; other CTAs zero the rows
+// that no id names.
 //
 // Gradient, more ids, three or four kernels:
 //   sort_kernel       a cluster of 8 CTAs sorts the pairs, stably (4099 ids 8 us,
@@ -20,7 +21,7 @@
 //                     neighbours (32768 rows of d = 4096: 54 us, the rows at 5 TB/s
 //                     while the table's are written)
 //   run_join_kernel   the ids that cross runs, from their partial sums in order
-//                     (5 us at 4099 ids, 14 at 32768: latency)
+//                     (5 us at 4099 ids, 10 at 32768: latency)
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -908,8 +909,15 @@ namespace embed {
 namespace {
 
 // Sorted positions of a run (32 in the one-kernel gradient): long ones leave fewer
-// partial sums to join, short ones more warps.
-int64_t run_length(int64_t N) { return N <= kSmallMax ? 32 : N <= 8192 ? 16 : 64; }
+// partial sums to join, short ones more warps.  Measured with ids at frequencies
+// 1 / rank, in us a call, runs of 16 / 32 / 64 / 128:
+//   2048 ids, d = 2048   16.1 / 17.9 / 23.6 / 35.4     3000 ids  18.8 / 20.8 / 25.0 / 37.3
+//   4099 ids, d = 2048   22.2 / 21.4 / 25.4 / 37.9    12000 ids  44.7 / 39.0 / 39.0 / 51.3
+//   (4099 with nothing in L2 24.2 / 25.1)
+//   16384 ids, d = 2048  63.0 / 47.3 / 45.1           32768 ids, d = 4096  178 / 143 / 131 / 123
+int64_t run_length(int64_t N) {
+  return N <= kSmallMax ? 32 : N <= 5000 ? 16 : N <= 12000 ? 32 : N <= 20000 ? 64 : 128;
+}
 
 template <bool kAdd>
 const void* small_kernel(int y_dtype, int e_dtype) {

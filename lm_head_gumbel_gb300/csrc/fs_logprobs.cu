@@ -1098,6 +1098,8 @@ int64_t rows_per_launch(int64_t B) {
   return ceil_div(blocks, ceil_div(blocks, 5)) * 2 * kBM;
 }
 
+// A thread's list: K + 4 at least; longer ones cost registers, time and what the join
+// reads (64 rows at d = 4096, V = 151936, K = 4: 8 entries 191 us, 16 194, 24 197).
 int list_cap(int64_t K) { return K <= 0 ? 0 : K <= 4 ? 8 : K <= 12 ? 16 : 24; }
 
 // Columns of a single-CTA unit of the logits' kernels: the narrowest that still

@@ -268,6 +268,16 @@ def test_gradient_of_every_path(ty, to, N, V, d):
         check_gradient(ids, dY, V, scale=0.5, out=old, accumulate=True)
 
 
+@pytest.mark.parametrize("N", [2049, 5000, 5001, 12000, 12001, 20000, 20001])
+def test_gradient_run_lengths(N):
+    dY, _ = matrix(N, 40, torch.bfloat16, seed=N)
+    for kind in ("ragged", "few"):
+        ids = some_ids(kind, N, 5000, seed=N)
+        check_gradient(ids, dY, 5000, out_dtype=torch.float32)
+        old, _ = matrix(5000, 40, torch.bfloat16, seed=3)
+        check_gradient(ids, dY, 5000, scale=2.0, out=old, accumulate=True)
+
+
 def test_dense_gradient_in_a_graph_on_a_side_stream():
     """The zeroing runs beside the sort; what follows on the stream sees both done."""
     for N in (700, 5000, 20000):
