@@ -875,10 +875,13 @@ __global__ void __launch_bounds__(kSumThreads)
   }
 }
 
-// dH's partial tiles and dW in one launch, the first `n_h` CTAs the former's, where
-// a CTA has at most one unit of either: then a launch's start is most of its time
-// (4 rows at d = 256, V = 4096: 20.5 us a call in two launches, 16.4 in one).
+// dH's partial tiles and dW in one launch, the first `n_h` CTAs the former's, one unit
+// each, and the others dW's, where these have few: then a launch's start and end are
+// much of its time (a call in two launches / in one, us: 4 rows at d = 256, V = 4096
+// 20.5 / 16.4; 60 at 1024, 11137 29.4 / 24.1; 12 at 3214, 5280 37.1 / 35.3, dW's CTAs
+// with 7 units each; but 15 at 142, 125310, 11 units each, 53.3 / 56.8).
 constexpr size_t kBothSmem = std::max(smem_bytes<PartialEpi>(), smem_bytes<StoreEpi<false>>());
+template <bool kPair>
 __global__ void __launch_bounds__(kThreads, 1)
     both_kernel(const __grid_constant__ CUtensorMap h_a, const __grid_constant__ CUtensorMap h_b,
                 const __grid_constant__ CUtensorMap w_a, const __grid_constant__ CUtensorMap w_b,
@@ -886,9 +889,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const __grid_constant__ Shape w, const __grid_constant__ PartialEpi::Params hp,
                 const __grid_constant__ StoreEpi<false>::Params wp, int n_h) {
   if (int(blockIdx.x) < n_h)
-    contract<PartialEpi, false, false, true>(h_a, h_b, w_d, h, hp, int(blockIdx.x), n_h);
+    contract<PartialEpi, kPair, false, true>(h_a, h_b, w_d, h, hp, int(blockIdx.x), n_h);
   else
-    contract<StoreEpi<false>, false, true, true>(w_a, w_b, w_d, w, wp, int(blockIdx.x) - n_h,
+    contract<StoreEpi<false>, kPair, true, true>(w_a, w_b, w_d, w, wp, int(blockIdx.x) - n_h,
                                                  int(gridDim.x) - n_h);
 }
 
@@ -1010,7 +1013,9 @@ fs_status device_setup(const Device** out) {
           prepare_kernel<PartialEpi, true, false, true>(d.sms, &d.pairs) &&
           prepare_kernel<StoreEpi<false>, false, true, true>(d.sms, &d.pairs) &&
           prepare_kernel<StoreEpi<false>, true, true, true>(d.sms, &d.pairs) &&
-          cudaFuncSetAttribute(both_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+          cudaFuncSetAttribute(both_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               int(kBothSmem)) == cudaSuccess &&
+          cudaFuncSetAttribute(both_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                int(kBothSmem)) == cudaSuccess &&
           cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000,
                                            cudaEnableDefault, &q) == cudaSuccess &&
@@ -1227,9 +1232,10 @@ fs_status run_scores(const fs_logprobs_args* a, const Device& dev, cudaStream_t 
 // How dH = G W is split along k (the vocabulary).  Unsplit, the tiles of
 // [B, d] leave workers idle or in a thin last wave; each split adds partial tiles
 // written and read in fp32 and a kernel to sum them.  Costs in us as measured: a
-// k slice 0.33 (9 rows at d = 2492, V = 2769: 44 slices of one CTA 18 us, in splits
-// 7), 8 slices to fill the pipeline and drain a tile, 4 for the sum kernel and
-// 0.06 for each partial tile.
+// k slice 0.33 (0.45 unsplit: its ring is shorter by the store's staging; 6 rows at
+// d = 4193, V = 1940, 31 slices, unsplit 18.7 us with G's 19, in 4 splits 5.5), 8
+// slices to fill the pipeline and drain a tile, 4 for the sum kernel and 0.06 for
+// each partial tile.
 int64_t plan_split(int64_t B, int64_t d, int64_t V) {
   const bool pair = B > kBM;
   const int64_t workers = pair ? kPlanSms / 2 : kPlanSms;
@@ -1241,7 +1247,7 @@ int64_t plan_split(int64_t B, int64_t d, int64_t V) {
     const int64_t kb = ceil_div(n_kb, want), n = ceil_div(n_kb, kb);
     const int64_t waves = ceil_div(tiles * n, workers);
     const double sum = n > 1 ? 4.0 + 0.06 * double(n * tiles * (pair ? 2 : 1)) : 0.0;
-    const double cost = double(waves * (kb + 8)) * 0.33 + sum;
+    const double cost = double(waves * (kb + 8)) * (n > 1 ? 0.33 : 0.45) + sum;
     if (cost < best_cost) {
       best_cost = cost;
       best = n;
@@ -1433,9 +1439,9 @@ extern "C" fs_status fs_logprobs_grad(const fs_logprobs_grad_args* a, void* stre
 
   // dW = G^T H: M is the vocabulary, so the units of one vocabulary block
   // (its slice of G) run over the columns of H next to one another.
-  const bool both = a->out_dH && a->out_dW && !pair && n_splits > 1 &&
-                    h.n_units + ceil_div(V, kBM) * ceil_div(d, kBN) <= dev.sms;
-  const bool wpair = !both && V > kBM;
+  const bool both = a->out_dH && a->out_dW && n_splits > 1 && h.n_units * 3 <= workers * 2 &&
+                    ceil_div(V, kBM * ctas) * ceil_div(d, kBN) <= 8 * (workers - h.n_units);
+  const bool wpair = both ? pair : V > kBM;
   CUtensorMap wg, wh, wo;
   Shape w = {};
   if (a->out_dW) {
@@ -1463,24 +1469,36 @@ extern "C" fs_status fs_logprobs_grad(const fs_logprobs_grad_args* a, void* stre
                                        int32_t(V), static_cast<const __nv_bfloat16*>(a->H),
                                        a->ldh}};
 
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;  // of pairs
+  attr[1].val.clusterDim.x = 2;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.stream = stream;
-  cfg.attrs = &attr;
+  cfg.attrs = attr;
   cfg.numAttrs = 1;
   if (both) {
-    fill_ring<PartialEpi, false, false>(dev, h);
-    fill_ring<StoreEpi<false>, false, true>(dev, w);
-    cfg.gridDim = dim3(unsigned(h.n_units + w.n_units), 1, 1);
+    if (pair) {
+      fill_ring<PartialEpi, true, false>(dev, h);
+      fill_ring<StoreEpi<false>, true, true>(dev, w);
+    } else {
+      fill_ring<PartialEpi, false, false>(dev, h);
+      fill_ring<StoreEpi<false>, false, true>(dev, w);
+    }
+    const int n_w = balanced(w.n_units, workers - h.n_units);
+    cfg.gridDim = dim3(unsigned((h.n_units + n_w) * ctas), 1, 1);
     cfg.blockDim = dim3(kThreads, 1, 1);
     cfg.dynamicSmemBytes = kBothSmem;
-    if (cudaLaunchKernelEx(&cfg, both_kernel, hg, hw, wg, wh, wo, h, w, hp, wp, int(h.n_units)) !=
-        cudaSuccess) {
+    cfg.numAttrs = pair ? 2 : 1;
+    const int n_h = h.n_units * ctas;
+    if (cudaLaunchKernelEx(&cfg, pair ? both_kernel<true> : both_kernel<false>, hg, hw, wg, wh,
+                           wo, h, w, hp, wp, n_h) != cudaSuccess) {
       cudaGetLastError();
       return FS_ERR_CUDA;
     }
+    cfg.numAttrs = 1;
   } else if (a->out_dH) {
     const int n = balanced(h.n_units, workers);
     if (n_splits == 1) {

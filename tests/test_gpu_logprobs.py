@@ -435,7 +435,8 @@ def test_rows_per_launch(B):
 
 
 @pytest.mark.parametrize("B,d,V", [(9, 2492, 300), (2, 8, 5000), (260, 40, 3000), (130, 520, 129),
-                                   (16, 72, 19457)])
+                                   (16, 72, 19457), (6, 1200, 1940), (130, 260, 4096),
+                                   (300, 520, 2000), (60, 300, 11137), (128, 264, 5281)])
 def test_gradient_splits(B, d, V):
     """dH with and without splits, singles and pairs, narrow and wide units."""
     p = problem(B, d, V, T="rows", mask_frac=0.02, seed=B + d)
