@@ -96,7 +96,8 @@ fs_status fs_logprobs(const fs_logprobs_args *args, void *stream);
  * V) the one-hot term lies in another shard and only the p term is added here.
  * A fully masked row (lse -inf) gets no gradient.
  * H and W must be finite, masked ids' rows of W and fully masked rows of H too:
- * where G is 0 they are multiplied by 0, and 0 times NaN is NaN.
+ * where G is 0 they are multiplied by 0, and 0 times NaN is NaN.  dH and dW must
+ * not overlap H, W, the workspace or one another.
  */
 typedef struct fs_logprobs_grad_args {
   const void *H;
