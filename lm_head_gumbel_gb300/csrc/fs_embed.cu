@@ -121,19 +121,57 @@ __device__ __forceinline__ void store(float* p, const float (&f)[8]) {
   reinterpret_cast<float4*>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
 }
 
+// Eight columns 32 apart of a row (kStrided), a warp's next to one another: rows that
+// do not start on 16-byte boundaries.  `n` columns are left from p; a column past the
+// end is read from p instead and not written.  (8377 fp32 ids, d = 2229, into a whole
+// table: 53.6 us; one column a lane 69.7, d = 2232 on 16-byte boundaries 40.8.)
+constexpr int kStrided = -8;
+template <typename T>
+struct Piece<T, kStrided> {
+  T v[8];
+  __device__ __forceinline__ void load(const T* p, int n) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = p[32 * i < n ? 32 * i : 0];
+  }
+  __device__ __forceinline__ void get(float (&f)[8]) const {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = to_float(v[i]);
+  }
+};
+// C columns, or with C = kStrided 8.
+template <int C>
+constexpr int kColumns = C < 0 ? -C : C;
+template <int C, typename T>
+__device__ __forceinline__ void load_piece(Piece<T, C>& piece, const T* p, int n) {
+  if constexpr (C < 0)
+    piece.load(p, n);
+  else
+    piece.load(p);
+}
+template <int C, typename T>
+__device__ __forceinline__ void store_piece(T* p, const float (&f)[kColumns<C>], int n) {
+  if constexpr (C < 0) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (32 * i < n) put(p + 32 * i, f[i]);
+  } else {
+    store(p, f);
+  }
+}
+
 // How a row's columns are divided among warps: columns below `vec` (a multiple
 // of 8; 0 where rows do not start on 16-byte boundaries) in segments of C columns
-// a lane and G groups of lanes, the rest in segments of one column a lane.  A
+// a lane and G groups of lanes, the rest in segments of R columns a lane.  A
 // warp works on one segment, so its path is uniform.
 struct Columns {
   int32_t d, vec, vec_segments, segments;
 };
-__host__ Columns columns_of(int64_t d, bool vec, int C, int groups) {
+__host__ Columns columns_of(int64_t d, bool vec, int C, int groups, int R) {
   Columns c;
   c.d = int32_t(d);
   c.vec = vec ? int32_t(d & ~int64_t(7)) : 0;
   c.vec_segments = (c.vec + 32 * C * groups - 1) / (32 * C * groups);
-  c.segments = c.vec_segments + (c.d - c.vec + 32 * groups - 1) / (32 * groups);
+  c.segments = c.vec_segments + (c.d - c.vec + 32 * R - 1) / (32 * R);
   return c;
 }
 
@@ -603,31 +641,32 @@ __device__ __forceinline__ TO* table_at(const RunParams& p, uint32_t row, int co
 // A row's finished sum, scaled and (kAdd) added to what the row held.
 template <bool kAdd, typename TO, int C>
 __device__ __forceinline__ void write_sum(const RunParams& p, TO* dst, const Piece<TO, C>& old,
-                                          const float (&sum)[C]) {
-  float v[C];
+                                          const float (&sum)[kColumns<C>], int n) {
+  float v[kColumns<C>];
 #pragma unroll
-  for (int i = 0; i < C; ++i) v[i] = sum[i] * p.scale;
+  for (int i = 0; i < kColumns<C>; ++i) v[i] = sum[i] * p.scale;
   if (kAdd) {
-    float o[C];
+    float o[kColumns<C>];
     old.get(o);
 #pragma unroll
-    for (int i = 0; i < C; ++i) v[i] += o[i];
+    for (int i = 0; i < kColumns<C>; ++i) v[i] += o[i];
   }
-  store(dst, v);
+  store_piece<C>(dst, v, n);
 }
 
-// One warp, one run, C columns a lane from col (inactive lanes, `in` false,
-// follow along on the row's first columns).  The run's ids come in order; the
+// One warp, one run, C columns a lane from col, of which n are left (lanes without
+// any, n <= 0, follow along on the row's first columns).  The run's ids come in order; the
 // first may continue the previous run's last (then its sum is the run's start
 // partial), the last may go on in the next run (the end partial; a run that is
 // one id crossing both ways has a start partial only).  The rows of dY, and
 // with kAdd the table's rows that are finished here, are loaded kAhead at once.
 template <typename TY, typename TO, int C, bool kAdd>
-__device__ __forceinline__ void sum_run(const RunParams& p, int run, int col, bool in, int lane) {
+__device__ __forceinline__ void sum_run(const RunParams& p, int run, int col, int n, int lane) {
+  const bool in = n > 0;
   const int i0 = run * p.run, i1 = min(i0 + p.run, p.N);
   const uint32_t dropped = uint32_t(p.V);
   const TY* src = static_cast<const TY*>(p.dY) + (in ? col : 0);
-  float sum[C] = {};
+  float sum[kColumns<C>] = {};
   uint32_t prev = i0 > 0 ? p.key[i0 - 1] : dropped;
   bool crosses_start = false;  // the sum continues the previous run's
   bool open = false;           // the sum goes on past the last position seen
@@ -651,58 +690,61 @@ __device__ __forceinline__ void sum_run(const RunParams& p, int run, int col, bo
 #pragma unroll
       for (int a = 0; a < kAhead; ++a) {  // past the end: the last row again, unused
         const int i = min(g + a, live - 1);
-        piece[a].load(src + int64_t(__shfl_sync(0xFFFFFFFFu, pos, i)) * p.ldy);
+        load_piece<C>(piece[a], src + int64_t(__shfl_sync(0xFFFFFFFFu, pos, i)) * p.ldy, n);
         if (kAdd && ((ends >> i) & 1u))
-          old[a].load(table_at<TO>(p, __shfl_sync(0xFFFFFFFFu, key, i), in ? col : 0));
+          load_piece<C>(old[a], table_at<TO>(p, __shfl_sync(0xFFFFFFFFu, key, i), in ? col : 0),
+                        n);
       }
 #pragma unroll
       for (int a = 0; a < kAhead; ++a) {
         if (g + a >= live) break;
-        float v[C];
+        float v[kColumns<C>];
         piece[a].get(v);
 #pragma unroll
-        for (int i = 0; i < C; ++i) sum[i] += v[i];
+        for (int i = 0; i < kColumns<C>; ++i) sum[i] += v[i];
         if (!((ends >> (g + a)) & 1u)) continue;  // warp-uniform
         const uint32_t row = __shfl_sync(0xFFFFFFFFu, key, g + a);
         if (in) {
           if (crosses_start)
-            store(partial_at(p, run, 0, col), sum);
+            store_piece<C>(partial_at(p, run, 0, col), sum, n);
           else
-            write_sum<kAdd>(p, table_at<TO>(p, row, col), old[kAdd ? a : 0], sum);
+            write_sum<kAdd, TO, C>(p, table_at<TO>(p, row, col), old[kAdd ? a : 0], sum, n);
         }
         crosses_start = false;
 #pragma unroll
-        for (int i = 0; i < C; ++i) sum[i] = 0.0f;
+        for (int i = 0; i < kColumns<C>; ++i) sum[i] = 0.0f;
       }
     }
     open = !((ends >> (live - 1)) & 1u);
   }
-  if (open && in) store(partial_at(p, run, crosses_start ? 0 : 1, col), sum);
+  if (open && in) store_piece<C>(partial_at(p, run, crosses_start ? 0 : 1, col), sum, n);
 }
 
 // The id that begins in run `run` and goes on up to run `last`: its partial
 // sums in order.
 template <typename TO, int C, bool kAdd>
 __device__ __forceinline__ void join_runs(const RunParams& p, int run, int last, uint32_t id,
-                                          int col) {
-  float sum[C];
+                                          int col, int n) {
+  float sum[kColumns<C>];
   Piece<TO, C> old;
-  if (kAdd) old.load(table_at<TO>(p, id, col));
+  if (kAdd) load_piece<C>(old, static_cast<const TO*>(table_at<TO>(p, id, col)), n);
   Piece<float, C> piece;
-  piece.load(partial_at(p, run, 1, col));
+  load_piece<C>(piece, static_cast<const float*>(partial_at(p, run, 1, col)), n);
   piece.get(sum);
 #pragma unroll 8
   for (int r = run + 1; r <= last; ++r) {
-    float v[C];
-    piece.load(partial_at(p, r, 0, col));
+    float v[kColumns<C>];
+    load_piece<C>(piece, static_cast<const float*>(partial_at(p, r, 0, col)), n);
     piece.get(v);
 #pragma unroll
-    for (int i = 0; i < C; ++i) sum[i] += v[i];
+    for (int i = 0; i < kColumns<C>; ++i) sum[i] += v[i];
   }
-  write_sum<kAdd>(p, table_at<TO>(p, id, col), old, sum);
+  write_sum<kAdd, TO, C>(p, table_at<TO>(p, id, col), old, sum, n);
 }
 
-template <typename TY, typename TO, bool kAdd>
+// kVec: rows on 16-byte boundaries.  (A kernel for each: the strided loads take twice
+// the registers of the bf16 ones.)
+template <typename TY, typename TO, bool kAdd, bool kVec>
 __global__ void __launch_bounds__(kRunThreads) run_sum_kernel(const RunParams p) {
   ptx::grid_dependency_wait();
   const int lane = threadIdx.x & 31;
@@ -710,12 +752,15 @@ __global__ void __launch_bounds__(kRunThreads) run_sum_kernel(const RunParams p)
   const int run = int(item / p.cols.segments);
   if (run >= p.n_runs) return;
   const int seg = int(item - int64_t(run) * p.cols.segments);
-  if (seg < p.cols.vec_segments) {
+  if constexpr (!kVec) {
+    const int col = seg * 256 + lane;
+    sum_run<TY, TO, kStrided, kAdd>(p, run, col, p.cols.d - col, lane);
+  } else if (seg < p.cols.vec_segments) {
     const int col = seg * 256 + lane * 8;
-    sum_run<TY, TO, 8, kAdd>(p, run, col, col < p.cols.vec, lane);
+    sum_run<TY, TO, 8, kAdd>(p, run, col, p.cols.vec - col, lane);
   } else {
     const int col = p.cols.vec + (seg - p.cols.vec_segments) * 32 + lane;
-    sum_run<TY, TO, 1, kAdd>(p, run, col, col < p.cols.d, lane);
+    sum_run<TY, TO, 1, kAdd>(p, run, col, p.cols.d - col, lane);
   }
 }
 
@@ -749,10 +794,13 @@ __global__ void __launch_bounds__(kRunThreads) run_join_kernel(const RunParams p
   const uint32_t id = p.key[(run + 1) * p.run - 1];
   if (seg < p.cols.vec_segments) {
     const int col = seg * 256 + lane * 8;
-    if (col < p.cols.vec) join_runs<TO, 8, kAdd>(p, run, last, id, col);
+    if (col < p.cols.vec) join_runs<TO, 8, kAdd>(p, run, last, id, col, p.cols.vec - col);
+  } else if (p.cols.vec == 0) {
+    const int col = seg * 256 + lane;
+    if (col < p.cols.d) join_runs<TO, kStrided, kAdd>(p, run, last, id, col, p.cols.d - col);
   } else {
     const int col = p.cols.vec + (seg - p.cols.vec_segments) * 32 + lane;
-    if (col < p.cols.d) join_runs<TO, 1, kAdd>(p, run, last, id, col);
+    if (col < p.cols.d) join_runs<TO, 1, kAdd>(p, run, last, id, col, p.cols.d - col);
   }
 }
 
@@ -767,12 +815,12 @@ struct SmallShared {
 
 template <typename TY, typename TO, int C, bool kAdd>
 __device__ __forceinline__ void small_segment(const RunParams& p, int warp, int lane, int col,
-                                              bool in) {
-  if (warp < p.n_runs) sum_run<TY, TO, C, kAdd>(p, warp, col, in, lane);
+                                              int n) {
+  if (warp < p.n_runs) sum_run<TY, TO, C, kAdd>(p, warp, col, n, lane);
   __syncthreads();
   const int last = last_run(p, warp, lane);
-  if (last >= 0 && in)
-    join_runs<TO, C, kAdd>(p, warp, last, p.key[(warp + 1) * p.run - 1], col);
+  if (last >= 0 && n > 0)
+    join_runs<TO, C, kAdd>(p, warp, last, p.key[(warp + 1) * p.run - 1], col, n);
 }
 
 // CTAs 0 .. segments - 1: a segment of the columns, a warp for each run of 32
@@ -797,11 +845,11 @@ __global__ void __launch_bounds__(kSortThreads)
   if (seg < p.cols.vec_segments) {
     const int col0 = seg * 64, col = col0 + lane * 2;
     p.partial = sm.partial - col0;
-    small_segment<TY, TO, 2, kAdd>(p, warp, lane, col, col < p.cols.vec);
+    small_segment<TY, TO, 2, kAdd>(p, warp, lane, col, p.cols.vec - col);
   } else {
     const int col0 = p.cols.vec + (seg - p.cols.vec_segments) * 32, col = col0 + lane;
     p.partial = sm.partial - col0;
-    small_segment<TY, TO, 1, kAdd>(p, warp, lane, col, col < p.cols.d);
+    small_segment<TY, TO, 1, kAdd>(p, warp, lane, col, p.cols.d - col);
   }
 }
 
@@ -887,7 +935,8 @@ extern "C" fs_status fs_embed(const int64_t* ids, int64_t N, const void* E, int6
       !aligned(out, element(dtype)))
     return FS_ERR_INVALID_ARG;
   const Columns cols =
-      columns_of(d, rows_vec(E, lde, dtype) && rows_vec(out, ldo, dtype), 8, kLookupGroups);
+      columns_of(d, rows_vec(E, lde, dtype) && rows_vec(out, ldo, dtype), 8, kLookupGroups,
+                 kLookupGroups);
   const int64_t blocks = ceil_div(N * cols.segments, kLookupThreads / 32);
   if (blocks > INT_MAX) return FS_ERR_INVALID_ARG;
   const fs_status st = device_check();
@@ -928,13 +977,13 @@ const void* small_kernel(int y_dtype, int e_dtype) {
   return reinterpret_cast<const void*>(&small_grad_kernel<__nv_bfloat16, __nv_bfloat16, kAdd>);
 }
 
-template <bool kAdd>
+template <bool kAdd, bool kVec>
 const void* sum_kernel(int y_dtype, int e_dtype) {
   if (y_dtype == FS_F32)
-    return reinterpret_cast<const void*>(&run_sum_kernel<float, float, kAdd>);
+    return reinterpret_cast<const void*>(&run_sum_kernel<float, float, kAdd, kVec>);
   if (e_dtype == FS_F32)
-    return reinterpret_cast<const void*>(&run_sum_kernel<__nv_bfloat16, float, kAdd>);
-  return reinterpret_cast<const void*>(&run_sum_kernel<__nv_bfloat16, __nv_bfloat16, kAdd>);
+    return reinterpret_cast<const void*>(&run_sum_kernel<__nv_bfloat16, float, kAdd, kVec>);
+  return reinterpret_cast<const void*>(&run_sum_kernel<__nv_bfloat16, __nv_bfloat16, kAdd, kVec>);
 }
 template <bool kAdd>
 const void* join_kernel_of(int e_dtype) {
@@ -978,8 +1027,8 @@ extern "C" fs_status fs_embed_grad(const int64_t* ids, int64_t N, const void* dY
   if (!ids || !dY || !aligned(ids, 8) || !aligned(dY, element(y_dtype))) return FS_ERR_INVALID_ARG;
   const bool small = N <= kSmallMax;
   const int64_t run = run_length(N), n_runs = ceil_div(N, run);
-  const bool vec = rows_vec(dY, ldy, y_dtype) && rows_vec(dE, lde, e_dtype);
-  const Columns cols = columns_of(d, vec, small ? 2 : 8, 1);
+  const bool vec = d >= 8 && rows_vec(dY, ldy, y_dtype) && rows_vec(dE, lde, e_dtype);
+  const Columns cols = columns_of(d, vec, small ? 2 : 8, 1, small || vec ? 1 : 8);  // kStrided's 8
   const int64_t blocks = ceil_div(n_runs * cols.segments, kRunWarps);
   if (blocks > INT_MAX) return FS_ERR_INVALID_ARG;
   if (!workspace || !aligned(workspace, 256) ||
@@ -1050,8 +1099,10 @@ extern "C" fs_status fs_embed_grad(const int64_t* ids, int64_t N, const void* dY
   if (err == cudaSuccess && !accumulate)
     err = launch(reinterpret_cast<const void*>(&zero_kernel), fill, kSortThreads, 0, true,
                  sort_args, stream);
-  const void* sum = accumulate ? sum_kernel<true>(y_dtype, e_dtype)
-                               : sum_kernel<false>(y_dtype, e_dtype);
+  const void* sum = accumulate ? (vec ? sum_kernel<true, true>(y_dtype, e_dtype)
+                                      : sum_kernel<true, false>(y_dtype, e_dtype))
+                               : (vec ? sum_kernel<false, true>(y_dtype, e_dtype)
+                                      : sum_kernel<false, false>(y_dtype, e_dtype));
   const void* join = accumulate ? join_kernel_of<true>(e_dtype) : join_kernel_of<false>(e_dtype);
   void* args[] = {&rp};
   if (err == cudaSuccess) err = launch(sum, blocks, kRunThreads, 0, true, args, stream);

@@ -339,3 +339,21 @@ def test_tables_past_32_bits():
         fs.fs_embed_grad(ids, dY, V, out=dE, accumulate=True)
         assert torch.equal(dE.float(), 2 * sums)
         del dE
+
+
+@pytest.mark.parametrize("ty,to", COMBOS)
+@pytest.mark.parametrize("d,ld", [(1, 1), (5, 5), (7, 8), (31, 33), (33, 33), (255, 255), (256, 257),
+                                  (263, 263), (300, 301), (513, 515)])
+def test_gradient_of_unaligned_rows(ty, to, d, ld):
+    """Rows that do not start on 16-byte boundaries, of dY or of the table."""
+    N, V = 2500, 600
+    for kind in ("ragged", "few"):
+        ids = some_ids(kind, N, V, seed=d)
+        for dY_ld, out_ld in ((ld, ld), ((d + 7) // 8 * 8, ld), (ld, (d + 7) // 8 * 8)):
+            dY, _ = matrix(N, d, ty, ld=dY_ld, seed=d)
+            old, buf = matrix(V, d, to, ld=out_ld, seed=3)
+            check_gradient(ids, dY, V, scale=0.5, out=old, accumulate=True)
+            old, buf = matrix(V, d, to, ld=out_ld, seed=3)
+            check_gradient(ids, dY, V, out=old)
+            assert bool((buf[V * out_ld:] == 5.0).all())  # behind the last row
+            assert bool((buf[:V * out_ld].view(V, out_ld)[:, d:] == 5.0).all())  # between rows
