@@ -3,7 +3,8 @@
 //
 // Lookup: a copy bound by memory; a warp takes 2 KB of one row, 64 bytes a
 // lane in flight (16384 ids at d = 5120, bf16: 35 us with what L2 holds, 42 with
-// none of it, 5.8 TB/s).
+// none of it, 5.8 TB/s), or 16 columns a lane, one at a time, of rows that are not
+// aligned (16384 ids at d = 5119: 65 us, 114 with 4 at a time; d = 5120 52).
 //
 // Gradient, up to 1024 ids, one kernel (512 ids, d = 256: 11.1 us, 13.1 by the
 // kernels below; 1024 ids, d = 2048: 14.7, 14.3): every CTA sorts the (id, position)
@@ -100,6 +101,14 @@ struct Piece<float, 8> {
     f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
   }
 };
+template <>
+struct Piece<float, 4> {
+  float4 v;
+  __device__ __forceinline__ void load(const float* p) { v = *reinterpret_cast<const float4*>(p); }
+  __device__ __forceinline__ void get(float (&f)[4]) const {
+    f[0] = v.x, f[1] = v.y, f[2] = v.z, f[3] = v.w;
+  }
+};
 template <typename T>
 __device__ __forceinline__ void store(T* p, const float (&f)[1]) {
   put(p, f[0]);
@@ -109,6 +118,9 @@ __device__ __forceinline__ void store(__nv_bfloat16* p, const float (&f)[2]) {
 }
 __device__ __forceinline__ void store(float* p, const float (&f)[2]) {
   *reinterpret_cast<float2*>(p) = make_float2(f[0], f[1]);
+}
+__device__ __forceinline__ void store(float* p, const float (&f)[4]) {
+  *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
 }
 __device__ __forceinline__ void store(__nv_bfloat16* p, const float (&f)[8]) {
   __nv_bfloat162 h[4];
@@ -179,22 +191,23 @@ __host__ Columns columns_of(int64_t d, bool vec, int C, int groups, int R) {
 // Lookup
 // ---------------------------------------------------------------------------
 constexpr int kLookupThreads = 128;
-constexpr int kLookupGroups = 4;
+constexpr int kLookupGroups = 4;    // of 16 bytes a lane
+constexpr int kLookupSingles = 16;  // of one column a lane
 
 // G pieces of C columns from col0, 32 C apart, of one row.
-template <typename T, int C>
+template <typename T, int C, int G>
 __device__ __forceinline__ void lookup_piece(const T* src, T* dst, int col0, int end, bool held,
                                              float scale) {
-  Piece<T, C> piece[kLookupGroups];
+  Piece<T, C> piece[G];
   if (held) {
 #pragma unroll
-    for (int g = 0; g < kLookupGroups; ++g) {
+    for (int g = 0; g < G; ++g) {
       const int col = col0 + g * 32 * C;
-      piece[g].load(src + (col < end ? col : 0));  // always a column of the row
+      if (col < end) piece[g].load(src + col);
     }
   }
 #pragma unroll
-  for (int g = 0; g < kLookupGroups; ++g) {
+  for (int g = 0; g < G; ++g) {
     const int col = col0 + g * 32 * C;
     if (col >= end) break;
     float v[C] = {};
@@ -212,6 +225,7 @@ __global__ void __launch_bounds__(kLookupThreads)
     lookup_kernel(const int64_t* __restrict__ ids, int64_t N, const T* __restrict__ E, int32_t V,
                   int64_t lde, float scale, int64_t vocab_offset, T* __restrict__ out,
                   int64_t ldo, const Columns cols) {
+  constexpr int C = 16 / sizeof(T);
   const int lane = threadIdx.x & 31;
   const int64_t item = (int64_t(blockIdx.x) * kLookupThreads + threadIdx.x) >> 5;
   const int64_t n = item / cols.segments;
@@ -222,11 +236,12 @@ __global__ void __launch_bounds__(kLookupThreads)
   const T* src = E + (held ? id : 0) * lde;
   T* dst = out + n * ldo;
   if (seg < cols.vec_segments)
-    lookup_piece<T, 8>(src, dst, seg * (256 * kLookupGroups) + lane * 8, cols.vec, held, scale);
+    lookup_piece<T, C, kLookupGroups>(src, dst, seg * (32 * C * kLookupGroups) + lane * C,
+                                      cols.vec, held, scale);
   else
-    lookup_piece<T, 1>(src, dst,
-                       cols.vec + (seg - cols.vec_segments) * (32 * kLookupGroups) + lane, cols.d,
-                       held, scale);
+    lookup_piece<T, 1, kLookupSingles>(
+        src, dst, cols.vec + (seg - cols.vec_segments) * (32 * kLookupSingles) + lane, cols.d,
+        held, scale);
 }
 
 // ---------------------------------------------------------------------------
@@ -935,8 +950,9 @@ extern "C" fs_status fs_embed(const int64_t* ids, int64_t N, const void* E, int6
       !aligned(out, element(dtype)))
     return FS_ERR_INVALID_ARG;
   const Columns cols =
-      columns_of(d, rows_vec(E, lde, dtype) && rows_vec(out, ldo, dtype), 8, kLookupGroups,
-                 kLookupGroups);
+      columns_of(d, rows_vec(E, lde, dtype) && rows_vec(out, ldo, dtype),
+                 int(16 / element(dtype)), kLookupGroups,
+                 kLookupSingles);
   const int64_t blocks = ceil_div(N * cols.segments, kLookupThreads / 32);
   if (blocks > INT_MAX) return FS_ERR_INVALID_ARG;
   const fs_status st = device_check();
