@@ -980,8 +980,13 @@ namespace {
 //   4099 ids, d = 2048   22.2 / 21.4 / 25.4 / 37.9    12000 ids  44.7 / 39.0 / 39.0 / 51.3
 //   (4099 with nothing in L2 24.2 / 25.1)
 //   16384 ids, d = 2048  63.0 / 47.3 / 45.1           32768 ids, d = 4096  178 / 143 / 131 / 123
-int64_t run_length(int64_t N) {
-  return N <= kSmallMax ? 32 : N <= 5000 ? 16 : N <= 12000 ? 32 : N <= 20000 ? 64 : 128;
+//   16384 ids, d = 512   36.1 / 32.8 / 36.2 / 47.9    32768 ids, d = 256    - /  50 /  56 /  69
+// (the last two: a warp takes 256 columns, so long runs leave too few warps).
+int64_t run_length(int64_t N, int64_t d) {
+  if (N <= kSmallMax) return 32;
+  int64_t run = N <= 5000 ? 16 : N <= 12000 ? 32 : N <= 20000 ? 64 : 128;
+  while (run > 16 && N / run * ceil_div(d, 256) < 1000) run /= 2;
+  return run;
 }
 
 template <bool kAdd>
@@ -1015,7 +1020,7 @@ const void* join_kernel_of(int e_dtype) {
 extern "C" size_t fs_embed_grad_workspace_size(int64_t N, int64_t d) {
   if (N < 1 || !sizes_ok(N, 1, d, 0)) return 0;
   return 4 * round256(size_t(N) * 4u) +
-         round256(size_t(ceil_div(N, run_length(N))) * 2u * size_t(partial_ld(d)) * 4u);
+         round256(size_t(ceil_div(N, run_length(N, d))) * 2u * size_t(partial_ld(d)) * 4u);
 }
 
 extern "C" fs_status fs_embed_grad(const int64_t* ids, int64_t N, const void* dY, int64_t V,
@@ -1042,7 +1047,7 @@ extern "C" fs_status fs_embed_grad(const int64_t* ids, int64_t N, const void* dY
   }
   if (!ids || !dY || !aligned(ids, 8) || !aligned(dY, element(y_dtype))) return FS_ERR_INVALID_ARG;
   const bool small = N <= kSmallMax;
-  const int64_t run = run_length(N), n_runs = ceil_div(N, run);
+  const int64_t run = run_length(N, d), n_runs = ceil_div(N, run);
   const bool vec = d >= 8 && rows_vec(dY, ldy, y_dtype) && rows_vec(dE, lde, e_dtype);
   const Columns cols = columns_of(d, vec, small ? 2 : 8, 1, small || vec ? 1 : 8);  // kStrided's 8
   const int64_t blocks = ceil_div(n_runs * cols.segments, kRunWarps);
