@@ -147,7 +147,9 @@ Mask mask_of(PyObject* o, const Head& s) {
   if (t.scalar_type() != at::kInt || t.device() != s.dev || t.dim() != 2 || t.size(0) != s.B ||
       t.size(1) < (s.V + 31) / 32 || t.stride(1) != 1)
     refuse("vocab_mask must be an int32 matrix [B, >= ceil(V/32)] on " + s.dev.str());
-  return {t.data_ptr(), std::max(t.stride(0), t.size(1))};
+  // A stride below the row's words (0 for one mask expanded to all rows) is the
+  // library's to refuse; a single row's is never used.
+  return {t.data_ptr(), s.B > 1 ? t.stride(0) : t.size(1)};
 }
 
 struct Workspace {

@@ -554,3 +554,40 @@ def test_gradient_whose_logits_pass_32_bits():
     p = (Wd[ids] @ Hd.T - f.lse.double()).exp()  # lse's own error is in the bound
     hot = (ids.unsqueeze(1) == t.unsqueeze(0)).double()
     compare(dW[ids], p, hot, a.double(), Hd, B, "dW")
+
+
+# --------------------------------------------------------------------------- masks' row strides
+def test_masks_whose_rows_overlap_are_refused():
+    """One row of allow-bits expanded to all rows, and rows closer than their words:
+    the library has no stride for the first and must not make one up."""
+    B, V = 4, 500
+    p = problem(B, 64, V, mask_frac=0.1, seed=90)
+    words = p["vocab_mask"].shape[1]
+    flat = p["vocab_mask"].reshape(-1)
+    f = fs.fs_logprobs(p["H"], p["W"], p["tokens"])
+    for mask in (p["vocab_mask"][:1].expand(B, -1),
+                 torch.as_strided(flat, (B, words), (words - 1, 1))):
+        with pytest.raises(fs.FsError):
+            fs.fs_logprobs(p["H"], p["W"], p["tokens"], vocab_mask=mask)
+        with pytest.raises(fs.FsError):
+            fs.fs_logprobs_grad(p["H"], p["W"], p["tokens"], f.lse, f.lse, vocab_mask=mask)
+
+
+def test_masks_of_other_row_strides():
+    """Rows further apart than their words, rows wider than the vocabulary needs, a
+    single row out of an expanded mask: the same results."""
+    B, V = 5, 500
+    p = problem(B, 64, V, T="rows", mask_frac=0.3, seed=91)
+    want, _ = check_forward(p, 4)
+    mask = p["vocab_mask"]
+    wide = torch.full((B, mask.shape[1] + 7), -1, dtype=torch.int32, device="cuda")
+    wide[:, :mask.shape[1]] = mask
+    for m in (wide, wide[:, :mask.shape[1]], wide[:, :mask.shape[1] + 3]):
+        got = fs.fs_logprobs(p["H"], p["W"], p["tokens"], 4, temperature=p["temperature"],
+                             vocab_mask=m)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    one = fs.fs_logprobs(p["H"][:1], p["W"], p["tokens"][:1], 4, temperature=p["temperature"][:1],
+                         vocab_mask=mask[:1].expand(3, -1)[:1])
+    first = fs.fs_logprobs(p["H"][:1], p["W"], p["tokens"][:1], 4,
+                           temperature=p["temperature"][:1], vocab_mask=mask[:1])
+    assert all(torch.equal(a, b) for a, b in zip(one, first))
