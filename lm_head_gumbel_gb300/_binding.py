@@ -418,7 +418,9 @@ def fs_gumbel_noise(b0, nb, v0, nv, *, seed=0, offset=0, seeds=None, out=None, d
 
 # ---- the operators of fs_vocab.h ------------------------------------------
 # Keyword interfaces; _marshal.so checks the tensors, makes the results that were
-# not given and calls the library.
+# not given and calls the library.  With `stream`, what it makes (results,
+# workspaces) is allocated as under torch.cuda.stream(stream): it belongs to that
+# stream, which the user of a result on another one waits for.
 def _handle(stream):
     """A stream as _marshal.so takes it: None (the current one) or its handle."""
     return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else stream

@@ -106,16 +106,35 @@ Matrix matrix(const char* name, const at::Tensor& t, at::ScalarType type, int64_
   return {t.data_ptr(), n > 1 ? t.stride(0) : std::max(t.stride(0), (d + 7) / 8 * 8)};
 }
 
-// A new tensor from torch's caching allocator, in the order of the current stream.
+// A new tensor from torch's caching allocator, in the order of the call's stream (On).
 at::Tensor empty(at::IntArrayRef sizes, at::ScalarType type, c10::Device dev) {
   return at::detail::empty_cuda(sizes, type, dev, std::nullopt);
 }
 
-// The stream handle of an int, or the device's current stream for None.
-void* stream_of(PyObject* o, c10::Device dev) {
-  if (o != Py_None) return reinterpret_cast<void*>(static_cast<intptr_t>(integer(o)));
-  return c10::cuda::getCurrentCUDAStream(dev.index()).stream();
-}
+// Makes a call's device and stream current while it is alive: the stream of a handle,
+// or the device's current one for None.  What is allocated meanwhile belongs to that
+// stream, so its memory has no other stream's work pending, and a workspace may be
+// freed while the kernels still run.
+class On {
+ public:
+  On(PyObject* stream, c10::Device dev) : device_(dev) {
+    const c10::cuda::CUDAStream current = c10::cuda::getCurrentCUDAStream(dev.index());
+    handle_ = current.stream();
+    if (stream == Py_None) return;
+    handle_ = reinterpret_cast<cudaStream_t>(static_cast<intptr_t>(integer(stream)));
+    if (handle_ == current.stream()) return;
+    // 0 and cudaStreamLegacy are the same stream, torch's default one.
+    stream_.reset_stream(handle_ == nullptr || handle_ == cudaStreamLegacy
+                             ? c10::cuda::getDefaultCUDAStream(dev.index())
+                             : c10::cuda::getStreamFromExternal(handle_, dev.index()));
+  }
+  void* handle() const { return handle_; }
+
+ private:
+  c10::cuda::OptionalCUDAGuard device_;
+  c10::cuda::OptionalCUDAStreamGuard stream_;
+  cudaStream_t handle_;
+};
 
 void check(const char* name, int status) {
   if (status != FS_OK) throw Refused{status, name};
@@ -153,7 +172,7 @@ Mask mask_of(PyObject* o, const Head& s) {
 }
 
 struct Workspace {
-  at::Tensor made;  // may be freed after the call: reused in stream order
+  at::Tensor made;  // freed after the call: reused in the order of its stream (On)
   void* data = nullptr;
   size_t bytes = 0;
 };
@@ -253,7 +272,7 @@ PyObject* py_logprobs(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (K < 0 || K > FS_LOGPROBS_TOPK_MAX)
       refuse("K must be 0 to " + std::to_string(FS_LOGPROBS_TOPK_MAX));
     const Mask m = mask_of(a[5], s);
-    const c10::cuda::OptionalCUDAGuard on(s.dev);
+    const On on(a[13], s.dev);
     Result logp{a[2] == Py_None ? nullptr : a[7], {}}, entropy{a[8], {}}, lse{a[9], {}};
     Result idx{K > 0 ? a[10] : nullptr, {}}, top{K > 0 ? a[11] : nullptr, {}};
     fs_logprobs_args p = {};
@@ -284,7 +303,7 @@ PyObject* py_logprobs(PyObject*, PyObject* const* a, Py_ssize_t n) {
     p.workspace = ws.data;
     p.workspace_bytes = ws.bytes;
     p.flags = uint32_t(integer(a[14]));
-    check("fs_logprobs", g.logprobs(&p, stream_of(a[13], s.dev)));
+    check("fs_logprobs", g.logprobs(&p, on.handle()));
     return tuple_of({&logp, &entropy, &lse, &idx, &top});
   });
 }
@@ -308,7 +327,7 @@ PyObject* py_logprobs_grad(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (!need_dH && !need_dW) refuse("neither dH nor dW is asked for");
     if (a[6] != Py_None && a[5] == Py_None) refuse("grad_entropy needs entropy");
     const Mask m = mask_of(a[8], s);
-    const c10::cuda::OptionalCUDAGuard on(s.dev);
+    const On on(a[15], s.dev);
     Result dH{need_dH ? a[10] : nullptr, {}}, dW{need_dW ? a[11] : nullptr, {}};
     fs_logprobs_grad_args p = {};
     p.H = s.h.data;
@@ -344,7 +363,7 @@ PyObject* py_logprobs_grad(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const Workspace ws = workspace_of(a[14], g.grad_size(s.B, s.d, s.V), s.dev);
     p.workspace = ws.data;
     p.workspace_bytes = ws.bytes;
-    check("fs_logprobs_grad", g.grad(&p, stream_of(a[15], s.dev)));
+    check("fs_logprobs_grad", g.grad(&p, on.handle()));
     return tuple_of({&dH, &dW});
   });
 }
@@ -368,7 +387,7 @@ PyObject* py_embed(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int64_t N = ids.dim() == 1 ? ids.size(0) : -1;
     const auto* id = static_cast<const int64_t*>(vector("ids", a[0], at::kLong, N, dev));
     const Matrix e = matrix("E", E, E.scalar_type(), V, d, dev);
-    const c10::cuda::OptionalCUDAGuard on(dev);
+    const On on(a[5], dev);
     Result out{a[4], {}};
     Matrix o{nullptr, d};
     if (a[4] == Py_None) {
@@ -378,7 +397,7 @@ PyObject* py_embed(PyObject*, PyObject* const* a, Py_ssize_t n) {
       o = matrix("out", tensor("out", a[4]), E.scalar_type(), N, d, dev);
     }
     check("fs_embed", g.embed(id, N, e.data, V, d, e.ld, code, float(real(a[2])), integer(a[3]),
-                              o.data, o.ld, stream_of(a[5], dev)));
+                              o.data, o.ld, on.handle()));
     return out.wrap();
   });
 }
@@ -394,7 +413,7 @@ PyObject* py_embed_grad(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const bool accumulate = truth(a[6]);
     const Matrix y = matrix("dY", dY, dY.scalar_type(), N, d, dev);
     const auto* id = static_cast<const int64_t*>(vector("ids", a[0], at::kLong, N, dev));
-    const c10::cuda::OptionalCUDAGuard on(dev);
+    const On on(a[9], dev);
     Result out{a[5], {}};
     if (a[5] == Py_None) {
       if (accumulate) refuse("accumulate needs out");
@@ -408,7 +427,7 @@ PyObject* py_embed_grad(PyObject*, PyObject* const* a, Py_ssize_t n) {
     check("fs_embed_grad",
           g.embed_grad(id, N, y.data, V, d, y.ld, y_code, float(real(a[3])), integer(a[4]), e.data,
                        e.ld, e_code, accumulate ? 1 : 0, ws.data, ws.bytes,
-                       stream_of(a[9], dev)));
+                       on.handle()));
     return out.wrap();
   });
 }

@@ -357,3 +357,27 @@ def test_gradient_of_unaligned_rows(ty, to, d, ld):
             check_gradient(ids, dY, V, out=old)
             assert bool((buf[V * out_ld:] == 5.0).all())  # behind the last row
             assert bool((buf[:V * out_ld].view(V, out_ld)[:, d:] == 5.0).all())  # between rows
+
+
+def test_workspaces_of_two_streams():
+    """Gradients on two streams, neither waited for, with workspaces made inside."""
+    V, N, d = 3000, 6000, 256
+    cases = []
+    for seed in (40, 41):
+        dY, _ = matrix(N, d, torch.bfloat16, seed=seed)
+        cases.append((some_ids("spread", N, V, seed).cuda(), dY))
+    want = [fs.fs_embed_grad(ids, dY, V, out_dtype=torch.float32) for ids, dY in cases]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = []
+    for _ in range(4):
+        for (ids, dY), stream, w in zip(cases, streams, want):
+            got.append((fs.fs_embed_grad(ids, dY, V, out_dtype=torch.float32, stream=stream), w))
+        scratch = [torch.full((1 << 20,), 255, dtype=torch.uint8, device="cuda")
+                   for _ in range(4)]  # the current stream's allocations meanwhile
+    torch.cuda.synchronize()
+    del scratch
+    assert all(torch.equal(g, w) for g, w in got)
+    owner = {seg["stream"] for g, _ in got[:1] for seg in torch.cuda.memory_snapshot()
+             if seg["address"] <= g.data_ptr() < seg["address"] + seg["total_size"]}
+    assert owner == {streams[0].cuda_stream}

@@ -591,3 +591,66 @@ def test_masks_of_other_row_strides():
     first = fs.fs_logprobs(p["H"][:1], p["W"], p["tokens"][:1], 4,
                            temperature=p["temperature"][:1], vocab_mask=mask[:1])
     assert all(torch.equal(a, b) for a, b in zip(one, first))
+
+
+# --------------------------------------------------------------------------- memory of the stream's own
+def pool_of(t):
+    """The stream whose blocks of the caching allocator `t` lies in."""
+    at = t.data_ptr()
+    for segment in torch.cuda.memory_snapshot():
+        if segment["address"] <= at < segment["address"] + segment["total_size"]:
+            return segment["stream"]
+    raise AssertionError("not the allocator's")
+
+
+def test_results_and_workspaces_belong_to_the_given_stream():
+    """Results lie in the given stream's blocks, whether it is given as a stream, a
+    handle or 0; the workspace does too: nothing is taken from the current
+    stream's blocks, where it could be handed out again while the kernels run."""
+    p = problem(200, 128, 3000, seed=92)
+    side = torch.cuda.Stream()
+    f = fs.fs_logprobs(p["H"], p["W"], p["tokens"])
+    torch.cuda.synchronize()
+    for stream, owner in ((side, side.cuda_stream), (side.cuda_stream, side.cuda_stream), (0, 0)):
+        r = fs.fs_logprobs(p["H"], p["W"], p["tokens"], 3, stream=stream)
+        g = fs.fs_logprobs_grad(p["H"], p["W"], p["tokens"], f.lse, f.lse, stream=stream)
+        torch.cuda.synchronize()
+        assert [pool_of(t) for t in (*r, *g)] == [owner] * 7
+    with torch.cuda.stream(side):  # the current stream is another than the given one
+        r = fs.fs_logprobs(p["H"], p["W"], p["tokens"], 3, stream=0)
+        torch.cuda.synchronize()
+        assert torch.cuda.current_stream() == side and pool_of(r.lse) == 0
+    # The workspace, freed on return, left its block to the given stream.
+    need = fs.fs_logprobs_grad_workspace_size(200, 128, 3000)
+    fresh = torch.cuda.Stream()
+    g = fs.fs_logprobs_grad(p["H"], p["W"], p["tokens"], f.lse, f.lse, stream=fresh)
+    torch.cuda.synchronize()
+    sizes = [segment["total_size"] for segment in torch.cuda.memory_snapshot()
+             if segment["stream"] == fresh.cuda_stream]
+    assert sum(sizes) >= need + 2 * (g[0].numel() + g[1].numel())
+
+
+def test_two_streams_at_once():
+    """Calls on two streams, none waited for, their workspaces made inside: each as alone."""
+    p = problem(300, 512, 40000, T="rows", seed=93)
+    q = problem(96, 512, 40000, T="rows", seed=94)
+    a, e = upstream(300, True, 93)
+    call = lambda x, **kw: fs.fs_logprobs(x["H"], x["W"], x["tokens"], 10,
+                                          temperature=x["temperature"], **kw)
+    f = call(p)
+    grad = lambda **kw: fs.fs_logprobs_grad(p["H"], p["W"], p["tokens"], f.lse, a,
+                                            entropy=f.entropy, grad_entropy=e,
+                                            temperature=p["temperature"], **kw)
+    want = [tuple(call(p)), tuple(call(q)), grad()]
+    torch.cuda.synchronize()
+    one, two = torch.cuda.Stream(), torch.cuda.Stream()
+    got = []
+    for _ in range(4):
+        got.append([tuple(call(p, stream=one)), tuple(call(q, stream=two)), grad(stream=one)])
+        scratch = [torch.full((1 << 20,), 255, dtype=torch.uint8, device="cuda")
+                   for _ in range(8)]  # the current stream's allocations meanwhile
+    torch.cuda.synchronize()
+    del scratch
+    for r in got:
+        for x, y in zip(r, want):
+            assert all(torch.equal(s, t) for s, t in zip(x, y))
