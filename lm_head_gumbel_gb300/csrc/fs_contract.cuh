@@ -136,6 +136,36 @@ __host__ __device__ constexpr int slices() {
   return kBN / Epi::kN;
 }
 
+// Ring stages for a box of `a_bytes` of A per slice.  An MMA reads kBM rows of A, 16 KB,
+// whatever the box holds (rows past it feed accumulator rows that no epilogue reads),
+// so the ring leaves room for the last slice's: with a short box and 64 columns of B
+// that reach goes past the slice (48 rows: 2 KB; 3 stages of 4 slices instead of 4).
+template <class Epi, bool kPair>
+__host__ __device__ constexpr uint32_t ring_stages(uint32_t a_bytes) {
+  const uint32_t slice = a_bytes + (kPair ? Epi::kN / 2 : Epi::kN) * kBK * 2;
+  const uint32_t a_read = kBM * kBK * 2;
+  const uint32_t past = a_read > slice ? a_read - slice : 0;
+  const uint32_t n = (ring_bytes<Epi>() - past) / (slices<Epi>() * slice);
+  return n < kMaxStages ? n : kMaxStages;
+}
+// Where the MMAs' reads of the ring end, from its start.
+template <class Epi, bool kPair>
+__host__ __device__ constexpr uint32_t ring_reach(uint32_t a_bytes) {
+  const uint32_t slice = a_bytes + (kPair ? Epi::kN / 2 : Epi::kN) * kBK * 2;
+  const uint32_t a_read = kBM * kBK * 2;
+  const uint32_t all = ring_stages<Epi, kPair>(a_bytes) * slices<Epi>() * slice;
+  return all - slice + (slice > a_read ? slice : a_read);
+}
+// For every height of A's box (8 rows to kBM): at least two stages, in the ring.
+template <class Epi, bool kPair>
+__host__ __device__ constexpr bool ring_fits() {
+  for (uint32_t rows = 8; rows <= kBM; rows += 8)
+    if (ring_stages<Epi, kPair>(rows * 128u) < 2 ||
+        ring_reach<Epi, kPair>(rows * 128u) > ring_bytes<Epi>())
+      return false;
+  return true;
+}
+
 enum : uint32_t { kPolicyNormal = 0, kPolicyFirst = 1, kPolicyLast = 2 };
 
 struct Shape {
@@ -275,6 +305,7 @@ __device__ __forceinline__ void contract(const CUtensorMap& tmap_a, const CUtens
   constexpr int kN = Epi::kN;
   constexpr uint32_t kTmemCols = 2 * kN;
   static_assert(kN == 256 || (!kPair && !kBmn && (kN == 64 || kN == 128)), "unit columns");
+  static_assert(ring_fits<Epi, kPair>(), "MMAs read no further than the ring");
   constexpr int kBRows = kN / kCtas;  // B rows in this CTA's shared memory
   constexpr uint32_t kBBytes = kBRows * kBK * 2;
   constexpr int kS = slices<Epi>();

@@ -1049,7 +1049,7 @@ void fill_ring(const Device& dev, Shape& s) {
   constexpr uint32_t kBBytes = (kPair ? Epi::kN / 2 : Epi::kN) * kBK * 2;
   s.a_bytes = kAmn ? kBM * kBK * 2 : s.a_box_rows * 128u;
   s.stage_bytes = slices<Epi>() * (s.a_bytes + kBBytes);
-  s.n_stages = std::min<uint32_t>(kMaxStages, ring_bytes<Epi>() / s.stage_bytes);
+  s.n_stages = ring_stages<Epi, kPair>(s.a_bytes);
   s.wait_limit_ns = kWaitLimitNs;
   s.error_word = dev.error_word;
 }

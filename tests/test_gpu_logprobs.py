@@ -654,3 +654,10 @@ def test_two_streams_at_once():
     for r in got:
         for x, y in zip(r, want):
             assert all(torch.equal(s, t) for s, t in zip(x, y))
+
+
+@pytest.mark.parametrize("B", [7, 8, 17, 24, 25, 41, 48, 49, 57, 65])
+def test_box_heights_of_narrow_units(B):
+    """Units of 64 ids with every slice of every stage in use: short boxes of H."""
+    check_forward(problem(B, 2120, 1500, T="rows", seed=100 + B), 5)
+    check_forward(problem(B, 1100, 9000, T="rows", seed=101 + B), 0)

@@ -195,3 +195,41 @@ def test_embed_grad_bad_arguments(lib, kw, want):
 
 def test_embed_grad_of_nothing_added(lib):
     assert _call_grad(lib, N=0, ids=None, dY=None, accumulate=1, ws=None, wsb=0) == 0
+
+
+def test_matrix_reads_stay_in_the_ring(tmp_path):
+    """An MMA reads 128 rows of A, 16 KB, however few the box in shared memory holds:
+    the last slice's read ends inside the ring for every box height and unit width."""
+    from lm_head_gumbel_gb300 import build as libbuild
+    src = tmp_path / "ring.cu"
+    src.write_text("""
+#include <cstdio>
+#include "fs_contract.cuh"
+using namespace fs::vocab;
+template <int N, bool kSt> struct Epi { static constexpr int kN = N; static constexpr bool kStaged = kSt; };
+template <class E, bool kPair> void print() {
+  for (unsigned rows = 8; rows <= 128; rows += 8)
+    std::printf("%d %d %u %u %u %d\\n", E::kN, int(kPair), rows, ring_stages<E, kPair>(rows * 128u),
+                ring_bytes<E>(), slices<E>());
+}
+int main() {
+  print<Epi<64, false>, false>(); print<Epi<128, false>, false>(); print<Epi<256, false>, false>();
+  print<Epi<256, false>, true>(); print<Epi<128, true>, false>(); print<Epi<256, true>, false>();
+  print<Epi<256, true>, true>();
+}
+""")
+    exe = tmp_path / "ring"
+    try:
+        nvcc = libbuild.nvcc_path()
+    except RuntimeError as e:
+        pytest.skip(str(e))
+    subprocess.run([nvcc, *libbuild.ARCH_FLAGS, "-std=c++17", f"-I{libbuild.CSRC}",
+                    f"-I{libbuild.INCLUDE}", "-o", str(exe), str(src)], check=True)
+    out = subprocess.run([str(exe)], capture_output=True, text=True, check=True).stdout
+    lines = [[int(x) for x in line.split()] for line in out.splitlines()]
+    assert len(lines) == 7 * 16
+    for n, pair, rows, stages, ring, slices in lines:
+        piece = rows * 128 + (n // 2 if pair else n) * 128  # A's box and B's columns, bf16 x 64
+        last = (stages * slices - 1) * piece
+        assert 2 <= stages <= 8
+        assert last + max(piece, 128 * 128) <= ring, (n, pair, rows)
