@@ -427,6 +427,9 @@ __device__ void sort_cluster_small(const SortParams& p, uint32_t rank, SmallClus
   const int bins = 1 << p.bits;
   const int warps = (n + 31) / 32;
   const bool has = tid < n;
+  // Every CTA has started before any writes to another's shared memory; the first
+  // pass's counts are taken meanwhile.
+  ptx::cluster_arrive();
   uint32_t key = has ? row_of(p, p.ids[e0 + tid]) : 0u;
   uint32_t pos = uint32_t(e0 + tid);
   for (int pass = 0; pass < p.passes; ++pass) {
@@ -438,6 +441,7 @@ __device__ void sort_cluster_small(const SortParams& p, uint32_t rank, SmallClus
     const uint32_t earlier = __popc(peers & ((1u << lane) - 1u));
     if (has && earlier == 0u) wc[warp][digit] = uint16_t(__popc(peers));
     __syncthreads();
+    if (pass == 0) ptx::cluster_wait();
     if (tid < bins) {
       uint32_t run = 0u;
 #pragma unroll 8

@@ -381,3 +381,15 @@ def test_workspaces_of_two_streams():
     owner = {seg["stream"] for g, _ in got[:1] for seg in torch.cuda.memory_snapshot()
              if seg["address"] <= g.data_ptr() < seg["address"] + seg["total_size"]}
     assert owner == {streams[0].cuda_stream}
+
+
+@pytest.mark.parametrize("N", [1025, 1032, 2049, 8191, 8192])
+def test_cluster_sort_call_after_call(N):
+    """Sorts in one cluster's shared memory, right behind one another: CTAs that get
+    their first pairs while others of the cluster have only just started."""
+    V, d = 700, 8
+    ids = some_ids("ragged", N, V, seed=N)
+    dY, _ = matrix(N, d, torch.float32, seed=N)
+    want = check_gradient(ids, dY, V)
+    got = [fs.fs_embed_grad(ids, dY, V) for _ in range(50)]
+    assert all(torch.equal(g, want) for g in got)
