@@ -38,10 +38,12 @@ extern "C" {
  * The [B,V] logits never reach device memory.
  *
  * The logits of the token and of K + 4 candidates (the best by their tensor-core
- * sums, compared in 17 bits) are summed again in compensated fp32, about 45
- * bits, and ranked on that: ids whose logits differ by less than fp32 resolves
- * still come in the order of their exact logits, and the alternatives do not
- * depend on B or on how the work was split.
+ * sums in fp32, ties to the lower id) are summed again in compensated fp32, about
+ * 45 bits, and ranked on that.  So alternatives come in the order of their exact
+ * logits, also where those differ by less than fp32 resolves, and do not depend on
+ * B or on how the work was split.  One of the K largest is missed only where K + 4
+ * other ids' fp32 sums are no smaller than its own: where more than 4 ids lie within
+ * those sums' error (about 1e-6 of the sum of |H W|) of the K-th.
  *
  * Conventions: T_b <= 0, NaN or +inf (greedy rows of the sampler) means T = 1.
  * A token below 0 means "no token": logp 0.  A token that the mask clears, or

@@ -112,19 +112,16 @@ __device__ __forceinline__ float pick32(const uint32_t (&v)[32], uint32_t j) {
 
 // A logit as a sort key: an order-preserving unsigned integer whose low 7 bits
 // hold 127 - j, so that of equal values the one at the lower column j < 128 is
-// the greater.  The value's own low 7 bits go (it is rounded down to 17 bits):
-// lists only choose candidates, four more than asked for, whose logits are
-// summed again.  0: no candidate (-inf, NaN).
+// the greater.  The value's own low 7 bits go (it is rounded down to 17 bits), so
+// keys only show an order between different steps of 2^-16 of the value: see
+// ScoreEpi::fill.  0: no candidate (-inf, NaN).
 __device__ __forceinline__ uint32_t sort_key(uint32_t bits, int j) {
   const float f = __uint_as_float(bits) + 0.0f;  // -0 counts as +0
   const uint32_t b = __float_as_uint(f);
   const uint32_t u = b ^ (uint32_t(int32_t(b) >> 31) | 0x80000000u);
   return f > -INFINITY ? (u & ~127u) | uint32_t(127 - j) : 0u;
 }
-__device__ __forceinline__ float key_value(uint32_t key) {
-  const uint32_t u = key & ~127u;
-  return __uint_as_float((u & 0x80000000u) ? u ^ 0x80000000u : ~u);
-}
+__device__ __forceinline__ int key_column(uint32_t key) { return 127 - int(key & 127u); }
 
 // Bitonic networks on 32 keys in registers, largest first.
 __device__ __forceinline__ void order_pair(uint32_t& a, uint32_t& b) {
@@ -228,6 +225,75 @@ struct ScoreEpi {
     }
     st.m = m;
   }
+  // The list from the first unit's logits: sorted by key, 32 at a time, and merged; then
+  // the values of the KC + 4 best keys are fetched (by their columns, from a copy of each
+  // chunk in local memory) and put in order where they share a step.  False, with the
+  // list empty, if for some lane 4 keys more than it keeps share the step of the last
+  // it keeps: a larger logit may have been dropped.  Inserting one by one, as is done
+  // then, takes 28 us a call at KC = 24 where a CTA has one unit, this 6; sorting
+  // whole values with their columns (64-bit keys) took 20.
+  static __device__ __forceinline__ bool fill(const Params& p, State& st, const TileAt& at,
+                                              const AllowWords& allow, bool valid) {
+    constexpr int kFetch = KC + 4;
+    uint32_t best[32];
+#pragma unroll
+    for (int i = 0; i < 32; ++i) best[i] = 0u;
+#pragma unroll 1
+    for (int c = 0; c < kN / 64; ++c) {
+      if (at.col0 + c * 32 >= p.V) break;
+      uint32_t r[32];
+      ptx::tmem_ld_32x32b_x32(at.taddr + uint32_t(c * 32), r);
+      ptx::tmem_wait_ld();
+      const uint32_t w = valid ? allow.at(c) : 0u;
+#pragma unroll
+      for (int j = 0; j < 32; ++j) r[j] = ((w >> j) & 1u) ? sort_key(r[j], c * 32 + j) : 0u;
+      sort32(r);
+      merge32(best, r);
+    }
+    const bool open = best[kFetch] != 0u && (best[kFetch] ^ best[KC - 1]) < 128u;
+    if (__any_sync(0xFFFFFFFFu, open)) return false;
+    float v[kFetch];
+#pragma unroll
+    for (int q = 0; q < kFetch; ++q) v[q] = -INFINITY;
+#pragma unroll 1
+    for (int c = 0; c < kN / 64; ++c) {
+      if (at.col0 + c * 32 >= p.V) break;
+      uint32_t r[32];
+      ptx::tmem_ld_32x32b_x32(at.taddr + uint32_t(c * 32), r);
+      ptx::tmem_wait_ld();
+#pragma unroll
+      for (int q = 0; q < kFetch; ++q) {
+        const int col = key_column(best[q]);
+        if (best[q] != 0u && (col >> 5) == c) v[q] = __uint_as_float(r[col & 31]) + 0.0f;
+      }
+    }
+    // Neighbours of one step change places, at most kFetch rounds; equal values stay in
+    // the order of their columns.
+    while (true) {
+      bool rising = false;
+#pragma unroll
+      for (int q = 0; q + 1 < kFetch; ++q) rising |= v[q] < v[q + 1];
+      if (!__any_sync(0xFFFFFFFFu, rising)) break;
+#pragma unroll
+      for (int odd = 0; odd < 2; ++odd)
+#pragma unroll
+        for (int q = odd; q + 1 < kFetch; q += 2) {
+          const bool swap = v[q] < v[q + 1];
+          const float a = v[q], b = v[q + 1];
+          const uint32_t ka = best[q], kb = best[q + 1];
+          v[q] = swap ? b : a;
+          v[q + 1] = swap ? a : b;
+          best[q] = swap ? kb : ka;
+          best[q + 1] = swap ? ka : kb;
+        }
+    }
+#pragma unroll
+    for (int q = 0; q < KC; ++q) {
+      st.ts[q] = v[q];
+      st.ti[q] = best[q] != 0u ? at.col0 + key_column(best[q]) : -1;
+    }
+    return true;
+  }
   template <class Release>
   static __device__ __forceinline__ void tile(const Params& p, State& st, const TileAt& at,
                                               int lane, uint8_t*, const void*, const Shape& s,
@@ -251,32 +317,10 @@ struct ScoreEpi {
       else
         chunk<true>(st, r, w);
     };
-    if (KC > 0 && st.first) {
-      // The first unit fills the list: its logits are sorted, 32 at a time, and
-      // merged (inserting them one by one took 28 us a call at KC = 24 where a
-      // CTA has one unit, this 4).
-      uint32_t best[32];
-#pragma unroll
-      for (int i = 0; i < 32; ++i) best[i] = 0u;
-#pragma unroll 1
-      for (int c = 0; c < kN / 64; ++c) {
-        if (at.col0 + c * 32 >= p.V) break;
-        uint32_t r[32];
-        load(c, r);
-#pragma unroll
-        for (int j = 0; j < 32; ++j) r[j] = sort_key(r[j], c * 32 + j);
-        sort32(r);
-        merge32(best, r);
-      }
+    bool filled = false;
+    if constexpr (KC > 0) {
+      if (st.first) filled = fill(p, st, at, allow, valid);
       st.first = false;
-#pragma unroll
-      for (int q = 0; q < KC; ++q) {
-        const uint32_t key = best[q];
-        st.ts[q] = key != 0u ? key_value(key) : -INFINITY;
-        st.ti[q] = key != 0u ? at.col0 + 127 - int(key & 127u) : -1;
-      }
-      release();
-      return;
     }
 #pragma unroll 1
     for (int c = 0; c < kN / 64; ++c) {
@@ -284,6 +328,7 @@ struct ScoreEpi {
       uint32_t r[32];
       load(c, r);
       if constexpr (KC > 0) {
+        if (filled) continue;
         // Every lane marks the logits that beat its list's last entry; the
         // warp then inserts one per lane and round, lowest id first.  (An
         // entry of the row's best is among the best of any subset holding it.)
@@ -297,7 +342,7 @@ struct ScoreEpi {
           if (want != 0u) {
             const uint32_t j = uint32_t(__ffs(want) - 1);
             want &= want - 1u;
-            const float v = key_value(sort_key(__float_as_uint(pick32(r, j)), 0));
+            const float v = pick32(r, j) + 0.0f;  // -0 counts as +0
             if (v > st.ts[KC - 1]) list_insert<KC>(st.ts, st.ti, v, at.col0 + c * 32 + int(j));
           }
         }

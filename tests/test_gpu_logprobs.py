@@ -661,3 +661,49 @@ def test_box_heights_of_narrow_units(B):
     """Units of 64 ids with every slice of every stage in use: short boxes of H."""
     check_forward(problem(B, 2120, 1500, T="rows", seed=100 + B), 5)
     check_forward(problem(B, 1100, 9000, T="rows", seed=101 + B), 0)
+
+
+@pytest.mark.parametrize("K", [1, 2, 4, 5, 12, 20])
+@pytest.mark.parametrize("B,V,at", [
+    (1, 300, "one thread"), (1, 300, "spread"), (20, 15000, "spread"), (1, 45000, "spread"),
+    (3, 90000, "far"), (150, 3000, "spread"), (150, 60000, "far")])
+def test_alternatives_close_together(B, V, at, K):
+    """30 logits 2^-9 apart at 4096, where fp32 has 2^-11: all within 2^-16 of their
+    size.  Sums of two exact terms, so tensor-core sums are exact and the order known:
+    the highest ids are the best.  "far": in the units that a worker visits later."""
+    d = 72
+    W = torch.zeros((V, d))
+    gen = torch.Generator().manual_seed(B + V + K)
+    W[:, 0] = torch.randn(V, generator=gen) * 50
+    ids = {"one thread": torch.arange(30), "spread": torch.randperm(V, generator=gen)[:30].sort().values,
+           "far": V - 30 * 61 + torch.arange(30) * 61}[at]
+    W[ids, 0] = 4096.0
+    W[ids, 40] = torch.arange(30) / 512.0
+    H = torch.zeros((B, d))
+    H[:, 0] = 1.0
+    H[:, 40] = 1.0
+    tokens = ids[torch.arange(B) % 30].cuda()
+    p = dict(H=H.bfloat16().cuda(), W=W.bfloat16().cuda(), tokens=tokens, temperature=None,
+             vocab_mask=None)
+    r, _ = check_forward(p, K)
+    assert torch.equal(r.topk_idx.cpu(), ids.flip(0)[:K].expand(B, K))
+
+
+@pytest.mark.parametrize("K", [1, 5, 20])
+@pytest.mark.parametrize("B,V", [(8, 20000), (8, 60000), (140, 20000)])
+def test_alternatives_beside_a_common_offset(B, V, K):
+    """Logits of 60 and a deviation of 0.03, as a common direction of H and W leaves
+    them: neighbours in rank are several fp32 steps of the sum apart, and closer than
+    2^-16 of it.  (Seeds without 5 ids within 1e-6 of 60 of the K-th, checked here.)"""
+    d = 64
+    gen = torch.Generator().manual_seed(2)
+    W = torch.randn((V, d), generator=gen) * 0.004
+    W[:, 0] = 60.0
+    H = torch.randn((B, d), generator=gen)
+    H[:, 0] = 1.0
+    p = dict(H=H.bfloat16().cuda(), W=W.bfloat16().cuda(), temperature=None, vocab_mask=None,
+             tokens=torch.randint(0, V, (B,), generator=gen).cuda())
+    l = (p["H"].double() @ p["W"].double().T).sort(dim=1, descending=True).values
+    near_kth = (l - l[:, K - 1:K]).abs() < 2 * 60e-6
+    assert int(near_kth.sum(1).max()) <= 5
+    check_forward(p, K)
