@@ -45,6 +45,14 @@ extern "C" {
  * other ids' fp32 sums are no smaller than its own: where more than 4 ids lie within
  * those sums' error (about 1e-6 of the sum of |H W|) of the K-th.
  *
+ * The tensor core cuts its fp32 sums off towards zero, on average by 1.55e-8 of the
+ * logit for every 16 products, which is corrected.  The ids that decide a row do not
+ * depend on that: the token, the K + 4 candidates and, with K = 0, one id of a logit near
+ * the largest enter the row's sums with the logits summed again.  The other ids'
+ * probabilities are off by a quarter of the mean, each in its own way (1e-6 |x| at
+ * d = 4096, relative), or by all of it where a row's sums are exact on the way, as with
+ * few non-zeros in H (4e-6 |x|).
+ *
  * Conventions: T_b <= 0, NaN or +inf (greedy rows of the sampler) means T = 1.
  * A token below 0 means "no token": logp 0.  A token that the mask clears, or
  * that lies outside [vocab_offset, vocab_offset + V), has logp -inf.  A fully

@@ -42,11 +42,18 @@ constexpr float kLn2 = 0.6931471805599453f;
 // the accumulator's last place per step: measured over heads of d = 256 to 5120,
 // 1.55e-8 (0.26 2^-24) of the logit per step of 16 -- 4e-6 at d = 4096, a bias
 // that does not average out of the log-sum-exp.  The scale that turns logits
-// into base-2 units carries the correction; what is left is the part that
-// differs from logit to logit.
+// into base-2 units carries the mean of it.  That mean is a fact of sums of many
+// terms of either sign: one logit differs from it by a quarter, and sums that are
+// exact on the way (hidden states of few non-zeros) are not cut off at all.  So
+// what single ids decide does not rest on it: the terms of the token, the
+// candidates (without any, of an id near the row's maximum) in a row's sums, and G
+// at the token, come from logits summed again in compensated fp32.
 constexpr float kCutPerStep = 1.55e-8f;
+__device__ __forceinline__ float mean_cut(int n_kb) {
+  return kCutPerStep * float(n_kb * (kBK / kUK));
+}
 __device__ __forceinline__ float scale_to_log2(float T, int n_kb) {
-  return kLog2e / T * (1.0f + kCutPerStep * float(n_kb * (kBK / kUK)));
+  return kLog2e / T * (1.0f + mean_cut(n_kb));
 }
 
 __device__ __forceinline__ float row_temperature(const float* temperature, int row) {
@@ -74,9 +81,15 @@ struct AllowWords {
 // Forward: row statistics and candidates
 // ---------------------------------------------------------------------------
 
-// One thread's state of a row, as left in the workspace.
+// One thread's state of a row, as left in the workspace: m the largest raw logit.
 struct RowPart {
-  float m, S, U, pad;  // 16 bytes
+  float m, S, U;
+  float at_token;  // the raw logit of the row's token, -inf if it is not the thread's
+};
+// Without lists, an id near the thread's maximum.
+struct RowRef {
+  float val;  // its raw logit
+  int32_t id;  // -1 for none
 };
 
 // Insert (v, id) into a list sorted by decreasing value whose last entry it
@@ -162,7 +175,10 @@ struct ScoreParams {
   const float* temperature;
   const uint32_t* mask;
   int64_t mask_ld;
+  const int64_t* tokens;  // or null
+  int64_t vocab_offset;
   RowPart* part;     // [B][n_slots]
+  RowRef* ref;       // KC = 0: [B][n_slots]
   float* cand_val;   // [B][n_slots][KC] raw logits, best first
   int32_t* cand_id;  // ids from 0, -1 past the end
   int32_t n_slots;
@@ -178,6 +194,9 @@ struct ScoreEpi {
     float scale2 = 0.0f;                      // log2(e) / T
     const uint32_t* mrow = nullptr;
     int row = -1;
+    int32_t token = -1;  // id from 0, -1 for none
+    float at_token = -INFINITY;
+    RowRef ref{-INFINITY, -1};  // KC = 0
     bool first = true;  // no unit seen yet
     float ts[KC > 0 ? KC : 1];
     int32_t ti[KC > 0 ? KC : 1];
@@ -192,16 +211,17 @@ struct ScoreEpi {
   }
   static __device__ __forceinline__ void before(const Params&, State&, const TileAt&, int, int,
                                                 const Shape&) {}
-  // 32 logits.  kMasked: a cleared id's logit counts as -inf, whatever it is.
+  // 32 logits; returns the largest.  kMasked: a cleared id's logit counts as -inf,
+  // whatever it is.
   template <bool kMasked>
-  static __device__ __forceinline__ void chunk(State& st, uint32_t (&r)[32], uint32_t allow) {
+  static __device__ __forceinline__ float chunk(State& st, uint32_t (&r)[32], uint32_t allow) {
     float top = -INFINITY;
 #pragma unroll
     for (int j = 0; j < 32; ++j) {
       if (kMasked) r[j] = ((allow >> j) & 1u) ? r[j] : 0xFF800000u;
       top = ptx::max_nan(top, __uint_as_float(r[j]));
     }
-    if (top == -INFINITY) return;  // nothing allowed (false for NaN)
+    if (top == -INFINITY) return top;  // nothing allowed (false for NaN)
     const float m = ptx::max_nan(st.m, top);
     float acc = 0.0f, ent = 0.0f;
 #pragma unroll
@@ -224,12 +244,13 @@ struct ScoreEpi {
       st.S = fmaf(f, st.S, acc);
     }
     st.m = m;
+    return top;
   }
   // The list from the first unit's logits: sorted by key, 32 at a time, and merged; then
   // the values of the KC + 4 best keys are fetched (by their columns, from a copy of each
   // chunk in local memory) and put in order where they share a step.  False, with the
-  // list empty, if for some lane 4 keys more than it keeps share the step of the last
-  // it keeps: a larger logit may have been dropped.  Inserting one by one, as is done
+  // list empty, if for some lane more than 4 keys beyond those it keeps share the step
+  // of the last it keeps: a larger logit may have been dropped.  Inserting one by one, as is done
   // then, takes 28 us a call at KC = 24 where a CTA has one unit, this 6; sorting
   // whole values with their columns (64-bit keys) took 20.
   static __device__ __forceinline__ bool fill(const Params& p, State& st, const TileAt& at,
@@ -304,6 +325,10 @@ struct ScoreEpi {
       st.row = row;
       st.scale2 = scale_to_log2(row_temperature(p.temperature, row), s.n_kb);
       if (p.mask) st.mrow = p.mask + int64_t(row) * p.mask_ld;
+      if (p.tokens) {
+        const int64_t local = p.tokens[row] - p.vocab_offset;
+        if (local >= 0 && local < p.V) st.token = int32_t(local);
+      }
     }
     const AllowWords allow(st.mrow, at.col0, p.V);
     auto load = [&](int c, uint32_t (&r)[32]) {
@@ -312,10 +337,17 @@ struct ScoreEpi {
       const uint32_t w = allow.at(c);
       const bool full = __all_sync(0xFFFFFFFFu, !valid || w == 0xFFFFFFFFu);
       if (!valid) return;
-      if (full)
-        chunk<false>(st, r, w);
-      else
-        chunk<true>(st, r, w);
+      const float top = full ? chunk<false>(st, r, w) : chunk<true>(st, r, w);
+      const uint32_t tok = uint32_t(st.token - (at.col0 + c * 32));
+      if (tok < 32u) st.at_token = pick32(r, tok);
+      // Any id within 2^4 of the row's largest term serves: looking for the column
+      // costs 64 instructions a chunk, so small rises are passed over.
+      if (KC == 0 && (top - st.ref.val) * st.scale2 > 4.0f) {
+        uint32_t hit = 0u;
+#pragma unroll
+        for (int j = 0; j < 32; ++j) hit |= __uint_as_float(r[j]) == top ? 1u << j : 0u;
+        st.ref = RowRef{top, at.col0 + c * 32 + __ffs(hit) - 1};
+      }
     };
     bool filled = false;
     if constexpr (KC > 0) {
@@ -356,9 +388,10 @@ struct ScoreEpi {
     // one is written, also by a thread whose columns lay past V.
     if (row >= p.B) return;
     const int64_t slot = int64_t(row) * p.n_slots + (worker / s.n_mt) * 2 + half;
-    const float m2 = st.m == -INFINITY ? st.m : st.m * st.scale2;
-    p.part[slot] = RowPart{m2, st.S, st.U, 0.0f};
-    if constexpr (KC > 0) {
+    p.part[slot] = RowPart{st.m, st.S, st.U, st.at_token};
+    if constexpr (KC == 0) {
+      p.ref[slot] = st.ref;
+    } else {
       float4* v4 = reinterpret_cast<float4*>(p.cand_val + slot * KC);
       int4* i4 = reinterpret_cast<int4*>(p.cand_id + slot * KC);
 #pragma unroll
@@ -379,6 +412,7 @@ struct JoinParams {
   const __nv_bfloat16* W;
   int64_t ldh, ldw;
   int32_t d, V, n_slots, K;
+  int32_t n_kb;  // k slices of the contraction
   int32_t ctas;  // blocks (a cluster) per row
   const float* temperature;
   const uint32_t* mask;
@@ -386,6 +420,7 @@ struct JoinParams {
   const int64_t* tokens;
   int64_t vocab_offset;
   const RowPart* part;
+  const RowRef* ref;
   const float* cand_val;
   const int32_t* cand_id;
   float *out_logp, *out_entropy, *out_lse;
@@ -459,14 +494,23 @@ __device__ __forceinline__ float2 warp_logit(const __nv_bfloat16* __restrict__ h
   return make_float2(sum, err);
 }
 
-// logit / T - lse in fp32 without the quotient's rounding; at most 0 (lse is off
-// by its own rounding where one token has nearly all the mass).  NaN stays.
-__device__ __forceinline__ float scaled_logp(float2 logit, float T, float lse) {
-  const float q = __fdiv_rn(logit.x, T);
-  if (!isfinite(q)) return q - lse;
-  const float rest = (__fmaf_rn(-q, T, logit.x) + logit.y) / T;
-  const float logp = (q - lse) + rest;
+// A row's normaliser: lse = L / T + log_sum, L one id's logit as an exact pair.
+struct Norm {
+  float2 L;
+  float log_sum;
+};
+// (logit - L) / T - log_sum, so that neither the logits' size nor the rounding of lse
+// enters; at most 0 (log_sum is off by its own rounding where one token has nearly all
+// the mass).  NaN stays.
+__device__ __forceinline__ float scaled_logp(float2 logit, float T, const Norm& n) {
+  const float logp = ((logit.x - n.L.x) + (logit.y - n.L.y)) / T - n.log_sum;
   return logp > 0.0f ? 0.0f : logp;
+}
+// a / T + b without the quotient's rounding.
+__device__ __forceinline__ float scaled_sum(float2 a, float T, float b) {
+  const float q = __fdiv_rn(a.x, T);
+  if (!isfinite(q)) return q + b;
+  return q + ((__fmaf_rn(-q, T, a.x) + a.y) / T + b);
 }
 
 // An order-preserving map of floats to unsigned integers; NaN counts as +inf
@@ -484,6 +528,12 @@ __device__ __forceinline__ uint64_t entry_key(float f, int32_t id) {
   return (uint64_t(order_bits(f)) << 32) | (0xFFFFFFFFu - uint32_t(id));
 }
 
+// The value of an entry's key.
+__device__ __forceinline__ float entry_value(uint64_t key) {
+  const uint32_t u = uint32_t(key >> 32);
+  return __uint_as_float((u & 0x80000000u) ? u ^ 0x80000000u : ~u);
+}
+
 // How many of the n keys in shared memory exceed `key`.
 __device__ __forceinline__ int count_above(const uint64_t* keys, int n, uint64_t key) {
   int above[4] = {};
@@ -499,29 +549,40 @@ __device__ __forceinline__ int count_above(const uint64_t* keys, int n, uint64_t
   return above[0] + above[1] + above[2] + above[3];
 }
 
-// Fold the state (m1, S1, U1) into (m0, S0, U0).
+// Fold the state (m1, S1, U1) into (m0, S0, U0); raw logits times scale2 are in base 2.
 __device__ __forceinline__ void join_state(float& m0, float& S0, float& U0, float m1, float S1,
-                                           float U1) {
+                                           float U1, float scale2) {
   if (m1 == -INFINITY) return;
   if (m0 == -INFINITY) {
     m0 = m1, S0 = S1, U0 = U1;
     return;
   }
   const float mm = ptx::max_nan(m0, m1);
-  const float d0 = ptx::max_nan(m0 - mm, -16384.0f), d1 = ptx::max_nan(m1 - mm, -16384.0f);
+  const float d0 = ptx::max_nan((m0 - mm) * scale2, -16384.0f);
+  const float d1 = ptx::max_nan((m1 - mm) * scale2, -16384.0f);
   const float f0 = exp2f(d0), f1 = exp2f(d1);
   U0 = f0 * fmaf(d0, S0, U0) + f1 * fmaf(d1, S1, U1);
   S0 = f0 * S0 + f1 * S1;
   m0 = mm;
 }
-__device__ __forceinline__ void join_lanes(float& m, float& S, float& U) {
+__device__ __forceinline__ void join_lanes(float& m, float& S, float& U, float scale2) {
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) {
     const float om = __shfl_xor_sync(0xFFFFFFFFu, m, off);
     const float oS = __shfl_xor_sync(0xFFFFFFFFu, S, off);
     const float oU = __shfl_xor_sync(0xFFFFFFFFu, U, off);
-    join_state(m, S, U, om, oS, oU);
+    join_state(m, S, U, om, oS, oU, scale2);
   }
+}
+__device__ __forceinline__ uint64_t max_lanes(uint64_t key) {
+  const uint32_t hi = __reduce_max_sync(0xFFFFFFFFu, uint32_t(key >> 32));
+  const uint32_t lo = uint32_t(key >> 32) == hi ? uint32_t(key) : 0u;
+  return (uint64_t(hi) << 32) | __reduce_max_sync(0xFFFFFFFFu, lo);
+}
+__device__ __forceinline__ float sum_lanes(float v) {
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, off);
+  return v;
 }
 
 // Blocks of the join kernel: a thread per slot at least.  Up to a block per SM
@@ -541,7 +602,7 @@ static_assert(kMaxSlots <= JoinWide::kThreads && kPlanSms <= JoinNarrow::kThread
 
 // A row's block, or with more logits to sum than a block has warps and few
 // rows, its cluster of `ctas` blocks: every block selects the candidates, the
-// logits are dealt out to all warps, and block 0 ranks and writes them.
+// logits are dealt out to all warps, and block 0 sums, ranks and writes.
 // Launched as a programmatic dependent of the contraction.
 //
 // The n = K + 4 best entries of the row's lists, in three steps:
@@ -566,22 +627,27 @@ __global__ void __launch_bounds__(Block::kThreads, Block::kBlocks)
   constexpr int kList = KC > 0 ? KC : 1;
   constexpr int kGroups = kJoinThreads / 8;
   constexpr int kEntries = kList * (kList + 1) / 2;
+  static_assert(KC < 31, "a lane per candidate, and the last one for the token");
   __shared__ float s_m[kJoinWarps], s_S[kJoinWarps], s_U[kJoinWarps];
+  __shared__ uint32_t s_at[kJoinWarps];  // order_bits of the token's raw logit
+  __shared__ float2 s_token;
+  __shared__ Norm s_norm;
   __shared__ uint32_t s_group[kGroups];
   __shared__ uint32_t s_bound;
   __shared__ int32_t s_heads, s_entries;
-  __shared__ uint64_t s_head[KC > 0 ? kJoinThreads : 1];
+  __shared__ uint64_t s_head[KC > 0 ? kJoinThreads : kJoinWarps];
   __shared__ int32_t s_slot[KC > 0 ? kJoinThreads : 1];
   __shared__ uint64_t s_entry[kEntries];
   __shared__ int32_t s_list[kList];
   __shared__ uint64_t s_least;
   __shared__ int32_t s_id[kList], s_rank[kList];
+  __shared__ float s_raw[kList];  // the candidates' fp32 sums
   __shared__ uint64_t s_key[kList];
   __shared__ float2 s_logit[kList];
   const int cta = int(blockIdx.x) % p.ctas;
   const int row = int(blockIdx.x) / p.ctas;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int n_cand = KC > 0 ? p.K + 4 : 0;  // at most KC
+  const int n_cand = KC > 0 ? p.K + 4 : 1;  // at most KC; without lists, the reference id
   if (tid < kList) s_list[tid] = s_id[tid] = -1, s_rank[tid] = 0, s_key[tid] = 0u;
   if (tid == 0) s_bound = 0u, s_heads = s_entries = 0, s_least = 0u;
   if (KC > 0 && p.ctas > 1) ptx::cluster_sync();  // block 0's keys are cleared before any arrives
@@ -589,15 +655,19 @@ __global__ void __launch_bounds__(Block::kThreads, Block::kBlocks)
 
   // ---- what the row needs from memory, at once
   const int64_t slot0 = int64_t(row) * p.n_slots;
-  float m = -INFINITY, S = 0.0f, U = 0.0f;
+  float m = -INFINITY, S = 0.0f, U = 0.0f, at_token = -INFINITY;
   uint64_t head = 0u;
   if (tid < p.n_slots) {
     const RowPart r = p.part[slot0 + tid];
-    if constexpr (KC > 0)
+    if constexpr (KC > 0) {
       head = entry_key(p.cand_val[(slot0 + tid) * KC], p.cand_id[(slot0 + tid) * KC]);
-    m = r.m, S = r.S, U = r.U;
+    } else {
+      const RowRef ref = p.ref[slot0 + tid];
+      head = entry_key(ref.val, ref.id);
+    }
+    m = r.m, S = r.S, U = r.U, at_token = r.at_token;
   }
-  const float T = row_temperature(p.temperature, row);
+  const float T = row_temperature(p.temperature, row), scale2 = scale_to_log2(T, p.n_kb);
   int64_t token = -1, local = -1;
   bool scored = false;  // the token has a logit
   if (p.tokens) {
@@ -609,11 +679,17 @@ __global__ void __launch_bounds__(Block::kThreads, Block::kBlocks)
   }
 
   // ---- statistics: lanes, then (below) warps
-  join_lanes(m, S, U);
-  if (lane == 0) s_m[warp] = m, s_S[warp] = S, s_U[warp] = U;
+  join_lanes(m, S, U, scale2);
+  const uint32_t at = __reduce_max_sync(0xFFFFFFFFu, order_bits(at_token));
+  if (lane == 0) s_m[warp] = m, s_S[warp] = S, s_U[warp] = U, s_at[warp] = at;
 
   // ---- candidates
-  if constexpr (KC > 0) {
+  if constexpr (KC == 0) {
+    head = max_lanes(head);
+    if (lane == 0) s_head[warp] = head;
+    __syncthreads();
+    head = max_lanes(lane < kJoinWarps ? s_head[lane] : 0u);  // the row's, in every warp
+  } else {
     const uint32_t value = uint32_t(head >> 32);
     uint32_t top = value;
 #pragma unroll
@@ -657,37 +733,55 @@ __global__ void __launch_bounds__(Block::kThreads, Block::kBlocks)
     for (int i = tid; i < s_entries; i += kJoinThreads) {
       const uint64_t key = s_entry[i];
       const int r = count_above(s_entry, s_entries, key);
-      if (r < n_cand) s_id[r] = int32_t(0xFFFFFFFFu - uint32_t(key));
+      if (r < n_cand) {
+        s_id[r] = int32_t(0xFFFFFFFFu - uint32_t(key));
+        s_raw[r] = entry_value(key);
+      }
     }
+    __syncthreads();
   }
-  __syncthreads();
 
   // ---- the logits again, a warp each (0: the token, from 1: candidates), dealt
   // out to the warps of all blocks
   const __nv_bfloat16* h = p.H + int64_t(row) * p.ldh;
+  auto cand_id = [&](int i) {
+    if constexpr (KC == 0) return head != 0u ? int32_t(0xFFFFFFFFu - uint32_t(head)) : -1;
+    return s_id[min(i, kList - 1)];
+  };
+  auto cand_raw = [&](int i) {
+    if constexpr (KC == 0) return entry_value(head);
+    return s_raw[min(i, kList - 1)];
+  };
+  // The last warp of block 0 joins the row's sums meanwhile and takes the terms of the
+  // known ids out: the candidates, a lane each, and the token in the last lane.
+  const bool sums = cta == 0 && warp == kJoinWarps - 1;
+  float rest_S = 0.0f, rest_U = 0.0f;
+  bool known = false;  // the lane has such an id
+  if (sums) {
+    m = lane < kJoinWarps ? s_m[lane] : -INFINITY;
+    S = lane < kJoinWarps ? s_S[lane] : 0.0f;
+    U = lane < kJoinWarps ? s_U[lane] : 0.0f;
+    const uint32_t all_at = __reduce_max_sync(0xFFFFFFFFu, lane < kJoinWarps ? s_at[lane] : 0u);
+    join_lanes(m, S, U, scale2);
+    const bool held = lane < n_cand && cand_id(lane) >= 0;
+    const bool listed = __any_sync(0xFFFFFFFFu, held && cand_id(lane) == local);
+    const float raw = held ? cand_raw(lane)
+                      : lane == 31 && scored && !listed ? entry_value(uint64_t(all_at) << 32)
+                                                        : -INFINITY;
+    known = isfinite(raw);
+    const float t = fmaxf((raw - m) * scale2, -16384.0f), e = known ? exp2f(t) : 0.0f;
+    rest_S = ptx::max_nan(S - sum_lanes(e), 0.0f);
+    rest_U = -ptx::max_nan(sum_lanes(e * t) - U, 0.0f);
+  }
   for (int j = cta * kJoinWarps + warp; j <= n_cand; j += p.ctas * kJoinWarps) {
-    if (j == 0) {  // and the row's statistics
-      m = lane < kJoinWarps ? s_m[lane] : -INFINITY;
-      S = lane < kJoinWarps ? s_S[lane] : 0.0f;
-      U = lane < kJoinWarps ? s_U[lane] : 0.0f;
-      join_lanes(m, S, U);
-      const bool none = m == -INFINITY;
-      const float log2S = log2f(S);
-      const float lse = none ? -INFINITY : kLn2 * (m + log2S);
-      __syncwarp();
-      if (lane == 0) {
-        s_m[0] = lse;
-        if (p.out_lse) p.out_lse[row] = lse;
-        if (p.out_entropy) p.out_entropy[row] = none ? 0.0f : kLn2 * (log2S - U / S);
-      }
-      if (p.tokens) {
-        float logp = token < 0 ? 0.0f : -INFINITY;
-        if (scored) logp = scaled_logp(warp_logit<Block::kDeep>(h, p.W + local * p.ldw, p.d, lane), T, lse);
-        if (lane == 0) p.out_logp[row] = logp;
+    if (j == 0) {
+      if (scored) {
+        const float2 l = warp_logit<Block::kDeep>(h, p.W + local * p.ldw, p.d, lane);
+        if (lane == 0) s_token = l;
       }
       continue;
     }
-    const int32_t id = s_id[j - 1];
+    const int32_t id = cand_id(j - 1);
     if (id < 0) continue;
     const float2 l = warp_logit<Block::kDeep>(h, p.W + int64_t(id) * p.ldw, p.d, lane);
     if (lane == 0) {
@@ -702,13 +796,49 @@ __global__ void __launch_bounds__(Block::kThreads, Block::kBlocks)
       }
     }
   }
-  if constexpr (KC > 0) {
-    if (p.ctas > 1) {
-      ptx::cluster_sync();
-      if (cta != 0) return;
-    } else {
-      __syncthreads();
+  if (KC > 0 && p.ctas > 1) {
+    ptx::cluster_sync();
+    if (cta != 0) return;
+  } else {
+    __syncthreads();
+  }
+
+  // ---- the row's sums, with the known ids' terms from their exact logits in place of
+  // those the contraction added: relative to the largest of them, L, so that a row that
+  // one token decides is as exact as L.
+  if (sums) {
+    const float2 l = !known ? make_float2(0.0f, 0.0f) : lane == 31 ? s_token : s_logit[min(lane, kList - 1)];
+    const uint64_t key =
+        known ? (uint64_t(order_bits(l.x)) << 32) | order_bits(l.y) : 0u;
+    const uint64_t top = max_lanes(key);
+    const int lead = __ffs(__ballot_sync(0xFFFFFFFFu, key == top)) - 1;
+    Norm norm;
+    norm.L = make_float2(__shfl_sync(0xFFFFFFFFu, l.x, lead), __shfl_sync(0xFFFFFFFFu, l.y, lead));
+    if (top == 0u) norm.L = make_float2(m, 0.0f);  // none known
+    // The others' terms relative to L (m in base 2 is m scale2), and the known ids' own.
+    const float unit = kLog2e / T;
+    const float up = unit * ((norm.L.x - m) + (norm.L.y - m * mean_cut(p.n_kb)));
+    const float f = exp2f(-up);
+    const float t = fmaxf(unit * ((l.x - norm.L.x) + (l.y - norm.L.y)), -16384.0f);
+    const float e = known ? exp2f(t) : 0.0f;
+    S = fmaf(rest_S, f, sum_lanes(e));
+    U = fmaf(f, fmaf(-up, rest_S, rest_U), sum_lanes(e * t));
+    const bool none = m == -INFINITY;
+    const float log2S = log2f(S);
+    norm.log_sum = none ? -INFINITY : kLn2 * log2S;
+    if (lane == 0) {
+      s_norm = norm;
+      if (p.out_lse) p.out_lse[row] = none ? -INFINITY : scaled_sum(norm.L, T, norm.log_sum);
+      if (p.out_entropy) {
+        const float entropy = kLn2 * (log2S - U / S);
+        p.out_entropy[row] = none || entropy < 0.0f ? 0.0f : entropy;
+      }
+      if (p.tokens)
+        p.out_logp[row] =
+            scored ? scaled_logp(s_token, T, norm) : token < 0 ? 0.0f : -INFINITY;
     }
+  }
+  if constexpr (KC > 0) {
     for (int pair = tid; pair < n_cand * n_cand; pair += kJoinThreads) {
       const int j = pair / n_cand, i = pair - j * n_cand;
       const uint64_t a = s_key[i], b = s_key[j];  // 0: absent
@@ -721,7 +851,7 @@ __global__ void __launch_bounds__(Block::kThreads, Block::kBlocks)
       if (rank < p.K) {
         const int64_t o = int64_t(row) * p.K + rank;
         p.out_topk_idx[o] = id < 0 ? -1 : p.vocab_offset + id;
-        p.out_topk_logp[o] = id < 0 ? -INFINITY : scaled_logp(s_logit[tid], T, s_m[0]);
+        p.out_topk_logp[o] = id < 0 ? -INFINITY : scaled_logp(s_logit[tid], T, s_norm);
       }
     }
   }
@@ -1003,7 +1133,7 @@ cudaError_t launch_join(JoinParams j, int64_t rows, cudaStream_t stream) {
   // More logits than a block has warps: as many blocks as leave every SM at
   // most one.
   j.ctas = 1;
-  while (wide && j.ctas < 4 && (j.K > 0 ? j.K + 5 : 1) > j.ctas * (JoinWide::kThreads / 32) &&
+  while (wide && j.ctas < 4 && (j.K > 0 ? j.K + 5 : 2) > j.ctas * (JoinWide::kThreads / 32) &&
          rows * j.ctas * 2 <= kPlanSms)
     j.ctas *= 2;
   cudaLaunchAttribute attr[2];
@@ -1220,8 +1350,11 @@ fs_status run_scores(const fs_logprobs_args* a, const Device& dev, cudaStream_t 
     ep.mask = a->vocab_mask ? a->vocab_mask + b0 * a->mask_ld : nullptr;
     ep.mask_ld = a->mask_ld;
     ep.n_slots = n_slots;
+    ep.tokens = a->tokens ? a->tokens + b0 : nullptr;
+    ep.vocab_offset = a->vocab_offset;
     uint8_t* ws = static_cast<uint8_t*>(a->workspace);
     ep.part = reinterpret_cast<RowPart*>(ws);
+    ep.ref = reinterpret_cast<RowRef*>(ep.part + size_t(rows) * n_slots);  // without lists
     ws += round256(size_t(rows) * n_slots * sizeof(RowPart));
     ep.cand_val = reinterpret_cast<float*>(ws);
     ws += round256(size_t(rows) * n_slots * KC * 4u);
@@ -1254,9 +1387,11 @@ fs_status run_scores(const fs_logprobs_args* a, const Device& dev, cudaStream_t 
     j.temperature = ep.temperature;
     j.mask = ep.mask;
     j.mask_ld = a->mask_ld;
-    j.tokens = a->tokens ? a->tokens + b0 : nullptr;
+    j.n_kb = s.n_kb;
+    j.tokens = ep.tokens;
     j.vocab_offset = a->vocab_offset;
     j.part = ep.part;
+    j.ref = ep.ref;
     j.cand_val = ep.cand_val;
     j.cand_id = ep.cand_id;
     j.out_logp = a->out_logp ? a->out_logp + b0 : nullptr;
@@ -1330,7 +1465,8 @@ extern "C" size_t fs_logprobs_workspace_size(int64_t B, int64_t V, int64_t K) {
   // The last launch may have fewer rows, and so more slots a row.
   for (const int64_t r : {rows, B % rows == 0 ? rows : B % rows}) {
     const size_t entries = size_t(r) * size_t(plan_slots(r, V));
-    most = std::max(most, round256(entries * sizeof(RowPart)) + 2 * round256(entries * KC * 4u));
+    const size_t own = sizeof(RowPart) + (KC == 0 ? sizeof(RowRef) : 0);
+    most = std::max(most, round256(entries * own) + 2 * round256(entries * KC * 4u));
   }
   return most;
 }

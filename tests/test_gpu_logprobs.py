@@ -707,3 +707,58 @@ def test_alternatives_beside_a_common_offset(B, V, K):
     near_kth = (l - l[:, K - 1:K]).abs() < 2 * 60e-6
     assert int(near_kth.sum(1).max()) <= 5
     check_forward(p, K)
+
+
+def decided_rows(kind, B, d, V, seed):
+    """Rows that one id decides, 60 units of x or more ahead of the next, whose logits are
+    not what the tensor core's mean cut-off expects: "few" non-zeros in H (sums are exact
+    on the way), partial sums 100 times the logit that "cancel", "dense" ones."""
+    gen = torch.Generator().manual_seed(seed)
+    W = torch.randn((V, d), generator=gen) / math.sqrt(d)
+    H = torch.randn((B, d), generator=gen)
+    best = torch.randperm(V, generator=gen)[:B]
+    if kind == "few":
+        H.zero_()
+        H[torch.arange(B), torch.arange(B) * 7 % d] = 256.0
+        W = (W * math.sqrt(d)).clamp_(max=5.0)
+        W[best, torch.arange(B) * 7 % d] = 7.8125          # 2000, the others at most 1280
+    elif kind == "cancel":
+        half = d // 2
+        sign = torch.randint(0, 2, (B, half), generator=gen) * 2.0 - 1.0
+        W[:, half:] = W[:, :half]
+        W += 4.0
+        H = H.abs()
+        H[:, :half] *= 1.0 + 0.9 * sign
+        H[:, half:] = -H[:, :half]
+        W[best, half:] -= 0.5 * sign                       # ahead by 0.45 sum |H|
+    else:
+        W[best] += (H * 0.1)                               # ahead by |H|^2 / 10
+    return H.bfloat16().cuda(), W.bfloat16().cuda(), best
+
+
+@pytest.mark.parametrize("kind", ["few", "cancel", "dense"])
+@pytest.mark.parametrize("B,V,K", [(3, 3000, 0), (3, 3000, 5), (3, 50000, 0), (3, 50000, 20),
+                                   (140, 3000, 0), (140, 3000, 5)])
+def test_rows_that_one_id_decides(kind, B, V, K):
+    """lse is the id's logit, summed exactly: off by the rounding of its result, 2 u.  A
+    log-probability is a difference of two exact logits over T, each operation off by u
+    of its result; the log-sum of one term of 1 is 0 but for the others' e^-60."""
+    d = 4096
+    H, W, best = decided_rows(kind, B, d, V, seed=110 + B + V)
+    tokens = best.clone()
+    tokens[1::2] = (tokens[1::2] + 17) % V
+    T = torch.full((B,), 0.5)
+    T[::3] = 1.0
+    p = dict(H=H, W=W, tokens=tokens.cuda(), temperature=T.cuda(), vocab_mask=None)
+    r = fs.fs_logprobs(H, W, p["tokens"], K, temperature=p["temperature"])
+    w = ref.forward(H, W, p["tokens"], K, p["temperature"])
+    x = (H.double() @ W.double().T).cpu() / T.double().unsqueeze(1)
+    first = x.topk(2, dim=1).values
+    assert float((first[:, 0] - first[:, 1]).min()) > 60.0
+    near(r.lse, w["lse"], 2 * ref.U * w["lse"].abs() + 2 * ref.U, "lse")
+    near(r.logp, w["logp"], 6 * ref.U * w["logp"].abs() + 2 * ref.U, "logp")
+    near(r.entropy, w["entropy"], 2.0 ** -22, "entropy")
+    assert bool((r.logp.cpu()[tokens == best] >= -2 * ref.U).all())
+    if K:
+        assert torch.equal(r.topk_idx[:, 0].cpu(), best)
+        near(r.topk_logp[:, 0], w["topk_logp"][:, 0], 2 * ref.U, "topk_logp")
