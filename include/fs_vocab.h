@@ -98,10 +98,11 @@ fs_status fs_logprobs(const fs_logprobs_args *args, void *stream);
  *   dH[b,:] = sum_v G[b,v] W[v,:]        dW[v,:] = sum_b G[b,v] H[b,:]
  * The logits are computed again; G goes through the workspace in bf16 (each
  * term rounded once, relative error at most 2^-8, sums in fp32), but for G at the
- * row's token, most of a row's gradient, what that rounding takes is kept in fp32
- * and added to the sums; dH, dW are rounded to bf16 once.  lse and entropy are fs_logprobs' outputs; on a shard of
- * the vocabulary they are those of the whole vocabulary, and the shards' dH add
- * up to the whole one.  A token below 0 or cleared by the mask (logp 0 or -inf)
+ * row's token, most of a row's gradient: that comes from the token's logit in
+ * compensated fp32, and what rounding takes of it is kept in fp32 and added to the
+ * sums; dH, dW are rounded to bf16 once.  lse and entropy are fs_logprobs' outputs; on
+ * a shard of the vocabulary they are those of the whole vocabulary, and the shards' dH
+ * add up to the whole one.  A token below 0 or cleared by the mask (logp 0 or -inf)
  * gets no gradient from logp; for a token outside [vocab_offset, vocab_offset +
  * V) the one-hot term lies in another shard and only the p term is added here.
  * A fully masked row (lse -inf) gets no gradient.

@@ -862,7 +862,10 @@ __global__ void __launch_bounds__(Block::kThreads, Block::kBlocks)
 // ---------------------------------------------------------------------------
 
 struct GradParams {
-  int32_t B, V;
+  int32_t B, V, d;
+  const __nv_bfloat16* H;
+  const __nv_bfloat16* W;
+  int64_t ldh, ldw;
   const float* temperature;
   const uint32_t* mask;
   int64_t mask_ld;
@@ -885,27 +888,30 @@ struct GradEpi {
   // the others' average out; so what bf16 leaves of it is kept (delta) and added
   // to those rows in fp32: with it the results are as close as their own bf16
   // rounding allows (4 to 96 rows: 1.0 times the error of that rounding alone,
-  // without it 1.3 to 1.6).
+  // without it 1.3 to 1.6).  At a likely token the element is a (1 - P), which the
+  // tensor core's sum is not good enough for beside an exact lse: it is taken from
+  // the token's logit summed again.
   struct State {
     int row = -1;
     float scale2, lse2, c0, c1, a;
+    float T, lse;
     int32_t token;  // id from 0, -1 for none among W's
     const uint32_t* mrow;
     bool live;  // false: the row's G is 0
+    float at_token;  // G at the token, if that is among the unit's columns
   };
   static __device__ __forceinline__ void start(const Params&, State&, int, int, const Shape&) {}
-  static __device__ __forceinline__ void before(const Params&, State&, const TileAt&, int, int,
-                                                const Shape&) {}
   static __device__ __forceinline__ void load_row(const Params& p, State& st, int row,
                                                   int n_kb) {
     st.row = row;
     st.mrow = nullptr;
     st.live = false;
     st.token = -1;
-    st.scale2 = st.lse2 = st.c0 = st.c1 = st.a = 0.0f;
+    st.scale2 = st.lse2 = st.c0 = st.c1 = st.a = st.lse = 0.0f;
+    st.T = 1.0f;
     if (row >= p.B) return;
-    const float T = row_temperature(p.temperature, row);
-    const float lse = p.lse[row];
+    const float T = st.T = row_temperature(p.temperature, row);
+    const float lse = st.lse = p.lse[row];
     if (p.mask) st.mrow = p.mask + int64_t(row) * p.mask_ld;
     st.scale2 = scale_to_log2(T, n_kb);
     st.lse2 = lse * kLog2e;
@@ -926,12 +932,33 @@ struct GradEpi {
       st.c1 = -e * kLn2;
     }
   }
-  // 32 columns of G into the box; returns the token's, if it is among them.
+  // G at the row's token, whose logit is l.
+  static __device__ __forceinline__ float token_gradient(const State& st, float2 l) {
+    const float logp = scaled_sum(l, st.T, -st.lse), x = (logp > 0.0f ? 0.0f : logp) * kLog2e;
+    return fmaf(exp2f(x), fmaf(st.c1, ptx::max_nan(x, -16384.0f), st.c0), st.a);
+  }
+  // The tokens among the warp's columns, while the unit's MMAs run (their logits one by
+  // one: behind the wait, 128 rows at d = 2048, V = 30000 took 98 us instead of 92).
+  static __device__ __forceinline__ void before(const Params& p, State& st, const TileAt& at, int,
+                                                int lane, const Shape& s) {
+    const int row = at.row0 + lane;
+    if (row != st.row) load_row(p, st, row, s.n_kb);
+    const uint32_t tok = uint32_t(st.token - at.col0);
+#pragma unroll 1
+    for (uint32_t left = __ballot_sync(0xFFFFFFFFu, tok < uint32_t(kN / 2)); left != 0u;
+         left &= left - 1u) {
+      const int i = __ffs(left) - 1;
+      const int64_t id = at.col0 + int(__shfl_sync(0xFFFFFFFFu, tok, i));
+      const float2 l = warp_logit<8>(p.H + int64_t(at.row0 + i) * p.ldh, p.W + id * p.ldw, p.d,
+                                     lane);
+      if (lane == i) st.at_token = token_gradient(st, l);
+    }
+  }
+  // 32 columns of G into the box, `at_token` at the token's, if it is among them.
   template <bool kToken>
-  static __device__ __forceinline__ float put_chunk(const State& st, const uint32_t (&r)[32],
-                                                    uint32_t w, uint32_t tok, uint8_t* box,
-                                                    int lane, int c) {
-    float at_token = 0.0f;
+  static __device__ __forceinline__ void put_chunk(const State& st, const uint32_t (&r)[32],
+                                                   uint32_t w, uint32_t tok, float at_token,
+                                                   uint8_t* box, int lane, int c) {
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       float g[8];
@@ -942,39 +969,38 @@ struct GradEpi {
         const float x =
             ptx::max_nan(fmaf(__uint_as_float(r[j]), st.scale2, -st.lse2), -16384.0f);
         float v = ptx::ex2(x) * fmaf(st.c1, x, st.c0);
-        if (kToken && tok == uint32_t(j)) v += st.a;
+        if (kToken && tok == uint32_t(j)) v = at_token;
         g[i] = ((w >> j) & 1u) ? v : 0.0f;
-        if (kToken && tok == uint32_t(j)) at_token = g[i];
       }
       box_put(box, lane, c * 4 + q, pack_bf16(g[0], g[1]), pack_bf16(g[2], g[3]),
               pack_bf16(g[4], g[5]), pack_bf16(g[6], g[7]));
     }
-    return at_token;
   }
   template <class Release>
   static __device__ __forceinline__ void tile(const Params& p, State& st, const TileAt& at,
                                               int lane, uint8_t* box, const void* tmap,
                                               const Shape& s, Release release) {
     const int row = at.row0 + lane;
-    if (row != st.row) load_row(p, st, row, s.n_kb);
     const AllowWords allow(st.mrow, at.col0, p.V);
     box_begin(lane);
     const int blocks = (p.B + 31) / 32;
 #pragma unroll 1
     for (int c = 0; c < kN / 64; ++c) {
-      uint32_t r[32];
-      ptx::tmem_ld_32x32b_x32(at.taddr + uint32_t(c * 32), r);
-      ptx::tmem_wait_ld();
       const uint32_t w = st.live ? allow.at(c) : 0u;  // 0 past V
       const uint32_t tok = uint32_t(st.token - (at.col0 + c * 32));
       // The rows with their token here: dW's epilogue looks for them, and a warp
       // without one need not.
       const uint32_t marked = __ballot_sync(0xFFFFFFFFu, tok < 32u);
+      uint32_t r[32];
+      ptx::tmem_ld_32x32b_x32(at.taddr + uint32_t(c * 32), r);
+      ptx::tmem_wait_ld();
       uint4 mark = make_uint4(marked, 0u, 0u, 0u);
       if (marked == 0u) {
-        put_chunk<false>(st, r, w, tok, box, lane, c);
+        put_chunk<false>(st, r, w, tok, 0.0f, box, lane, c);
       } else {
-        const float at_token = put_chunk<true>(st, r, w, tok, box, lane, c);
+        const bool held = tok < 32u && ((w >> (tok & 31u)) & 1u);  // not masked, a live row
+        const float at_token = held ? st.at_token : 0.0f;
+        put_chunk<true>(st, r, w, tok, at_token, box, lane, c);
         float delta = at_token - __bfloat162float(__float2bfloat16_rn(at_token));
         if (!isfinite(delta)) delta = 0.0f;
         if (tok < 32u) p.delta[row] = delta;  // one thread of the grid for each row
@@ -1575,6 +1601,11 @@ extern "C" fs_status fs_logprobs_grad(const fs_logprobs_grad_args* a, void* stre
     GradParams ep = {};
     ep.B = int32_t(B);
     ep.V = int32_t(V);
+    ep.d = int32_t(d);
+    ep.H = static_cast<const __nv_bfloat16*>(a->H);
+    ep.W = static_cast<const __nv_bfloat16*>(a->W);
+    ep.ldh = a->ldh;
+    ep.ldw = a->ldw;
     ep.temperature = a->temperature;
     ep.mask = a->vocab_mask;
     ep.mask_ld = a->mask_ld;

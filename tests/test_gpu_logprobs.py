@@ -762,3 +762,43 @@ def test_rows_that_one_id_decides(kind, B, V, K):
     if K:
         assert torch.equal(r.topk_idx[:, 0].cpu(), best)
         near(r.topk_logp[:, 0], w["topk_logp"][:, 0], 2 * ref.U, "topk_logp")
+
+
+@pytest.mark.parametrize("kind", ["few", "dense"])
+@pytest.mark.parametrize("B,V", [(3, 3000), (20, 50000), (140, 3000)])
+def test_gradient_of_likely_tokens(kind, B, V):
+    """Tokens of probability 1 - e^-4 or more: G there is a (1 - P), a small difference, of
+    an exact logit and lse: off by the rounding of lse, u |lse| of P, and a few u.  The
+    others' logits are the tensor core's: their probabilities off by its cut-off, 1.55e-8
+    per 16 products and twice that for one id, u |lse|, and bf16."""
+    d = 4096
+    H, W, best = decided_rows(kind, B, d, V, seed=120 + B + V)
+    free = torch.ones(V, dtype=torch.bool).index_fill(0, best, False)
+    second = free.nonzero().squeeze(1)[:B]
+    if kind == "few":
+        W[second.cuda(), (torch.arange(B) * 7 % d).cuda()] = 7.78125  # 1992 to 2000
+    else:
+        W[second.cuda()] = (W[best.cuda()].float() * 0.985).bfloat16()
+    gen = torch.Generator().manual_seed(B)
+    a = torch.randn(B, generator=gen)
+    f = fs.fs_logprobs(H, W, best.cuda())
+    dH, dW = fs.fs_logprobs_grad(H, W, best.cuda(), f.lse, a.cuda())
+    Hd, Wd = H.cpu().double(), W.cpu().double()
+    x = Hd @ Wd.T
+    lse = torch.logsumexp(x, 1, keepdim=True)
+    p = (x - lse).exp()
+    at = best.unsqueeze(1)
+    assert float(p.gather(1, at).min()) > 1 - math.exp(-4)
+    rest = p.scatter(1, at, 0.0)
+    G = -a.double().unsqueeze(1) * rest
+    G.scatter_(1, at, a.double().unsqueeze(1) * rest.sum(1, keepdim=True))
+    e_lse = 2 * ref.U * lse.abs()
+    dG = a.double().abs().unsqueeze(1) * rest * (
+        ref.BF16 + e_lse + 3 * 1.55e-8 * (d / 16) * x.abs() + 8 * ref.U) * (1 + ref.BF16)
+    dG.scatter_(1, at, a.double().abs().unsqueeze(1) * (e_lse + 8 * ref.U))
+    sums = (V / 16 + 64) * 2.0 ** -23
+    wH, wW = G @ Wd, G.T @ Hd
+    bH = dG @ Wd.abs() + sums * (G.abs() @ Wd.abs())
+    bW = dG.T @ Hd.abs() + sums * (G.abs().T @ Hd.abs())
+    near(dH, wH, bH * (1 + ref.BF16) + ref.BF16 * wH.abs() + 1e-38, "dH")
+    near(dW, wW, bW * (1 + ref.BF16) + ref.BF16 * wW.abs() + 1e-38, "dW")
