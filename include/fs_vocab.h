@@ -59,7 +59,8 @@ extern "C" {
  * masked row has lse -inf and entropy 0; alternatives past the allowed count
  * are id -1, log-probability -inf.  Whatever W holds for a masked id -- NaN or
  * infinity too -- changes nothing; a NaN or +inf logit of an allowed id makes
- * the row's lse, entropy and log-probabilities NaN.
+ * the row's lse, entropy and log-probabilities NaN, also those of missing
+ * alternatives (ids with a NaN logit are not listed).
  */
 typedef struct fs_logprobs_args {
   /* As in fs_sample_args: bf16 [B, d] and [V, d], 16-byte aligned, row strides

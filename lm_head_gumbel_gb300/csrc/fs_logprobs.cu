@@ -851,7 +851,9 @@ __global__ void __launch_bounds__(Block::kThreads, Block::kBlocks)
       if (rank < p.K) {
         const int64_t o = int64_t(row) * p.K + rank;
         p.out_topk_idx[o] = id < 0 ? -1 : p.vocab_offset + id;
-        p.out_topk_logp[o] = id < 0 ? -INFINITY : scaled_logp(s_logit[tid], T, s_norm);
+        // Missing ones have -inf, but NaN as all of the row has if a logit is not a number.
+        p.out_topk_logp[o] = id >= 0 ? scaled_logp(s_logit[tid], T, s_norm)
+                             : isnan(s_norm.log_sum) ? s_norm.log_sum : -INFINITY;
       }
     }
   }

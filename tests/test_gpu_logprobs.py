@@ -802,3 +802,27 @@ def test_gradient_of_likely_tokens(kind, B, V):
     bW = dG.T @ Hd.abs() + sums * (G.abs().T @ Hd.abs())
     near(dH, wH, bH * (1 + ref.BF16) + ref.BF16 * wH.abs() + 1e-38, "dH")
     near(dW, wW, bW * (1 + ref.BF16) + ref.BF16 * wW.abs() + 1e-38, "dW")
+
+
+@pytest.mark.parametrize("B", [4, 140])
+@pytest.mark.parametrize("K", [3, 20])
+def test_rows_of_nan(B, K):
+    """No id of a row whose logits are all NaN can be listed; what is returned for it is
+    NaN, as in a row with one NaN and fewer ids than places."""
+    p = problem(B, 64, 500, mask_frac=0.1, seed=130)
+    p["H"][1] = math.nan
+    p["vocab_mask"][2] = 0
+    p["vocab_mask"][2, 1] = 3 << 8          # ids 40 and 41
+    p["W"][40] = math.nan
+    p["vocab_mask"][0, 1] &= ~(1 << 8)      # masked in rows 0 and 3
+    p["vocab_mask"][3:, 1] &= ~(1 << 8)
+    p["vocab_mask"][3] = 0                  # a row that allows nothing is not NaN
+    r = fs.fs_logprobs(p["H"], p["W"], p["tokens"], K, vocab_mask=p["vocab_mask"])
+    for b in (1, 2):
+        assert bool(torch.isnan(r.lse[b])) and bool(torch.isnan(r.entropy[b]))
+        assert bool(torch.isnan(r.topk_logp[b]).all())
+    assert bool((r.topk_idx[1] == -1).all())
+    assert r.topk_idx[2].tolist() == [41] + [-1] * (K - 1)
+    assert r.lse[3].item() == -math.inf
+    assert bool((r.topk_logp[3] == -math.inf).all()) and bool((r.topk_idx[3] == -1).all())
+    assert bool(torch.isfinite(r.topk_logp[0]).all()) and not bool((r.topk_idx[0] == 40).any())
