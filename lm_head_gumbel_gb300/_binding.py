@@ -4,13 +4,14 @@
 Argument marshalling only: tensors become device pointers, sizes and strides;
 every step of the operators runs in the library's CUDA kernels.  PyTorch
 provides device memory and the current stream.  The operators of fs_vocab.h are
-marshalled by ``_marshal.so`` (``csrc/fs_marshal.cpp``), the same in C++.  When
-the libraries have not been built, every call raises ``FsError`` -- there is no
-fallback.
+marshalled by ``_marshal.so`` (``csrc/fs_marshal.cpp``), the same in C++, loaded
+with the first of them.  When a library has not been built, every call that needs
+it raises ``FsError`` -- there is no fallback.
 """
 from __future__ import annotations
 
 import ctypes
+import importlib
 import os
 from typing import NamedTuple, Optional
 
@@ -148,22 +149,31 @@ def load_library(path: str = LIB_PATH):
     lib.fs_status_string.argtypes = [ctypes.c_int]
     lib.fs_status_string.restype = ctypes.c_char_p
     _lib = lib
-    _bind_marshal(lib)
     return lib
 
 
-def _bind_marshal(lib):
-    """Load _marshal.so (once) and hand it the library's entry points."""
+def load_marshal():
+    """Load _marshal.so (once), which only the operators of fs_vocab.h need, and hand
+    it the library's entry points.  Raises FsError if it was not built, or for another
+    torch."""
     global _marshal
+    if _marshal is not None:
+        return _marshal
+    lib = load_library()
     try:
-        from . import _marshal
+        module = importlib.import_module(__package__ + "._marshal")
     except ImportError as e:
         raise FsError(FS_ERR_UNSUPPORTED, f"_marshal.so cannot be loaded ({e}); build it with "
                                           "lm_head_gumbel_gb300.build.build()") from e
-    _marshal.bind(FsError, *(ctypes.cast(f, ctypes.c_void_p).value for f in (
+    if module.torch_version != torch.__version__:
+        raise FsError(FS_ERR_UNSUPPORTED, f"_marshal.so was built for torch {module.torch_version}, "
+                                          f"this is {torch.__version__}; build it again")
+    module.bind(FsError, *(ctypes.cast(f, ctypes.c_void_p).value for f in (
         lib.fs_logprobs, lib.fs_logprobs_workspace_size, lib.fs_logprobs_grad,
         lib.fs_logprobs_grad_workspace_size, lib.fs_embed, lib.fs_embed_grad,
         lib.fs_embed_grad_workspace_size)))
+    _marshal = module
+    return module
 
 
 def _ptr(t):
@@ -452,8 +462,8 @@ def fs_logprobs(H, W, tokens=None, K=0, *, temperature=None, vocab_mask=None, vo
     fs_sample (rows it samples greedily are scored at T = 1).  out_*: result
     tensors to fill, made when None.  workspace: a uint8 tensor of
     fs_logprobs_workspace_size(B, V, K) bytes, or None.  Returns FsLogprobs."""
-    if _lib is None:
-        load_library()
+    if _marshal is None:
+        load_marshal()
     return FsLogprobs(*_marshal.logprobs(
         H, W, tokens, K, temperature, vocab_mask, vocab_offset, out_logp, out_entropy, out_lse,
         out_topk_idx, out_topk_logp, workspace, _handle(stream),
@@ -474,8 +484,8 @@ def fs_logprobs_grad(H, W, tokens, lse, grad_logp, *, entropy=None, grad_entropy
     grad_entropy: fp32 [B].  Returns (dH, dW) in bf16 ([B, d], [V, d]; out_dH /
     out_dW when given), None where need_dH / need_dW is false.  workspace: a
     uint8 tensor of fs_logprobs_grad_workspace_size(B, d, V) bytes, or None."""
-    if _lib is None:
-        load_library()
+    if _marshal is None:
+        load_marshal()
     return _marshal.logprobs_grad(H, W, tokens, lse, grad_logp, entropy, grad_entropy,
                                   temperature, vocab_mask, vocab_offset, out_dH, out_dW, need_dH,
                                   need_dW, workspace, _handle(stream))
@@ -485,8 +495,8 @@ def fs_embed(ids, E, *, scale=1.0, vocab_offset=0, out=None, stream=None):
     """Embedding lookup: scale * E[ids - vocab_offset], 0 where the id is not
     one of E's rows (padding, another shard).  ids: int64 [N]; E: bf16 or fp32
     [V, d].  Returns out ([N, d] of E's type)."""
-    if _lib is None:
-        load_library()
+    if _marshal is None:
+        load_marshal()
     return _marshal.embed(ids, E, scale, vocab_offset, out, _handle(stream))
 
 
@@ -503,8 +513,8 @@ def fs_embed_grad(ids, dY, V, *, scale=1.0, vocab_offset=0, out=None, out_dtype=
     a result made here (dY's when None).  The same inputs always give the same
     bits.  workspace: a uint8 tensor of fs_embed_grad_workspace_size(N, d)
     bytes, or None."""
-    if _lib is None:
-        load_library()
+    if _marshal is None:
+        load_marshal()
     if out_dtype is not None and out_dtype not in (torch.bfloat16, torch.float32):
         raise FsError(FS_ERR_INVALID_ARG, "out_dtype must be bfloat16 or float32")
     if out is None and out_dtype is torch.bfloat16 and dY.dtype is torch.float32:

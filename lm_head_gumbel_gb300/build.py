@@ -41,11 +41,19 @@ def marshal_command(output: str = MARSHAL) -> list:
     home = os.path.dirname(torch.__file__)
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc_path())))
     return [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
-            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", f"-I{INCLUDE}",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+            f'-DFS_TORCH_VERSION="{torch.__version__}"', f"-I{INCLUDE}",
             f"-I{home}/include", f"-I{home}/include/torch/csrc/api/include",
             f"-I{sysconfig.get_path('include')}", f"-I{cuda}/include", "-o", output,
             MARSHAL_DEPENDS[0], f"-L{home}/lib", "-ltorch_python", "-ltorch", "-ltorch_cpu",
             "-ltorch_cuda", "-lc10", "-lc10_cuda"]
+
+
+def marshal_depends() -> list:
+    """The module's sources, and torch: one installed behind the build is not the one
+    that the module was built for."""
+    import torch
+    return MARSHAL_DEPENDS + [torch.version.__file__]
 
 
 def up_to_date(output: str = LIBRARY, depends=tuple(DEPENDS)) -> bool:
@@ -62,7 +70,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if force or not up_to_date():
         tmp = LIBRARY + f".tmp{os.getpid()}"
         jobs.append((LIBRARY, tmp, command(tmp, ["-Xptxas", "-v"] if verbose else [])))
-    if force or not up_to_date(MARSHAL, MARSHAL_DEPENDS):
+    if force or not up_to_date(MARSHAL, marshal_depends()):
         tmp = MARSHAL + f".tmp{os.getpid()}"
         jobs.append((MARSHAL, tmp, marshal_command(tmp)))
     running = [(job, subprocess.Popen(job[2], stdout=subprocess.PIPE, stderr=subprocess.STDOUT,

@@ -5,6 +5,7 @@ import ctypes
 import os
 import re
 import subprocess
+import sys
 
 import pytest
 
@@ -233,3 +234,62 @@ int main() {
         last = (stages * slices - 1) * piece
         assert 2 <= stages <= 8
         assert last + max(piece, 128 * 128) <= ring, (n, pair, rows)
+
+
+def _without_marshal(code):
+    """Runs `code` in a new process where _marshal cannot be imported."""
+    head = ("import sys; sys.path.insert(0, %r)\n"
+            "sys.modules['lm_head_gumbel_gb300._marshal'] = None\n"
+            "import torch, lm_head_gumbel_gb300 as fs\n" % ROOT)
+    return subprocess.run([sys.executable, "-c", head + code], capture_output=True, text=True)
+
+
+def test_the_sampler_needs_no_marshalling_module(lib):
+    """Only libfs.so: the sampler's functions and the sizes work from the first call on."""
+    r = _without_marshal("print(fs.fs_num_tiles(300), fs.fs_workspace_size(4, 1000) > 0,\n"
+                         "      fs.fs_status_string(0), fs.fs_embed_grad_workspace_size(1, 8))")
+    assert r.returncode == 0, r.stderr
+    assert r.stdout.split()[:2] == ["3", "True"] and r.stdout.split()[-1] == "1280"
+
+
+def test_the_operators_say_that_the_module_is_missing(lib):
+    """FsError, on the first call and on every later one."""
+    r = _without_marshal("""
+t = torch.zeros(1)
+for _ in range(2):
+    for call in (lambda: fs.fs_embed(t, t), lambda: fs.fs_embed_grad(t, t, 4),
+                 lambda: fs.fs_logprobs(t, t, t), lambda: fs.fs_logprobs_grad(t, t, t, t, t)):
+        try:
+            call()
+        except fs.FsError as e:
+            assert e.status == fs.FS_ERR_UNSUPPORTED and "_marshal" in str(e), str(e)
+        else:
+            raise SystemExit("no error")
+""")
+    assert r.returncode == 0, r.stderr + r.stdout
+
+
+def test_a_module_for_another_torch_is_refused(lib):
+    r = _without_marshal("""
+import types
+sys.modules['lm_head_gumbel_gb300._marshal'] = types.SimpleNamespace(torch_version="0.1")
+try:
+    fs.fs_embed(torch.zeros(1), torch.zeros(1))
+except fs.FsError as e:
+    assert e.status == fs.FS_ERR_UNSUPPORTED and "0.1" in str(e), str(e)
+else:
+    raise SystemExit("no error")
+""")
+    assert r.returncode == 0, r.stderr + r.stdout
+
+
+def test_the_module_is_built_again_for_another_torch(lib):
+    from lm_head_gumbel_gb300 import build as libbuild
+    import torch
+    assert torch.version.__file__ in libbuild.marshal_depends()
+    assert libbuild.up_to_date(libbuild.MARSHAL, libbuild.marshal_depends())
+    import lm_head_gumbel_gb300 as fs
+    from lm_head_gumbel_gb300 import _binding
+    assert _binding.load_marshal().torch_version == torch.__version__
+    with pytest.raises(fs.FsError):                       # refused by the module itself
+        fs.fs_embed(torch.zeros(1, dtype=torch.int64), torch.zeros(4, 4))
