@@ -510,13 +510,15 @@ def fs_embed_grad(ids, dY, V, *, scale=1.0, vocab_offset=0, out=None, out_dtype=
     n with ids[n] = vocab_offset + v, added to `out` with accumulate (which
     needs out), else 0 for rows no id names.  ids: int64 [N]; dY: bf16 or fp32
     [N, d]; out: [V, d], bf16 or fp32 (fp32 for fp32 dY); out_dtype: the type of
-    a result made here (dY's when None).  The same inputs always give the same
+    a result made here (dY's when None), or out's.  The same inputs always give the same
     bits.  workspace: a uint8 tensor of fs_embed_grad_workspace_size(N, d)
     bytes, or None."""
     if _marshal is None:
         load_marshal()
     if out_dtype is not None and out_dtype not in (torch.bfloat16, torch.float32):
         raise FsError(FS_ERR_INVALID_ARG, "out_dtype must be bfloat16 or float32")
+    if out is not None and out_dtype is not None and out.dtype is not out_dtype:
+        raise FsError(FS_ERR_INVALID_ARG, f"out is {out.dtype}, out_dtype {out_dtype}")
     if out is None and out_dtype is torch.bfloat16 and dY.dtype is torch.float32:
         raise FsError(FS_ERR_INVALID_ARG, "the gradient of float32 dY is float32")
     return _marshal.embed_grad(ids, dY, V, scale, vocab_offset, out, accumulate,

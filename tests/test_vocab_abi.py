@@ -293,3 +293,14 @@ def test_the_module_is_built_again_for_another_torch(lib):
     assert _binding.load_marshal().torch_version == torch.__version__
     with pytest.raises(fs.FsError):                       # refused by the module itself
         fs.fs_embed(torch.zeros(1, dtype=torch.int64), torch.zeros(4, 4))
+
+
+def test_out_dtype_is_not_ignored(lib):
+    import lm_head_gumbel_gb300 as fs
+    import torch
+    ids, dY = torch.zeros(2, dtype=torch.int64), torch.zeros(2, 8)
+    with pytest.raises(fs.FsError, match="out_dtype"):
+        fs.fs_embed_grad(ids, dY, 4, out=torch.zeros(4, 8), out_dtype=torch.bfloat16)
+    with pytest.raises(fs.FsError, match="out_dtype"):
+        fs.fs_embed_grad(ids, dY.bfloat16(), 4, out=torch.zeros(4, 8).bfloat16(),
+                         out_dtype=torch.float32, accumulate=True)
