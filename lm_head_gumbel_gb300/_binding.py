@@ -10,6 +10,7 @@ it raises ``FsError`` -- there is no fallback.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import importlib
 import os
@@ -188,6 +189,19 @@ def _stream_handle(stream, device):
     return ctypes.c_void_p(int(stream))
 
 
+def _allocating_on(stream, device):
+    """A context in which new tensors belong to `stream` (None: the current one), so
+    that a workspace made for a call is filled before its kernels run and may be freed
+    while they do."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = int(stream)
+        stream = (torch.cuda.ExternalStream(handle, device=device) if handle > 1  # 1: legacy
+                  else torch.cuda.default_stream(device))
+    return torch.cuda.stream(stream)
+
+
 def fs_num_tiles(V: int) -> int:
     return int(load_library().fs_num_tiles(int(V)))
 
@@ -259,7 +273,8 @@ def fs_sample(H, W, *, temperature=None, vocab_mask=None, seeds=None, seed=0, of
             raise FsError(FS_ERR_INVALID_ARG, "reduce=False needs out_tile_max and out_tile_idx")
         out_idx = None
     elif out_idx is None:
-        out_idx = torch.empty(B, dtype=torch.int64, device=dev)
+        with _allocating_on(stream, dev):
+            out_idx = torch.empty(B, dtype=torch.int64, device=dev)
     mask_ld = 0
     if vocab_mask is not None:
         if vocab_mask.dtype != torch.int32 or vocab_mask.dim() != 2 or vocab_mask.stride(1) != 1:
@@ -270,7 +285,8 @@ def fs_sample(H, W, *, temperature=None, vocab_mask=None, seeds=None, seed=0, of
     if temperature is not None and temperature.dtype != torch.float32:
         raise FsError(FS_ERR_INVALID_ARG, "temperature must be float32")
     if reduce and workspace is None:  # zero-filled, as the library requires
-        workspace = torch.zeros(fs_workspace_size(B, V), dtype=torch.uint8, device=dev)
+        with _allocating_on(stream, dev):
+            workspace = torch.zeros(fs_workspace_size(B, V), dtype=torch.uint8, device=dev)
     args = FsSampleArgs(
         H=_ptr(H), W=_ptr(W), temperature=_ptr(temperature), vocab_mask=_ptr(vocab_mask),
         mask_ld=mask_ld, seeds=_ptr(seeds), seed=int(seed) & (2**64 - 1),
@@ -339,10 +355,12 @@ def fs_sample_topk(H, W, K, *, temperature=None, vocab_mask=None, seeds=None, se
     V = W.shape[0]
     dev = H.device
     if out_topk_idx is None:
-        out_topk_idx = torch.empty((B, K), dtype=torch.int64, device=dev)
+        with _allocating_on(stream, dev):
+            out_topk_idx = torch.empty((B, K), dtype=torch.int64, device=dev)
     if workspace is None:
-        workspace = torch.empty(max(1, fs_topk_workspace_size(B, V, K)), dtype=torch.uint8,
-                                device=dev)
+        with _allocating_on(stream, dev):
+            workspace = torch.empty(max(1, fs_topk_workspace_size(B, V, K)), dtype=torch.uint8,
+                                    device=dev)
     mask_ld = 0 if vocab_mask is None else vocab_mask.stride(0)
     args = FsSampleArgs(
         H=_ptr(H), W=_ptr(W), temperature=_ptr(temperature), vocab_mask=_ptr(vocab_mask),
@@ -367,7 +385,8 @@ def fs_group_merge(z, *, m=None, L=None, mode=FS_MERGE_EXACT, seeds=None, seed=0
     P, B = z.shape
     dev = z.device
     if out_idx is None:
-        out_idx = torch.empty(B, dtype=torch.int64, device=dev)
+        with _allocating_on(stream, dev):
+            out_idx = torch.empty(B, dtype=torch.int64, device=dev)
     with torch.cuda.device(dev):
         st = lib.fs_group_merge(_ptr(z), _ptr(m), _ptr(L), P, B, int(mode), _ptr(seeds),
                                 int(seed) & (2**64 - 1), int(offset) & (2**64 - 1),
@@ -400,7 +419,8 @@ def fs_gumbel_transform(words, out=None, stream=None):
     if words.dtype != torch.int32 or not words.is_cuda or not words.is_contiguous():
         raise FsError(FS_ERR_INVALID_ARG, "words must be a contiguous int32 CUDA tensor")
     if out is None:
-        out = torch.empty(words.shape, dtype=torch.float32, device=words.device)
+        with _allocating_on(stream, words.device):
+            out = torch.empty(words.shape, dtype=torch.float32, device=words.device)
     with torch.cuda.device(words.device):
         st = lib.fs_gumbel_transform(_ptr(words), int(words.numel()), _ptr(out),
                                      _stream_handle(stream, words.device))
@@ -416,7 +436,8 @@ def fs_gumbel_noise(b0, nb, v0, nv, *, seed=0, offset=0, seeds=None, out=None, d
     lib = load_library()
     device = torch.device(device or (seeds.device if seeds is not None else "cuda"))
     if out is None:
-        out = torch.empty((nb, nv), dtype=torch.float32, device=device)
+        with _allocating_on(stream, device):
+            out = torch.empty((nb, nv), dtype=torch.float32, device=device)
     with torch.cuda.device(device):
         st = lib.fs_gumbel_noise(_ptr(seeds), int(seed) & (2**64 - 1), int(offset) & (2**64 - 1),
                                  int(b0), int(nb), int(v0), int(nv), _ptr(out),

@@ -188,3 +188,30 @@ def test_noalloc_entry_point_with_the_flag():
         assert lib.fs_sample_noalloc(ctypes.byref(a), ctypes.c_void_p(s.cuda_stream)) == fs.FS_OK
         torch.cuda.synchronize()
         assert torch.equal(out.cpu(), want)
+
+
+def test_what_is_made_for_a_given_stream_belongs_to_it():
+    """Results and default workspaces of calls with `stream` lie in that stream's blocks of
+    the caching allocator, and the workspace is zeroed in its order."""
+    from lm_head_gumbel_gb300 import workloads as wl
+
+    def owner(t):
+        at = t.data_ptr()
+        return [s["stream"] for s in torch.cuda.memory_snapshot()
+                if s["address"] <= at < s["address"] + s["total_size"]]
+
+    H = wl.make_hidden(20, 128, seed=1, device="cuda")
+    W = wl.make_weights(128, 5000, seed=2, device="cuda")
+    want = fs.fs_sample(H, W, seed=3)
+    top = fs.fs_sample_topk(H, W, 4, seed=3)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for stream, at in ((side, side.cuda_stream), (side.cuda_stream, side.cuda_stream), (0, 0)):
+        for _ in range(5):
+            got = fs.fs_sample(H, W, seed=3, stream=stream)
+            junk = [torch.full((1 << 16,), 255, dtype=torch.uint8, device="cuda") for _ in range(4)]
+            got_top = fs.fs_sample_topk(H, W, 4, seed=3, stream=stream)
+        torch.cuda.synchronize()
+        del junk
+        assert owner(got) == [at] and owner(got_top) == [at]
+        assert torch.equal(got, want) and torch.equal(got_top, top)
