@@ -101,7 +101,9 @@ fs_status fs_logprobs(const fs_logprobs_args *args, void *stream);
  * term rounded once, relative error at most 2^-8, sums in fp32), but for G at the
  * row's token, most of a row's gradient: that comes from the token's logit in
  * compensated fp32, and what rounding takes of it is kept in fp32 and added to the
- * sums; dH, dW are rounded to bf16 once.  lse and entropy are fs_logprobs' outputs; on
+ * sums; dH, dW are rounded to bf16 once.  An id other than the token that holds
+ * most of a row repeats its rounding in the row of dH and in its own of dW: their
+ * error is then up to twice that of rounding them to bf16.  lse and entropy are fs_logprobs' outputs; on
  * a shard of the vocabulary they are those of the whole vocabulary, and the shards' dH
  * add up to the whole one.  A token below 0 or cleared by the mask (logp 0 or -inf)
  * gets no gradient from logp; for a token outside [vocab_offset, vocab_offset +

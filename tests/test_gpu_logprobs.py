@@ -826,3 +826,21 @@ def test_rows_of_nan(B, K):
     assert r.lse[3].item() == -math.inf
     assert bool((r.topk_logp[3] == -math.inf).all()) and bool((r.topk_idx[3] == -1).all())
     assert bool(torch.isfinite(r.topk_logp[0]).all()) and not bool((r.topk_idx[0] == 40).any())
+
+
+@pytest.mark.parametrize("B,d,V", [(16, 520, 3000), (140, 264, 2000)])
+@pytest.mark.parametrize("share", [0.5, 0.9, 0.99])
+def test_gradient_of_rows_that_another_id_holds(B, d, V, share):
+    """Row b's mass is on id b, its token is another: G there is -a p, rounded to bf16 as
+    every element but the token's, which the elementwise bounds hold."""
+    p = problem(B, d, V, seed=140 + B)
+    H, W = p["H"].double(), p["W"].double()
+    rows = torch.arange(B, device="cuda")
+    x = H @ W.T
+    rise = torch.logsumexp(x, 1) + math.log(share / (1 - share)) - x[rows, rows]
+    p["W"][:B] = (W[:B] + (rise / (H * H).sum(1)).unsqueeze(1) * H).bfloat16()
+    p["tokens"] = p["tokens"] % (V - B) + B
+    f = fs.fs_logprobs(p["H"], p["W"], p["tokens"], 1)
+    assert torch.equal(f.topk_idx[:, 0], rows)
+    assert float((f.topk_logp[:, 0].exp() - share).abs().max()) < 0.3 * share
+    check_gradient(p, *upstream(B, True, B))
