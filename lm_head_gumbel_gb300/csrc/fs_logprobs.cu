@@ -182,6 +182,7 @@ struct ScoreParams {
   float* cand_val;   // [B][n_slots][KC] raw logits, best first
   int32_t* cand_id;  // ids from 0, -1 past the end
   int32_t n_slots;
+  bool sorted_start;  // the lists are filled by ScoreEpi::fill
 };
 
 template <int KC, int kCols>
@@ -251,8 +252,9 @@ struct ScoreEpi {
   // chunk in local memory) and put in order where they share a step.  False, with the
   // list empty, if for some lane more than 4 keys beyond those it keeps share the step
   // of the last it keeps: a larger logit may have been dropped.  Inserting one by one, as is done
-  // then, takes 28 us a call at KC = 24 where a CTA has one unit, this 6; sorting
-  // whole values with their columns (64-bit keys) took 20.
+  // then, is slower where the first unit's logits hold the rest up (16 rows, d = 1024,
+  // V = 30000, K = 20, one unit a CTA: 56 us a call against 34.5, 1.7 of these for the
+  // values); so is sorting whole values with their columns, 64-bit keys (18 us more).
   static __device__ __forceinline__ bool fill(const Params& p, State& st, const TileAt& at,
                                               const AllowWords& allow, bool valid) {
     constexpr int kFetch = KC + 4;
@@ -351,7 +353,7 @@ struct ScoreEpi {
     };
     bool filled = false;
     if constexpr (KC > 0) {
-      if (st.first) filled = fill(p, st, at, allow, valid);
+      if (st.first && p.sorted_start) filled = fill(p, st, at, allow, valid);
       st.first = false;
     }
 #pragma unroll 1
@@ -588,8 +590,8 @@ __device__ __forceinline__ float sum_lanes(float v) {
 // Blocks of the join kernel: a thread per slot at least.  Up to a block per SM
 // what counts is a row's latency: a warp for every logit of K <= 5, whole rows
 // of W in flight.  Beyond (CTA pairs: half the slots) it is the number of rows
-// in flight: small blocks of fewer registers (1000 rows at d = 4096, K = 5: 29 us,
-// with the large blocks 64).
+// in flight: small blocks of fewer registers (1000 rows at d = 4096, K = 5: 35 us,
+// with the large blocks 63).
 struct JoinWide {
   static constexpr int kThreads = 320, kDeep = 16, kBlocks = 2;
 };
@@ -617,8 +619,9 @@ static_assert(kMaxSlots <= JoinWide::kThreads && kPlanSms <= JoinNarrow::kThread
 // threads came in.
 //
 // What bounds it is latency: dependent loads, barriers and short loops, hidden
-// behind other rows where there are more rows than SMs.  It adds 9 us to 64 rows at
-// d = 4096 with K = 5 (18 us alone, cold), 17 to 1000.
+// behind other rows where there are more rows than SMs.  In a call, in part while the
+// contraction ends: 12 us of 64 rows at d = 4096 with K = 5, 8 with K = 0; 35 of 1000
+// rows, 14 with K = 0.
 template <int KC, class Block>
 __global__ void __launch_bounds__(Block::kThreads, Block::kBlocks)
     join_kernel(const JoinParams p) {
@@ -1311,14 +1314,17 @@ int64_t rows_per_launch(int64_t B) {
 }
 
 // A thread's list: K + 4 at least; longer ones cost registers, time and what the join
-// reads (64 rows at d = 4096, V = 151936, K = 4: 8 entries 191 us, 16 194, 24 197).
+// reads (64 rows at d = 4096, V = 151936, K = 4: 8 entries 194 us, 16 196, 24 200).
 int list_cap(int64_t K) { return K <= 0 ? 0 : K <= 4 ? 8 : K <= 12 ? 16 : 24; }
 
 // Columns of a single-CTA unit of the logits' kernels: the narrowest that still
 // gives every SM at most one unit, so that a small vocabulary starts as many
-// CTAs as it can (6 rows at d = 1790, V = 11137, K = 5: 256 wide 27.6 us, 128 23.6;
-// 64 would need two units of some CTAs: 37.2), else 256 (at V = 38281 47.7 us,
-// 128 wide 51.0): wide units read H least often and need the fewest barriers.
+// CTAs as it can (6 rows at d = 1790, V = 11137, K = 5: 256 wide 30.6 us, 128 24.1, 64,
+// which needs two units of some CTAs, 26.3).  Else 256: wide units read H least often and
+// need the fewest barriers, narrow ones have fewer logits before a CTA's first list is
+// full, and neither is better throughout (256 / 128 wide, us: 6 rows, d = 1790, V = 38281,
+// K = 0 30.7 / 29.9, K = 5 43.3 / 39.6, K = 20 46.2 / 46.5; 100 rows, d = 256, V = 60000,
+// K = 20 47.0 / 52.6; 8 rows, d = 512, V = 151936, K = 20 67.4 / 71.0).
 int unit_cols(int64_t V, int least) {
   int n = least;
   while (n < kBN && ceil_div(V, n) > kPlanSms) n *= 2;
@@ -1382,6 +1388,12 @@ fs_status run_scores(const fs_logprobs_args* a, const Device& dev, cudaStream_t 
     ep.mask = a->vocab_mask ? a->vocab_mask + b0 * a->mask_ld : nullptr;
     ep.mask_ld = a->mask_ld;
     ep.n_slots = n_slots;
+    // A unit of few rows and a long k takes longer to stream than its logits to insert one
+    // by one, and the code of the sorting start is not fetched (start sorted / inserted, us:
+    // 64 rows, d = 4096, V = 151936, K = 5 197.1 / 195.0, 1 row, K = 20 198.7 / 196.9; with
+    // fewer units a CTA, 64 rows, V = 60000, K = 20 103.0 / 108.6, or a shorter k, 1 row,
+    // d = 2048, V = 100000, K = 20 75.1 / 83.7, the first unit's logits hold the rest up).
+    ep.sorted_start = pair || s.n_kb < 64 || s.n_units < 3 * groups;
     ep.tokens = a->tokens ? a->tokens + b0 : nullptr;
     ep.vocab_offset = a->vocab_offset;
     uint8_t* ws = static_cast<uint8_t*>(a->workspace);

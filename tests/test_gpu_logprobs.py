@@ -844,3 +844,12 @@ def test_gradient_of_rows_that_another_id_holds(B, d, V, share):
     assert torch.equal(f.topk_idx[:, 0], rows)
     assert float((f.topk_logp[:, 0].exp() - share).abs().max()) < 0.3 * share
     check_gradient(p, *upstream(B, True, B))
+
+
+@pytest.mark.parametrize("B,d,V,K", [(2, 4096, 117000, 5), (2, 4096, 117000, 20), (2, 4096, 117000, 1),
+                                     (2, 4032, 117000, 5)])
+def test_long_units_of_few_rows(B, d, V, K):
+    """Three units a CTA and more, of 64 k slices, where lists begin without a sort."""
+    p = problem(B, d, V, T=0.7, seed=150 + K)
+    p["W"][V - 40 * 37::37] = p["W"][5]  # equal rows in units visited late
+    check_forward(p, K)
