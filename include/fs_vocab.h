@@ -53,7 +53,8 @@ extern "C" {
  * d = 4096, relative), or by all of it where a row's sums are exact on the way, as with
  * few non-zeros in H (4e-6 |x|).
  *
- * Conventions: T_b <= 0, NaN or +inf (greedy rows of the sampler) means T = 1.
+ * Conventions: T_b <= 0, NaN or +inf (greedy rows of the sampler) means T = 1, a T_b
+ * below 2^-126 counts as 2^-126.
  * A token below 0 means "no token": logp 0.  A token that the mask clears, or
  * that lies outside [vocab_offset, vocab_offset + V), has logp -inf.  A fully
  * masked row has lse -inf and entropy 0; alternatives past the allowed count

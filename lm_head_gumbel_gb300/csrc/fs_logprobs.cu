@@ -58,7 +58,8 @@ __device__ __forceinline__ float scale_to_log2(float T, int n_kb) {
 
 __device__ __forceinline__ float row_temperature(const float* temperature, int row) {
   const float T = temperature ? temperature[row] : 1.0f;
-  return (T > 0.0f && !isinf(T)) ? T : 1.0f;
+  // (1 / T has to be finite.)
+  return (T > 0.0f && !isinf(T)) ? fmaxf(T, 0x1p-126f) : 1.0f;
 }
 
 // The allow-words of one row's 128 ids from v0, ids at or past V cleared.
@@ -820,7 +821,10 @@ __global__ void __launch_bounds__(Block::kThreads, Block::kBlocks)
     if (top == 0u) norm.L = make_float2(m, 0.0f);  // none known
     // The others' terms relative to L (m in base 2 is m scale2), and the known ids' own.
     const float unit = kLog2e / T;
-    const float up = unit * ((norm.L.x - m) + (norm.L.y - m * mean_cut(p.n_kb)));
+    // At a temperature near 0 the one cut-off more is any number of units: bounded, so
+    // that where there are no other terms they stay 0.
+    const float up = fminf(
+        fmaxf(unit * ((norm.L.x - m) + (norm.L.y - m * mean_cut(p.n_kb))), -100.0f), 100.0f);
     const float f = exp2f(-up);
     const float t = fmaxf(unit * ((l.x - norm.L.x) + (l.y - norm.L.y)), -16384.0f);
     const float e = known ? exp2f(t) : 0.0f;

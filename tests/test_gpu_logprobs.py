@@ -853,3 +853,26 @@ def test_long_units_of_few_rows(B, d, V, K):
     p = problem(B, d, V, T=0.7, seed=150 + K)
     p["W"][V - 40 * 37::37] = p["W"][5]  # equal rows in units visited late
     check_forward(p, K)
+
+
+@pytest.mark.parametrize("T", [1e-5, 1e-7, 1e-12, 1e-30, 2e-38, 1e-40])
+@pytest.mark.parametrize("B,K", [(3, 0), (3, 5), (140, 0), (140, 20)])
+def test_temperatures_near_zero(B, K, T):
+    """As some write greedy decoding: the largest logit has all the mass however small T
+    is, also below what the logits' own rounding amounts to in units of T."""
+    d, V = 1024, 3000
+    H, W, best = decided_rows("dense", B, d, V, seed=160 + B)
+    tokens = best.clone()
+    tokens[1::2] = (tokens[1::2] + 17) % V
+    temp = torch.full((B,), T)
+    r = fs.fs_logprobs(H, W, tokens.cuda(), K, temperature=temp.cuda())
+    t = temp.double().clamp_min(2.0 ** -126)
+    x = (H.double() @ W.double().T).cpu()
+    top = x.gather(1, best.unsqueeze(1)).squeeze(1)
+    lse = (top / t).float().double()               # +inf where fp32 ends
+    near(r.lse, lse, 4 * ref.U * lse.abs(), "lse")
+    want = ((x.gather(1, tokens.unsqueeze(1)).squeeze(1) - top) / t).float().double()
+    near(r.logp, want, 6 * ref.U * want.abs(), "logp")
+    assert bool((r.entropy == 0).all())
+    if K:
+        assert torch.equal(r.topk_idx[:, 0].cpu(), best) and bool((r.topk_logp[:, 0] == 0).all())
