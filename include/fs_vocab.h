@@ -104,7 +104,9 @@ fs_status fs_logprobs(const fs_logprobs_args *args, void *stream);
  * compensated fp32, and what rounding takes of it is kept in fp32 and added to the
  * sums; dH, dW are rounded to bf16 once.  An id other than the token that holds
  * most of a row repeats its rounding in the row of dH and in its own of dW: their
- * error is then up to twice that of rounding them to bf16.  lse and entropy are fs_logprobs' outputs; on
+ * error is then up to twice that of rounding them to bf16.  The probabilities of the
+ * other ids are those of the tensor core's logits, as far off as said above (and never
+ * above 1), and all are off by the rounding of lse, 2^-24 |lse|.  lse and entropy are fs_logprobs' outputs; on
  * a shard of the vocabulary they are those of the whole vocabulary, and the shards' dH
  * add up to the whole one.  A token below 0 or cleared by the mask (logp 0 or -inf)
  * gets no gradient from logp; for a token outside [vocab_offset, vocab_offset +

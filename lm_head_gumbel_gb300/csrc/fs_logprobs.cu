@@ -911,6 +911,7 @@ struct GradEpi {
     int32_t token;  // id from 0, -1 for none among W's
     const uint32_t* mrow;
     bool live;  // false: the row's G is 0
+    bool far;   // the logits' error, in units of T, is not small
     float at_token;  // G at the token, if that is among the unit's columns
   };
   static __device__ __forceinline__ void start(const Params&, State&, int, int, const Shape&) {}
@@ -918,7 +919,7 @@ struct GradEpi {
                                                   int n_kb) {
     st.row = row;
     st.mrow = nullptr;
-    st.live = false;
+    st.live = st.far = false;
     st.token = -1;
     st.scale2 = st.lse2 = st.c0 = st.c1 = st.a = st.lse = 0.0f;
     st.T = 1.0f;
@@ -929,6 +930,7 @@ struct GradEpi {
     st.scale2 = scale_to_log2(T, n_kb);
     st.lse2 = lse * kLog2e;
     st.live = lse != -INFINITY;
+    st.far = fabsf(st.lse2) * mean_cut(n_kb) > 0x1p-10f;
     float a = p.grad_logp[row] / T;
     const int64_t token = p.tokens[row], local = token - p.vocab_offset;
     if (token < 0) {
@@ -967,8 +969,10 @@ struct GradEpi {
       if (lane == i) st.at_token = token_gradient(st, l);
     }
   }
-  // 32 columns of G into the box, `at_token` at the token's, if it is among them.
-  template <bool kToken>
+  // 32 columns of G into the box; kCareful: `at_token` at the token's, if it is among
+  // them, and no probability above 1 (the tensor core's logit of an id that has all the
+  // mass may be above lse by more than ex2 takes, at temperatures near 0).
+  template <bool kCareful>
   static __device__ __forceinline__ void put_chunk(const State& st, const uint32_t (&r)[32],
                                                    uint32_t w, uint32_t tok, float at_token,
                                                    uint8_t* box, int lane, int c) {
@@ -979,10 +983,10 @@ struct GradEpi {
       for (int i = 0; i < 8; ++i) {
         const int j = q * 8 + i;
         // Far below 1, p is 0 in fp32; the bound keeps 0 * -inf out of G.
-        const float x =
-            ptx::max_nan(fmaf(__uint_as_float(r[j]), st.scale2, -st.lse2), -16384.0f);
+        float x = ptx::max_nan(fmaf(__uint_as_float(r[j]), st.scale2, -st.lse2), -16384.0f);
+        if (kCareful) x = x > 0.0f ? 0.0f : x;
         float v = ptx::ex2(x) * fmaf(st.c1, x, st.c0);
-        if (kToken && tok == uint32_t(j)) v = at_token;
+        if (kCareful && tok == uint32_t(j)) v = at_token;
         g[i] = ((w >> j) & 1u) ? v : 0.0f;
       }
       box_put(box, lane, c * 4 + q, pack_bf16(g[0], g[1]), pack_bf16(g[2], g[3]),
@@ -997,6 +1001,7 @@ struct GradEpi {
     const AllowWords allow(st.mrow, at.col0, p.V);
     box_begin(lane);
     const int blocks = (p.B + 31) / 32;
+    const bool far = __any_sync(0xFFFFFFFFu, st.far);
 #pragma unroll 1
     for (int c = 0; c < kN / 64; ++c) {
       const uint32_t w = st.live ? allow.at(c) : 0u;  // 0 past V
@@ -1008,7 +1013,7 @@ struct GradEpi {
       ptx::tmem_ld_32x32b_x32(at.taddr + uint32_t(c * 32), r);
       ptx::tmem_wait_ld();
       uint4 mark = make_uint4(marked, 0u, 0u, 0u);
-      if (marked == 0u) {
+      if (marked == 0u && !far) {
         put_chunk<false>(st, r, w, tok, 0.0f, box, lane, c);
       } else {
         const bool held = tok < 32u && ((w >> (tok & 31u)) & 1u);  // not masked, a live row

@@ -876,3 +876,32 @@ def test_temperatures_near_zero(B, K, T):
     assert bool((r.entropy == 0).all())
     if K:
         assert torch.equal(r.topk_idx[:, 0].cpu(), best) and bool((r.topk_logp[:, 0] == 0).all())
+
+
+@pytest.mark.parametrize("T", [0.3, 1e-2, 1e-4, 1e-7, 1e-20])
+@pytest.mark.parametrize("B", [3, 140])
+def test_gradient_at_temperatures_near_zero(B, T):
+    """Rows that an id other than the token holds: dH = (a/T) (W[token] - P W[id]), P = 1.
+    P is at least exp(-off), off what the tensor core cuts off (3 times its mean at most, as
+    in test_gradient_of_likely_tokens) and lse's rounding, in units of T, and at most 1.  So
+    dH lies between the two ends, but for G's rounding, u = 2^-8 of P, the result's, 2^-8 of
+    the larger end, and the fp32 sums' (a few 2^-23 of the two terms)."""
+    d, V = 1024, 3000
+    H, W, best = decided_rows("dense", B, d, V, seed=170 + B)
+    tokens = torch.ones(V, dtype=torch.bool).index_fill(0, best, False).nonzero().squeeze(1)[:B]
+    temp = torch.full((B,), T).cuda()
+    a = torch.randn(B, generator=torch.Generator().manual_seed(B))
+    f = fs.fs_logprobs(H, W, tokens.cuda(), temperature=temp)
+    dH, dW = fs.fs_logprobs_grad(H, W, tokens.cuda(), f.lse, a.cuda(), temperature=temp)
+    assert bool(torch.isfinite(dH).all()) and bool(torch.isfinite(dW).all())
+    t = temp.cpu().double()
+    x = ((H.double() @ W.double().T).cpu() / t.unsqueeze(1)).max(1).values
+    low = torch.exp(-(3 * 1.55e-8 * (d / 16) + 2 * ref.U) * x - 8 * ref.U).unsqueeze(1)
+    scale = (a.double() / t).unsqueeze(1)
+    named, held = scale * W[tokens.cuda()].cpu().double(), scale * W[best.cuda()].cpu().double()
+    ends = torch.stack([named - held, named - low * held])
+    slack = (ref.BF16 * held.abs() + ref.BF16 * (1 + ref.BF16) * ends.abs().max(0).values
+             + (V / 16 + 64) * 2.0 ** -23 * (named.abs() + held.abs()) + 1e-38)
+    got = dH.cpu().double()
+    assert bool((got >= ends.min(0).values - slack).all())
+    assert bool((got <= ends.max(0).values + slack).all())
