@@ -19,7 +19,7 @@
 // Bound: W's bytes for few rows, the tensor cores for many.  Measured (GB300, copy
 // 6.7 TB/s, bf16 1900 TFLOP/s in bursts, 1730 held at the power limit): scores of 64
 // rows at d = 4096, V = 151936 read W at 6.6 TB/s with what follows them; of 1000
-// rows 1480 TFLOP/s held, 1680 in bursts (a slice of a CTA pair takes 600 cycles, 544
+// rows 1470 TFLOP/s held, 1640 in bursts (a slice of a CTA pair takes 600 cycles, 544
 // at the unit's nominal rate); dH of 96 rows at d = 2048 6.5 TB/s; dW of 96 rows
 // writes 5.4 TB/s: 2 slices a unit, its epilogue and stores bound it.
 #pragma once

@@ -6,8 +6,10 @@
 // launch, so each epilogue thread owns one row and half of the vocabulary
 // blocks its CTA visits, and carries in registers, in one pass over its logits,
 //   m = max x,  S = sum 2^(x-m),  U = sum 2^(x-m) (x-m)      (x in base-2 units)
-// and the best KC raw logits with their ids.  A second kernel joins the
-// threads' states of a row and ranks its alternatives.
+// and the best KC raw logits with their ids (without alternatives, one id near the
+// maximum).  A second kernel joins the threads' states of a row, sums the logits of the
+// ids that decide it again in compensated fp32, puts their terms into the sums in place of
+// the tensor core's, and ranks the alternatives.
 //
 // Backward, three contractions: G = dLoss/dlogits in bf16 (the logits again,
 // turned into G in the epilogue), dH = G W, dW = G^T H.
