@@ -1,10 +1,10 @@
-"""ctypes binding of ``libfs.so`` (declared in ``include/fs_sample.h`` and
-``include/fs_vocab.h``).
+"""ctypes binding of ``libfs.so`` (declared in ``include/fs_sample.h``,
+``include/fs_vocab.h`` and ``include/fs_speculate.h``).
 
 Argument marshalling only: tensors become device pointers, sizes and strides;
 every step of the operators runs in the library's CUDA kernels.  PyTorch
-provides device memory and the current stream.  The operators of fs_vocab.h are
-marshalled by ``_marshal.so`` (``csrc/fs_marshal.cpp``), the same in C++, loaded
+provides device memory and the current stream.  The operators of fs_vocab.h and
+fs_speculate.h are marshalled by ``_marshal.so`` (``csrc/fs_marshal.cpp``), the same in C++, loaded
 with the first of them.  When a library has not been built, every call that needs
 it raises ``FsError`` -- there is no fallback.
 """
@@ -32,6 +32,8 @@ FS_SYNC_NONE, FS_SYNC_STREAM, FS_SYNC_IDS = 0, 1, 2
 FS_FLAG_OVERLAP_PREVIOUS = 1
 FS_LOGPROBS_TOPK_MAX = 20
 FS_BF16, FS_F32 = 0, 1
+FS_FP8_BLOCK = 128
+FS_VERIFY_DRAFTS_MAX = 1024
 FS_MERGE_EXACT = 0
 FS_MERGE_GROUP_GUMBEL = 1
 
@@ -84,6 +86,36 @@ class FsLogprobsGradArgs(ctypes.Structure):
         ("vocab_offset", _c_i64), ("out_dH", _c_ptr), ("out_dW", _c_ptr),
         ("lddh", _c_i64), ("lddw", _c_i64),
         ("workspace", _c_ptr), ("workspace_bytes", ctypes.c_size_t),
+    ]
+
+
+class FsMatmulFp8Args(ctypes.Structure):
+    """Mirror of ``fs_matmul_fp8_args``."""
+    _fields_ = [
+        ("A", _c_ptr), ("a_scale", _c_ptr), ("W", _c_ptr), ("w_scale", _c_ptr),
+        ("M", _c_i64), ("d", _c_i64), ("V", _c_i64), ("lda", _c_i64), ("lda_scale", _c_i64),
+        ("ldw", _c_i64), ("ldw_scale", _c_i64), ("out", _c_ptr), ("ldo", _c_i64),
+        ("out_dtype", ctypes.c_int), ("flags", ctypes.c_uint32),
+    ]
+
+
+class FsProbsArgs(ctypes.Structure):
+    """Mirror of ``fs_probs_args``."""
+    _fields_ = [
+        ("logits", _c_ptr), ("N", _c_i64), ("V", _c_i64), ("ldl", _c_i64),
+        ("temperature", _c_ptr), ("vocab_mask", _c_ptr), ("mask_ld", _c_i64), ("out", _c_ptr),
+        ("ldo", _c_i64), ("dtype", ctypes.c_int), ("out_dtype", ctypes.c_int),
+    ]
+
+
+class FsVerifyArgs(ctypes.Structure):
+    """Mirror of ``fs_verify_args``."""
+    _fields_ = [
+        ("p", _c_ptr), ("q", _c_ptr), ("draft_ids", _c_ptr), ("u", _c_ptr),
+        ("B", _c_i64), ("K", _c_i64), ("V", _c_i64), ("p_seq", _c_i64), ("p_pos", _c_i64),
+        ("q_seq", _c_i64), ("q_pos", _c_i64), ("ld_ids", _c_i64), ("ldu", _c_i64),
+        ("out_ids", _c_ptr), ("ld_out", _c_i64), ("out_accepted", _c_ptr),
+        ("dtype", ctypes.c_int),
     ]
 
 
@@ -147,6 +179,15 @@ def load_library(path: str = LIB_PATH):
                                   ctypes.c_float, _c_i64, _c_ptr, _c_i64, ctypes.c_int,
                                   ctypes.c_int, _c_ptr, ctypes.c_size_t, _c_ptr]
     lib.fs_embed_grad.restype = ctypes.c_int
+    lib.fs_quantize.argtypes = [_c_ptr, _c_i64, _c_i64, _c_i64, ctypes.c_int, ctypes.c_int,
+                                _c_ptr, _c_i64, _c_ptr, _c_i64, _c_ptr]
+    lib.fs_quantize.restype = ctypes.c_int
+    lib.fs_matmul_fp8.argtypes = [ctypes.POINTER(FsMatmulFp8Args), _c_ptr]
+    lib.fs_matmul_fp8.restype = ctypes.c_int
+    lib.fs_probs.argtypes = [ctypes.POINTER(FsProbsArgs), _c_ptr]
+    lib.fs_probs.restype = ctypes.c_int
+    lib.fs_verify.argtypes = [ctypes.POINTER(FsVerifyArgs), _c_ptr]
+    lib.fs_verify.restype = ctypes.c_int
     lib.fs_status_string.argtypes = [ctypes.c_int]
     lib.fs_status_string.restype = ctypes.c_char_p
     _lib = lib
@@ -154,8 +195,8 @@ def load_library(path: str = LIB_PATH):
 
 
 def load_marshal():
-    """Load _marshal.so (once), which only the operators of fs_vocab.h need, and hand
-    it the library's entry points.  Raises FsError if it was not built, or for another
+    """Load _marshal.so (once), which only the operators of fs_vocab.h and
+    fs_speculate.h need, and hand it the library's entry points.  Raises FsError if it was not built, or for another
     torch."""
     global _marshal
     if _marshal is not None:
@@ -172,7 +213,8 @@ def load_marshal():
     module.bind(FsError, *(ctypes.cast(f, ctypes.c_void_p).value for f in (
         lib.fs_logprobs, lib.fs_logprobs_workspace_size, lib.fs_logprobs_grad,
         lib.fs_logprobs_grad_workspace_size, lib.fs_embed, lib.fs_embed_grad,
-        lib.fs_embed_grad_workspace_size)))
+        lib.fs_embed_grad_workspace_size, lib.fs_quantize, lib.fs_matmul_fp8, lib.fs_probs,
+        lib.fs_verify)))
     _marshal = module
     return module
 
@@ -447,7 +489,7 @@ def fs_gumbel_noise(b0, nb, v0, nv, *, seed=0, offset=0, seeds=None, out=None, d
     return out
 
 
-# ---- the operators of fs_vocab.h ------------------------------------------
+# ---- the operators of fs_vocab.h and fs_speculate.h -------------------------
 # Keyword interfaces; _marshal.so checks the tensors, makes the results that were
 # not given and calls the library.  With `stream`, what it makes (results,
 # workspaces) is allocated as under torch.cuda.stream(stream): it belongs to that
@@ -544,3 +586,79 @@ def fs_embed_grad(ids, dY, V, *, scale=1.0, vocab_offset=0, out=None, out_dtype=
         raise FsError(FS_ERR_INVALID_ARG, "the gradient of float32 dY is float32")
     return _marshal.embed_grad(ids, dY, V, scale, vocab_offset, out, accumulate,
                                out_dtype is torch.float32, workspace, _handle(stream))
+
+
+class FsQuantized(NamedTuple):
+    """What fs_quantize returns: x stands as values * scale, block by block."""
+    values: torch.Tensor  # float8_e4m3fn [N, d]
+    scale: torch.Tensor   # fp32 [ceil(N / block_rows), ceil(d / 128)]
+
+
+def fs_quantize(x, block_rows=1, *, out=None, out_scale=None, stream=None):
+    """x (bf16 or fp32 [N, d]) in 8-bit floating point with a scale for each block of
+    block_rows x 128: 1 for hidden states, 128 for a head's weight.  out: a
+    float8_e4m3fn [N, d] tensor to fill, out_scale an fp32 one of the scales' shape;
+    made when None (rows of values on 16-byte boundaries, as fs_matmul_fp8 reads
+    them).  Returns FsQuantized."""
+    if _marshal is None:
+        load_marshal()
+    return FsQuantized(*_marshal.quantize(x, block_rows, out, out_scale, _handle(stream)))
+
+
+def _out_code(out, out_dtype, default):
+    """FS_BF16 / FS_F32 of a result that is made; out_dtype must not contradict out."""
+    if out_dtype is not None and out_dtype not in (torch.bfloat16, torch.float32):
+        raise FsError(FS_ERR_INVALID_ARG, "out_dtype must be bfloat16 or float32")
+    if out is not None and out_dtype is not None and out.dtype is not out_dtype:
+        raise FsError(FS_ERR_INVALID_ARG, f"out is {out.dtype}, out_dtype {out_dtype}")
+    return FS_F32 if (out_dtype or default) is torch.float32 else FS_BF16
+
+
+def fs_matmul_fp8(A, a_scale, W, w_scale, *, out=None, out_dtype=None, stream=None,
+                  overlap_previous=False):
+    """Product of matrices in 8-bit floating point: hidden states A [M, d] with a
+    scale for 128 columns of a row, a head's weight W [V, d] with one for 128 x 128 (both
+    as fs_quantize leaves them) -> logits [M, V].  out: a bf16 or fp32 tensor to
+    fill, or None for one of out_dtype (bf16 when None; its rows start on 16-byte
+    boundaries).  overlap_previous: as in fs_sample (W and w_scale are read while the
+    kernel before ends; it may write A and a_scale).  Returns out."""
+    if _marshal is None:
+        load_marshal()
+    return _marshal.matmul_fp8(A, a_scale, W, w_scale, out,
+                               _out_code(out, out_dtype, torch.bfloat16), _handle(stream),
+                               FS_FLAG_OVERLAP_PREVIOUS if overlap_previous else 0)
+
+
+def fs_probs(logits, *, temperature=None, vocab_mask=None, out=None, out_dtype=None,
+             stream=None):
+    """Probabilities softmax(logits / T) over each row's allowed ids, 0 elsewhere.
+    logits: bf16 or fp32 [N, V]; temperature, vocab_mask: as in fs_sample (rows it
+    samples greedily: 1 at the largest logit).  out: a bf16 or fp32 [N, V] tensor
+    to fill (it may be logits), or None for one of out_dtype (fp32 when None; its rows
+    start on 16-byte boundaries).  Returns out."""
+    if _marshal is None:
+        load_marshal()
+    return _marshal.probs(logits, temperature, vocab_mask, out,
+                          _out_code(out, out_dtype, torch.float32), _handle(stream))
+
+
+class FsVerified(NamedTuple):
+    """What fs_verify returns."""
+    ids: torch.Tensor       # int64 [B, K + 1]: accepted drafts, the drawn token, -1 behind
+    accepted: torch.Tensor  # int64 [B]: how many drafts were accepted
+
+
+def fs_verify(p, draft_ids, u, q=None, *, out_ids=None, out_accepted=None, stream=None):
+    """Verify drafted tokens against the target's probabilities: draft i of a
+    sequence is accepted if u_i q_i < p_i at its id, and behind the last accepted one
+    a token is drawn, by u_K, from max(p - q, 0) after a rejection and from p if there
+    was none, so that the tokens are distributed as the target's alone.
+
+    p: [B, K + 1, V], bf16 or fp32; draft_ids: int64 [B, K], a sequence's drafts
+    ending at an id below 0; u: fp32 [B, K + 1] in [0, 1); q: the drafter's
+    probabilities [B, K, V] of p's type, or None for a drafter that names its token.
+    With K = 0 this draws from p.  Returns FsVerified."""
+    if _marshal is None:
+        load_marshal()
+    return FsVerified(*_marshal.verify(p, draft_ids, u, q, out_ids, out_accepted,
+                                       _handle(stream)))

@@ -14,12 +14,14 @@ INCLUDE = os.path.join(ROOT, "include")
 LIBRARY = os.path.join(PKG, "libfs.so")
 MARSHAL = os.path.join(PKG, "_marshal.so")
 MARSHAL_DEPENDS = [os.path.join(CSRC, "fs_marshal.cpp")] + [
-    os.path.join(INCLUDE, f) for f in ("fs_sample.h", "fs_vocab.h")]
+    os.path.join(INCLUDE, f) for f in ("fs_sample.h", "fs_vocab.h",
+                                                  "fs_speculate.h")]
 SOURCES = [os.path.join(CSRC, f) for f in ("fs_sample.cu", "fs_merge.cu", "fs_logprobs.cu",
-                                          "fs_embed.cu")]
+                                          "fs_embed.cu", "fs_fp8.cu", "fs_verify.cu")]
 DEPENDS = SOURCES + [os.path.join(CSRC, f) for f in ("fs_kernels.cuh", "fs_ptx.cuh",
                                                     "fs_noise.cuh", "fs_contract.cuh")] + [
-    os.path.join(INCLUDE, f) for f in ("fs_sample.h", "fs_vocab.h")]
+    os.path.join(INCLUDE, f) for f in ("fs_sample.h", "fs_vocab.h",
+                                                  "fs_speculate.h")]
 
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

@@ -1,0 +1,789 @@
+// fs_fp8.cu -- fs_quantize and fs_matmul_fp8 (fs_speculate.h): matrices in 8-bit
+// floating point (e4m3) with a scale for each block of 128, and their product.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <climits>
+#include <cstdint>
+#include <mutex>
+
+#include "fs_contract.cuh"
+#include "fs_ptx.cuh"
+#include "fs_speculate.h"
+
+namespace fs {
+int* device_error_word();  // fs_sample.cu
+
+namespace ptx {
+
+// kind::f8f6f4: 8-bit A and B (one byte an element, 32 along k), fp32 accumulate.
+__device__ __forceinline__ void mma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                       uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void mma_f8_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                            uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// Instruction descriptor of kind::f8f6f4 with e4m3 A/B (format 0), fp32 D, both K-major.
+__host__ __device__ constexpr uint32_t idesc_e4m3_f32(uint32_t M, uint32_t N) {
+  return (1u << 4) | ((N >> 3) << 17) | ((M >> 4) << 24);
+}
+// d += a * b on two fp32 values at once.
+__device__ __forceinline__ void fma2(uint64_t& d, uint64_t a, uint64_t b) {
+  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(d) : "l"(a), "l"(b));
+}
+__device__ __forceinline__ uint64_t pack2(uint32_t lo, uint32_t hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
+  return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, uint32_t& lo, uint32_t& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=r"(lo), "=r"(hi) : "l"(v));
+}
+// Two values in e4m3, to nearest even, past 448 to 448; lo in the low byte.
+__device__ __forceinline__ uint32_t cvt_e4m3x2(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+}  // namespace ptx
+
+namespace fp8 {
+namespace {
+
+constexpr int kBlock = FS_FP8_BLOCK;
+constexpr float kMostE4m3 = 448.0f;
+constexpr float kLeastMax = 0x1p-100f;
+
+// ---------------------------------------------------------------------------
+// Quantisation
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ float value_of(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ float value_of(float x) { return x; }
+
+// A thread's 8 elements from x, of which n exist; 0 for the others.
+template <class T, bool kVec>
+__device__ __forceinline__ void load8(const T* x, int n, float (&v)[8]) {
+  if (kVec && n >= 8) {
+    if constexpr (sizeof(T) == 2) {
+      const uint4 w = __ldcs(reinterpret_cast<const uint4*>(x));
+      const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v[2 * i] = __uint_as_float(u[i] << 16);
+        v[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
+      }
+    } else {
+      const float4 a = __ldcs(reinterpret_cast<const float4*>(x));
+      const float4 b = __ldcs(reinterpret_cast<const float4*>(x) + 1);
+      v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
+      v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+    }
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = i < n ? value_of(x[i]) : 0.0f;
+}
+
+__device__ __forceinline__ float max_abs(const float (&v)[8]) {
+  float m = fabsf(v[0]);
+#pragma unroll
+  for (int i = 1; i < 8; ++i) m = ptx::max_nan(m, fabsf(v[i]));
+  return m;
+}
+
+template <bool kVec>
+__device__ __forceinline__ void store8(uint8_t* out, int n, const float (&v)[8], float inv) {
+  uint32_t h[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) h[i] = ptx::cvt_e4m3x2(v[2 * i] * inv, v[2 * i + 1] * inv);
+  const uint2 w = make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16);
+  if (kVec && n >= 8) {
+    *reinterpret_cast<uint2*>(out) = w;
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (i < n) out[i] = uint8_t((i < 4 ? w.x : w.y) >> (8 * (i & 3)));
+}
+
+struct QuantParams {
+  const void* x;
+  int64_t ldx;
+  uint8_t* values;
+  int64_t ldv;
+  float* scale;
+  int64_t lds;
+  int32_t N, d, col_blocks;
+};
+
+// A block of 1 x 128 to 16 lanes, 8 elements each.
+constexpr int kRowThreads = 256;
+template <class T, bool kVec>
+__global__ void __launch_bounds__(kRowThreads) quantize_rows_kernel(const QuantParams p) {
+  const int64_t block = int64_t(blockIdx.x) * (kRowThreads / 16) + (threadIdx.x >> 4);
+  const int64_t row = block / p.col_blocks;
+  const int cb = int(block - row * p.col_blocks);
+  const int col = cb * kBlock + int(threadIdx.x & 15) * 8;
+  const int n = row < p.N ? p.d - col : 0;
+  float v[8];
+  load8<T, kVec>(static_cast<const T*>(p.x) + row * p.ldx + col, n, v);
+  float m = max_abs(v);
+#pragma unroll
+  for (int s = 8; s > 0; s >>= 1) m = ptx::max_nan(m, __shfl_xor_sync(0xFFFFFFFFu, m, s));
+  m = ptx::max_nan(m, kLeastMax);
+  if (row >= p.N) return;
+  if ((threadIdx.x & 15) == 0) p.scale[row * p.lds + cb] = __fdiv_rn(m, kMostE4m3);
+  if (n > 0)
+    store8<kVec>(p.values + row * p.ldv + col, n, v, __fdiv_rn(kMostE4m3, m));
+}
+
+// A block of 128 x 128 to a CTA: 8 rows of 8 elements a thread, all loaded at once.
+constexpr int kTileThreads = 256;
+template <class T, bool kVec>
+__global__ void __launch_bounds__(kTileThreads) quantize_tile_kernel(const QuantParams p) {
+  __shared__ float warp_max[kTileThreads / 32];
+  const int rb = int(blockIdx.x / p.col_blocks), cb = int(blockIdx.x - unsigned(rb) * p.col_blocks);
+  const int col = cb * kBlock + int(threadIdx.x & 15) * 8;
+  const int row0 = rb * kBlock + int(threadIdx.x >> 4);
+  float v[8][8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int row = row0 + 16 * i;
+    load8<T, kVec>(static_cast<const T*>(p.x) + int64_t(row) * p.ldx + col,
+                   row < p.N ? p.d - col : 0, v[i]);
+  }
+  float m = kLeastMax;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = ptx::max_nan(m, max_abs(v[i]));
+#pragma unroll
+  for (int s = 16; s > 0; s >>= 1) m = ptx::max_nan(m, __shfl_xor_sync(0xFFFFFFFFu, m, s));
+  if ((threadIdx.x & 31) == 0) warp_max[threadIdx.x >> 5] = m;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kTileThreads / 32; ++i) m = ptx::max_nan(m, warp_max[i]);
+  if (threadIdx.x == 0) p.scale[int64_t(rb) * p.lds + cb] = __fdiv_rn(m, kMostE4m3);
+  const float inv = __fdiv_rn(kMostE4m3, m);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int row = row0 + 16 * i;
+    if (row < p.N)
+      store8<kVec>(p.values + int64_t(row) * p.ldv + col, p.d - col, v[i], inv);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Product
+//
+// Warp roles as in fs_contract.cuh: warp 0 issues TMA copies into a ring of 128-wide
+// k slices (128 bytes a row, so the swizzle and the descriptors are those of 64 bf16),
+// warp 1 issues the MMAs (M = 128 per CTA, kN vocabulary columns; for CTA pairs M = 256
+// over both), warps 2-9 take the sums out.  The scales change with every slice, so a
+// slice is an accumulator of its own: the MMAs alternate over kAcc of them in tensor
+// memory, and the warps add each, times the two scales, to sums in registers.
+// ---------------------------------------------------------------------------
+using vocab::BoundedWait;
+using vocab::kEpiWarps;
+using vocab::kThreads;
+
+constexpr int kBM = 128;
+constexpr int kBK = 128;          // k slice: 128 e4m3 = one 128-byte swizzle row
+constexpr int kUK = 32;           // k of one MMA
+constexpr int kMaxStages = 8;
+constexpr uint32_t kRingBytes = 216u * 1024u;
+constexpr uint32_t kARead = kBM * kBK;  // bytes of A an MMA reads, whatever the box holds
+constexpr uint32_t kBarrierBytes = 256;
+constexpr size_t kSmemBytes = 1024 + kRingBytes + kBarrierBytes;
+
+template <int kN>
+__host__ __device__ constexpr int accumulators() {
+  return kN == 256 ? 2 : 4;
+}
+// Ring stages for a box of `a_bytes` of A: the last stage's MMAs read kARead of A too.
+template <int kN, bool kPair>
+__host__ __device__ constexpr uint32_t ring_stages(uint32_t a_bytes) {
+  const uint32_t stage = a_bytes + (kPair ? kN / 2 : kN) * kBK;
+  const uint32_t past = kARead > stage ? kARead - stage : 0;
+  const uint32_t n = (kRingBytes - past) / stage;
+  return n < kMaxStages ? n : kMaxStages;
+}
+
+struct Plan {
+  int32_t n_mt, n_nt, n_units;  // tiles along M (128 rows, 256 for pairs) and V; their product
+  int32_t n_kb;                 // k slices
+  int32_t M, V;
+  uint32_t a_bytes, stage_bytes, n_stages;
+  uint32_t pdl;
+  const float* a_scale;
+  int64_t lda_scale;
+  const float* w_scale;
+  int64_t ldw_scale;
+  void* out;
+  int64_t ldo;
+  uint32_t out_f32, out_vec;  // type; rows on 16-byte boundaries
+  uint64_t wait_limit_ns;
+  int* error_word;
+};
+
+template <int kN, bool kPair>
+__global__ void __launch_bounds__(kThreads, 1)
+    matmul_kernel(const __grid_constant__ CUtensorMap tmap_a,
+                  const __grid_constant__ CUtensorMap tmap_b, const __grid_constant__ Plan s) {
+  constexpr int kCtas = kPair ? 2 : 1;
+  constexpr int kAcc = accumulators<kN>();
+  constexpr uint32_t kTmemCols = kAcc * kN;
+  constexpr int kBRows = kN / kCtas;
+  constexpr uint32_t kBBytes = kBRows * kBK;
+  constexpr int kCols = kN / 2;  // columns of an epilogue warp
+  constexpr uint32_t kIdesc = ptx::idesc_e4m3_f32(kBM * kCtas, kN);
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* full_bar = reinterpret_cast<uint64_t*>(smem + kRingBytes);
+  uint64_t* empty_bar = full_bar + kMaxStages;
+  uint64_t* tfull_bar = empty_bar + kMaxStages;
+  uint64_t* tempty_bar = tfull_bar + 4;
+  uint64_t* drain_bar = tempty_bar + 4;
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drain_bar + 1);
+  volatile uint32_t* abort_flag = tmem_holder + 1;
+  static_assert((2 * kMaxStages + 9) * 8 + 8 <= kBarrierBytes, "barriers, tensor-memory address, flag");
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const int rank = kPair ? int(ptx::cluster_ctarank()) : 0;
+  const bool leader = rank == 0;
+  const int worker = int(blockIdx.x) / kCtas;
+  const int n_workers = int(gridDim.x) / kCtas;
+
+  if (threadIdx.x == 0) {
+    for (uint32_t i = 0; i < s.n_stages; ++i) {
+      ptx::mbar_init(&full_bar[i], 1);
+      ptx::mbar_init(&empty_bar[i], 1);
+    }
+    for (int a = 0; a < kAcc; ++a) {
+      ptx::mbar_init(&tfull_bar[a], 1);
+      ptx::mbar_init(&tempty_bar[a], kCtas * kEpiWarps);
+    }
+    ptx::mbar_init(drain_bar, 1);
+    *abort_flag = 0u;
+    ptx::fence_barrier_init();
+    ptx::prefetch_tmap(&tmap_a);
+    ptx::prefetch_tmap(&tmap_b);
+  }
+  if (warp == 1) {
+    if constexpr (kPair) {
+      ptx::tmem_alloc_pair(tmem_holder, kTmemCols);
+      ptx::tmem_relinquish_pair();
+    } else {
+      ptx::tmem_alloc(tmem_holder, kTmemCols);
+      ptx::tmem_relinquish();
+    }
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  if constexpr (kPair) ptx::cluster_sync();
+  ptx::tc_fence_after();
+  ptx::grid_launch_dependents();
+  const uint32_t tmem_base = *tmem_holder;
+  const BoundedWait waiter{abort_flag, s.wait_limit_ns, s.error_word};
+
+  if (warp == 0) {
+    // ---------------- TMA producer ----------------
+    const bool issuer = ptx::elect_one();
+    const uint64_t pol_a = ptx::policy_evict_last();
+    const uint64_t pol_b = s.n_mt > 1 ? ptx::policy_evict_normal() : ptx::policy_evict_first();
+    auto load = [&](uint8_t* dst, const CUtensorMap* map, uint32_t stage, int x, int y,
+                    uint64_t pol) {
+      if constexpr (kPair)
+        ptx::tma_load_2d_pair(dst, map, ptx::cluster_addr(&full_bar[stage], 0), x, y, pol);
+      else
+        ptx::tma_load_2d(dst, map, &full_bar[stage], x, y, pol);
+    };
+    // Rows past the end read as 0.
+    auto load_a = [&](uint32_t stage, int kb, int mt) {
+      load(smem + size_t(stage) * s.stage_bytes, &tmap_a, stage, kb * kBK,
+           (mt * kCtas + rank) * kBM, pol_a);
+    };
+    uint32_t stage = 0, phase = 0, issued = 0;
+    bool ok = true;
+    // The first ring fill's A copies, held back until the kernel before is done.
+    bool deferring = s.pdl != 0;
+    int n_held = 0, held_kb[kMaxStages], held_mt[kMaxStages];
+    auto release = [&]() {
+      ptx::grid_dependency_wait();
+      if (issuer)
+        for (int h = 0; h < n_held; ++h) load_a(uint32_t(h), held_kb[h], held_mt[h]);
+      deferring = false;
+    };
+    for (int u = worker; ok && u < s.n_units; u += n_workers) {
+      const int nt = u / s.n_mt, mt = u - nt * s.n_mt;
+      for (int kb = 0; kb < s.n_kb; ++kb) {
+        if (!waiter.wait_warp(&empty_bar[stage], phase ^ 1u)) {
+          ok = false;
+          break;
+        }
+        if (issuer) {
+          if (leader)
+            ptx::mbar_arrive_expect_tx(&full_bar[stage], kCtas * (s.a_bytes + kBBytes));
+          load(smem + size_t(stage) * s.stage_bytes + s.a_bytes, &tmap_b, stage, kb * kBK,
+               nt * kN + rank * kBRows, pol_b);
+          if (!deferring) load_a(stage, kb, mt);
+        }
+        if (deferring) {  // the first fill: stage n_held
+          held_kb[n_held] = kb;
+          held_mt[n_held++] = mt;
+        }
+        ++issued;
+        if (++stage == s.n_stages) {
+          stage = 0;
+          phase ^= 1u;
+        }
+        if (deferring && n_held == int(s.n_stages)) release();
+      }
+    }
+    if (deferring) release();
+    // Every issued copy lands before the CTA's shared memory goes away (the
+    // leader's barriers see both CTAs' copies).
+    if (leader) {
+      for (uint32_t i = 0; i < s.n_stages; ++i) {
+        const uint32_t fills = issued / s.n_stages + (i < issued % s.n_stages ? 1u : 0u);
+        if (fills) waiter.drain(&full_bar[i], (fills - 1u) & 1u);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ---------------- MMA issuer (the leader CTA's) ----------------
+    if (leader) {
+      const bool issuer = ptx::elect_one();
+      uint32_t stage = 0, phase = 0, acc = 0, acc_phase = 0;
+      bool ok = true;
+      const uint32_t s0 = ptx::smem_u32(smem);
+      const uint64_t desc_a0 = ptx::smem_desc_sw128(s0);
+      const uint64_t desc_b0 = ptx::smem_desc_sw128(s0 + s.a_bytes);
+      auto commit = [&](uint64_t* bar) {
+        if constexpr (kPair)
+          ptx::mma_commit_pair_multicast(bar, 0x3);
+        else
+          ptx::mma_commit(bar);
+      };
+      for (int u = worker; ok && u < s.n_units; u += n_workers) {
+        for (int kb = 0; kb < s.n_kb; ++kb) {
+          if (!waiter.wait_warp(&tempty_bar[acc], acc_phase ^ 1u) ||
+              !waiter.wait_warp(&full_bar[stage], phase)) {
+            ok = false;
+            break;
+          }
+          ptx::tc_fence_after();
+          if (issuer) {
+            const uint32_t d_tmem = tmem_base + acc * kN;
+            const uint64_t off = uint64_t((stage * s.stage_bytes) >> 4);
+#pragma unroll
+            for (int k = 0; k < kBK / kUK; ++k) {
+              const uint64_t da = desc_a0 + off + uint64_t(kUK >> 4) * k;
+              const uint64_t db = desc_b0 + off + uint64_t(kUK >> 4) * k;
+              if constexpr (kPair)
+                ptx::mma_f8_pair(d_tmem, da, db, kIdesc, k != 0 ? 1u : 0u);
+              else
+                ptx::mma_f8(d_tmem, da, db, kIdesc, k != 0 ? 1u : 0u);
+            }
+            commit(&empty_bar[stage]);
+            commit(&tfull_bar[acc]);
+          }
+          __syncwarp();
+          if (++stage == s.n_stages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+          if (++acc == kAcc) {
+            acc = 0;
+            acc_phase ^= 1u;
+          }
+        }
+      }
+      // All MMAs complete before tensor memory is released.
+      if (issuer) {
+        if constexpr (kPair)
+          ptx::mma_commit_pair(drain_bar);
+        else
+          ptx::mma_commit(drain_bar);
+      }
+      __syncwarp();
+      waiter.drain(drain_bar, 0);
+    }
+    __syncwarp();
+  } else {
+    // ---------------- sums ----------------
+    if (s.pdl) ptx::grid_dependency_wait();  // a_scale may still be in flight
+    const int quad = warp & 3;  // the tensor-memory lane quadrant this warp may read
+    const int half = (warp - 2) >> 2;
+    uint32_t acc = 0, acc_phase = 0;
+    bool ok = true;
+    for (int u = worker; ok && u < s.n_units; u += n_workers) {
+      const int nt = u / s.n_mt, mt = u - nt * s.n_mt;
+      const int row0 = (mt * kCtas + rank) * kBM + quad * 32;
+      const int row = row0 + lane;
+      const int col0 = nt * kN + half * kCols;
+      const bool busy = row0 < s.M && col0 < s.V;
+      const float* sa = s.a_scale + int64_t(min(row, s.M - 1)) * s.lda_scale;
+      const float* sw = s.w_scale + int64_t(min(col0, s.V - 1) / kBlock) * s.ldw_scale;
+      uint64_t sum[kCols / 2];
+#pragma unroll
+      for (int i = 0; i < kCols / 2; ++i) sum[i] = 0ull;
+      for (int kb = 0; kb < s.n_kb; ++kb) {
+        const uint32_t f = __float_as_uint(sa[kb] * sw[kb]);
+        const uint64_t scale = ptx::pack2(f, f);
+        if (!waiter.wait_warp(&tfull_bar[acc], acc_phase)) {
+          ok = false;
+          break;
+        }
+        ptx::tc_fence_after();
+        if (busy) {
+          const uint32_t taddr =
+              tmem_base + (uint32_t(quad * 32) << 16) + acc * kN + uint32_t(half * kCols);
+#pragma unroll
+          for (int c = 0; c < kCols / 32; ++c) {
+            uint32_t r[32];
+            ptx::tmem_ld_32x32b_x32(taddr + uint32_t(c * 32), r);
+            ptx::tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              ptx::fma2(sum[c * 16 + i], ptx::pack2(r[2 * i], r[2 * i + 1]), scale);
+          }
+        }
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if constexpr (kPair)
+            ptx::mbar_arrive_cluster_relaxed(ptx::cluster_addr(&tempty_bar[acc], 0));
+          else
+            ptx::mbar_arrive(&tempty_bar[acc]);
+        }
+        if (++acc == kAcc) {
+          acc = 0;
+          acc_phase ^= 1u;
+        }
+      }
+      if (!ok || !busy || row >= s.M) continue;
+      if (s.out_f32) {
+        float* out = static_cast<float*>(s.out) + int64_t(row) * s.ldo + col0;
+#pragma unroll
+        for (int i = 0; i < kCols / 4; ++i) {
+          uint32_t v[4];
+          ptx::unpack2(sum[2 * i], v[0], v[1]);
+          ptx::unpack2(sum[2 * i + 1], v[2], v[3]);
+          if (s.out_vec && col0 + 4 * i + 4 <= s.V) {
+            *reinterpret_cast<uint4*>(out + 4 * i) = make_uint4(v[0], v[1], v[2], v[3]);
+          } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              if (col0 + 4 * i + j < s.V) out[4 * i + j] = __uint_as_float(v[j]);
+          }
+        }
+      } else {
+        uint16_t* out = static_cast<uint16_t*>(s.out) + int64_t(row) * s.ldo + col0;
+#pragma unroll
+        for (int i = 0; i < kCols / 8; ++i) {
+          uint32_t v[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            uint32_t lo, hi;
+            ptx::unpack2(sum[4 * i + j], lo, hi);
+            v[j] = vocab::pack_bf16(__uint_as_float(lo), __uint_as_float(hi));
+          }
+          if (s.out_vec && col0 + 8 * i + 8 <= s.V) {
+            *reinterpret_cast<uint4*>(out + 8 * i) = make_uint4(v[0], v[1], v[2], v[3]);
+          } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              if (col0 + 8 * i + j < s.V) out[8 * i + j] = uint16_t(v[j / 2] >> (16 * (j & 1)));
+          }
+        }
+      }
+    }
+  }
+
+  ptx::tc_fence_before();
+  __syncthreads();
+  // Both CTAs are done with each other's barriers and the MMAs have drained
+  // before the pair's tensor memory is released.
+  if constexpr (kPair) ptx::cluster_sync();
+  if (warp == 1) {
+    ptx::tc_fence_after();
+    if constexpr (kPair)
+      ptx::tmem_dealloc_pair(tmem_base, kTmemCols);
+    else
+      ptx::tmem_dealloc(tmem_base, kTmemCols);
+  }
+  if constexpr (kPair) ptx::cluster_sync();
+}
+
+// ---------------------------------------------------------------------------
+// Host side
+// ---------------------------------------------------------------------------
+using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                   const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                   const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+constexpr int kMaxDevices = 64;
+constexpr int64_t kMost = INT_MAX - 512;  // sizes, so that a tile's end fits 32 bits
+constexpr uint64_t kWaitLimitNs = 2000000000ull;  // 2 s
+
+struct Device {
+  bool initialised = false;
+  fs_status status = FS_ERR_UNSUPPORTED;
+  int sms = 0, pairs = 0;
+  EncodeTiledFn encode = nullptr;
+  int* error_word = nullptr;
+};
+std::mutex g_mu;
+Device g_devices[kMaxDevices];
+
+bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+int64_t element(int dtype) { return dtype == FS_F32 ? 4 : 2; }
+bool known(int dtype) { return dtype == FS_BF16 || dtype == FS_F32; }
+
+template <int kN, bool kPair>
+bool prepare_kernel(int sms, int* pairs) {
+  auto k = matmul_kernel<kN, kPair>;
+  if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kSmemBytes)) !=
+      cudaSuccess)
+    return false;
+  if (!kPair) return true;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = 2;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.gridDim = dim3(unsigned(sms / 2 * 2), 1, 1);
+  cfg.dynamicSmemBytes = kSmemBytes;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  int n = 0;
+  if (cudaOccupancyMaxActiveClusters(&n, k, &cfg) != cudaSuccess || n < 1) return false;
+  *pairs = std::min(*pairs, n);
+  return true;
+}
+
+// The current device, if it is a GB300 (sm_103).
+fs_status device_setup(const Device** out) {
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) {
+    cudaGetLastError();
+    return FS_ERR_UNSUPPORTED;
+  }
+  std::lock_guard<std::mutex> lock(g_mu);
+  Device& d = g_devices[dev];
+  if (!d.initialised) {
+    int major = 0, minor = 0;
+    if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+      cudaGetLastError();
+      return FS_ERR_CUDA;
+    }
+    d.status = FS_ERR_UNSUPPORTED;
+    if (major == 10 && minor == 3) {
+      d.pairs = d.sms / 2;
+      void* fn = nullptr;
+      cudaDriverEntryPointQueryResult q;
+      d.error_word = device_error_word();
+      const bool ok = d.error_word != nullptr && prepare_kernel<64, false>(d.sms, &d.pairs) &&
+                      prepare_kernel<128, false>(d.sms, &d.pairs) &&
+                      prepare_kernel<256, false>(d.sms, &d.pairs) &&
+                      prepare_kernel<256, true>(d.sms, &d.pairs) &&
+                      cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000,
+                                                       cudaEnableDefault, &q) == cudaSuccess &&
+                      q == cudaDriverEntryPointSuccess && fn != nullptr;
+      cudaGetLastError();
+      d.encode = reinterpret_cast<EncodeTiledFn>(fn);
+      d.status = ok ? FS_OK : FS_ERR_CUDA;
+    }
+    d.initialised = true;
+  }
+  *out = &d;
+  return d.status;
+}
+
+// 2-D tensor map of bytes with 128-byte-swizzled boxes of 128 x rows; elements past
+// the extents read as zero.
+bool encode(const Device& dev, CUtensorMap* m, const void* base, int64_t inner, int64_t outer,
+            int64_t ld, int box_rows) {
+  const cuuint64_t dims[2] = {cuuint64_t(inner), cuuint64_t(outer)};
+  const cuuint64_t strides[1] = {cuuint64_t(ld)};
+  const cuuint32_t box[2] = {cuuint32_t(kBK), cuuint32_t(box_rows)};
+  const cuuint32_t estr[2] = {1, 1};
+  return dev.encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides,
+                    box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// The smallest number of workers that needs no more waves than all of them.
+int balanced(int64_t units, int workers) {
+  if (units <= workers) return int(units);
+  return int(ceil_div(units, ceil_div(units, workers)));
+}
+
+template <int kN, bool kPair>
+fs_status launch(const Device& dev, const fs_matmul_fp8_args& a, Plan s, cudaStream_t stream) {
+  const int64_t n_mt = ceil_div(a.M, kPair ? 2 * kBM : kBM), n_nt = ceil_div(a.V, kN);
+  if (n_mt * n_nt > INT_MAX - 1024) return FS_ERR_INVALID_ARG;  // past it by a stride
+  s.n_mt = int32_t(n_mt);
+  s.n_nt = int32_t(n_nt);
+  s.n_units = int32_t(n_mt * n_nt);
+  const int box_rows = int(std::min<int64_t>(kBM, ceil_div(a.M, 8) * 8));
+  s.a_bytes = uint32_t(box_rows) * kBK;
+  s.stage_bytes = s.a_bytes + (kPair ? kN / 2 : kN) * kBK;
+  s.n_stages = ring_stages<kN, kPair>(s.a_bytes);
+  CUtensorMap ta, tb;
+  // Of a single row the stride is any that the map takes.
+  const int64_t lda = a.M > 1 ? a.lda : ceil_div(a.d, 16) * 16;
+  const int64_t ldw = a.V > 1 ? a.ldw : ceil_div(a.d, 16) * 16;
+  if (!encode(dev, &ta, a.A, a.d, a.M, lda, box_rows) ||
+      !encode(dev, &tb, a.W, a.d, a.V, ldw, kPair ? kN / 2 : kN))
+    return FS_ERR_CUDA;
+  cudaLaunchAttribute attr[2];
+  unsigned n = 0;
+  if (kPair) {
+    attr[n].id = cudaLaunchAttributeClusterDimension;
+    attr[n].val.clusterDim.x = 2;
+    attr[n].val.clusterDim.y = attr[n].val.clusterDim.z = 1;
+    ++n;
+  }
+  if (s.pdl) {
+    attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[n].val.programmaticStreamSerializationAllowed = 1;
+    ++n;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(balanced(s.n_units, kPair ? dev.pairs : dev.sms) * (kPair ? 2 : 1)));
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.dynamicSmemBytes = kSmemBytes;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = n;
+  if (cudaLaunchKernelEx(&cfg, matmul_kernel<kN, kPair>, ta, tb, s) != cudaSuccess) {
+    cudaGetLastError();
+    return FS_ERR_CUDA;
+  }
+  return FS_OK;
+}
+
+template <class T>
+void launch_quantize(const QuantParams& p, int block_rows, bool vec, unsigned blocks,
+                     cudaStream_t stream) {
+  if (block_rows == 1) {
+    if (vec)
+      quantize_rows_kernel<T, true><<<blocks, kRowThreads, 0, stream>>>(p);
+    else
+      quantize_rows_kernel<T, false><<<blocks, kRowThreads, 0, stream>>>(p);
+  } else {
+    if (vec)
+      quantize_tile_kernel<T, true><<<blocks, kTileThreads, 0, stream>>>(p);
+    else
+      quantize_tile_kernel<T, false><<<blocks, kTileThreads, 0, stream>>>(p);
+  }
+}
+
+}  // namespace
+}  // namespace fp8
+}  // namespace fs
+
+using namespace fs::fp8;
+
+extern "C" fs_status fs_quantize(const void* x, int64_t N, int64_t d, int64_t ldx, int x_dtype,
+                                 int block_rows, void* values, int64_t ldv, float* scale,
+                                 int64_t lds, void* stream_ptr) {
+  if (N < 0 || N > INT_MAX - kBlock || d < 1 || d > INT_MAX - kBlock || !known(x_dtype) ||
+      (block_rows != 1 && block_rows != kBlock))
+    return FS_ERR_INVALID_ARG;
+  if (N == 0) return FS_OK;
+  const int64_t col_blocks = ceil_div(d, kBlock);
+  if ((N > 1 && (ldx < d || ldv < d)) || (N > block_rows && lds < col_blocks))
+    return FS_ERR_INVALID_ARG;
+  if (!x || !values || !scale || !aligned(x, element(x_dtype)) || !aligned(scale, 4))
+    return FS_ERR_INVALID_ARG;
+  const int64_t blocks = block_rows == 1 ? ceil_div(N * col_blocks, kRowThreads / 16)
+                                         : ceil_div(N, kBlock) * col_blocks;
+  if (blocks > INT_MAX) return FS_ERR_INVALID_ARG;
+  const Device* dev = nullptr;
+  const fs_status st = device_setup(&dev);
+  if (st != FS_OK) return st;
+  QuantParams p = {};
+  p.x = x;
+  p.ldx = N > 1 ? ldx : 0;
+  p.values = static_cast<uint8_t*>(values);
+  p.ldv = N > 1 ? ldv : 0;
+  p.scale = scale;
+  p.lds = lds;
+  p.N = int32_t(N);
+  p.d = int32_t(d);
+  p.col_blocks = int32_t(col_blocks);
+  const bool vec = aligned(x, 16) && p.ldx * element(x_dtype) % 16 == 0 && aligned(values, 8) &&
+                   p.ldv % 8 == 0;
+  cudaStream_t stream = static_cast<cudaStream_t>(stream_ptr);
+  if (x_dtype == FS_F32)
+    launch_quantize<float>(p, block_rows, vec, unsigned(blocks), stream);
+  else
+    launch_quantize<__nv_bfloat16>(p, block_rows, vec, unsigned(blocks), stream);
+  return cudaGetLastError() == cudaSuccess ? FS_OK : FS_ERR_CUDA;
+}
+
+extern "C" fs_status fs_matmul_fp8(const fs_matmul_fp8_args* args, void* stream_ptr) {
+  if (!args) return FS_ERR_INVALID_ARG;
+  const fs_matmul_fp8_args& a = *args;
+  if (a.M < 0 || a.M > kMost || a.d < 1 || a.d > kMost || a.V < 1 || a.V > kMost ||
+      !known(a.out_dtype) || (a.flags & ~FS_FLAG_OVERLAP_PREVIOUS))
+    return FS_ERR_INVALID_ARG;
+  if (ceil_div(a.M, kBM) * ceil_div(a.V, 64) > INT_MAX) return FS_ERR_INVALID_ARG;
+  if (a.M == 0) return FS_OK;
+  const int64_t n_kb = ceil_div(a.d, kBK);
+  if ((a.M > 1 && (a.lda < a.d || a.lda % 16 || a.lda_scale < n_kb || a.ldo < a.V)) ||
+      (a.V > 1 && (a.ldw < a.d || a.ldw % 16)) || (a.V > kBlock && a.ldw_scale < n_kb))
+    return FS_ERR_INVALID_ARG;
+  if (!a.A || !a.a_scale || !a.W || !a.w_scale || !a.out || !aligned(a.A, 16) ||
+      !aligned(a.W, 16) || !aligned(a.a_scale, 4) || !aligned(a.w_scale, 4) ||
+      !aligned(a.out, element(a.out_dtype)))
+    return FS_ERR_INVALID_ARG;
+  const Device* dev = nullptr;
+  const fs_status st = device_setup(&dev);
+  if (st != FS_OK) return st;
+  Plan s = {};
+  s.n_kb = int32_t(n_kb);
+  s.M = int32_t(a.M);
+  s.V = int32_t(a.V);
+  s.pdl = (a.flags & FS_FLAG_OVERLAP_PREVIOUS) ? 1u : 0u;
+  s.a_scale = a.a_scale;
+  s.lda_scale = a.lda_scale;
+  s.w_scale = a.w_scale;
+  s.ldw_scale = a.ldw_scale;
+  s.out = a.out;
+  s.ldo = a.M > 1 ? a.ldo : 0;
+  s.out_f32 = a.out_dtype == FS_F32;
+  s.out_vec = aligned(a.out, 16) && s.ldo * element(a.out_dtype) % 16 == 0;
+  s.wait_limit_ns = kWaitLimitNs;
+  s.error_word = dev->error_word;
+  cudaStream_t stream = static_cast<cudaStream_t>(stream_ptr);
+  if (a.M > kBM) return launch<256, true>(*dev, a, s, stream);
+  // Few units leave SMs without work: the widest that still gives each SM one.
+  if (ceil_div(a.V, 64) <= dev->sms) return launch<64, false>(*dev, a, s, stream);
+  if (ceil_div(a.V, 128) <= dev->sms) return launch<128, false>(*dev, a, s, stream);
+  return launch<256, false>(*dev, a, s, stream);
+}

@@ -1,5 +1,5 @@
-// fs_marshal.cpp -- argument marshalling of the vocabulary-end operators
-// (fs_vocab.h) for Python: tensors are checked and become device pointers, sizes
+// fs_marshal.cpp -- argument marshalling of the operators of fs_vocab.h and
+// fs_speculate.h for Python: tensors are checked and become device pointers, sizes
 // and strides, results are allocated, and the C ABI is called.  No part of an
 // operator is computed here.
 //
@@ -23,9 +23,11 @@
 #include <algorithm>
 #include <cstdint>
 #include <cstdio>
+#include <cstring>
 #include <exception>
 #include <string>
 
+#include "fs_speculate.h"
 #include "fs_vocab.h"
 
 namespace {
@@ -38,6 +40,10 @@ struct Entries {
   decltype(&fs_embed) embed;
   decltype(&fs_embed_grad) embed_grad;
   decltype(&fs_embed_grad_workspace_size) embed_grad_size;
+  decltype(&fs_quantize) quantize;
+  decltype(&fs_matmul_fp8) matmul_fp8;
+  decltype(&fs_probs) probs;
+  decltype(&fs_verify) verify;
 } g;
 PyObject* g_error = nullptr;
 
@@ -73,8 +79,13 @@ bool truth(PyObject* o) {
 }
 
 const char* type_name(at::ScalarType t) {
-  return t == at::kBFloat16 ? "bfloat16" : t == at::kFloat ? "float32" : t == at::kLong ? "int64"
-                                                                                        : "int32";
+  switch (t) {
+    case at::kBFloat16: return "bfloat16";
+    case at::kFloat: return "float32";
+    case at::kLong: return "int64";
+    case at::kFloat8_e4m3fn: return "float8_e4m3fn";
+    default: return "int32";
+  }
 }
 
 // Address of a contiguous vector of n elements.
@@ -160,16 +171,17 @@ struct Mask {
   void* data = nullptr;
   int64_t ld = 0;
 };
-Mask mask_of(PyObject* o, const Head& s) {
+Mask mask_of(PyObject* o, int64_t rows, int64_t V, c10::Device dev) {
   if (o == Py_None) return {};
   const at::Tensor& t = tensor("vocab_mask", o);
-  if (t.scalar_type() != at::kInt || t.device() != s.dev || t.dim() != 2 || t.size(0) != s.B ||
-      t.size(1) < (s.V + 31) / 32 || t.stride(1) != 1)
-    refuse("vocab_mask must be an int32 matrix [B, >= ceil(V/32)] on " + s.dev.str());
+  if (t.scalar_type() != at::kInt || t.device() != dev || t.dim() != 2 || t.size(0) != rows ||
+      t.size(1) < (V + 31) / 32 || t.stride(1) != 1)
+    refuse("vocab_mask must be an int32 matrix [B, >= ceil(V/32)] on " + dev.str());
   // A stride below the row's words (0 for one mask expanded to all rows) is the
   // library's to refuse; a single row's is never used.
-  return {t.data_ptr(), s.B > 1 ? t.stride(0) : t.size(1)};
+  return {t.data_ptr(), rows > 1 ? t.stride(0) : t.size(1)};
 }
+Mask mask_of(PyObject* o, const Head& s) { return mask_of(o, s.B, s.V, s.dev); }
 
 struct Workspace {
   at::Tensor made;  // freed after the call: reused in the order of its stream (On)
@@ -432,27 +444,198 @@ PyObject* py_embed_grad(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// ---- fs_speculate.h ---------------------------------------------------------
+at::ScalarType type_of(int code) { return code == FS_F32 ? at::kFloat : at::kBFloat16; }
+
+// A result [n, d], given or made here with rows on 16-byte boundaries.
+Matrix rows_result(const char* name, Result& r, at::ScalarType type, int64_t n, int64_t d,
+                   c10::Device dev) {
+  if (r.given != Py_None) return matrix(name, tensor(name, r.given), type, n, d, dev);
+  const int64_t unit = type == at::kFloat8_e4m3fn ? 16 : 8;
+  const int64_t ld = (d + unit - 1) / unit * unit;
+  r.made = empty({n, ld}, type, dev);
+  const Matrix m{r.made.data_ptr(), ld};
+  if (ld != d) r.made = r.made.narrow(1, 0, d);
+  return m;
+}
+// The element type of a result: the given tensor's, else the one asked for.
+int result_code(const char* name, PyObject* given, PyObject* code) {
+  return given == Py_None ? int(integer(code)) : element_code(name, tensor(name, given));
+}
+
+// (x, block_rows, out, out_scale, stream) -> (values, scale)
+PyObject* py_quantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 5, [&]() -> PyObject* {
+    const at::Tensor& x = tensor("x", a[0]);
+    const int code = element_code("x", x);
+    const c10::Device dev = x.device();
+    const int64_t N = x.size(0), d = x.size(1), block = integer(a[1]);
+    if (block != 1 && block != FS_FP8_BLOCK)
+      refuse("block_rows must be 1 or " + std::to_string(FS_FP8_BLOCK));
+    const Matrix m = matrix("x", x, x.scalar_type(), N, d, dev);
+    const On on(a[4], dev);
+    Result values{a[2], {}}, scale{a[3], {}};
+    const Matrix v = rows_result("out", values, at::kFloat8_e4m3fn, N, d, dev);
+    const int64_t rows = (N + block - 1) / block, cols = (d + FS_FP8_BLOCK - 1) / FS_FP8_BLOCK;
+    Matrix s{nullptr, cols};
+    if (a[3] == Py_None) {
+      scale.made = empty({rows, cols}, at::kFloat, dev);
+      s.data = scale.made.data_ptr();
+    } else {
+      s = matrix("out_scale", tensor("out_scale", a[3]), at::kFloat, rows, cols, dev);
+    }
+    check("fs_quantize", g.quantize(m.data, N, d, m.ld, code, int(block), v.data, v.ld,
+                                    static_cast<float*>(s.data), s.ld, on.handle()));
+    return tuple_of({&values, &scale});
+  });
+}
+
+// (A, a_scale, W, w_scale, out, out_code, stream, flags) -> out
+PyObject* py_matmul_fp8(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 8, [&]() -> PyObject* {
+    const at::Tensor &A = tensor("A", a[0]), &W = tensor("W", a[2]);
+    if (A.dim() != 2 || W.dim() != 2 || !A.is_cuda())
+      refuse("A and W must be CUDA float8_e4m3fn matrices");
+    const c10::Device dev = A.device();
+    fs_matmul_fp8_args p = {};
+    p.M = A.size(0);
+    p.d = A.size(1);
+    p.V = W.size(0);
+    const int64_t kb = (p.d + FS_FP8_BLOCK - 1) / FS_FP8_BLOCK;
+    const Matrix m = matrix("A", A, at::kFloat8_e4m3fn, p.M, p.d, dev);
+    const Matrix w = matrix("W", W, at::kFloat8_e4m3fn, p.V, p.d, dev);
+    const Matrix as =
+        matrix("a_scale", tensor("a_scale", a[1]), at::kFloat, p.M, kb, dev);
+    const Matrix ws = matrix("w_scale", tensor("w_scale", a[3]), at::kFloat,
+                             (p.V + FS_FP8_BLOCK - 1) / FS_FP8_BLOCK, kb, dev);
+    const On on(a[6], dev);
+    Result out{a[4], {}};
+    p.out_dtype = result_code("out", a[4], a[5]);
+    const Matrix o = rows_result("out", out, type_of(p.out_dtype), p.M, p.V, dev);
+    p.A = m.data;
+    p.lda = m.ld;
+    p.a_scale = static_cast<const float*>(as.data);
+    p.lda_scale = as.ld;
+    p.W = w.data;
+    p.ldw = w.ld;
+    p.w_scale = static_cast<const float*>(ws.data);
+    p.ldw_scale = ws.ld;
+    p.out = o.data;
+    p.ldo = o.ld;
+    p.flags = uint32_t(integer(a[7]));
+    check("fs_matmul_fp8", g.matmul_fp8(&p, on.handle()));
+    return out.wrap();
+  });
+}
+
+// (logits, temperature, vocab_mask, out, out_code, stream) -> out
+PyObject* py_probs(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 6, [&]() -> PyObject* {
+    const at::Tensor& x = tensor("logits", a[0]);
+    fs_probs_args p = {};
+    p.dtype = element_code("logits", x);
+    const c10::Device dev = x.device();
+    p.N = x.size(0);
+    p.V = x.size(1);
+    const Matrix m = matrix("logits", x, x.scalar_type(), p.N, p.V, dev);
+    p.temperature =
+        static_cast<const float*>(vector_or_none("temperature", a[1], at::kFloat, p.N, dev));
+    const Mask mask = mask_of(a[2], p.N, p.V, dev);
+    const On on(a[5], dev);
+    Result out{a[3], {}};
+    p.out_dtype = result_code("out", a[3], a[4]);
+    const Matrix o = rows_result("out", out, type_of(p.out_dtype), p.N, p.V, dev);
+    p.logits = m.data;
+    p.ldl = m.ld;
+    p.vocab_mask = static_cast<const uint32_t*>(mask.data);
+    p.mask_ld = mask.ld;
+    p.out = o.data;
+    p.ldo = o.ld;
+    check("fs_probs", g.probs(&p, on.handle()));
+    return out.wrap();
+  });
+}
+
+// A [B, n, V] tensor of `type` with unit stride along V.
+const at::Tensor& positions(const char* name, PyObject* o, at::ScalarType type, int64_t B,
+                            int64_t n, int64_t V, c10::Device dev) {
+  const at::Tensor& t = tensor(name, o);
+  if (t.scalar_type() != type || t.device() != dev || t.dim() != 3 || t.size(0) != B ||
+      t.size(1) != n || t.size(2) != V || (t.stride(2) != 1 && V > 1))
+    refuse(std::string(name) + " must be a " + type_name(type) + " tensor [" + std::to_string(B) +
+           ", " + std::to_string(n) + ", " + std::to_string(V) + "] with unit stride along V on " +
+           dev.str());
+  return t;
+}
+
+// (p, draft_ids, u, q, out_ids, out_accepted, stream) -> (ids, accepted)
+PyObject* py_verify(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 7, [&]() -> PyObject* {
+    const at::Tensor& t = tensor("p", a[0]);
+    if (t.dim() != 3 || !t.is_cuda() || t.size(1) < 1 ||
+        (t.scalar_type() != at::kBFloat16 && t.scalar_type() != at::kFloat))
+      refuse("p must be a CUDA bfloat16 or float32 tensor [B, K + 1, V]");
+    const c10::Device dev = t.device();
+    fs_verify_args p = {};
+    p.dtype = t.scalar_type() == at::kFloat ? FS_F32 : FS_BF16;
+    p.B = t.size(0);
+    p.K = t.size(1) - 1;
+    p.V = t.size(2);
+    positions("p", a[0], t.scalar_type(), p.B, p.K + 1, p.V, dev);
+    p.p = t.data_ptr();
+    p.p_seq = t.stride(0);
+    p.p_pos = t.stride(1);
+    if (a[3] != Py_None && p.K > 0) {
+      const at::Tensor& q = positions("q", a[3], t.scalar_type(), p.B, p.K, p.V, dev);
+      p.q = q.data_ptr();
+      p.q_seq = q.stride(0);
+      p.q_pos = q.stride(1);
+    }
+    const Matrix ids = matrix("draft_ids", tensor("draft_ids", a[1]), at::kLong, p.B, p.K, dev);
+    const Matrix u = matrix("u", tensor("u", a[2]), at::kFloat, p.B, p.K + 1, dev);
+    const On on(a[6], dev);
+    Result out{a[4], {}}, accepted{a[5], {}};
+    Matrix o{nullptr, p.K + 1};
+    if (a[4] == Py_None) {
+      out.made = empty({p.B, p.K + 1}, at::kLong, dev);
+      o.data = out.made.data_ptr();
+    } else {
+      o = matrix("out_ids", tensor("out_ids", a[4]), at::kLong, p.B, p.K + 1, dev);
+    }
+    if (a[5] == Py_None) {
+      accepted.made = empty({p.B}, at::kLong, dev);
+      p.out_accepted = accepted.made.data_ptr<int64_t>();
+    } else {
+      p.out_accepted = static_cast<int64_t*>(vector("out_accepted", a[5], at::kLong, p.B, dev));
+    }
+    p.draft_ids = static_cast<const int64_t*>(ids.data);
+    p.ld_ids = ids.ld;
+    p.u = static_cast<const float*>(u.data);
+    p.ldu = u.ld;
+    p.out_ids = static_cast<int64_t*>(o.data);
+    p.ld_out = o.ld;
+    check("fs_verify", g.verify(&p, on.handle()));
+    return tuple_of({&out, &accepted});
+  });
+}
+
 // bind(error class, address of each entry point in the order of Entries)
+constexpr int kEntries = 11;
+static_assert(sizeof(Entries) == kEntries * sizeof(void*), "one address each");
 PyObject* py_bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  if (n != 8) {
-    PyErr_SetString(PyExc_TypeError, "bind takes the exception class and 7 addresses");
+  if (n != kEntries + 1) {
+    PyErr_Format(PyExc_TypeError, "bind takes the exception class and %d addresses", kEntries);
     return nullptr;
   }
-  void* at[7];
-  for (int i = 0; i < 7; ++i) {
+  void* at[kEntries];
+  for (int i = 0; i < kEntries; ++i) {
     at[i] = PyLong_AsVoidPtr(a[i + 1]);
     if (at[i] == nullptr) {
       if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "null entry point");
       return nullptr;
     }
   }
-  g.logprobs = reinterpret_cast<decltype(g.logprobs)>(at[0]);
-  g.logprobs_size = reinterpret_cast<decltype(g.logprobs_size)>(at[1]);
-  g.grad = reinterpret_cast<decltype(g.grad)>(at[2]);
-  g.grad_size = reinterpret_cast<decltype(g.grad_size)>(at[3]);
-  g.embed = reinterpret_cast<decltype(g.embed)>(at[4]);
-  g.embed_grad = reinterpret_cast<decltype(g.embed_grad)>(at[5]);
-  g.embed_grad_size = reinterpret_cast<decltype(g.embed_grad_size)>(at[6]);
+  std::memcpy(&g, at, sizeof(g));
   Py_INCREF(a[0]);
   Py_XDECREF(g_error);
   g_error = a[0];
@@ -470,6 +653,10 @@ PyMethodDef g_methods[] = {
     {"logprobs_grad", fast<py_logprobs_grad>(), METH_FASTCALL, "fs_logprobs_grad"},
     {"embed", fast<py_embed>(), METH_FASTCALL, "fs_embed"},
     {"embed_grad", fast<py_embed_grad>(), METH_FASTCALL, "fs_embed_grad"},
+    {"quantize", fast<py_quantize>(), METH_FASTCALL, "fs_quantize"},
+    {"matmul_fp8", fast<py_matmul_fp8>(), METH_FASTCALL, "fs_matmul_fp8"},
+    {"probs", fast<py_probs>(), METH_FASTCALL, "fs_probs"},
+    {"verify", fast<py_verify>(), METH_FASTCALL, "fs_verify"},
     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_marshal", nullptr, -1, g_methods,
                         nullptr, nullptr, nullptr, nullptr};

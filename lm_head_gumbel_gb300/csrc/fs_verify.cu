@@ -1,0 +1,539 @@
+// fs_verify.cu -- fs_probs and fs_verify (fs_speculate.h): probabilities from logits,
+// and the verification of drafted tokens against the target's.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <climits>
+#include <cmath>
+#include <cstdint>
+#include <mutex>
+
+#include "fs_ptx.cuh"
+#include "fs_speculate.h"
+
+namespace fs {
+namespace verify {
+namespace {
+
+__device__ __forceinline__ float wide(float x) { return x; }
+__device__ __forceinline__ float wide(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ void narrow(float* out, float x) { *out = x; }
+__device__ __forceinline__ void narrow(__nv_bfloat16* out, float x) { *out = __float2bfloat16_rn(x); }
+
+// ---------------------------------------------------------------------------
+// Probabilities
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+// exp((l - m) / T) for l <= m, to 3 2^-24 relative at any distance: l - m, and its
+// product with log2(e) / T, are held in two floats, the exponent's whole part goes in
+// as bits.  Below 2^-126 it is 0.
+struct Exp {
+  float m, c_hi, c_lo;  // the maximum, log2(e) / T
+  __device__ __forceinline__ Exp(float max, float T) : m(max) {
+    constexpr float kHi = 1.44269502f, kLo = 1.92596299e-8f;  // log2(e)
+    const float t = fmaxf(T, 0x1p-126f);
+    c_hi = __fdiv_rn(kHi, t);
+    c_lo = __fdiv_rn(fmaf(-c_hi, t, kHi) + kLo, t);
+  }
+  __device__ __forceinline__ float operator()(float l) const {
+    const float t = l - m;
+    const float b = t - l;
+    const float t_lo = (l - (t - b)) - (m + b);
+    const float y = t * c_hi;
+    if (y < -126.0f) return 0.0f;  // -inf too, whose t_lo is NaN
+    const float n = rintf(y);
+    const float f = fmaf(t, c_hi, -n) + fmaf(t, c_lo, t_lo * c_hi);
+    float e;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(f));
+    return e * __int_as_float((int(n) + 127) << 23);
+  }
+};
+
+struct ProbsParams {
+  const void* logits;
+  int64_t ldl;
+  const float* temperature;
+  const uint32_t* mask;
+  int64_t mask_ld;
+  void* out;
+  int64_t ldo;
+  int32_t N, V;
+};
+
+constexpr int kProbThreads = 512;
+
+template <class T, class TO>
+__global__ void __launch_bounds__(kProbThreads) probs_kernel(const ProbsParams p) {
+  __shared__ float s_val[kProbThreads / 32];
+  __shared__ int s_idx[kProbThreads / 32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t row = blockIdx.x;
+  const T* x = static_cast<const T*>(p.logits) + row * p.ldl;
+  TO* out = static_cast<TO*>(p.out) + row * p.ldo;
+  const uint32_t* mask = p.mask ? p.mask + row * p.mask_ld : nullptr;
+  const float temp = p.temperature ? p.temperature[row] : 1.0f;
+  const bool greedy = !(temp > 0.0f && temp < INFINITY);
+  auto allowed = [&](int v) { return mask == nullptr || (mask[v >> 5] >> (v & 31) & 1u) != 0u; };
+
+  float m = -INFINITY;
+  int at = INT_MAX;
+  for (int v = threadIdx.x; v < p.V; v += kProbThreads) {
+    if (!allowed(v)) continue;
+    const float l = wide(x[v]);
+    if (greedy) {
+      if (l > m) m = l, at = v;
+    } else {
+      m = max_nan(m, l);
+    }
+  }
+#pragma unroll
+  for (int s = 16; s > 0; s >>= 1) {
+    const float om = __shfl_xor_sync(0xFFFFFFFFu, m, s);
+    const int oa = __shfl_xor_sync(0xFFFFFFFFu, at, s);
+    if (greedy) {
+      if (om > m || (om == m && oa < at)) m = om, at = oa;
+    } else {
+      m = max_nan(m, om);
+    }
+  }
+  if (lane == 0) s_val[warp] = m, s_idx[warp] = at;
+  __syncthreads();
+  m = s_val[0], at = s_idx[0];
+  for (int w = 1; w < kProbThreads / 32; ++w) {
+    if (greedy) {
+      if (s_val[w] > m || (s_val[w] == m && s_idx[w] < at)) m = s_val[w], at = s_idx[w];
+    } else {
+      m = max_nan(m, s_val[w]);
+    }
+  }
+  if (greedy || m == -INFINITY) {
+    __syncthreads();
+    for (int v = threadIdx.x; v < p.V; v += kProbThreads)
+      narrow(out + v, greedy && v == at ? 1.0f : 0.0f);
+    return;
+  }
+  const Exp e(m, temp);
+  float sum = 0.0f;
+  for (int v = threadIdx.x; v < p.V; v += kProbThreads)
+    if (allowed(v)) sum += e(wide(x[v]));
+#pragma unroll
+  for (int s = 16; s > 0; s >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, s);
+  __syncthreads();
+  if (lane == 0) s_val[warp] = sum;
+  __syncthreads();
+  sum = 0.0f;
+  for (int w = 0; w < kProbThreads / 32; ++w) sum += s_val[w];
+  const float inv = __fdiv_rn(1.0f, sum);
+  for (int v = threadIdx.x; v < p.V; v += kProbThreads)
+    narrow(out + v, allowed(v) ? e(wide(x[v])) * inv : 0.0f);
+}
+
+// ---------------------------------------------------------------------------
+// Verification
+// ---------------------------------------------------------------------------
+constexpr int kThreads = 512;
+constexpr int kWarps = kThreads / 32;
+constexpr int kSegment = 1024;      // elements of a segment, doubled until there are
+constexpr int kMaxSegments = 1024;  // at most so many
+constexpr int kMaxCluster = 8;
+
+struct VerifyParams {
+  const void* p;
+  const void* q;
+  const int64_t* ids;
+  const float* u;
+  int64_t p_seq, p_pos, q_seq, q_pos, ld_ids, ldu;
+  int64_t* out_ids;
+  int64_t ld_out;
+  int64_t* accepted;
+  int32_t K, V;
+  int32_t segment, n_segments;
+};
+
+// A sum in two floats: 2^-46 or so of the total, whatever the order.
+struct Sum {
+  float hi = 0.0f, lo = 0.0f;
+  __device__ __forceinline__ void add(float w) {
+    const float s = hi + w;
+    const float b = s - hi;
+    lo += (hi - (s - b)) + (w - b);
+    hi = s;
+  }
+  __device__ __forceinline__ double total() const { return double(hi) + double(lo); }
+};
+
+__device__ __forceinline__ double shfl_xor(double v, int s) {
+  return __shfl_xor_sync(0xFFFFFFFFu, v, s);
+}
+
+enum Mode { kTarget = 0, kResidual = 1, kWithout = 2 };
+
+// The weights that a sequence's last token is drawn with.
+template <class T>
+struct Weights {
+  const T* p;
+  const T* q;
+  int mode, without;
+  __device__ __forceinline__ float of(float pv, float qv, int v) const {
+    const float w = mode == kResidual ? pv - qv : pv;
+    // Negative, infinite and NaN weights are 0.
+    return w > 0.0f && w < INFINITY && !(mode == kWithout && v == without) ? w : 0.0f;
+  }
+  __device__ __forceinline__ float at(int v) const {
+    return of(wide(p[v]), mode == kResidual ? wide(q[v]) : 0.0f, v);
+  }
+};
+
+// A warp's sum of a segment.  Every lane takes runs of 4 (fp32) or 8 (bf16) elements,
+// 32 runs side by side.
+template <class T>
+__device__ __forceinline__ double segment_sum(const Weights<T>& w, int begin, int end, int lane) {
+  constexpr int kRun = 16 / int(sizeof(T));
+  Sum s;
+  for (int v0 = begin + lane * kRun; v0 < end; v0 += 32 * kRun) {
+#pragma unroll
+    for (int i = 0; i < kRun; ++i)
+      if (v0 + i < end) s.add(w.at(v0 + i));
+  }
+  double t = s.total();
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) t += shfl_xor(t, d);
+  return t;
+}
+
+struct Shared {
+  double sums[kMaxSegments];
+  double scan[kWarps];
+  double before;  // sum of the segments before the chosen one
+  double target;
+  int accepted, mode, without;
+  int segment, first, last;
+};
+
+// How many drafts pass, and what the next token is drawn from.  One warp.
+template <class T>
+__device__ __forceinline__ void accept(const VerifyParams& a, int64_t b, Shared& sm, int lane) {
+  int n = 0;
+  bool rejected = false;
+  int without = -1;
+  for (int i0 = 0; i0 < a.K; i0 += 32) {
+    const int i = i0 + lane;
+    bool pass = false, none = true;
+    int x32 = -1;
+    if (i < a.K) {
+      const int64_t x = a.ids[b * a.ld_ids + i];
+      none = x < 0;
+      if (x >= 0 && x < a.V) {
+        x32 = int(x);
+        const float u = a.u[b * a.ldu + i];
+        const float uc = u > 0.0f ? fminf(u, 0x1.fffffep-1f) : 0.0f;
+        const float px = wide(static_cast<const T*>(a.p)[b * a.p_seq + i * a.p_pos + x]);
+        const float qx =
+            a.q ? wide(static_cast<const T*>(a.q)[b * a.q_seq + i * a.q_pos + x]) : 1.0f;
+        pass = double(uc) * double(qx) < double(px);
+      }
+    }
+    const uint32_t stop = __ballot_sync(0xFFFFFFFFu, !pass);
+    if (stop != 0u) {
+      const int at = __ffs(stop) - 1;
+      n = i0 + at;  // K where the lanes past the last draft stop
+      rejected = !__shfl_sync(0xFFFFFFFFu, int(none), at);
+      without = __shfl_sync(0xFFFFFFFFu, x32, at);
+      break;
+    }
+    n = i0 + 32;
+  }
+  if (lane == 0) {
+    sm.accepted = n;
+    sm.mode = !rejected ? kTarget : a.q ? kResidual : kWithout;
+    sm.without = without;
+  }
+}
+
+// The segment in which the sums pass u times their total; false if all are 0.  One warp.
+__device__ __forceinline__ bool find_segment(const VerifyParams& a, float u, Shared& sm,
+                                             int lane) {
+  const int per = (a.n_segments + 31) / 32;
+  const int s0 = lane * per, s1 = min(s0 + per, a.n_segments);
+  double own = 0.0;
+  for (int s = s0; s < s1; ++s) own += sm.sums[s];
+  double incl = own;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const double o = __shfl_up_sync(0xFFFFFFFFu, incl, d);
+    if (lane >= d) incl += o;
+  }
+  const double total = __shfl_sync(0xFFFFFFFFu, incl, 31);
+  const uint32_t some = __ballot_sync(0xFFFFFFFFu, own > 0.0);
+  if (some == 0u) return false;
+  const float uc = u > 0.0f ? fminf(u, 0x1.fffffep-1f) : 0.0f;
+  const double target = double(uc) * total;
+  const uint32_t past = __ballot_sync(0xFFFFFFFFu, own > 0.0 && incl > target);
+  // Past every sum (by their rounding): the last one that is not 0.
+  const int at = past != 0u ? __ffs(past) - 1 : 31 - __clz(some);
+  if (lane == at) {
+    double before = incl - own, run = before;
+    int chosen = -1;
+    for (int s = s0; s < s1; ++s) {
+      if (!(sm.sums[s] > 0.0)) continue;
+      before = run;
+      run += sm.sums[s];
+      chosen = s;
+      if (run > target) break;
+    }
+    sm.segment = chosen;
+    sm.before = before;
+    sm.target = target;
+  }
+  return true;
+}
+
+// The first element of the chosen segment whose sum passes the target.  All threads.
+template <class T>
+__device__ __forceinline__ int find_element(const VerifyParams& a, const Weights<T>& w, Shared& sm) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int per = a.segment / kThreads;
+  const int v0 = sm.segment * a.segment + int(threadIdx.x) * per;
+  const int v1 = v0 < a.V ? v0 + min(per, a.V - v0) : v0;
+  double own = 0.0;
+  for (int v = v0; v < v1; ++v) own += double(w.at(v));
+  double incl = own;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const double o = __shfl_up_sync(0xFFFFFFFFu, incl, d);
+    if (lane >= d) incl += o;
+  }
+  if (lane == 31) sm.scan[warp] = incl;
+  if (threadIdx.x == 0) sm.first = INT_MAX, sm.last = -1;
+  __syncthreads();
+  double run = sm.before;
+  for (int i = 0; i < warp; ++i) run += sm.scan[i];
+  run += incl - own;
+  for (int v = v0; v < v1; ++v) {
+    const float x = w.at(v);
+    if (!(x > 0.0f)) continue;
+    run += double(x);
+    atomicMax(&sm.last, v);
+    if (run > sm.target) {
+      atomicMin(&sm.first, v);
+      break;
+    }
+  }
+  __syncthreads();
+  return sm.first != INT_MAX ? sm.first : sm.last;
+}
+
+template <class T>
+__global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyParams a) {
+  __shared__ Shared sm;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  uint32_t n_ctas;
+  asm("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(n_ctas));
+  const int rank = int(ptx::cluster_ctarank());
+  const int64_t b = blockIdx.x / n_ctas;
+  if (warp == 0) accept<T>(a, b, sm, lane);
+  __syncthreads();
+  // Every CTA of the cluster has started before another one writes its memory.
+  ptx::cluster_sync();
+  const int n = sm.accepted;
+  Weights<T> w;
+  w.p = static_cast<const T*>(a.p) + b * a.p_seq + n * a.p_pos;
+  w.mode = sm.mode;
+  w.without = sm.without;
+  w.q = w.mode == kResidual ? static_cast<const T*>(a.q) + b * a.q_seq + n * a.q_pos : nullptr;
+  const uint32_t sums0 = ptx::cluster_addr(sm.sums, 0);
+  for (int s = rank * kWarps + warp; s < a.n_segments; s += int(n_ctas) * kWarps) {
+    const int begin = s * a.segment;
+    const double t = segment_sum(w, begin, begin + min(a.segment, a.V - begin), lane);
+    if (lane == 0)
+      asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(sums0 + uint32_t(s) * 8u), "d"(t)
+                   : "memory");
+  }
+  ptx::cluster_sync();
+  if (rank != 0) return;
+  const float u = a.u[b * a.ldu + a.K];
+  __shared__ int found;
+  if (warp == 0) {
+    const bool some = find_segment(a, u, sm, lane);
+    if (lane == 0) found = some;
+  }
+  __syncthreads();
+  if (!found && w.mode != kTarget) {
+    // Nothing is left of p after a rejection: the draw is from p.
+    w.mode = kTarget;
+    for (int s = warp; s < a.n_segments; s += kWarps) {
+      const int begin = s * a.segment;
+      const double t = segment_sum(w, begin, begin + min(a.segment, a.V - begin), lane);
+      if (lane == 0) sm.sums[s] = t;
+    }
+    __syncthreads();
+    if (warp == 0) {
+      const bool some = find_segment(a, u, sm, lane);
+      if (lane == 0) found = some;
+    }
+    __syncthreads();
+  }
+  const int drawn = found ? find_element(a, w, sm) : -1;
+  for (int i = threadIdx.x; i <= a.K; i += kThreads)
+    a.out_ids[b * a.ld_out + i] = i < n ? a.ids[b * a.ld_ids + i] : i == n ? int64_t(drawn) : -1;
+  if (threadIdx.x == 0 && a.accepted) a.accepted[b] = n;
+}
+
+// ---------------------------------------------------------------------------
+// Host side
+// ---------------------------------------------------------------------------
+constexpr int kMaxDevices = 64;
+std::mutex g_mu;
+struct Device {
+  bool known = false;
+  fs_status status = FS_ERR_UNSUPPORTED;
+  int sms = 0;
+};
+Device g_devices[kMaxDevices];
+
+// The current device, if it is a GB300 (sm_103).
+fs_status device_setup(const Device** out) {
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) {
+    cudaGetLastError();
+    return FS_ERR_UNSUPPORTED;
+  }
+  std::lock_guard<std::mutex> lock(g_mu);
+  Device& d = g_devices[dev];
+  if (!d.known) {
+    int major = 0, minor = 0;
+    if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+      cudaGetLastError();
+      return FS_ERR_CUDA;
+    }
+    d.status = major == 10 && minor == 3 ? FS_OK : FS_ERR_UNSUPPORTED;
+    d.known = true;
+  }
+  *out = &d;
+  return d.status;
+}
+
+bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+uintptr_t element(int dtype) { return dtype == FS_F32 ? 4 : 2; }
+bool known(int dtype) { return dtype == FS_BF16 || dtype == FS_F32; }
+constexpr int64_t kMostV = INT_MAX - 65536;  // a segment's end fits 32 bits
+
+template <class T>
+void launch_probs(const ProbsParams& p, int out_dtype, cudaStream_t stream) {
+  if (out_dtype == FS_F32)
+    probs_kernel<T, float><<<unsigned(p.N), kProbThreads, 0, stream>>>(p);
+  else
+    probs_kernel<T, __nv_bfloat16><<<unsigned(p.N), kProbThreads, 0, stream>>>(p);
+}
+
+}  // namespace
+}  // namespace verify
+}  // namespace fs
+
+using namespace fs::verify;
+
+extern "C" fs_status fs_probs(const fs_probs_args* args, void* stream_ptr) {
+  if (!args) return FS_ERR_INVALID_ARG;
+  const fs_probs_args& a = *args;
+  if (a.N < 0 || a.N > INT_MAX || a.V < 1 || a.V > kMostV || !known(a.dtype) ||
+      !known(a.out_dtype))
+    return FS_ERR_INVALID_ARG;
+  if (a.N == 0) return FS_OK;
+  if (a.N > 1 && (a.ldl < a.V || a.ldo < a.V || (a.vocab_mask && a.mask_ld < ceil_div(a.V, 32))))
+    return FS_ERR_INVALID_ARG;
+  if (!a.logits || !a.out || !aligned(a.logits, element(a.dtype)) ||
+      !aligned(a.out, element(a.out_dtype)) || !aligned(a.temperature, 4) ||
+      !aligned(a.vocab_mask, 4))
+    return FS_ERR_INVALID_ARG;
+  if (a.out == a.logits && (a.dtype != a.out_dtype || (a.N > 1 && a.ldl != a.ldo)))
+    return FS_ERR_INVALID_ARG;
+  const Device* dev = nullptr;
+  const fs_status st = device_setup(&dev);
+  if (st != FS_OK) return st;
+  ProbsParams p = {};
+  p.logits = a.logits;
+  p.ldl = a.ldl;
+  p.temperature = a.temperature;
+  p.mask = a.vocab_mask;
+  p.mask_ld = a.mask_ld;
+  p.out = a.out;
+  p.ldo = a.ldo;
+  p.N = int32_t(a.N);
+  p.V = int32_t(a.V);
+  cudaStream_t stream = static_cast<cudaStream_t>(stream_ptr);
+  if (a.dtype == FS_F32)
+    launch_probs<float>(p, a.out_dtype, stream);
+  else
+    launch_probs<__nv_bfloat16>(p, a.out_dtype, stream);
+  return cudaGetLastError() == cudaSuccess ? FS_OK : FS_ERR_CUDA;
+}
+
+extern "C" fs_status fs_verify(const fs_verify_args* args, void* stream_ptr) {
+  if (!args) return FS_ERR_INVALID_ARG;
+  const fs_verify_args& a = *args;
+  if (a.B < 0 || a.B >= (1 << 24) || a.K < 0 || a.K > FS_VERIFY_DRAFTS_MAX || a.V < 1 ||
+      a.V > kMostV || !known(a.dtype))
+    return FS_ERR_INVALID_ARG;
+  if (a.B == 0) return FS_OK;
+  if (!a.p || !a.u || !a.out_ids || (a.K > 0 && !a.draft_ids) || !aligned(a.p, element(a.dtype)) ||
+      !aligned(a.q, element(a.dtype)) || !aligned(a.u, 4) || !aligned(a.draft_ids, 8) ||
+      !aligned(a.out_ids, 8) || !aligned(a.out_accepted, 8))
+    return FS_ERR_INVALID_ARG;
+  if (a.p_seq < 0 || a.p_pos < 0 || a.q_seq < 0 || a.q_pos < 0 ||
+      (a.B > 1 && (a.ld_ids < a.K || a.ldu < a.K + 1 || a.ld_out < a.K + 1)))
+    return FS_ERR_INVALID_ARG;
+  const Device* dev = nullptr;
+  const fs_status st = device_setup(&dev);
+  if (st != FS_OK) return st;
+  VerifyParams p = {};
+  p.p = a.p;
+  p.q = a.K > 0 ? a.q : nullptr;
+  p.ids = a.draft_ids;
+  p.u = a.u;
+  p.p_seq = a.p_seq;
+  p.p_pos = a.p_pos;
+  p.q_seq = a.q_seq;
+  p.q_pos = a.q_pos;
+  p.ld_ids = a.ld_ids;
+  p.ldu = a.ldu;
+  p.out_ids = a.out_ids;
+  p.ld_out = a.ld_out;
+  p.accepted = a.out_accepted;
+  p.K = int32_t(a.K);
+  p.V = int32_t(a.V);
+  int64_t segment = kSegment;
+  while (ceil_div(a.V, segment) > kMaxSegments) segment *= 2;
+  p.segment = int32_t(segment);
+  p.n_segments = int32_t(ceil_div(a.V, segment));
+  // A sequence's row over as many CTAs as leave every SM at most two.
+  int ctas = 1;
+  while (ctas < kMaxCluster && a.B * ctas * 2 <= 2 * dev->sms && ctas * kWarps < p.n_segments)
+    ctas *= 2;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = unsigned(ctas);
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(a.B * ctas));
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = static_cast<cudaStream_t>(stream_ptr);
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  const cudaError_t err = a.dtype == FS_F32
+                              ? cudaLaunchKernelEx(&cfg, verify_kernel<float>, p)
+                              : cudaLaunchKernelEx(&cfg, verify_kernel<__nv_bfloat16>, p);
+  if (err != cudaSuccess) {
+    cudaGetLastError();
+    return FS_ERR_CUDA;
+  }
+  return FS_OK;
+}
