@@ -41,17 +41,17 @@ __device__ __forceinline__ void mma_f8_pair(uint32_t d_tmem, uint64_t a_desc, ui
 __host__ __device__ constexpr uint32_t idesc_e4m3_f32(uint32_t M, uint32_t N) {
   return (1u << 4) | ((N >> 3) << 17) | ((M >> 4) << 24);
 }
-// d += a * b on two fp32 values at once.
-__device__ __forceinline__ void fma2(uint64_t& d, uint64_t a, uint64_t b) {
-  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(d) : "l"(a), "l"(b));
-}
-__device__ __forceinline__ uint64_t pack2(uint32_t lo, uint32_t hi) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
-  return r;
-}
-__device__ __forceinline__ void unpack2(uint64_t v, uint32_t& lo, uint32_t& hi) {
-  asm("mov.b64 {%0, %1}, %2;" : "=r"(lo), "=r"(hi) : "l"(v));
+// Whether the phase with parity `parity` has completed; does not wait.
+__device__ __forceinline__ bool mbar_test_wait(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
 }
 // Two values in e4m3, to nearest even, past 448 to 448; lo in the low byte.
 __device__ __forceinline__ uint32_t cvt_e4m3x2(float lo, float hi) {
@@ -192,22 +192,30 @@ __global__ void __launch_bounds__(kTileThreads) quantize_tile_kernel(const Quant
 // Warp roles as in fs_contract.cuh: warp 0 issues TMA copies into a ring of 128-wide
 // k slices (128 bytes a row, so the swizzle and the descriptors are those of 64 bf16),
 // warp 1 issues the MMAs (M = 128 per CTA, kN vocabulary columns; for CTA pairs M = 256
-// over both), warps 2-9 take the sums out.  The scales change with every slice, so a
+// over both), warps 4-11 take the sums out.  The scales change with every slice, so a
 // slice is an accumulator of its own: the MMAs alternate over kAcc of them in tensor
 // memory, and the warps add each, times the two scales, to sums in registers.
 // ---------------------------------------------------------------------------
 using vocab::BoundedWait;
 using vocab::kEpiWarps;
-using vocab::kThreads;
+
+// Three groups of four warps, so that registers can be moved between them: the
+// copying and issuing warps give theirs to the sums, 128 registers a thread.
+constexpr int kThreads = 384;
+constexpr int kFirstSum = 4;  // the first warp of the sums
+constexpr int kIssueRegs = 40, kSumRegs = 232;
+static_assert(kIssueRegs * 128 + kSumRegs * 256 <= 168 * kThreads, "registers at launch");
 
 constexpr int kBM = 128;
 constexpr int kBK = 128;          // k slice: 128 e4m3 = one 128-byte swizzle row
 constexpr int kUK = 32;           // k of one MMA
 constexpr int kMaxStages = 8;
-constexpr uint32_t kRingBytes = 216u * 1024u;
+constexpr uint32_t kRingBytes = 192u * 1024u;
+constexpr uint32_t kBoxBytes = 4096;  // a warp's 32 rows x 128 bytes of output
 constexpr uint32_t kARead = kBM * kBK;  // bytes of A an MMA reads, whatever the box holds
 constexpr uint32_t kBarrierBytes = 256;
-constexpr size_t kSmemBytes = 1024 + kRingBytes + kBarrierBytes;
+constexpr size_t kSmemBytes =
+    1024 /* alignment slack */ + kRingBytes + kEpiWarps * kBoxBytes + kBarrierBytes;
 
 template <int kN>
 __host__ __device__ constexpr int accumulators() {
@@ -234,15 +242,81 @@ struct Plan {
   int64_t ldw_scale;
   void* out;
   int64_t ldo;
-  uint32_t out_f32, out_vec;  // type; rows on 16-byte boundaries
+  uint32_t out_f32;
+  int32_t whole_v;  // columns below it go by TMA, in whole 16-byte pieces
+  uint32_t scale_vec;         // both scales' rows on 16-byte boundaries
   uint64_t wait_limit_ns;
   int* error_word;
 };
 
+// How a box of output lies in shared memory: 32 columns of fp32 or 64 of bf16 a row (32
+// where a warp has no more), in the store's swizzle.
+template <int kCols, bool kF32>
+struct Box {
+  static constexpr int kSize = kF32 ? 4 : 2;
+  static constexpr int kWidth = kCols * kSize < 128 ? kCols : 128 / kSize;
+  static constexpr int kPitch = kWidth * kSize;
+  static_assert(kPitch == 128 || kPitch == 64, "rows of the swizzle");
+  // Of 16-byte chunk c of a row.
+  static __device__ __forceinline__ uint32_t at(int row, int c) {
+    return uint32_t(row * kPitch + ((c ^ (kPitch == 128 ? row & 7 : (row >> 1) & 3)) << 4));
+  }
+};
+
+// A warp's 32 rows x kCols sums, rounded once, through its box: a lane has a row, whose
+// pieces stored from registers would be 32 rows' 16 bytes at a time (4 times the store
+// traffic's time; 300 cycles a slice at d = 4096).  TMA stores take them out; columns
+// that it cannot write, behind the last whole 16 bytes or of rows off 16-byte boundaries,
+// go row by row.
+template <int kCols, bool kF32>
+__device__ __forceinline__ void store_sums(const Plan& s, const void* tmap, uint8_t* box, int lane,
+                                           const float (&sum)[kCols], int row0, int col0) {
+  using B = Box<kCols, kF32>;
+#pragma unroll
+  for (int part = 0; part < kCols / B::kWidth; ++part) {
+    const int x = col0 + part * B::kWidth;
+    vocab::box_begin(lane);
+#pragma unroll
+    for (int c = 0; c < B::kPitch / 16; ++c) {
+      const float* v = sum + part * B::kWidth + c * (16 / B::kSize);
+      uint4 w;
+      if constexpr (kF32)
+        w = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
+                       __float_as_uint(v[3]));
+      else
+        w = make_uint4(vocab::pack_bf16(v[0], v[1]), vocab::pack_bf16(v[2], v[3]),
+                       vocab::pack_bf16(v[4], v[5]), vocab::pack_bf16(v[6], v[7]));
+      *reinterpret_cast<uint4*>(box + B::at(lane, c)) = w;
+    }
+    ptx::fence_async_smem();
+    __syncwarp();
+    if (lane == 0 && x < s.whole_v) {
+      ptx::tma_store_2d(tmap, box, x, row0);
+      ptx::bulk_commit();
+    }
+    const int from = max(x, s.whole_v), to = min(x + B::kWidth, s.V);
+    if (from < to) {
+      for (int r = 0; r < 32 && row0 + r < s.M; ++r) {
+        const int64_t out = int64_t(row0 + r) * s.ldo;
+        for (int v = from + lane; v < to; v += 32) {
+          const int byte = (v - x) * B::kSize;
+          const uint8_t* p = box + B::at(r, byte >> 4) + (byte & 15);
+          if constexpr (kF32)
+            static_cast<float*>(s.out)[out + v] = *reinterpret_cast<const float*>(p);
+          else
+            static_cast<uint16_t*>(s.out)[out + v] = *reinterpret_cast<const uint16_t*>(p);
+        }
+      }
+      __syncwarp();
+    }
+  }
+}
+
 template <int kN, bool kPair>
 __global__ void __launch_bounds__(kThreads, 1)
     matmul_kernel(const __grid_constant__ CUtensorMap tmap_a,
-                  const __grid_constant__ CUtensorMap tmap_b, const __grid_constant__ Plan s) {
+                  const __grid_constant__ CUtensorMap tmap_b,
+                  const __grid_constant__ CUtensorMap tmap_o, const __grid_constant__ Plan s) {
   constexpr int kCtas = kPair ? 2 : 1;
   constexpr int kAcc = accumulators<kN>();
   constexpr uint32_t kTmemCols = kAcc * kN;
@@ -253,7 +327,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint64_t* full_bar = reinterpret_cast<uint64_t*>(smem + kRingBytes);
+  uint64_t* full_bar = reinterpret_cast<uint64_t*>(smem + kRingBytes + kEpiWarps * kBoxBytes);
   uint64_t* empty_bar = full_bar + kMaxStages;
   uint64_t* tfull_bar = empty_bar + kMaxStages;
   uint64_t* tempty_bar = tfull_bar + 4;
@@ -283,6 +357,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     ptx::fence_barrier_init();
     ptx::prefetch_tmap(&tmap_a);
     ptx::prefetch_tmap(&tmap_b);
+    ptx::prefetch_tmap(&tmap_o);
   }
   if (warp == 1) {
     if constexpr (kPair) {
@@ -301,6 +376,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem_base = *tmem_holder;
   const BoundedWait waiter{abort_flag, s.wait_limit_ns, s.error_word};
 
+  if (warp < kFirstSum) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
   if (warp == 0) {
     // ---------------- TMA producer ----------------
     const bool issuer = ptx::elect_one();
@@ -425,13 +502,30 @@ __global__ void __launch_bounds__(kThreads, 1)
       waiter.drain(drain_bar, 0);
     }
     __syncwarp();
+    }
   } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSumRegs));
     // ---------------- sums ----------------
     if (s.pdl) ptx::grid_dependency_wait();  // a_scale may still be in flight
     const int quad = warp & 3;  // the tensor-memory lane quadrant this warp may read
-    const int half = (warp - 2) >> 2;
+    const int half = (warp - kFirstSum) >> 2;
+    uint8_t* box = smem + kRingBytes + (warp - kFirstSum) * kBoxBytes;
+    constexpr int kChunks = kCols / 32;
+    const uint32_t taddr0 = tmem_base + (uint32_t(quad * 32) << 16) + uint32_t(half * kCols);
+    const uint32_t tempty0 = ptx::cluster_addr(tempty_bar, 0);
     uint32_t acc = 0, acc_phase = 0;
     bool ok = true;
+    // An accumulator goes back once its last load has completed (the wait for that is
+    // the whole warp's).
+    auto give_back = [&](uint32_t a) {
+      ptx::tc_fence_before();
+      if (lane == 0) {
+        if constexpr (kPair)
+          ptx::mbar_arrive_cluster_relaxed(tempty0 + 8u * a);
+        else
+          ptx::mbar_arrive(&tempty_bar[a]);
+      }
+    };
     for (int u = worker; ok && u < s.n_units; u += n_workers) {
       const int nt = u / s.n_mt, mt = u - nt * s.n_mt;
       const int row0 = (mt * kCtas + rank) * kBM + quad * 32;
@@ -440,80 +534,96 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool busy = row0 < s.M && col0 < s.V;
       const float* sa = s.a_scale + int64_t(min(row, s.M - 1)) * s.lda_scale;
       const float* sw = s.w_scale + int64_t(min(col0, s.V - 1) / kBlock) * s.ldw_scale;
-      uint64_t sum[kCols / 2];
+      // Both scales of four slices.
+      auto scales = [&](int kb, float (&x)[4], float (&y)[4]) {
+        if (s.scale_vec && kb + 4 <= s.n_kb) {
+          const float4 a = *reinterpret_cast<const float4*>(sa + kb);
+          const float4 w = *reinterpret_cast<const float4*>(sw + kb);
+          x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
+          y[0] = w.x, y[1] = w.y, y[2] = w.z, y[3] = w.w;
+        } else {
 #pragma unroll
-      for (int i = 0; i < kCols / 2; ++i) sum[i] = 0ull;
+          for (int i = 0; i < 4; ++i) {
+            x[i] = kb + i < s.n_kb ? sa[kb + i] : 0.0f;
+            y[i] = kb + i < s.n_kb ? sw[kb + i] : 0.0f;
+          }
+        }
+      };
+      float now[4], x[4], y[4];
+      if (busy) scales(0, x, y);
+      float sum[kCols];
+#pragma unroll
+      for (int i = 0; i < kCols; ++i) sum[i] = 0.0f;
+      uint32_t r[2][32];
+      auto add = [&](int c, float scale) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+          sum[c * 32 + i] = fmaf(__uint_as_float(r[c & 1][i]), scale, sum[c * 32 + i]);
+      };
+      if (!waiter.wait_warp(&tfull_bar[acc], acc_phase)) {
+        ok = false;
+        break;
+      }
+      ptx::tc_fence_after();
+      if (busy) {
+        ptx::tmem_ld_32x32b_x32(taddr0 + acc * kN, r[0]);
+        if (kChunks > 1) ptx::tmem_ld_32x32b_x32(taddr0 + acc * kN + 32u, r[1]);
+      }
       for (int kb = 0; kb < s.n_kb; ++kb) {
-        const uint32_t f = __float_as_uint(sa[kb] * sw[kb]);
-        const uint64_t scale = ptx::pack2(f, f);
-        if (!waiter.wait_warp(&tfull_bar[acc], acc_phase)) {
-          ok = false;
-          break;
-        }
-        ptx::tc_fence_after();
-        if (busy) {
-          const uint32_t taddr =
-              tmem_base + (uint32_t(quad * 32) << 16) + acc * kN + uint32_t(half * kCols);
+        // The accumulator of the next slice.
+        const uint32_t next = acc + 1 == kAcc ? 0 : acc + 1;
+        const uint32_t next_phase = acc + 1 == kAcc ? acc_phase ^ 1u : acc_phase;
+        const bool more = kb + 1 < s.n_kb;
+        if (!busy) {
+          give_back(acc);
+          if (more && !waiter.wait_warp(&tfull_bar[next], next_phase)) ok = false;
+          ptx::tc_fence_after();
+        } else {
+          // The scales' products of four slices, the loads of the next four's far ahead.
+          if ((kb & 3) == 0) {
 #pragma unroll
-          for (int c = 0; c < kCols / 32; ++c) {
-            uint32_t r[32];
-            ptx::tmem_ld_32x32b_x32(taddr + uint32_t(c * 32), r);
-            ptx::tmem_wait_ld();
+            for (int i = 0; i < 4; ++i) now[i] = x[i] * y[i];
+            scales(kb + 4, x, y);
+          }
+          const float scale = now[0];
+          now[0] = now[1], now[1] = now[2], now[2] = now[3];
+          // Loads go out as soon as their registers are free, 32 columns at a time, the
+          // next slice's first ones beside the last additions of this one's.
+          const uint32_t taddr = taddr0 + acc * kN, tnext = taddr0 + next * kN;
+          ptx::tmem_wait_ld();
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-              ptx::fma2(sum[c * 16 + i], ptx::pack2(r[2 * i], r[2 * i + 1]), scale);
+          for (int c = 2; c < kChunks; ++c) {
+            add(c - 2, scale);
+            ptx::tmem_ld_32x32b_x32(taddr + uint32_t(c * 32), r[c & 1]);
+          }
+          const bool ready = more && ptx::mbar_test_wait(&tfull_bar[next], next_phase);
+          if (kChunks > 2) ptx::tmem_wait_ld();
+          give_back(acc);
+          if (kChunks > 1) add(kChunks - 2, scale);
+          if (more) {
+            if (!__all_sync(0xFFFFFFFFu, ready) &&
+                !waiter.wait_warp(&tfull_bar[next], next_phase))
+              ok = false;
+            ptx::tc_fence_after();
+          }
+          if (kChunks == 1) add(0, scale);
+          if (ok && more) ptx::tmem_ld_32x32b_x32(tnext, r[0]);
+          if (kChunks > 1) {
+            add(kChunks - 1, scale);
+            if (ok && more) ptx::tmem_ld_32x32b_x32(tnext + 32u, r[1]);
           }
         }
-        ptx::tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          if constexpr (kPair)
-            ptx::mbar_arrive_cluster_relaxed(ptx::cluster_addr(&tempty_bar[acc], 0));
-          else
-            ptx::mbar_arrive(&tempty_bar[acc]);
-        }
-        if (++acc == kAcc) {
-          acc = 0;
-          acc_phase ^= 1u;
-        }
+        acc = next;
+        acc_phase = next_phase;
+        if (!ok) break;
       }
-      if (!ok || !busy || row >= s.M) continue;
-      if (s.out_f32) {
-        float* out = static_cast<float*>(s.out) + int64_t(row) * s.ldo + col0;
-#pragma unroll
-        for (int i = 0; i < kCols / 4; ++i) {
-          uint32_t v[4];
-          ptx::unpack2(sum[2 * i], v[0], v[1]);
-          ptx::unpack2(sum[2 * i + 1], v[2], v[3]);
-          if (s.out_vec && col0 + 4 * i + 4 <= s.V) {
-            *reinterpret_cast<uint4*>(out + 4 * i) = make_uint4(v[0], v[1], v[2], v[3]);
-          } else {
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              if (col0 + 4 * i + j < s.V) out[4 * i + j] = __uint_as_float(v[j]);
-          }
-        }
-      } else {
-        uint16_t* out = static_cast<uint16_t*>(s.out) + int64_t(row) * s.ldo + col0;
-#pragma unroll
-        for (int i = 0; i < kCols / 8; ++i) {
-          uint32_t v[4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            uint32_t lo, hi;
-            ptx::unpack2(sum[4 * i + j], lo, hi);
-            v[j] = vocab::pack_bf16(__uint_as_float(lo), __uint_as_float(hi));
-          }
-          if (s.out_vec && col0 + 8 * i + 8 <= s.V) {
-            *reinterpret_cast<uint4*>(out + 8 * i) = make_uint4(v[0], v[1], v[2], v[3]);
-          } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-              if (col0 + 8 * i + j < s.V) out[8 * i + j] = uint16_t(v[j / 2] >> (16 * (j & 1)));
-          }
-        }
-      }
+      if (!ok || !busy) continue;
+      if (s.out_f32)
+        store_sums<kCols, true>(s, &tmap_o, box, lane, sum, row0, col0);
+      else
+        store_sums<kCols, false>(s, &tmap_o, box, lane, sum, row0, col0);
     }
+    if (lane == 0) ptx::bulk_wait();
   }
 
   ptx::tc_fence_before();
@@ -621,16 +731,17 @@ fs_status device_setup(const Device** out) {
   return d.status;
 }
 
-// 2-D tensor map of bytes with 128-byte-swizzled boxes of 128 x rows; elements past
-// the extents read as zero.
-bool encode(const Device& dev, CUtensorMap* m, const void* base, int64_t inner, int64_t outer,
-            int64_t ld, int box_rows) {
+// 2-D tensor map with boxes of `width` x `rows` elements, swizzled over their rows of 64
+// or 128 bytes; elements past the extents read as zero and are not written.
+bool encode(const Device& dev, CUtensorMap* m, CUtensorMapDataType type, int size,
+            const void* base, int64_t inner, int64_t outer, int64_t ld, int width, int rows) {
   const cuuint64_t dims[2] = {cuuint64_t(inner), cuuint64_t(outer)};
-  const cuuint64_t strides[1] = {cuuint64_t(ld)};
-  const cuuint32_t box[2] = {cuuint32_t(kBK), cuuint32_t(box_rows)};
+  const cuuint64_t strides[1] = {cuuint64_t(ld) * unsigned(size)};
+  const cuuint32_t box[2] = {cuuint32_t(width), cuuint32_t(rows)};
   const cuuint32_t estr[2] = {1, 1};
-  return dev.encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides,
-                    box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+  return dev.encode(m, type, 2, const_cast<void*>(base), dims, strides, box, estr,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE,
+                    width * size == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -652,13 +763,22 @@ fs_status launch(const Device& dev, const fs_matmul_fp8_args& a, Plan s, cudaStr
   s.a_bytes = uint32_t(box_rows) * kBK;
   s.stage_bytes = s.a_bytes + (kPair ? kN / 2 : kN) * kBK;
   s.n_stages = ring_stages<kN, kPair>(s.a_bytes);
-  CUtensorMap ta, tb;
+  CUtensorMap ta, tb, to;
   // Of a single row the stride is any that the map takes.
   const int64_t lda = a.M > 1 ? a.lda : ceil_div(a.d, 16) * 16;
   const int64_t ldw = a.V > 1 ? a.ldw : ceil_div(a.d, 16) * 16;
-  if (!encode(dev, &ta, a.A, a.d, a.M, lda, box_rows) ||
-      !encode(dev, &tb, a.W, a.d, a.V, ldw, kPair ? kN / 2 : kN))
+  const auto bytes = CU_TENSOR_MAP_DATA_TYPE_UINT8;
+  if (!encode(dev, &ta, bytes, 1, a.A, a.d, a.M, lda, kBK, box_rows) ||
+      !encode(dev, &tb, bytes, 1, a.W, a.d, a.V, ldw, kBK, kPair ? kN / 2 : kN))
     return FS_ERR_CUDA;
+  to = tb;  // where nothing goes by it
+  if (s.whole_v > 0) {
+    const int64_t ldo = a.M > 1 ? a.ldo : ceil_div(a.V, 8) * 8;
+    const auto type = s.out_f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    const int width = s.out_f32 ? Box<kN / 2, true>::kWidth : Box<kN / 2, false>::kWidth;
+    if (!encode(dev, &to, type, s.out_f32 ? 4 : 2, a.out, s.whole_v, a.M, ldo, width, 32))
+      return FS_ERR_CUDA;
+  }
   cudaLaunchAttribute attr[2];
   unsigned n = 0;
   if (kPair) {
@@ -679,7 +799,7 @@ fs_status launch(const Device& dev, const fs_matmul_fp8_args& a, Plan s, cudaStr
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = n;
-  if (cudaLaunchKernelEx(&cfg, matmul_kernel<kN, kPair>, ta, tb, s) != cudaSuccess) {
+  if (cudaLaunchKernelEx(&cfg, matmul_kernel<kN, kPair>, ta, tb, to, s) != cudaSuccess) {
     cudaGetLastError();
     return FS_ERR_CUDA;
   }
@@ -777,7 +897,10 @@ extern "C" fs_status fs_matmul_fp8(const fs_matmul_fp8_args* args, void* stream_
   s.out = a.out;
   s.ldo = a.M > 1 ? a.ldo : 0;
   s.out_f32 = a.out_dtype == FS_F32;
-  s.out_vec = aligned(a.out, 16) && s.ldo * element(a.out_dtype) % 16 == 0;
+  const int64_t piece = 16 / element(a.out_dtype);
+  if (aligned(a.out, 16) && s.ldo % piece == 0) s.whole_v = int32_t(a.V / piece * piece);
+  s.scale_vec = aligned(a.a_scale, 16) && aligned(a.w_scale, 16) &&
+                (a.M == 1 || a.lda_scale % 4 == 0) && (a.V <= kBlock || a.ldw_scale % 4 == 0);
   s.wait_limit_ns = kWaitLimitNs;
   s.error_word = dev->error_word;
   cudaStream_t stream = static_cast<cudaStream_t>(stream_ptr);
