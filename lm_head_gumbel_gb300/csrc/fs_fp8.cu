@@ -8,6 +8,7 @@
 #include <climits>
 #include <cstdint>
 #include <mutex>
+#include <type_traits>
 
 #include "fs_contract.cuh"
 #include "fs_ptx.cuh"
@@ -41,17 +42,37 @@ __device__ __forceinline__ void mma_f8_pair(uint32_t d_tmem, uint64_t a_desc, ui
 __host__ __device__ constexpr uint32_t idesc_e4m3_f32(uint32_t M, uint32_t N) {
   return (1u << 4) | ((N >> 3) << 17) | ((M >> 4) << 24);
 }
-// Whether the phase with parity `parity` has completed; does not wait.
-__device__ __forceinline__ bool mbar_test_wait(uint64_t* bar, uint32_t parity) {
+// d += a * b on two fp32 values at once (a register pair each).
+__device__ __forceinline__ void fma2(uint64_t& d, uint64_t a, uint64_t b) {
+  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(d) : "l"(a), "l"(b));
+}
+__device__ __forceinline__ uint64_t pack2(uint32_t lo, uint32_t hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
+  return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+// Barriers and values in shared memory by 32-bit addresses.
+__device__ __forceinline__ bool mbar_try_wait_at(uint32_t bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
-      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
       "selp.u32 %0, 1, 0, p;\n\t}"
       : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity)
+      : "r"(bar), "r"(parity)
       : "memory");
   return ok != 0;
+}
+__device__ __forceinline__ void mbar_arrive_at(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ float ld_shared_f32(uint32_t at) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
+  return v;
 }
 // Two values in e4m3, to nearest even, past 448 to 448; lo in the low byte.
 __device__ __forceinline__ uint32_t cvt_e4m3x2(float lo, float hi) {
@@ -203,23 +224,38 @@ using vocab::kEpiWarps;
 // copying and issuing warps give theirs to the sums, 128 registers a thread.
 constexpr int kThreads = 384;
 constexpr int kFirstSum = 4;  // the first warp of the sums
-constexpr int kIssueRegs = 40, kSumRegs = 232;
+constexpr int kIssueRegs = 56, kSumRegs = 224;
 static_assert(kIssueRegs * 128 + kSumRegs * 256 <= 168 * kThreads, "registers at launch");
 
 constexpr int kBM = 128;
 constexpr int kBK = 128;          // k slice: 128 e4m3 = one 128-byte swizzle row
 constexpr int kUK = 32;           // k of one MMA
 constexpr int kMaxStages = 8;
-constexpr uint32_t kRingBytes = 192u * 1024u;
+constexpr uint32_t kRingBytes = 176u * 1024u;
 constexpr uint32_t kBoxBytes = 4096;  // a warp's 32 rows x 128 bytes of output
 constexpr uint32_t kARead = kBM * kBK;  // bytes of A an MMA reads, whatever the box holds
 constexpr uint32_t kBarrierBytes = 256;
-constexpr size_t kSmemBytes =
-    1024 /* alignment slack */ + kRingBytes + kEpiWarps * kBoxBytes + kBarrierBytes;
+// The scales of some slices: of A's 128 rows, times W's of either half's columns.
+constexpr int kGroups = 2;
+constexpr int kGroupSlices = 8;
+struct ScaleGroup {
+  float product[2][kGroupSlices][kBM];
+};
+constexpr uint32_t kBoxesAt = kRingBytes;
+constexpr uint32_t kScalesAt = kBoxesAt + kEpiWarps * kBoxBytes;
+constexpr uint32_t kBarriersAt = kScalesAt + kGroups * uint32_t(sizeof(ScaleGroup));
+constexpr size_t kSmemBytes = 1024 /* alignment slack */ + kBarriersAt + kBarrierBytes;
+static_assert(kSmemBytes <= 227 * 1024 && kScalesAt % 16 == 0 && kBarriersAt % 8 == 0, "layout");
 
 template <int kN>
 __host__ __device__ constexpr int accumulators() {
   return kN == 256 ? 2 : 4;
+}
+// Parts of an accumulator, side by side, with barriers of their own: the second part's
+// MMAs run while the first one's sums are taken out, by the warps of one group each.
+template <int kN>
+__host__ __device__ constexpr int parts() {
+  return kN == 256 ? 2 : 1;
 }
 // Ring stages for a box of `a_bytes` of A: the last stage's MMAs read kARead of A too.
 template <int kN, bool kPair>
@@ -312,6 +348,17 @@ __device__ __forceinline__ void store_sums(const Plan& s, const void* tmap, uint
   }
 }
 
+// The rest of a wait whose first try failed, with BoundedWait's limit and abort flag.
+__device__ __forceinline__ void wait_on(const BoundedWait& w, uint32_t bar, uint32_t parity) {
+  const uint64_t t0 = ptx::global_timer_ns();
+  while (!ptx::mbar_try_wait_at(bar, parity) && !*w.abort_flag) {
+    if (ptx::global_timer_ns() - t0 > w.limit_ns) {
+      *w.abort_flag = 1u;
+      atomicOr(w.error_word, vocab::kErrWaitTimeout);
+    }
+  }
+}
+
 template <int kN, bool kPair>
 __global__ void __launch_bounds__(kThreads, 1)
     matmul_kernel(const __grid_constant__ CUtensorMap tmap_a,
@@ -322,21 +369,29 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr uint32_t kTmemCols = kAcc * kN;
   constexpr int kBRows = kN / kCtas;
   constexpr uint32_t kBBytes = kBRows * kBK;
-  constexpr int kCols = kN / 2;  // columns of an epilogue warp
-  constexpr uint32_t kIdesc = ptx::idesc_e4m3_f32(kBM * kCtas, kN);
+  constexpr int kCols = kN / 2;  // columns of a summing warp
+  constexpr int kParts = parts<kN>();
+  constexpr int kPartRows = kBRows / kParts;  // of B in this CTA's shared memory
+  constexpr uint32_t kIdesc = ptx::idesc_e4m3_f32(kBM * kCtas, kN / kParts);
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint64_t* full_bar = reinterpret_cast<uint64_t*>(smem + kRingBytes + kEpiWarps * kBoxBytes);
+  uint64_t* full_bar = reinterpret_cast<uint64_t*>(smem + kBarriersAt);
   uint64_t* empty_bar = full_bar + kMaxStages;
   uint64_t* tfull_bar = empty_bar + kMaxStages;
-  uint64_t* tempty_bar = tfull_bar + 4;
-  uint64_t* drain_bar = tempty_bar + 4;
+  uint64_t* tempty_bar = tfull_bar + 4;  // of accumulator a, part h: [a * kParts + h]
+  uint64_t* sfull_bar = tempty_bar + 4;
+  uint64_t* sempty_bar = sfull_bar + kGroups;
+  uint64_t* drain_bar = sempty_bar + kGroups;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drain_bar + 1);
   volatile uint32_t* abort_flag = tmem_holder + 1;
-  static_assert((2 * kMaxStages + 9) * 8 + 8 <= kBarrierBytes, "barriers, tensor-memory address, flag");
+  static_assert((2 * kMaxStages + 9 + 2 * kGroups) * 8 + 8 <= kBarrierBytes,
+                "barriers, tensor-memory address, flag");
+  ScaleGroup* groups = reinterpret_cast<ScaleGroup*>(smem + kScalesAt);
 
-  const int warp = threadIdx.x >> 5;
+  // The same in all lanes, which the compiler cannot see: addresses that depend on it then
+  // stay in uniform registers, as tensor-memory loads take them.
+  const int warp = __shfl_sync(0xFFFFFFFFu, int(threadIdx.x >> 5), 0);
   const int lane = threadIdx.x & 31;
   const int rank = kPair ? int(ptx::cluster_ctarank()) : 0;
   const bool leader = rank == 0;
@@ -348,9 +403,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       ptx::mbar_init(&full_bar[i], 1);
       ptx::mbar_init(&empty_bar[i], 1);
     }
-    for (int a = 0; a < kAcc; ++a) {
+    for (int a = 0; a < kAcc * kParts; ++a) {
       ptx::mbar_init(&tfull_bar[a], 1);
-      ptx::mbar_init(&tempty_bar[a], kCtas * kEpiWarps);
+      ptx::mbar_init(&tempty_bar[a], kCtas * kEpiWarps / kParts);
+    }
+    for (int g = 0; g < kGroups; ++g) {
+      ptx::mbar_init(&sfull_bar[g], 1);
+      ptx::mbar_init(&sempty_bar[g], kEpiWarps);
     }
     ptx::mbar_init(drain_bar, 1);
     *abort_flag = 0u;
@@ -416,8 +475,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (issuer) {
           if (leader)
             ptx::mbar_arrive_expect_tx(&full_bar[stage], kCtas * (s.a_bytes + kBBytes));
-          load(smem + size_t(stage) * s.stage_bytes + s.a_bytes, &tmap_b, stage, kb * kBK,
-               nt * kN + rank * kBRows, pol_b);
+          // A part's columns of a pair's tile lie half in each CTA.
+#pragma unroll
+          for (int h = 0; h < kParts; ++h)
+            load(smem + size_t(stage) * s.stage_bytes + s.a_bytes + h * kPartRows * kBK, &tmap_b,
+                 stage, kb * kBK, nt * kN + h * (kN / kParts) + rank * kPartRows, pol_b);
           if (!deferring) load_a(stage, kb, mt);
         }
         if (deferring) {  // the first fill: stage n_held
@@ -459,28 +521,36 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       for (int u = worker; ok && u < s.n_units; u += n_workers) {
         for (int kb = 0; kb < s.n_kb; ++kb) {
-          if (!waiter.wait_warp(&tempty_bar[acc], acc_phase ^ 1u) ||
-              !waiter.wait_warp(&full_bar[stage], phase)) {
+          if (!waiter.wait_warp(&full_bar[stage], phase)) {
             ok = false;
             break;
           }
-          ptx::tc_fence_after();
-          if (issuer) {
-            const uint32_t d_tmem = tmem_base + acc * kN;
-            const uint64_t off = uint64_t((stage * s.stage_bytes) >> 4);
+          const uint64_t off = uint64_t((stage * s.stage_bytes) >> 4);
 #pragma unroll
-            for (int k = 0; k < kBK / kUK; ++k) {
-              const uint64_t da = desc_a0 + off + uint64_t(kUK >> 4) * k;
-              const uint64_t db = desc_b0 + off + uint64_t(kUK >> 4) * k;
-              if constexpr (kPair)
-                ptx::mma_f8_pair(d_tmem, da, db, kIdesc, k != 0 ? 1u : 0u);
-              else
-                ptx::mma_f8(d_tmem, da, db, kIdesc, k != 0 ? 1u : 0u);
+          for (int h = 0; h < kParts; ++h) {
+            if (!waiter.wait_warp(&tempty_bar[acc * kParts + h], acc_phase ^ 1u)) {
+              ok = false;
+              break;
             }
-            commit(&empty_bar[stage]);
-            commit(&tfull_bar[acc]);
+            ptx::tc_fence_after();
+            if (issuer) {
+              const uint32_t d_tmem = tmem_base + acc * kN + h * (kN / kParts);
+#pragma unroll
+              for (int k = 0; k < kBK / kUK; ++k) {
+                const uint64_t da = desc_a0 + off + uint64_t(kUK >> 4) * k;
+                const uint64_t db =
+                    desc_b0 + off + uint64_t(h * ((kPartRows * kBK) >> 4) + (kUK >> 4) * k);
+                if constexpr (kPair)
+                  ptx::mma_f8_pair(d_tmem, da, db, kIdesc, k != 0 ? 1u : 0u);
+                else
+                  ptx::mma_f8(d_tmem, da, db, kIdesc, k != 0 ? 1u : 0u);
+              }
+              if (h == kParts - 1) commit(&empty_bar[stage]);
+              commit(&tfull_bar[acc * kParts + h]);
+            }
+            __syncwarp();
           }
-          __syncwarp();
+          if (!ok) break;
           if (++stage == s.n_stages) {
             stage = 0;
             phase ^= 1u;
@@ -502,122 +572,179 @@ __global__ void __launch_bounds__(kThreads, 1)
       waiter.drain(drain_bar, 0);
     }
     __syncwarp();
+    } else if (warp == 2) {
+      // ---------------- scales ----------------
+      // From memory by a warp of its own: a wait for tensor-memory loads waits for a
+      // warp's loads from memory too (450 cycles every four slices).
+      if (s.pdl) ptx::grid_dependency_wait();
+      uint32_t g = 0, phase = 0;
+      bool ok = true;
+      for (int u = worker; ok && u < s.n_units; u += n_workers) {
+        const int nt = u / s.n_mt, mt = u - nt * s.n_mt;
+        const int row0 = (mt * kCtas + rank) * kBM;
+        for (int kb0 = 0; kb0 < s.n_kb; kb0 += kGroupSlices) {
+          if (!waiter.wait_warp(&sempty_bar[g], phase ^ 1u)) {
+            ok = false;
+            break;
+          }
+          const int end = min(s.n_kb, kb0 + kGroupSlices);
+          for (int kb = kb0; kb < end; kb += 4) {
+            const int n = min(4, end - kb);
+            float v[4][4], w[2][4];
+            auto four = [&](const float* p, float (&x)[4]) {
+              if (s.scale_vec && n == 4) {
+                const float4 f = *reinterpret_cast<const float4*>(p);
+                x[0] = f.x, x[1] = f.y, x[2] = f.z, x[3] = f.w;
+              } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) x[i] = i < n ? p[i] : 0.0f;
+              }
+            };
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              four(s.a_scale + int64_t(min(row0 + 32 * j + lane, s.M - 1)) * s.lda_scale + kb,
+                   v[j]);
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              four(s.w_scale + int64_t(min(nt * kN + h * kCols, s.V - 1) / kBlock) * s.ldw_scale + kb,
+                   w[h]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                groups[g].product[0][kb - kb0 + i][32 * j + lane] = v[j][i] * w[0][i];
+                groups[g].product[1][kb - kb0 + i][32 * j + lane] = v[j][i] * w[1][i];
+              }
+            }
+          }
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(&sfull_bar[g]);
+          if (++g == kGroups) {
+            g = 0;
+            phase ^= 1u;
+          }
+        }
+      }
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSumRegs));
     // ---------------- sums ----------------
-    if (s.pdl) ptx::grid_dependency_wait();  // a_scale may still be in flight
+    if (s.pdl) ptx::grid_dependency_wait();  // before the first output
     const int quad = warp & 3;  // the tensor-memory lane quadrant this warp may read
     const int half = (warp - kFirstSum) >> 2;
-    uint8_t* box = smem + kRingBytes + (warp - kFirstSum) * kBoxBytes;
     constexpr int kChunks = kCols / 32;
     const uint32_t taddr0 = tmem_base + (uint32_t(quad * 32) << 16) + uint32_t(half * kCols);
-    const uint32_t tempty0 = ptx::cluster_addr(tempty_bar, 0);
-    uint32_t acc = 0, acc_phase = 0;
-    bool ok = true;
+    const int part = kParts == 2 ? half : 0;
+    const uint32_t tfull0 = ptx::smem_u32(tfull_bar + part);
+    const uint32_t tempty0 = ptx::cluster_addr(tempty_bar + part, 0);
+    const uint32_t sfull0 = ptx::smem_u32(sfull_bar), sempty0 = ptx::smem_u32(sempty_bar);
+    const uint32_t scales0 = ptx::smem_u32(&groups[0].product[half][0][quad * 32 + lane]);
+    uint32_t acc = 0, acc_phase = 0, group = 0, group_phase = 0;
+    // Past its limit a wait raises the abort flag and returns, and so does every later one
+    // at once: the loops end, with the error reported and sums of no use.
+    auto wait = [&](uint32_t bar, uint32_t parity) {
+      if (!ptx::mbar_try_wait_at(bar, parity)) wait_on(waiter, bar, parity);
+      __syncwarp();
+    };
     // An accumulator goes back once its last load has completed (the wait for that is
-    // the whole warp's).
-    auto give_back = [&](uint32_t a) {
-      ptx::tc_fence_before();
-      if (lane == 0) {
-        if constexpr (kPair)
-          ptx::mbar_arrive_cluster_relaxed(tempty0 + 8u * a);
-        else
-          ptx::mbar_arrive(&tempty_bar[a]);
+    // the whole warp's), a group of scales with its last one.
+    auto arrive = [&](uint32_t bar) {
+      if (lane == 0) ptx::mbar_arrive_cluster_relaxed(bar);
+    };
+    auto next_group = [&]() {
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive_at(sempty0 + 8u * group);
+      if (++group == kGroups) {
+        group = 0;
+        group_phase ^= 1u;
       }
     };
-    for (int u = worker; ok && u < s.n_units; u += n_workers) {
+    for (int u = worker; u < s.n_units; u += n_workers) {
       const int nt = u / s.n_mt, mt = u - nt * s.n_mt;
       const int row0 = (mt * kCtas + rank) * kBM + quad * 32;
-      const int row = row0 + lane;
       const int col0 = nt * kN + half * kCols;
-      const bool busy = row0 < s.M && col0 < s.V;
-      const float* sa = s.a_scale + int64_t(min(row, s.M - 1)) * s.lda_scale;
-      const float* sw = s.w_scale + int64_t(min(col0, s.V - 1) / kBlock) * s.ldw_scale;
-      // Both scales of four slices.
-      auto scales = [&](int kb, float (&x)[4], float (&y)[4]) {
-        if (s.scale_vec && kb + 4 <= s.n_kb) {
-          const float4 a = *reinterpret_cast<const float4*>(sa + kb);
-          const float4 w = *reinterpret_cast<const float4*>(sw + kb);
-          x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
-          y[0] = w.x, y[1] = w.y, y[2] = w.z, y[3] = w.w;
-        } else {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            x[i] = kb + i < s.n_kb ? sa[kb + i] : 0.0f;
-            y[i] = kb + i < s.n_kb ? sw[kb + i] : 0.0f;
+      if (row0 >= s.M || col0 >= s.V) {  // nothing here
+        for (int kb = 0; kb < s.n_kb; ++kb) {
+          wait(tfull0 + 8u * kParts * acc, acc_phase);
+          ptx::tc_fence_before();
+          arrive(tempty0 + 8u * kParts * acc);
+          if (++acc == kAcc) {
+            acc = 0;
+            acc_phase ^= 1u;
+          }
+          if (kb % kGroupSlices == kGroupSlices - 1 || kb + 1 == s.n_kb) {
+            wait(sfull0 + 8u * group, group_phase);
+            next_group();
           }
         }
-      };
-      float now[4], x[4], y[4];
-      if (busy) scales(0, x, y);
-      float sum[kCols];
+        continue;
+      }
+      uint64_t sums[kCols / 2];
 #pragma unroll
-      for (int i = 0; i < kCols; ++i) sum[i] = 0.0f;
+      for (int i = 0; i < kCols / 2; ++i) sums[i] = 0ull;
       uint32_t r[2][32];
       auto add = [&](int c, float scale) {
+        const uint64_t f = ptx::pack2(__float_as_uint(scale), __float_as_uint(scale));
 #pragma unroll
-        for (int i = 0; i < 32; ++i)
-          sum[c * 32 + i] = fmaf(__uint_as_float(r[c & 1][i]), scale, sum[c * 32 + i]);
+        for (int i = 0; i < 16; ++i)
+          ptx::fma2(sums[c * 16 + i], ptx::pack2(r[c & 1][2 * i], r[c & 1][2 * i + 1]), f);
       };
-      if (!waiter.wait_warp(&tfull_bar[acc], acc_phase)) {
-        ok = false;
-        break;
-      }
+      wait(sfull0 + 8u * group, group_phase);
+      uint32_t scale_at = scales0 + group * uint32_t(sizeof(ScaleGroup));
+      float scale = ptx::ld_shared_f32(scale_at);
+      uint32_t taddr = taddr0 + acc * kN;
+      wait(tfull0 + 8u * kParts * acc, acc_phase);
       ptx::tc_fence_after();
-      if (busy) {
-        ptx::tmem_ld_32x32b_x32(taddr0 + acc * kN, r[0]);
-        if (kChunks > 1) ptx::tmem_ld_32x32b_x32(taddr0 + acc * kN + 32u, r[1]);
-      }
-      for (int kb = 0; kb < s.n_kb; ++kb) {
-        // The accumulator of the next slice.
-        const uint32_t next = acc + 1 == kAcc ? 0 : acc + 1;
-        const uint32_t next_phase = acc + 1 == kAcc ? acc_phase ^ 1u : acc_phase;
-        const bool more = kb + 1 < s.n_kb;
-        if (!busy) {
-          give_back(acc);
-          if (more && !waiter.wait_warp(&tfull_bar[next], next_phase)) ok = false;
-          ptx::tc_fence_after();
-        } else {
-          // The scales' products of four slices, the loads of the next four's far ahead.
-          if ((kb & 3) == 0) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) now[i] = x[i] * y[i];
-            scales(kb + 4, x, y);
+      ptx::tmem_ld_32x32b_x32(taddr, r[0]);
+      if (kChunks > 1) ptx::tmem_ld_32x32b_x32(taddr + 32u, r[1]);
+      // A slice; `more`: another one of the unit follows.  Loads go out as soon as their
+      // registers are free, 32 columns at a time, the next slice's first ones beside the
+      // last additions of this one's.
+      auto slice = [&](int kb, auto more) {
+        float scale_next = 0.0f;
+        if constexpr (decltype(more)::value) {
+          scale_at += kBM * 4;
+          if (kb % kGroupSlices == kGroupSlices - 1) {
+            next_group();
+            wait(sfull0 + 8u * group, group_phase);
+            scale_at = scales0 + group * uint32_t(sizeof(ScaleGroup));
           }
-          const float scale = now[0];
-          now[0] = now[1], now[1] = now[2], now[2] = now[3];
-          // Loads go out as soon as their registers are free, 32 columns at a time, the
-          // next slice's first ones beside the last additions of this one's.
-          const uint32_t taddr = taddr0 + acc * kN, tnext = taddr0 + next * kN;
-          ptx::tmem_wait_ld();
-#pragma unroll
-          for (int c = 2; c < kChunks; ++c) {
-            add(c - 2, scale);
-            ptx::tmem_ld_32x32b_x32(taddr + uint32_t(c * 32), r[c & 1]);
-          }
-          const bool ready = more && ptx::mbar_test_wait(&tfull_bar[next], next_phase);
-          if (kChunks > 2) ptx::tmem_wait_ld();
-          give_back(acc);
-          if (kChunks > 1) add(kChunks - 2, scale);
-          if (more) {
-            if (!__all_sync(0xFFFFFFFFu, ready) &&
-                !waiter.wait_warp(&tfull_bar[next], next_phase))
-              ok = false;
-            ptx::tc_fence_after();
-          }
-          if (kChunks == 1) add(0, scale);
-          if (ok && more) ptx::tmem_ld_32x32b_x32(tnext, r[0]);
-          if (kChunks > 1) {
-            add(kChunks - 1, scale);
-            if (ok && more) ptx::tmem_ld_32x32b_x32(tnext + 32u, r[1]);
-          }
+          scale_next = ptx::ld_shared_f32(scale_at);
         }
-        acc = next;
-        acc_phase = next_phase;
-        if (!ok) break;
-      }
-      if (!ok || !busy) continue;
+        ptx::tmem_wait_ld();
+#pragma unroll
+        for (int c = 2; c < kChunks; ++c) {
+          add(c - 2, scale);
+          ptx::tmem_ld_32x32b_x32(taddr + uint32_t(c * 32), r[c & 1]);
+        }
+        if (kChunks > 2) ptx::tmem_wait_ld();
+        ptx::tc_fence_before();
+        arrive(tempty0 + 8u * kParts * acc);
+        if (++acc == kAcc) {
+          acc = 0;
+          acc_phase ^= 1u;
+        }
+        taddr = taddr0 + acc * kN;
+        if (kChunks > 1) add(kChunks - 2, scale);
+        if constexpr (decltype(more)::value) {
+          wait(tfull0 + 8u * kParts * acc, acc_phase);
+          ptx::tc_fence_after();
+        }
+        if (kChunks == 1) add(0, scale);
+        if constexpr (decltype(more)::value) ptx::tmem_ld_32x32b_x32(taddr, r[0]);
+        if (kChunks > 1) {
+          add(kChunks - 1, scale);
+          if constexpr (decltype(more)::value) ptx::tmem_ld_32x32b_x32(taddr + 32u, r[1]);
+        }
+        scale = scale_next;
+      };
+      for (int kb = 0; kb + 1 < s.n_kb; ++kb) slice(kb, std::true_type());
+      slice(s.n_kb - 1, std::false_type());
+      next_group();
+      float sum[kCols];
+#pragma unroll
+      for (int i = 0; i < kCols / 2; ++i) ptx::unpack2(sums[i], sum[2 * i], sum[2 * i + 1]);
+      uint8_t* box = smem + kBoxesAt + (warp - kFirstSum) * kBoxBytes;
       if (s.out_f32)
         store_sums<kCols, true>(s, &tmap_o, box, lane, sum, row0, col0);
       else
@@ -769,7 +896,8 @@ fs_status launch(const Device& dev, const fs_matmul_fp8_args& a, Plan s, cudaStr
   const int64_t ldw = a.V > 1 ? a.ldw : ceil_div(a.d, 16) * 16;
   const auto bytes = CU_TENSOR_MAP_DATA_TYPE_UINT8;
   if (!encode(dev, &ta, bytes, 1, a.A, a.d, a.M, lda, kBK, box_rows) ||
-      !encode(dev, &tb, bytes, 1, a.W, a.d, a.V, ldw, kBK, kPair ? kN / 2 : kN))
+      !encode(dev, &tb, bytes, 1, a.W, a.d, a.V, ldw, kBK,
+              (kPair ? kN / 2 : kN) / parts<kN>()))
     return FS_ERR_CUDA;
   to = tb;  // where nothing goes by it
   if (s.whole_v > 0) {
