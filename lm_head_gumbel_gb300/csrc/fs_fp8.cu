@@ -88,50 +88,75 @@ namespace {
 
 constexpr int kBlock = FS_FP8_BLOCK;
 constexpr float kMostE4m3 = 448.0f;
-constexpr float kLeastMax = 0x1p-100f;
 
 // ---------------------------------------------------------------------------
 // Quantisation
 // ---------------------------------------------------------------------------
-__device__ __forceinline__ float value_of(__nv_bfloat16 x) { return __bfloat162float(x); }
-__device__ __forceinline__ float value_of(float x) { return x; }
+// Bound: memory.  A head of 151936 x 4096 in bf16 (1.87 GB read and written) takes HEAD_US us,
+// PROMPT_RATE; kept as bits until they are scaled, so that a thread's loads are all in flight and
+// the largest magnitude is an unsigned maximum (a NaN's bits are above every number's).
+constexpr uint32_t kLeastMaxBits = 0x0D800000u;  // 2^-100
 
-// A thread's 8 elements from x, of which n exist; 0 for the others.
+// 8 elements as they lie in memory.
+template <class T>
+struct Eight {
+  uint32_t w[2 * sizeof(T)];
+};
+// Those from x, of which n exist, the others 0, are read in two steps, so that the first
+// of several pieces can be in flight at once: whole ones (of rows on 16-byte boundaries;
+// past a row's end lies the next row, so `last` rows are left out), then what is left.
 template <class T, bool kVec>
-__device__ __forceinline__ void load8(const T* x, int n, float (&v)[8]) {
-  if (kVec && n >= 8) {
-    if constexpr (sizeof(T) == 2) {
-      const uint4 w = __ldcs(reinterpret_cast<const uint4*>(x));
-      const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+__device__ __forceinline__ bool load_whole(Eight<T>& e, const T* x, int n, bool last) {
+  const bool can = kVec && (last ? n >= 8 : n > 0);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        v[2 * i] = __uint_as_float(u[i] << 16);
-        v[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
-      }
-    } else {
-      const float4 a = __ldcs(reinterpret_cast<const float4*>(x));
-      const float4 b = __ldcs(reinterpret_cast<const float4*>(x) + 1);
-      v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
-      v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-    }
-    return;
+  for (int i = 0; i < int(sizeof(T)) / 2; ++i) {
+    uint4 v = make_uint4(0u, 0u, 0u, 0u);
+    if (can) v = __ldcs(reinterpret_cast<const uint4*>(x) + i);
+    e.w[4 * i] = v.x, e.w[4 * i + 1] = v.y, e.w[4 * i + 2] = v.z, e.w[4 * i + 3] = v.w;
   }
-#pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = i < n ? value_of(x[i]) : 0.0f;
+  return can;
 }
-
-__device__ __forceinline__ float max_abs(const float (&v)[8]) {
-  float m = fabsf(v[0]);
+template <class T>
+__device__ __forceinline__ void load_rest(Eight<T>& e, const T* x, int n, bool whole) {
+  if (n <= 0 || (whole && n >= 8)) return;
+  if constexpr (sizeof(T) == 2) {
+    const uint16_t* p = reinterpret_cast<const uint16_t*>(x);
 #pragma unroll
-  for (int i = 1; i < 8; ++i) m = ptx::max_nan(m, fabsf(v[i]));
+    for (int i = 0; i < 4; ++i)
+      e.w[i] = (2 * i < n ? p[2 * i] : 0u) | (2 * i + 1 < n ? uint32_t(p[2 * i + 1]) << 16 : 0u);
+  } else {
+    const uint32_t* p = reinterpret_cast<const uint32_t*>(x);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) e.w[i] = i < n ? p[i] : 0u;
+  }
+}
+// The bits of the largest magnitude, as fp32.
+__device__ __forceinline__ uint32_t most(const Eight<__nv_bfloat16>& e) {
+  uint32_t m = 0u;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    asm("max.u16x2 %0, %1, %2;" : "=r"(m) : "r"(m), "r"(e.w[i] & 0x7FFF7FFFu));
+  return max(m & 0xFFFF0000u, m << 16);
+}
+__device__ __forceinline__ uint32_t most(const Eight<float>& e) {
+  uint32_t m = 0u;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = max(m, e.w[i] & 0x7FFFFFFFu);
   return m;
 }
+__device__ __forceinline__ float element_of(const Eight<__nv_bfloat16>& e, int i) {
+  return __uint_as_float((i & 1) ? e.w[i / 2] & 0xFFFF0000u : e.w[i / 2] << 16);
+}
+__device__ __forceinline__ float element_of(const Eight<float>& e, int i) {
+  return __uint_as_float(e.w[i]);
+}
 
-template <bool kVec>
-__device__ __forceinline__ void store8(uint8_t* out, int n, const float (&v)[8], float inv) {
+template <bool kVec, class E>
+__device__ __forceinline__ void store8(uint8_t* out, int n, const E& e, float inv) {
   uint32_t h[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) h[i] = ptx::cvt_e4m3x2(v[2 * i] * inv, v[2 * i + 1] * inv);
+  for (int i = 0; i < 4; ++i)
+    h[i] = ptx::cvt_e4m3x2(element_of(e, 2 * i) * inv, element_of(e, 2 * i + 1) * inv);
   const uint2 w = make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16);
   if (kVec && n >= 8) {
     *reinterpret_cast<uint2*>(out) = w;
@@ -152,58 +177,105 @@ struct QuantParams {
   int32_t N, d, col_blocks;
 };
 
-// A block of 1 x 128 to 16 lanes, 8 elements each.
-constexpr int kRowThreads = 256;
-template <class T, bool kVec>
+// Blocks of 1 x 128 to 8 lanes, which take pieces l and l + 8 of a block's 16; kPer blocks
+// side by side in a thread's registers.  16 lanes a block, a division of the block's number
+// and two for the scales in every lane left 16384 x 5120 bound by instructions: 59 us.
+constexpr int kRowThreads = 128;
+constexpr int kRowLanes = 8;
+constexpr int kRowBlocks = kRowThreads / kRowLanes;  // a CTA's side by side
+template <class T, bool kVec, int kPer>
 __global__ void __launch_bounds__(kRowThreads) quantize_rows_kernel(const QuantParams p) {
-  const int64_t block = int64_t(blockIdx.x) * (kRowThreads / 16) + (threadIdx.x >> 4);
-  const int64_t row = block / p.col_blocks;
-  const int cb = int(block - row * p.col_blocks);
-  const int col = cb * kBlock + int(threadIdx.x & 15) * 8;
-  const int n = row < p.N ? p.d - col : 0;
-  float v[8];
-  load8<T, kVec>(static_cast<const T*>(p.x) + row * p.ldx + col, n, v);
-  float m = max_abs(v);
+  const int lane = threadIdx.x % kRowLanes;
+  int64_t block = int64_t(blockIdx.x) * (kRowBlocks * kPer) + threadIdx.x / kRowLanes;
+  int64_t row = int64_t(p.N) * p.col_blocks <= UINT_MAX
+                    ? int64_t(uint32_t(block) / uint32_t(p.col_blocks))
+                    : block / p.col_blocks;
+  int cb = int(block - row * p.col_blocks);
+  int64_t rows[kPer];
+  int cbs[kPer];
+  Eight<T> e[kPer][2];
+  bool whole[kPer][2];
 #pragma unroll
-  for (int s = 8; s > 0; s >>= 1) m = ptx::max_nan(m, __shfl_xor_sync(0xFFFFFFFFu, m, s));
-  m = ptx::max_nan(m, kLeastMax);
-  if (row >= p.N) return;
-  if ((threadIdx.x & 15) == 0) p.scale[row * p.lds + cb] = __fdiv_rn(m, kMostE4m3);
-  if (n > 0)
-    store8<kVec>(p.values + row * p.ldv + col, n, v, __fdiv_rn(kMostE4m3, m));
+  for (int i = 0; i < kPer; ++i) {
+    rows[i] = row;
+    cbs[i] = cb;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int col = cb * kBlock + (lane + kRowLanes * j) * 8;
+      whole[i][j] = load_whole<T, kVec>(e[i][j], static_cast<const T*>(p.x) + row * p.ldx + col,
+                                        row < p.N ? p.d - col : 0, row == p.N - 1);
+    }
+    for (cb += kRowBlocks; cb >= p.col_blocks; cb -= p.col_blocks) ++row;
+  }
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const bool here = rows[i] < p.N;
+    const int col = cbs[i] * kBlock + lane * 8;
+    const T* x = static_cast<const T*>(p.x) + rows[i] * p.ldx + col;
+    uint32_t m = kLeastMaxBits;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      load_rest(e[i][j], x + 64 * j, here ? p.d - col - 64 * j : 0, whole[i][j]);
+      m = max(m, most(e[i][j]));
+    }
+#pragma unroll
+    for (int s = kRowLanes / 2; s > 0; s >>= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, s));
+    // One division for both: the first lane's is the scale, the others' its inverse.
+    const float top = __uint_as_float(m);
+    const float ratio = __fdiv_rn(lane == 0 ? top : kMostE4m3, lane == 0 ? kMostE4m3 : top);
+    const float inv = __shfl_sync(0xFFFFFFFFu, ratio, (threadIdx.x & 31) | 1);
+    if (!here) continue;
+    if (lane == 0) p.scale[rows[i] * p.lds + cbs[i]] = ratio;
+    uint8_t* out = p.values + rows[i] * p.ldv + col;
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      if (p.d - col > 64 * j) store8<kVec>(out + 64 * j, p.d - col - 64 * j, e[i][j], inv);
+  }
 }
 
-// A block of 128 x 128 to a CTA: 8 rows of 8 elements a thread, all loaded at once.
+// A block of 128 x 128 to a CTA, kTileLoads pieces of 8 elements a thread.
 constexpr int kTileThreads = 256;
+constexpr int kTileLoads = 8;
 template <class T, bool kVec>
 __global__ void __launch_bounds__(kTileThreads) quantize_tile_kernel(const QuantParams p) {
-  __shared__ float warp_max[kTileThreads / 32];
-  const int rb = int(blockIdx.x / p.col_blocks), cb = int(blockIdx.x - unsigned(rb) * p.col_blocks);
+  __shared__ uint32_t warp_max[kTileThreads / 32];
+  const int rb = int(blockIdx.x / unsigned(p.col_blocks));
+  const int cb = int(blockIdx.x - unsigned(rb) * unsigned(p.col_blocks));
   const int col = cb * kBlock + int(threadIdx.x & 15) * 8;
   const int row0 = rb * kBlock + int(threadIdx.x >> 4);
-  float v[8][8];
+  const T* x = static_cast<const T*>(p.x) + int64_t(row0) * p.ldx + col;
+  uint8_t* out = p.values + int64_t(row0) * p.ldv + col;
+  Eight<T> e[kTileLoads];
+  const bool whole = kVec && rb * kBlock + kBlock <= p.N && cb * kBlock + kBlock <= p.d;
+  if (whole) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int row = row0 + 16 * i;
-    load8<T, kVec>(static_cast<const T*>(p.x) + int64_t(row) * p.ldx + col,
-                   row < p.N ? p.d - col : 0, v[i]);
+    for (int i = 0; i < kTileLoads; ++i) load_whole<T, kVec>(e[i], x + 16 * i * p.ldx, 8, true);
+  } else {
+#pragma unroll
+    for (int i = 0; i < kTileLoads; ++i) {
+      const int n = row0 + 16 * i < p.N ? p.d - col : 0;
+      load_rest(e[i], x + 16 * i * p.ldx, n,
+                load_whole<T, kVec>(e[i], x + 16 * i * p.ldx, n, row0 + 16 * i == p.N - 1));
+    }
   }
-  float m = kLeastMax;
+  uint32_t m = kLeastMaxBits;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) m = ptx::max_nan(m, max_abs(v[i]));
-#pragma unroll
-  for (int s = 16; s > 0; s >>= 1) m = ptx::max_nan(m, __shfl_xor_sync(0xFFFFFFFFu, m, s));
+  for (int i = 0; i < kTileLoads; ++i) m = max(m, most(e[i]));
+  m = __reduce_max_sync(0xFFFFFFFFu, m);
   if ((threadIdx.x & 31) == 0) warp_max[threadIdx.x >> 5] = m;
   __syncthreads();
 #pragma unroll
-  for (int i = 0; i < kTileThreads / 32; ++i) m = ptx::max_nan(m, warp_max[i]);
-  if (threadIdx.x == 0) p.scale[int64_t(rb) * p.lds + cb] = __fdiv_rn(m, kMostE4m3);
-  const float inv = __fdiv_rn(kMostE4m3, m);
+  for (int i = 0; i < kTileThreads / 32; ++i) m = max(m, warp_max[i]);
+  const float top = __uint_as_float(m);
+  if (threadIdx.x == 0) p.scale[int64_t(rb) * p.lds + cb] = __fdiv_rn(top, kMostE4m3);
+  const float inv = __fdiv_rn(kMostE4m3, top);
+  if (whole) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int row = row0 + 16 * i;
-    if (row < p.N)
-      store8<kVec>(p.values + int64_t(row) * p.ldv + col, p.d - col, v[i], inv);
+    for (int i = 0; i < kTileLoads; ++i) store8<kVec>(out + 16 * i * p.ldv, 8, e[i], inv);
+  } else {
+#pragma unroll
+    for (int i = 0; i < kTileLoads; ++i)
+      if (row0 + 16 * i < p.N) store8<kVec>(out + 16 * i * p.ldv, p.d - col, e[i], inv);
   }
 }
 
@@ -934,20 +1006,21 @@ fs_status launch(const Device& dev, const fs_matmul_fp8_args& a, Plan s, cudaStr
   return FS_OK;
 }
 
-template <class T>
-void launch_quantize(const QuantParams& p, int block_rows, bool vec, unsigned blocks,
+// Rows' blocks a thread takes: one while they leave SMs without work, else two (four loads
+// in flight).
+int64_t blocks_per_thread(int64_t blocks, int sms) {
+  return blocks >= int64_t(sms) * 16 * kRowBlocks * 2 ? 2 : 1;
+}
+
+template <class T, bool kVec>
+void launch_quantize(const QuantParams& p, int block_rows, int64_t per, unsigned ctas,
                      cudaStream_t stream) {
-  if (block_rows == 1) {
-    if (vec)
-      quantize_rows_kernel<T, true><<<blocks, kRowThreads, 0, stream>>>(p);
-    else
-      quantize_rows_kernel<T, false><<<blocks, kRowThreads, 0, stream>>>(p);
-  } else {
-    if (vec)
-      quantize_tile_kernel<T, true><<<blocks, kTileThreads, 0, stream>>>(p);
-    else
-      quantize_tile_kernel<T, false><<<blocks, kTileThreads, 0, stream>>>(p);
-  }
+  if (block_rows != 1)
+    quantize_tile_kernel<T, kVec><<<ctas, kTileThreads, 0, stream>>>(p);
+  else if (per == 2)
+    quantize_rows_kernel<T, kVec, 2><<<ctas, kRowThreads, 0, stream>>>(p);
+  else
+    quantize_rows_kernel<T, kVec, 1><<<ctas, kRowThreads, 0, stream>>>(p);
 }
 
 }  // namespace
@@ -968,12 +1041,16 @@ extern "C" fs_status fs_quantize(const void* x, int64_t N, int64_t d, int64_t ld
     return FS_ERR_INVALID_ARG;
   if (!x || !values || !scale || !aligned(x, element(x_dtype)) || !aligned(scale, 4))
     return FS_ERR_INVALID_ARG;
-  const int64_t blocks = block_rows == 1 ? ceil_div(N * col_blocks, kRowThreads / 16)
-                                         : ceil_div(N, kBlock) * col_blocks;
-  if (blocks > INT_MAX) return FS_ERR_INVALID_ARG;
+  const int64_t all = N * col_blocks;
+  if ((block_rows == 1 ? ceil_div(all, kRowBlocks) : ceil_div(N, kBlock) * col_blocks) >
+      INT_MAX)
+    return FS_ERR_INVALID_ARG;
   const Device* dev = nullptr;
   const fs_status st = device_setup(&dev);
   if (st != FS_OK) return st;
+  const int64_t per = blocks_per_thread(all, dev->sms);
+  const unsigned ctas = unsigned(block_rows == 1 ? ceil_div(all, kRowBlocks * per)
+                                                 : ceil_div(N, kBlock) * col_blocks);
   QuantParams p = {};
   p.x = x;
   p.ldx = N > 1 ? ldx : 0;
@@ -988,9 +1065,11 @@ extern "C" fs_status fs_quantize(const void* x, int64_t N, int64_t d, int64_t ld
                    p.ldv % 8 == 0;
   cudaStream_t stream = static_cast<cudaStream_t>(stream_ptr);
   if (x_dtype == FS_F32)
-    launch_quantize<float>(p, block_rows, vec, unsigned(blocks), stream);
+    vec ? launch_quantize<float, true>(p, block_rows, per, ctas, stream)
+        : launch_quantize<float, false>(p, block_rows, per, ctas, stream);
   else
-    launch_quantize<__nv_bfloat16>(p, block_rows, vec, unsigned(blocks), stream);
+    vec ? launch_quantize<__nv_bfloat16, true>(p, block_rows, per, ctas, stream)
+        : launch_quantize<__nv_bfloat16, false>(p, block_rows, per, ctas, stream);
   return cudaGetLastError() == cudaSuccess ? FS_OK : FS_ERR_CUDA;
 }
 
