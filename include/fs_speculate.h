@@ -101,7 +101,7 @@ typedef struct fs_probs_args {
   int dtype, out_dtype;
 } fs_probs_args;
 
-/* Limits: 0 <= N < 2^31 (0 does nothing), 1 <= V < 2^31 - 2^16. */
+/* Limits: 0 <= N < 2^28 (0 does nothing), 1 <= V < 2^31 - 2^16. */
 fs_status fs_probs(const fs_probs_args *args, void *stream);
 
 /* Largest K of fs_verify. */

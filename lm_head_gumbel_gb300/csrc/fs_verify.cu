@@ -64,12 +64,214 @@ struct ProbsParams {
   void* out;
   int64_t ldo;
   int32_t N, V;
+  int32_t part;  // a CTA's elements of a row, a multiple of 4
+};
+
+// exp for a whole row in registers.  p = 2^(l c - K) / sum of the same for any K, so K is
+// the whole number nearest m c, c = log2(e) / T in two floats: then l c - K - n, n a whole
+// number too, is one rounding of a number of at most 1/2 (off by 2^-25), and 2^n goes into
+// the exponent.  10 operations; where m c is too large for that, Exp.
+struct FastExp {
+  float k, c_hi, c_lo;
+  static __device__ __forceinline__ bool can(float m, float c_hi) { return fabsf(m * c_hi) < 0x1p22f; }
+  __device__ __forceinline__ float operator()(float l) const {
+    constexpr float kMagic = 0x1.8p23f;  // adding it rounds to a whole number, in the low bits
+    const float y = fmaf(l, c_hi, -k);
+    const float r = y + kMagic;
+    const float f = fmaf(l, c_lo, fmaf(l, c_hi, -(k + (r - kMagic))));
+    float e;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(f));
+    return y < -126.0f ? 0.0f : __int_as_float(__float_as_int(e) + (__float_as_int(r) << 23));
+  }
 };
 
 constexpr int kProbThreads = 512;
+constexpr int kProbWarps = kProbThreads / 32;
+constexpr int kMaxProbCluster = 8;
 
+// Four elements from v0, -infinity for those that do not exist, are masked or (greedy) NaN.
+template <class T, bool kVec>
+__device__ __forceinline__ void load_logits(const T* x, int v0, int end, float (&l)[4]) {
+  if (kVec && v0 + 4 <= end) {
+    if constexpr (sizeof(T) == 2) {
+      const uint2 w = __ldcs(reinterpret_cast<const uint2*>(x + v0));
+      l[0] = __uint_as_float(w.x << 16), l[1] = __uint_as_float(w.x & 0xFFFF0000u);
+      l[2] = __uint_as_float(w.y << 16), l[3] = __uint_as_float(w.y & 0xFFFF0000u);
+    } else {
+      const float4 w = __ldcs(reinterpret_cast<const float4*>(x + v0));
+      l[0] = w.x, l[1] = w.y, l[2] = w.z, l[3] = w.w;
+    }
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) l[i] = v0 + i < end ? wide(x[v0 + i]) : -INFINITY;
+}
+template <class TO, bool kVec>
+__device__ __forceinline__ void store_probs(TO* out, int v0, int end, const float (&p)[4]) {
+  if (kVec && v0 + 4 <= end) {
+    if constexpr (sizeof(TO) == 2) {
+      const __nv_bfloat162 a = __floats2bfloat162_rn(p[0], p[1]), b = __floats2bfloat162_rn(p[2], p[3]);
+      *reinterpret_cast<uint2*>(out + v0) = make_uint2(*reinterpret_cast<const uint32_t*>(&a),
+                                                       *reinterpret_cast<const uint32_t*>(&b));
+    } else {
+      *reinterpret_cast<float4*>(out + v0) = make_float4(p[0], p[1], p[2], p[3]);
+    }
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (v0 + i < end) narrow(out + v0 + i, p[i]);
+}
+
+// What the CTAs of a row's cluster tell one another.
+struct ProbsShared {
+  float warp[kProbWarps];
+  int warp_at[kProbWarps];
+  float max[kMaxProbCluster], sum[kMaxProbCluster];
+  int at[kMaxProbCluster];
+};
+__device__ __forceinline__ void tell(const void* slot, int n_ctas, uint32_t v) {
+  if (int(threadIdx.x) < n_ctas)
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(ptx::cluster_addr(slot, threadIdx.x)),
+                 "r"(v)
+                 : "memory");
+}
+
+// A row to a cluster of CTAs, kGroups times 4 elements a thread in registers: read once,
+// written once.  Bound: memory.  The loads of a row are all in flight at once; the maximum
+// and the sum go through the cluster's shared memory, in the order of its CTAs.
+template <class T, class TO, bool kVec, int kGroups>
+__global__ void __launch_bounds__(kProbThreads, kGroups <= 8 ? 2 : 1)
+    probs_kernel(const ProbsParams p) {
+  __shared__ ProbsShared sm;
+  uint32_t n_ctas_u;
+  asm("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(n_ctas_u));
+  const int n_ctas = int(n_ctas_u);
+  const int rank = int(ptx::cluster_ctarank());
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t row = blockIdx.x / n_ctas_u;
+  ptx::cluster_arrive();  // this CTA has started
+  const T* x = static_cast<const T*>(p.logits) + row * p.ldl;
+  TO* out = static_cast<TO*>(p.out) + row * p.ldo;
+  const int begin = min(rank * p.part, p.V);
+  const int end = begin + min(p.part, p.V - begin);
+  const int v0 = begin + int(threadIdx.x) * 4;
+  float l[kGroups][4];
+#pragma unroll
+  for (int g = 0; g < kGroups; ++g) load_logits<T, kVec>(x, v0 + g * kProbThreads * 4, end, l[g]);
+  const float temp = p.temperature ? p.temperature[row] : 1.0f;
+  const bool greedy = !(temp > 0.0f && temp < INFINITY);
+  if (p.mask) {
+    const uint32_t* mask = p.mask + row * p.mask_ld;
+#pragma unroll
+    for (int g = 0; g < kGroups; ++g) {
+      const int v = v0 + g * kProbThreads * 4;
+      const uint32_t bits = v < end ? mask[v >> 5] >> (v & 31) : 0u;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (!(bits >> i & 1u)) l[g][i] = -INFINITY;
+    }
+  }
+  float m = -INFINITY;
+  if (greedy) {
+#pragma unroll
+    for (int g = 0; g < kGroups; ++g)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) m = fmaxf(m, l[g][i]);  // of a number and NaN the number
+  } else {
+#pragma unroll
+    for (int g = 0; g < kGroups; ++g)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) m = max_nan(m, l[g][i]);
+  }
+#pragma unroll
+  for (int s = 16; s > 0; s >>= 1) m = max_nan(m, __shfl_xor_sync(0xFFFFFFFFu, m, s));
+  if (lane == 0) sm.warp[warp] = m;
+  __syncthreads();
+  m = sm.warp[0];
+#pragma unroll
+  for (int w = 1; w < kProbWarps; ++w) m = max_nan(m, sm.warp[w]);
+  ptx::cluster_wait();
+  tell(&sm.max[rank], n_ctas, __float_as_uint(m));
+  ptx::cluster_sync();
+  for (int c = 0; c < n_ctas; ++c) m = max_nan(m, sm.max[c]);
+
+  if (greedy) {
+    int at = INT_MAX;
+#pragma unroll
+    for (int g = kGroups - 1; g >= 0; --g)
+#pragma unroll
+      for (int i = 3; i >= 0; --i)
+        if (l[g][i] == m) at = v0 + g * kProbThreads * 4 + i;
+    if (m == -INFINITY) at = INT_MAX;
+    at = __reduce_min_sync(0xFFFFFFFFu, at);
+    if (lane == 0) sm.warp_at[warp] = at;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kProbWarps; ++w) at = min(at, sm.warp_at[w]);
+    tell(&sm.at[rank], n_ctas, uint32_t(at));
+    ptx::cluster_sync();
+    for (int c = 0; c < n_ctas; ++c) at = min(at, sm.at[c]);
+#pragma unroll
+    for (int g = 0; g < kGroups; ++g) {
+      const int v = v0 + g * kProbThreads * 4;
+      const float one[4] = {v == at ? 1.0f : 0.0f, v + 1 == at ? 1.0f : 0.0f,
+                            v + 2 == at ? 1.0f : 0.0f, v + 3 == at ? 1.0f : 0.0f};
+      store_probs<TO, kVec>(out, v, end, one);
+    }
+    return;
+  }
+  float sum = 0.0f;
+  if (m > -INFINITY && m < INFINITY) {
+    const Exp exact(m, temp);
+    if (FastExp::can(m, exact.c_hi)) {
+      const FastExp e{rintf(m * exact.c_hi), exact.c_hi, exact.c_lo};
+#pragma unroll
+      for (int g = 0; g < kGroups; ++g)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sum += l[g][i] = e(l[g][i]);
+    } else {
+#pragma unroll
+      for (int g = 0; g < kGroups; ++g)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sum += l[g][i] = exact(l[g][i]);
+    }
+  } else {
+    // No allowed id: all 0.  A NaN or +inf among them: all of them NaN.
+    const float nan = __int_as_float(0x7FFFFFFF);
+#pragma unroll
+    for (int g = 0; g < kGroups; ++g) {
+      const int v = v0 + g * kProbThreads * 4;
+      const uint32_t bits =
+          !p.mask ? 15u : v < end ? p.mask[row * p.mask_ld + (v >> 5)] >> (v & 31) : 0u;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) l[g][i] = m == -INFINITY || !(bits >> i & 1u) ? 0.0f : nan;
+    }
+    sum = 1.0f;
+  }
+#pragma unroll
+  for (int s = 16; s > 0; s >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, s);
+  if (lane == 0) sm.warp[warp] = sum;
+  __syncthreads();
+  sum = sm.warp[0];
+#pragma unroll
+  for (int w = 1; w < kProbWarps; ++w) sum += sm.warp[w];
+  tell(&sm.sum[rank], n_ctas, __float_as_uint(sum));
+  ptx::cluster_sync();
+  sum = 0.0f;
+  for (int c = 0; c < n_ctas; ++c) sum += sm.sum[c];
+  const float inv = __fdiv_rn(1.0f, sum);
+#pragma unroll
+  for (int g = 0; g < kGroups; ++g) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) l[g][i] *= inv;
+    store_probs<TO, kVec>(out, v0 + g * kProbThreads * 4, end, l[g]);
+  }
+}
+
+// Rows longer than a cluster's registers: one CTA, three passes, the later two mostly from L2.
 template <class T, class TO>
-__global__ void __launch_bounds__(kProbThreads) probs_kernel(const ProbsParams p) {
+__global__ void __launch_bounds__(kProbThreads) long_probs_kernel(const ProbsParams p) {
   __shared__ float s_val[kProbThreads / 32];
   __shared__ int s_idx[kProbThreads / 32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -427,12 +629,41 @@ uintptr_t element(int dtype) { return dtype == FS_F32 ? 4 : 2; }
 bool known(int dtype) { return dtype == FS_BF16 || dtype == FS_F32; }
 constexpr int64_t kMostV = INT_MAX - 65536;  // a segment's end fits 32 bits
 
-template <class T>
-void launch_probs(const ProbsParams& p, int out_dtype, cudaStream_t stream) {
-  if (out_dtype == FS_F32)
-    probs_kernel<T, float><<<unsigned(p.N), kProbThreads, 0, stream>>>(p);
-  else
-    probs_kernel<T, __nv_bfloat16><<<unsigned(p.N), kProbThreads, 0, stream>>>(p);
+template <class T, class TO, bool kVec>
+cudaError_t launch_probs(ProbsParams p, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.blockDim = dim3(kProbThreads);
+  cfg.stream = stream;
+  // CTAs of a row's cluster and their threads' registers by V alone, so that a row's sum
+  // does not depend on what else is computed.  Up to 16 elements a thread more CTAs, which
+  // read and write a row sooner; then more elements.
+  int ctas = 1;
+  while (ctas < kMaxProbCluster && int64_t(ctas) * kProbThreads * 16 < p.V) ctas *= 2;
+  const int64_t per = ceil_div(ceil_div(p.V, ctas), kProbThreads * 4);
+  if (per > 16) {
+    cfg.gridDim = dim3(unsigned(p.N));
+    return cudaLaunchKernelEx(&cfg, long_probs_kernel<T, TO>, p);
+  }
+  p.part = int32_t(ceil_div(ceil_div(p.V, ctas), 4) * 4);
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = unsigned(ctas);
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.gridDim = dim3(unsigned(p.N * ctas));
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return per <= 2    ? cudaLaunchKernelEx(&cfg, probs_kernel<T, TO, kVec, 2>, p)
+         : per <= 4  ? cudaLaunchKernelEx(&cfg, probs_kernel<T, TO, kVec, 4>, p)
+         : per <= 8  ? cudaLaunchKernelEx(&cfg, probs_kernel<T, TO, kVec, 8>, p)
+         : per <= 10 ? cudaLaunchKernelEx(&cfg, probs_kernel<T, TO, kVec, 10>, p)
+                     : cudaLaunchKernelEx(&cfg, probs_kernel<T, TO, kVec, 16>, p);
+}
+
+template <class T, class TO>
+cudaError_t launch_probs(const ProbsParams& p, cudaStream_t stream) {
+  const bool vec = aligned(p.logits, 4 * sizeof(T)) && p.ldl % 4 == 0 &&
+                   aligned(p.out, 4 * sizeof(TO)) && p.ldo % 4 == 0;
+  return vec ? launch_probs<T, TO, true>(p, stream) : launch_probs<T, TO, false>(p, stream);
 }
 
 }  // namespace
@@ -444,7 +675,7 @@ using namespace fs::verify;
 extern "C" fs_status fs_probs(const fs_probs_args* args, void* stream_ptr) {
   if (!args) return FS_ERR_INVALID_ARG;
   const fs_probs_args& a = *args;
-  if (a.N < 0 || a.N > INT_MAX || a.V < 1 || a.V > kMostV || !known(a.dtype) ||
+  if (a.N < 0 || a.N > INT_MAX / kMaxProbCluster || a.V < 1 || a.V > kMostV || !known(a.dtype) ||
       !known(a.out_dtype))
     return FS_ERR_INVALID_ARG;
   if (a.N == 0) return FS_OK;
@@ -461,20 +692,26 @@ extern "C" fs_status fs_probs(const fs_probs_args* args, void* stream_ptr) {
   if (st != FS_OK) return st;
   ProbsParams p = {};
   p.logits = a.logits;
-  p.ldl = a.ldl;
+  p.ldl = a.N > 1 ? a.ldl : 0;
   p.temperature = a.temperature;
   p.mask = a.vocab_mask;
   p.mask_ld = a.mask_ld;
   p.out = a.out;
-  p.ldo = a.ldo;
+  p.ldo = a.N > 1 ? a.ldo : 0;
   p.N = int32_t(a.N);
   p.V = int32_t(a.V);
   cudaStream_t stream = static_cast<cudaStream_t>(stream_ptr);
-  if (a.dtype == FS_F32)
-    launch_probs<float>(p, a.out_dtype, stream);
-  else
-    launch_probs<__nv_bfloat16>(p, a.out_dtype, stream);
-  return cudaGetLastError() == cudaSuccess ? FS_OK : FS_ERR_CUDA;
+  const cudaError_t err =
+      a.dtype == FS_F32
+          ? (a.out_dtype == FS_F32 ? launch_probs<float, float>(p, stream)
+                                   : launch_probs<float, __nv_bfloat16>(p, stream))
+          : (a.out_dtype == FS_F32 ? launch_probs<__nv_bfloat16, float>(p, stream)
+                                   : launch_probs<__nv_bfloat16, __nv_bfloat16>(p, stream));
+  if (err != cudaSuccess) {
+    cudaGetLastError();
+    return FS_ERR_CUDA;
+  }
+  return FS_OK;
 }
 
 extern "C" fs_status fs_verify(const fs_verify_args* args, void* stream_ptr) {
