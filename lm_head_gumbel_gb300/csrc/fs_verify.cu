@@ -13,8 +13,13 @@
 #include "fs_speculate.h"
 
 namespace fs {
+int* device_error_word();  // fs_sample.cu
+
 namespace verify {
 namespace {
+
+constexpr uint64_t kWaitLimitNs = 2000000000ull;  // 2 s
+constexpr int kErrWaitTimeout = 1;                // the library's device error word, bit 0
 
 __device__ __forceinline__ float wide(float x) { return x; }
 __device__ __forceinline__ float wide(__nv_bfloat16 x) { return __bfloat162float(x); }
@@ -64,7 +69,9 @@ struct ProbsParams {
   void* out;
   int64_t ldo;
   int32_t N, V;
-  int32_t part;  // a CTA's elements of a row, a multiple of 4
+  int32_t part;  // a CTA's elements of a row, a multiple of 32
+  uint64_t wait_limit_ns;
+  int* error_word;
 };
 
 // exp for a whole row in registers.  p = 2^(l c - K) / sum of the same for any K, so K is
@@ -87,185 +94,256 @@ struct FastExp {
 
 constexpr int kProbThreads = 512;
 constexpr int kProbWarps = kProbThreads / 32;
-constexpr int kMaxProbCluster = 8;
+constexpr int kMaxProbCluster = 16;  // more than 8 need the kernel's leave
+constexpr int kMaxProbGroups = 8;
+constexpr int kMaxPart = kMaxProbGroups * 4 * kProbThreads;  // a CTA's elements of a row
 
-// Four elements from v0, -infinity for those that do not exist, are masked or (greedy) NaN.
-template <class T, bool kVec>
-__device__ __forceinline__ void load_logits(const T* x, int v0, int end, float (&l)[4]) {
-  if (kVec && v0 + 4 <= end) {
+// Four elements at x, of which n exist, the others -infinity.
+template <class T, bool kWhole>
+__device__ __forceinline__ void load4(const T* x, int n, float (&l)[4]) {
+  if (kWhole && n >= 4) {
     if constexpr (sizeof(T) == 2) {
-      const uint2 w = __ldcs(reinterpret_cast<const uint2*>(x + v0));
+      const uint2 w = *reinterpret_cast<const uint2*>(x);
       l[0] = __uint_as_float(w.x << 16), l[1] = __uint_as_float(w.x & 0xFFFF0000u);
       l[2] = __uint_as_float(w.y << 16), l[3] = __uint_as_float(w.y & 0xFFFF0000u);
     } else {
-      const float4 w = __ldcs(reinterpret_cast<const float4*>(x + v0));
+      const float4 w = *reinterpret_cast<const float4*>(x);
       l[0] = w.x, l[1] = w.y, l[2] = w.z, l[3] = w.w;
     }
     return;
   }
 #pragma unroll
-  for (int i = 0; i < 4; ++i) l[i] = v0 + i < end ? wide(x[v0 + i]) : -INFINITY;
+  for (int i = 0; i < 4; ++i) l[i] = i < n ? wide(x[i]) : -INFINITY;
 }
-template <class TO, bool kVec>
-__device__ __forceinline__ void store_probs(TO* out, int v0, int end, const float (&p)[4]) {
-  if (kVec && v0 + 4 <= end) {
+template <class TO, bool kWhole>
+__device__ __forceinline__ void store4(TO* out, int n, const float (&p)[4]) {
+  if (kWhole && n >= 4) {
     if constexpr (sizeof(TO) == 2) {
       const __nv_bfloat162 a = __floats2bfloat162_rn(p[0], p[1]), b = __floats2bfloat162_rn(p[2], p[3]);
-      *reinterpret_cast<uint2*>(out + v0) = make_uint2(*reinterpret_cast<const uint32_t*>(&a),
-                                                       *reinterpret_cast<const uint32_t*>(&b));
+      *reinterpret_cast<uint2*>(out) = make_uint2(*reinterpret_cast<const uint32_t*>(&a),
+                                                  *reinterpret_cast<const uint32_t*>(&b));
     } else {
-      *reinterpret_cast<float4*>(out + v0) = make_float4(p[0], p[1], p[2], p[3]);
+      *reinterpret_cast<float4*>(out) = make_float4(p[0], p[1], p[2], p[3]);
     }
     return;
   }
 #pragma unroll
   for (int i = 0; i < 4; ++i)
-    if (v0 + i < end) narrow(out + v0 + i, p[i]);
+    if (i < n) narrow(out + i, p[i]);
 }
 
-// What the CTAs of a row's cluster tell one another.
-struct ProbsShared {
-  float warp[kProbWarps];
+struct alignas(16) ProbsShared {
+  float warp_max[kProbWarps], warp_sum[kProbWarps];
   int warp_at[kProbWarps];
-  float max[kMaxProbCluster], sum[kMaxProbCluster];
-  int at[kMaxProbCluster];
+  // What the CTAs of a row's cluster tell one another: maxima; sums, or of a greedy row
+  // the ids.
+  uint32_t first[kMaxProbCluster], second[kMaxProbCluster];
+  uint32_t mask[2][kMaxPart / 32];  // this row's and the next one's words
+  uint64_t full;                    // the row's elements have arrived
+  uint64_t told[2];                 // every CTA's word has
+  uint32_t gave_up;
 };
-__device__ __forceinline__ void tell(const void* slot, int n_ctas, uint32_t v) {
+
+// A barrier's phase has completed, or the wait's limit has passed: then the error word says
+// so, and no later wait waits.
+__device__ __forceinline__ void wait_for(const ProbsParams& p, ProbsShared& sm, uint64_t* bar,
+                                         uint32_t phase) {
+  if (ptx::mbar_try_wait(bar, phase)) return;
+  const uint64_t t0 = ptx::global_timer_ns();
+  while (!ptx::mbar_try_wait(bar, phase) && !*static_cast<volatile uint32_t*>(&sm.gave_up)) {
+    if (ptx::global_timer_ns() - t0 > p.wait_limit_ns) {
+      *static_cast<volatile uint32_t*>(&sm.gave_up) = 1u;
+      atomicOr(p.error_word, kErrWaitTimeout);
+    }
+  }
+}
+// This CTA's word into slot `rank` of every CTA of the cluster, by stores that count on the
+// receiver's barrier.  (A cluster's barrier would also wait for the stores of the row before.)
+// A word of the next row cannot overtake: its sender has had this row's words from everyone.
+__device__ __forceinline__ void tell(uint32_t* slots, uint64_t* bar, int rank, int n_ctas,
+                                     uint32_t v) {
+  if (threadIdx.x == 0) ptx::mbar_arrive_expect_tx(bar, uint32_t(n_ctas) * 4u);
   if (int(threadIdx.x) < n_ctas)
-    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(ptx::cluster_addr(slot, threadIdx.x)),
-                 "r"(v)
-                 : "memory");
+    asm volatile(
+        "st.async.shared::cluster.mbarrier::complete_tx::bytes.u32 [%0], %1, [%2];" ::"r"(
+            ptx::cluster_addr(slots + rank, threadIdx.x)),
+        "r"(v), "r"(ptx::cluster_addr(bar, threadIdx.x))
+        : "memory");
+}
+template <class Op>
+__device__ __forceinline__ float of_warps(const float (&v)[kProbWarps], Op op) {
+  float r = v[0];
+#pragma unroll
+  for (int w = 1; w < kProbWarps; ++w) r = op(r, v[w]);
+  return r;
+}
+// `bytes` (a multiple of 16) from global to shared memory, arriving on `bar`.
+__device__ __forceinline__ void copy_async(void* to, const void* from, uint32_t bytes,
+                                           uint64_t* bar) {
+  ptx::mbar_arrive_expect_tx(bar, bytes);
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::
+          "r"(ptx::smem_u32(to)),
+      "l"(from), "r"(bytes), "r"(ptx::smem_u32(bar))
+      : "memory");
 }
 
 // A row to a cluster of CTAs, kGroups times 4 elements a thread in registers: read once,
-// written once.  Bound: memory.  The loads of a row are all in flight at once; the maximum
-// and the sum go through the cluster's shared memory, in the order of its CTAs.
-template <class T, class TO, bool kVec, int kGroups>
-__global__ void __launch_bounds__(kProbThreads, kGroups <= 8 ? 2 : 1)
-    probs_kernel(const ProbsParams p) {
+// written once.  Bound: memory.  The clusters stay for many rows: a row's elements are copied
+// to shared memory while the row before is summed and written (without that a cluster's life
+// was a chain of waits: 320 rows of 128256, masked, 139 us, now PROBS_US).  The maximum and the
+// sum go through the cluster's shared memory, in the order of its CTAs.
+// kAsync: rows on 16-byte boundaries; else they are read element by element.
+template <class T, class TO, bool kAsync, int kGroups>
+__global__ void __launch_bounds__(kProbThreads, 2) probs_kernel(const ProbsParams p) {
   __shared__ ProbsShared sm;
+  extern __shared__ __align__(16) uint8_t buffer_raw[];
+  T* buffer = reinterpret_cast<T*>(buffer_raw);
   uint32_t n_ctas_u;
   asm("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(n_ctas_u));
   const int n_ctas = int(n_ctas_u);
   const int rank = int(ptx::cluster_ctarank());
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t row = blockIdx.x / n_ctas_u;
-  ptx::cluster_arrive();  // this CTA has started
-  const T* x = static_cast<const T*>(p.logits) + row * p.ldl;
-  TO* out = static_cast<TO*>(p.out) + row * p.ldo;
+  const int n_clusters = int(gridDim.x / n_ctas_u);
   const int begin = min(rank * p.part, p.V);
-  const int end = begin + min(p.part, p.V - begin);
-  const int v0 = begin + int(threadIdx.x) * 4;
-  float l[kGroups][4];
-#pragma unroll
-  for (int g = 0; g < kGroups; ++g) load_logits<T, kVec>(x, v0 + g * kProbThreads * 4, end, l[g]);
-  const float temp = p.temperature ? p.temperature[row] : 1.0f;
-  const bool greedy = !(temp > 0.0f && temp < INFINITY);
-  if (p.mask) {
-    const uint32_t* mask = p.mask + row * p.mask_ld;
+  const int n = min(p.part, p.V - begin);  // this CTA's elements
+  constexpr int kWholeCopy = 16 / int(sizeof(T));
+  const int copied = kAsync ? n / kWholeCopy * kWholeCopy : 0;  // the rest is read directly
+  const int words = (n + 31) / 32;
+  if (threadIdx.x == 0) {
+    ptx::mbar_init(&sm.full, 1);
+    ptx::mbar_init(&sm.told[0], 1);
+    ptx::mbar_init(&sm.told[1], 1);
+    ptx::fence_barrier_init();
+    sm.gave_up = 0u;
+  }
+  auto row_of = [&](int64_t row) { return static_cast<const T*>(p.logits) + row * p.ldl + begin; };
+  auto mask_word = [&](int64_t row) {
+    return int(threadIdx.x) < words ? p.mask[row * p.mask_ld + begin / 32 + threadIdx.x] : 0u;
+  };
+  int64_t row = blockIdx.x / n_ctas_u;
+  if (p.mask) sm.mask[0][threadIdx.x] = mask_word(row);
+  float temp = p.temperature ? p.temperature[row] : 1.0f;
+  __syncthreads();
+  if (copied > 0 && threadIdx.x == 0)
+    copy_async(buffer, row_of(row), uint32_t(copied) * sizeof(T), &sm.full);
+  ptx::cluster_sync();  // every CTA has started before another one writes its memory
+  const int i0 = int(threadIdx.x) * 4;
+  for (int turn = 0; row < p.N; ++turn) {
+    const T* x = row_of(row);
+    const int64_t next = row + n_clusters;
+    const bool more = next < p.N;
+    const uint32_t* mask = sm.mask[turn & 1];
+    const bool greedy = !(temp > 0.0f && temp < INFINITY);
+    const uint32_t phase = uint32_t(turn & 1);
+    if (copied > 0) wait_for(p, sm, &sm.full, phase);
+    float l[kGroups][4];
+    float m = -INFINITY;
 #pragma unroll
     for (int g = 0; g < kGroups; ++g) {
-      const int v = v0 + g * kProbThreads * 4;
-      const uint32_t bits = v < end ? mask[v >> 5] >> (v & 31) : 0u;
+      const int i = i0 + g * kProbThreads * 4;
+      if (i + 4 <= copied)
+        load4<T, true>(buffer + i, 4, l[g]);
+      else
+        load4<T, false>(x + i, n - i, l[g]);  // past a piece that is copied in part: from memory
+      if (p.mask) {
+        const uint32_t bits = i < n ? mask[i >> 5] >> (i & 31) : 0u;
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (!(bits >> i & 1u)) l[g][i] = -INFINITY;
+        for (int k = 0; k < 4; ++k)
+          if (!(bits >> k & 1u)) l[g][k] = -INFINITY;
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k)  // of a number and NaN, fmaxf is the number
+        m = greedy ? fmaxf(m, l[g][k]) : max_nan(m, l[g][k]);
     }
-  }
-  float m = -INFINITY;
-  if (greedy) {
 #pragma unroll
-    for (int g = 0; g < kGroups; ++g)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) m = fmaxf(m, l[g][i]);  // of a number and NaN the number
-  } else {
-#pragma unroll
-    for (int g = 0; g < kGroups; ++g)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) m = max_nan(m, l[g][i]);
-  }
-#pragma unroll
-  for (int s = 16; s > 0; s >>= 1) m = max_nan(m, __shfl_xor_sync(0xFFFFFFFFu, m, s));
-  if (lane == 0) sm.warp[warp] = m;
-  __syncthreads();
-  m = sm.warp[0];
-#pragma unroll
-  for (int w = 1; w < kProbWarps; ++w) m = max_nan(m, sm.warp[w]);
-  ptx::cluster_wait();
-  tell(&sm.max[rank], n_ctas, __float_as_uint(m));
-  ptx::cluster_sync();
-  for (int c = 0; c < n_ctas; ++c) m = max_nan(m, sm.max[c]);
+    for (int s = 16; s > 0; s >>= 1) m = max_nan(m, __shfl_xor_sync(0xFFFFFFFFu, m, s));
+    if (lane == 0) sm.warp_max[warp] = m;
+    __syncthreads();  // and every thread has read the buffer
+    if (more && copied > 0 && threadIdx.x == 0)
+      copy_async(buffer, row_of(next), uint32_t(copied) * sizeof(T), &sm.full);
+    const uint32_t next_word = more && p.mask ? mask_word(next) : 0u;
+    const float next_temp = more && p.temperature ? p.temperature[next] : 1.0f;
+    m = of_warps(sm.warp_max, max_nan);
+    tell(sm.first, &sm.told[0], rank, n_ctas, __float_as_uint(m));
+    wait_for(p, sm, &sm.told[0], phase);
+    for (int c = 0; c < n_ctas; ++c) m = max_nan(m, __uint_as_float(sm.first[c]));
 
-  if (greedy) {
-    int at = INT_MAX;
+    TO* out = static_cast<TO*>(p.out) + row * p.ldo + begin;
+    if (greedy) {
+      int at = INT_MAX;
+      if (m > -INFINITY) {
 #pragma unroll
-    for (int g = kGroups - 1; g >= 0; --g)
+        for (int g = kGroups - 1; g >= 0; --g)
 #pragma unroll
-      for (int i = 3; i >= 0; --i)
-        if (l[g][i] == m) at = v0 + g * kProbThreads * 4 + i;
-    if (m == -INFINITY) at = INT_MAX;
-    at = __reduce_min_sync(0xFFFFFFFFu, at);
-    if (lane == 0) sm.warp_at[warp] = at;
-    __syncthreads();
+          for (int k = 3; k >= 0; --k)
+            if (l[g][k] == m) at = begin + i0 + g * kProbThreads * 4 + k;
+      }
+      at = __reduce_min_sync(0xFFFFFFFFu, at);
+      if (lane == 0) sm.warp_at[warp] = at;
+      sm.mask[phase ^ 1u][threadIdx.x] = next_word;
+      __syncthreads();
 #pragma unroll
-    for (int w = 0; w < kProbWarps; ++w) at = min(at, sm.warp_at[w]);
-    tell(&sm.at[rank], n_ctas, uint32_t(at));
-    ptx::cluster_sync();
-    for (int c = 0; c < n_ctas; ++c) at = min(at, sm.at[c]);
+      for (int w = 0; w < kProbWarps; ++w) at = min(at, sm.warp_at[w]);
+      tell(sm.second, &sm.told[1], rank, n_ctas, uint32_t(at));
+      wait_for(p, sm, &sm.told[1], phase);
+      for (int c = 0; c < n_ctas; ++c) at = min(at, int(sm.second[c]));
 #pragma unroll
-    for (int g = 0; g < kGroups; ++g) {
-      const int v = v0 + g * kProbThreads * 4;
-      const float one[4] = {v == at ? 1.0f : 0.0f, v + 1 == at ? 1.0f : 0.0f,
-                            v + 2 == at ? 1.0f : 0.0f, v + 3 == at ? 1.0f : 0.0f};
-      store_probs<TO, kVec>(out, v, end, one);
-    }
-    return;
-  }
-  float sum = 0.0f;
-  if (m > -INFINITY && m < INFINITY) {
-    const Exp exact(m, temp);
-    if (FastExp::can(m, exact.c_hi)) {
-      const FastExp e{rintf(m * exact.c_hi), exact.c_hi, exact.c_lo};
-#pragma unroll
-      for (int g = 0; g < kGroups; ++g)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) sum += l[g][i] = e(l[g][i]);
+      for (int g = 0; g < kGroups; ++g) {
+        const int i = i0 + g * kProbThreads * 4, v = begin + i;
+        const float one[4] = {v == at ? 1.0f : 0.0f, v + 1 == at ? 1.0f : 0.0f,
+                              v + 2 == at ? 1.0f : 0.0f, v + 3 == at ? 1.0f : 0.0f};
+        store4<TO, kAsync>(out + i, n - i, one);
+      }
     } else {
+      float sum = 0.0f;
+      if (m > -INFINITY && m < INFINITY) {
+        const Exp exact(m, temp);
+        if (FastExp::can(m, exact.c_hi)) {
+          const FastExp e{rintf(m * exact.c_hi), exact.c_hi, exact.c_lo};
 #pragma unroll
-      for (int g = 0; g < kGroups; ++g)
+          for (int g = 0; g < kGroups; ++g)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) sum += l[g][i] = exact(l[g][i]);
+            for (int k = 0; k < 4; ++k) sum += l[g][k] = e(l[g][k]);
+        } else {
+#pragma unroll
+          for (int g = 0; g < kGroups; ++g)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) sum += l[g][k] = exact(l[g][k]);
+        }
+      } else {
+        // No allowed id: all 0.  A NaN or +inf among them: all of them NaN.
+        const float nan = __int_as_float(0x7FFFFFFF);
+#pragma unroll
+        for (int g = 0; g < kGroups; ++g) {
+          const int i = i0 + g * kProbThreads * 4;
+          const uint32_t bits = !p.mask ? 15u : i < n ? mask[i >> 5] >> (i & 31) : 0u;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) l[g][k] = m == -INFINITY || !(bits >> k & 1u) ? 0.0f : nan;
+        }
+        sum = 1.0f;
+      }
+#pragma unroll
+      for (int s = 16; s > 0; s >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, s);
+      if (lane == 0) sm.warp_sum[warp] = sum;
+      sm.mask[phase ^ 1u][threadIdx.x] = next_word;
+      __syncthreads();
+      sum = of_warps(sm.warp_sum, [](float a, float b) { return a + b; });
+      tell(sm.second, &sm.told[1], rank, n_ctas, __float_as_uint(sum));
+      wait_for(p, sm, &sm.told[1], phase);
+      sum = 0.0f;
+      for (int c = 0; c < n_ctas; ++c) sum += __uint_as_float(sm.second[c]);
+      const float inv = __fdiv_rn(1.0f, sum);
+#pragma unroll
+      for (int g = 0; g < kGroups; ++g) {
+        const int i = i0 + g * kProbThreads * 4;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) l[g][k] *= inv;
+        store4<TO, kAsync>(out + i, n - i, l[g]);
+      }
     }
-  } else {
-    // No allowed id: all 0.  A NaN or +inf among them: all of them NaN.
-    const float nan = __int_as_float(0x7FFFFFFF);
-#pragma unroll
-    for (int g = 0; g < kGroups; ++g) {
-      const int v = v0 + g * kProbThreads * 4;
-      const uint32_t bits =
-          !p.mask ? 15u : v < end ? p.mask[row * p.mask_ld + (v >> 5)] >> (v & 31) : 0u;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) l[g][i] = m == -INFINITY || !(bits >> i & 1u) ? 0.0f : nan;
-    }
-    sum = 1.0f;
-  }
-#pragma unroll
-  for (int s = 16; s > 0; s >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, s);
-  if (lane == 0) sm.warp[warp] = sum;
-  __syncthreads();
-  sum = sm.warp[0];
-#pragma unroll
-  for (int w = 1; w < kProbWarps; ++w) sum += sm.warp[w];
-  tell(&sm.sum[rank], n_ctas, __float_as_uint(sum));
-  ptx::cluster_sync();
-  sum = 0.0f;
-  for (int c = 0; c < n_ctas; ++c) sum += sm.sum[c];
-  const float inv = __fdiv_rn(1.0f, sum);
-#pragma unroll
-  for (int g = 0; g < kGroups; ++g) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) l[g][i] *= inv;
-    store_probs<TO, kVec>(out, v0 + g * kProbThreads * 4, end, l[g]);
+    row = next;
+    temp = next_temp;
   }
 }
 
@@ -596,6 +674,7 @@ struct Device {
   bool known = false;
   fs_status status = FS_ERR_UNSUPPORTED;
   int sms = 0;
+  int* error_word = nullptr;
 };
 Device g_devices[kMaxDevices];
 
@@ -616,7 +695,11 @@ fs_status device_setup(const Device** out) {
       cudaGetLastError();
       return FS_ERR_CUDA;
     }
-    d.status = major == 10 && minor == 3 ? FS_OK : FS_ERR_UNSUPPORTED;
+    d.status = FS_ERR_UNSUPPORTED;
+    if (major == 10 && minor == 3) {
+      d.error_word = device_error_word();
+      d.status = d.error_word != nullptr ? FS_OK : FS_ERR_CUDA;
+    }
     d.known = true;
   }
   *out = &d;
@@ -629,41 +712,80 @@ uintptr_t element(int dtype) { return dtype == FS_F32 ? 4 : 2; }
 bool known(int dtype) { return dtype == FS_BF16 || dtype == FS_F32; }
 constexpr int64_t kMostV = INT_MAX - 65536;  // a segment's end fits 32 bits
 
-template <class T, class TO, bool kVec>
-cudaError_t launch_probs(ProbsParams p, cudaStream_t stream) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.blockDim = dim3(kProbThreads);
-  cfg.stream = stream;
-  // CTAs of a row's cluster and their threads' registers by V alone, so that a row's sum
-  // does not depend on what else is computed.  Up to 16 elements a thread more CTAs, which
-  // read and write a row sooner; then more elements.
-  int ctas = 1;
-  while (ctas < kMaxProbCluster && int64_t(ctas) * kProbThreads * 16 < p.V) ctas *= 2;
-  const int64_t per = ceil_div(ceil_div(p.V, ctas), kProbThreads * 4);
-  if (per > 16) {
-    cfg.gridDim = dim3(unsigned(p.N));
-    return cudaLaunchKernelEx(&cfg, long_probs_kernel<T, TO>, p);
-  }
-  p.part = int32_t(ceil_div(ceil_div(p.V, ctas), 4) * 4);
+template <class T, class TO, bool kAsync, int kGroups>
+cudaError_t launch_probs(ProbsParams p, int ctas, cudaStream_t stream) {
+  auto kernel = probs_kernel<T, TO, kAsync, kGroups>;
+  const size_t smem = kAsync ? size_t(p.part) * sizeof(T) : 0;
+  // How many clusters fit, once for each kernel, device and size of cluster.
+  static std::mutex mu;
+  static int fit[kMaxDevices][kMaxProbCluster + 1];
+  int dev = 0;
+  cudaError_t err = cudaGetDevice(&dev);
+  if (err != cudaSuccess) return err;
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeClusterDimension;
   attr.val.clusterDim.x = unsigned(ctas);
   attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-  cfg.gridDim = dim3(unsigned(p.N * ctas));
+  cudaLaunchConfig_t cfg = {};
+  cfg.blockDim = dim3(kProbThreads);
+  cfg.gridDim = dim3(unsigned(ctas));
+  cfg.dynamicSmemBytes = kAsync ? kGroups * 4 * kProbThreads * sizeof(T) : 0;
+  cfg.stream = stream;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return per <= 2    ? cudaLaunchKernelEx(&cfg, probs_kernel<T, TO, kVec, 2>, p)
-         : per <= 4  ? cudaLaunchKernelEx(&cfg, probs_kernel<T, TO, kVec, 4>, p)
-         : per <= 8  ? cudaLaunchKernelEx(&cfg, probs_kernel<T, TO, kVec, 8>, p)
-         : per <= 10 ? cudaLaunchKernelEx(&cfg, probs_kernel<T, TO, kVec, 10>, p)
-                     : cudaLaunchKernelEx(&cfg, probs_kernel<T, TO, kVec, 16>, p);
+  int clusters;
+  {
+    std::lock_guard<std::mutex> lock(mu);
+    int& f = fit[dev][ctas];
+    if (f == 0) {
+      if (kAsync)
+        err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                   int(cfg.dynamicSmemBytes));
+      if (err == cudaSuccess && ctas > 8)
+        err = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+      int n = 0;
+      if (err == cudaSuccess) err = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg);
+      if (err != cudaSuccess) return err;
+      if (n < 1) return cudaErrorInvalidConfiguration;
+      f = n;
+    }
+    clusters = f;
+  }
+  // No more than the rows need in as many turns.
+  const int64_t turns = ceil_div(p.N, clusters);
+  cfg.gridDim = dim3(unsigned(ceil_div(p.N, turns) * ctas));
+  cfg.dynamicSmemBytes = smem;
+  return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
 template <class T, class TO>
-cudaError_t launch_probs(const ProbsParams& p, cudaStream_t stream) {
-  const bool vec = aligned(p.logits, 4 * sizeof(T)) && p.ldl % 4 == 0 &&
-                   aligned(p.out, 4 * sizeof(TO)) && p.ldo % 4 == 0;
-  return vec ? launch_probs<T, TO, true>(p, stream) : launch_probs<T, TO, false>(p, stream);
+cudaError_t launch_probs(ProbsParams p, cudaStream_t stream) {
+  // CTAs of a row's cluster and their threads' registers by V alone, so that a row's sum
+  // does not depend on what else is computed: up to 16 elements a thread more CTAs, which
+  // read and write a row sooner; then more elements.
+  int ctas = 1;
+  while (ctas < 8 && int64_t(ctas) * kProbThreads * 16 < p.V) ctas *= 2;
+  if (p.V > 8 * kMaxPart) ctas = kMaxProbCluster;
+  const int64_t part = ceil_div(ceil_div(p.V, ctas), 32) * 32;
+  if (part > kMaxPart) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.blockDim = dim3(kProbThreads);
+    cfg.gridDim = dim3(unsigned(p.N));
+    cfg.stream = stream;
+    return cudaLaunchKernelEx(&cfg, long_probs_kernel<T, TO>, p);
+  }
+  p.part = int32_t(part);
+  const bool whole = aligned(p.logits, 16) && p.ldl * sizeof(T) % 16 == 0 && aligned(p.out, 16) &&
+                     p.ldo * sizeof(TO) % 16 == 0;
+  const int64_t per = ceil_div(part, kProbThreads * 4);
+  if (per <= 2)
+    return whole ? launch_probs<T, TO, true, 2>(p, ctas, stream)
+                 : launch_probs<T, TO, false, 2>(p, ctas, stream);
+  if (per <= 4)
+    return whole ? launch_probs<T, TO, true, 4>(p, ctas, stream)
+                 : launch_probs<T, TO, false, 4>(p, ctas, stream);
+  return whole ? launch_probs<T, TO, true, 8>(p, ctas, stream)
+               : launch_probs<T, TO, false, 8>(p, ctas, stream);
 }
 
 }  // namespace
@@ -700,6 +822,8 @@ extern "C" fs_status fs_probs(const fs_probs_args* args, void* stream_ptr) {
   p.ldo = a.N > 1 ? a.ldo : 0;
   p.N = int32_t(a.N);
   p.V = int32_t(a.V);
+  p.wait_limit_ns = kWaitLimitNs;
+  p.error_word = dev->error_word;
   cudaStream_t stream = static_cast<cudaStream_t>(stream_ptr);
   const cudaError_t err =
       a.dtype == FS_F32
