@@ -76,19 +76,22 @@ struct ProbsParams {
 
 // exp for a whole row in registers.  p = 2^(l c - K) / sum of the same for any K, so K is
 // the whole number nearest m c, c = log2(e) / T in two floats: then l c - K - n, n a whole
-// number too, is one rounding of a number of at most 1/2 (off by 2^-25), and 2^n goes into
-// the exponent.  10 operations; where m c is too large for that, Exp.
+// number too, is one rounding of a number of little over 1/2 (off by 2^-24), and 2^n goes into
+// the exponent.  8 operations; where m c is too large for that, Exp.
 struct FastExp {
-  float k, c_hi, c_lo;
+  static constexpr float kMagic = 0x1.8p23f;  // adding it rounds to a whole number, in the low bits
+  float at, c_hi, c_lo;                       // kMagic - K
   static __device__ __forceinline__ bool can(float m, float c_hi) { return fabsf(m * c_hi) < 0x1p22f; }
+  __device__ __forceinline__ FastExp(float m, float hi, float lo)
+      : at(kMagic - rintf(m * hi)), c_hi(hi), c_lo(lo) {}
   __device__ __forceinline__ float operator()(float l) const {
-    constexpr float kMagic = 0x1.8p23f;  // adding it rounds to a whole number, in the low bits
-    const float y = fmaf(l, c_hi, -k);
-    const float r = y + kMagic;
-    const float f = fmaf(l, c_lo, fmaf(l, c_hi, -(k + (r - kMagic))));
+    const float r = fmaf(l, c_hi, at);  // kMagic + n
+    const float f = fmaf(l, c_lo, fmaf(l, c_hi, at - r));
     float e;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(f));
-    return y < -126.0f ? 0.0f : __int_as_float(__float_as_int(e) + (__float_as_int(r) << 23));
+    // 0 below 2^-126 (off by up to a third of that right above it), of -infinity too, whose f is NaN.
+    return r < kMagic - 126.0f ? 0.0f
+                               : __int_as_float(__float_as_int(e) + __float_as_int(r) * (1 << 23));
   }
 };
 
@@ -133,11 +136,9 @@ __device__ __forceinline__ void store4(TO* out, int n, const float (&p)[4]) {
 }
 
 struct alignas(16) ProbsShared {
-  float warp_max[kProbWarps], warp_sum[kProbWarps];
-  int warp_at[kProbWarps];
-  // What the CTAs of a row's cluster tell one another: maxima; sums, or of a greedy row
-  // the ids.
-  uint32_t first[kMaxProbCluster], second[kMaxProbCluster];
+  // What the warps of a row's cluster tell one another: maxima; sums, or of a greedy row
+  // the ids.  Slots that no warp has hold what changes nothing.
+  uint32_t first[kMaxProbCluster * kProbWarps], second[kMaxProbCluster * kProbWarps];
   uint32_t mask[2][kMaxPart / 32];  // this row's and the next one's words
   uint64_t full;                    // the row's elements have arrived
   uint64_t told[2];                 // every CTA's word has
@@ -157,24 +158,35 @@ __device__ __forceinline__ void wait_for(const ProbsParams& p, ProbsShared& sm, 
     }
   }
 }
-// This CTA's word into slot `rank` of every CTA of the cluster, by stores that count on the
+// This warp's word into its slot in every CTA of the cluster, by stores that count on the
 // receiver's barrier.  (A cluster's barrier would also wait for the stores of the row before.)
 // A word of the next row cannot overtake: its sender has had this row's words from everyone.
 __device__ __forceinline__ void tell(uint32_t* slots, uint64_t* bar, int rank, int n_ctas,
                                      uint32_t v) {
-  if (threadIdx.x == 0) ptx::mbar_arrive_expect_tx(bar, uint32_t(n_ctas) * 4u);
-  if (int(threadIdx.x) < n_ctas)
+  const uint32_t lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) ptx::mbar_arrive_expect_tx(bar, uint32_t(n_ctas * kProbWarps) * 4u);
+  if (int(lane) < n_ctas)
     asm volatile(
         "st.async.shared::cluster.mbarrier::complete_tx::bytes.u32 [%0], %1, [%2];" ::"r"(
-            ptx::cluster_addr(slots + rank, threadIdx.x)),
-        "r"(v), "r"(ptx::cluster_addr(bar, threadIdx.x))
+            ptx::cluster_addr(slots + rank * kProbWarps + int(threadIdx.x >> 5), lane)),
+        "r"(v), "r"(ptx::cluster_addr(bar, lane))
         : "memory");
 }
+// All slots in one, in a fixed order; the whole warp.
 template <class Op>
-__device__ __forceinline__ float of_warps(const float (&v)[kProbWarps], Op op) {
-  float r = v[0];
+__device__ __forceinline__ float of_slots(const uint32_t* slots, int n_ctas, Op op) {
+  const int lane = int(threadIdx.x & 31);
+  const uint4* at = reinterpret_cast<const uint4*>(slots) + lane;
+  uint4 v = at[0];
+  float r = op(op(__uint_as_float(v.x), __uint_as_float(v.y)),
+               op(__uint_as_float(v.z), __uint_as_float(v.w)));
+  if (n_ctas > 8) {
+    v = at[32];
+    r = op(r, op(op(__uint_as_float(v.x), __uint_as_float(v.y)),
+                 op(__uint_as_float(v.z), __uint_as_float(v.w))));
+  }
 #pragma unroll
-  for (int w = 1; w < kProbWarps; ++w) r = op(r, v[w]);
+  for (int s = 16; s > 0; s >>= 1) r = op(r, __shfl_xor_sync(0xFFFFFFFFu, r, s));
   return r;
 }
 // `bytes` (a multiple of 16) from global to shared memory, arriving on `bar`.
@@ -203,12 +215,12 @@ __global__ void __launch_bounds__(kProbThreads, 2) probs_kernel(const ProbsParam
   asm("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(n_ctas_u));
   const int n_ctas = int(n_ctas_u);
   const int rank = int(ptx::cluster_ctarank());
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
   const int n_clusters = int(gridDim.x / n_ctas_u);
   const int begin = min(rank * p.part, p.V);
   const int n = min(p.part, p.V - begin);  // this CTA's elements
   constexpr int kWholeCopy = 16 / int(sizeof(T));
-  const int copied = kAsync ? n / kWholeCopy * kWholeCopy : 0;  // the rest is read directly
+  const int copied = kAsync ? n / kWholeCopy * kWholeCopy : 0;
   const int words = (n + 31) / 32;
   if (threadIdx.x == 0) {
     ptx::mbar_init(&sm.full, 1);
@@ -217,11 +229,26 @@ __global__ void __launch_bounds__(kProbThreads, 2) probs_kernel(const ProbsParam
     ptx::fence_barrier_init();
     sm.gave_up = 0u;
   }
+  if (threadIdx.x < kMaxProbCluster * kProbWarps) {
+    sm.first[threadIdx.x] = 0xFF800000u;  // -infinity
+    sm.second[threadIdx.x] = 0u;
+  }
   auto row_of = [&](int64_t row) { return static_cast<const T*>(p.logits) + row * p.ldl + begin; };
   auto mask_word = [&](int64_t row) {
     return int(threadIdx.x) < words ? p.mask[row * p.mask_ld + begin / 32 + threadIdx.x] : 0u;
   };
+  // The few elements behind the last whole 16 bytes come one by one, and behind them lies
+  // -infinity.
+  const int at_end = copied + int(threadIdx.x);
+  auto copy_end = [&](const T* x) {
+    if (kAsync && at_end < n) buffer[at_end] = x[at_end];
+  };
   int64_t row = blockIdx.x / n_ctas_u;
+  if (kAsync) {
+    for (int i = n + int(threadIdx.x); i < kGroups * 4 * kProbThreads; i += kProbThreads)
+      narrow(buffer + i, -INFINITY);
+    copy_end(row_of(row));
+  }
   if (p.mask) sm.mask[0][threadIdx.x] = mask_word(row);
   float temp = p.temperature ? p.temperature[row] : 1.0f;
   __syncthreads();
@@ -238,37 +265,48 @@ __global__ void __launch_bounds__(kProbThreads, 2) probs_kernel(const ProbsParam
     const uint32_t phase = uint32_t(turn & 1);
     if (copied > 0) wait_for(p, sm, &sm.full, phase);
     float l[kGroups][4];
-    float m = -INFINITY;
 #pragma unroll
     for (int g = 0; g < kGroups; ++g) {
       const int i = i0 + g * kProbThreads * 4;
-      if (i + 4 <= copied)
+      if constexpr (kAsync)
         load4<T, true>(buffer + i, 4, l[g]);
       else
-        load4<T, false>(x + i, n - i, l[g]);  // past a piece that is copied in part: from memory
-      if (p.mask) {
-        const uint32_t bits = i < n ? mask[i >> 5] >> (i & 31) : 0u;
+        load4<T, false>(x + i, n - i, l[g]);
+    }
+    if (p.mask) {
+#pragma unroll
+      for (int g = 0; g < kGroups; ++g) {
+        const int i = i0 + g * kProbThreads * 4;
+        const uint32_t bits = mask[i >> 5] >> (i & 31);
 #pragma unroll
         for (int k = 0; k < 4; ++k)
           if (!(bits >> k & 1u)) l[g][k] = -INFINITY;
       }
+    }
+    float m = -INFINITY;
+    if (greedy) {
 #pragma unroll
-      for (int k = 0; k < 4; ++k)  // of a number and NaN, fmaxf is the number
-        m = greedy ? fmaxf(m, l[g][k]) : max_nan(m, l[g][k]);
+      for (int g = 0; g < kGroups; ++g)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) m = fmaxf(m, l[g][k]);  // of a number and NaN the number
+    } else {
+#pragma unroll
+      for (int g = 0; g < kGroups; ++g)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) m = max_nan(m, l[g][k]);
     }
 #pragma unroll
     for (int s = 16; s > 0; s >>= 1) m = max_nan(m, __shfl_xor_sync(0xFFFFFFFFu, m, s));
-    if (lane == 0) sm.warp_max[warp] = m;
-    __syncthreads();  // and every thread has read the buffer
+    tell(sm.first, &sm.told[0], rank, n_ctas, __float_as_uint(m));
+    __syncthreads();  // every thread has read the buffer
     if (more && copied > 0 && threadIdx.x == 0)
       copy_async(buffer, row_of(next), uint32_t(copied) * sizeof(T), &sm.full);
+    if (more) copy_end(row_of(next));
     const uint32_t next_word = more && p.mask ? mask_word(next) : 0u;
     const float next_temp = more && p.temperature ? p.temperature[next] : 1.0f;
-    m = of_warps(sm.warp_max, max_nan);
-    tell(sm.first, &sm.told[0], rank, n_ctas, __float_as_uint(m));
+    Exp exact(0.0f, temp);
     wait_for(p, sm, &sm.told[0], phase);
-    for (int c = 0; c < n_ctas; ++c) m = max_nan(m, __uint_as_float(sm.first[c]));
-
+    m = of_slots(sm.first, n_ctas, max_nan);
     TO* out = static_cast<TO*>(p.out) + row * p.ldo + begin;
     if (greedy) {
       int at = INT_MAX;
@@ -279,15 +317,14 @@ __global__ void __launch_bounds__(kProbThreads, 2) probs_kernel(const ProbsParam
           for (int k = 3; k >= 0; --k)
             if (l[g][k] == m) at = begin + i0 + g * kProbThreads * 4 + k;
       }
-      at = __reduce_min_sync(0xFFFFFFFFu, at);
-      if (lane == 0) sm.warp_at[warp] = at;
+      at = INT_MAX - __reduce_min_sync(0xFFFFFFFFu, at);
       sm.mask[phase ^ 1u][threadIdx.x] = next_word;
-      __syncthreads();
-#pragma unroll
-      for (int w = 0; w < kProbWarps; ++w) at = min(at, sm.warp_at[w]);
       tell(sm.second, &sm.told[1], rank, n_ctas, uint32_t(at));
+      __syncthreads();
       wait_for(p, sm, &sm.told[1], phase);
-      for (int c = 0; c < n_ctas; ++c) at = min(at, int(sm.second[c]));
+      at = 0;
+      for (int c = lane; c < n_ctas * kProbWarps; c += 32) at = max(at, int(sm.second[c]));
+      at = INT_MAX - __reduce_max_sync(0xFFFFFFFFu, at);
 #pragma unroll
       for (int g = 0; g < kGroups; ++g) {
         const int i = i0 + g * kProbThreads * 4, v = begin + i;
@@ -298,9 +335,9 @@ __global__ void __launch_bounds__(kProbThreads, 2) probs_kernel(const ProbsParam
     } else {
       float sum = 0.0f;
       if (m > -INFINITY && m < INFINITY) {
-        const Exp exact(m, temp);
+        exact.m = m;
         if (FastExp::can(m, exact.c_hi)) {
-          const FastExp e{rintf(m * exact.c_hi), exact.c_hi, exact.c_lo};
+          const FastExp e(m, exact.c_hi, exact.c_lo);
 #pragma unroll
           for (int g = 0; g < kGroups; ++g)
 #pragma unroll
@@ -317,7 +354,7 @@ __global__ void __launch_bounds__(kProbThreads, 2) probs_kernel(const ProbsParam
 #pragma unroll
         for (int g = 0; g < kGroups; ++g) {
           const int i = i0 + g * kProbThreads * 4;
-          const uint32_t bits = !p.mask ? 15u : i < n ? mask[i >> 5] >> (i & 31) : 0u;
+          const uint32_t bits = !p.mask ? 15u : mask[i >> 5] >> (i & 31);
 #pragma unroll
           for (int k = 0; k < 4; ++k) l[g][k] = m == -INFINITY || !(bits >> k & 1u) ? 0.0f : nan;
         }
@@ -325,14 +362,11 @@ __global__ void __launch_bounds__(kProbThreads, 2) probs_kernel(const ProbsParam
       }
 #pragma unroll
       for (int s = 16; s > 0; s >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, s);
-      if (lane == 0) sm.warp_sum[warp] = sum;
       sm.mask[phase ^ 1u][threadIdx.x] = next_word;
-      __syncthreads();
-      sum = of_warps(sm.warp_sum, [](float a, float b) { return a + b; });
       tell(sm.second, &sm.told[1], rank, n_ctas, __float_as_uint(sum));
+      __syncthreads();
       wait_for(p, sm, &sm.told[1], phase);
-      sum = 0.0f;
-      for (int c = 0; c < n_ctas; ++c) sum += __uint_as_float(sm.second[c]);
+      sum = of_slots(sm.second, n_ctas, [](float a, float b) { return a + b; });
       const float inv = __fdiv_rn(1.0f, sum);
 #pragma unroll
       for (int g = 0; g < kGroups; ++g) {
@@ -715,7 +749,6 @@ constexpr int64_t kMostV = INT_MAX - 65536;  // a segment's end fits 32 bits
 template <class T, class TO, bool kAsync, int kGroups>
 cudaError_t launch_probs(ProbsParams p, int ctas, cudaStream_t stream) {
   auto kernel = probs_kernel<T, TO, kAsync, kGroups>;
-  const size_t smem = kAsync ? size_t(p.part) * sizeof(T) : 0;
   // How many clusters fit, once for each kernel, device and size of cluster.
   static std::mutex mu;
   static int fit[kMaxDevices][kMaxProbCluster + 1];
@@ -754,7 +787,6 @@ cudaError_t launch_probs(ProbsParams p, int ctas, cudaStream_t stream) {
   // No more than the rows need in as many turns.
   const int64_t turns = ceil_div(p.N, clusters);
   cfg.gridDim = dim3(unsigned(ceil_div(p.N, turns) * ctas));
-  cfg.dynamicSmemBytes = smem;
   return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
@@ -778,12 +810,18 @@ cudaError_t launch_probs(ProbsParams p, cudaStream_t stream) {
   const bool whole = aligned(p.logits, 16) && p.ldl * sizeof(T) % 16 == 0 && aligned(p.out, 16) &&
                      p.ldo * sizeof(TO) % 16 == 0;
   const int64_t per = ceil_div(part, kProbThreads * 4);
+  if (per <= 1)
+    return whole ? launch_probs<T, TO, true, 1>(p, ctas, stream)
+                 : launch_probs<T, TO, false, 1>(p, ctas, stream);
   if (per <= 2)
     return whole ? launch_probs<T, TO, true, 2>(p, ctas, stream)
                  : launch_probs<T, TO, false, 2>(p, ctas, stream);
   if (per <= 4)
     return whole ? launch_probs<T, TO, true, 4>(p, ctas, stream)
                  : launch_probs<T, TO, false, 4>(p, ctas, stream);
+  if (per <= 5)
+    return whole ? launch_probs<T, TO, true, 5>(p, ctas, stream)
+                 : launch_probs<T, TO, false, 5>(p, ctas, stream);
   return whole ? launch_probs<T, TO, true, 8>(p, ctas, stream)
                : launch_probs<T, TO, false, 8>(p, ctas, stream);
 }
