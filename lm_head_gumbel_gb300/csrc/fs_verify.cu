@@ -455,7 +455,7 @@ constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kSegment = 1024;      // elements of a segment, doubled until there are
 constexpr int kMaxSegments = 1024;  // at most so many
-constexpr int kMaxCluster = 8;
+constexpr int kMaxCluster = 16;     // more than 8 need the kernel's leave
 
 struct VerifyParams {
   const void* p;
@@ -468,25 +468,77 @@ struct VerifyParams {
   int64_t* accepted;
   int32_t K, V;
   int32_t segment, n_segments;
+  uint64_t wait_limit_ns;
+  int* error_word;
 };
 
-// A sum in two floats: 2^-46 or so of the total, whatever the order.
+// A sum in two floats, the second at most half the last place of the first: to 2^-46 or so
+// of the total.  (64-bit arithmetic is slow on this GPU: a scan by 16 warps in it took as
+// long as reading the row.)
 struct Sum {
   float hi = 0.0f, lo = 0.0f;
+  // A term; `lo` is only gathered, for normal().
   __device__ __forceinline__ void add(float w) {
     const float s = hi + w;
     const float b = s - hi;
     lo += (hi - (s - b)) + (w - b);
     hi = s;
   }
-  __device__ __forceinline__ double total() const { return double(hi) + double(lo); }
+  __device__ __forceinline__ Sum normal() const {
+    Sum r;
+    r.hi = hi + lo;
+    r.lo = lo - (r.hi - hi);
+    return r;
+  }
+  __device__ __forceinline__ Sum operator+(const Sum& o) const {
+    Sum r = *this;
+    r.add(o.hi);
+    r.lo += o.lo;
+    return r.normal();
+  }
+  __device__ __forceinline__ bool operator>(const Sum& o) const {
+    return hi > o.hi || (hi == o.hi && lo > o.lo);
+  }
+  __device__ __forceinline__ Sum operator*(float u) const {
+    Sum r;
+    r.hi = hi * u;
+    r.lo = fmaf(lo, u, fmaf(hi, u, -r.hi));
+    return r.normal();
+  }
 };
-
-__device__ __forceinline__ double shfl_xor(double v, int s) {
-  return __shfl_xor_sync(0xFFFFFFFFu, v, s);
+__device__ __forceinline__ Sum shfl_xor(const Sum& v, int d) {
+  Sum r;
+  r.hi = __shfl_xor_sync(0xFFFFFFFFu, v.hi, d);
+  r.lo = __shfl_xor_sync(0xFFFFFFFFu, v.lo, d);
+  return r;
+}
+// The sum of the lanes up to and with this one.
+__device__ __forceinline__ Sum scan(Sum v, int lane) {
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    Sum o;
+    o.hi = __shfl_up_sync(0xFFFFFFFFu, v.hi, d);
+    o.lo = __shfl_up_sync(0xFFFFFFFFu, v.lo, d);
+    if (lane >= d) v = o + v;
+  }
+  return v;
+}
+// The sum before it, given that.
+__device__ __forceinline__ Sum exclusive(const Sum& inclusive, int lane) {
+  Sum r;
+  r.hi = __shfl_up_sync(0xFFFFFFFFu, inclusive.hi, 1);
+  r.lo = __shfl_up_sync(0xFFFFFFFFu, inclusive.lo, 1);
+  if (lane == 0) r = Sum();
+  return r;
 }
 
 enum Mode { kTarget = 0, kResidual = 1, kWithout = 2 };
+
+// Negative, infinite and NaN weights are 0.
+__device__ __forceinline__ float weight(float w) {
+  w = fmaxf(w, 0.0f);
+  return w < INFINITY ? w : 0.0f;
+}
 
 // The weights that a sequence's last token is drawn with.
 template <class T>
@@ -494,41 +546,99 @@ struct Weights {
   const T* p;
   const T* q;
   int mode, without;
-  __device__ __forceinline__ float of(float pv, float qv, int v) const {
-    const float w = mode == kResidual ? pv - qv : pv;
-    // Negative, infinite and NaN weights are 0.
-    return w > 0.0f && w < INFINITY && !(mode == kWithout && v == without) ? w : 0.0f;
-  }
   __device__ __forceinline__ float at(int v) const {
-    return of(wide(p[v]), mode == kResidual ? wide(q[v]) : 0.0f, v);
+    if (mode == kWithout && v == without) return 0.0f;
+    return weight(mode == kResidual ? wide(p[v]) - wide(q[v]) : wide(p[v]));
   }
 };
 
-// A warp's sum of a segment.  Every lane takes runs of 4 (fp32) or 8 (bf16) elements,
-// 32 runs side by side.
 template <class T>
-__device__ __forceinline__ double segment_sum(const Weights<T>& w, int begin, int end, int lane) {
-  constexpr int kRun = 16 / int(sizeof(T));
-  Sum s;
-  for (int v0 = begin + lane * kRun; v0 < end; v0 += 32 * kRun) {
+__device__ __forceinline__ void unpack(const uint4& v, float (&x)[16 / sizeof(T)]) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-    for (int i = 0; i < kRun; ++i)
-      if (v0 + i < end) s.add(w.at(v0 + i));
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (sizeof(T) == 2) {
+      x[2 * i] = __uint_as_float(w[i] << 16);
+      x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    } else {
+      x[i] = __uint_as_float(w[i]);
+    }
   }
-  double t = s.total();
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) t += shfl_xor(t, d);
-  return t;
 }
 
-struct Shared {
-  double sums[kMaxSegments];
-  double scan[kWarps];
-  double before;  // sum of the segments before the chosen one
-  double target;
+// A warp's sum of a segment.  Every lane takes runs of 16 bytes, 32 runs side by side, in
+// the same order however they are read: 16 bytes at a time where rows allow it, four runs of
+// each row in flight.
+template <class T, bool kTwo>
+__device__ __forceinline__ Sum whole_segment(const T* p, const T* q, int segment, int lane) {
+  constexpr int kRun = 16 / int(sizeof(T));
+  const uint4* pv = reinterpret_cast<const uint4*>(p) + lane;
+  const uint4* qv = reinterpret_cast<const uint4*>(q) + lane;
+  Sum s;
+  for (int j = 0; j < segment / (32 * kRun); j += 4) {
+    uint4 a[4], b[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) a[i] = __ldcs(pv + 32 * (j + i));
+    if (kTwo) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) b[i] = __ldcs(qv + 32 * (j + i));
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float x[kRun], y[kRun];
+      unpack<T>(a[i], x);
+      if (kTwo) unpack<T>(b[i], y);
+#pragma unroll
+      for (int k = 0; k < kRun; ++k) s.add(weight(kTwo ? x[k] - y[k] : x[k]));
+    }
+  }
+  return s;
+}
+template <class T>
+__device__ __forceinline__ Sum segment_sum(const Weights<T>& w, int begin, int length, int segment,
+                                           bool vec, int lane) {
+  constexpr int kRun = 16 / int(sizeof(T));
+  Sum s;
+  if (vec && length == segment &&
+      !(w.mode == kWithout && w.without >= begin && w.without - begin < length)) {
+    s = w.mode == kResidual ? whole_segment<T, true>(w.p + begin, w.q + begin, segment, lane)
+                            : whole_segment<T, false>(w.p + begin, nullptr, segment, lane);
+  } else {
+    for (int v0 = lane * kRun; v0 < length; v0 += 32 * kRun) {
+#pragma unroll
+      for (int i = 0; i < kRun; ++i)
+        if (v0 + i < length) s.add(w.at(begin + v0 + i));
+    }
+  }
+  s = s.normal();
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) s = s + shfl_xor(s, d);
+  return s;
+}
+
+struct alignas(16) Shared {
+  Sum sums[kMaxSegments];
+  Sum warps[kWarps];
+  Sum before;  // sum of the segments before the chosen one
+  Sum target;
+  uint64_t arrived;  // the segments' sums have
   int accepted, mode, without;
-  int segment, first, last;
+  int segment, first, last, found;
 };
+
+// The segments' sums are there, or the wait's limit has passed: then the error word says so.
+__device__ __forceinline__ void wait_arrived(const VerifyParams& a, Shared& sm) {
+  if (!ptx::mbar_try_wait(&sm.arrived, 0)) {
+    const uint64_t t0 = ptx::global_timer_ns();
+    while (!ptx::mbar_try_wait(&sm.arrived, 0)) {
+      if (ptx::global_timer_ns() - t0 > a.wait_limit_ns) {
+        atomicOr(a.error_word, kErrWaitTimeout);
+        break;
+      }
+    }
+  }
+  __syncwarp();
+}
 
 // How many drafts pass, and what the next token is drawn from.  One warp.
 template <class T>
@@ -542,10 +652,10 @@ __device__ __forceinline__ void accept(const VerifyParams& a, int64_t b, Shared&
     int x32 = -1;
     if (i < a.K) {
       const int64_t x = a.ids[b * a.ld_ids + i];
+      const float u = a.u[b * a.ldu + i];
       none = x < 0;
       if (x >= 0 && x < a.V) {
         x32 = int(x);
-        const float u = a.u[b * a.ldu + i];
         const float uc = u > 0.0f ? fminf(u, 0x1.fffffep-1f) : 0.0f;
         const float px = wide(static_cast<const T*>(a.p)[b * a.p_seq + i * a.p_pos + x]);
         const float qx =
@@ -574,36 +684,35 @@ __device__ __forceinline__ void accept(const VerifyParams& a, int64_t b, Shared&
 __device__ __forceinline__ bool find_segment(const VerifyParams& a, float u, Shared& sm,
                                              int lane) {
   const int per = (a.n_segments + 31) / 32;
-  const int s0 = lane * per, s1 = min(s0 + per, a.n_segments);
-  double own = 0.0;
-  for (int s = s0; s < s1; ++s) own += sm.sums[s];
-  double incl = own;
-#pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const double o = __shfl_up_sync(0xFFFFFFFFu, incl, d);
-    if (lane >= d) incl += o;
-  }
-  const double total = __shfl_sync(0xFFFFFFFFu, incl, 31);
-  const uint32_t some = __ballot_sync(0xFFFFFFFFu, own > 0.0);
+  const int s0 = min(lane * per, a.n_segments), s1 = min(s0 + per, a.n_segments);
+  Sum own;
+  for (int s = s0; s < s1; ++s) own = own + sm.sums[s];
+  const Sum upto = scan(own, lane), ahead = exclusive(upto, lane);
+  Sum total;
+  total.hi = __shfl_sync(0xFFFFFFFFu, upto.hi, 31);
+  total.lo = __shfl_sync(0xFFFFFFFFu, upto.lo, 31);
+  const uint32_t some = __ballot_sync(0xFFFFFFFFu, own.hi > 0.0f);
   if (some == 0u) return false;
-  const float uc = u > 0.0f ? fminf(u, 0x1.fffffep-1f) : 0.0f;
-  const double target = double(uc) * total;
-  const uint32_t past = __ballot_sync(0xFFFFFFFFu, own > 0.0 && incl > target);
+  const Sum target = total * (u > 0.0f ? fminf(u, 0x1.fffffep-1f) : 0.0f);
+  const uint32_t past = __ballot_sync(0xFFFFFFFFu, own.hi > 0.0f && upto > target);
   // Past every sum (by their rounding): the last one that is not 0.
   const int at = past != 0u ? __ffs(past) - 1 : 31 - __clz(some);
   if (lane == at) {
-    double before = incl - own, run = before;
+    Sum before = ahead, run = ahead;
     int chosen = -1;
     for (int s = s0; s < s1; ++s) {
-      if (!(sm.sums[s] > 0.0)) continue;
+      const Sum x = sm.sums[s];
+      if (!(x.hi > 0.0f)) continue;
       before = run;
-      run += sm.sums[s];
+      run = run + x;
       chosen = s;
       if (run > target) break;
     }
     sm.segment = chosen;
     sm.before = before;
     sm.target = target;
+    sm.first = INT_MAX;
+    sm.last = -1;
   }
   return true;
 }
@@ -615,85 +724,111 @@ __device__ __forceinline__ int find_element(const VerifyParams& a, const Weights
   const int per = a.segment / kThreads;
   const int v0 = sm.segment * a.segment + int(threadIdx.x) * per;
   const int v1 = v0 < a.V ? v0 + min(per, a.V - v0) : v0;
-  double own = 0.0;
-  for (int v = v0; v < v1; ++v) own += double(w.at(v));
-  double incl = own;
-#pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const double o = __shfl_up_sync(0xFFFFFFFFu, incl, d);
-    if (lane >= d) incl += o;
-  }
-  if (lane == 31) sm.scan[warp] = incl;
-  if (threadIdx.x == 0) sm.first = INT_MAX, sm.last = -1;
-  __syncthreads();
-  double run = sm.before;
-  for (int i = 0; i < warp; ++i) run += sm.scan[i];
-  run += incl - own;
+  Sum own;
+  int last = -1;
   for (int v = v0; v < v1; ++v) {
     const float x = w.at(v);
-    if (!(x > 0.0f)) continue;
-    run += double(x);
-    atomicMax(&sm.last, v);
-    if (run > sm.target) {
-      atomicMin(&sm.first, v);
-      break;
-    }
+    own.add(x);
+    if (x > 0.0f) last = v;
   }
+  own = own.normal();
+  const Sum upto = scan(own, lane);
+  if (lane == 31) sm.warps[warp] = upto;
+  __syncthreads();
+  const Sum warps = scan(lane < kWarps ? sm.warps[lane] : Sum(), lane);
+  Sum ahead;  // of the warps before this one
+  ahead.hi = __shfl_sync(0xFFFFFFFFu, warps.hi, max(warp - 1, 0));
+  ahead.lo = __shfl_sync(0xFFFFFFFFu, warps.lo, max(warp - 1, 0));
+  if (warp == 0) ahead = Sum();
+  ahead = sm.before + ahead;
+  // Only lanes where the target may be passed look again; the lowest counts.
+  const uint32_t past = __ballot_sync(0xFFFFFFFFu, last >= 0 && ahead + upto > sm.target);
+  Sum run = ahead + exclusive(upto, lane);
+  if (past != 0u && lane == __ffs(past) - 1) {
+    int first = last;
+    for (int v = v0; v < v1; ++v) {
+      const float x = w.at(v);
+      if (!(x > 0.0f)) continue;
+      Sum term;
+      term.hi = x;
+      run = run + term;
+      if (run > sm.target) {
+        first = v;
+        break;
+      }
+    }
+    atomicMin(&sm.first, first);
+  }
+  last = __reduce_max_sync(0xFFFFFFFFu, last);
+  if (lane == 0) atomicMax(&sm.last, last);
   __syncthreads();
   return sm.first != INT_MAX ? sm.first : sm.last;
 }
 
+// A sequence to a cluster of CTAs.  Each finds out which drafts pass (that is 2 dependent reads,
+// and less than telling one another); the row's segments go around their warps; the first CTA
+// gathers the segments' sums, finds the segment that u falls into and sums that again, element
+// by element.  Bound: memory for large batches, for small ones the chain of those reads.
 template <class T>
-__global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyParams a) {
+__global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyParams a) {
   __shared__ Shared sm;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   uint32_t n_ctas;
   asm("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(n_ctas));
   const int rank = int(ptx::cluster_ctarank());
   const int64_t b = blockIdx.x / n_ctas;
+  if (threadIdx.x == 0) {
+    ptx::mbar_init(&sm.arrived, 1);
+    ptx::fence_barrier_init();
+    if (rank == 0) ptx::mbar_arrive_expect_tx(&sm.arrived, uint32_t(a.n_segments) * 8u);
+  }
+  ptx::cluster_arrive();
   if (warp == 0) accept<T>(a, b, sm, lane);
+  const float u = a.u[b * a.ldu + a.K];
   __syncthreads();
-  // Every CTA of the cluster has started before another one writes its memory.
-  ptx::cluster_sync();
   const int n = sm.accepted;
   Weights<T> w;
   w.p = static_cast<const T*>(a.p) + b * a.p_seq + n * a.p_pos;
   w.mode = sm.mode;
   w.without = sm.without;
   w.q = w.mode == kResidual ? static_cast<const T*>(a.q) + b * a.q_seq + n * a.q_pos : nullptr;
-  const uint32_t sums0 = ptx::cluster_addr(sm.sums, 0);
+  const bool vec =
+      ((reinterpret_cast<uintptr_t>(w.p) | reinterpret_cast<uintptr_t>(w.q)) & 15) == 0;
+  ptx::cluster_wait();  // the first CTA's barrier is there
+  const uint32_t sums0 = ptx::cluster_addr(sm.sums, 0), arrived0 = ptx::cluster_addr(&sm.arrived, 0);
   for (int s = rank * kWarps + warp; s < a.n_segments; s += int(n_ctas) * kWarps) {
     const int begin = s * a.segment;
-    const double t = segment_sum(w, begin, begin + min(a.segment, a.V - begin), lane);
+    const Sum t = segment_sum(w, begin, min(a.segment, a.V - begin), a.segment, vec, lane);
     if (lane == 0)
-      asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(sums0 + uint32_t(s) * 8u), "d"(t)
-                   : "memory");
+      asm volatile(
+          "st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%1, %2}, [%3];" ::"r"(
+              sums0 + uint32_t(s) * 8u),
+          "f"(t.hi), "f"(t.lo), "r"(arrived0)
+          : "memory");
   }
-  ptx::cluster_sync();
   if (rank != 0) return;
-  const float u = a.u[b * a.ldu + a.K];
-  __shared__ int found;
   if (warp == 0) {
+    wait_arrived(a, sm);
     const bool some = find_segment(a, u, sm, lane);
-    if (lane == 0) found = some;
+    if (lane == 0) sm.found = some;
   }
   __syncthreads();
-  if (!found && w.mode != kTarget) {
+  if (!sm.found && w.mode != kTarget) {
     // Nothing is left of p after a rejection: the draw is from p.
     w.mode = kTarget;
     for (int s = warp; s < a.n_segments; s += kWarps) {
       const int begin = s * a.segment;
-      const double t = segment_sum(w, begin, begin + min(a.segment, a.V - begin), lane);
+      const Sum t = segment_sum(w, begin, min(a.segment, a.V - begin), a.segment, vec, lane);
       if (lane == 0) sm.sums[s] = t;
     }
     __syncthreads();
     if (warp == 0) {
       const bool some = find_segment(a, u, sm, lane);
-      if (lane == 0) found = some;
+      if (lane == 0) sm.found = some;
     }
     __syncthreads();
   }
-  const int drawn = found ? find_element(a, w, sm) : -1;
+  const int drawn = sm.found ? find_element(a, w, sm) : -1;
   for (int i = threadIdx.x; i <= a.K; i += kThreads)
     a.out_ids[b * a.ld_out + i] = i < n ? a.ids[b * a.ld_ids + i] : i == n ? int64_t(drawn) : -1;
   if (threadIdx.x == 0 && a.accepted) a.accepted[b] = n;
@@ -732,7 +867,14 @@ fs_status device_setup(const Device** out) {
     d.status = FS_ERR_UNSUPPORTED;
     if (major == 10 && minor == 3) {
       d.error_word = device_error_word();
-      d.status = d.error_word != nullptr ? FS_OK : FS_ERR_CUDA;
+      const bool ok =
+          d.error_word != nullptr &&
+          cudaFuncSetAttribute(verify_kernel<float>,
+                               cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess &&
+          cudaFuncSetAttribute(verify_kernel<__nv_bfloat16>,
+                               cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess;
+      cudaGetLastError();
+      d.status = ok ? FS_OK : FS_ERR_CUDA;
     }
     d.known = true;
   }
@@ -913,10 +1055,12 @@ extern "C" fs_status fs_verify(const fs_verify_args* args, void* stream_ptr) {
   while (ceil_div(a.V, segment) > kMaxSegments) segment *= 2;
   p.segment = int32_t(segment);
   p.n_segments = int32_t(ceil_div(a.V, segment));
-  // A sequence's row over as many CTAs as leave every SM at most two.
+  p.wait_limit_ns = kWaitLimitNs;
+  p.error_word = dev->error_word;
+  // A sequence's row over as many CTAs as fit beside the others', a segment a warp at most.
   int ctas = 1;
-  while (ctas < kMaxCluster && a.B * ctas * 2 <= 2 * dev->sms && ctas * kWarps < p.n_segments)
-    ctas *= 2;
+  while (ctas < 8 && a.B * ctas * 2 <= 4 * 2 * dev->sms && ctas * kWarps < p.n_segments) ctas *= 2;
+  if (a.B <= 9 && 8 * kWarps < p.n_segments) ctas = 16;
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeClusterDimension;
   attr.val.clusterDim.x = unsigned(ctas);
