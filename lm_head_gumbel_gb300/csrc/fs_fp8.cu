@@ -303,21 +303,27 @@ constexpr int kBM = 128;
 constexpr int kBK = 128;          // k slice: 128 e4m3 = one 128-byte swizzle row
 constexpr int kUK = 32;           // k of one MMA
 constexpr int kMaxStages = 8;
-constexpr uint32_t kRingBytes = 176u * 1024u;
-constexpr uint32_t kBoxBytes = 4096;  // a warp's 32 rows x 128 bytes of output
 constexpr uint32_t kARead = kBM * kBK;  // bytes of A an MMA reads, whatever the box holds
 constexpr uint32_t kBarrierBytes = 256;
 // The scales of some slices: of A's 128 rows, times W's of either half's columns.
 constexpr int kGroups = 2;
-constexpr int kGroupSlices = 8;
+constexpr int kGroupSlices = 16;
 struct ScaleGroup {
   float product[2][kGroupSlices][kBM];
 };
-constexpr uint32_t kBoxesAt = kRingBytes;
-constexpr uint32_t kScalesAt = kBoxesAt + kEpiWarps * kBoxBytes;
-constexpr uint32_t kBarriersAt = kScalesAt + kGroups * uint32_t(sizeof(ScaleGroup));
-constexpr size_t kSmemBytes = 1024 /* alignment slack */ + kBarriersAt + kBarrierBytes;
-static_assert(kSmemBytes <= 227 * 1024 && kScalesAt % 16 == 0 && kBarriersAt % 8 == 0, "layout");
+// Shared memory.  CTA pairs: 4 stages of 32 KB do as well as 6, and a second box lets a warp
+// fill one while the other is stored.  Single CTAs: as much as fits, 3 to 4 stages.
+constexpr uint32_t kBoxBytes = 4096;  // a warp's 32 rows x 128 bytes of output
+template <bool kPair>
+struct Layout {
+  static constexpr uint32_t kRing = (kPair ? 128u : 160u) * 1024u;
+  static constexpr int kBoxes = kPair ? 2 : 1;
+  static constexpr uint32_t kBoxesAt = kRing;
+  static constexpr uint32_t kScalesAt = kBoxesAt + kEpiWarps * kBoxes * kBoxBytes;
+  static constexpr uint32_t kBarriersAt = kScalesAt + kGroups * uint32_t(sizeof(ScaleGroup));
+  static constexpr size_t kBytes = 1024 /* alignment slack */ + kBarriersAt + kBarrierBytes;
+  static_assert(kBytes <= 227 * 1024 && kScalesAt % 16 == 0 && kBarriersAt % 8 == 0, "layout");
+};
 
 template <int kN>
 __host__ __device__ constexpr int accumulators() {
@@ -334,7 +340,7 @@ template <int kN, bool kPair>
 __host__ __device__ constexpr uint32_t ring_stages(uint32_t a_bytes) {
   const uint32_t stage = a_bytes + (kPair ? kN / 2 : kN) * kBK;
   const uint32_t past = kARead > stage ? kARead - stage : 0;
-  const uint32_t n = (kRingBytes - past) / stage;
+  const uint32_t n = (Layout<kPair>::kRing - past) / stage;
   return n < kMaxStages ? n : kMaxStages;
 }
 
@@ -376,14 +382,18 @@ struct Box {
 // traffic's time; 300 cycles a slice at d = 4096).  TMA stores take them out; columns
 // that it cannot write, behind the last whole 16 bytes or of rows off 16-byte boundaries,
 // go row by row.
-template <int kCols, bool kF32>
-__device__ __forceinline__ void store_sums(const Plan& s, const void* tmap, uint8_t* box, int lane,
+template <int kCols, bool kF32, int kBoxes>
+__device__ __forceinline__ void store_sums(const Plan& s, const void* tmap, uint8_t* boxes, int lane,
                                            const float (&sum)[kCols], int row0, int col0) {
   using B = Box<kCols, kF32>;
 #pragma unroll
   for (int part = 0; part < kCols / B::kWidth; ++part) {
     const int x = col0 + part * B::kWidth;
-    vocab::box_begin(lane);
+    uint8_t* box = boxes + part % kBoxes * kBoxBytes;
+    // The box's last store has been read (kBoxes - 1 later ones may not).
+    if (lane == 0)
+      asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(kBoxes - 1) : "memory");
+    __syncwarp();
 #pragma unroll
     for (int c = 0; c < B::kPitch / 16; ++c) {
       const float* v = sum + part * B::kWidth + c * (16 / B::kSize);
@@ -398,9 +408,9 @@ __device__ __forceinline__ void store_sums(const Plan& s, const void* tmap, uint
     }
     ptx::fence_async_smem();
     __syncwarp();
-    if (lane == 0 && x < s.whole_v) {
-      ptx::tma_store_2d(tmap, box, x, row0);
-      ptx::bulk_commit();
+    if (lane == 0) {
+      if (x < s.whole_v) ptx::tma_store_2d(tmap, box, x, row0);
+      ptx::bulk_commit();  // (perhaps an empty group: a box is always so many groups ago)
     }
     const int from = max(x, s.whole_v), to = min(x + B::kWidth, s.V);
     if (from < to) {
@@ -436,6 +446,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     matmul_kernel(const __grid_constant__ CUtensorMap tmap_a,
                   const __grid_constant__ CUtensorMap tmap_b,
                   const __grid_constant__ CUtensorMap tmap_o, const __grid_constant__ Plan s) {
+  using L = Layout<kPair>;
   constexpr int kCtas = kPair ? 2 : 1;
   constexpr int kAcc = accumulators<kN>();
   constexpr uint32_t kTmemCols = kAcc * kN;
@@ -448,7 +459,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint64_t* full_bar = reinterpret_cast<uint64_t*>(smem + kBarriersAt);
+  uint64_t* full_bar = reinterpret_cast<uint64_t*>(smem + L::kBarriersAt);
   uint64_t* empty_bar = full_bar + kMaxStages;
   uint64_t* tfull_bar = empty_bar + kMaxStages;
   uint64_t* tempty_bar = tfull_bar + 4;  // of accumulator a, part h: [a * kParts + h]
@@ -459,7 +470,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile uint32_t* abort_flag = tmem_holder + 1;
   static_assert((2 * kMaxStages + 9 + 2 * kGroups) * 8 + 8 <= kBarrierBytes,
                 "barriers, tensor-memory address, flag");
-  ScaleGroup* groups = reinterpret_cast<ScaleGroup*>(smem + kScalesAt);
+  ScaleGroup* groups = reinterpret_cast<ScaleGroup*>(smem + L::kScalesAt);
 
   // The same in all lanes, which the compiler cannot see: addresses that depend on it then
   // stay in uniform registers, as tensor-memory loads take them.
@@ -781,7 +792,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             wait(sfull0 + 8u * group, group_phase);
             scale_at = scales0 + group * uint32_t(sizeof(ScaleGroup));
           }
-          scale_next = ptx::ld_shared_f32(scale_at);
         }
         ptx::tmem_wait_ld();
 #pragma unroll
@@ -789,6 +799,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           add(c - 2, scale);
           ptx::tmem_ld_32x32b_x32(taddr + uint32_t(c * 32), r[c & 1]);
         }
+        if constexpr (decltype(more)::value) scale_next = ptx::ld_shared_f32(scale_at);
         if (kChunks > 2) ptx::tmem_wait_ld();
         ptx::tc_fence_before();
         arrive(tempty0 + 8u * kParts * acc);
@@ -816,11 +827,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       float sum[kCols];
 #pragma unroll
       for (int i = 0; i < kCols / 2; ++i) ptx::unpack2(sums[i], sum[2 * i], sum[2 * i + 1]);
-      uint8_t* box = smem + kBoxesAt + (warp - kFirstSum) * kBoxBytes;
+      uint8_t* box = smem + L::kBoxesAt + (warp - kFirstSum) * (L::kBoxes * kBoxBytes);
       if (s.out_f32)
-        store_sums<kCols, true>(s, &tmap_o, box, lane, sum, row0, col0);
+        store_sums<kCols, true, L::kBoxes>(s, &tmap_o, box, lane, sum, row0, col0);
       else
-        store_sums<kCols, false>(s, &tmap_o, box, lane, sum, row0, col0);
+        store_sums<kCols, false, L::kBoxes>(s, &tmap_o, box, lane, sum, row0, col0);
     }
     if (lane == 0) ptx::bulk_wait();
   }
@@ -870,7 +881,7 @@ bool known(int dtype) { return dtype == FS_BF16 || dtype == FS_F32; }
 template <int kN, bool kPair>
 bool prepare_kernel(int sms, int* pairs) {
   auto k = matmul_kernel<kN, kPair>;
-  if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kSmemBytes)) !=
+  if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, int(Layout<kPair>::kBytes)) !=
       cudaSuccess)
     return false;
   if (!kPair) return true;
@@ -881,7 +892,7 @@ bool prepare_kernel(int sms, int* pairs) {
   cudaLaunchConfig_t cfg = {};
   cfg.blockDim = dim3(kThreads, 1, 1);
   cfg.gridDim = dim3(unsigned(sms / 2 * 2), 1, 1);
-  cfg.dynamicSmemBytes = kSmemBytes;
+  cfg.dynamicSmemBytes = Layout<kPair>::kBytes;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
   int n = 0;
@@ -995,7 +1006,7 @@ fs_status launch(const Device& dev, const fs_matmul_fp8_args& a, Plan s, cudaStr
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(balanced(s.n_units, kPair ? dev.pairs : dev.sms) * (kPair ? 2 : 1)));
   cfg.blockDim = dim3(kThreads, 1, 1);
-  cfg.dynamicSmemBytes = kSmemBytes;
+  cfg.dynamicSmemBytes = Layout<kPair>::kBytes;
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = n;
