@@ -515,6 +515,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   if constexpr (kPair) ptx::cluster_sync();
   ptx::tc_fence_after();
   ptx::grid_launch_dependents();
+  // The launch always overlaps the kernel before it on the stream; without the caller's
+  // word only this set-up does.
+  if (!s.pdl) ptx::grid_dependency_wait();
   const uint32_t tmem_base = *tmem_holder;
   const BoundedWait waiter{abort_flag, s.wait_limit_ns, s.error_word};
 
@@ -998,11 +1001,9 @@ fs_status launch(const Device& dev, const fs_matmul_fp8_args& a, Plan s, cudaStr
     attr[n].val.clusterDim.y = attr[n].val.clusterDim.z = 1;
     ++n;
   }
-  if (s.pdl) {
-    attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[n].val.programmaticStreamSerializationAllowed = 1;
-    ++n;
-  }
+  attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[n].val.programmaticStreamSerializationAllowed = 1;
+  ++n;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(balanced(s.n_units, kPair ? dev.pairs : dev.sms) * (kPair ? 2 : 1)));
   cfg.blockDim = dim3(kThreads, 1, 1);

@@ -237,6 +237,7 @@ __global__ void __launch_bounds__(kProbThreads, 2) probs_kernel(const ProbsParam
   auto mask_word = [&](int64_t row) {
     return int(threadIdx.x) < words ? p.mask[row * p.mask_ld + begin / 32 + threadIdx.x] : 0u;
   };
+  ptx::grid_dependency_wait();  // the launch overlaps the kernel before it on the stream
   // The few elements behind the last whole 16 bytes come one by one, and behind them lies
   // -infinity.
   const int at_end = copied + int(threadIdx.x);
@@ -783,6 +784,7 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyParams 
     if (rank == 0) ptx::mbar_arrive_expect_tx(&sm.arrived, uint32_t(a.n_segments) * 8u);
   }
   ptx::cluster_arrive();
+  ptx::grid_dependency_wait();  // the launch overlaps the kernel before it on the stream
   if (warp == 0) accept<T>(a, b, sm, lane);
   const float u = a.u[b * a.ldu + a.K];
   __syncthreads();
@@ -897,16 +899,18 @@ cudaError_t launch_probs(ProbsParams p, int ctas, cudaStream_t stream) {
   int dev = 0;
   cudaError_t err = cudaGetDevice(&dev);
   if (err != cudaSuccess) return err;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = unsigned(ctas);
-  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = unsigned(ctas);
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.blockDim = dim3(kProbThreads);
   cfg.gridDim = dim3(unsigned(ctas));
   cfg.dynamicSmemBytes = kAsync ? kGroups * 4 * kProbThreads * sizeof(T) : 0;
   cfg.stream = stream;
-  cfg.attrs = &attr;
+  cfg.attrs = attr;
   cfg.numAttrs = 1;
   int clusters;
   {
@@ -929,6 +933,7 @@ cudaError_t launch_probs(ProbsParams p, int ctas, cudaStream_t stream) {
   // No more than the rows need in as many turns.
   const int64_t turns = ceil_div(p.N, clusters);
   cfg.gridDim = dim3(unsigned(ceil_div(p.N, turns) * ctas));
+  cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
@@ -1068,16 +1073,18 @@ extern "C" fs_status fs_verify(const fs_verify_args* args, void* stream_ptr) {
          (a.B * ctas * 2 <= slots || a.B * (ctas * 2) * (ctas * 2) * 150 <= slots * row_kb))
     ctas *= 2;
   if (a.B <= 9 && 8 * kWarps < p.n_segments) ctas = 16;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = unsigned(ctas);
-  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = unsigned(ctas);
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(a.B * ctas));
   cfg.blockDim = dim3(kThreads);
   cfg.stream = static_cast<cudaStream_t>(stream_ptr);
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
   const cudaError_t err = a.dtype == FS_F32
                               ? cudaLaunchKernelEx(&cfg, verify_kernel<float>, p)
                               : cudaLaunchKernelEx(&cfg, verify_kernel<__nv_bfloat16>, p);
