@@ -1123,9 +1123,17 @@ extern "C" fs_status fs_matmul_fp8(const fs_matmul_fp8_args* args, void* stream_
   s.wait_limit_ns = kWaitLimitNs;
   s.error_word = dev->error_word;
   cudaStream_t stream = static_cast<cudaStream_t>(stream_ptr);
-  if (a.M > kBM) return launch<256, true>(*dev, a, s, stream);
   // Few units leave SMs without work: the widest that still gives each SM one.
-  if (ceil_div(a.V, 64) <= dev->sms) return launch<64, false>(*dev, a, s, stream);
-  if (ceil_div(a.V, 128) <= dev->sms) return launch<128, false>(*dev, a, s, stream);
-  return launch<256, false>(*dev, a, s, stream);
+  const int64_t n_mt = ceil_div(a.M, kBM);
+  if (n_mt * ceil_div(a.V, 64) <= dev->sms) return launch<64, false>(*dev, a, s, stream);
+  if (n_mt * ceil_div(a.V, 128) <= dev->sms) return launch<128, false>(*dev, a, s, stream);
+  if (a.M <= kBM) return launch<256, false>(*dev, a, s, stream);
+  // CTA pairs read W once for 256 rows, but take 256 at a time.  Where the last ones are few,
+  // single CTAs need fewer turns, each 1.12 times as long: at d = 4096, V = 128256, pairs / single
+  // CTAs, 200 rows 120 / 149 us, 320 219 / 191, 600 317 / 310, 1000 (V = 151936) 510 / 568.
+  const int64_t n_nt = ceil_div(a.V, 256);
+  const int64_t pair_turns = ceil_div(ceil_div(a.M, 2 * kBM) * n_nt, dev->pairs);
+  const int64_t single_turns = ceil_div(n_mt * n_nt, dev->sms);
+  return single_turns * 9 < pair_turns * 8 ? launch<256, false>(*dev, a, s, stream)
+                                           : launch<256, true>(*dev, a, s, stream);
 }
