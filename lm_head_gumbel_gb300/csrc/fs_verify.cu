@@ -203,7 +203,7 @@ __device__ __forceinline__ void copy_async(void* to, const void* from, uint32_t 
 // A row to a cluster of CTAs, kGroups times 4 elements a thread in registers: read once,
 // written once.  Bound: memory.  The clusters stay for many rows: a row's elements are copied
 // to shared memory while the row before is summed and written (without that a cluster's life
-// was a chain of waits: 320 rows of 128256, masked, 139 us, now PROBS_US).  The maximum and the
+// was a chain of waits: 320 rows of 128256, masked, 139 us, now 58).  The maximum and the
 // sum go through the cluster's shared memory, in the order of its CTAs.
 // kAsync: rows on 16-byte boundaries; else they are read element by element.
 template <class T, class TO, bool kAsync, int kGroups>
@@ -939,12 +939,12 @@ cudaError_t launch_probs(ProbsParams p, int ctas, cudaStream_t stream) {
 
 template <class T, class TO>
 cudaError_t launch_probs(ProbsParams p, cudaStream_t stream) {
-  // CTAs of a row's cluster and their threads' registers by V alone, so that a row's sum
-  // does not depend on what else is computed: up to 16 elements a thread more CTAs, which
-  // read and write a row sooner; then more elements.
-  int ctas = 1;
-  while (ctas < 8 && int64_t(ctas) * kProbThreads * 16 < p.V) ctas *= 2;
-  if (p.V > 8 * kMaxPart) ctas = kMaxProbCluster;
+  // CTAs of a row's cluster by V alone, so that a row's sum does not depend on what else is
+  // computed: as few as hold it, of any number, since a row's chain of waits costs each CTA
+  // the same (320 rows of 151936 in fp32: 10 CTAs 72 us, 16 of 19 elements a thread 98; 1000 of
+  // 40000: 3 CTAs 60, 8 88); two where that makes a single row faster (16000: 7.8 and 9.7).
+  const int ctas = int(std::max<int64_t>(std::min<int64_t>(kMaxProbCluster, ceil_div(p.V, kMaxPart)),
+                                         p.V > kMaxPart / 2 ? 2 : 1));
   const int64_t part = ceil_div(ceil_div(p.V, ctas), 32) * 32;
   if (part > kMaxPart) {
     cudaLaunchConfig_t cfg = {};
@@ -966,9 +966,9 @@ cudaError_t launch_probs(ProbsParams p, cudaStream_t stream) {
   if (per <= 4)
     return whole ? launch_probs<T, TO, true, 4>(p, ctas, stream)
                  : launch_probs<T, TO, false, 4>(p, ctas, stream);
-  if (per <= 5)
-    return whole ? launch_probs<T, TO, true, 5>(p, ctas, stream)
-                 : launch_probs<T, TO, false, 5>(p, ctas, stream);
+  if (per <= 6)
+    return whole ? launch_probs<T, TO, true, 6>(p, ctas, stream)
+                 : launch_probs<T, TO, false, 6>(p, ctas, stream);
   return whole ? launch_probs<T, TO, true, 8>(p, ctas, stream)
                : launch_probs<T, TO, false, 8>(p, ctas, stream);
 }
