@@ -121,7 +121,9 @@ def operands(M, d, V, seed=0):
     (64, 640, 1000), (127, 256, 300), (128, 384, 513),        # one tile of rows
     (129, 256, 300), (200, 130, 700), (256, 512, 1000), (257, 300, 255), (385, 200, 520),  # pairs
     (5, 256, 12000), (5, 256, 21000), (33, 130, 40000), (700, 128, 3000),  # wider units, waves
-    (2, 5120, 100), (130, 2000, 130)])
+    (2, 5120, 100), (130, 2000, 130),
+    (200, 130, 25000), (385, 200, 20001), (700, 128, 30000),  # CTA pairs, several rows of tiles
+    (320, 256, 30000), (129, 2100, 45000), (300, 300, 10000)])  # single CTAs, several rows
 def test_product(M, d, V, dtype):
     check_product(*operands(M, d, V, seed=M + d + V), dtype)
 
@@ -159,11 +161,12 @@ def test_product_into_given_rows(M, ldo, shift, dtype):
     assert torch.equal(buf, guard)
 
 
-def test_rows_do_not_depend_on_the_batch():
+@pytest.mark.parametrize("V", [2000, 12000, 30000])
+def test_rows_do_not_depend_on_the_batch(V):
     """A row's logits have the same bits alone, in a batch and in a pair's tile."""
-    a, sa, w, sw = operands(300, 1000, 2000, seed=9)
+    a, sa, w, sw = operands(700, 1000, V, seed=9)
     whole = fs.fs_matmul_fp8(a, sa, w, sw, out_dtype=torch.float32)
-    for n in (1, 5, 64, 128, 129, 300):
+    for n in (1, 5, 64, 128, 129, 200, 320, 700):
         part = fs.fs_matmul_fp8(a[:n], sa[:n], w, sw, out_dtype=torch.float32)
         assert torch.equal(part, whole[:n])
 
@@ -207,12 +210,12 @@ def test_refusals():
         assert e.value.status == fs.FS_ERR_INVALID_ARG
 
 
-@pytest.mark.parametrize("M", [6, 300])
-def test_streams_graphs_and_overlap(M):
+@pytest.mark.parametrize("M,V", [(6, 3000), (300, 3000), (200, 25000)])
+def test_streams_graphs_and_overlap(M, V):
     """The same bits on another stream, in a replayed graph with new inputs, and behind the
     kernel that makes A with overlap_previous."""
     x, _ = matrix(M, 1000, torch.bfloat16, seed=21)
-    w, _ = matrix(3000, 1000, torch.bfloat16, seed=22)
+    w, _ = matrix(V, 1000, torch.bfloat16, seed=22)
     head = fs.fs_quantize(w, 128)
     first = fs.fs_quantize(x)
     want = fs.fs_matmul_fp8(*first, *head)
@@ -235,8 +238,29 @@ def test_streams_graphs_and_overlap(M):
         assert torch.equal(fs.fs_matmul_fp8(*q, *head, overlap_previous=True), want)
 
 
+def test_call_after_call():
+    """Calls right behind one another that write what the next one reads: no call starts on
+    what the one before has not finished."""
+    a, sa, w, sw = operands(150, 640, 640, seed=17)
+    x = a.float()
+    want = []
+    for _ in range(4):
+        q = fs.fs_quantize(x)
+        torch.cuda.synchronize()
+        x = fs.fs_matmul_fp8(*q, w, sw, out_dtype=torch.float32)
+        torch.cuda.synchronize()
+        want.append(x)
+    for _ in range(20):
+        x = a.float()
+        got = []
+        for _ in range(4):
+            x = fs.fs_matmul_fp8(*fs.fs_quantize(x), w, sw, out_dtype=torch.float32)
+            got.append(x)
+        assert all(torch.equal(g, w) for g, w in zip(got, want))
+
+
 def test_two_streams_at_once():
-    cases = [operands(M, 1000, 5000, seed=M) for M in (20, 260)]
+    cases = [operands(M, 1000, 25000, seed=M) for M in (20, 260)]
     want = [fs.fs_matmul_fp8(*c) for c in cases]
     torch.cuda.synchronize()
     streams = [torch.cuda.Stream(), torch.cuda.Stream()]

@@ -75,6 +75,63 @@ def test_probs(N, V, ld, shift, ti, to):
 
 
 @pytest.mark.parametrize("ti", TYPES)
+@pytest.mark.parametrize("V,ld", [
+    (8193, 8200), (16384, 16384), (16385, 16392), (33001, 33008), (49153, 49160), (100002, 100008),
+    (131072, 131072), (131073, 131080), (170001, 170001), (262145, 262152)])
+def test_probs_of_every_number_of_ctas(V, ld, ti):
+    """Rows held by 1 to 16 CTAs and longer ones, whose last CTA has few elements or none, and
+    whose ends do not fill 16 bytes."""
+    x, _ = logits(2, V, ti, ld=ld, seed=V)
+    x[0, V - 1] = 25.0
+    gen = torch.Generator().manual_seed(V)
+    check_probs(x, dtype=ti)
+    check_probs(x, torch.tensor([0.7, 0.0]).cuda(), pack(torch.rand((2, V), generator=gen) < 0.5))
+
+
+@pytest.mark.parametrize("ti", TYPES)
+@pytest.mark.parametrize("N,V,ld", [(2000, 515, 520), (1300, 2051, 2056), (700, 4099, 4099),
+                                    (130, 50003, 50008)])
+def test_probs_of_more_rows_than_fit(N, V, ld, ti):
+    """Clusters that take several rows, sampled and greedy ones, with their own masks."""
+    x, _ = logits(N, V, ti, ld=ld, seed=N)
+    gen = torch.Generator().manual_seed(N)
+    T = torch.rand(N, generator=gen) + 0.5
+    T[torch.rand(N, generator=gen) < 0.3] = 0.0
+    allow = torch.rand((N, V), generator=gen) < 0.6
+    allow[5], allow[N - 1, 1:] = False, False
+    x[7] = -float("inf")
+    mask = pack(allow)
+    got = check_probs(x, T.cuda(), mask, ti)
+    for _ in range(5):
+        assert torch.equal(fs.fs_probs(x, temperature=T.cuda(), vocab_mask=mask, out_dtype=ti), got)
+    for n in (0, 5, 7, N // 2, N - 1):  # a row's bits do not depend on the others
+        one = fs.fs_probs(x[n:n + 1], temperature=T[n:n + 1].cuda(),
+                          vocab_mask=mask[n:n + 1].contiguous(), out_dtype=ti)
+        assert torch.equal(one, got[n:n + 1])
+
+
+def test_probs_behind_the_kernel_that_makes_the_logits():
+    """Call after call in place, then verification of what the last one made: none starts on
+    what the one before has not finished."""
+    z, _ = logits(40, 30000, torch.float32, seed=23)
+    ids = torch.zeros((40, 0), dtype=torch.int64, device="cuda")
+    u = torch.rand((40, 1), generator=torch.Generator().manual_seed(1)).cuda()
+
+    def chain(sync):
+        x = z.clone()
+        for _ in range(4):
+            x *= 3.0
+            fs.fs_probs(x, out=x)
+            sync()
+        return x, fs.fs_verify(x.unsqueeze(1), ids, u).ids
+
+    want, drawn = chain(torch.cuda.synchronize)
+    for _ in range(20):
+        x, got = chain(lambda: None)
+        assert torch.equal(x, want) and torch.equal(got, drawn)
+
+
+@pytest.mark.parametrize("ti", TYPES)
 @pytest.mark.parametrize("V", [5, 1000, 70001])
 def test_probs_of_greedy_rows(V, ti):
     """All on the lowest id of the largest allowed logit, whichever way T says greedy."""
