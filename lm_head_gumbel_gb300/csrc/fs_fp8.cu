@@ -594,7 +594,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---------------- MMA issuer (the leader CTA's) ----------------
     if (leader) {
       const bool issuer = ptx::elect_one();
-      uint32_t stage = 0, phase = 0, acc = 0, acc_phase = 0;
+      uint32_t stage = 0, phase = 0, acc_phases = 0;  // a bit for each accumulator
       bool ok = true;
       const uint32_t s0 = ptx::smem_u32(smem);
       const uint64_t desc_a0 = ptx::smem_desc_sw128(s0);
@@ -612,9 +612,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             break;
           }
           const uint64_t off = uint64_t((stage * s.stage_bytes) >> 4);
+          const uint32_t acc = uint32_t(kb) % kAcc;  // a unit begins with the first one
 #pragma unroll
           for (int h = 0; h < kParts; ++h) {
-            if (!waiter.wait_warp(&tempty_bar[acc * kParts + h], acc_phase ^ 1u)) {
+            if (!waiter.wait_warp(&tempty_bar[acc * kParts + h], (acc_phases >> acc & 1u) ^ 1u)) {
               ok = false;
               break;
             }
@@ -641,10 +642,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             stage = 0;
             phase ^= 1u;
           }
-          if (++acc == kAcc) {
-            acc = 0;
-            acc_phase ^= 1u;
-          }
+          acc_phases ^= 1u << acc;
         }
       }
       // All MMAs complete before tensor memory is released.
@@ -725,7 +723,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tempty0 = ptx::cluster_addr(tempty_bar + part, 0);
     const uint32_t sfull0 = ptx::smem_u32(sfull_bar), sempty0 = ptx::smem_u32(sempty_bar);
     const uint32_t scales0 = ptx::smem_u32(&groups[0].product[half][0][quad * 32 + lane]);
-    uint32_t acc = 0, acc_phase = 0, group = 0, group_phase = 0;
+    uint32_t acc_phases = 0, group = 0, group_phase = 0;
     // Past its limit a wait raises the abort flag and returns, and so does every later one
     // at once: the loops end, with the error reported and sums of no use.
     auto wait = [&](uint32_t bar, uint32_t parity) {
@@ -751,13 +749,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int col0 = nt * kN + half * kCols;
       if (row0 >= s.M || col0 >= s.V) {  // nothing here
         for (int kb = 0; kb < s.n_kb; ++kb) {
-          wait(tfull0 + 8u * kParts * acc, acc_phase);
+          const uint32_t acc = uint32_t(kb) % kAcc;
+          wait(tfull0 + 8u * kParts * acc, acc_phases >> acc & 1u);
+          acc_phases ^= 1u << acc;
           ptx::tc_fence_before();
           arrive(tempty0 + 8u * kParts * acc);
-          if (++acc == kAcc) {
-            acc = 0;
-            acc_phase ^= 1u;
-          }
           if (kb % kGroupSlices == kGroupSlices - 1 || kb + 1 == s.n_kb) {
             wait(sfull0 + 8u * group, group_phase);
             next_group();
@@ -778,17 +774,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       wait(sfull0 + 8u * group, group_phase);
       uint32_t scale_at = scales0 + group * uint32_t(sizeof(ScaleGroup));
       float scale = ptx::ld_shared_f32(scale_at);
-      uint32_t taddr = taddr0 + acc * kN;
-      wait(tfull0 + 8u * kParts * acc, acc_phase);
+      wait(tfull0, acc_phases & 1u);
+      acc_phases ^= 1u;
       ptx::tc_fence_after();
-      ptx::tmem_ld_32x32b_x32(taddr, r[0]);
-      if (kChunks > 1) ptx::tmem_ld_32x32b_x32(taddr + 32u, r[1]);
-      // A slice; `more`: another one of the unit follows.  Loads go out as soon as their
-      // registers are free, 32 columns at a time, the next slice's first ones beside the
-      // last additions of this one's.
-      auto slice = [&](int kb, auto more) {
+      ptx::tmem_ld_32x32b_x32(taddr0, r[0]);
+      if (kChunks > 1) ptx::tmem_ld_32x32b_x32(taddr0 + 32u, r[1]);
+      // A slice, from accumulator a; `more`: another one of the unit follows.  Loads go out as
+      // soon as their registers are free, 32 columns at a time, the next slice's first ones
+      // beside the last additions of this one's.  A unit begins with the first accumulator,
+      // so that every address is known ahead (made from a counter they held the loads up by
+      // 100 cycles).
+      auto slice = [&](int kb, auto which, bool more) {
+        constexpr int a = decltype(which)::value;
+        constexpr int next = (a + 1) % kAcc;
         float scale_next = 0.0f;
-        if constexpr (decltype(more)::value) {
+        if (more) {
           scale_at += kBM * 4;
           if (kb % kGroupSlices == kGroupSlices - 1) {
             next_group();
@@ -800,32 +800,37 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int c = 2; c < kChunks; ++c) {
           add(c - 2, scale);
-          ptx::tmem_ld_32x32b_x32(taddr + uint32_t(c * 32), r[c & 1]);
+          ptx::tmem_ld_32x32b_x32(taddr0 + uint32_t(a * kN + c * 32), r[c & 1]);
         }
-        if constexpr (decltype(more)::value) scale_next = ptx::ld_shared_f32(scale_at);
+        if (more) scale_next = ptx::ld_shared_f32(scale_at);
         if (kChunks > 2) ptx::tmem_wait_ld();
         ptx::tc_fence_before();
-        arrive(tempty0 + 8u * kParts * acc);
-        if (++acc == kAcc) {
-          acc = 0;
-          acc_phase ^= 1u;
-        }
-        taddr = taddr0 + acc * kN;
+        arrive(tempty0 + uint32_t(8 * kParts * a));
         if (kChunks > 1) add(kChunks - 2, scale);
-        if constexpr (decltype(more)::value) {
-          wait(tfull0 + 8u * kParts * acc, acc_phase);
+        if (more) {
+          wait(tfull0 + uint32_t(8 * kParts * next), acc_phases >> next & 1u);
+          acc_phases ^= 1u << next;
           ptx::tc_fence_after();
+          if (kChunks > 1) ptx::tmem_ld_32x32b_x32(taddr0 + uint32_t(next * kN), r[0]);
         }
-        if (kChunks == 1) add(0, scale);
-        if constexpr (decltype(more)::value) ptx::tmem_ld_32x32b_x32(taddr, r[0]);
-        if (kChunks > 1) {
-          add(kChunks - 1, scale);
-          if constexpr (decltype(more)::value) ptx::tmem_ld_32x32b_x32(taddr + 32u, r[1]);
+        add(kChunks - 1, scale);
+        if (more) {
+          if (kChunks > 1)
+            ptx::tmem_ld_32x32b_x32(taddr0 + uint32_t(next * kN) + 32u, r[1]);
+          else
+            ptx::tmem_ld_32x32b_x32(taddr0 + uint32_t(next * kN), r[0]);
         }
         scale = scale_next;
       };
-      for (int kb = 0; kb + 1 < s.n_kb; ++kb) slice(kb, std::true_type());
-      slice(s.n_kb - 1, std::false_type());
+#pragma unroll 1
+      for (int kb = 0; kb < s.n_kb; kb += kAcc) {
+        slice(kb, std::integral_constant<int, 0>(), kb + 1 < s.n_kb);
+        if (kb + 1 < s.n_kb) slice(kb + 1, std::integral_constant<int, 1>(), kb + 2 < s.n_kb);
+        if constexpr (kAcc == 4) {
+          if (kb + 2 < s.n_kb) slice(kb + 2, std::integral_constant<int, 2>(), kb + 3 < s.n_kb);
+          if (kb + 3 < s.n_kb) slice(kb + 3, std::integral_constant<int, 3>(), kb + 4 < s.n_kb);
+        }
+      }
       next_group();
       float sum[kCols];
 #pragma unroll
