@@ -93,8 +93,10 @@ constexpr float kMostE4m3 = 448.0f;
 // Quantisation
 // ---------------------------------------------------------------------------
 // Bound: memory.  A head of 151936 x 4096 in bf16 (1.87 GB read and written) takes 264 us,
-// 7.1 TB/s, 16384 x 5120 hidden states 41 (6.2 TB/s); kept as bits until they are scaled, so that a thread's loads are all in flight and
-// the largest magnitude is an unsigned maximum (a NaN's bits are above every number's).
+// 7.1 TB/s, 16384 x 5120 hidden states 41 us, 6.2 TB/s.  Elements stay bits until they are
+// scaled, so that a thread's loads are all in flight (branches between them: 779 us for the
+// head), and the largest magnitude is an unsigned maximum: a NaN's bits are above every
+// number's.
 constexpr uint32_t kLeastMaxBits = 0x0D800000u;  // 2^-100
 
 // 8 elements as they lie in memory.
@@ -187,7 +189,7 @@ template <class T, bool kVec, int kPer>
 __global__ void __launch_bounds__(kRowThreads) quantize_rows_kernel(const QuantParams p) {
   const int lane = threadIdx.x % kRowLanes;
   int64_t block = int64_t(blockIdx.x) * (kRowBlocks * kPer) + threadIdx.x / kRowLanes;
-  int64_t row = int64_t(p.N) * p.col_blocks <= UINT_MAX
+  int64_t row = int64_t(p.N) * p.col_blocks <= UINT_MAX - 4096  // past it by a CTA
                     ? int64_t(uint32_t(block) / uint32_t(p.col_blocks))
                     : block / p.col_blocks;
   int cb = int(block - row * p.col_blocks);
@@ -285,9 +287,20 @@ __global__ void __launch_bounds__(kTileThreads) quantize_tile_kernel(const Quant
 // Warp roles as in fs_contract.cuh: warp 0 issues TMA copies into a ring of 128-wide
 // k slices (128 bytes a row, so the swizzle and the descriptors are those of 64 bf16),
 // warp 1 issues the MMAs (M = 128 per CTA, kN vocabulary columns; for CTA pairs M = 256
-// over both), warps 4-11 take the sums out.  The scales change with every slice, so a
-// slice is an accumulator of its own: the MMAs alternate over kAcc of them in tensor
-// memory, and the warps add each, times the two scales, to sums in registers.
+// over both), warp 2 brings the scales, warps 4-11 take the sums out.  The scales change
+// with every slice, so a slice is an accumulator of its own: the MMAs alternate over kAcc of
+// them in tensor memory, and the warps add each, times the product of the two scales, to
+// sums in registers.
+//
+// Bound: W's bytes for few rows (one row at d = 4096, V = 151936 takes 92 us, 6.75 TB/s; 128
+// rows 114).  For many, what follows the MMAs: an accumulator's 256 columns are 128 additions
+// of two values a thread, and an accumulator is free again 1200 cycles after its MMAs were
+// issued (256 a part, 340 until the sums' warps know, 340 until they have loaded it, 270 until
+// the next MMAs run), of which two overlap: 876 cycles a slice where the MMAs alone take 640 with
+// their waits and 512 at the nominal rate.  1000 rows: 487 us in bursts, 550 held at the power
+// limit (2560 and 2260 TFLOP/s).  First 1045: tensor-memory loads one at a time with their
+// additions between, scales read by the same warps (a wait for tensor-memory loads waits for
+// those too), outputs stored from registers.
 // ---------------------------------------------------------------------------
 using vocab::BoundedWait;
 using vocab::kEpiWarps;
@@ -592,8 +605,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else if (warp == 1) {
     // ---------------- MMA issuer (the leader CTA's) ----------------
-    if (leader) {
-      const bool issuer = ptx::elect_one();
+    // One thread does it all: what it takes from an accumulator's return to its next MMAs is
+    // on the chain that bounds the kernel (votes of the warp's lanes at its waits: 20 cycles a
+    // slice of 890).
+    if (leader && ptx::elect_one()) {
       uint32_t stage = 0, phase = 0, acc_phases = 0;  // a bit for each accumulator
       bool ok = true;
       const uint32_t s0 = ptx::smem_u32(smem);
@@ -606,38 +621,29 @@ __global__ void __launch_bounds__(kThreads, 1)
           ptx::mma_commit(bar);
       };
       for (int u = worker; ok && u < s.n_units; u += n_workers) {
-        for (int kb = 0; kb < s.n_kb; ++kb) {
-          if (!waiter.wait_warp(&full_bar[stage], phase)) {
-            ok = false;
-            break;
-          }
+        for (int kb = 0; ok && kb < s.n_kb; ++kb) {
           const uint64_t off = uint64_t((stage * s.stage_bytes) >> 4);
           const uint32_t acc = uint32_t(kb) % kAcc;  // a unit begins with the first one
+          ok = waiter.wait(&full_bar[stage], phase);
 #pragma unroll
           for (int h = 0; h < kParts; ++h) {
-            if (!waiter.wait_warp(&tempty_bar[acc * kParts + h], (acc_phases >> acc & 1u) ^ 1u)) {
-              ok = false;
-              break;
-            }
+            ok = ok && waiter.wait(&tempty_bar[acc * kParts + h], (acc_phases >> acc & 1u) ^ 1u);
+            if (!ok) break;
             ptx::tc_fence_after();
-            if (issuer) {
-              const uint32_t d_tmem = tmem_base + acc * kN + h * (kN / kParts);
+            const uint32_t d_tmem = tmem_base + acc * kN + h * (kN / kParts);
 #pragma unroll
-              for (int k = 0; k < kBK / kUK; ++k) {
-                const uint64_t da = desc_a0 + off + uint64_t(kUK >> 4) * k;
-                const uint64_t db =
-                    desc_b0 + off + uint64_t(h * ((kPartRows * kBK) >> 4) + (kUK >> 4) * k);
-                if constexpr (kPair)
-                  ptx::mma_f8_pair(d_tmem, da, db, kIdesc, k != 0 ? 1u : 0u);
-                else
-                  ptx::mma_f8(d_tmem, da, db, kIdesc, k != 0 ? 1u : 0u);
-              }
-              if (h == kParts - 1) commit(&empty_bar[stage]);
-              commit(&tfull_bar[acc * kParts + h]);
+            for (int k = 0; k < kBK / kUK; ++k) {
+              const uint64_t da = desc_a0 + off + uint64_t(kUK >> 4) * k;
+              const uint64_t db =
+                  desc_b0 + off + uint64_t(h * ((kPartRows * kBK) >> 4) + (kUK >> 4) * k);
+              if constexpr (kPair)
+                ptx::mma_f8_pair(d_tmem, da, db, kIdesc, k != 0 ? 1u : 0u);
+              else
+                ptx::mma_f8(d_tmem, da, db, kIdesc, k != 0 ? 1u : 0u);
             }
-            __syncwarp();
+            commit(&tfull_bar[acc * kParts + h]);
+            if (h == kParts - 1) commit(&empty_bar[stage]);
           }
-          if (!ok) break;
           if (++stage == s.n_stages) {
             stage = 0;
             phase ^= 1u;
@@ -646,15 +652,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       // All MMAs complete before tensor memory is released.
-      if (issuer) {
-        if constexpr (kPair)
-          ptx::mma_commit_pair(drain_bar);
-        else
-          ptx::mma_commit(drain_bar);
-      }
-      __syncwarp();
-      waiter.drain(drain_bar, 0);
+      if constexpr (kPair)
+        ptx::mma_commit_pair(drain_bar);
+      else
+        ptx::mma_commit(drain_bar);
     }
+    __syncwarp();
+    if (leader) waiter.drain(drain_bar, 0);
     __syncwarp();
     } else if (warp == 2) {
       // ---------------- scales ----------------
