@@ -536,130 +536,130 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp < kFirstSum) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
-  if (warp == 0) {
-    // ---------------- TMA producer ----------------
-    const bool issuer = ptx::elect_one();
-    const uint64_t pol_a = ptx::policy_evict_last();
-    const uint64_t pol_b = s.n_mt > 1 ? ptx::policy_evict_normal() : ptx::policy_evict_first();
-    auto load = [&](uint8_t* dst, const CUtensorMap* map, uint32_t stage, int x, int y,
-                    uint64_t pol) {
-      if constexpr (kPair)
-        ptx::tma_load_2d_pair(dst, map, ptx::cluster_addr(&full_bar[stage], 0), x, y, pol);
-      else
-        ptx::tma_load_2d(dst, map, &full_bar[stage], x, y, pol);
-    };
-    // Rows past the end read as 0.
-    auto load_a = [&](uint32_t stage, int kb, int mt) {
-      load(smem + size_t(stage) * s.stage_bytes, &tmap_a, stage, kb * kBK,
-           (mt * kCtas + rank) * kBM, pol_a);
-    };
-    uint32_t stage = 0, phase = 0, issued = 0;
-    bool ok = true;
-    // The first ring fill's A copies, held back until the kernel before is done.
-    bool deferring = s.pdl != 0;
-    int n_held = 0, held_kb[kMaxStages], held_mt[kMaxStages];
-    auto release = [&]() {
-      ptx::grid_dependency_wait();
-      if (issuer)
-        for (int h = 0; h < n_held; ++h) load_a(uint32_t(h), held_kb[h], held_mt[h]);
-      deferring = false;
-    };
-    for (int u = worker; ok && u < s.n_units; u += n_workers) {
-      const int nt = u / s.n_mt, mt = u - nt * s.n_mt;
-      for (int kb = 0; kb < s.n_kb; ++kb) {
-        if (!waiter.wait_warp(&empty_bar[stage], phase ^ 1u)) {
-          ok = false;
-          break;
-        }
-        if (issuer) {
-          if (leader)
-            ptx::mbar_arrive_expect_tx(&full_bar[stage], kCtas * (s.a_bytes + kBBytes));
-          // A part's columns of a pair's tile lie half in each CTA.
-#pragma unroll
-          for (int h = 0; h < kParts; ++h)
-            load(smem + size_t(stage) * s.stage_bytes + s.a_bytes + h * kPartRows * kBK, &tmap_b,
-                 stage, kb * kBK, nt * kN + h * (kN / kParts) + rank * kPartRows, pol_b);
-          if (!deferring) load_a(stage, kb, mt);
-        }
-        if (deferring) {  // the first fill: stage n_held
-          held_kb[n_held] = kb;
-          held_mt[n_held++] = mt;
-        }
-        ++issued;
-        if (++stage == s.n_stages) {
-          stage = 0;
-          phase ^= 1u;
-        }
-        if (deferring && n_held == int(s.n_stages)) release();
-      }
-    }
-    if (deferring) release();
-    // Every issued copy lands before the CTA's shared memory goes away (the
-    // leader's barriers see both CTAs' copies).
-    if (leader) {
-      for (uint32_t i = 0; i < s.n_stages; ++i) {
-        const uint32_t fills = issued / s.n_stages + (i < issued % s.n_stages ? 1u : 0u);
-        if (fills) waiter.drain(&full_bar[i], (fills - 1u) & 1u);
-      }
-    }
-    __syncwarp();
-  } else if (warp == 1) {
-    // ---------------- MMA issuer (the leader CTA's) ----------------
-    // One thread does it all: what it takes from an accumulator's return to its next MMAs is
-    // on the chain that bounds the kernel (votes of the warp's lanes at its waits: 20 cycles a
-    // slice of 890).
-    if (leader && ptx::elect_one()) {
-      uint32_t stage = 0, phase = 0, acc_phases = 0;  // a bit for each accumulator
-      bool ok = true;
-      const uint32_t s0 = ptx::smem_u32(smem);
-      const uint64_t desc_a0 = ptx::smem_desc_sw128(s0);
-      const uint64_t desc_b0 = ptx::smem_desc_sw128(s0 + s.a_bytes);
-      auto commit = [&](uint64_t* bar) {
+    if (warp == 0) {
+      // ---------------- TMA producer ----------------
+      const bool issuer = ptx::elect_one();
+      const uint64_t pol_a = ptx::policy_evict_last();
+      const uint64_t pol_b = s.n_mt > 1 ? ptx::policy_evict_normal() : ptx::policy_evict_first();
+      auto load = [&](uint8_t* dst, const CUtensorMap* map, uint32_t stage, int x, int y,
+                      uint64_t pol) {
         if constexpr (kPair)
-          ptx::mma_commit_pair_multicast(bar, 0x3);
+          ptx::tma_load_2d_pair(dst, map, ptx::cluster_addr(&full_bar[stage], 0), x, y, pol);
         else
-          ptx::mma_commit(bar);
+          ptx::tma_load_2d(dst, map, &full_bar[stage], x, y, pol);
+      };
+      // Rows past the end read as 0.
+      auto load_a = [&](uint32_t stage, int kb, int mt) {
+        load(smem + size_t(stage) * s.stage_bytes, &tmap_a, stage, kb * kBK,
+             (mt * kCtas + rank) * kBM, pol_a);
+      };
+      uint32_t stage = 0, phase = 0, issued = 0;
+      bool ok = true;
+      // The first ring fill's A copies, held back until the kernel before is done.
+      bool deferring = s.pdl != 0;
+      int n_held = 0, held_kb[kMaxStages], held_mt[kMaxStages];
+      auto release = [&]() {
+        ptx::grid_dependency_wait();
+        if (issuer)
+          for (int h = 0; h < n_held; ++h) load_a(uint32_t(h), held_kb[h], held_mt[h]);
+        deferring = false;
       };
       for (int u = worker; ok && u < s.n_units; u += n_workers) {
-        for (int kb = 0; ok && kb < s.n_kb; ++kb) {
-          const uint64_t off = uint64_t((stage * s.stage_bytes) >> 4);
-          const uint32_t acc = uint32_t(kb) % kAcc;  // a unit begins with the first one
-          ok = waiter.wait(&full_bar[stage], phase);
-#pragma unroll
-          for (int h = 0; h < kParts; ++h) {
-            ok = ok && waiter.wait(&tempty_bar[acc * kParts + h], (acc_phases >> acc & 1u) ^ 1u);
-            if (!ok) break;
-            ptx::tc_fence_after();
-            const uint32_t d_tmem = tmem_base + acc * kN + h * (kN / kParts);
-#pragma unroll
-            for (int k = 0; k < kBK / kUK; ++k) {
-              const uint64_t da = desc_a0 + off + uint64_t(kUK >> 4) * k;
-              const uint64_t db =
-                  desc_b0 + off + uint64_t(h * ((kPartRows * kBK) >> 4) + (kUK >> 4) * k);
-              if constexpr (kPair)
-                ptx::mma_f8_pair(d_tmem, da, db, kIdesc, k != 0 ? 1u : 0u);
-              else
-                ptx::mma_f8(d_tmem, da, db, kIdesc, k != 0 ? 1u : 0u);
-            }
-            commit(&tfull_bar[acc * kParts + h]);
-            if (h == kParts - 1) commit(&empty_bar[stage]);
+        const int nt = u / s.n_mt, mt = u - nt * s.n_mt;
+        for (int kb = 0; kb < s.n_kb; ++kb) {
+          if (!waiter.wait_warp(&empty_bar[stage], phase ^ 1u)) {
+            ok = false;
+            break;
           }
+          if (issuer) {
+            if (leader)
+              ptx::mbar_arrive_expect_tx(&full_bar[stage], kCtas * (s.a_bytes + kBBytes));
+            // A part's columns of a pair's tile lie half in each CTA.
+#pragma unroll
+            for (int h = 0; h < kParts; ++h)
+              load(smem + size_t(stage) * s.stage_bytes + s.a_bytes + h * kPartRows * kBK, &tmap_b,
+                   stage, kb * kBK, nt * kN + h * (kN / kParts) + rank * kPartRows, pol_b);
+            if (!deferring) load_a(stage, kb, mt);
+          }
+          if (deferring) {  // the first fill: stage n_held
+            held_kb[n_held] = kb;
+            held_mt[n_held++] = mt;
+          }
+          ++issued;
           if (++stage == s.n_stages) {
             stage = 0;
             phase ^= 1u;
           }
-          acc_phases ^= 1u << acc;
+          if (deferring && n_held == int(s.n_stages)) release();
         }
       }
-      // All MMAs complete before tensor memory is released.
-      if constexpr (kPair)
-        ptx::mma_commit_pair(drain_bar);
-      else
-        ptx::mma_commit(drain_bar);
-    }
-    __syncwarp();
-    if (leader) waiter.drain(drain_bar, 0);
-    __syncwarp();
+      if (deferring) release();
+      // Every issued copy lands before the CTA's shared memory goes away (the
+      // leader's barriers see both CTAs' copies).
+      if (leader) {
+        for (uint32_t i = 0; i < s.n_stages; ++i) {
+          const uint32_t fills = issued / s.n_stages + (i < issued % s.n_stages ? 1u : 0u);
+          if (fills) waiter.drain(&full_bar[i], (fills - 1u) & 1u);
+        }
+      }
+      __syncwarp();
+    } else if (warp == 1) {
+      // ---------------- MMA issuer (the leader CTA's) ----------------
+      // One thread does it all: what it takes from an accumulator's return to its next MMAs is
+      // on the chain that bounds the kernel (votes of the warp's lanes at its waits: 20 cycles a
+      // slice of 890).
+      if (leader && ptx::elect_one()) {
+        uint32_t stage = 0, phase = 0, acc_phases = 0;  // a bit for each accumulator
+        bool ok = true;
+        const uint32_t s0 = ptx::smem_u32(smem);
+        const uint64_t desc_a0 = ptx::smem_desc_sw128(s0);
+        const uint64_t desc_b0 = ptx::smem_desc_sw128(s0 + s.a_bytes);
+        auto commit = [&](uint64_t* bar) {
+          if constexpr (kPair)
+            ptx::mma_commit_pair_multicast(bar, 0x3);
+          else
+            ptx::mma_commit(bar);
+        };
+        for (int u = worker; ok && u < s.n_units; u += n_workers) {
+          for (int kb = 0; ok && kb < s.n_kb; ++kb) {
+            const uint64_t off = uint64_t((stage * s.stage_bytes) >> 4);
+            const uint32_t acc = uint32_t(kb) % kAcc;  // a unit begins with the first one
+            ok = waiter.wait(&full_bar[stage], phase);
+#pragma unroll
+            for (int h = 0; h < kParts; ++h) {
+              ok = ok && waiter.wait(&tempty_bar[acc * kParts + h], (acc_phases >> acc & 1u) ^ 1u);
+              if (!ok) break;
+              ptx::tc_fence_after();
+              const uint32_t d_tmem = tmem_base + acc * kN + h * (kN / kParts);
+#pragma unroll
+              for (int k = 0; k < kBK / kUK; ++k) {
+                const uint64_t da = desc_a0 + off + uint64_t(kUK >> 4) * k;
+                const uint64_t db =
+                    desc_b0 + off + uint64_t(h * ((kPartRows * kBK) >> 4) + (kUK >> 4) * k);
+                if constexpr (kPair)
+                  ptx::mma_f8_pair(d_tmem, da, db, kIdesc, k != 0 ? 1u : 0u);
+                else
+                  ptx::mma_f8(d_tmem, da, db, kIdesc, k != 0 ? 1u : 0u);
+              }
+              commit(&tfull_bar[acc * kParts + h]);
+              if (h == kParts - 1) commit(&empty_bar[stage]);
+            }
+            if (++stage == s.n_stages) {
+              stage = 0;
+              phase ^= 1u;
+            }
+            acc_phases ^= 1u << acc;
+          }
+        }
+        // All MMAs complete before tensor memory is released.
+        if constexpr (kPair)
+          ptx::mma_commit_pair(drain_bar);
+        else
+          ptx::mma_commit(drain_bar);
+      }
+      __syncwarp();
+      if (leader) waiter.drain(drain_bar, 0);
+      __syncwarp();
     } else if (warp == 2) {
       // ---------------- scales ----------------
       // From memory by a warp of its own: a wait for tensor-memory loads waits for a
