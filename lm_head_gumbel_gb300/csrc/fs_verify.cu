@@ -380,6 +380,10 @@ __global__ void __launch_bounds__(kProbThreads, 2) probs_kernel(const ProbsParam
     row = next;
     temp = next_temp;
   }
+  // After a wait that ran out the others may still store here: this CTA ends behind them
+  // (the barrier is of those that have not ended).
+  __syncthreads();
+  if (sm.gave_up) ptx::cluster_sync();
 }
 
 // Rows longer than a cluster's registers: one CTA, three passes, the later two mostly from L2.
@@ -625,6 +629,7 @@ struct alignas(16) Shared {
   uint64_t arrived;  // the segments' sums have
   int accepted, mode, without;
   int segment, first, last, found;
+  int gave_up;
 };
 
 // The segments' sums are there, or the wait's limit has passed: then the error word says so.
@@ -634,6 +639,7 @@ __device__ __forceinline__ void wait_arrived(const VerifyParams& a, Shared& sm) 
     while (!ptx::mbar_try_wait(&sm.arrived, 0)) {
       if (ptx::global_timer_ns() - t0 > a.wait_limit_ns) {
         atomicOr(a.error_word, kErrWaitTimeout);
+        sm.gave_up = 1;
         break;
       }
     }
@@ -779,6 +785,7 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyParams 
   const int rank = int(ptx::cluster_ctarank());
   const int64_t b = blockIdx.x / n_ctas;
   if (threadIdx.x == 0) {
+    sm.gave_up = 0;
     ptx::mbar_init(&sm.arrived, 1);
     ptx::fence_barrier_init();
     if (rank == 0) ptx::mbar_arrive_expect_tx(&sm.arrived, uint32_t(a.n_segments) * 8u);
@@ -834,6 +841,9 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyParams 
   for (int i = threadIdx.x; i <= a.K; i += kThreads)
     a.out_ids[b * a.ld_out + i] = i < n ? a.ids[b * a.ld_ids + i] : i == n ? int64_t(drawn) : -1;
   if (threadIdx.x == 0 && a.accepted) a.accepted[b] = n;
+  // After a wait that ran out the others may still store here: this CTA ends behind them
+  // (the barrier is of those that have not ended).
+  if (sm.gave_up) ptx::cluster_sync();
 }
 
 // ---------------------------------------------------------------------------
