@@ -538,40 +538,41 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
     if (warp == 0) {
       // ---------------- TMA producer ----------------
-      const bool issuer = ptx::elect_one();
-      const uint64_t pol_a = ptx::policy_evict_last();
-      const uint64_t pol_b = s.n_mt > 1 ? ptx::policy_evict_normal() : ptx::policy_evict_first();
-      auto load = [&](uint8_t* dst, const CUtensorMap* map, uint32_t stage, int x, int y,
-                      uint64_t pol) {
-        if constexpr (kPair)
-          ptx::tma_load_2d_pair(dst, map, ptx::cluster_addr(&full_bar[stage], 0), x, y, pol);
-        else
-          ptx::tma_load_2d(dst, map, &full_bar[stage], x, y, pol);
-      };
-      // Rows past the end read as 0.
-      auto load_a = [&](uint32_t stage, int kb, int mt) {
-        load(smem + size_t(stage) * s.stage_bytes, &tmap_a, stage, kb * kBK,
-             (mt * kCtas + rank) * kBM, pol_a);
-      };
-      uint32_t stage = 0, phase = 0, issued = 0;
-      bool ok = true;
-      // The first ring fill's A copies, held back until the kernel before is done.
-      bool deferring = s.pdl != 0;
-      int n_held = 0, held_kb[kMaxStages], held_mt[kMaxStages];
-      auto release = [&]() {
-        ptx::grid_dependency_wait();
-        if (issuer)
+      // One thread: with votes of all lanes at its waits it took 40 cycles a slice longer
+      // than the MMAs.
+      uint32_t issued = 0;
+      if (ptx::elect_one()) {
+        const uint64_t pol_a = ptx::policy_evict_last();
+        const uint64_t pol_b = s.n_mt > 1 ? ptx::policy_evict_normal() : ptx::policy_evict_first();
+        auto load = [&](uint8_t* dst, const CUtensorMap* map, uint32_t stage, int x, int y,
+                        uint64_t pol) {
+          if constexpr (kPair)
+            ptx::tma_load_2d_pair(dst, map, ptx::cluster_addr(&full_bar[stage], 0), x, y, pol);
+          else
+            ptx::tma_load_2d(dst, map, &full_bar[stage], x, y, pol);
+        };
+        // Rows past the end read as 0.
+        auto load_a = [&](uint32_t stage, int kb, int mt) {
+          load(smem + size_t(stage) * s.stage_bytes, &tmap_a, stage, kb * kBK,
+               (mt * kCtas + rank) * kBM, pol_a);
+        };
+        uint32_t stage = 0, phase = 0;
+        bool ok = true;
+        // The first ring fill's A copies, held back until the kernel before is done.
+        bool deferring = s.pdl != 0;
+        int n_held = 0, held_kb[kMaxStages], held_mt[kMaxStages];
+        auto release = [&]() {
+          ptx::grid_dependency_wait();
           for (int h = 0; h < n_held; ++h) load_a(uint32_t(h), held_kb[h], held_mt[h]);
-        deferring = false;
-      };
-      for (int u = worker; ok && u < s.n_units; u += n_workers) {
-        const int nt = u / s.n_mt, mt = u - nt * s.n_mt;
-        for (int kb = 0; kb < s.n_kb; ++kb) {
-          if (!waiter.wait_warp(&empty_bar[stage], phase ^ 1u)) {
-            ok = false;
-            break;
-          }
-          if (issuer) {
+          deferring = false;
+        };
+        for (int u = worker; ok && u < s.n_units; u += n_workers) {
+          const int nt = u / s.n_mt, mt = u - nt * s.n_mt;
+          for (int kb = 0; kb < s.n_kb; ++kb) {
+            if (!waiter.wait(&empty_bar[stage], phase ^ 1u)) {
+              ok = false;
+              break;
+            }
             if (leader)
               ptx::mbar_arrive_expect_tx(&full_bar[stage], kCtas * (s.a_bytes + kBBytes));
             // A part's columns of a pair's tile lie half in each CTA.
@@ -580,20 +581,21 @@ __global__ void __launch_bounds__(kThreads, 1)
               load(smem + size_t(stage) * s.stage_bytes + s.a_bytes + h * kPartRows * kBK, &tmap_b,
                    stage, kb * kBK, nt * kN + h * (kN / kParts) + rank * kPartRows, pol_b);
             if (!deferring) load_a(stage, kb, mt);
+            if (deferring) {  // the first fill: stage n_held
+              held_kb[n_held] = kb;
+              held_mt[n_held++] = mt;
+            }
+            ++issued;
+            if (++stage == s.n_stages) {
+              stage = 0;
+              phase ^= 1u;
+            }
+            if (deferring && n_held == int(s.n_stages)) release();
           }
-          if (deferring) {  // the first fill: stage n_held
-            held_kb[n_held] = kb;
-            held_mt[n_held++] = mt;
-          }
-          ++issued;
-          if (++stage == s.n_stages) {
-            stage = 0;
-            phase ^= 1u;
-          }
-          if (deferring && n_held == int(s.n_stages)) release();
         }
+        if (deferring) release();
       }
-      if (deferring) release();
+      issued = __reduce_max_sync(0xFFFFFFFFu, issued);
       // Every issued copy lands before the CTA's shared memory goes away (the
       // leader's barriers see both CTAs' copies).
       if (leader) {
