@@ -294,13 +294,14 @@ __global__ void __launch_bounds__(kTileThreads) quantize_tile_kernel(const Quant
 //
 // Bound: W's bytes for few rows (one row at d = 4096, V = 151936 takes 92 us, 6.75 TB/s; 128
 // rows 114).  For many, what follows the MMAs: an accumulator's 256 columns are 128 additions
-// of two values a thread, and an accumulator is free again 1200 cycles after its MMAs were
+// of two values a thread, and an accumulator is free again some 1200 cycles after its MMAs were
 // issued (256 a part, 340 until the sums' warps know, 340 until they have loaded it, 270 until
-// the next MMAs run), of which two overlap: 876 cycles a slice where the MMAs alone take 640 with
-// their waits and 512 at the nominal rate.  1000 rows: 487 us in bursts, 550 held at the power
-// limit (2560 and 2260 TFLOP/s).  First 1045: tensor-memory loads one at a time with their
-// additions between, scales read by the same warps (a wait for tensor-memory loads waits for
-// those too), outputs stored from registers.
+// the next MMAs run), of which two overlap: 810 cycles a slice where the MMAs alone take 640 with
+// their waits and 512 at the nominal rate.  1000 rows: 455 us in bursts, 2740 TFLOP/s.  First
+// 1045: tensor-memory loads one at a time with their additions between, scales read by the same
+// warps (a wait for tensor-memory loads waits for those too), outputs stored from registers,
+// all lanes at every wait.  Polling is not free here: the same waits without the clock reads
+// between their tries took 790 us.
 // ---------------------------------------------------------------------------
 using vocab::BoundedWait;
 using vocab::kEpiWarps;
@@ -396,8 +397,9 @@ struct Box {
 // that it cannot write, behind the last whole 16 bytes or of rows off 16-byte boundaries,
 // go row by row.
 template <int kCols, bool kF32, int kBoxes>
-__device__ __forceinline__ void store_sums(const Plan& s, const void* tmap, uint8_t* boxes, int lane,
-                                           const float (&sum)[kCols], int row0, int col0) {
+__device__ __forceinline__ void store_sums(const Plan& s, const void* tmap, uint8_t* boxes,
+                                           int lane, const float (&sum)[kCols], int row0,
+                                           int col0) {
   using B = Box<kCols, kF32>;
 #pragma unroll
   for (int part = 0; part < kCols / B::kWidth; ++part) {
@@ -695,9 +697,10 @@ __global__ void __launch_bounds__(kThreads, 1)
               four(s.a_scale + int64_t(min(row0 + 32 * j + lane, s.M - 1)) * s.lda_scale + kb,
                    v[j]);
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
-              four(s.w_scale + int64_t(min(nt * kN + h * kCols, s.V - 1) / kBlock) * s.ldw_scale + kb,
-                   w[h]);
+            for (int h = 0; h < 2; ++h) {
+              const int row = min(nt * kN + h * kCols, s.V - 1) / kBlock;
+              four(s.w_scale + int64_t(row) * s.ldw_scale + kb, w[h]);
+            }
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
 #pragma unroll
@@ -895,8 +898,8 @@ bool known(int dtype) { return dtype == FS_BF16 || dtype == FS_F32; }
 template <int kN, bool kPair>
 bool prepare_kernel(int sms, int* pairs) {
   auto k = matmul_kernel<kN, kPair>;
-  if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, int(Layout<kPair>::kBytes)) !=
-      cudaSuccess)
+  if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           int(Layout<kPair>::kBytes)) != cudaSuccess)
     return false;
   if (!kPair) return true;
   cudaLaunchAttribute attr;
@@ -999,7 +1002,8 @@ fs_status launch(const Device& dev, const fs_matmul_fp8_args& a, Plan s, cudaStr
   to = tb;  // where nothing goes by it
   if (s.whole_v > 0) {
     const int64_t ldo = a.M > 1 ? a.ldo : ceil_div(a.V, 8) * 8;
-    const auto type = s.out_f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    const auto type =
+        s.out_f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
     const int width = s.out_f32 ? Box<kN / 2, true>::kWidth : Box<kN / 2, false>::kWidth;
     if (!encode(dev, &to, type, s.out_f32 ? 4 : 2, a.out, s.whole_v, a.M, ldo, width, 32))
       return FS_ERR_CUDA;
@@ -1140,11 +1144,12 @@ extern "C" fs_status fs_matmul_fp8(const fs_matmul_fp8_args* args, void* stream_
   if (n_mt * ceil_div(a.V, 128) <= dev->sms) return launch<128, false>(*dev, a, s, stream);
   if (a.M <= kBM) return launch<256, false>(*dev, a, s, stream);
   // CTA pairs read W once for 256 rows, but take 256 at a time.  Where the last ones are few,
-  // single CTAs need fewer turns, each 1.12 times as long: at d = 4096, V = 128256, pairs / single
-  // CTAs, 200 rows 120 / 149 us, 320 219 / 191, 600 317 / 310, 1000 (V = 151936) 510 / 568.
+  // single CTAs need fewer turns, each 1.25 times as long: at d = 4096, V = 128256, pairs / single
+  // CTAs, 200 rows 116 / 144 us, 320 201 / 185, 450 209 / 248, 600 287 / 295, 1000 (V = 151936)
+  // 455 / 542.
   const int64_t n_nt = ceil_div(a.V, 256);
   const int64_t pair_turns = ceil_div(ceil_div(a.M, 2 * kBM) * n_nt, dev->pairs);
   const int64_t single_turns = ceil_div(n_mt * n_nt, dev->sms);
-  return single_turns * 9 < pair_turns * 8 ? launch<256, false>(*dev, a, s, stream)
+  return single_turns * 5 < pair_turns * 4 ? launch<256, false>(*dev, a, s, stream)
                                            : launch<256, true>(*dev, a, s, stream);
 }
