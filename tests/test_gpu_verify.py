@@ -1,6 +1,9 @@
 """Probabilities from logits and the verification of drafted tokens on the GPU against
 the forms of speculate_ref, and the operators of speculative decoding together."""
 import math
+import os
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -14,6 +17,7 @@ from oracle.merge import chi_square_gof
 pytestmark = pytest.mark.gpu
 
 TYPES = [torch.bfloat16, torch.float32]
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -449,6 +453,32 @@ def test_a_very_long_row():
         check_verify(p, ids, torch.tensor([u, u], device="cuda"), q)
     x = z.view(4, V)[:, :V]
     check_probs(x)
+
+
+@pytest.mark.parametrize("call", [
+    "fs.fs_quantize(x).scale", "fs.fs_matmul_fp8(*fs.fs_quantize(x), *fs.fs_quantize(w, 128))",
+    "fs.fs_probs(w)", "fs.fs_verify(p, ids, u).ids"])
+def test_first_calls_of_a_process_in_a_captured_graph(call):
+    code = f"""
+import sys
+sys.path.insert(0, {ROOT!r})
+import torch, lm_head_gumbel_gb300 as fs
+gen = torch.Generator(device="cuda").manual_seed(1)
+x = torch.randn((40, 30000), generator=gen, device="cuda")
+w = torch.randn((300, 30000), generator=gen, device="cuda")
+p = torch.rand((2, 3, 160000), generator=gen, device="cuda") * 1e-5
+ids = torch.randint(0, 1000, (2, 2), generator=gen, device="cuda")
+u = torch.rand((2, 3), generator=gen, device="cuda")
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    out = {call}
+graph.replay()
+torch.cuda.synchronize()
+assert torch.equal(out, {call})
+"""
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
 
 
 # --------------------------------------------------------------------------- together
