@@ -89,6 +89,26 @@ def test_quantize_extremes(block):
     check_quantized(x, block)
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("block", [1, 128])
+def test_quantize_rounds_each_division_once(block, dtype):
+    """448 / a and a / 448 are the nearest fp32 values, which a rounded reciprocal times 448 (or a
+    times a rounded 1 / 448) often is not; it decides values on a middle between two e4m3 ones."""
+    gen = torch.Generator().manual_seed(40 + block)
+    n = 4096 if block == 1 else 128 * 40
+    x = torch.randn((n, 128 * 8), generator=gen).to(dtype)
+    got = fs.fs_quantize(x.cuda(), block)
+    top = x.double().abs().view(n // block, block, 8, 128).amax((1, 3))
+    # 64 bits are more than twice 24 and 2: the second rounding changes nothing
+    inverse, scale = (448.0 / top).float(), (top / 448.0).float()
+    two = torch.full_like(inverse, 448.0) * (torch.ones_like(inverse) / top.float())
+    assert bool((two != inverse).any())  # the inputs tell the two apart
+    assert torch.equal(got.scale.cpu(), scale)
+    wide = inverse.repeat_interleave(block, 0).repeat_interleave(128, 1)
+    want = (x.float() * wide).clamp(-448.0, 448.0).to(torch.float8_e4m3fn)
+    same_bits(got.values, want, torch.uint8)
+
+
 def test_quantize_of_nothing():
     r = fs.fs_quantize(torch.zeros((0, 300), device="cuda"))
     assert r.values.shape == (0, 300) and r.scale.shape == (0, 3)
