@@ -992,7 +992,8 @@ using namespace fs::verify;
 extern "C" fs_status fs_probs(const fs_probs_args* args, void* stream_ptr) {
   if (!args) return FS_ERR_INVALID_ARG;
   const fs_probs_args& a = *args;
-  if (a.N < 0 || a.N > INT_MAX / kMaxProbCluster || a.V < 1 || a.V > kMostV || !known(a.dtype) ||
+  // (A long row is a CTA; of the others' grid there are never more CTAs than fit at once.)
+  if (a.N < 0 || a.N >= (1 << 28) || a.V < 1 || a.V > kMostV || !known(a.dtype) ||
       !known(a.out_dtype))
     return FS_ERR_INVALID_ARG;
   if (a.N == 0) return FS_OK;

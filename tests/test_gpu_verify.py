@@ -222,6 +222,15 @@ def test_probs_refusals():
     assert fs.fs_probs(x[:0]).shape == (0, 100)
 
 
+def test_probs_of_very_many_rows():
+    """More rows than 16 CTAs each would leave 32 bits for."""
+    N = 2 ** 27 + 3
+    x = torch.zeros((N, 1), dtype=torch.bfloat16, device="cuda")
+    x[::5] = -float("inf")
+    got = fs.fs_probs(x, out=x)
+    assert bool((got[::5] == 0).all()) and int((got == 1).sum()) == N - (N + 4) // 5
+
+
 # --------------------------------------------------------------------------- verification
 def problem(B, K, V, dtype, *, seed=0, near=0.5, std=3.0, ragged=False, q=True, ld=None):
     gen = torch.Generator().manual_seed(seed)

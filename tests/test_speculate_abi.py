@@ -11,6 +11,7 @@ import pytest
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 HEADER = os.path.join(ROOT, "include", "fs_speculate.h")
 INVALID = 1
+UNSUPPORTED = 2  # no device
 
 
 @pytest.fixture(scope="module")
@@ -163,3 +164,13 @@ def test_the_module_refuses_what_the_library_cannot_see(lib):
         with pytest.raises(fs.FsError) as e:
             call()
         assert e.value.status == INVALID
+
+
+@pytest.mark.parametrize("V,ld", [(1, 1), (1000, 1000), (300000, 300000)])
+def test_probs_takes_every_documented_number_of_rows(lib, V, ld):
+    """0 <= N < 2^28: one row more is refused, as an argument; the largest number is not."""
+    import torch
+    if torch.cuda.is_available():
+        pytest.skip("the pointers are made up")
+    for N, status in ((2**28, INVALID), (2**28 - 1, UNSUPPORTED), (2**27, UNSUPPORTED)):
+        assert lib.fs_probs(ctypes.byref(_probs(N=N, V=V, ldl=ld, ldo=ld)), None) == status
