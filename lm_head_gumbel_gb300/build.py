@@ -19,7 +19,8 @@ MARSHAL_DEPENDS = [os.path.join(CSRC, "fs_marshal.cpp")] + [
 SOURCES = [os.path.join(CSRC, f) for f in ("fs_sample.cu", "fs_merge.cu", "fs_logprobs.cu",
                                           "fs_embed.cu", "fs_fp8.cu", "fs_verify.cu")]
 DEPENDS = SOURCES + [os.path.join(CSRC, f) for f in ("fs_kernels.cuh", "fs_ptx.cuh",
-                                                    "fs_noise.cuh", "fs_contract.cuh")] + [
+                                                    "fs_noise.cuh", "fs_contract.cuh",
+                                                    "fs_pieces.h")] + [
     os.path.join(INCLUDE, f) for f in ("fs_sample.h", "fs_vocab.h",
                                                   "fs_speculate.h")]
 

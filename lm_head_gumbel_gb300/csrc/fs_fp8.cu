@@ -11,6 +11,7 @@
 #include <type_traits>
 
 #include "fs_contract.cuh"
+#include "fs_pieces.h"
 #include "fs_ptx.cuh"
 #include "fs_speculate.h"
 
@@ -105,11 +106,10 @@ struct Eight {
   uint32_t w[2 * sizeof(T)];
 };
 // Those from x, of which n exist, the others 0, are read in two steps, so that the first
-// of several pieces can be in flight at once: whole ones (of rows on 16-byte boundaries;
-// past a row's end lies the next row, so `last` rows are left out), then what is left.
+// of several pieces can be in flight at once: whole ones (fs_pieces.h), then what is left.
 template <class T, bool kVec>
 __device__ __forceinline__ bool load_whole(Eight<T>& e, const T* x, int n, bool last) {
-  const bool can = kVec && (last ? n >= 8 : n > 0);
+  const bool can = kVec && whole_piece(n, last);
 #pragma unroll
   for (int i = 0; i < int(sizeof(T)) / 2; ++i) {
     uint4 v = make_uint4(0u, 0u, 0u, 0u);
@@ -1088,8 +1088,8 @@ extern "C" fs_status fs_quantize(const void* x, int64_t N, int64_t d, int64_t ld
   p.N = int32_t(N);
   p.d = int32_t(d);
   p.col_blocks = int32_t(col_blocks);
-  const bool vec = aligned(x, 16) && p.ldx * element(x_dtype) % 16 == 0 && aligned(values, 8) &&
-                   p.ldv % 8 == 0;
+  const bool vec = whole_pieces(reinterpret_cast<uintptr_t>(x), N, p.ldx, int(element(x_dtype))) &&
+                   aligned(values, 8) && p.ldv % 8 == 0;
   cudaStream_t stream = static_cast<cudaStream_t>(stream_ptr);
   if (x_dtype == FS_F32)
     vec ? launch_quantize<float, true>(p, block_rows, per, ctas, stream)

@@ -109,6 +109,17 @@ def test_quantize_rounds_each_division_once(block, dtype):
     same_bits(got.values, want, torch.uint8)
 
 
+@pytest.mark.parametrize("block", [1, 128])
+@pytest.mark.parametrize("N,d,ld", [(2, 1, 4), (5, 3, 4), (130, 2, 4), (300, 4, 4), (3, 5, 8), (3, 9, 12)])
+def test_quantize_of_very_narrow_rows(N, d, ld, block):
+    """fp32 rows 16 bytes apart, up to the end of their buffer."""
+    gen = torch.Generator().manual_seed(N)
+    buf = torch.full(((N - 1) * ld + d,), float("nan"), device="cuda")
+    x = buf.as_strided((N, d), (ld, 1))
+    x.copy_(torch.randn((N, d), generator=gen))
+    check_quantized(x, block)
+
+
 def test_quantize_of_nothing():
     r = fs.fs_quantize(torch.zeros((0, 300), device="cuda"))
     assert r.values.shape == (0, 300) and r.scale.shape == (0, 3)

@@ -174,3 +174,40 @@ def test_probs_takes_every_documented_number_of_rows(lib, V, ld):
         pytest.skip("the pointers are made up")
     for N, status in ((2**28, INVALID), (2**28 - 1, UNSUPPORTED), (2**27, UNSUPPORTED)):
         assert lib.fs_probs(ctypes.byref(_probs(N=N, V=V, ldl=ld, ldo=ld)), None) == status
+
+
+PIECES = r"""
+#include <cstdio>
+#include "fs_pieces.h"
+using namespace fs::fp8;
+// Every piece that is read whole, of every small matrix, ends inside it: N rows of d elements,
+// ldx apart, have (N - 1) ldx + d.
+int main() {
+  int bad = 0, whole = 0;
+  for (int size = 2; size <= 4; size += 2)
+    for (int N = 1; N <= 5; ++N)
+      for (int d = 1; d <= 40; ++d)
+        for (int ldx = d; ldx <= d + 20; ++ldx) {
+          if (!whole_pieces(0x1000, N, N > 1 ? ldx : 0, size)) continue;
+          for (int row = 0; row < N; ++row)
+            for (int col = 0; col < d; col += kPiece) {
+              if (!whole_piece(d - col, row == N - 1)) continue;
+              ++whole;
+              if (row * ldx + col + kPiece > (N - 1) * ldx + d) {
+                if (bad++ < 5) printf("size %d: [%d, %d], stride %d, row %d, column %d\n", size, N, d, ldx, row, col);
+              }
+            }
+        }
+  if (whole == 0) printf("no piece\n");
+  return bad != 0 || whole == 0;
+}
+"""
+
+
+def test_quantisation_reads_inside_its_matrix(tmp_path):
+    src, exe = tmp_path / "pieces.cpp", tmp_path / "pieces"
+    src.write_text(PIECES)
+    subprocess.run(["g++", "-std=c++17", "-I", os.path.join(ROOT, "lm_head_gumbel_gb300", "csrc"),
+                    str(src), "-o", str(exe)], check=True)
+    r = subprocess.run([str(exe)], capture_output=True, text=True)
+    assert r.returncode == 0, r.stdout
