@@ -71,7 +71,10 @@ typedef struct fs_matmul_fp8_args {
   int64_t ldo;
   int out_dtype;
   /* FS_FLAG_OVERLAP_PREVIOUS or 0: with it W streams while the kernel before on the
-   * stream ends, which may write A and a_scale but neither W nor w_scale. */
+   * stream ends, which may write A and a_scale but neither W nor w_scale.  If that kernel was
+   * itself launched so and lets its dependents start at once (an overlapping sampling call),
+   * neither may the one before it.  The product lets its dependents start once the
+   * kernel before it has ended, with the flag and without. */
   uint32_t flags;
 } fs_matmul_fp8_args;
 

@@ -529,10 +529,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   if constexpr (kPair) ptx::cluster_sync();
   ptx::tc_fence_after();
-  ptx::grid_launch_dependents();
   // The launch always overlaps the kernel before it on the stream; without the caller's
-  // word only this set-up does.
-  if (!s.pdl) ptx::grid_dependency_wait();
+  // word only this set-up does.  Its own dependents may start once that kernel has ended (with
+  // the caller's word a warp says so later): what they read ahead cannot be what a kernel
+  // further back still writes.
+  if (!s.pdl) {
+    ptx::grid_dependency_wait();
+    ptx::grid_launch_dependents();
+  }
   const uint32_t tmem_base = *tmem_holder;
   const BoundedWait waiter{abort_flag, s.wait_limit_ns, s.error_word};
 
@@ -668,7 +672,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ---------------- scales ----------------
       // From memory by a warp of its own: a wait for tensor-memory loads waits for a
       // warp's loads from memory too (450 cycles every four slices).
-      if (s.pdl) ptx::grid_dependency_wait();
+      if (s.pdl) {
+        ptx::grid_dependency_wait();
+        ptx::grid_launch_dependents();
+      }
       uint32_t g = 0, phase = 0;
       bool ok = true;
       for (int u = worker; ok && u < s.n_units; u += n_workers) {
