@@ -133,7 +133,9 @@ typedef struct fs_sample_args {
  * as without the flag.  The results are the same with or without it.  Used by
  * fs_sample, fs_sample_noalloc, fs_sample_host (whose own copy kernel already
  * overlaps it when in_bytes > 0) and fs_sample_topk.  The library's sampling
- * kernels allow such a dependent to be scheduled as soon as they start.
+ * kernels allow such a dependent to be scheduled as soon as they start: behind
+ * one that overlaps its own predecessor, that one may still be running too, and
+ * must not write W either.
  */
 #define FS_FLAG_OVERLAP_PREVIOUS 1u
 
