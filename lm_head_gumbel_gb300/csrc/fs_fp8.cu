@@ -617,6 +617,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       // on the chain that bounds the kernel (votes of the warp's lanes at its waits: 20 cycles a
       // slice of 890).
       if (leader && ptx::elect_one()) {
+        // A's copies come behind the kernel before; its time does not count against a wait's limit.
+        if (s.pdl) ptx::grid_dependency_wait();
         uint32_t stage = 0, phase = 0, acc_phases = 0;  // a bit for each accumulator
         bool ok = true;
         const uint32_t s0 = ptx::smem_u32(smem);

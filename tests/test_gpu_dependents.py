@@ -68,3 +68,17 @@ def test_product_starts_nothing_before_its_predecessor_has_ended(late_copy, flag
         got = fs.fs_matmul_fp8(*a, written, w.scale, overlap_previous=True)
         torch.cuda.synchronize()
         assert torch.equal(got_other, want_other) and torch.equal(got, want)
+
+
+@pytest.mark.parametrize("M", [3, 200])
+def test_product_waits_as_long_as_its_predecessor_takes(late_copy, M):
+    """The limit of a device wait (2 s) is not for the kernel that makes A."""
+    a, w = hidden(M, 512, 1), head(3000, 512, 3)
+    want = fs.fs_matmul_fp8(*a, *w)
+    A = torch.zeros_like(a.values)
+    torch.cuda.synchronize()
+    late_copy(A, a.values, 2600)
+    got = fs.fs_matmul_fp8(A, a.scale, *w, overlap_previous=True)
+    torch.cuda.synchronize()
+    assert fs.fs_last_device_error() == (fs.FS_OK, 0)
+    assert torch.equal(got, want)
