@@ -462,6 +462,8 @@ __device__ __forceinline__ void contract(const CUtensorMap& tmap_a, const CUtens
   } else if (warp == 1) {
     // ---------------- MMA issuer (the leader CTA's) ----------------
     if (leader) {
+      // A's copies come behind the kernel before; its time does not count against a wait's limit.
+      if (s.pdl) ptx::grid_dependency_wait();
       const bool issuer = ptx::elect_one();
       uint32_t stage = 0, phase = 0, acc = 0, acc_phase = 0;
       bool ok = true;

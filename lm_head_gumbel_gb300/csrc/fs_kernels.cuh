@@ -757,6 +757,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     // below 256 KB, so the 14-bit field never carries), and a K step of 16
     // bf16 (32 bytes) adds 2.
     {
+      // H's copies come behind the kernel before; its time does not count against a wait's limit.
+      if (p.pdl) ptx::grid_dependency_wait();
       const bool issuer = ptx::elect_one();
       uint32_t stage = 0, phase = 0, acc = 0, acc_phase = 0;
       bool ok = true;
@@ -1029,6 +1031,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---------------- MMA issuer (leader CTA only) ----------------
     // Warp-wide, one elected lane issuing (as in stage1_kernel).
     if (leader) {
+      if (p.pdl) ptx::grid_dependency_wait();  // as in stage1_kernel
       const bool issuer = ptx::elect_one();
       uint32_t stage = 0, phase = 0, acc = 0, acc_phase = 0;
       bool ok = true;

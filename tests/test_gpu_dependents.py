@@ -82,3 +82,27 @@ def test_product_waits_as_long_as_its_predecessor_takes(late_copy, M):
     torch.cuda.synchronize()
     assert fs.fs_last_device_error() == (fs.FS_OK, 0)
     assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("B", [4, 200])
+@pytest.mark.parametrize("call", ["sample", "logprobs"])
+def test_sampler_and_logprobs_wait_as_long_as_their_predecessor_takes(late_copy, call, B):
+    """The same of the kernel that makes H, for single CTAs and pairs."""
+    gen = torch.Generator().manual_seed(B)
+    H = torch.randn((B, 256), generator=gen).bfloat16().cuda()
+    W = (torch.randn((3000, 256), generator=gen) * 0.1).bfloat16().cuda()
+    ids = torch.randint(0, 3000, (B,), generator=gen).cuda()
+
+    def run(h, overlap):
+        if call == "sample":
+            return fs.fs_sample(h, W, seed=5, offset=1, overlap_previous=overlap)
+        return fs.fs_logprobs(h, W, ids, overlap_previous=overlap).logp
+
+    want = run(H, False)
+    late = torch.zeros_like(H)
+    torch.cuda.synchronize()
+    late_copy(late, H, 2600)
+    got = run(late, True)
+    torch.cuda.synchronize()
+    assert fs.fs_last_device_error() == (fs.FS_OK, 0)
+    assert torch.equal(got, want)
