@@ -632,19 +632,20 @@ struct alignas(16) Shared {
   int gave_up;
 };
 
-// The segments' sums are there, or the wait's limit has passed: then the error word says so.
-__device__ __forceinline__ void wait_arrived(const VerifyParams& a, Shared& sm) {
-  if (!ptx::mbar_try_wait(&sm.arrived, 0)) {
+// The segments' sums are there, or (false) the wait's limit has passed: then the error word
+// says so.  One warp.
+__device__ __forceinline__ bool wait_arrived(const VerifyParams& a, Shared& sm) {
+  bool there = ptx::mbar_try_wait(&sm.arrived, 0);
+  if (!there) {
     const uint64_t t0 = ptx::global_timer_ns();
-    while (!ptx::mbar_try_wait(&sm.arrived, 0)) {
+    while (!(there = ptx::mbar_try_wait(&sm.arrived, 0))) {
       if (ptx::global_timer_ns() - t0 > a.wait_limit_ns) {
         atomicOr(a.error_word, kErrWaitTimeout);
-        sm.gave_up = 1;
         break;
       }
     }
   }
-  __syncwarp();
+  return __all_sync(0xFFFFFFFFu, there);
 }
 
 // How many drafts pass, and what the next token is drawn from.  One warp.
@@ -706,7 +707,7 @@ __device__ __forceinline__ bool find_segment(const VerifyParams& a, float u, Sha
   const int at = past != 0u ? __ffs(past) - 1 : 31 - __clz(some);
   if (lane == at) {
     Sum before = ahead, run = ahead;
-    int chosen = -1;
+    int chosen = s0;
     for (int s = s0; s < s1; ++s) {
       const Sum x = sm.sums[s];
       if (!(x.hi > 0.0f)) continue;
@@ -772,6 +773,37 @@ __device__ __forceinline__ int find_element(const VerifyParams& a, const Weights
   return sm.first != INT_MAX ? sm.first : sm.last;
 }
 
+// The token drawn with the weights w, once the segments' sums have arrived; -1 if all of them
+// are 0.  After a wait that ran out it is -1 too: what lies in the sums' places is not looked at,
+// and not written either, since others may still store there.  All threads.
+template <class T>
+__device__ __forceinline__ int draw(const VerifyParams& a, Weights<T>& w, float u, bool vec,
+                                    Shared& sm) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (warp == 0) {
+    const bool there = wait_arrived(a, sm);
+    const bool some = there && find_segment(a, u, sm, lane);
+    if (lane == 0) sm.found = some, sm.gave_up = !there;
+  }
+  __syncthreads();
+  if (!sm.found && !sm.gave_up && w.mode != kTarget) {
+    // Nothing is left of p after a rejection: the draw is from p.
+    w.mode = kTarget;
+    for (int s = warp; s < a.n_segments; s += kWarps) {
+      const int begin = s * a.segment;
+      const Sum t = segment_sum(w, begin, min(a.segment, a.V - begin), a.segment, vec, lane);
+      if (lane == 0) sm.sums[s] = t;
+    }
+    __syncthreads();
+    if (warp == 0) {
+      const bool some = find_segment(a, u, sm, lane);
+      if (lane == 0) sm.found = some;
+    }
+    __syncthreads();
+  }
+  return sm.found ? find_element(a, w, sm) : -1;
+}
+
 // A sequence to a cluster of CTAs.  Each finds out which drafts pass (that is 2 dependent reads,
 // and less than telling one another); the row's segments go around their warps; the first CTA
 // gathers the segments' sums, finds the segment that u falls into and sums that again, element
@@ -785,7 +817,6 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyParams 
   const int rank = int(ptx::cluster_ctarank());
   const int64_t b = blockIdx.x / n_ctas;
   if (threadIdx.x == 0) {
-    sm.gave_up = 0;
     ptx::mbar_init(&sm.arrived, 1);
     ptx::fence_barrier_init();
     if (rank == 0) ptx::mbar_arrive_expect_tx(&sm.arrived, uint32_t(a.n_segments) * 8u);
@@ -816,34 +847,16 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyParams 
           : "memory");
   }
   if (rank != 0) return;
-  if (warp == 0) {
-    wait_arrived(a, sm);
-    const bool some = find_segment(a, u, sm, lane);
-    if (lane == 0) sm.found = some;
-  }
-  __syncthreads();
-  if (!sm.found && w.mode != kTarget) {
-    // Nothing is left of p after a rejection: the draw is from p.
-    w.mode = kTarget;
-    for (int s = warp; s < a.n_segments; s += kWarps) {
-      const int begin = s * a.segment;
-      const Sum t = segment_sum(w, begin, min(a.segment, a.V - begin), a.segment, vec, lane);
-      if (lane == 0) sm.sums[s] = t;
-    }
-    __syncthreads();
-    if (warp == 0) {
-      const bool some = find_segment(a, u, sm, lane);
-      if (lane == 0) sm.found = some;
-    }
-    __syncthreads();
-  }
-  const int drawn = sm.found ? find_element(a, w, sm) : -1;
+  const int drawn = draw(a, w, u, vec, sm);
   for (int i = threadIdx.x; i <= a.K; i += kThreads)
     a.out_ids[b * a.ld_out + i] = i < n ? a.ids[b * a.ld_ids + i] : i == n ? int64_t(drawn) : -1;
   if (threadIdx.x == 0 && a.accepted) a.accepted[b] = n;
   // After a wait that ran out the others may still store here: this CTA ends behind them
-  // (the barrier is of those that have not ended).
-  if (sm.gave_up) ptx::cluster_sync();
+  // (the barrier is of those that have not ended) and their stores.
+  if (sm.gave_up) {
+    ptx::cluster_sync();
+    if (warp == 0) wait_arrived(a, sm);
+  }
 }
 
 // ---------------------------------------------------------------------------
