@@ -142,6 +142,7 @@ struct alignas(16) ProbsShared {
   uint32_t mask[2][kMaxPart / 32];  // this row's and the next one's words
   uint64_t full;                    // the row's elements have arrived
   uint64_t told[2];                 // every CTA's word has
+  uint32_t copies;                  // issued so far
   uint32_t gave_up;
 };
 
@@ -158,12 +159,18 @@ __device__ __forceinline__ void wait_for(const ProbsParams& p, ProbsShared& sm, 
     }
   }
 }
+// Behind a wait of this thread: whether it has ended well, and so the phase is complete.
+__device__ __forceinline__ bool waited_well(ProbsShared& sm) {
+  return !*static_cast<volatile uint32_t*>(&sm.gave_up);
+}
 // This warp's word into its slot in every CTA of the cluster, by stores that count on the
 // receiver's barrier.  (A cluster's barrier would also wait for the stores of the row before.)
 // A word of the next row cannot overtake: its sender has had this row's words from everyone.
+// After a wait that ran out nothing is told, so that the others' waits run out too.
 __device__ __forceinline__ void tell(uint32_t* slots, uint64_t* bar, int rank, int n_ctas,
-                                     uint32_t v) {
+                                     uint32_t v, bool well) {
   const uint32_t lane = threadIdx.x & 31;
+  if (!well) return;
   if (threadIdx.x == 0) ptx::mbar_arrive_expect_tx(bar, uint32_t(n_ctas * kProbWarps) * 4u);
   if (int(lane) < n_ctas)
     asm volatile(
@@ -227,7 +234,7 @@ __global__ void __launch_bounds__(kProbThreads, 2) probs_kernel(const ProbsParam
     ptx::mbar_init(&sm.told[0], 1);
     ptx::mbar_init(&sm.told[1], 1);
     ptx::fence_barrier_init();
-    sm.gave_up = 0u;
+    sm.copies = sm.gave_up = 0u;
   }
   if (threadIdx.x < kMaxProbCluster * kProbWarps) {
     sm.first[threadIdx.x] = 0xFF800000u;  // -infinity
@@ -253,8 +260,11 @@ __global__ void __launch_bounds__(kProbThreads, 2) probs_kernel(const ProbsParam
   if (p.mask) sm.mask[0][threadIdx.x] = mask_word(row);
   float temp = p.temperature ? p.temperature[row] : 1.0f;
   __syncthreads();
-  if (copied > 0 && threadIdx.x == 0)
+  auto copy_row = [&](int64_t row) {  // one thread
     copy_async(buffer, row_of(row), uint32_t(copied) * sizeof(T), &sm.full);
+    ++sm.copies;
+  };
+  if (copied > 0 && threadIdx.x == 0) copy_row(row);
   ptx::cluster_sync();  // every CTA has started before another one writes its memory
   const int i0 = int(threadIdx.x) * 4;
   for (int turn = 0; row < p.N; ++turn) {
@@ -296,12 +306,12 @@ __global__ void __launch_bounds__(kProbThreads, 2) probs_kernel(const ProbsParam
 #pragma unroll
         for (int k = 0; k < 4; ++k) m = max_nan(m, l[g][k]);
     }
+    const bool well = waited_well(sm);
 #pragma unroll
     for (int s = 16; s > 0; s >>= 1) m = max_nan(m, __shfl_xor_sync(0xFFFFFFFFu, m, s));
-    tell(sm.first, &sm.told[0], rank, n_ctas, __float_as_uint(m));
+    tell(sm.first, &sm.told[0], rank, n_ctas, __float_as_uint(m), well);
     __syncthreads();  // every thread has read the buffer
-    if (more && copied > 0 && threadIdx.x == 0)
-      copy_async(buffer, row_of(next), uint32_t(copied) * sizeof(T), &sm.full);
+    if (more && copied > 0 && threadIdx.x == 0 && well) copy_row(next);
     if (more) copy_end(row_of(next));
     const uint32_t next_word = more && p.mask ? mask_word(next) : 0u;
     const float next_temp = more && p.temperature ? p.temperature[next] : 1.0f;
@@ -320,7 +330,7 @@ __global__ void __launch_bounds__(kProbThreads, 2) probs_kernel(const ProbsParam
       }
       at = INT_MAX - __reduce_min_sync(0xFFFFFFFFu, at);
       sm.mask[phase ^ 1u][threadIdx.x] = next_word;
-      tell(sm.second, &sm.told[1], rank, n_ctas, uint32_t(at));
+      tell(sm.second, &sm.told[1], rank, n_ctas, uint32_t(at), waited_well(sm));
       __syncthreads();
       wait_for(p, sm, &sm.told[1], phase);
       at = 0;
@@ -361,10 +371,11 @@ __global__ void __launch_bounds__(kProbThreads, 2) probs_kernel(const ProbsParam
         }
         sum = 1.0f;
       }
+      const bool well = waited_well(sm);
 #pragma unroll
       for (int s = 16; s > 0; s >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, s);
       sm.mask[phase ^ 1u][threadIdx.x] = next_word;
-      tell(sm.second, &sm.told[1], rank, n_ctas, __float_as_uint(sum));
+      tell(sm.second, &sm.told[1], rank, n_ctas, __float_as_uint(sum), well);
       __syncthreads();
       wait_for(p, sm, &sm.told[1], phase);
       sum = of_slots(sm.second, n_ctas, [](float a, float b) { return a + b; });
@@ -380,10 +391,18 @@ __global__ void __launch_bounds__(kProbThreads, 2) probs_kernel(const ProbsParam
     row = next;
     temp = next_temp;
   }
-  // After a wait that ran out the others may still store here: this CTA ends behind them
-  // (the barrier is of those that have not ended).
+  // After a wait that ran out a copy may be on its way, and the others may still store here: this
+  // CTA ends behind them (the barrier is of those that have not ended).
   __syncthreads();
-  if (sm.gave_up) ptx::cluster_sync();
+  if (sm.gave_up) {
+    if (threadIdx.x == 0 && sm.copies > 0) {
+      const uint64_t t0 = ptx::global_timer_ns();
+      while (!ptx::mbar_try_wait(&sm.full, (sm.copies - 1u) & 1u) &&
+             ptx::global_timer_ns() - t0 <= p.wait_limit_ns) {
+      }
+    }
+    ptx::cluster_sync();
+  }
 }
 
 // Rows longer than a cluster's registers: one CTA, three passes, the later two mostly from L2.

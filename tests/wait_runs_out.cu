@@ -1,4 +1,6 @@
-// Verification's draw behind a barrier that nothing arrives on, over sums that nobody wrote.
+// Waits that run out: verification's draw behind a barrier that nothing arrives on, over sums
+// that nobody wrote; probabilities whose CTAs have half their warps, so that the other half's
+// words never come (every access stays in its buffers, every wait ends).
 #include "fs_verify.cu"
 
 namespace test_of_waits {
@@ -62,6 +64,41 @@ extern "C" int stale_draw(const float* p, const float* q, int V, int mode, uint6
   a.error_word = static_cast<int*>(at);
   test_of_waits::stale_draw_kernel<<<1, fs::verify::kThreads, 0, static_cast<cudaStream_t>(stream)>>>(a, mode, out);
   if (cudaGetLastError() != cudaSuccess ||
+      cudaMemcpyFromSymbol(&word, test_of_waits::g_word, sizeof(int)) != cudaSuccess)
+    return -1;
+  return word;
+}
+
+// N rows of 8000 logits, more than one row to a cluster of two CTAs.  Returns the error word, or -1.
+extern "C" int half_probs(const float* logits, float* out, int N, int clusters, uint64_t limit_ns,
+                          void* stream) {
+  using namespace fs::verify;
+  if (limit_ns > 1000000000ull || N < 1 || clusters < 1 || clusters > N) return -1;
+  int word = 0;
+  void* at = nullptr;
+  if (cudaGetSymbolAddress(&at, test_of_waits::g_word) != cudaSuccess ||
+      cudaMemcpyToSymbol(test_of_waits::g_word, &word, sizeof(int)) != cudaSuccess)
+    return -1;
+  ProbsParams p = {};
+  p.logits = logits;
+  p.out = out;
+  p.ldl = p.ldo = p.V = 8000;
+  p.N = N;
+  p.part = 4000;
+  p.wait_limit_ns = limit_ns;
+  p.error_word = static_cast<int*>(at);
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = 2;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(2 * clusters));
+  cfg.blockDim = dim3(kProbThreads / 2);
+  cfg.dynamicSmemBytes = 2 * 4 * kProbThreads * sizeof(float);
+  cfg.stream = static_cast<cudaStream_t>(stream);
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, probs_kernel<float, float, true, 2>, p) != cudaSuccess ||
       cudaMemcpyFromSymbol(&word, test_of_waits::g_word, sizeof(int)) != cudaSuccess)
     return -1;
   return word;
