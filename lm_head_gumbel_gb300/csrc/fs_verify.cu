@@ -501,7 +501,7 @@ struct VerifyParams {
 // long as reading the row.)
 struct Sum {
   float hi = 0.0f, lo = 0.0f;
-  // A term; `lo` is only gathered, for normal().
+  // A term; `lo` is only gathered, for normal() after a few dozen at most.
   __device__ __forceinline__ void add(float w) {
     const float s = hi + w;
     const float b = s - hi;
@@ -590,16 +590,20 @@ __device__ __forceinline__ void unpack(const uint4& v, float (&x)[16 / sizeof(T)
   }
 }
 
-// A warp's sum of a segment.  Every lane takes runs of 16 bytes, 32 runs side by side, in
-// the same order however they are read: 16 bytes at a time where rows allow it, four runs of
-// each row in flight.
+// A warp's sum of a segment, 1024 elements at a time.  Every lane takes runs of 16 bytes, 32
+// runs side by side, in the same order however they are read: 16 bytes at a time where rows allow
+// it, four runs of each row in flight.  What a lane's 32 terms lose is gathered, no more: after
+// 65536 terms (a segment of the longest rows) it would itself be off, by 2^-23 of a sum of equal
+// weights.
+constexpr int kTerms = 32;
 template <class T, bool kTwo>
-__device__ __forceinline__ Sum whole_segment(const T* p, const T* q, int segment, int lane) {
+__device__ __forceinline__ Sum whole_piece(const T* p, const T* q, int lane) {
   constexpr int kRun = 16 / int(sizeof(T));
   const uint4* pv = reinterpret_cast<const uint4*>(p) + lane;
   const uint4* qv = reinterpret_cast<const uint4*>(q) + lane;
   Sum s;
-  for (int j = 0; j < segment / (32 * kRun); j += 4) {
+#pragma unroll 1
+  for (int j = 0; j < kSegment / (32 * kRun); j += 4) {
     uint4 a[4], b[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) a[i] = __ldcs(pv + 32 * (j + i));
@@ -616,6 +620,14 @@ __device__ __forceinline__ Sum whole_segment(const T* p, const T* q, int segment
       for (int k = 0; k < kRun; ++k) s.add(weight(kTwo ? x[k] - y[k] : x[k]));
     }
   }
+  return s.normal();
+}
+template <class T, bool kTwo>
+__device__ __forceinline__ Sum whole_segment(const T* p, const T* q, int segment, int lane) {
+  static_assert(kSegment == 32 * kTerms, "terms of a lane");
+  Sum s = whole_piece<T, kTwo>(p, q, lane);
+  for (int v = kSegment; v < segment; v += kSegment)
+    s = s + whole_piece<T, kTwo>(p + v, kTwo ? q + v : q, lane);
   return s;
 }
 template <class T>
@@ -628,13 +640,17 @@ __device__ __forceinline__ Sum segment_sum(const Weights<T>& w, int begin, int l
     s = w.mode == kResidual ? whole_segment<T, true>(w.p + begin, w.q + begin, segment, lane)
                             : whole_segment<T, false>(w.p + begin, nullptr, segment, lane);
   } else {
-    for (int v0 = lane * kRun; v0 < length; v0 += 32 * kRun) {
+    for (int at = 0; at < length; at += kSegment) {
+      const int end = min(length, at + kSegment);
+      Sum piece;
+      for (int v0 = at + lane * kRun; v0 < end; v0 += 32 * kRun) {
 #pragma unroll
-      for (int i = 0; i < kRun; ++i)
-        if (v0 + i < length) s.add(w.at(begin + v0 + i));
+        for (int i = 0; i < kRun; ++i)
+          if (v0 + i < end) piece.add(w.at(begin + v0 + i));
+      }
+      s = at == 0 ? piece.normal() : s + piece.normal();
     }
   }
-  s = s.normal();
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) s = s + shfl_xor(s, d);
   return s;
@@ -751,14 +767,18 @@ __device__ __forceinline__ int find_element(const VerifyParams& a, const Weights
   const int per = a.segment / kThreads;
   const int v0 = sm.segment * a.segment + int(threadIdx.x) * per;
   const int v1 = v0 < a.V ? v0 + min(per, a.V - v0) : v0;
+  // kTerms at a time, as in a segment's sum.
   Sum own;
   int last = -1;
-  for (int v = v0; v < v1; ++v) {
-    const float x = w.at(v);
-    own.add(x);
-    if (x > 0.0f) last = v;
+  for (int at = v0; at < v1; at += kTerms) {
+    Sum piece;
+    for (int v = at; v < min(v1, at + kTerms); ++v) {
+      const float x = w.at(v);
+      piece.add(x);
+      if (x > 0.0f) last = v;
+    }
+    own = at == v0 ? piece.normal() : own + piece.normal();
   }
-  own = own.normal();
   const Sum upto = scan(own, lane);
   if (lane == 31) sm.warps[warp] = upto;
   __syncthreads();
@@ -770,19 +790,25 @@ __device__ __forceinline__ int find_element(const VerifyParams& a, const Weights
   ahead = sm.before + ahead;
   // Only lanes where the target may be passed look again; the lowest counts.
   const uint32_t past = __ballot_sync(0xFFFFFFFFu, last >= 0 && ahead + upto > sm.target);
-  Sum run = ahead + exclusive(upto, lane);
+  const Sum base = ahead + exclusive(upto, lane);
   if (past != 0u && lane == __ffs(past) - 1) {
     int first = last;
-    for (int v = v0; v < v1; ++v) {
-      const float x = w.at(v);
-      if (!(x > 0.0f)) continue;
-      Sum term;
-      term.hi = x;
-      run = run + term;
-      if (run > sm.target) {
-        first = v;
-        break;
+    Sum done;  // of the pieces before
+    for (int at = v0; at < v1 && first == last; at += kTerms) {
+      Sum run = at == v0 ? base : base + done, piece;
+      for (int v = at; v < min(v1, at + kTerms); ++v) {
+        const float x = w.at(v);
+        if (!(x > 0.0f)) continue;
+        piece.add(x);
+        Sum term;
+        term.hi = x;
+        run = run + term;
+        if (run > sm.target) {
+          first = v;
+          break;
+        }
       }
+      if (at + kTerms < v1) done = done + piece.normal();
     }
     atomicMin(&sm.first, first);
   }

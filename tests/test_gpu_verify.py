@@ -464,6 +464,54 @@ def test_a_very_long_row():
     check_probs(x)
 
 
+@pytest.mark.parametrize("shift", [0, 1])  # 16 bytes at a time, element by element
+def test_sums_of_the_longest_segments(shift):
+    """2^29 weights, of which every lane adds 16384: half of the row such that a plain gathering of
+    what those lose is off by 2^-36.8 of them, half of it equal.  Uniform numbers whose target lies
+    2^-44 to 2^-41 of the total from a border: the sums are held to 2^-45."""
+    half, terms = 2 ** 28, 16384
+    gen = torch.Generator().manual_seed(197)
+    odd = torch.randint(0, 2 ** 23, (terms,), generator=gen) * 2 + 1
+    down = torch.randint(0, 13, (terms,), generator=gen)
+    units = odd << (12 - down)                                # of 2^-36
+    lane = (odd.double() * 2.0 ** -24 * torch.exp2(-down.double())).float().cuda()
+    buf = torch.empty(2 * half + shift, device="cuda")
+    p = buf[shift:]
+    p[:half] = lane.view(-1, 1, 4).expand(-1, 32, 4).reshape(-1).repeat(half // (32 * terms))
+    p[half:] = 2.0 ** -4
+    first, step = half // terms * int(units.sum()), 2 ** 32   # the half's sum, an equal weight
+    total = first + half * step
+    # target - first = (k total - first 2^24) / 2^24 for u = k 2^-24, in steps of 2^56 / 2^24
+    k = np.arange(int(0.6 * 2 ** 24), int(0.98 * 2 ** 24), dtype=np.uint64)
+    word = (1 << 64) - 1
+    behind = (k * np.uint64(total & word) - np.uint64((first << 24) & word)) & np.uint64(2 ** 56 - 1)
+    off = np.minimum(behind, np.uint64(2 ** 56) - behind).astype(np.float64) / 2 ** 24 / total
+    k = k[(off > 2.0 ** -44) & (off < 2.0 ** -41)]
+    k = k[::max(1, len(k) // 120)]
+    want = [half + ((int(i) * total - (first << 24)) >> 56) for i in k]
+    assert len(k) > 100
+    u = torch.from_numpy(k.astype(np.float64) * 2.0 ** -24).float().cuda().unsqueeze(1)
+    ids = torch.zeros((len(k), 0), dtype=torch.int64, device="cuda")
+    got = fs.fs_verify(p.expand(len(k), 1, 2 * half), ids, u).ids[:, 0].tolist()
+    assert got == want
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_long_rows_whatever_their_alignment(dtype):
+    """Segments of 2048 and 4096 elements, as whole and element by element: the same ids."""
+    for V in (1_300_001, 2_500_000):
+        gen = torch.Generator(device="cuda").manual_seed(V)
+        buf = torch.rand(V + 1, generator=gen, device="cuda").to(dtype)
+        u = torch.rand((40, 1), generator=gen, device="cuda")
+        ids = torch.zeros((40, 0), dtype=torch.int64, device="cuda")
+        rows = [buf[:V].clone(), torch.cat([buf[:1], buf[:V]])[1:]]
+        one, two = (fs.fs_verify(r.expand(40, 1, V), ids, u).ids for r in rows)
+        assert torch.equal(one, two)
+        sums = rows[0].double().cumsum(0)
+        want = torch.searchsorted(sums, u[:, 0].double() * sums[-1], right=True)
+        assert torch.equal(one[:, 0], want)
+
+
 @pytest.mark.parametrize("call", [
     "fs.fs_quantize(x).scale", "fs.fs_matmul_fp8(*fs.fs_quantize(x), *fs.fs_quantize(w, 128))",
     "fs.fs_probs(w)", "fs.fs_verify(p, ids, u).ids"])
