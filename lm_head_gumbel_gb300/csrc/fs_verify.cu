@@ -4,6 +4,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <cfloat>
 #include <climits>
 #include <cmath>
 #include <cstdint>
@@ -456,7 +457,12 @@ __global__ void __launch_bounds__(kProbThreads) long_probs_kernel(const ProbsPar
       narrow(out + v, greedy && v == at ? 1.0f : 0.0f);
     return;
   }
-  const Exp e(m, temp);
+  const Exp exact(m, temp);
+  // Where l - m may be past the largest number and T is not far below it, FastExp, which makes
+  // no difference of the two.
+  const FastExp fast(m, exact.c_hi, exact.c_lo);
+  const bool far = -FLT_MAX - m == -INFINITY && FastExp::can(m, exact.c_hi);
+  auto e = [&](float l) { return far ? fast(l) : exact(l); };
   float sum = 0.0f;
   for (int v = threadIdx.x; v < p.V; v += kProbThreads)
     if (allowed(v)) sum += e(wide(x[v]));

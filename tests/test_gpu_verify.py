@@ -184,6 +184,17 @@ def test_probs_temperatures(T):
     check_probs(x, torch.full((3,), T, device="cuda"))
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("V", [3000, 70000, 262145, 300000])
+def test_probs_of_the_largest_logits_and_temperatures(V, dtype):
+    """Logits whose difference is past the largest number, at temperatures that make it an
+    ordinary one; and at ones that do not."""
+    gen = torch.Generator().manual_seed(V)
+    x = ((torch.rand((4, V), generator=gen) * 2 - 1) * 3.3e38).to(dtype).cuda()
+    x[3, ::3] = -float("inf")
+    check_probs(x, torch.tensor([1e38, 3e37, 1.0, 2e38]).cuda(), dtype=torch.float32)
+
+
 def test_probs_far_below_the_largest():
     """Probabilities down to 2^-126 as exactly as the large ones."""
     x = torch.linspace(-87.0, 0.0, 4096, device="cuda").repeat(2, 1)
