@@ -36,9 +36,10 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return r;
 }
 
-// exp((l - m) / T) for l <= m, to 3 2^-24 relative at any distance: l - m, and its
+// exp((l - m) / T) for l <= m, to 2^-22 relative at any distance: l - m, and its
 // product with log2(e) / T, are held in two floats, the exponent's whole part goes in
-// as bits.  Below 2^-126 it is 0.
+// as bits (an argument off by 2^-24 at most; the rest is the hardware's base-2 exponential).
+// At T past 2^100, where c_lo falls among the subnormals, to 2^-20.  Below 2^-126 it is 0.
 struct Exp {
   float m, c_hi, c_lo;  // the maximum, log2(e) / T
   __device__ __forceinline__ Exp(float max, float T) : m(max) {
