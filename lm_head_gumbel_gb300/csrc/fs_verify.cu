@@ -92,8 +92,9 @@ struct FastExp {
     float e;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(f));
     // 0 below 2^-126 (off by up to a third of that right above it), of -infinity too, whose f is NaN.
-    return r < kMagic - 126.0f ? 0.0f
-                               : __int_as_float(__float_as_int(e) + __float_as_int(r) * (1 << 23));
+    return r < kMagic - 126.0f
+               ? 0.0f
+               : __uint_as_float(__float_as_uint(e) + (__float_as_uint(r) << 23));
   }
 };
 
