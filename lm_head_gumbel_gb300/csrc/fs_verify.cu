@@ -487,7 +487,6 @@ constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kSegment = 1024;      // elements of a segment, doubled until there are
 constexpr int kMaxSegments = 1024;  // at most so many
-constexpr int kMaxCluster = 16;     // more than 8 need the kernel's leave
 
 struct VerifyParams {
   const void* p;
