@@ -487,6 +487,7 @@ constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kSegment = 1024;      // elements of a segment, doubled until there are
 constexpr int kMaxSegments = 1024;  // at most so many
+constexpr int kMaxCluster = 16;     // more than 8 need the kernel's leave
 
 struct VerifyParams {
   const void* p;
@@ -920,9 +921,30 @@ struct Device {
   bool known = false;
   fs_status status = FS_ERR_UNSUPPORTED;
   int sms = 0;
+  bool wide_clusters = false;  // of kMaxCluster CTAs fit
   int* error_word = nullptr;
 };
 Device g_devices[kMaxDevices];
+
+// Whether clusters of kMaxCluster CTAs of a verification kernel can run here at all.
+bool wide_clusters_fit(void (*kernel)(VerifyParams)) {
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = kMaxCluster;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(kMaxCluster);
+  cfg.blockDim = dim3(kThreads);
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  int n = 0;
+  const bool fit =
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) ==
+          cudaSuccess &&
+      cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) == cudaSuccess && n >= 1;
+  cudaGetLastError();
+  return fit;
+}
 
 // The current device, if it is a GB300 (sm_103).
 fs_status device_setup(const Device** out) {
@@ -944,12 +966,9 @@ fs_status device_setup(const Device** out) {
     d.status = FS_ERR_UNSUPPORTED;
     if (major == 10 && minor == 3) {
       d.error_word = device_error_word();
-      const bool ok =
-          d.error_word != nullptr &&
-          cudaFuncSetAttribute(verify_kernel<float>,
-                               cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess &&
-          cudaFuncSetAttribute(verify_kernel<__nv_bfloat16>,
-                               cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess;
+      d.wide_clusters = wide_clusters_fit(verify_kernel<float>) &&
+                        wide_clusters_fit(verify_kernel<__nv_bfloat16>);
+      const bool ok = d.error_word != nullptr;
       cudaGetLastError();
       d.status = ok ? FS_OK : FS_ERR_CUDA;
     }
@@ -1138,17 +1157,25 @@ extern "C" fs_status fs_verify(const fs_verify_args* args, void* stream_ptr) {
   p.n_segments = int32_t(ceil_div(a.V, segment));
   p.wait_limit_ns = kWaitLimitNs;
   p.error_word = dev->error_word;
-  // A sequence's row over as many CTAs as fit beside the others' (two an SM), and where its
-  // bytes are worth what a CTA costs before it reads (about 5 us of its place), more.
-  // Measured, in us, 128256 in bf16 without q, 1 / 2 / 4 / 8 CTAs: 16 sequences 24 / 19 / 17 /
-  // 15, 64: 25 / 20 / 19 / 24, 152: 26 / 24 / 32 / 41, 256: 32 / 40 / 47 / 61.
+  // A sequence's row over as many CTAs as fit beside the others' (two an SM), and over twice as
+  // many again while each one's part stays worth its place: kPlaceKb for every turn that they
+  // take on the SMs (what a CTA would read, at 22 KB a us, in the 5 to 7 us that it is there before
+  // and after it reads).  Up to 16 where that leaves a sequence's CTAs an SM each.
+  // Measured, in us, calls behind one another on inputs past L2, 1 / 2 / 4 / 8 CTAs: 128256 in
+  // bf16 without q, 16 sequences 18.3 / 13.0 / 10.2 / 9.6, 64: 19.4 / 13.8 / 13.2 / 17.4, 152: 19.8 /
+  // 18.2 / 25.6 / 32.7, 256: 27.2 / 33.9 / 40.4 / 50.9; alone and from memory 25 / 19 / 17 / 16, 25 /
+  // 21 / 19 / 23, 27 / 24 / 33 / 42, 33 / 42 / 48 / 60.  8 and 16 CTAs, 151936 in fp32 with q: 1
+  // sequence 8.1 and 6.6, 9: 9.6 and 8.8, 16: 11.4 and 11.8.  Where rows are long and batches large
+  // it takes too many by up to a fifth: 256 sequences of 151936 in fp32 41.5 with 2 CTAs, 33.9 with 1.
+  constexpr int64_t kPlaceKb = 150;
   const int64_t slots = 2 * int64_t(dev->sms);
   const int64_t row_kb = (a.V * int64_t(element(a.dtype)) * (p.q ? 2 : 1)) >> 10;
   int ctas = 1;
   while (ctas < 8 && ctas * kWarps < p.n_segments &&
-         (a.B * ctas * 2 <= slots || a.B * (ctas * 2) * (ctas * 2) * 150 <= slots * row_kb))
+         (a.B * ctas * 2 <= slots || a.B * (ctas * 2) * (ctas * 2) * kPlaceKb <= slots * row_kb))
     ctas *= 2;
-  if (a.B <= 9 && 8 * kWarps < p.n_segments) ctas = 16;
+  if (a.B * kMaxCluster <= dev->sms && 8 * kWarps < p.n_segments && dev->wide_clusters)
+    ctas = kMaxCluster;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = unsigned(ctas);
