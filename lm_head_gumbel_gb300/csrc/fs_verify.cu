@@ -610,7 +610,6 @@ __device__ __forceinline__ Sum whole_piece(const T* p, const T* q, int lane) {
   const uint4* pv = reinterpret_cast<const uint4*>(p) + lane;
   const uint4* qv = reinterpret_cast<const uint4*>(q) + lane;
   Sum s;
-#pragma unroll 1
   for (int j = 0; j < kSegment / (32 * kRun); j += 4) {
     uint4 a[4], b[4];
 #pragma unroll
@@ -648,16 +647,18 @@ __device__ __forceinline__ Sum segment_sum(const Weights<T>& w, int begin, int l
     s = w.mode == kResidual ? whole_segment<T, true>(w.p + begin, w.q + begin, segment, lane)
                             : whole_segment<T, false>(w.p + begin, nullptr, segment, lane);
   } else {
-    for (int at = 0; at < length; at += kSegment) {
-      const int end = min(length, at + kSegment);
+    auto add_up = [&](int at, int end) {
       Sum piece;
       for (int v0 = at + lane * kRun; v0 < end; v0 += 32 * kRun) {
 #pragma unroll
         for (int i = 0; i < kRun; ++i)
           if (v0 + i < end) piece.add(w.at(begin + v0 + i));
       }
-      s = at == 0 ? piece.normal() : s + piece.normal();
-    }
+      return piece.normal();
+    };
+    s = add_up(0, min(length, kSegment));
+    for (int at = kSegment; at < length; at += kSegment)
+      s = s + add_up(at, min(length, at + kSegment));
   }
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) s = s + shfl_xor(s, d);
@@ -775,17 +776,22 @@ __device__ __forceinline__ int find_element(const VerifyParams& a, const Weights
   const int per = a.segment / kThreads;
   const int v0 = sm.segment * a.segment + int(threadIdx.x) * per;
   const int v1 = v0 < a.V ? v0 + min(per, a.V - v0) : v0;
-  // kTerms at a time, as in a segment's sum.
-  Sum own;
+  // kTerms at a time, as in a segment's sum; mostly there are 2 in all.
   int last = -1;
-  for (int at = v0; at < v1; at += kTerms) {
-    Sum piece;
-    for (int v = at; v < min(v1, at + kTerms); ++v) {
+  auto add_up = [&](int from, int to) {
+    Sum t;
+    for (int v = from; v < to; ++v) {
       const float x = w.at(v);
-      piece.add(x);
+      t.add(x);
       if (x > 0.0f) last = v;
     }
-    own = at == v0 ? piece.normal() : own + piece.normal();
+    return t.normal();
+  };
+  Sum own;
+  if (per <= kTerms) {
+    own = add_up(v0, v1);
+  } else {
+    for (int at = v0; at < v1; at += kTerms) own = own + add_up(at, min(v1, at + kTerms));
   }
   const Sum upto = scan(own, lane);
   if (lane == 31) sm.warps[warp] = upto;
@@ -801,22 +807,26 @@ __device__ __forceinline__ int find_element(const VerifyParams& a, const Weights
   const Sum base = ahead + exclusive(upto, lane);
   if (past != 0u && lane == __ffs(past) - 1) {
     int first = last;
-    Sum done;  // of the pieces before
-    for (int at = v0; at < v1 && first == last; at += kTerms) {
-      Sum run = at == v0 ? base : base + done, piece;
-      for (int v = at; v < min(v1, at + kTerms); ++v) {
+    auto search = [&](Sum run, int from, int to) {
+      for (int v = from; v < to; ++v) {
         const float x = w.at(v);
         if (!(x > 0.0f)) continue;
-        piece.add(x);
         Sum term;
         term.hi = x;
         run = run + term;
         if (run > sm.target) {
           first = v;
-          break;
+          return true;
         }
       }
-      if (at + kTerms < v1) done = done + piece.normal();
+      return false;
+    };
+    if (per <= kTerms) {
+      search(base, v0, v1);
+    } else {
+      Sum done;  // of the terms before
+      for (int at = v0; at < v1 && !search(base + done, at, min(v1, at + kTerms)); at += kTerms)
+        done = done + add_up(at, min(v1, at + kTerms));
     }
     atomicMin(&sm.first, first);
   }
