@@ -597,3 +597,33 @@ def test_a_step_of_speculative_decoding():
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(ids2, ids) and torch.equal(r2.ids, r.ids)
+
+
+@pytest.mark.parametrize("q", [True, False])
+@pytest.mark.parametrize("dtype", TYPES)
+def test_greedy_drafts_verify_as_greedy_decoding(dtype, q):
+    """At T = 0 the accepted drafts are the leading ones that are the target's likeliest ids, and
+    the token behind them is that id too: what greedy decoding of the target alone gives."""
+    B, K, V = 64, 4, 3001
+    gen = torch.Generator().manual_seed(41)
+    target = torch.randint(-20, 21, (B, K + 1, V), generator=gen).float()  # equal largest ones too
+    drafter = target[:, :K].clone()
+    wrong = torch.rand((B, K), generator=gen) < 0.3
+    drafter[wrong] = torch.randint(-20, 21, (int(wrong.sum()), V), generator=gen).float()
+    zero = torch.zeros(B * (K + 1), device="cuda")
+    p = fs.fs_probs(target.view(-1, V).to(dtype).cuda(), temperature=zero, out_dtype=dtype)
+    qs = fs.fs_probs(drafter.view(-1, V).to(dtype).cuda(), temperature=zero[:B * K], out_dtype=dtype)
+    none = torch.zeros((B * K, 0), dtype=torch.int64, device="cuda")
+    u = torch.rand((B * K, 1), generator=gen).cuda()
+    ids = fs.fs_verify(qs.unsqueeze(1), none, u).ids.view(B, K)
+    lowest = torch.arange(V, 0, -1)
+    likeliest = (torch.where(target == target.amax(-1, keepdim=True), lowest, 0)).argmax(-1)
+    assert torch.equal(ids.cpu(), torch.where(
+        drafter == drafter.amax(-1, keepdim=True), lowest, 0).argmax(-1))
+    u = torch.rand((B, K + 1), generator=gen).cuda()
+    r = fs.fs_verify(p.view(B, K + 1, V), ids, u, qs.view(B, K, V) if q else None)
+    n = (ids.cpu() == likeliest[:, :K]).long().cumprod(1).sum(1)
+    assert 0 < int((n == K).sum()) < B and int((n == 0).sum()) > 0
+    assert torch.equal(r.accepted.cpu(), n)
+    at = torch.arange(K + 1)
+    assert torch.equal(r.ids.cpu(), torch.where(at <= n.unsqueeze(1), likeliest, -1))
