@@ -94,7 +94,8 @@ constexpr float kMostE4m3 = 448.0f;
 // Quantisation
 // ---------------------------------------------------------------------------
 // Bound: memory.  A head of 151936 x 4096 in bf16 (1.87 GB read and written) takes 264 us,
-// 7.1 TB/s, 16384 x 5120 hidden states 41 us, 6.2 TB/s.  Elements stay bits until they are
+// 7.1 TB/s, in fp32 439; 16384 x 5120 hidden states 40 us, 6.4 TB/s, in fp32 62.  Rows off 16-byte
+// boundaries go element by element: 103 and 133 us for those hidden states.  Elements stay bits until they are
 // scaled, so that a thread's loads are all in flight (branches between them: 779 us for the
 // head), and the largest magnitude is an unsigned maximum: a NaN's bits are above every
 // number's.
@@ -293,15 +294,19 @@ __global__ void __launch_bounds__(kTileThreads) quantize_tile_kernel(const Quant
 // sums in registers.
 //
 // Bound: W's bytes for few rows (one row at d = 4096, V = 151936 takes 92 us, 6.75 TB/s; 128
-// rows 114).  For many, what follows the MMAs: an accumulator's 256 columns are 128 additions
-// of two values a thread, and an accumulator is free again some 1200 cycles after its MMAs were
-// issued (256 a part, 340 until the sums' warps know, 340 until they have loaded it, 270 until
-// the next MMAs run), of which two overlap: 810 cycles a slice where the MMAs alone take 640 with
-// their waits and 512 at the nominal rate.  1000 rows: 455 us in bursts, 2740 TFLOP/s.  First
-// 1045: tensor-memory loads one at a time with their additions between, scales read by the same
-// warps (a wait for tensor-memory loads waits for those too), outputs stored from registers,
-// all lanes at every wait.  Polling is not free here: the same waits without the clock reads
-// between their tries took 790 us.
+// rows of 128256 90).  For many, what follows the MMAs: 1000 rows (CTA pairs) take 459 us in
+// bursts, 2720 TFLOP/s, 800 cycles a slice; by leaving parts out in copies of the kernel, the MMAs
+// with their waits alone 550 (512 at the nominal rate; a CTA's copies are 60 bytes a cycle
+// then), with loads from tensor memory but no additions 733, with additions but no loads 729, all but
+// outputs 752.  So neither loads nor additions by themselves bound it, but the way of an
+// accumulator from the MMAs to the sums' warps and back, of which two overlap; which part of it stays
+// uncovered is not known.  320 rows (single CTAs): 1012 cycles, of which 857 without the sums, at
+// 57 bytes of copies a cycle.  ptxas spills 44 bytes of stores and 188 of loads in the pairs'
+// kernel, 8 and 72 to 80 in the single CTAs' (in which warps is not known).
+// First 1045 us: tensor-memory loads one at a time with their additions between, scales read by
+// the same warps (a wait for tensor-memory loads waits for those too), outputs stored from
+// registers, all lanes at every wait.  Polling is not free here: the same waits without the clock
+// reads between their tries took 790 us.
 // ---------------------------------------------------------------------------
 using vocab::BoundedWait;
 using vocab::kEpiWarps;
@@ -1154,8 +1159,9 @@ extern "C" fs_status fs_matmul_fp8(const fs_matmul_fp8_args* args, void* stream_
   if (a.M <= kBM) return launch<256, false>(*dev, a, s, stream);
   // CTA pairs read W once for 256 rows, but take 256 at a time.  Where the last ones are few,
   // single CTAs need fewer turns, each 1.25 times as long: at d = 4096, V = 128256, pairs / single
-  // CTAs, 200 rows 116 / 144 us, 320 201 / 185, 450 209 / 248, 600 287 / 295, 1000 (V = 151936)
-  // 455 / 542.
+  // CTAs in bursts (held at the power limit), 200 rows 111 / 136 us (123 / 141), 320 200 / 181 (213 /
+  // 193), 384 202 / 184, 450 205 / 242, 600 286 / 292 (317 / 312), 1000 (V = 151936) 458 / 537 (528 /
+  // 592).
   const int64_t n_nt = ceil_div(a.V, 256);
   const int64_t pair_turns = ceil_div(ceil_div(a.M, 2 * kBM) * n_nt, dev->pairs);
   const int64_t single_turns = ceil_div(n_mt * n_nt, dev->sms);
