@@ -38,7 +38,7 @@ __device__ __forceinline__ float max_nan(float a, float b) {
 
 // exp((l - m) / T) for l <= m, to 2^-22 relative at any distance: l - m, and its
 // product with log2(e) / T, are held in two floats, the exponent's whole part goes in
-// as bits (an argument off by 2^-24 at most; the rest is the hardware's base-2 exponential).
+// as bits (Cody and Waite's reduction; an argument off by 2^-24 at most; the rest is the hardware's base-2 exponential).
 // At T past 2^100, where c_lo falls among the subnormals, to 2^-20.  Below 2^-126 it is 0.
 struct Exp {
   float m, c_hi, c_lo;  // the maximum, log2(e) / T
@@ -510,8 +510,8 @@ struct VerifyParams {
   int* error_word;
 };
 
-// A sum in two floats, the second at most half the last place of the first: to 2^-46 or so
-// of the total.  (64-bit arithmetic is slow on this GPU: a scan by 16 warps in it took as
+// A sum in two floats, the second at most half the last place of the first (Knuth's two-sum): to
+// 2^-46 or so of the total.  (64-bit arithmetic is slow on this GPU: a scan by 16 warps in it took as
 // long as reading the row.)
 struct Sum {
   float hi = 0.0f, lo = 0.0f;
